@@ -24,6 +24,7 @@ __all__ = [
     "mfx_weighted_squared_relu_fwd", "mfx_weighted_squared_relu_bwd",
     "mfx_scaled_masked_softmax_fwd", "mfx_scaled_upper_triang_masked_softmax_fwd",
     "mfx_scaled_masked_softmax_bwd", "mfx_scaled_upper_triang_masked_softmax_bwd",
+    "mfx_relbias_softmax_dropout_fwd", "mfx_relbias_softmax_dropout_bwd",
     "mfx_bias_dropout_add_train", "mfx_bias_dropout_add_inference", "mfx_bias_dropout_add_bwd",
     "mfx_bias_dropout_add_train_packed", "mfx_bias_dropout_add_bwd_packed",
     "mfx_bias_gelu_bwd_dbias", "mfx_bias_geglu_bwd_dbias", "mfx_bias_swiglu_bwd_dbias",
@@ -52,6 +53,7 @@ class MfxError(RuntimeError):
 _lib = None
 
 _P, _I, _I64, _U64, _F = C.c_void_p, C.c_int, C.c_int64, C.c_uint64, C.c_float
+_RELBIAS = [_I, _P, _I64, _I64, _I, _P, _I64, _I64, _I64, _I, _I64, _P, _F, _U64, _U64, _U64]
 _SIGS = {
     "mfx_bias_gelu_fwd": [_I, _I64, _I64, _P, _P, _P, _P],
     "mfx_bias_gelu_bwd": [_I, _I64, _I64, _P, _P, _P, _P, _P],
@@ -65,6 +67,9 @@ _SIGS = {
     "mfx_scaled_upper_triang_masked_softmax_fwd": [_I, _I64, _I64, _P, _F, _P, _P],
     "mfx_scaled_masked_softmax_bwd": [_I, _I64, _I64, _P, _P, _F, _P, _P],
     "mfx_scaled_upper_triang_masked_softmax_bwd": [_I, _I64, _I64, _P, _P, _F, _P, _P],
+    "mfx_relbias_softmax_dropout_fwd": [_I, _I64, _I64, _I64, _I64, _P, _F, *_RELBIAS, _P, _P, _P],
+    "mfx_relbias_softmax_dropout_bwd": [_I, _I64, _I64, _I64, _I64, _P, _P, _P, _F, *_RELBIAS, _P, _P, _P,
+                                        C.POINTER(C.c_size_t), _P],
     "mfx_bias_dropout_add_train": [_I, _I, _I64, _I64, _P, _P, _P, _F, _U64, _U64, _U64, _P, _P, _P],
     "mfx_bias_dropout_add_inference": [_I, _I, _I64, _I64, _P, _P, _P, _F, _U64, _U64, _P],
     "mfx_bias_dropout_add_bwd": [_I, _I, _I64, _I64, _P, _P, _F, _U64, _U64, _U64, _P, _P, _P],
@@ -125,6 +130,14 @@ def _cuda(t, name, dtype=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t
+
+
+def _like(t, name, shape, dtype):
+    """A CUDA tensor of the given shape and dtype (an output or gradient buffer)."""
+    _cuda(t, name, dtype)
+    if t is None or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
     return t
 
 
@@ -352,6 +365,82 @@ def mfx_scaled_upper_triang_masked_softmax_bwd(dy, y, scale, dx=None, stream=Non
     _call("mfx_scaled_upper_triang_masked_softmax_bwd", dtype_code(y.dtype), ab, sq, _ptr(dy), _ptr(y),
           float(scale), _ptr(dx), _stream(stream, y))
     return dx
+
+
+# ---------------------------------------------------------------------------
+# scale-mask-softmax with a learned relative position bias and dropout
+# ---------------------------------------------------------------------------
+def _relbias_args(x, table, mask, max_distance, bidirectional, causal, q_start, seq_start, p, seed, offset, elem_base):
+    """The arguments that forward and backward share, from table_dt on."""
+    _cuda(x, "x")
+    _cuda(table, "table")
+    _cuda(mask, "mask", x.dtype)
+    _cuda(seq_start, "seq_start", torch.int32)
+    if x.dim() != 4:
+        raise ValueError("x must have 4 dims [b, np, sq, sk]")
+    b, np_, sq, sk = x.shape
+    buckets = 0
+    if table is not None:
+        if table.dim() != 2 or table.shape[1] != np_:
+            raise ValueError("table must have the shape [num_buckets, np]")
+        buckets = table.shape[0]
+    mb = mnp = msq = 1
+    if mask is not None:
+        if mask.dim() != 4 or mask.shape[3] != sk:
+            raise ValueError("mask must have the shape [1 or b, 1 or np, 1 or sq, sk]")
+        mb, mnp, msq, _ = mask.shape
+    if seq_start is not None and tuple(seq_start.shape) != (b,):
+        raise ValueError("seq_start must have one entry per batch")
+    for name, t in (("table", table), ("mask", mask), ("seq_start", seq_start)):
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{name} must be on x's device")
+    return (dtype_code(table.dtype if table is not None else x.dtype), _ptr(table), buckets, int(max_distance),
+            int(bool(bidirectional)), _ptr(mask), mb, mnp, msq, int(bool(causal)), int(q_start), _ptr(seq_start),
+            float(p), int(seed) % 2**64, int(offset) % 2**64, int(elem_base))
+
+
+def mfx_relbias_softmax_dropout_fwd(x, scale, table=None, mask=None, max_distance=128, bidirectional=True,
+                                    causal=False, q_start=0, seq_start=None, p=0.0, seed=0, offset=0, elem_base=0,
+                                    y=None, stats=None, need_stats=True, stream=None):
+    """y = dropout(softmax(x * scale + table[bucket(k - pos)] + mask), p) over
+    the last dim of x [b, np, sq, sk]; table: [num_buckets, np] (x's dtype or
+    float32); pos = q_start + seq_start[b] + q.  Returns (y, stats); stats
+    [b, np, sq, 2] is what the backward needs (None with need_stats=False)."""
+    shared = _relbias_args(x, table, mask, max_distance, bidirectional, causal, q_start, seq_start, p, seed, offset,
+                           elem_base)
+    y = torch.empty_like(x) if y is None else _like(y, "y", x.shape, x.dtype)
+    if stats is not None:
+        _like(stats, "stats", (*x.shape[:3], 2), torch.float32)
+    elif need_stats:
+        stats = torch.empty((*x.shape[:3], 2), dtype=torch.float32, device=x.device)
+    _call("mfx_relbias_softmax_dropout_fwd", dtype_code(x.dtype), *x.shape, _ptr(x), float(scale), *shared, _ptr(y),
+          _ptr(stats), _stream(stream, x))
+    return y, stats
+
+
+def mfx_relbias_softmax_dropout_bwd(dy, x, stats, scale, table=None, mask=None, max_distance=128, bidirectional=True,
+                                    causal=False, q_start=0, seq_start=None, p=0.0, seed=0, offset=0, elem_base=0,
+                                    dx=None, dtable=None, need_dtable=True, workspace=None, stream=None):
+    """(dx, dtable) from the forward's inputs and stats; dtable has table's
+    shape and dtype (None without a table or with need_dtable=False)."""
+    shared = _relbias_args(x, table, mask, max_distance, bidirectional, causal, q_start, seq_start, p, seed, offset,
+                           elem_base)
+    _like(dy, "dy", x.shape, x.dtype)
+    _like(stats, "stats", (*x.shape[:3], 2), torch.float32)
+    dx = torch.empty_like(x) if dx is None else _like(dx, "dx", x.shape, x.dtype)
+    if dtable is not None:
+        if table is None:
+            raise ValueError("dtable needs a table")
+        _like(dtable, "dtable", table.shape, table.dtype)
+    elif table is not None and need_dtable:
+        dtable = torch.empty_like(table)
+    head = (dtype_code(x.dtype), *x.shape, _ptr(dy), _ptr(x), _ptr(stats), float(scale), *shared, _ptr(dx), _ptr(dtable))
+    st = _stream(stream, x)
+    if dtable is None:
+        _call("mfx_relbias_softmax_dropout_bwd", *head, None, None, st)
+    else:
+        _with_workspace("mfx_relbias_softmax_dropout_bwd", head, (st,), x.device, workspace)
+    return dx, dtable
 
 
 # ---------------------------------------------------------------------------

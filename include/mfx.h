@@ -38,6 +38,7 @@
 #ifndef MFX_H
 #define MFX_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -195,6 +196,75 @@ int mfx_scaled_masked_softmax_bwd(int dt, int64_t rows, int64_t sk,
 int mfx_scaled_upper_triang_masked_softmax_bwd(int dt, int64_t attn_batches, int64_t sq,
                                                const void* dy, const void* y, float scale,
                                                void* dx, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Scale-mask-softmax with a learned relative position bias by buckets and   */
+/* dropout: the attention-score path of encoder-decoder layers in one pass   */
+/* each way.  Beside mfx_scaled_masked_softmax_fwd it needs no [np, sq, sk]  */
+/* bias tensor, no stored keep mask and no stored probabilities.             */
+/* ------------------------------------------------------------------------ */
+
+/* For score row (i, h, q) of x [b, np, sq, sk], with the query at position
+ * pos = q_start + (seq_start ? seq_start[i] : 0) + q of the keys 0 .. sk - 1:
+ *   s_k = x_k * scale + table[bucket(k - pos), h] + mask_k
+ *   P   = softmax of s over the keys that take part
+ *   y_k = keep_k ? P_k * (1 / (1 - p)) : 0.
+ * table: [num_buckets, np] of dtype table_dt (either code), or NULL (no bias;
+ * num_buckets, max_distance and bidirectional are then not looked at).
+ * Buckets of a direction, n = |k - pos|: with S of them (num_buckets / 2 per
+ * direction when bidirectional, keys after the query in the upper half; else
+ * num_buckets, with n = 0 for every key after the query), F = S / 2 rounded
+ * down: n itself below F, else
+ *   min(S - 1, F + floor((S - F) * log(n / F) / log(max_distance / F))),
+ * whose borders are exact (whole-number powers are compared, so a border that
+ * is a whole number belongs to the upper bucket).  2 <= S <= 128, num_buckets
+ * even when bidirectional, F < max_distance <= 8192, else MFX_ERR_SHAPE.
+ * mask: NULL or an ADDITIVE mask of dtype dt, [mask_b, mask_np, mask_sq, sk]
+ * with each size 1 or x's; a key whose mask is -inf takes no part whatever x
+ * holds there.  Finite masks are added exactly in effect: a row whose every
+ * mask is the type's lowest value is the softmax of its scores.  causal != 0
+ * leaves out the keys k > pos, whose x is not read (with seq_start: each
+ * sequence's unwritten part of a longer key axis).  A row in which no key
+ * takes part is zeros.
+ * Dropout: element (r, k), r = (i * np + h) * sq + q, has the index e =
+ * elem_base + r * sk + k, and keep as in mfx_bias_dropout_add_train (same
+ * generator, words and threshold); p = 0 keeps everything.
+ * stats: [b, np, sq, 2] fp32, what the backward needs of each row (the shift
+ * of its mask and the log of its sum of exponentials), or NULL (inference).
+ * y: x's shape and dtype; y may equal x (in place, when no backward follows).
+ * sk <= 2^30, |q_start| <= 2^40.  One query per sequence over a long key axis
+ * (decoding) splits a row over several thread blocks. */
+int mfx_relbias_softmax_dropout_fwd(int dt, int64_t b, int64_t np, int64_t sq, int64_t sk,
+                                    const void* x, float scale,
+                                    int table_dt, const void* table, int64_t num_buckets, int64_t max_distance,
+                                    int bidirectional,
+                                    const void* mask, int64_t mask_b, int64_t mask_np, int64_t mask_sq,
+                                    int causal, int64_t q_start, const int32_t* seq_start,
+                                    float p, uint64_t seed, uint64_t offset, uint64_t elem_base,
+                                    void* y, float* stats, void* stream);
+
+/* Backward, from the forward's inputs and stats and the gradient dy of y:
+ *   dP_k = keep_k ? dy_k * (1 / (1 - p)) : 0,  D = sum_k dP_k P_k
+ *   dS_k = P_k (dP_k - D)
+ *   dx_k = scale * dS_k                        (dtype dt; zeros where left out)
+ *   dtable[u, h] = sum of dS over the positions of head h in bucket u
+ * P and keep are formed again; dy counts only where P is not zero.  dtable:
+ * [num_buckets, np] of dtype table_dt, from fp32 sums rounded once, or NULL
+ * (not formed; needs no workspace).  The sums run in a fixed order, so dtable
+ * is bitwise reproducible on a given GPU model; with an empty x it is set to
+ * zero.  The workspace protocol is that of the fused bias gradients below
+ * (workspace == NULL with workspace_bytes given asks for the size).  dx may
+ * equal dy or x; other overlaps -> MFX_ERR_ALIAS.  The other arguments are
+ * the forward's. */
+int mfx_relbias_softmax_dropout_bwd(int dt, int64_t b, int64_t np, int64_t sq, int64_t sk,
+                                    const void* dy, const void* x, const float* stats, float scale,
+                                    int table_dt, const void* table, int64_t num_buckets, int64_t max_distance,
+                                    int bidirectional,
+                                    const void* mask, int64_t mask_b, int64_t mask_np, int64_t mask_sq,
+                                    int causal, int64_t q_start, const int32_t* seq_start,
+                                    float p, uint64_t seed, uint64_t offset, uint64_t elem_base,
+                                    void* dx, void* dtable, void* workspace, size_t* workspace_bytes,
+                                    void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Bias + dropout + residual add, fusions page §3.2-§3.3                     */
