@@ -25,8 +25,11 @@ __all__ = [
     "mfx_scaled_masked_softmax_fwd", "mfx_scaled_upper_triang_masked_softmax_fwd",
     "mfx_scaled_masked_softmax_bwd", "mfx_scaled_upper_triang_masked_softmax_bwd",
     "mfx_relbias_softmax_dropout_fwd", "mfx_relbias_softmax_dropout_bwd",
+    "mfx_moe_rows", "mfx_moe_sort", "mfx_moe_permute_fwd", "mfx_moe_permute_bwd",
+    "mfx_moe_unpermute_fwd", "mfx_moe_unpermute_bwd",
     "mfx_bias_dropout_add_train", "mfx_bias_dropout_add_inference", "mfx_bias_dropout_add_bwd",
     "mfx_bias_dropout_add_train_packed", "mfx_bias_dropout_add_bwd_packed",
+    "mfx_bias_dropout_add_train_nomask", "mfx_dropout_fwd", "mfx_dropout_bwd",
     "mfx_bias_gelu_bwd_dbias", "mfx_bias_geglu_bwd_dbias", "mfx_bias_swiglu_bwd_dbias",
     "mfx_bias_dropout_add_bwd_dbias", "mfx_device_error",
 ]
@@ -70,11 +73,19 @@ _SIGS = {
     "mfx_relbias_softmax_dropout_fwd": [_I, _I64, _I64, _I64, _I64, _P, _F, *_RELBIAS, _P, _P, _P],
     "mfx_relbias_softmax_dropout_bwd": [_I, _I64, _I64, _I64, _I64, _P, _P, _P, _F, *_RELBIAS, _P, _P, _P,
                                         C.POINTER(C.c_size_t), _P],
+    "mfx_moe_sort": [_I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, C.POINTER(C.c_size_t), _P],
+    "mfx_moe_permute_fwd": [_I, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P],
+    "mfx_moe_permute_bwd": [_I, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P],
+    "mfx_moe_unpermute_fwd": [_I, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P],
+    "mfx_moe_unpermute_bwd": [_I, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P],
     "mfx_bias_dropout_add_train": [_I, _I, _I64, _I64, _P, _P, _P, _F, _U64, _U64, _U64, _P, _P, _P],
     "mfx_bias_dropout_add_inference": [_I, _I, _I64, _I64, _P, _P, _P, _F, _U64, _U64, _P],
     "mfx_bias_dropout_add_bwd": [_I, _I, _I64, _I64, _P, _P, _F, _U64, _U64, _U64, _P, _P, _P],
     "mfx_bias_dropout_add_train_packed": [_I, _I, _I64, _I64, _P, _P, _P, _F, _U64, _U64, _U64, _P, _P, _P],
     "mfx_bias_dropout_add_bwd_packed": [_I, _I, _I64, _I64, _P, _P, _F, _P, _P, _P],
+    "mfx_bias_dropout_add_train_nomask": [_I, _I, _I64, _I64, _P, _P, _P, _F, _U64, _U64, _U64, _P, _P],
+    "mfx_dropout_fwd": [_I, _I64, _P, _F, _U64, _U64, _U64, _P, _P],
+    "mfx_dropout_bwd": [_I, _I64, _P, _F, _U64, _U64, _U64, _P, _P],
     "mfx_bias_gelu_bwd_dbias": [_I, _I64, _I64, _P, _P, _P, _P, _P, _P, C.POINTER(C.c_size_t), _P],
     "mfx_bias_gelu_bwd_dbias_noalloc": [_I, _I64, _I64, _P, _P, _P, _P, _P, _P],
     "mfx_bias_geglu_bwd_dbias": [_I, _I64, _I64, _P, _P, _P, _P, _P, _P, C.POINTER(C.c_size_t), _P],
@@ -101,6 +112,8 @@ def lib():
         L.mfx_status_string.restype = C.c_char_p
         L.mfx_last_cuda_error.argtypes = []
         L.mfx_last_cuda_error.restype = C.c_int
+        L.mfx_moe_rows.argtypes = [_I64, _I64, _I64, _I64]
+        L.mfx_moe_rows.restype = _I64
         L.mfx_version.argtypes = []
         L.mfx_version.restype = C.c_int
         L.mfx_device_error.argtypes = [C.POINTER(C.c_uint)]
@@ -444,6 +457,135 @@ def mfx_relbias_softmax_dropout_bwd(dy, x, stats, scale, table=None, mask=None, 
 
 
 # ---------------------------------------------------------------------------
+# tokens sorted by expert and back
+# ---------------------------------------------------------------------------
+def mfx_moe_rows(tokens, topk, experts, align=1):
+    """Rows that the sorted layout of tokens x topk slots needs at most."""
+    n = lib().mfx_moe_rows(tokens, topk, experts, align)
+    if n < 0:
+        raise MfxError(2, "mfx_moe_rows")
+    return n
+
+
+def mfx_moe_sort(expert_of, experts, align=1, capacity=0, rows=None, row_of=None, slot_of=None, offsets=None,
+                 counts=None, workspace=None, stream=None):
+    """(row_of [tokens, topk], slot_of [rows], offsets [experts + 1], counts
+    [experts]), all int32, of the layout of expert_of's slots (int32 [tokens,
+    topk]) by expert; rows defaults to mfx_moe_rows()."""
+    _cuda(expert_of, "expert_of", torch.int32)
+    if expert_of.dim() != 2:
+        raise ValueError("expert_of must have the shape [tokens, topk]")
+    tokens, topk = expert_of.shape
+    if rows is None:
+        rows = slot_of.numel() if slot_of is not None else mfx_moe_rows(tokens, topk, experts, align)
+    new = lambda t, name, shape: (torch.empty(shape, dtype=torch.int32, device=expert_of.device) if t is None  # noqa: E731
+                                  else _like(t, name, shape, torch.int32))
+    row_of, slot_of = new(row_of, "row_of", (tokens, topk)), new(slot_of, "slot_of", (rows,))
+    offsets, counts = new(offsets, "offsets", (experts + 1,)), new(counts, "counts", (experts,))
+    _with_workspace("mfx_moe_sort", (tokens, topk, experts, align, capacity, rows, _ptr(expert_of), _ptr(row_of),
+                                     _ptr(slot_of), _ptr(offsets), _ptr(counts)),
+                    (_stream(stream, expert_of),), expert_of.device, workspace)
+    return row_of, slot_of, offsets, counts
+
+
+def _moe_maps(x, row_of, slot_of):
+    _cuda(row_of, "row_of", torch.int32)
+    if row_of.dim() != 2:
+        raise ValueError("row_of must have the shape [tokens, topk]")
+    for name, t in (("row_of", row_of), ("slot_of", slot_of)):
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{name} must be on the data's device")
+    if slot_of is not None:
+        _cuda(slot_of, "slot_of", torch.int32)
+        if slot_of.dim() != 1:
+            raise ValueError("slot_of must have the shape [rows]")
+    return row_of.shape
+
+
+def _moe_data(t, name, rows):
+    _cuda(t, name)
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must have the shape [{'rows' if rows is None else rows}, cols]")
+    return t.shape
+
+
+def mfx_moe_permute_fwd(x, row_of, slot_of, weight=None, out=None, out_weight=None, stream=None):
+    """(out [rows, cols], out_weight [rows]): x [tokens, cols] by the maps of
+    mfx_moe_sort, padding rows zero; out_weight is None without weight
+    [tokens, topk] (fp32)."""
+    tokens, topk = _moe_maps(x, row_of, slot_of)
+    _, cols = _moe_data(x, "x", tokens)
+    rows = slot_of.shape[0]
+    out = x.new_empty((rows, cols)) if out is None else _like(out, "out", (rows, cols), x.dtype)
+    if weight is not None:
+        _like(weight, "weight", (tokens, topk), torch.float32)
+        out_weight = (torch.empty(rows, dtype=torch.float32, device=x.device) if out_weight is None
+                      else _like(out_weight, "out_weight", (rows,), torch.float32))
+    elif out_weight is not None:
+        raise ValueError("out_weight needs a weight")
+    _call("mfx_moe_permute_fwd", dtype_code(x.dtype), tokens, topk, cols, rows, _ptr(x), _ptr(row_of), _ptr(slot_of),
+          _ptr(weight), _ptr(out), _ptr(out_weight), _stream(stream, x))
+    return out, out_weight
+
+
+def mfx_moe_permute_bwd(g, row_of, g_weight=None, dx=None, dweight=None, stream=None):
+    """(dx [tokens, cols], dweight [tokens, topk]) from the gradients g [rows,
+    cols] and g_weight [rows] of mfx_moe_permute_fwd's outputs; dweight is
+    None without g_weight."""
+    tokens, topk = _moe_maps(g, row_of, None)
+    rows, cols = _moe_data(g, "g", None)
+    dx = g.new_empty((tokens, cols)) if dx is None else _like(dx, "dx", (tokens, cols), g.dtype)
+    if g_weight is not None:
+        _like(g_weight, "g_weight", (rows,), torch.float32)
+        dweight = (torch.empty((tokens, topk), dtype=torch.float32, device=g.device) if dweight is None
+                   else _like(dweight, "dweight", (tokens, topk), torch.float32))
+    elif dweight is not None:
+        raise ValueError("dweight needs g_weight")
+    _call("mfx_moe_permute_bwd", dtype_code(g.dtype), tokens, topk, cols, rows, _ptr(g), _ptr(row_of), _ptr(g_weight),
+          _ptr(dx), _ptr(dweight), _stream(stream, g))
+    return dx, dweight
+
+
+def mfx_moe_unpermute_fwd(y, row_of, weight=None, out=None, stream=None):
+    """out [tokens, cols] = sum over a token's rows of y [rows, cols], times
+    weight [tokens, topk] (fp32) where given."""
+    tokens, topk = _moe_maps(y, row_of, None)
+    rows, cols = _moe_data(y, "y", None)
+    if weight is not None:
+        _like(weight, "weight", (tokens, topk), torch.float32)
+    out = y.new_empty((tokens, cols)) if out is None else _like(out, "out", (tokens, cols), y.dtype)
+    _call("mfx_moe_unpermute_fwd", dtype_code(y.dtype), tokens, topk, cols, rows, _ptr(y), _ptr(row_of), _ptr(weight),
+          _ptr(out), _stream(stream, y))
+    return out
+
+
+def mfx_moe_unpermute_bwd(g, y, row_of, slot_of, weight=None, dy=None, dweight=None, need_dweight=None, stream=None):
+    """(dy [rows, cols], dweight [tokens, topk]) from the gradient g [tokens,
+    cols] of mfx_moe_unpermute_fwd's output.  dweight is formed where weight
+    is given (need_dweight overrides); without it y may be None."""
+    tokens, topk = _moe_maps(g, row_of, slot_of)
+    _, cols = _moe_data(g, "g", tokens)
+    rows = slot_of.shape[0]
+    if weight is not None:
+        _like(weight, "weight", (tokens, topk), torch.float32)
+    if y is not None:
+        _like(y, "y", (rows, cols), g.dtype)
+    if need_dweight is None:
+        need_dweight = weight is not None or dweight is not None
+    if need_dweight:
+        if y is None:
+            raise ValueError("dweight needs y")
+        dweight = (torch.empty((tokens, topk), dtype=torch.float32, device=g.device) if dweight is None
+                   else _like(dweight, "dweight", (tokens, topk), torch.float32))
+    else:
+        dweight = None
+    dy = g.new_empty((rows, cols)) if dy is None else _like(dy, "dy", (rows, cols), g.dtype)
+    _call("mfx_moe_unpermute_bwd", dtype_code(g.dtype), tokens, topk, cols, rows, _ptr(g), _ptr(y), _ptr(row_of),
+          _ptr(slot_of), _ptr(weight), _ptr(dy), _ptr(dweight), _stream(stream, g))
+    return dy, dweight
+
+
+# ---------------------------------------------------------------------------
 # bias-dropout-add
 # ---------------------------------------------------------------------------
 def mfx_bias_dropout_add_train(x, bias, residual, p, seed, offset=0, elem_base=0, out=None,
@@ -537,6 +679,44 @@ def mfx_bias_dropout_add_bwd_packed(g, keep_bits, p, dx=None, dresidual=None, re
     _call("mfx_bias_dropout_add_bwd_packed", dtype_code(g.dtype), rdt, rows, cols, _ptr(g), _ptr(keep_bits),
           float(p), _ptr(dx), _ptr(dresidual), _stream(stream, g))
     return dx, dresidual
+
+
+def mfx_bias_dropout_add_train_nomask(x, bias, residual, p, seed, offset=0, elem_base=0, out=None, stream=None):
+    """out of mfx_bias_dropout_add_train, without writing a mask; the backward
+    regenerates it (mfx_bias_dropout_add_bwd with keep_mask=None)."""
+    _cuda(x, "x")
+    _cuda(bias, "bias", x.dtype)
+    _cuda(residual, "residual")
+    if residual.shape != x.shape:
+        raise ValueError("residual must have x's shape")
+    out = torch.empty_like(x) if out is None else _like(out, "out", x.shape, x.dtype)
+    rows, cols = _rows_cols(x)
+    if bias is not None and bias.numel() != cols:
+        raise ValueError("bias must have one element per column of x")
+    _call("mfx_bias_dropout_add_train_nomask", dtype_code(x.dtype), dtype_code(residual.dtype), rows, cols, _ptr(x),
+          _ptr(bias), _ptr(residual), float(p), int(seed) % 2**64, int(offset) % 2**64, int(elem_base), _ptr(out),
+          _stream(stream, x))
+    return out
+
+
+def _dropout(name, x, p, seed, offset, elem_base, out, what, stream):
+    _cuda(x, what[0])
+    out = torch.empty_like(x) if out is None else _like(out, what[1], x.shape, x.dtype)
+    _call(name, dtype_code(x.dtype), x.numel(), _ptr(x), float(p), int(seed) % 2**64, int(offset) % 2**64,
+          int(elem_base), _ptr(out), _stream(stream, x))
+    return out
+
+
+def mfx_dropout_fwd(x, p, seed, offset=0, elem_base=0, out=None, stream=None):
+    """out = dropout(x, p); the mask is a function of (seed, offset, element
+    index) and is not stored."""
+    return _dropout("mfx_dropout_fwd", x, p, seed, offset, elem_base, out, ("x", "out"), stream)
+
+
+def mfx_dropout_bwd(g, p, seed, offset=0, elem_base=0, dx=None, stream=None):
+    """dx of mfx_dropout_fwd from the gradient g and the forward's p, seed,
+    offset and elem_base."""
+    return _dropout("mfx_dropout_bwd", g, p, seed, offset, elem_base, dx, ("g", "dx"), stream)
 
 
 # ---------------------------------------------------------------------------

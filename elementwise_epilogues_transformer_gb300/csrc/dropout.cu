@@ -108,7 +108,7 @@ __device__ __forceinline__ uint2 combine8_pairs(uint32_t xw[4], const float b[8]
 // cols/8.  Unit u = elements [8u, 8u + 8) = exactly Philox block
 // elem_base/8 + u, so one generator call serves the thread's 8 elements.
 // ---------------------------------------------------------------------------
-template <typename TX, typename TR, bool TRAIN>
+template <typename TX, typename TR, bool TRAIN, bool KEEP = true>
 __global__ void __launch_bounds__(kThreads, MFX_MINB_BDA)
 bda_fixed(const TX* x, const TX* __restrict__ bias, const TR* __restrict__ res, TX* out,
           uint8_t* __restrict__ keep, int64_t units, int64_t cols, float scale, uint32_t thresh,
@@ -151,7 +151,7 @@ bda_fixed(const TX* x, const TX* __restrict__ bias, const TR* __restrict__ res, 
                                                  [&](int j) { return word16(blk, j); });
                 narrow8(v, rx[k]);
                 st8(out + uk * 8, rx[k]);
-                if (TRAIN)
+                if (TRAIN && KEEP)
                     st8(keep + uk * 8, kb);
             }
         }
@@ -204,8 +204,9 @@ static_assert(pipe_smem_bytes<float, float, true>() <= (int)kMaxBlockSmem &&
 // global index e0), with the arithmetic of combine8: the head and tail of a
 // pipelined call, whose elements are not whole 16-byte units.
 // With PACKED the keep flags are bits of a bit mask and [i0, i0 + cnt) is
-// one of its bytes (i0 % 8 == 0, cnt <= 8).
-template <typename TX, typename TR, bool TRAIN, bool PACKED = false>
+// one of its bytes (i0 % 8 == 0, cnt <= 8).  Without KEEP no flags are
+// written (here and in the kernels below).
+template <typename TX, typename TR, bool TRAIN, bool PACKED = false, bool KEEP = true>
 __device__ __forceinline__ void bda_elems(const TX* x, const TX* __restrict__ bias, const TR* __restrict__ res,
                                           TX* out, uint8_t* __restrict__ keep, int64_t i0, int cnt, int64_t c,
                                           int64_t cols, float scale, uint32_t thresh, uint64_t seed,
@@ -223,7 +224,7 @@ __device__ __forceinline__ void bda_elems(const TX* x, const TX* __restrict__ bi
             t = kept ? __fmul_rn(t, scale) : 0.0f;
             if (PACKED)
                 bits |= (uint32_t)kept << j;
-            else
+            else if (KEEP)
                 keep[i0 + j] = (uint8_t)kept;
         }
         store1(out + i0 + j, __fadd_rn(t, r));
@@ -243,7 +244,7 @@ __device__ __forceinline__ void bda_elems(const TX* x, const TX* __restrict__ bi
 // With PACKED (training, no head) keep is a bit mask: unit u's flags are
 // byte u.  PHASED (training, phase != 0) draws two generator blocks per unit;
 // the other instances never carry that code.
-template <typename TX, typename TR, bool TRAIN, bool PACKED = false, bool PHASED = false>
+template <typename TX, typename TR, bool TRAIN, bool PACKED = false, bool PHASED = false, bool KEEP = true>
 __global__ void __launch_bounds__(kPipeThreads, TRAIN ? MFX_PIPE_MINB_BDA_TRAIN : MFX_PIPE_MINB_BDA)
 bda_pipe(const TX* x, const TX* __restrict__ bias, const TR* __restrict__ res, TX* out,
          uint8_t* __restrict__ keep, int64_t units, int64_t cols, float scale, uint32_t thresh,
@@ -370,7 +371,7 @@ bda_pipe(const TX* x, const TX* __restrict__ bias, const TR* __restrict__ res, T
                 st8(out + u * 8, rx);
                 if (TRAIN && PACKED)
                     keep[u] = (uint8_t)keep_bits8(kb);
-                else if (TRAIN)
+                else if (TRAIN && KEEP)
                     st8(keep + u * 8, kb);
             }
         }
@@ -378,11 +379,11 @@ bda_pipe(const TX* x, const TX* __restrict__ bias, const TR* __restrict__ res, T
     }
     if (blockIdx.x == 0 && t == 0) {
         if (!PACKED)
-            bda_elems<TX, TR, TRAIN>(x, bias, res, out, keep, -head, head, 0, cols, scale, thresh, seed, offset,
-                                     e_head);
-        bda_elems<TX, TR, TRAIN, PACKED>(x, bias, res, out, keep, units * 8, tail,
-                                         (c_off + (units % cols) * 8) % cols, cols, scale, thresh, seed, offset,
-                                         (block_base + (uint64_t)units) * 8 + phase);
+            bda_elems<TX, TR, TRAIN, false, KEEP>(x, bias, res, out, keep, -head, head, 0, cols, scale, thresh, seed,
+                                                  offset, e_head);
+        bda_elems<TX, TR, TRAIN, PACKED, KEEP>(x, bias, res, out, keep, units * 8, tail,
+                                               (c_off + (units % cols) * 8) % cols, cols, scale, thresh, seed, offset,
+                                               (block_base + (uint64_t)units) * 8 + phase);
     }
 }
 
@@ -392,7 +393,7 @@ bda_pipe(const TX* x, const TX* __restrict__ bias, const TR* __restrict__ res, T
 // is not 0 a unit straddles two generator blocks; element j then reads word
 // (o + j) % 8 of block (elem_base + 8u) / 8 + (o + j) / 8.
 // ---------------------------------------------------------------------------
-template <typename TX, typename TR, bool TRAIN, bool PACKED = false>
+template <typename TX, typename TR, bool TRAIN, bool PACKED = false, bool KEEP = true>
 __global__ void __launch_bounds__(kThreads)
 bda_generic(const TX* x, const TX* __restrict__ bias, const TR* __restrict__ res, TX* out,
             uint8_t* __restrict__ keep, int64_t n, int64_t cols, int64_t dcol, float scale,
@@ -431,7 +432,7 @@ bda_generic(const TX* x, const TX* __restrict__ bias, const TR* __restrict__ res
         store8f(out + i0, vec_x, cnt, v);
         if (TRAIN && PACKED) {
             keep[u] = (uint8_t)(keep_bits8(kb) & ((1u << cnt) - 1u));
-        } else if (TRAIN) {
+        } else if (TRAIN && KEEP) {
             if (vec_m && cnt == 8) {
                 st8(keep + i0, kb);
             } else {
@@ -849,7 +850,7 @@ int launch_bwd_dbias(const void* g, const uint8_t* keep, void* dx, void* dres, v
     return st != MFX_OK ? st : launch_dbias_finish(dtype_code<TX>(), ws, J_gen, cols, dbias, s);
 }
 
-template <typename TX, typename TR, bool TRAIN, bool PACKED = false>
+template <typename TX, typename TR, bool TRAIN, bool PACKED = false, bool KEEP = true>
 int launch(const void* x, const void* bias, const void* res, void* out, uint8_t* keep, int64_t n,
            int64_t cols, float p, uint64_t seed, uint64_t offset, uint64_t elem_base, cudaStream_t s)
 {
@@ -863,7 +864,7 @@ int launch(const void* x, const void* bias, const void* res, void* out, uint8_t*
     const float scale = TRAIN ? 1.0f / (1.0f - p) : 1.0f;
     const bool vec_x = aligned16(x) && aligned16(out);
     const bool vec_r = aligned16(res);
-    const bool vec_m = !TRAIN || aligned8(keep);
+    const bool vec_m = !TRAIN || !KEEP || aligned8(keep);
     const bool fixed_ok = vec_x && vec_r && vec_m && cols % 8 == 0 && elem_base % 8 == 0 &&
                           (!bias || aligned16(bias));
     // the pipeline takes any width when x, out and the residual sit the same
@@ -875,49 +876,49 @@ int launch(const void* x, const void* bias, const void* res, void* out, uint8_t*
     // (a bit mask takes the pipeline without a head: its units are its bytes)
     const bool same = mis % sizeof(TX) == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == mis &&
                       ((reinterpret_cast<uintptr_t>(res) + head * sizeof(TR)) & 15u) == 0 &&
-                      (!TRAIN || PACKED || ((reinterpret_cast<uintptr_t>(keep) + head) & 7u) == 0) &&
+                      (!TRAIN || PACKED || !KEEP || ((reinterpret_cast<uintptr_t>(keep) + head) & 7u) == 0) &&
                       (!PACKED || head == 0);
     if (same && MFX_PIPE_BDA && n - head >= 8) {
         const int phase = TRAIN ? (int)((elem_base + head) % 8) : 0;
-        const auto kern = phase ? bda_pipe<TX, TR, TRAIN, PACKED, true> : bda_pipe<TX, TR, TRAIN, PACKED, false>;
+        const auto kern = phase ? bda_pipe<TX, TR, TRAIN, PACKED, true, KEEP>
+                                : bda_pipe<TX, TR, TRAIN, PACKED, false, KEEP>;
         constexpr size_t smem = pipe_smem_bytes<TX, TR, TRAIN>();
         const int64_t units = (n - head) / 8;
         const Grid grid = plan_fixed_any((const void*)kern, kPipeThreads, smem, units, cols);
         if (grid.fixed) {
             kern<<<(unsigned)grid.blocks, kPipeThreads, smem, s>>>(
-                xp + head, bp, rp + head, op + head, TRAIN ? keep + head : keep, units, cols, scale, thresh, seed,
+                xp + head, bp, rp + head, op + head, TRAIN && KEEP ? keep + head : keep, units, cols, scale, thresh, seed,
                 offset, (elem_base + head) / 8, grid.S, head, (int)((n - head) % 8), head % cols, elem_base, phase);
             return launch_status();
         }
     }
     if (fixed_ok && !PACKED) {
-        const Grid grid = plan_grid((const void*)bda_fixed<TX, TR, TRAIN>, n / 8, cols / 8, true);
+        const Grid grid = plan_grid((const void*)bda_fixed<TX, TR, TRAIN, KEEP>, n / 8, cols / 8, true);
         if (grid.fixed) {
-            bda_fixed<TX, TR, TRAIN><<<(unsigned)grid.blocks, kThreads, 0, s>>>(
+            bda_fixed<TX, TR, TRAIN, KEEP><<<(unsigned)grid.blocks, kThreads, 0, s>>>(
                 xp, bp, rp, op, keep, n / 8, cols, scale, thresh, seed, offset, elem_base / 8);
             return launch_status();
         }
     }
-    const Grid grid = plan_grid((const void*)bda_generic<TX, TR, TRAIN, PACKED>, (n + 7) / 8, 0, false);
+    const Grid grid = plan_grid((const void*)bda_generic<TX, TR, TRAIN, PACKED, KEEP>, (n + 7) / 8, 0, false);
     const int64_t dcol = (grid.blocks * kThreads * 8) % cols;
-    bda_generic<TX, TR, TRAIN, PACKED><<<(unsigned)grid.blocks, kThreads, 0, s>>>(
+    bda_generic<TX, TR, TRAIN, PACKED, KEEP><<<(unsigned)grid.blocks, kThreads, 0, s>>>(
         xp, bp, rp, op, keep, n, cols, dcol, scale, thresh, seed, offset, elem_base, vec_x, vec_r, vec_m);
     return launch_status();
 }
 
-template <bool TRAIN, bool PACKED = false>
+template <bool TRAIN, bool PACKED = false, bool KEEP = true>
 int dispatch(int x_dt, int r_dt, const void* x, const void* bias, const void* res, void* out,
              uint8_t* keep, int64_t n, int64_t cols, float p, uint64_t seed, uint64_t offset,
              uint64_t elem_base, cudaStream_t s)
 {
+    const auto go = [&](auto tx, auto tr) {
+        return launch<decltype(tx), decltype(tr), TRAIN, PACKED, KEEP>(x, bias, res, out, keep, n, cols, p, seed,
+                                                                       offset, elem_base, s);
+    };
     if (x_dt == MFX_BF16)
-        return r_dt == MFX_BF16
-                   ? launch<bf16, bf16, TRAIN, PACKED>(x, bias, res, out, keep, n, cols, p, seed, offset, elem_base, s)
-                   : launch<bf16, float, TRAIN, PACKED>(x, bias, res, out, keep, n, cols, p, seed, offset, elem_base,
-                                                        s);
-    return r_dt == MFX_BF16
-               ? launch<float, bf16, TRAIN, PACKED>(x, bias, res, out, keep, n, cols, p, seed, offset, elem_base, s)
-               : launch<float, float, TRAIN, PACKED>(x, bias, res, out, keep, n, cols, p, seed, offset, elem_base, s);
+        return r_dt == MFX_BF16 ? go(bf16{}, bf16{}) : go(bf16{}, float{});
+    return r_dt == MFX_BF16 ? go(float{}, bf16{}) : go(float{}, float{});
 }
 
 int check(int x_dt, int r_dt, int64_t rows, int64_t cols, float p, int64_t* n_out)
@@ -1043,6 +1044,60 @@ extern "C" int mfx_bias_dropout_add_train_packed(int x_dt, int res_dt, int64_t r
         return MFX_ERR_ALIAS;
     return dispatch<true, true>(x_dt, res_dt, x, bias, residual, out, keep_bits, n, cols, p, seed, offset,
                                 elem_base, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int mfx_bias_dropout_add_train_nomask(int x_dt, int res_dt, int64_t rows, int64_t cols, const void* x,
+                                                 const void* bias, const void* residual, float p, uint64_t seed,
+                                                 uint64_t offset, uint64_t elem_base, void* out, void* stream)
+{
+    using namespace mfx;
+    int64_t n = 0;
+    int st = check(x_dt, res_dt, rows, cols, p, &n);
+    if (st != MFX_OK || n == 0)
+        return st;
+    if (!x || !residual || !out)
+        return MFX_ERR_NULL;
+    if (elem_base > UINT64_MAX - (uint64_t)n)
+        return MFX_ERR_SHAPE;
+    const int64_t xe = dtype_bytes(x_dt), re = dtype_bytes(res_dt);
+    const int64_t xb = n * xe, rb = n * re, bb = cols * xe;
+    if (partial_overlap(x, xb, out, xb) || overlaps(residual, rb, out, xb) || overlaps(bias, bb, out, xb))
+        return MFX_ERR_ALIAS;
+    return dispatch<true, false, false>(x_dt, res_dt, x, bias, residual, out, nullptr, n, cols, p, seed, offset,
+                                        elem_base, static_cast<cudaStream_t>(stream));
+}
+
+namespace mfx {
+namespace {
+// Plain dropout is its own backward: the same keep flags on the values or on
+// their gradient.
+int dropout_entry(int dt, int64_t n, const void* x, float p, uint64_t seed, uint64_t offset, uint64_t elem_base,
+                  void* out, void* stream)
+{
+    int64_t m = 0;
+    int st = check(dt, dt, n, 1, p, &m);
+    if (st != MFX_OK || n == 0)
+        return st;
+    st = bwd_check(dt, dt, n, x, nullptr, elem_base, out, nullptr, 0);
+    if (st != MFX_OK)
+        return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dt == MFX_BF16 ? launch_bwd<bf16, bf16>(x, nullptr, out, nullptr, n, p, seed, offset, elem_base, s)
+                          : launch_bwd<float, float>(x, nullptr, out, nullptr, n, p, seed, offset, elem_base, s);
+}
+}  // namespace
+}  // namespace mfx
+
+extern "C" int mfx_dropout_fwd(int dt, int64_t n, const void* x, float p, uint64_t seed, uint64_t offset,
+                               uint64_t elem_base, void* out, void* stream)
+{
+    return mfx::dropout_entry(dt, n, x, p, seed, offset, elem_base, out, stream);
+}
+
+extern "C" int mfx_dropout_bwd(int dt, int64_t n, const void* g, float p, uint64_t seed, uint64_t offset,
+                               uint64_t elem_base, void* dx, void* stream)
+{
+    return mfx::dropout_entry(dt, n, g, p, seed, offset, elem_base, dx, stream);
 }
 
 extern "C" int mfx_bias_dropout_add_bwd_packed(int x_dt, int res_dt, int64_t rows, int64_t cols, const void* g,

@@ -267,6 +267,72 @@ int mfx_relbias_softmax_dropout_bwd(int dt, int64_t b, int64_t np, int64_t sq, i
                                     void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Tokens sorted by expert and back, with weights applied, and the gradients: */
+/* what makes, and takes up again, the rows of expert MLPs (whose activations */
+/* are the weighted SwiGLU and the weighted squared ReLU above).             */
+/*                                                                           */
+/* Slot t * topk + j is choice j of token t.  The sorted layout has the slots */
+/* of expert 0, then of expert 1, ..., in slot order within an expert; each   */
+/* expert's rows begin at a multiple of `align` (1 = packed; tiles of a       */
+/* grouped matrix product otherwise).  Rows without a slot are padding.       */
+/* ------------------------------------------------------------------------ */
+
+/* Rows that the layout needs at most: tokens * topk + min(experts, tokens *
+ * topk) * (align - 1); -1 for negative or overflowing sizes. */
+int64_t mfx_moe_rows(int64_t tokens, int64_t topk, int64_t experts, int64_t align);
+
+/* The maps of the sorted layout, by a stable counting sort.
+ * expert_of: [tokens, topk]; a value outside [0, experts) has no row (a
+ * choice that the router dropped).  capacity > 0 keeps the first `capacity`
+ * slots of each expert and drops the others; 0 keeps all.
+ * rows: rows of the sorted buffers, at least mfx_moe_rows() (or, with a
+ * capacity, experts * capacity rounded up to align, if that is less), else
+ * MFX_ERR_SHAPE.  1 <= experts <= 4096; tokens * topk and rows below 2^31.
+ * row_of:  [tokens, topk] row of each slot, -1 for none.
+ * slot_of: [rows] slot of each row, -1 for padding.
+ * offsets: [experts + 1] first row of each expert, and the end of the last.
+ * counts:  [experts] slots of each expert that have a row.
+ * All int32.  Workspace protocol as for the fused bias gradients (the size
+ * may be 0: up to 2048 slots need none, and one kernel does it all). */
+int mfx_moe_sort(int64_t tokens, int64_t topk, int64_t experts, int64_t align, int64_t capacity, int64_t rows,
+                 const int32_t* expert_of, int32_t* row_of, int32_t* slot_of, int32_t* offsets, int32_t* counts,
+                 void* workspace, size_t* workspace_bytes, void* stream);
+
+/* out[row_of[t, j]] = x[t], padding rows zero; with weight, also
+ * out_weight[row_of[t, j]] = weight[t, j] (0 on padding), the per-row weight
+ * that the weighted activations take.
+ * x: [tokens, cols], out: [rows, cols] of dtype dt; weight: [tokens, topk]
+ * fp32 or NULL; out_weight: [rows] fp32, required iff weight.  Outputs must
+ * not overlap anything else -> MFX_ERR_ALIAS.  Entries of the maps outside
+ * their range count as -1 (here and below). */
+int mfx_moe_permute_fwd(int dt, int64_t tokens, int64_t topk, int64_t cols, int64_t rows,
+                        const void* x, const int32_t* row_of, const int32_t* slot_of, const float* weight,
+                        void* out, float* out_weight, void* stream);
+
+/* dx[t] = sum_j g[row_of[t, j]] (fp32 sum in choice order, rounded once), and
+ * with g_weight (the gradient [rows] of out_weight) dweight[t, j] =
+ * g_weight[row_of[t, j]], 0 where the slot has no row. */
+int mfx_moe_permute_bwd(int dt, int64_t tokens, int64_t topk, int64_t cols, int64_t rows,
+                        const void* g, const int32_t* row_of, const float* g_weight,
+                        void* dx, float* dweight, void* stream);
+
+/* out[t] = sum_j weight[t, j] * y[row_of[t, j]] (fp32 sum in choice order,
+ * rounded once); weight NULL counts as ones (weights that the activation has
+ * applied).  A token without rows is zeros.  y: [rows, cols], out: [tokens,
+ * cols]; out must not overlap anything else -> MFX_ERR_ALIAS. */
+int mfx_moe_unpermute_fwd(int dt, int64_t tokens, int64_t topk, int64_t cols, int64_t rows,
+                          const void* y, const int32_t* row_of, const float* weight,
+                          void* out, void* stream);
+
+/* dy[row_of[t, j]] = weight[t, j] * g[t] (dtype dt), padding rows zero;
+ * dweight[t, j] = sum_c g[t, c] * y[row_of[t, j], c] (fp32, in a fixed order;
+ * 0 where the slot has no row), or NULL (not formed; y is then not read).
+ * Outputs must not overlap anything else -> MFX_ERR_ALIAS. */
+int mfx_moe_unpermute_bwd(int dt, int64_t tokens, int64_t topk, int64_t cols, int64_t rows,
+                          const void* g, const void* y, const int32_t* row_of, const int32_t* slot_of,
+                          const float* weight, void* dy, float* dweight, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Bias + dropout + residual add, fusions page §3.2-§3.3                     */
 /* (_bias_dropout_add_func(x_with_bias, residual, prob, training) and its    */
 /* two entry points bias_dropout_add_fused_train / _inference).              */
@@ -307,6 +373,27 @@ int mfx_bias_dropout_add_train_packed(int x_dt, int res_dt, int64_t rows, int64_
                                       const void* x, const void* bias, const void* residual,
                                       float p, uint64_t seed, uint64_t offset, uint64_t elem_base,
                                       void* out, uint8_t* keep_bits, void* stream);
+
+/* mfx_bias_dropout_add_train without a mask: the same elements are kept and
+ * out is the same bits, but no keep flags are written.  The backward draws
+ * them again: mfx_bias_dropout_add_bwd (or _dbias) with keep_mask NULL and
+ * this call's p, seed, offset and elem_base.  8 instead of 9 bytes per
+ * element (bf16 x, fp32 residual). */
+int mfx_bias_dropout_add_train_nomask(int x_dt, int res_dt, int64_t rows, int64_t cols,
+                                      const void* x, const void* bias, const void* residual,
+                                      float p, uint64_t seed, uint64_t offset, uint64_t elem_base,
+                                      void* out, void* stream);
+
+/* Plain dropout (embeddings, a layer stack's last output) whose mask is never
+ * stored: out[i] = keep ? x[i] * (1 / (1 - p)) : 0 for n elements of dtype dt,
+ * element i having the index elem_base + i of the generator described at
+ * mfx_bias_dropout_add_train.  The backward does the same to the gradient:
+ * dx[i] = keep ? g[i] * (1 / (1 - p)) : 0.  out may equal x (dx g); any other
+ * overlap -> MFX_ERR_ALIAS.  Bit-exact: fp32 multiply, one rounding. */
+int mfx_dropout_fwd(int dt, int64_t n, const void* x, float p, uint64_t seed, uint64_t offset,
+                    uint64_t elem_base, void* out, void* stream);
+int mfx_dropout_bwd(int dt, int64_t n, const void* g, float p, uint64_t seed, uint64_t offset,
+                    uint64_t elem_base, void* dx, void* stream);
 
 /* Inference: x = (x + bias) + r~, IN PLACE in x (§3.2: when not training the
  * bias add, dropout and residual add all run in place).  p, seed and offset
