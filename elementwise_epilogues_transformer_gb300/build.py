@@ -18,8 +18,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmfx.so")
 
-SOURCES = ["mfx_abi.cu", "gelu.cu", "glu.cu", "dropout.cu", "dbias.cu", "sqrelu.cu", "softmax.cu", "relbias.cu", "moe.cu"]
-HEADERS = ["mfx_device.cuh", "mfx_host.h", "mfx_pipe.cuh"]
+SOURCES = ["mfx_abi.cu", "gelu.cu", "glu.cu", "dropout.cu", "dbias.cu", "sqrelu.cu", "softmax.cu", "relbias_fwd.cu",
+           "relbias_bwd.cu", "moe.cu"]
+HEADERS = ["mfx_device.cuh", "mfx_host.h", "mfx_pipe.cuh", "relbias.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-O2",
               "-I", INCLUDE, "-I", CSRC, "--expt-relaxed-constexpr", "-Xptxas", "-v"]

@@ -1,0 +1,636 @@
+// relbias.cuh -- what the forward and the backward of the relative-position-
+// bias softmax share: the bucket function and its window in shared memory,
+// rows and chunks, scores, keep flags, and the host's argument checks and
+// launch plan.  See relbias_fwd.cu for the operation and the layout.
+#pragma once
+
+#include <cmath>
+#include <type_traits>
+
+#include "mfx_device.cuh"
+#include "mfx_host.h"
+
+namespace mfx {
+namespace relbias {
+
+constexpr int kTeam = 256;            // threads per row where rows are not long
+constexpr int kLongTeam = 512;        // ... where they are
+constexpr int kSmallBlock = 128;      // threads of a block whose teams are a warp or less
+constexpr int kMaxBuckets = 256;      // buckets of a table
+constexpr int kMaxSide = 128;         // buckets of one direction
+constexpr int kMaxDistance = 2048;    // keeps the window and its sums within a block's shared memory
+constexpr int kMaxCluster = 8;        // blocks that may share a row
+constexpr int kBwdBlocksPerSm = 16;   // most blocks of a backward grid per SM (what its workspace goes by)
+constexpr float kLog2eF = 1.4426950408889634f;
+
+// The bucket function of one direction: distances below `first` have a bucket
+// each, bucket first + 1 + j begins at border[j], and `reach` is where the
+// last one begins.
+struct Buckets {
+    int num, side, first, reach, hi;  // hi: first position right of the query whose bias no longer changes
+    int border[kMaxSide];
+};
+
+struct Geom {
+    int sq, sk, np;
+    int64_t rows;              // b * sq: rows of one head
+    int64_t mask_b, mask_np, mask_sq;  // strides of the mask in elements (0 = broadcast)
+    int q_start;
+    const int32_t* seq_start;  // per batch, or null
+    int64_t slices;            // blocks (clusters) per head
+    int team, teams, cluster;  // threads per row, rows per block, blocks per row
+    int blocks;                // register blocks that a row takes
+    int causal, table_bf16;
+    int exact;                 // a row is exactly the chunks that its threads hold
+    int drop;                  // p > 0
+    int phase0;                // (phase0 + element index) mod 8 = 0 at a chunk's start
+    float scale, scale2;       // the score scale; the same times log2 e
+    float keep_scale, keep_log2, keep_inv;  // 1 / (1 - p), its base-2 logarithm, and 1 - p
+    uint32_t thresh_hi;        // keep threshold in the upper half-word
+    uint64_t elem_base;
+    uint32_t off_lo, off_hi;   // the generator's counter words 2 and 3
+    uint32_t key0[10], key1[10];  // its key of each round
+};
+
+// mask_block() with the rounds' keys read from the parameters instead of kept
+// in registers.
+__device__ __forceinline__ uint4 keep_block(const Geom& g, uint64_t j)
+{
+    uint4 c = make_uint4((uint32_t)j, (uint32_t)(j >> 32), g.off_lo, g.off_hi);
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+        uint32_t lo0, hi0, lo1, hi1;
+        mul_hilo(0xD2511F53u, c.x, lo0, hi0);
+        mul_hilo(0xCD9E8D57u, c.z, lo1, hi1);
+        c = make_uint4(hi1 ^ c.y ^ g.key0[i], lo1, hi0 ^ c.w ^ g.key1[i], lo0);
+    }
+    return c;
+}
+
+// The window holds the bias (times log2 e) of the positions around the query:
+// entry i is the one at k - pos = i - reach, -8 <= i <= reach + hi + 8, the
+// ones past either end repeating the far values.  A chunk of 8 begins at any
+// entry, so each entry is stored with the three after it as one 16-byte
+// vector and a chunk is two of them; entries lie by residue mod 8 first, so
+// that the lanes of a warp, whose chunks are 8 entries apart, read
+// consecutive vectors.
+__device__ __host__ __forceinline__ int window_stride(const Buckets& w) { return ((w.reach + w.hi + 16) >> 3) + 1; }
+__device__ __forceinline__ int window_slot(int stride, int i)
+{
+    const int u = i + 8;
+    return (u & 7) * stride + (u >> 3);
+}
+inline size_t window_bytes(const Buckets& w) { return (size_t)8 * window_stride(w) * sizeof(float4); }
+
+__device__ __forceinline__ int side_bucket(const Buckets& w, int n)
+{
+    if (n < w.first)
+        return n;
+    int lo = 0, hi = w.side - w.first - 1;  // borders not above n
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (w.border[mid] <= n)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    return w.first + lo;
+}
+
+// First distance of bucket v of a direction (v = side: past the window).
+__device__ __forceinline__ int side_start(const Buckets& w, int v)
+{
+    return v <= w.first ? v : v >= w.side ? w.reach + 1 : w.border[v - w.first - 1];
+}
+
+// The bias of head h at window entry i, times log2 e.
+__device__ __forceinline__ float window_bias(const Buckets& w, const Geom& g, const void* table, int h, int i)
+{
+    if (!table)
+        return 0.0f;
+    const int last = w.reach + w.hi, rel = (i < 0 ? 0 : i > last ? last : i) - w.reach;
+    const int u = rel <= 0 ? side_bucket(w, -rel) : side_bucket(w, rel) + w.side;
+    const int64_t at = (int64_t)u * g.np + h;
+    return kLog2eF * (g.table_bf16 ? load1(static_cast<const bf16*>(table) + at)
+                                   : load1(static_cast<const float*>(table) + at));
+}
+
+// Fills the block's window for head h (call with all threads, then meet).
+// Each value is looked up once and put in the up to four vectors it is part of.
+__device__ __forceinline__ void fill_window(const Buckets& w, const Geom& g, const void* table, int h, float4* win)
+{
+    const int last = w.reach + w.hi, stride = window_stride(w);
+    float* f = reinterpret_cast<float*>(win);
+    for (int i = (int)threadIdx.x - 8; i <= last + 11; i += blockDim.x) {
+        const float v = window_bias(w, g, table, h, i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i - k >= -8 && i - k <= last + 8)
+                f[4 * window_slot(stride, i - k) + k] = v;
+    }
+}
+
+// 2^t by the hardware exponential (2 ulp); results below 2^-126 flush to zero.
+__device__ __forceinline__ float exp2_of(float t)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+    return r;
+}
+
+// (Pairs are for the layout only: the two-lane instructions measured slower
+// here, 0.104 against 0.094 ms for a 2x8x2048x2048 forward.)
+__device__ __forceinline__ float2 pfma(float2 a, float2 b, float2 c)
+{
+    return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
+}
+__device__ __forceinline__ float2 padd(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ float2 pmul(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
+
+// Eight elements as four pairs.
+__device__ __forceinline__ void pairs_of(const Raw8<bf16>& r, float2 (&f)[4])
+{
+    f[0] = widen2(r.v.x), f[1] = widen2(r.v.y), f[2] = widen2(r.v.z), f[3] = widen2(r.v.w);
+}
+__device__ __forceinline__ void pairs_of(const Raw8<float>& r, float2 (&f)[4])
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        f[2 * h] = make_float2(__uint_as_float(r.v[h].x), __uint_as_float(r.v[h].y));
+        f[2 * h + 1] = make_float2(__uint_as_float(r.v[h].z), __uint_as_float(r.v[h].w));
+    }
+}
+__device__ __forceinline__ void narrow_pairs(const float2 (&f)[4], Raw8<bf16>& r)
+{
+    r.v = make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                     pack_bf16x2(f[3].x, f[3].y));
+}
+__device__ __forceinline__ void narrow_pairs(const float2 (&f)[4], Raw8<float>& r)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        r.v[h] = make_uint4(__float_as_uint(f[2 * h].x), __float_as_uint(f[2 * h].y),
+                            __float_as_uint(f[2 * h + 1].x), __float_as_uint(f[2 * h + 1].y));
+}
+
+// Three-operand maximum and minimum (NaN operands are passed over).
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c)
+{
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max_of(float t, const float2 (&f)[4])
+{
+    return max3(max3(t, f[0].x, f[0].y), max3(f[1].x, f[1].y, f[2].x), max3(f[2].y, f[3].x, f[3].y));
+}
+__device__ __forceinline__ float min_of(const float2 (&f)[4])
+{
+    return min3(min3(f[0].x, f[0].y, f[1].x), min3(f[1].y, f[2].x, f[2].y), fminf(f[3].x, f[3].y));
+}
+
+// Sets the elements of a chunk outside [0, end) to v.
+__device__ __forceinline__ void fill_outside(float2 (&f)[4], int k0, int end, float v)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[i].x = k0 + 2 * i >= 0 && k0 + 2 * i < end ? f[i].x : v;
+        f[i].y = k0 + 2 * i + 1 >= 0 && k0 + 2 * i + 1 < end ? f[i].y : v;
+    }
+}
+
+// Elements [k0, k0 + 8) of a row, of which [0, end) exist.  FAST: the row is
+// whole chunks of 16-byte vectors.  Otherwise a chunk that is not whole, or
+// not aligned, is read element by element, zero where there is none.
+template <typename T, bool FAST>
+__device__ __forceinline__ void load_chunk(const T* p, int k0, int end, Raw8<T>& raw)
+{
+    if (FAST || (k0 >= 0 && k0 + 8 <= end && (reinterpret_cast<uintptr_t>(p) & 15u) == 0)) {
+        ld8(p, raw);
+    } else {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] = k0 + j >= 0 && k0 + j < end ? load1(p + j) : 0.0f;
+        narrow8(f, raw);
+    }
+}
+
+template <typename T, bool FAST>
+__device__ __forceinline__ void store_chunk(T* p, int k0, int end, const float2 (&f)[4])
+{
+    if (FAST || (k0 >= 0 && k0 + 8 <= end && (reinterpret_cast<uintptr_t>(p) & 15u) == 0)) {
+        Raw8<T> raw;
+        narrow_pairs(f, raw);
+        st8(p, raw);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (k0 + j >= 0 && k0 + j < end)
+                store1(p + j, j & 1 ? f[j >> 1].y : f[j >> 1].x);
+    }
+}
+
+// What a row's chunks share.
+template <typename T>
+struct Row {
+    int64_t r;        // row index of the tensor
+    int64_t e0;       // element index of chunk 0 in the tensor
+    uint64_t block0;  // generator block of chunk 0
+    const T* mask;    // its mask row, or null
+    int a, pos, end;  // chunk phase, clamped query position, keys that take part: [0, end)
+    int chunks;       // chunks of the row
+};
+
+// The rows that a team walks: row = first + n * step of the b * sq rows of one
+// head, as batch and query, advanced without divisions.
+struct Walk {
+    int i, q, step_i, step_q;
+    __device__ __forceinline__ Walk(int64_t row, int64_t step, int64_t sq)
+        : i((int)(row / sq)), q((int)(row % sq)), step_i((int)(step / sq)), step_q((int)(step % sq))
+    {
+    }
+    __device__ __forceinline__ void next(int sq)
+    {
+        i += step_i;
+        q += step_q;
+        if (q >= sq) {
+            q -= sq;
+            ++i;
+        }
+    }
+};
+
+template <typename T, bool FAST>
+__device__ __forceinline__ Row<T> row_at(const Geom& g, const Buckets& w, const T* mask, int h, const Walk& at,
+                                         bool live)
+{
+    Row<T> o;
+    o.r = ((int64_t)at.i * g.np + h) * g.sq + at.q;
+    const int64_t e = o.r * (int64_t)g.sk;
+    o.a = FAST ? 0 : (int)((uint64_t)(g.phase0 + e) & 7u);
+    o.e0 = e - o.a;
+    o.block0 = (g.elem_base + (uint64_t)e) >> 3;
+    o.mask = nullptr;
+    o.pos = o.end = o.chunks = 0;
+    if (!live)
+        return o;
+    o.pos = g.q_start + at.q;
+    if (g.seq_start) {
+        const int64_t pos = (int64_t)o.pos + g.seq_start[at.i], lo = -w.reach - 1, hi = g.sk + w.reach;
+        o.pos = (int)(pos < lo ? lo : pos > hi ? hi : pos);
+    }
+    o.end = g.causal ? (o.pos < 0 ? 0 : o.pos + 1 < g.sk ? o.pos + 1 : g.sk) : g.sk;
+    o.chunks = (int)((g.sk + o.a + 7) >> 3);
+    if (mask)
+        o.mask = mask + (at.i * g.mask_b + h * g.mask_np + at.q * g.mask_sq);
+    return o;
+}
+
+// Whether any position of the chunk whose first is `rel` from the query has a
+// bias of its own (-reach - 7 < rel < hi).
+__device__ __forceinline__ bool near_chunk(const Buckets& w, int rel)
+{
+    return (unsigned)(rel + w.reach + 6) < (unsigned)(w.reach + w.hi + 6);
+}
+
+// Scores of the chunk at k0 from its raw x, times log2 e: x * scale + bias
+// (+ mask - shift), -inf where no key takes part (CHECK: the chunk may have
+// such keys).  A key whose mask is -inf is left out whatever x holds there.
+// Call with whole warps: one with a near chunk reads the window in all lanes,
+// far ones at its ends.
+template <typename T, bool FAST, bool MASK, bool CHECK>
+__device__ __forceinline__ void score_chunk(const Raw8<T>& raw, const Row<T>& row, const Geom& g, const Buckets& w,
+                                            const float4* win, float far_lo, float far_hi, int k0, float shift,
+                                            float2 (&s)[4])
+{
+    pairs_of(raw, s);
+    const int rel = k0 - row.pos;
+    if (!__any_sync(0xFFFFFFFFu, near_chunk(w, rel))) {
+        const float2 b = f2(rel >= w.hi ? far_hi : far_lo);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s[i] = pfma(s[i], f2(g.scale2), b);
+    } else {
+        const int stride = window_stride(w), i0 = min(max(rel + w.reach, -8), w.reach + w.hi + 1);
+        const float4 lo = win[window_slot(stride, i0)], hi = win[window_slot(stride, i0 + 4)];
+        s[0] = pfma(s[0], f2(g.scale2), make_float2(lo.x, lo.y));
+        s[1] = pfma(s[1], f2(g.scale2), make_float2(lo.z, lo.w));
+        s[2] = pfma(s[2], f2(g.scale2), make_float2(hi.x, hi.y));
+        s[3] = pfma(s[3], f2(g.scale2), make_float2(hi.z, hi.w));
+    }
+    if (MASK && row.mask) {
+        Raw8<T> mraw;
+        load_chunk<T, FAST>(row.mask + (CHECK && FAST && k0 >= row.end ? 0 : k0), k0, row.end, mraw);
+        float2 m[4];
+        pairs_of(mraw, m);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[i].x = m[i].x == -INFINITY ? -INFINITY : fmaf(m[i].x - shift, kLog2eF, s[i].x);
+            s[i].y = m[i].y == -INFINITY ? -INFINITY : fmaf(m[i].y - shift, kLog2eF, s[i].y);
+        }
+    }
+    if (CHECK)
+        fill_outside(s, k0, row.end, -INFINITY);
+}
+
+// Keep flags of a chunk applied to its values: 16-bit word j of the block
+// belongs to element j.  On packed bf16 pairs the flags become bit masks: with
+// H the top bit of each half, (w | H) - (t & ~H) has it set where the low 15
+// bits of w reach those of t, one three-input operation adds the top bits'
+// say, and a byte permutation spreads it.
+__device__ __forceinline__ void drop_pairs(float2 (&v)[4], const uint4& blk, uint32_t thresh_hi)
+{
+    const uint32_t w[4] = {blk.x, blk.y, blk.z, blk.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i].x = (w[i] << 16) >= thresh_hi ? v[i].x : 0.0f;
+        v[i].y = w[i] >= thresh_hi ? v[i].y : 0.0f;
+    }
+}
+__device__ __forceinline__ uint32_t keep_bits2(uint32_t w, uint32_t t2)
+{
+    const uint32_t z = (w | 0x80008000u) - (t2 & 0x7FFF7FFFu);
+    const uint32_t ge = (w & ~t2) | (~(w ^ t2) & z);
+    uint32_t m;
+    asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(m) : "r"(ge));
+    return m;
+}
+__device__ __forceinline__ void drop_raw(Raw8<bf16>& r, const uint4& blk, uint32_t thresh_hi)
+{
+    const uint32_t t2 = thresh_hi | (thresh_hi >> 16);
+    r.v.x &= keep_bits2(blk.x, t2), r.v.y &= keep_bits2(blk.y, t2);
+    r.v.z &= keep_bits2(blk.z, t2), r.v.w &= keep_bits2(blk.w, t2);
+}
+__device__ __forceinline__ void drop_raw(Raw8<float>& r, const uint4& blk, uint32_t thresh_hi)
+{
+    float2 f[4];
+    pairs_of(r, f);
+    drop_pairs(f, blk, thresh_hi);
+    narrow_pairs(f, r);
+}
+
+// Reductions over the lanes of a team that share a warp: all 32, or (ANY) an
+// aligned group of 8, 16 or 32.
+template <bool ANY>
+__device__ __forceinline__ float lanes_max(float v, int lanes)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (!ANY || o < lanes)
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+template <bool ANY>
+__device__ __forceinline__ float lanes_sum(float v, int lanes)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (!ANY || o < lanes)
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+__device__ __forceinline__ float2 peer_pair(const float2* p, int rank)
+{
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), d;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(d) : "memory");
+    return v;
+}
+
+// (maximum, sum relative to it) of two parts of a row, in base-2 units.
+__device__ __forceinline__ float2 join(float2 a, float2 b)
+{
+    const float m = fmaxf(a.x, b.x);
+    if (m == -INFINITY)
+        return make_float2(m, a.y + b.y);
+    return make_float2(m, a.y * exp2_of(a.x - m) + b.y * exp2_of(b.x - m));
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+// Whether n^s * a^j >= b^j * a^s in whole numbers (all below 2^14, s and j at
+// most 64): products of up to 128 factors of 14 bits in 32-bit words.
+inline bool border_reached(int n, int s, int a, int b, int j)
+{
+    constexpr int kWords = 64;
+    uint32_t l[kWords] = {1}, r[kWords] = {1};
+    auto mul = [](uint32_t* v, uint32_t by) {
+        uint64_t carry = 0;
+        for (int i = 0; i < kWords; ++i) {
+            carry += (uint64_t)v[i] * by;
+            v[i] = (uint32_t)carry;
+            carry >>= 32;
+        }
+    };
+    for (int i = 0; i < s; ++i)
+        mul(l, n), mul(r, a);
+    for (int i = 0; i < j; ++i)
+        mul(l, a), mul(r, b);
+    for (int i = kWords - 1; i >= 0; --i)
+        if (l[i] != r[i])
+            return l[i] > r[i];
+    return true;
+}
+
+// Bucket j past the first ones begins at the least n with
+// steps * log(n / first) / log(far / first) >= j.  The logarithms decide where
+// they are clearly between whole numbers, whole-number products where not.
+inline bool make_buckets(int64_t num, int64_t far, bool bidirectional, Buckets* w)
+{
+    if (num == 0) {  // no bias: one window entry that stays zero
+        *w = Buckets{};
+        w->num = 0, w->side = 1, w->first = 1;
+        return true;
+    }
+    if (num < 2 || num > kMaxBuckets || (bidirectional && num % 2))
+        return false;
+    const int side = (int)(bidirectional ? num / 2 : num), first = side / 2, steps = side - first;
+    if (side < 2 || side > kMaxSide || far <= first || far > kMaxDistance)
+        return false;
+    struct Last {
+        int num, far, two;
+        Buckets w;
+    };
+    static thread_local Last last{0, 0, 0, {}};  // a model's calls share one bucket function
+    if (last.num != (int)num || last.far != (int)far || last.two != (int)bidirectional) {
+        Buckets& o = last.w;
+        o = Buckets{};
+        o.num = (int)num, o.side = side, o.first = first;
+        for (int j = 1; j < steps; ++j) {
+            const double t = first * std::pow((double)far / first, (double)j / steps);
+            int n = (int)std::ceil(t);
+            if (std::fabs(t - std::round(t)) < 1e-6 * t) {
+                n = (int)std::round(t) - 1;
+                while (!border_reached(n, steps, first, (int)far, j))
+                    ++n;
+            }
+            o.border[j - 1] = n;
+        }
+        o.reach = steps > 1 ? o.border[steps - 2] : first;
+        o.hi = bidirectional ? o.reach : 0;
+        last.num = (int)num, last.far = (int)far, last.two = bidirectional;
+    }
+    *w = last.w;
+    return true;
+}
+
+struct Args {
+    int dt;
+    int64_t b, np, sq, sk;
+    float scale;
+    int table_dt;
+    const void* table;
+    int64_t num_buckets, max_distance;
+    int bidirectional;
+    const void* mask;
+    int64_t mask_b, mask_np, mask_sq;
+    int causal;
+    int64_t q_start;
+    const int32_t* seq_start;
+    float p;
+    uint64_t seed, offset, elem_base;
+    int64_t n, mask_bytes, table_bytes;  // set by check()
+};
+
+// Sizes, dtypes and probabilities (no pointer of the data is looked at).
+inline int check(Args& a, Buckets* w)
+{
+    a.n = a.mask_bytes = a.table_bytes = 0;
+    if (!valid_dtype(a.dt) || (a.table && !valid_dtype(a.table_dt)))
+        return MFX_ERR_DTYPE;
+    if (!(a.p >= 0.0f && a.p < 1.0f))
+        return MFX_ERR_PROB;
+    constexpr int64_t kMost = (int64_t)1 << 29;
+    if (a.b < 0 || a.np < 0 || a.sq < 0 || a.sk < 0 || a.b > kMost || a.np > kMost || a.sq > kMost || a.sk > kMost ||
+        a.q_start > kMost || a.q_start < -kMost)
+        return MFX_ERR_SHAPE;
+    int64_t n = 1, bytes = 0;
+    if (!mul_ok(a.b, a.np, &n) || !mul_ok(n, a.sq, &n) || !mul_ok(n, a.sk, &n) || !mul_ok(n, 16, &bytes))
+        return MFX_ERR_SHAPE;
+    if (a.mask && ((a.mask_b != 1 && a.mask_b != a.b) || (a.mask_np != 1 && a.mask_np != a.np) ||
+                   (a.mask_sq != 1 && a.mask_sq != a.sq)))
+        return MFX_ERR_SHAPE;
+    if (!make_buckets(a.table ? a.num_buckets : 0, a.max_distance, a.bidirectional != 0, w) ||
+        (a.table && a.num_buckets == 0))
+        return MFX_ERR_SHAPE;
+    if (a.p > 0.0f && a.elem_base > UINT64_MAX - (uint64_t)n)
+        return MFX_ERR_SHAPE;
+    a.n = n;
+    if (a.mask && n)
+        a.mask_bytes = a.mask_b * a.mask_np * a.mask_sq * a.sk * dtype_bytes(a.dt);
+    if (a.table && !mul_ok(a.np, a.num_buckets * dtype_bytes(a.table_dt), &a.table_bytes))
+        return MFX_ERR_SHAPE;
+    return MFX_OK;
+}
+
+inline Geom make_geom(const Args& a, const Buckets& w, const void* x)
+{
+    Geom g = {};
+    g.sq = (int)a.sq, g.sk = (int)a.sk, g.np = (int)a.np, g.rows = a.b * a.sq;
+    g.mask_sq = a.mask_sq == 1 ? 0 : a.sk;
+    g.mask_np = a.mask_np == 1 ? 0 : a.mask_sq * a.sk;
+    g.mask_b = a.mask_b == 1 ? 0 : a.mask_np * a.mask_sq * a.sk;
+    // positions past the reach of every key have the same buckets wherever
+    // they are (with starts of the sequences' own, up to what those may add)
+    const int64_t slack = a.seq_start ? 0 : w.reach + 1, lo = -a.sq - slack, hi = a.sk + slack;
+    g.q_start = (int)(a.seq_start ? a.q_start : a.q_start < lo ? lo : a.q_start > hi ? hi : a.q_start);
+    g.seq_start = a.seq_start;
+    g.drop = a.p > 0.0f, g.causal = a.causal != 0, g.table_bf16 = a.table_dt == MFX_BF16;
+    // chunks follow the generator's blocks; without dropout, the buffer's vectors
+    g.phase0 = a.p > 0.0f ? (int)(a.elem_base & 7)
+                          : (int)((reinterpret_cast<uintptr_t>(x) / (size_t)dtype_bytes(a.dt)) & 7);
+    g.scale = a.scale, g.scale2 = (float)((double)a.scale * 1.4426950408889634);
+    g.keep_scale = 1.0f / (1.0f - a.p), g.keep_log2 = (float)std::log2((double)g.keep_scale), g.keep_inv = 1.0f - a.p;
+    const double t = std::ceil((double)a.p * 65536.0);
+    g.thresh_hi = (uint32_t)(t > 65535.0 ? 65535.0 : t) << 16;
+    g.elem_base = a.elem_base, g.off_lo = (uint32_t)a.offset, g.off_hi = (uint32_t)(a.offset >> 32);
+    for (uint32_t i = 0; i < 10; ++i)
+        g.key0[i] = (uint32_t)a.seed + i * 0x9E3779B9u, g.key1[i] = (uint32_t)(a.seed >> 32) + i * 0xBB67AE85u;
+    return g;
+}
+
+// Chunks of the longest row.
+inline int64_t chunks_of(const Geom& g, bool fast) { return (g.sk + (fast ? 0 : 7) + 7) / 8; }
+
+// Threads, rows and register blocks of a launch; returns the chunks that a
+// thread holds.  A thread holds up to `most` chunks, so that a row's
+// reduction and bookkeeping are small beside its work; rows of at most 32
+// chunks share a warp, 8, 16 or 32 lanes to a row.
+inline int plan(Geom& g, bool fast, int most)
+{
+    const int64_t chunks = chunks_of(g, fast);
+    g.cluster = 1, g.teams = 1, g.blocks = 1;
+    if (chunks <= 32 * most) {
+        g.team = chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
+        g.teams = kSmallBlock / g.team;
+        const int c = chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4;
+        g.exact = fast && chunks == (int64_t)g.team * c;
+        return c;
+    }
+    int64_t team = ((chunks + most - 1) / most + 31) / 32 * 32;
+    const int64_t held = (int64_t)kLongTeam * most;
+    g.team = (int)(team < kLongTeam ? team : kLongTeam);
+    g.blocks = (int)(chunks > held ? (chunks + held - 1) / held : 1);
+    g.exact = fast && chunks == (int64_t)g.team * most;
+    return most;
+}
+
+// Blocks per head, of which `slots` run at a time over all heads: the number
+// of waves, up to 8, whose longest block times waves is least, a block's start
+// (its window, say) counted as `extra` rows.
+inline int64_t slices_for(const Geom& g, int64_t slots, int64_t extra)
+{
+    const int64_t need = (g.rows + g.teams - 1) / g.teams;  // most that have a row each
+    int64_t best = 1, cost = INT64_MAX;
+    for (int64_t waves = 1; waves <= 8; ++waves) {
+        int64_t n = slots * waves / g.np;
+        n = n < 1 ? 1 : n < need ? n : need;
+        const int64_t rounds = (n * g.np + slots - 1) / slots;
+        const int64_t c = rounds * ((need + n - 1) / n + extra);
+        if (c < cost)
+            cost = c, best = n;
+    }
+    return best;
+}
+
+// Whether every row is whole chunks of 16-byte vectors.
+inline bool whole_chunks(const Args& a, const void* p, const void* q, const void* r)
+{
+    return a.sk % 8 == 0 && aligned16(p) && aligned16(q) && aligned16(r) && aligned16(a.mask) &&
+           (a.p == 0.0f || a.elem_base % 8 == 0);
+}
+
+// Calls f(type, dropout, mask, whole chunks) with the values as types.  Rows
+// that are not whole chunks have one kernel for any dropout and mask, which
+// asks at run time.
+template <typename F>
+int by_variant(const Args& a, bool fast, F f)
+{
+    using Y = std::true_type;
+    using N = std::false_type;
+    const auto one = [&](auto t) {
+        if (!fast)
+            return f(t, Y{}, Y{}, N{});
+        if (a.p > 0.0f)
+            return a.mask ? f(t, Y{}, Y{}, Y{}) : f(t, Y{}, N{}, Y{});
+        return a.mask ? f(t, N{}, Y{}, Y{}) : f(t, N{}, N{}, Y{});
+    };
+    return a.dt == MFX_BF16 ? one(bf16{}) : one(float{});
+}
+
+}  // namespace relbias
+}  // namespace mfx

@@ -1,0 +1,359 @@
+// relbias_bwd.cu -- backward of the relative-position-bias softmax with
+// dropout (relbias_fwd.cu has the operation).
+//
+// P and the keep flags are formed again from x, the row statistics and the
+// generator.  With Q = P / (1 - p), formed with log2(1 / (1 - p)) added to the
+// exponent, and z = keep * dy:  D = sum Q z,  dS = Q (z - (1 - p) D),  so the
+// dropout's factor costs nothing per element.
+//
+// The table's gradient takes the form of the bias: far positions add into two
+// registers a thread, near ones into a window in shared memory.  A row's
+// chunks all begin at the same residue (mod 8) of the window, so the window
+// is kept once per residue and a chunk adds to two aligned 16-byte vectors of
+// its row's.  Within a row every vector belongs to one thread, rows of a warp
+// or block follow one another, and teams that share a warp take turns: no
+// atomics, a fixed order.  Each block leaves its per-bucket sums in the
+// workspace, and a second kernel adds those in block order.
+#include "relbias.cuh"
+
+namespace mfx {
+namespace relbias {
+namespace {
+
+constexpr int kBwdBlocksPerSm = 16;  // most blocks of a backward grid per SM (what its workspace goes by)
+
+// Window sums: vector pair u of residue r holds the sums of entries
+// 8 u + r - 8 .. + 7; first the low halves of all pairs, then the high ones.
+__device__ __host__ __forceinline__ int sum_vectors(const Buckets& w) { return 8 * window_stride(w); }
+inline size_t sum_bytes(const Buckets& w) { return (size_t)2 * sum_vectors(w) * sizeof(float4); }
+
+__device__ __forceinline__ void add4(float4* p, float2 a, float2 b)
+{
+    float4 v = *p;
+    v.x += a.x, v.y += a.y, v.z += b.x, v.w += b.y;
+    *p = v;
+}
+
+template <typename T, int C, bool DROP, bool MASK, bool FAST, int MT>
+__global__ void __launch_bounds__(MT, MT > kTeam ? 1 : 2)
+relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, const T* __restrict__ mask,
+            const void* __restrict__ table, float* __restrict__ ws, const __grid_constant__ Geom g,
+            const __grid_constant__ Buckets w)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    float4* win = reinterpret_cast<float4*>(smem);
+    __shared__ float part[2][MT / 32];
+    __shared__ float2 far_part[MT / 32];
+    constexpr bool LONG = MT > kTeam, ANY = C == 1;
+    const int blocks = LONG ? g.blocks : 1;
+    const int h = (int)(blockIdx.x / g.slices);
+    const int64_t slice = blockIdx.x % g.slices;
+    const int tid = threadIdx.x % g.team, tm = threadIdx.x / g.team;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lanes = g.team < 32 ? g.team : 32, warps = g.team >> 5;
+    const int last = w.reach + w.hi, stride = window_stride(w), vectors = sum_vectors(w);
+    const int sets = g.team > 32 ? 1 : (int)(blockDim.x >> 5);  // one set of sums a block, or one a warp
+    float4* acc = win + 8 * stride + (g.team > 32 ? 0 : warp) * 2 * vectors;
+    fill_window(w, g, table, h, win);
+    if (ws)
+        for (int i = threadIdx.x; i < 2 * vectors * sets; i += blockDim.x)
+            win[8 * stride + i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    __syncthreads();
+    const float far_lo = win[window_slot(stride, 0)].x, far_hi = win[window_slot(stride, last)].x;
+    float sum_lo = 0.0f, sum_hi = 0.0f;
+
+    const int64_t step = g.slices * g.teams;
+    int64_t row = slice * g.teams + tm;
+    Walk at(row, step, g.sq);
+    int slot = 0;
+    for (int64_t first = slice * g.teams; first < g.rows; first += step, row += step, at.next(g.sq), slot ^= 1) {
+        const Row<T> o = row_at<T, FAST>(g, w, MASK ? mask : nullptr, h, at, row < g.rows);
+        float shift = 0.0f, lse = 0.0f;
+        if (row < g.rows) {
+            shift = stats[2 * o.r], lse = stats[2 * o.r + 1];
+            lse = lse == -INFINITY ? 0.0f : lse;  // an empty row: every score is -inf
+        }
+        const float ref = DROP ? g.keep_log2 - lse : -lse;
+        const auto run = [&](auto check) {
+            constexpr bool CHECK = decltype(check)::value;
+            float2 Q[C][4], D2 = f2(0.0f);
+            Raw8<T> z[C];
+            const auto load_block = [&](int blk) {
+                Raw8<T> rx[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int ch = (blk * C + c) * g.team + tid, k0 = ch * 8 - o.a;
+                    const int k = 8 * (CHECK && FAST && k0 >= o.end ? 0 : ch);
+                    load_chunk<T, FAST>(x + o.e0 + k, k0, o.end, rx[c]);
+                    load_chunk<T, FAST>(dy + o.e0 + k, k0, o.end, z[c]);
+                }
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int ch = (blk * C + c) * g.team + tid, k0 = ch * 8 - o.a;
+                    score_chunk<T, FAST, MASK, CHECK>(rx[c], o, g, w, win, far_lo, far_hi, k0, shift, Q[c]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        Q[c][i] = make_float2(exp2_of(Q[c][i].x + ref), exp2_of(Q[c][i].y + ref));
+                    if (DROP && g.drop && (!CHECK || k0 < o.end))
+                        drop_raw(z[c], keep_block(g, o.block0 + ch), g.thresh_hi);
+                    // what the upstream gradient holds at keys left out does not count
+                    if ((CHECK || MASK) && min_of(Q[c]) == 0.0f) {
+                        float2 f[4];
+                        pairs_of(z[c], f);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            f[i] = make_float2(Q[c][i].x == 0.0f ? 0.0f : f[i].x, Q[c][i].y == 0.0f ? 0.0f : f[i].y);
+                        narrow_pairs(f, z[c]);
+                    }
+                }
+            };
+            for (int blk = 0; blk < blocks; ++blk) {
+                load_block(blk);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    float2 f[4];
+                    pairs_of(z[c], f);
+                    float2 t = pmul(Q[c][0], f[0]);
+#pragma unroll
+                    for (int i = 1; i < 4; ++i)
+                        t = pfma(Q[c][i], f[i], t);
+                    D2 = padd(D2, t);
+                }
+            }
+            float D = lanes_sum<ANY>(D2.x + D2.y, lanes);
+            if (warps > 1) {
+                if (lane == 0)
+                    part[slot][warp] = D;
+                __syncthreads();
+                D = part[slot][0];
+                for (int i = 1; i < warps; ++i)
+                    D += part[slot][i];
+            } else {
+                __syncwarp();  // the previous row's window sums before this row's
+            }
+            if (DROP)
+                D *= g.keep_inv;
+            for (int blk = 0; blk < blocks; ++blk) {
+                if (LONG && blocks > 1)
+                    load_block(blk);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int ch = (blk * C + c) * g.team + tid, k0 = ch * 8 - o.a;
+                    float2 v[4];
+                    pairs_of(z[c], v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = pmul(Q[c][i], padd(v[i], f2(-D)));
+                    if (CHECK)
+                        fill_outside(v, k0, o.end, 0.0f);
+                    if (ws) {
+                        const int rel = k0 - o.pos;
+                        const bool near = near_chunk(w, rel) && (!CHECK || k0 < o.end);
+                        const float2 t = padd(padd(v[0], v[1]), padd(v[2], v[3]));
+                        const float far = near ? 0.0f : t.x + t.y;
+                        sum_lo += rel >= w.hi ? 0.0f : far;
+                        sum_hi += rel >= w.hi ? far : 0.0f;
+                        if (__any_sync(0xFFFFFFFFu, near)) {
+                            float4* p = acc + window_slot(stride, rel + w.reach);
+                            if (!ANY) {
+                                if (near) {
+                                    add4(p, v[0], v[1]);
+                                    add4(p + vectors, v[2], v[3]);
+                                }
+                            } else {
+                                for (int turn = 0; turn < 32; turn += lanes) {
+                                    if (near && turn == (lane & ~(lanes - 1))) {
+                                        add4(p, v[0], v[1]);
+                                        add4(p + vectors, v[2], v[3]);
+                                    }
+                                    __syncwarp();
+                                }
+                            }
+                        }
+                    }
+                    if (CHECK && ch >= o.chunks)
+                        continue;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = pmul(v[i], f2(g.scale));
+                    store_chunk<T, FAST>(dx + o.e0 + 8 * ch, k0, g.sk, v);
+                }
+            }
+        };
+        if constexpr (FAST) {
+            bool full = g.exact && o.end == g.sk;
+            if (ANY)
+                full = __all_sync(0xFFFFFFFFu, full);
+            if (full)
+                run(std::false_type{});
+            else
+                run(std::true_type{});
+        } else {
+            run(std::true_type{});
+        }
+    }
+    if (!ws)
+        return;
+    // the block's sum of each bucket: its entries of every residue and set,
+    // in order, and the far sums (entries past the window's ends are far too)
+    sum_lo = lanes_sum<false>(sum_lo, 32);
+    sum_hi = lanes_sum<false>(sum_hi, 32);
+    if (lane == 0)
+        far_part[warp] = make_float2(sum_lo, sum_hi);
+    __syncthreads();
+    const float* sums = reinterpret_cast<const float*>(win + 8 * stride);
+    const auto entry = [&](int i) {
+        float t = 0.0f;
+        for (int k = 0; k < sets; ++k)
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const int u = i + 8 - r;  // vector pair u / 8 of residue r, element u mod 8
+                if (u >= 0 && (u >> 3) < stride)
+                    t += sums[4 * (k * 2 * vectors + (u & 4 ? vectors : 0) + r * stride + (u >> 3)) + (u & 3)];
+            }
+        return t;
+    };
+    const int nw = blockDim.x >> 5;
+    for (int u = warp; u < w.num; u += nw) {
+        const bool right = u >= w.side;
+        const int v = right ? u - w.side : u;
+        const bool lo = u == w.side - 1, hi = u == (w.hi ? w.num - 1 : 0);
+        int n0 = side_start(w, v);
+        const int n1 = side_start(w, v + 1);
+        if (right && n0 < 1)
+            n0 = 1;
+        float t = 0.0f;
+        for (int n = n0 + lane; n < n1; n += 32)
+            t += entry(right ? w.reach + n : w.reach - n);
+        if (lo && lane < 8)
+            t += entry(lane - 8);
+        if (hi && lane < 8)
+            t += entry(last + 1 + lane);
+        t = lanes_sum<false>(t, 32);
+        if (lane == 0) {
+            for (int k = 0; k < nw; ++k)
+                t += (lo ? far_part[k].x : 0.0f) + (hi ? far_part[k].y : 0.0f);
+            ws[(slice * w.num + u) * g.np + h] = t;
+        }
+    }
+    pdl_launch_dependents();
+}
+
+// Most blocks per head of a backward: what its workspace is sized by, whatever
+// kernel the pointers' alignment leads to.
+int64_t bwd_slices(const Args& a)
+{
+    const int64_t most = ((int64_t)sm_count() * kBwdBlocksPerSm + a.np - 1) / a.np;
+    return a.b * a.sq < most ? a.b * a.sq : most;
+}
+
+template <typename T, int C, bool DROP, bool MASK, bool FAST, int MT>
+int launch_bwd(Geom g, const Buckets& w, const Args& a, const void* dy, const void* x, const float* stats, void* dx,
+               void* dtable, void* workspace, cudaStream_t s)
+{
+    const auto kern = relbias_bwd<T, C, DROP, MASK, FAST, MT>;
+    const size_t sums = dtable ? sum_bytes(w) : 0;
+    while (g.team <= 32 && g.team * g.teams > 32 && window_bytes(w) + sums * (g.team * g.teams / 32) > 64 * 1024)
+        g.teams /= 2;  // wide windows: fewer rows at a time
+    const int threads = g.team * g.teams;
+    const size_t smem = window_bytes(w) + sums * (g.team > 32 ? 1 : threads / 32);
+    const int64_t slots = (int64_t)sm_count() * occupancy((const void*)kern, threads, smem);
+    g.slices = slices_for(g, slots, 4);
+    if (g.slices > bwd_slices(a))
+        g.slices = bwd_slices(a);
+    if (g.slices * g.np > INT32_MAX)
+        return MFX_ERR_SHAPE;
+    kern<<<(unsigned)(g.slices * g.np), threads, smem, s>>>(
+        static_cast<const T*>(dy), static_cast<const T*>(x), stats, static_cast<T*>(dx), static_cast<const T*>(a.mask),
+        a.table, dtable ? static_cast<float*>(workspace) : nullptr, g, w);
+    const int st = launch_status();
+    if (st != MFX_OK || !dtable)
+        return st;
+    return launch_dbias_finish(a.table_dt, static_cast<const float*>(workspace), g.slices, (int64_t)w.num * g.np,
+                               dtable, s);
+}
+
+template <typename T, bool DROP, bool MASK, bool FAST>
+int dispatch_bwd(const Args& a, const Buckets& w, const void* dy, const void* x, const float* stats, void* dx,
+                 void* dtable, void* workspace, cudaStream_t s)
+{
+    // fp32 holds half the chunks: a chunk's gradient takes twice the registers
+    constexpr int kMost = sizeof(T) == 2 && FAST ? 4 : 2;
+    Geom g = make_geom(a, w, x);
+    const int c = plan(g, FAST, kMost);
+    const bool big = g.team * g.teams > kTeam || g.blocks > 1;
+    if (c == 1)
+        return launch_bwd<T, 1, DROP, MASK, FAST, kTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s);
+    if (c == 2 && kMost > 2)
+        return launch_bwd<T, 2, DROP, MASK, FAST, kTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s);
+    return big ? launch_bwd<T, kMost, DROP, MASK, FAST, kLongTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s)
+               : launch_bwd<T, kMost, DROP, MASK, FAST, kTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s);
+}
+
+}  // namespace
+}  // namespace relbias
+}  // namespace mfx
+
+extern "C" int mfx_relbias_softmax_dropout_bwd(int dt, int64_t b, int64_t np, int64_t sq, int64_t sk, const void* dy,
+                                               const void* x, const float* stats, float scale, int table_dt,
+                                               const void* table, int64_t num_buckets, int64_t max_distance,
+                                               int bidirectional, const void* mask, int64_t mask_b, int64_t mask_np,
+                                               int64_t mask_sq, int causal, int64_t q_start,
+                                               const int32_t* seq_start, float p, uint64_t seed, uint64_t offset,
+                                               uint64_t elem_base, void* dx, void* dtable, void* workspace,
+                                               size_t* workspace_bytes, void* stream)
+{
+    using namespace mfx;
+    using namespace mfx::relbias;
+    Args a{dt,     b,      np,      sq,      sk,     scale,   table_dt,  table, num_buckets, max_distance, bidirectional,
+           mask,   mask_b, mask_np, mask_sq, causal, q_start, seq_start, p,     seed,        offset,       elem_base,
+           0,      0,      0};
+    Buckets w;
+    int st = check(a, &w);
+    if (st != MFX_OK)
+        return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool query = workspace_bytes && !workspace;
+    if (query && !table) {
+        *workspace_bytes = 0;
+        return MFX_OK;
+    }
+    if (a.n == 0) {
+        if (query) {
+            *workspace_bytes = 0;
+            return MFX_OK;
+        }
+        if (!dtable || a.table_bytes == 0)
+            return MFX_OK;
+        return cudaMemsetAsync(dtable, 0, (size_t)a.table_bytes, s) == cudaSuccess ? MFX_OK
+                                                                                  : cuda_failure(cudaGetLastError());
+    }
+    if (!query) {
+        if (!dy || !x || !stats || !dx || (dtable && (!table || !workspace || !workspace_bytes)))
+            return MFX_ERR_NULL;
+        const int64_t bytes = a.n * dtype_bytes(dt), sb = b * np * sq * 8, tb = a.table_bytes;
+        if (partial_overlap(dy, bytes, dx, bytes) || partial_overlap(x, bytes, dx, bytes) ||
+            overlaps(mask, a.mask_bytes, dx, bytes) || overlaps(table, tb, dx, bytes) ||
+            overlaps(stats, sb, dx, bytes) || overlaps(seq_start, 4 * b, dx, bytes))
+            return MFX_ERR_ALIAS;
+        if (dtable) {
+            const int64_t wsb = (int64_t)*workspace_bytes;
+            const void* const other[] = {dy, x, dx, mask, stats, table, seq_start};
+            const int64_t size[] = {bytes, bytes, bytes, a.mask_bytes, sb, tb, 4 * b};
+            for (int i = 0; i < 7; ++i)
+                if (overlaps(dtable, tb, other[i], size[i]) || overlaps(workspace, wsb, other[i], size[i]))
+                    return MFX_ERR_ALIAS;
+            if (overlaps(dtable, tb, workspace, wsb))
+                return MFX_ERR_ALIAS;
+        }
+    }
+    if (query || dtable) {
+        bool asked = false;
+        st = dbias_workspace(bwd_slices(a), (int64_t)w.num * np, workspace, workspace_bytes, &asked);
+        if (st != MFX_OK || asked)
+            return st;
+    }
+    return by_variant(a, whole_chunks(a, x, dy, dx), [&](auto t, auto drop, auto masked, auto fast) {
+        return dispatch_bwd<decltype(t), decltype(drop)::value, decltype(masked)::value, decltype(fast)::value>(
+            a, w, dy, x, stats, dx, dtable, workspace, s);
+    });
+}

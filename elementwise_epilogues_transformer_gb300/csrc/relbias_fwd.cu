@@ -1,0 +1,346 @@
+// relbias_fwd.cu -- softmax of attention scores with a learned relative position
+// bias and dropout, forward and backward.
+//
+// Per score row (batch i, head h, query q at position pos):
+//   s_k = x_k * scale + table[bucket(k - pos), h] + mask_k,   P = softmax(s),
+//   y_k = keep_k * P_k / (1 - p),
+// and backwards, with P formed again from x and the row's statistics and the
+// keep flags from the generator (neither P nor the mask is ever stored),
+//   dP_k = keep_k * dy_k / (1 - p),  D = sum_k dP_k P_k,
+//   dS_k = P_k (dP_k - D),  dx_k = scale * dS_k,
+//   dtable[u, h] = sum of dS over the positions whose bucket is u.
+//
+// Layout: a team of threads (one or more warps) owns a row and keeps it in
+// registers, C chunks of 8 elements a thread; a chunk is exactly one block of
+// the generator (chunk boundaries sit where the element index is a multiple
+// of 8), so with 16-byte aligned buffers it is also one 16-byte access, at
+// any row length.  Rows longer than a team holds are walked in blocks, the
+// second walk reading what L2 still has; few long forward rows are split over
+// the blocks of a cluster, which exchange (maximum, sum) through distributed
+// shared memory.
+//
+// The bias needs no [np, sq, sk] tensor: along a row it is constant outside
+// the `reach` of the bucket function (the distance from which the last bucket
+// holds), and inside it comes from a window of 2 * reach + 1 values in shared
+// memory, built once per thread block, which works on one head.  The table's
+// gradient takes the same form: far positions add into two registers, near
+// ones into a shared-memory window with one slot per distance.  Within a row
+// every slot belongs to one thread, and rows follow one another behind the
+// row reduction's barrier, so the sums need no atomics and their order is
+// fixed; each block leaves its per-bucket sums in the workspace and a second
+// kernel adds those in block order.
+#include "relbias.cuh"
+
+namespace mfx {
+namespace relbias {
+namespace {
+
+// Sums and maxima over a team that may span warps (part) and the blocks of a
+// cluster (mine); `slot` alternates between calls so that one barrier each is
+// enough.
+struct Team {
+    float2 (*part)[kLongTeam / 32];
+    float2* mine;
+    int lanes, warps, warp0, cluster;
+};
+
+// (maximum, sum relative to it) over the team from each warp's.
+template <bool LONG>
+__device__ __forceinline__ float2 join_team(const Team& tm, float2 v, int slot)
+{
+    if (tm.warps <= 1)
+        return v;
+    if ((threadIdx.x & 31) == 0)
+        tm.part[slot][threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = tm.part[slot][0];
+    for (int i = 1; i < tm.warps; ++i)
+        v = join(v, tm.part[slot][i]);
+    if (LONG && tm.cluster > 1) {
+        if (threadIdx.x == 0)
+            tm.mine[slot] = v;
+        cluster_sync();
+        v = peer_pair(&tm.mine[slot], 0);
+        for (int i = 1; i < tm.cluster; ++i)
+            v = join(v, peer_pair(&tm.mine[slot], i));
+    }
+    return v;
+}
+
+// One row whose scores all lie far from zero (a mask of lowest values, say),
+// or that has no key left: the mask is shifted by its own maximum, which
+// leaves the softmax as it is and the scores their digits.  Element by
+// element, three passes; out of line, so that it costs other rows nothing.
+template <typename T, bool DROP, bool LONG>
+__device__ __noinline__ void shifted_row(const T* x, T* y, float* stats, const Row<T> o, const Geom& g,
+                                         const Buckets& w, const float4* win, const Team& tm, int rank, int tid,
+                                         int slot)
+{
+    const int step = g.team * tm.cluster, first = rank * g.team + tid, last = w.reach + w.hi;
+    const int64_t e = o.e0 + o.a;
+    float shift = -INFINITY;
+    for (int k = first; k < o.end; k += step)
+        shift = fmaxf(shift, load1(o.mask + k));
+    shift = join_team<LONG>(tm, make_float2(lanes_max<true>(shift, tm.lanes), 0.0f), slot ^ 1).x;
+    if (shift == -INFINITY)
+        shift = 0.0f;
+    const auto score = [&](int k) {
+        const float m = load1(o.mask + k);
+        const int i = k - o.pos + w.reach;
+        const float b = win[window_slot(window_stride(w), i < 0 ? 0 : i > last ? last : i)].x;
+        return m == -INFINITY ? -INFINITY : fmaf(m - shift, kLog2eF, fmaf(load1(x + e + k), g.scale2, b));
+    };
+    float m = -INFINITY, l = 0.0f;
+    for (int k = first; k < o.end; k += step)
+        m = fmaxf(m, score(k));
+    m = join_team<LONG>(tm, make_float2(lanes_max<true>(m, tm.lanes), 0.0f), slot).x;
+    const float ref = m == -INFINITY ? 0.0f : m;
+    for (int k = first; k < o.end; k += step)
+        l += exp2_of(score(k) - ref);
+    l = join_team<LONG>(tm, make_float2(ref, lanes_sum<true>(l, tm.lanes)), slot ^ 1).y;
+    if (stats && first == 0 && o.chunks) {
+        stats[2 * o.r] = shift;
+        stats[2 * o.r + 1] = m == -INFINITY ? m : m + log2f(l);
+    }
+    const float inv = m == -INFINITY && l == 0.0f ? 0.0f : 1.0f / l;
+    for (int k = first; o.chunks && k < g.sk; k += step) {
+        float v = k < o.end ? exp2_of(score(k) - ref) * inv : 0.0f;
+        if (DROP && g.drop && k < o.end)
+            v = word16(keep_block(g, o.block0 + ((k + o.a) >> 3)), (k + o.a) & 7) >= g.thresh_hi >> 16 ? v * g.keep_scale
+                                                                                                       : 0.0f;
+        store1(y + e + k, v);
+    }
+    // the next row's reduction may use either slot
+    if (tm.warps > 1)
+        __syncthreads();
+    if (LONG && tm.cluster > 1)
+        cluster_sync();
+}
+
+template <typename T, int C, bool DROP, bool MASK, bool FAST, int MT>
+__global__ void __launch_bounds__(MT, MT > kTeam ? 1 : sizeof(T) == 2 ? 3 : 2)
+relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ mask, const void* __restrict__ table,
+            const __grid_constant__ Geom g, const __grid_constant__ Buckets w)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    float4* win = reinterpret_cast<float4*>(smem);
+    __shared__ float2 part[2][kLongTeam / 32];
+    __shared__ float2 mine[2];
+    constexpr bool LONG = MT > kTeam, ANY = C == 1;
+    const int blocks = LONG ? g.blocks : 1, cluster = LONG ? g.cluster : 1;
+    const int rank = LONG ? (int)(blockIdx.x % cluster) : 0;
+    const int64_t unit = LONG ? blockIdx.x / cluster : blockIdx.x;
+    const int h = (int)(unit / g.slices);
+    const int64_t slice = unit % g.slices;
+    const int tid = threadIdx.x % g.team, tm = threadIdx.x / g.team;
+    const Team team{part, mine, g.team < 32 ? g.team : 32, g.team >> 5, 0, cluster};
+    fill_window(w, g, table, h, win);
+    __syncthreads();
+    const float far_lo = win[window_slot(window_stride(w), 0)].x;
+    const float far_hi = win[window_slot(window_stride(w), w.reach + w.hi)].x;
+
+    const int64_t step = g.slices * g.teams;
+    int64_t row = slice * g.teams + tm;
+    Walk at(row, step, g.sq);
+    int slot = 0;
+    for (int64_t first = slice * g.teams; first < g.rows; first += step, row += step, at.next(g.sq), slot ^= 1) {
+        const Row<T> o = row_at<T, FAST>(g, w, MASK ? mask : nullptr, h, at, row < g.rows);
+        const T* xr = x + o.e0;
+        T* yr = y + o.e0;
+        // CHECK: some chunk of the row is not there, or not all of it takes part
+        const auto run = [&](auto check) {
+            constexpr bool CHECK = decltype(check)::value;
+            float2 s[C][4];
+            float m = -INFINITY, l = 0.0f;
+            for (int blk = 0; blk < blocks; ++blk) {
+                const int c0 = (blk * cluster + rank) * (C * g.team) + tid;
+                Raw8<T> raw[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int ch = c0 + c * g.team, k0 = ch * 8 - o.a;
+                    load_chunk<T, FAST>(xr + 8 * (CHECK && FAST && k0 >= o.end ? 0 : ch), k0, o.end, raw[c]);
+                }
+                float t = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int k0 = (c0 + c * g.team) * 8 - o.a;
+                    score_chunk<T, FAST, MASK, CHECK>(raw[c], o, g, w, win, far_lo, far_hi, k0, 0.0f, s[c]);
+                    t = max_of(t, s[c]);
+                }
+                t = fmaxf(m, lanes_max<ANY>(t, team.lanes));
+                const float ref = t == -INFINITY ? 0.0f : t;
+                float2 sum = f2(0.0f);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[c][i] = make_float2(exp2_of(s[c][i].x - ref), exp2_of(s[c][i].y - ref));
+                    sum = padd(sum, padd(padd(s[c][0], s[c][1]), padd(s[c][2], s[c][3])));
+                }
+                l = (blk ? l * exp2_of(m - ref) : 0.0f) + (sum.x + sum.y);
+                m = t;
+            }
+            const float mw = m;  // what s is relative to
+            const float2 v = join_team<LONG>(team, make_float2(m, lanes_sum<ANY>(l, team.lanes)), slot);
+            m = v.x, l = v.y;
+            if (MASK && mask) {
+                // far from zero, or every sum below the type's range (teams that share a warp go together)
+                bool again = fabsf(m) > 96.0f && m < INFINITY;
+                if (ANY)
+                    again = __any_sync(0xFFFFFFFFu, again);
+                if (again) {
+                    shifted_row<T, DROP, LONG>(x, y, stats, o, g, w, win, team, rank, tid, slot);
+                    return;
+                }
+            }
+            if (stats && tid == 0 && rank == 0 && row < g.rows) {
+                stats[2 * o.r] = 0.0f;
+                stats[2 * o.r + 1] = m == -INFINITY ? m : m + log2f(l);
+            }
+            const float inv =
+                m == -INFINITY && l == 0.0f ? 0.0f : __fdividef(DROP && g.drop ? g.keep_scale : 1.0f, l);
+            const float f1 = mw == -INFINITY && l == l ? 0.0f : exp2_of(mw - m) * inv;
+            for (int blk = 0; blk < blocks; ++blk) {
+                const int c0 = (blk * cluster + rank) * (C * g.team) + tid;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int ch = c0 + c * g.team, k0 = ch * 8 - o.a;
+                    float f = f1;
+                    if (LONG && blocks > 1) {
+                        Raw8<T> raw;
+                        load_chunk<T, FAST>(xr + 8 * (FAST && k0 >= o.end ? 0 : ch), k0, o.end, raw);
+                        score_chunk<T, FAST, MASK, true>(raw, o, g, w, win, far_lo, far_hi, k0, 0.0f, s[c]);
+                        const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            s[c][i] = make_float2(exp2_of(s[c][i].x - ref), exp2_of(s[c][i].y - ref));
+                        f = inv;
+                    }
+                    if (CHECK && ch >= o.chunks)
+                        continue;
+                    float2 p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        p[i] = pmul(s[c][i], f2(f));
+                    if (DROP && g.drop && (!CHECK || k0 < o.end))
+                        drop_pairs(p, keep_block(g, o.block0 + ch), g.thresh_hi);
+                    if (CHECK)
+                        fill_outside(p, k0, o.end, 0.0f);
+                    store_chunk<T, FAST>(yr + 8 * ch, k0, g.sk, p);
+                }
+            }
+        };
+        if constexpr (FAST) {
+            bool full = g.exact && o.end == g.sk;
+            if (ANY)
+                full = __all_sync(0xFFFFFFFFu, full);
+            if (full)
+                run(std::false_type{});
+            else
+                run(std::true_type{});
+        } else {
+            run(std::true_type{});
+        }
+    }
+    if (LONG && cluster > 1)
+        cluster_sync();  // no block leaves while a peer may still read its pair
+}
+
+template <typename T, int C, bool DROP, bool MASK, bool FAST, int MT>
+int launch_fwd(Geom g, const Buckets& w, const Args& a, const void* x, void* y, float* stats, cudaStream_t s)
+{
+    const auto kern = relbias_fwd<T, C, DROP, MASK, FAST, MT>;
+    const size_t smem = window_bytes(w);
+    const int threads = g.team * g.teams;
+    const int64_t slots = (int64_t)sm_count() * occupancy((const void*)kern, threads, smem) / g.cluster;
+    g.slices = slices_for(g, slots > 0 ? slots : 1, 1);
+    const int64_t blocks = g.slices * g.np * g.cluster;
+    if (blocks > INT32_MAX)
+        return MFX_ERR_SHAPE;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)g.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g.cluster > 1 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<const T*>(x), static_cast<T*>(y), stats,
+                                             static_cast<const T*>(a.mask), a.table, (const Geom)g, (const Buckets)w);
+    return e == cudaSuccess ? launch_status() : cuda_failure(e);
+}
+
+template <typename T, bool DROP, bool MASK, bool FAST>
+int dispatch_fwd(const Args& a, const Buckets& w, const void* x, void* y, float* stats, cudaStream_t s)
+{
+    Geom g = make_geom(a, w, x);
+    int c = plan(g, FAST, 4);
+    const int64_t rows = a.b * a.np * a.sq, sms = sm_count(), chunks = chunks_of(g, FAST);
+    if (chunks > 32 && rows < 4 * sms) {
+        // few rows: as many threads on each as give every SM work, and rows
+        // too long for that over the blocks of a cluster
+        c = FAST ? 1 : 4;
+        while (g.cluster < kMaxCluster && rows * g.cluster < sms && chunks > 32 * c * g.cluster)
+            g.cluster *= 2;
+        while (c < 4 && chunks > (int64_t)kLongTeam * c * g.cluster)
+            c *= 4;
+        while (g.cluster < kMaxCluster && chunks > (int64_t)kLongTeam * c * g.cluster)
+            g.cluster *= 2;
+        const int64_t per = (int64_t)c * g.cluster, team = ((chunks + per - 1) / per + 31) / 32 * 32;
+        g.team = (int)(team < 64 ? 64 : team < kLongTeam ? team : kLongTeam);
+        g.teams = 1;
+        const int64_t held = g.team * per;
+        g.blocks = (int)((chunks + held - 1) / held);
+        g.exact = FAST && chunks == held;
+    }
+    const bool big = g.team * g.teams > kTeam || g.cluster > 1 || g.blocks > 1;
+    if constexpr (FAST) {
+        if (c == 1)
+            return big ? launch_fwd<T, 1, DROP, MASK, FAST, kLongTeam>(g, w, a, x, y, stats, s)
+                       : launch_fwd<T, 1, DROP, MASK, FAST, kTeam>(g, w, a, x, y, stats, s);
+        if (c == 2)
+            return launch_fwd<T, 2, DROP, MASK, FAST, kTeam>(g, w, a, x, y, stats, s);
+    } else if (c == 1) {
+        return launch_fwd<T, 1, DROP, MASK, FAST, kTeam>(g, w, a, x, y, stats, s);
+    }
+    return big ? launch_fwd<T, 4, DROP, MASK, FAST, kLongTeam>(g, w, a, x, y, stats, s)
+               : launch_fwd<T, 4, DROP, MASK, FAST, kTeam>(g, w, a, x, y, stats, s);
+}
+
+}  // namespace
+}  // namespace relbias
+}  // namespace mfx
+
+extern "C" int mfx_relbias_softmax_dropout_fwd(int dt, int64_t b, int64_t np, int64_t sq, int64_t sk, const void* x,
+                                               float scale, int table_dt, const void* table, int64_t num_buckets,
+                                               int64_t max_distance, int bidirectional, const void* mask,
+                                               int64_t mask_b, int64_t mask_np, int64_t mask_sq, int causal,
+                                               int64_t q_start, const int32_t* seq_start, float p, uint64_t seed,
+                                               uint64_t offset, uint64_t elem_base, void* y, float* stats,
+                                               void* stream)
+{
+    using namespace mfx;
+    using namespace mfx::relbias;
+    Args a{dt,     b,      np,      sq,      sk,     scale,   table_dt,  table, num_buckets, max_distance, bidirectional,
+           mask,   mask_b, mask_np, mask_sq, causal, q_start, seq_start, p,     seed,        offset,       elem_base,
+           0,      0,      0};
+    Buckets w;
+    const int st = check(a, &w);
+    if (st != MFX_OK || a.n == 0)
+        return st;
+    if (!x || !y)
+        return MFX_ERR_NULL;
+    const int64_t bytes = a.n * dtype_bytes(dt), sb = b * np * sq * 8;
+    if (partial_overlap(x, bytes, y, bytes) || overlaps(mask, a.mask_bytes, y, bytes) ||
+        overlaps(table, a.table_bytes, y, bytes) || overlaps(seq_start, 4 * b, y, bytes) ||
+        overlaps(stats, sb, y, bytes) || overlaps(stats, sb, x, bytes) || overlaps(stats, sb, mask, a.mask_bytes) ||
+        overlaps(stats, sb, table, a.table_bytes) || overlaps(stats, sb, seq_start, 4 * b))
+        return MFX_ERR_ALIAS;
+    return by_variant(a, whole_chunks(a, x, y, nullptr), [&](auto t, auto drop, auto masked, auto fast) {
+        return dispatch_fwd<decltype(t), decltype(drop)::value, decltype(masked)::value, decltype(fast)::value>(
+            a, w, x, y, stats, static_cast<cudaStream_t>(stream));
+    });
+}

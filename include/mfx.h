@@ -218,7 +218,7 @@ int mfx_scaled_upper_triang_masked_softmax_bwd(int dt, int64_t attn_batches, int
  *   min(S - 1, F + floor((S - F) * log(n / F) / log(max_distance / F))),
  * whose borders are exact (whole-number powers are compared, so a border that
  * is a whole number belongs to the upper bucket).  2 <= S <= 128, num_buckets
- * even when bidirectional, F < max_distance <= 8192, else MFX_ERR_SHAPE.
+ * even when bidirectional, F < max_distance <= 2048, else MFX_ERR_SHAPE.
  * mask: NULL or an ADDITIVE mask of dtype dt, [mask_b, mask_np, mask_sq, sk]
  * with each size 1 or x's; a key whose mask is -inf takes no part whatever x
  * holds there.  Finite masks are added exactly in effect: a row whose every
@@ -230,9 +230,9 @@ int mfx_scaled_upper_triang_masked_softmax_bwd(int dt, int64_t attn_batches, int
  * elem_base + r * sk + k, and keep as in mfx_bias_dropout_add_train (same
  * generator, words and threshold); p = 0 keeps everything.
  * stats: [b, np, sq, 2] fp32, what the backward needs of each row (the shift
- * of its mask and the log of its sum of exponentials), or NULL (inference).
+ * of its mask and the base-2 log of its sum of exponentials), or NULL (inference).
  * y: x's shape and dtype; y may equal x (in place, when no backward follows).
- * sk <= 2^30, |q_start| <= 2^40.  One query per sequence over a long key axis
+ * b, np, sq, sk and |q_start| at most 2^29.  One query per sequence over a long key axis
  * (decoding) splits a row over several thread blocks. */
 int mfx_relbias_softmax_dropout_fwd(int dt, int64_t b, int64_t np, int64_t sq, int64_t sk,
                                     const void* x, float scale,
@@ -248,7 +248,7 @@ int mfx_relbias_softmax_dropout_fwd(int dt, int64_t b, int64_t np, int64_t sq, i
  *   dS_k = P_k (dP_k - D)
  *   dx_k = scale * dS_k                        (dtype dt; zeros where left out)
  *   dtable[u, h] = sum of dS over the positions of head h in bucket u
- * P and keep are formed again; dy counts only where P is not zero.  dtable:
+ * P and keep are formed again; dy does not count at keys that take no part.  dtable:
  * [num_buckets, np] of dtype table_dt, from fp32 sums rounded once, or NULL
  * (not formed; needs no workspace).  The sums run in a fixed order, so dtable
  * is bitwise reproducible on a given GPU model; with an empty x it is set to
