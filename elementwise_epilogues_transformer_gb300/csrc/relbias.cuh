@@ -45,26 +45,47 @@ struct Geom {
     int drop;                  // p > 0
     int phase0;                // (phase0 + element index) mod 8 = 0 at a chunk's start
     float scale, scale2;       // the score scale; the same times log2 e
-    float keep_scale, keep_log2, keep_inv;  // 1 / (1 - p), its base-2 logarithm, and 1 - p
+    float keep_scale;          // 1 / (1 - p)
+    // backward: exponents get log2(keep_scale * fold), fold being the score
+    // scale where that is a positive normal number (1 else); dot = the factor
+    // that makes D of the sum, unfold = 1 / fold, post = scale / fold
+    float grad_log2, dot, unfold, post;
     uint32_t thresh_hi;        // keep threshold in the upper half-word
     uint64_t elem_base;
-    uint32_t off_lo, off_hi;   // the generator's counter words 2 and 3
-    uint32_t key0[10], key1[10];  // its key of each round
+    uint32_t first_x, first_y, first_z;  // what the generator's first round adds to each block
+    uint32_t key0[10], key1[10];         // its key of each round
 };
 
 // mask_block() with the rounds' keys read from the parameters instead of kept
-// in registers.
+// in registers, and the first round's product of the offset, the same for
+// every block, formed on the host.
+// N blocks, j, j + step, ..., go round by round together: a block alone is one
+// chain of dependent products.
+template <int N>
+__device__ __forceinline__ void keep_blocks(const Geom& g, uint64_t j, int step, uint4 (&c)[N])
+{
+    uint32_t lo0, hi0, lo1, hi1;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const uint64_t jn = j + (uint64_t)(n * step);
+        mul_hilo(0xD2511F53u, (uint32_t)jn, lo0, hi0);
+        c[n] = make_uint4((uint32_t)(jn >> 32) ^ g.first_x, g.first_y, hi0 ^ g.first_z, lo0);
+    }
+#pragma unroll
+    for (int i = 1; i < 10; ++i) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            mul_hilo(0xD2511F53u, c[n].x, lo0, hi0);
+            mul_hilo(0xCD9E8D57u, c[n].z, lo1, hi1);
+            c[n] = make_uint4(hi1 ^ c[n].y ^ g.key0[i], lo1, hi0 ^ c[n].w ^ g.key1[i], lo0);
+        }
+    }
+}
 __device__ __forceinline__ uint4 keep_block(const Geom& g, uint64_t j)
 {
-    uint4 c = make_uint4((uint32_t)j, (uint32_t)(j >> 32), g.off_lo, g.off_hi);
-#pragma unroll
-    for (int i = 0; i < 10; ++i) {
-        uint32_t lo0, hi0, lo1, hi1;
-        mul_hilo(0xD2511F53u, c.x, lo0, hi0);
-        mul_hilo(0xCD9E8D57u, c.z, lo1, hi1);
-        c = make_uint4(hi1 ^ c.y ^ g.key0[i], lo1, hi0 ^ c.w ^ g.key1[i], lo0);
-    }
-    return c;
+    uint4 c[1];
+    keep_blocks<1>(g, j, 0, c);
+    return c[0];
 }
 
 // The window holds the bias (times log2 e) of the positions around the query:
@@ -195,6 +216,17 @@ __device__ __forceinline__ float min_of(const float2 (&f)[4])
     return min3(min3(f[0].x, f[0].y, f[1].x), min3(f[1].y, f[2].x, f[2].y), fminf(f[3].x, f[3].y));
 }
 
+// A branch that stays one: a loop that runs once where c, because the compiler
+// turns a short if into predicated instructions that every chunk pays for
+// (measured: 4 of 28 instructions an element, without a chunk that needs it).
+__device__ __forceinline__ int done_once()
+{
+    int v;
+    asm volatile("mov.u32 %0, 0;" : "=r"(v));
+    return v;
+}
+#define MFX_RARELY(c) _Pragma("unroll 1") for (int todo_ = (c) ? 1 : 0; todo_; todo_ = done_once())
+
 // Sets the elements of a chunk outside [0, end) to v.
 __device__ __forceinline__ void fill_outside(float2 (&f)[4], int k0, int end, float v)
 {
@@ -208,17 +240,25 @@ __device__ __forceinline__ void fill_outside(float2 (&f)[4], int k0, int end, fl
 // Elements [k0, k0 + 8) of a row, of which [0, end) exist.  FAST: the row is
 // whole chunks of 16-byte vectors.  Otherwise a chunk that is not whole, or
 // not aligned, is read element by element, zero where there is none.
+template <typename T>
+__device__ __noinline__ void load_ragged(const T* p, int k0, int end, Raw8<T>* raw)
+{
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        f[j] = k0 + j >= 0 && k0 + j < end ? load1(p + j) : 0.0f;
+    narrow8(f, *raw);
+}
+
 template <typename T, bool FAST>
 __device__ __forceinline__ void load_chunk(const T* p, int k0, int end, Raw8<T>& raw)
 {
     if (FAST || (k0 >= 0 && k0 + 8 <= end && (reinterpret_cast<uintptr_t>(p) & 15u) == 0)) {
         ld8(p, raw);
     } else {
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            f[j] = k0 + j >= 0 && k0 + j < end ? load1(p + j) : 0.0f;
-        narrow8(f, raw);
+        Raw8<T> r;
+        load_ragged(p, k0, end, &r);
+        raw = r;
     }
 }
 
@@ -248,21 +288,27 @@ struct Row {
     int chunks;       // chunks of the row
 };
 
-// The rows that a team walks: row = first + n * step of the b * sq rows of one
-// head, as batch and query, advanced without divisions.
+// The rows that a team walks: first + n * step of the b * sq rows of head h,
+// as batch, query and row of the tensor, advanced without divisions.
 struct Walk {
+    int64_t r, step_r, wrap_r;
     int i, q, step_i, step_q;
-    __device__ __forceinline__ Walk(int64_t row, int64_t step, int64_t sq)
-        : i((int)(row / sq)), q((int)(row % sq)), step_i((int)(step / sq)), step_q((int)(step % sq))
+    __device__ __forceinline__ Walk(const Geom& g, int h, int64_t first, int64_t step)
+        : i((int)(first / g.sq)), q((int)(first % g.sq)), step_i((int)(step / g.sq)), step_q((int)(step % g.sq))
     {
+        wrap_r = (int64_t)(g.np - 1) * g.sq;
+        step_r = step + step_i * wrap_r;
+        r = first + i * wrap_r + (int64_t)h * g.sq;
     }
     __device__ __forceinline__ void next(int sq)
     {
         i += step_i;
         q += step_q;
+        r += step_r;
         if (q >= sq) {
             q -= sq;
             ++i;
+            r += wrap_r;
         }
     }
 };
@@ -272,7 +318,7 @@ __device__ __forceinline__ Row<T> row_at(const Geom& g, const Buckets& w, const 
                                          bool live)
 {
     Row<T> o;
-    o.r = ((int64_t)at.i * g.np + h) * g.sq + at.q;
+    o.r = at.r;
     const int64_t e = o.r * (int64_t)g.sk;
     o.a = FAST ? 0 : (int)((uint64_t)(g.phase0 + e) & 7u);
     o.e0 = e - o.a;
@@ -300,15 +346,51 @@ __device__ __forceinline__ bool near_chunk(const Buckets& w, int rel)
     return (unsigned)(rel + w.reach + 6) < (unsigned)(w.reach + w.hi + 6);
 }
 
-// Scores of the chunk at k0 from its raw x, times log2 e: x * scale + bias
-// (+ mask - shift), -inf where no key takes part (CHECK: the chunk may have
-// such keys).  A key whose mask is -inf is left out whatever x holds there.
+// ---------------------------------------------------------------------------
+// Staging: while a team works on one row, the chunks of its next row are on
+// their way into shared memory, each thread's into slots of its own (so that
+// waiting for its own copies is all it needs), one 16-byte vector a chunk.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void copy16_async(uint4* dst, const void* src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most N of this thread's committed groups are under way.
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Starts the copies of a row's chunks (those that take part; the others read as zero).
+template <int C>
+__device__ __forceinline__ void stage_row(uint4* stage, const bf16* src, const Row<bf16>& o, int tid, int team)
+{
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int ch = tid + c * team;
+        const bool there = ch * 8 < o.end;
+        copy16_async(stage + c * blockDim.x, src + o.e0 + (there ? 8 * ch : 0), there);
+    }
+    copies_commit();
+}
+
+__device__ __forceinline__ void unstage(const uint4* stage, int c, Raw8<bf16>& raw) { raw.v = stage[c * blockDim.x]; }
+__device__ __forceinline__ void restage(uint4* stage, int c, const Raw8<bf16>& raw) { stage[c * blockDim.x] = raw.v; }
+
+// Scores of the chunk at k0 from its raw x, times log2 e, plus `add`: x * scale
+// + (bias + add) (+ mask - shift).  A key whose mask is -inf is left out whatever x holds there.
 // Call with whole warps: one with a near chunk reads the window in all lanes,
-// far ones at its ends.
-template <typename T, bool FAST, bool MASK, bool CHECK>
+// far ones at its ends.  far_lo and far_hi have `add` in them already.
+template <typename T, bool FAST, bool MASK>
 __device__ __forceinline__ void score_chunk(const Raw8<T>& raw, const Row<T>& row, const Geom& g, const Buckets& w,
                                             const float4* win, float far_lo, float far_hi, int k0, float shift,
-                                            float2 (&s)[4])
+                                            float add, float2 (&s)[4])
 {
     pairs_of(raw, s);
     const int rel = k0 - row.pos;
@@ -320,14 +402,14 @@ __device__ __forceinline__ void score_chunk(const Raw8<T>& raw, const Row<T>& ro
     } else {
         const int stride = window_stride(w), i0 = min(max(rel + w.reach, -8), w.reach + w.hi + 1);
         const float4 lo = win[window_slot(stride, i0)], hi = win[window_slot(stride, i0 + 4)];
-        s[0] = pfma(s[0], f2(g.scale2), make_float2(lo.x, lo.y));
-        s[1] = pfma(s[1], f2(g.scale2), make_float2(lo.z, lo.w));
-        s[2] = pfma(s[2], f2(g.scale2), make_float2(hi.x, hi.y));
-        s[3] = pfma(s[3], f2(g.scale2), make_float2(hi.z, hi.w));
+        s[0] = pfma(s[0], f2(g.scale2), make_float2(lo.x + add, lo.y + add));
+        s[1] = pfma(s[1], f2(g.scale2), make_float2(lo.z + add, lo.w + add));
+        s[2] = pfma(s[2], f2(g.scale2), make_float2(hi.x + add, hi.y + add));
+        s[3] = pfma(s[3], f2(g.scale2), make_float2(hi.z + add, hi.w + add));
     }
     if (MASK && row.mask) {
         Raw8<T> mraw;
-        load_chunk<T, FAST>(row.mask + (CHECK && FAST && k0 >= row.end ? 0 : k0), k0, row.end, mraw);
+        load_chunk<T, FAST>(row.mask + (FAST && k0 >= row.end ? 0 : k0), k0, row.end, mraw);
         float2 m[4];
         pairs_of(mraw, m);
 #pragma unroll
@@ -336,8 +418,14 @@ __device__ __forceinline__ void score_chunk(const Raw8<T>& raw, const Row<T>& ro
             s[i].y = m[i].y == -INFINITY ? -INFINITY : fmaf(m[i].y - shift, kLog2eF, s[i].y);
         }
     }
-    if (CHECK)
-        fill_outside(s, k0, row.end, -INFINITY);
+}
+
+// Which of a thread's chunks, in a row that may end inside them, the warp
+// has to look at.
+template <bool CHECK>
+__device__ __forceinline__ bool some_part(int k0, int end)
+{
+    return !CHECK || __any_sync(0xFFFFFFFFu, k0 < end);
 }
 
 // Keep flags of a chunk applied to its values: 16-bit word j of the block
@@ -554,12 +642,19 @@ inline Geom make_geom(const Args& a, const Buckets& w, const void* x)
     g.phase0 = a.p > 0.0f ? (int)(a.elem_base & 7)
                           : (int)((reinterpret_cast<uintptr_t>(x) / (size_t)dtype_bytes(a.dt)) & 7);
     g.scale = a.scale, g.scale2 = (float)((double)a.scale * 1.4426950408889634);
-    g.keep_scale = 1.0f / (1.0f - a.p), g.keep_log2 = (float)std::log2((double)g.keep_scale), g.keep_inv = 1.0f - a.p;
+    g.keep_scale = 1.0f / (1.0f - a.p);
+    const double fold = a.scale >= 1e-30f && a.scale <= 1e30f ? a.scale : 1.0;
+    g.grad_log2 = (float)std::log2((double)g.keep_scale * fold);
+    g.dot = (float)(1.0 / ((double)g.keep_scale * fold)), g.unfold = (float)(1.0 / fold);
+    g.post = fold == 1.0 ? a.scale : 1.0f;
     const double t = std::ceil((double)a.p * 65536.0);
     g.thresh_hi = (uint32_t)(t > 65535.0 ? 65535.0 : t) << 16;
-    g.elem_base = a.elem_base, g.off_lo = (uint32_t)a.offset, g.off_hi = (uint32_t)(a.offset >> 32);
+    g.elem_base = a.elem_base;
     for (uint32_t i = 0; i < 10; ++i)
         g.key0[i] = (uint32_t)a.seed + i * 0x9E3779B9u, g.key1[i] = (uint32_t)(a.seed >> 32) + i * 0xBB67AE85u;
+    const uint64_t product = (uint64_t)0xCD9E8D57u * (uint32_t)a.offset;
+    g.first_x = (uint32_t)(product >> 32) ^ g.key0[0], g.first_y = (uint32_t)product;
+    g.first_z = (uint32_t)(a.offset >> 32) ^ g.key1[0];
     return g;
 }
 
@@ -574,15 +669,16 @@ inline int plan(Geom& g, bool fast, int most)
 {
     const int64_t chunks = chunks_of(g, fast);
     g.cluster = 1, g.teams = 1, g.blocks = 1;
-    if (chunks <= 32 * most) {
+    if (chunks <= 32 * (most < 4 ? most : 4)) {
         g.team = chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
         g.teams = kSmallBlock / g.team;
         const int c = chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4;
         g.exact = fast && chunks == (int64_t)g.team * c;
         return c;
     }
-    int64_t team = ((chunks + most - 1) / most + 31) / 32 * 32;
-    const int64_t held = (int64_t)kLongTeam * most;
+    if (most > 4 && chunks > (int64_t)kTeam * most)
+        most = 4;  // more threads first
+    const int64_t team = ((chunks + most - 1) / most + 31) / 32 * 32, held = (int64_t)kLongTeam * most;
     g.team = (int)(team < kLongTeam ? team : kLongTeam);
     g.blocks = (int)(chunks > held ? (chunks + held - 1) / held : 1);
     g.exact = fast && chunks == (int64_t)g.team * most;

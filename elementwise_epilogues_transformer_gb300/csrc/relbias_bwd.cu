@@ -2,9 +2,12 @@
 // dropout (relbias_fwd.cu has the operation).
 //
 // P and the keep flags are formed again from x, the row statistics and the
-// generator.  With Q = P / (1 - p), formed with log2(1 / (1 - p)) added to the
-// exponent, and z = keep * dy:  D = sum Q z,  dS = Q (z - (1 - p) D),  so the
-// dropout's factor costs nothing per element.
+// generator.  With Q = scale * P / (1 - p), formed by adding the logarithm of
+// the factor to the exponent, and z = keep * dy,
+//   D = (1 - p) / scale * sum Q z,   dx = Q (z - D),
+// so neither factor costs anything per element; the table's sums are divided
+// by scale at a block's end.  (A scale that is not a positive normal number
+// stays out of Q and is multiplied in.)
 //
 // The table's gradient takes the form of the bias: far positions add into two
 // registers a thread, near ones into a window in shared memory.  A row's
@@ -34,6 +37,16 @@ __device__ __forceinline__ void add4(float4* p, float2 a, float2 b)
     *p = v;
 }
 
+// Whether a row comes through shared memory, copied while the row before is
+// worked on, rather than straight into registers (bf16 only: fp32 measured
+// slower so, 0.38 against 0.31 ms at 2x8x2048x4096).  The gradient's chunks
+// then also wait there for the second half of the work, which saves registers.
+template <typename T, bool FAST, int MT>
+constexpr bool staged()
+{
+    return FAST && MT <= kTeam && sizeof(T) == 2;
+}
+
 template <typename T, int C, bool DROP, bool MASK, bool FAST, int MT>
 __global__ void __launch_bounds__(MT, MT > kTeam ? 1 : 2)
 relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, const T* __restrict__ mask,
@@ -44,7 +57,7 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
     float4* win = reinterpret_cast<float4*>(smem);
     __shared__ float part[2][MT / 32];
     __shared__ float2 far_part[MT / 32];
-    constexpr bool LONG = MT > kTeam, ANY = C == 1;
+    constexpr bool LONG = MT > kTeam, ANY = C == 1, STAGED = staged<T, FAST, MT>();
     const int blocks = LONG ? g.blocks : 1;
     const int h = (int)(blockIdx.x / g.slices);
     const int64_t slice = blockIdx.x % g.slices;
@@ -53,6 +66,9 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
     const int last = w.reach + w.hi, stride = window_stride(w), vectors = sum_vectors(w);
     const int sets = g.team > 32 ? 1 : (int)(blockDim.x >> 5);  // one set of sums a block, or one a warp
     float4* acc = win + 8 * stride + (g.team > 32 ? 0 : warp) * 2 * vectors;
+    // staged rows, after the window and the sums: x, and dy twice (this row's and the next one's)
+    uint4* stage = reinterpret_cast<uint4*>(win + 8 * stride + (ws ? 2 * vectors * sets : 0)) + threadIdx.x;
+    uint4* stage_dy = stage + C * blockDim.x;
     fill_window(w, g, table, h, win);
     if (ws)
         for (int i = threadIdx.x; i < 2 * vectors * sets; i += blockDim.x)
@@ -63,63 +79,105 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
 
     const int64_t step = g.slices * g.teams;
     int64_t row = slice * g.teams + tm;
-    Walk at(row, step, g.sq);
+    Walk at(g, h, row, step);
     int slot = 0;
-    for (int64_t first = slice * g.teams; first < g.rows; first += step, row += step, at.next(g.sq), slot ^= 1) {
-        const Row<T> o = row_at<T, FAST>(g, w, MASK ? mask : nullptr, h, at, row < g.rows);
+    Row<T> o = row_at<T, FAST>(g, w, MASK ? mask : nullptr, h, at, row < g.rows), ahead = o;
+    if constexpr (STAGED) {
+        stage_row<C>(stage, x, o, tid, g.team);
+        stage_row<C>(stage_dy, dy, o, tid, g.team);
+    }
+    for (int64_t first = slice * g.teams; first < g.rows; first += step, row += step, o = ahead, slot ^= 1) {
+        uint4* sz = stage_dy + slot * C * blockDim.x;
         float shift = 0.0f, lse = 0.0f;
         if (row < g.rows) {
             shift = stats[2 * o.r], lse = stats[2 * o.r + 1];
             lse = lse == -INFINITY ? 0.0f : lse;  // an empty row: every score is -inf
         }
-        const float ref = DROP ? g.keep_log2 - lse : -lse;
+        const float ref = g.grad_log2 - lse, lo = far_lo + ref, hi = far_hi + ref;
         const auto run = [&](auto check) {
             constexpr bool CHECK = decltype(check)::value;
             float2 Q[C][4], D2 = f2(0.0f);
-            Raw8<T> z[C];
-            const auto load_block = [&](int blk) {
+            Raw8<T> z[STAGED ? 1 : C];
+            // P and z of the row's (or block's) chunks, and their part of D
+            const auto first_half = [&](int blk) {
                 Raw8<T> rx[C];
+                if constexpr (STAGED) {
+                    if constexpr (DROP && !CHECK) {
+                        // the keep flags of all chunks together, while the copies arrive
+                        uint4 kb[C];
+                        keep_blocks<C>(g, o.block0 + tid, g.team, kb);
+                        copies_wait<0>();
+                        Raw8<T> r[C];
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const int ch = (blk * C + c) * g.team + tid, k0 = ch * 8 - o.a;
-                    const int k = 8 * (CHECK && FAST && k0 >= o.end ? 0 : ch);
-                    load_chunk<T, FAST>(x + o.e0 + k, k0, o.end, rx[c]);
-                    load_chunk<T, FAST>(dy + o.e0 + k, k0, o.end, z[c]);
-                }
+                        for (int c = 0; c < C; ++c)
+                            unstage(sz, c, r[c]);
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const int ch = (blk * C + c) * g.team + tid, k0 = ch * 8 - o.a;
-                    score_chunk<T, FAST, MASK, CHECK>(rx[c], o, g, w, win, far_lo, far_hi, k0, shift, Q[c]);
+                        for (int c = 0; c < C; ++c) {
+                            drop_raw(r[c], kb[c], g.thresh_hi);
+                            restage(sz, c, r[c]);
+                        }
+                    } else {
+                        copies_wait<0>();
+                    }
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        Q[c][i] = make_float2(exp2_of(Q[c][i].x + ref), exp2_of(Q[c][i].y + ref));
-                    if (DROP && g.drop && (!CHECK || k0 < o.end))
-                        drop_raw(z[c], keep_block(g, o.block0 + ch), g.thresh_hi);
-                    // what the upstream gradient holds at keys left out does not count
-                    if ((CHECK || MASK) && min_of(Q[c]) == 0.0f) {
-                        float2 f[4];
-                        pairs_of(z[c], f);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            f[i] = make_float2(Q[c][i].x == 0.0f ? 0.0f : f[i].x, Q[c][i].y == 0.0f ? 0.0f : f[i].y);
-                        narrow_pairs(f, z[c]);
+                    for (int c = 0; c < C; ++c) {
+                        const int ch = (blk * C + c) * g.team + tid, k0 = ch * 8 - o.a;
+                        const int k = 8 * (CHECK && FAST && k0 >= o.end ? 0 : ch);
+                        load_chunk<T, FAST>(x + o.e0 + k, k0, o.end, rx[c]);
+                        load_chunk<T, FAST>(dy + o.e0 + k, k0, o.end, z[c]);
                     }
                 }
-            };
-            for (int blk = 0; blk < blocks; ++blk) {
-                load_block(blk);
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
+                    const int ch = (blk * C + c) * g.team + tid, k0 = ch * 8 - o.a;
+                    if (!some_part<CHECK>(k0, o.end))
+                        continue;
+                    Raw8<T>& zc = z[STAGED ? 0 : c];
+                    if constexpr (STAGED) {
+                        unstage(stage, c, rx[c]);
+                        unstage(sz, c, zc);
+                    }
+                    score_chunk<T, FAST, MASK>(rx[c], o, g, w, win, lo, hi, k0, shift, ref, Q[c]);
+                    if (CHECK)
+                        MFX_RARELY((!FAST && k0 < 0) || k0 + 8 > o.end)
+                            fill_outside(Q[c], k0, o.end, -INFINITY);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        Q[c][i] = make_float2(exp2_of(Q[c][i].x), exp2_of(Q[c][i].y));
+                    if (DROP && (!STAGED || CHECK) && g.drop)
+                        drop_raw(zc, keep_block(g, o.block0 + ch), g.thresh_hi);
                     float2 f[4];
-                    pairs_of(z[c], f);
+                    pairs_of(zc, f);
+                    // what the upstream gradient holds at keys left out does not count
+                    if (CHECK || MASK) {
+                        MFX_RARELY(min_of(Q[c]) == 0.0f) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                f[i] = make_float2(Q[c][i].x == 0.0f ? 0.0f : f[i].x, Q[c][i].y == 0.0f ? 0.0f : f[i].y);
+                            narrow_pairs(f, zc);
+                        }
+                    }
+                    if constexpr (STAGED)
+                        if (CHECK || MASK)
+                            restage(sz, c, zc);
                     float2 t = pmul(Q[c][0], f[0]);
 #pragma unroll
                     for (int i = 1; i < 4; ++i)
                         t = pfma(Q[c][i], f[i], t);
                     D2 = padd(D2, t);
                 }
-            }
+            };
+            for (int blk = 0; blk < blocks; ++blk)
+                first_half(blk);
             float D = lanes_sum<ANY>(D2.x + D2.y, lanes);
+            // every chunk of this row has been read: on to the team's next row
+            at.next(g.sq);
+            ahead = row_at<T, FAST>(g, w, MASK ? mask : nullptr, h, at, row + step < g.rows);
+            if constexpr (STAGED) {
+                stage_row<C>(stage, x, ahead, tid, g.team);
+                stage_row<C>(stage_dy + (slot ^ 1) * C * blockDim.x, dy, ahead, tid, g.team);
+            }
             if (warps > 1) {
                 if (lane == 0)
                     part[slot][warp] = D;
@@ -130,51 +188,61 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
             } else {
                 __syncwarp();  // the previous row's window sums before this row's
             }
-            if (DROP)
-                D *= g.keep_inv;
+            D *= g.dot;
             for (int blk = 0; blk < blocks; ++blk) {
                 if (LONG && blocks > 1)
-                    load_block(blk);
+                    first_half(blk);
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     const int ch = (blk * C + c) * g.team + tid, k0 = ch * 8 - o.a;
                     float2 v[4];
-                    pairs_of(z[c], v);
+                    if (some_part<CHECK>(k0, o.end)) {
+                        if constexpr (STAGED)
+                            unstage(sz, c, z[0]);
+                        pairs_of(z[STAGED ? 0 : c], v);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = pmul(Q[c][i], padd(v[i], f2(-D)));
-                    if (CHECK)
-                        fill_outside(v, k0, o.end, 0.0f);
-                    if (ws) {
-                        const int rel = k0 - o.pos;
-                        const bool near = near_chunk(w, rel) && (!CHECK || k0 < o.end);
-                        const float2 t = padd(padd(v[0], v[1]), padd(v[2], v[3]));
-                        const float far = near ? 0.0f : t.x + t.y;
-                        sum_lo += rel >= w.hi ? 0.0f : far;
-                        sum_hi += rel >= w.hi ? far : 0.0f;
-                        if (__any_sync(0xFFFFFFFFu, near)) {
-                            float4* p = acc + window_slot(stride, rel + w.reach);
-                            if (!ANY) {
-                                if (near) {
-                                    add4(p, v[0], v[1]);
-                                    add4(p + vectors, v[2], v[3]);
-                                }
-                            } else {
-                                for (int turn = 0; turn < 32; turn += lanes) {
-                                    if (near && turn == (lane & ~(lanes - 1))) {
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = pmul(Q[c][i], padd(v[i], f2(-D)));
+                        if (CHECK)
+                            MFX_RARELY((!FAST && k0 < 0) || k0 + 8 > o.end)
+                                fill_outside(v, k0, o.end, 0.0f);
+                        if (ws) {
+                            const int rel = k0 - o.pos;
+                            const bool near = near_chunk(w, rel) && (!CHECK || k0 < o.end);
+                            const float2 t = padd(padd(v[0], v[1]), padd(v[2], v[3]));
+                            const float far = near ? 0.0f : t.x + t.y;
+                            sum_lo += rel >= w.hi ? 0.0f : far;
+                            sum_hi += rel >= w.hi ? far : 0.0f;
+                            if (__any_sync(0xFFFFFFFFu, near)) {
+                                float4* p = acc + window_slot(stride, rel + w.reach);
+                                if (!ANY) {
+                                    if (near) {
                                         add4(p, v[0], v[1]);
                                         add4(p + vectors, v[2], v[3]);
                                     }
-                                    __syncwarp();
+                                } else {
+                                    for (int turn = 0; turn < 32; turn += lanes) {
+                                        if (near && turn == (lane & ~(lanes - 1))) {
+                                            add4(p, v[0], v[1]);
+                                            add4(p + vectors, v[2], v[3]);
+                                        }
+                                        __syncwarp();
+                                    }
                                 }
                             }
                         }
+                        if (g.post != 1.0f) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                v[i] = pmul(v[i], f2(g.post));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = f2(0.0f);
                     }
                     if (CHECK && ch >= o.chunks)
                         continue;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = pmul(v[i], f2(g.scale));
                     store_chunk<T, FAST>(dx + o.e0 + 8 * ch, k0, g.sk, v);
                 }
             }
@@ -191,6 +259,8 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
             run(std::true_type{});
         }
     }
+    if (STAGED)
+        copies_wait<0>();
     if (!ws)
         return;
     // the block's sum of each bucket: its entries of every residue and set,
@@ -200,18 +270,30 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
     if (lane == 0)
         far_part[warp] = make_float2(sum_lo, sum_hi);
     __syncthreads();
-    const float* sums = reinterpret_cast<const float*>(win + 8 * stride);
-    const auto entry = [&](int i) {
+    float4* all = win + 8 * stride;
+    for (int i = threadIdx.x; i < 2 * vectors; i += blockDim.x) {
+        float4 t = all[i];
+        for (int k = 1; k < sets; ++k) {
+            const float4 v = all[k * 2 * vectors + i];
+            t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+        }
+        all[i] = t;
+    }
+    __syncthreads();
+    // one value per entry, in the window's place
+    float* entry = reinterpret_cast<float*>(win) + 8;
+    const float* sums = reinterpret_cast<const float*>(all);
+    for (int i = (int)threadIdx.x - 8; i <= last + 8; i += blockDim.x) {
         float t = 0.0f;
-        for (int k = 0; k < sets; ++k)
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const int u = i + 8 - r;  // vector pair u / 8 of residue r, element u mod 8
-                if (u >= 0 && (u >> 3) < stride)
-                    t += sums[4 * (k * 2 * vectors + (u & 4 ? vectors : 0) + r * stride + (u >> 3)) + (u & 3)];
-            }
-        return t;
-    };
+        for (int r = 0; r < 8; ++r) {
+            const int u = i + 8 - r;  // vector pair u / 8 of residue r, element u mod 8
+            if (u >= 0 && (u >> 3) < stride)
+                t += sums[4 * ((u & 4 ? vectors : 0) + r * stride + (u >> 3)) + (u & 3)];
+        }
+        entry[i] = t;
+    }
+    __syncthreads();
     const int nw = blockDim.x >> 5;
     for (int u = warp; u < w.num; u += nw) {
         const bool right = u >= w.side;
@@ -223,16 +305,16 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
             n0 = 1;
         float t = 0.0f;
         for (int n = n0 + lane; n < n1; n += 32)
-            t += entry(right ? w.reach + n : w.reach - n);
+            t += entry[right ? w.reach + n : w.reach - n];
         if (lo && lane < 8)
-            t += entry(lane - 8);
+            t += entry[lane - 8];
         if (hi && lane < 8)
-            t += entry(last + 1 + lane);
+            t += entry[last + 1 + lane];
         t = lanes_sum<false>(t, 32);
         if (lane == 0) {
             for (int k = 0; k < nw; ++k)
                 t += (lo ? far_part[k].x : 0.0f) + (hi ? far_part[k].y : 0.0f);
-            ws[(slice * w.num + u) * g.np + h] = t;
+            ws[(slice * w.num + u) * g.np + h] = t * g.unfold;
         }
     }
     pdl_launch_dependents();
@@ -255,7 +337,8 @@ int launch_bwd(Geom g, const Buckets& w, const Args& a, const void* dy, const vo
     while (g.team <= 32 && g.team * g.teams > 32 && window_bytes(w) + sums * (g.team * g.teams / 32) > 64 * 1024)
         g.teams /= 2;  // wide windows: fewer rows at a time
     const int threads = g.team * g.teams;
-    const size_t smem = window_bytes(w) + sums * (g.team > 32 ? 1 : threads / 32);
+    const size_t smem = window_bytes(w) + sums * (g.team > 32 ? 1 : threads / 32) +
+                        (staged<T, FAST, MT>() ? (size_t)3 * C * 16 * threads : 0);
     const int64_t slots = (int64_t)sm_count() * occupancy((const void*)kern, threads, smem);
     g.slices = slices_for(g, slots, 4);
     if (g.slices > bwd_slices(a))

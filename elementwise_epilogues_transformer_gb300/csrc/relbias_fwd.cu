@@ -118,7 +118,7 @@ __device__ __noinline__ void shifted_row(const T* x, T* y, float* stats, const R
 }
 
 template <typename T, int C, bool DROP, bool MASK, bool FAST, int MT>
-__global__ void __launch_bounds__(MT, MT > kTeam ? 1 : sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(MT, MT > kTeam ? 1 : sizeof(T) == 2 && C < 8 ? 3 : 2)
 relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ mask, const void* __restrict__ table,
             const __grid_constant__ Geom g, const __grid_constant__ Buckets w)
 {
@@ -141,7 +141,7 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
 
     const int64_t step = g.slices * g.teams;
     int64_t row = slice * g.teams + tm;
-    Walk at(row, step, g.sq);
+    Walk at(g, h, row, step);
     int slot = 0;
     for (int64_t first = slice * g.teams; first < g.rows; first += step, row += step, at.next(g.sq), slot ^= 1) {
         const Row<T> o = row_at<T, FAST>(g, w, MASK ? mask : nullptr, h, at, row < g.rows);
@@ -164,7 +164,16 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     const int k0 = (c0 + c * g.team) * 8 - o.a;
-                    score_chunk<T, FAST, MASK, CHECK>(raw[c], o, g, w, win, far_lo, far_hi, k0, 0.0f, s[c]);
+                    if (some_part<CHECK>(k0, o.end)) {
+                        score_chunk<T, FAST, MASK>(raw[c], o, g, w, win, far_lo, far_hi, k0, 0.0f, 0.0f, s[c]);
+                        if (CHECK)
+                            MFX_RARELY((!FAST && k0 < 0) || k0 + 8 > o.end)
+                                fill_outside(s[c], k0, o.end, -INFINITY);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            s[c][i] = f2(-INFINITY);
+                    }
                     t = max_of(t, s[c]);
                 }
                 t = fmaxf(m, lanes_max<ANY>(t, team.lanes));
@@ -202,30 +211,41 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
             const float f1 = mw == -INFINITY && l == l ? 0.0f : exp2_of(mw - m) * inv;
             for (int blk = 0; blk < blocks; ++blk) {
                 const int c0 = (blk * cluster + rank) * (C * g.team) + tid;
+                constexpr int PAIR = C > 1 && sizeof(T) == 2 ? 2 : 1;  // generator blocks drawn together (fp32: no gain)
+                uint4 kb[PAIR];
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     const int ch = c0 + c * g.team, k0 = ch * 8 - o.a;
-                    float f = f1;
-                    if (LONG && blocks > 1) {
-                        Raw8<T> raw;
-                        load_chunk<T, FAST>(xr + 8 * (FAST && k0 >= o.end ? 0 : ch), k0, o.end, raw);
-                        score_chunk<T, FAST, MASK, true>(raw, o, g, w, win, far_lo, far_hi, k0, 0.0f, s[c]);
-                        const float ref = m == -INFINITY ? 0.0f : m;
+                    if (DROP && !CHECK && c % PAIR == 0)
+                        keep_blocks<PAIR>(g, o.block0 + ch, g.team, kb);
+                    float2 p[4];
+                    if (some_part<CHECK>(k0, o.end)) {
+                        float f = f1;
+                        if (LONG && blocks > 1) {
+                            Raw8<T> raw;
+                            load_chunk<T, FAST>(xr + 8 * (FAST && k0 >= o.end ? 0 : ch), k0, o.end, raw);
+                            score_chunk<T, FAST, MASK>(raw, o, g, w, win, far_lo, far_hi, k0, 0.0f, 0.0f, s[c]);
+                            const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                s[c][i] = make_float2(exp2_of(s[c][i].x - ref), exp2_of(s[c][i].y - ref));
+                            f = inv;
+                        }
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            s[c][i] = make_float2(exp2_of(s[c][i].x - ref), exp2_of(s[c][i].y - ref));
-                        f = inv;
+                            p[i] = pmul(s[c][i], f2(f));
+                        if (DROP && g.drop)
+                            drop_pairs(p, CHECK ? keep_block(g, o.block0 + ch) : kb[c % PAIR], g.thresh_hi);
+                        if (CHECK)
+                            MFX_RARELY((!FAST && k0 < 0) || k0 + 8 > o.end)
+                                fill_outside(p, k0, o.end, 0.0f);
+                    } else {  // keys that a causal row leaves out
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            p[i] = f2(0.0f);
                     }
                     if (CHECK && ch >= o.chunks)
                         continue;
-                    float2 p[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        p[i] = pmul(s[c][i], f2(f));
-                    if (DROP && g.drop && (!CHECK || k0 < o.end))
-                        drop_pairs(p, keep_block(g, o.block0 + ch), g.thresh_hi);
-                    if (CHECK)
-                        fill_outside(p, k0, o.end, 0.0f);
                     store_chunk<T, FAST>(yr + 8 * ch, k0, g.sk, p);
                 }
             }
@@ -250,8 +270,8 @@ template <typename T, int C, bool DROP, bool MASK, bool FAST, int MT>
 int launch_fwd(Geom g, const Buckets& w, const Args& a, const void* x, void* y, float* stats, cudaStream_t s)
 {
     const auto kern = relbias_fwd<T, C, DROP, MASK, FAST, MT>;
-    const size_t smem = window_bytes(w);
     const int threads = g.team * g.teams;
+    const size_t smem = window_bytes(w);
     const int64_t slots = (int64_t)sm_count() * occupancy((const void*)kern, threads, smem) / g.cluster;
     g.slices = slices_for(g, slots > 0 ? slots : 1, 1);
     const int64_t blocks = g.slices * g.np * g.cluster;
@@ -277,7 +297,7 @@ template <typename T, bool DROP, bool MASK, bool FAST>
 int dispatch_fwd(const Args& a, const Buckets& w, const void* x, void* y, float* stats, cudaStream_t s)
 {
     Geom g = make_geom(a, w, x);
-    int c = plan(g, FAST, 4);
+    int c = plan(g, FAST, FAST && sizeof(T) == 2 ? 8 : 4);
     const int64_t rows = a.b * a.np * a.sq, sms = sm_count(), chunks = chunks_of(g, FAST);
     if (chunks > 32 && rows < 4 * sms) {
         // few rows: as many threads on each as give every SM work, and rows
@@ -303,6 +323,9 @@ int dispatch_fwd(const Args& a, const Buckets& w, const void* x, void* y, float*
                        : launch_fwd<T, 1, DROP, MASK, FAST, kTeam>(g, w, a, x, y, stats, s);
         if (c == 2)
             return launch_fwd<T, 2, DROP, MASK, FAST, kTeam>(g, w, a, x, y, stats, s);
+        if constexpr (sizeof(T) == 2)
+            if (c == 8)
+                return launch_fwd<T, 8, DROP, MASK, FAST, kTeam>(g, w, a, x, y, stats, s);
     } else if (c == 1) {
         return launch_fwd<T, 1, DROP, MASK, FAST, kTeam>(g, w, a, x, y, stats, s);
     }
