@@ -22,6 +22,9 @@
 #include "mfx_host.h"
 #include "mfx_pipe.cuh"
 
+#ifndef MFX_FLAT_DROP
+#define MFX_FLAT_DROP 1
+#endif
 namespace mfx {
 namespace {
 
@@ -768,6 +771,133 @@ bda_bwd_generic(const TX* g, const uint8_t* keep, TX* dx, TR* dres, int64_t n, f
     }
 }
 
+// ---------------------------------------------------------------------------
+// Regenerated mask, straight from and to global memory: the backward whose
+// keep flags were not stored, and plain dropout both ways.  A warp takes 32 U
+// consecutive units of 8 elements, U a lane; its loads are under way while the
+// generator runs, whose U blocks go through their rounds together.  With
+// elements that do not begin on a generator block (PHASED) a unit needs its
+// block and the next one, which is the block of the lane above: lane 0 hands
+// its next unit's to lane 31, and only the warp's last block is drawn twice.
+// Measured against the ring (bda_bwd_pipe), 32768 x 4099 bf16: see the call.
+// ---------------------------------------------------------------------------
+struct FlatDrop {
+    int64_t n;
+    uint64_t block0;  // generator block of unit 0
+    int phase;        // element 0's word in it
+    int vec;          // 16-byte aligned: g and dx (1), dres (2); 32-byte aligned fp32: g and dx (4), dres (8)
+    float scale;
+    uint32_t thresh_hi;
+    MaskGen gen;
+};
+
+template <typename T>
+__device__ __forceinline__ void flat_load(const T* p, int vec, Raw8<T>& r)
+{
+    if constexpr (!DTypeInfo<T>::kBf16)
+        if (vec & 4) {
+            ld32(p, r.v[0], r.v[1]);
+            return;
+        }
+    ld8(p, r);
+}
+template <typename T>
+__device__ __forceinline__ void flat_store(T* p, bool wide, const Raw8<T>& r)
+{
+    if constexpr (!DTypeInfo<T>::kBf16)
+        if (wide) {
+            st32(p, r.v[0], r.v[1]);
+            return;
+        }
+    st8(p, r);
+}
+
+template <typename TX, typename TR, int U, bool PHASED>
+__global__ void __launch_bounds__(kThreads, U > 1 ? 4 : 6)
+drop_flat(const TX* g, TX* dx, TR* dres, const __grid_constant__ FlatDrop d)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t units = (d.n + 7) / 8, whole = d.n / 8;
+    const int64_t step = (int64_t)gridDim.x * (kThreads * U);
+    for (int64_t first = ((int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31)) * U; first < units; first += step) {
+        const int64_t u0 = first + lane;
+        Raw8<TX> r[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if ((d.vec & 1) && u0 + 32 * k < whole)
+                flat_load(g + (u0 + 32 * k) * 8, d.vec, r[k]);
+        uint4 kb[U + (PHASED ? 1 : 0)];
+        mask_blocks<U + (PHASED ? 1 : 0)>(d.gen, d.block0 + (uint64_t)u0, 32, kb);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if constexpr (PHASED) {
+                uint4 s = lane == 0 ? kb[k + 1] : kb[k];
+                s.x = __shfl_sync(0xFFFFFFFFu, s.x, (lane + 1) & 31), s.y = __shfl_sync(0xFFFFFFFFu, s.y, (lane + 1) & 31);
+                s.z = __shfl_sync(0xFFFFFFFFu, s.z, (lane + 1) & 31), s.w = __shfl_sync(0xFFFFFFFFu, s.w, (lane + 1) & 31);
+                kb[k] = mask_words_at(kb[k], s, d.phase);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int64_t u = u0 + 32 * k, i0 = u * 8;
+            if (u >= units)
+                continue;
+            const int cnt = u < whole ? 8 : (int)(d.n - i0);
+            const bool vec = (d.vec & 1) && cnt == 8;
+            float f[8], v[8];
+            if (vec)
+                widen8(r[k], f);
+            else
+                load8f(g + i0, false, cnt, f);
+            const uint32_t w[4] = {kb[k].x, kb[k].y, kb[k].z, kb[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = (w[i] << 16) >= d.thresh_hi ? __fmul_rn(f[2 * i], d.scale) : 0.0f;
+                v[2 * i + 1] = w[i] >= d.thresh_hi ? __fmul_rn(f[2 * i + 1], d.scale) : 0.0f;
+            }
+            if (vec) {
+                narrow8(v, r[k]);
+                flat_store(dx + i0, d.vec & 4, r[k]);
+            } else {
+                store8f(dx + i0, false, cnt, v);
+            }
+            if (dres) {
+                if ((d.vec & 2) && cnt == 8) {
+                    Raw8<TR> o;
+                    narrow8(f, o);
+                    flat_store(dres + i0, d.vec & 8, o);
+                } else {
+                    store8f(dres + i0, false, cnt, f);
+                }
+            }
+        }
+    }
+}
+
+inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+template <typename TX, typename TR>
+int launch_flat(const TX* g, TX* dx, TR* dres, int64_t n, float scale, uint32_t thresh, uint64_t seed,
+                uint64_t offset, uint64_t elem_base, cudaStream_t s)
+{
+    FlatDrop d = {};
+    d.n = n, d.block0 = elem_base / 8, d.phase = (int)(elem_base % 8), d.scale = scale, d.thresh_hi = thresh << 16;
+    d.vec = (aligned16(g) && aligned16(dx) ? 1 : 0) | (aligned16(dres) ? 2 : 0) |
+            (sizeof(TX) == 4 && aligned32(g) && aligned32(dx) ? 4 : 0) | (sizeof(TR) == 4 && aligned32(dres) ? 8 : 0);
+    d.gen = make_mask_gen(seed, offset);
+    const int64_t units = (n + 7) / 8;
+    const auto go = [&](auto kern, int u) {
+        const int64_t need = (units + kThreads * u - 1) / (kThreads * u);
+        const int64_t most = (int64_t)sm_count() * blocks_per_sm((const void*)kern);
+        kern<<<(unsigned)(need < most ? need : most), kThreads, 0, s>>>(g, dx, dres, d);
+        return launch_status();
+    };
+    // four units a lane where that still gives every SM two blocks
+    if (units >= (int64_t)sm_count() * 2 * kThreads * 4)
+        return d.phase ? go(drop_flat<TX, TR, 4, true>, 4) : go(drop_flat<TX, TR, 4, false>, 4);
+    return d.phase ? go(drop_flat<TX, TR, 1, true>, 1) : go(drop_flat<TX, TR, 1, false>, 1);
+}
+
 template <typename TX, typename TR, bool PACKED = false>
 int launch_bwd(const void* g, const uint8_t* keep, void* dx, void* dres, int64_t n, float p, uint64_t seed,
                uint64_t offset, uint64_t elem_base, cudaStream_t s)
@@ -778,6 +908,8 @@ int launch_bwd(const void* g, const uint8_t* keep, void* dx, void* dres, int64_t
     double t = std::ceil((double)p * 65536.0);
     const uint32_t thresh = (uint32_t)(t > 65535.0 ? 65535.0 : t);
     const float scale = 1.0f / (1.0f - p);
+    if (!PACKED && !keep && MFX_FLAT_DROP)
+        return launch_flat<TX, TR>(gp, dxp, drp, n, scale, thresh, seed, offset, elem_base, s);
     const bool pipe_ok = MFX_PIPE_BDA && n % 8 == 0 && aligned16(g) && aligned16(dx) &&
                          (!dres || aligned16(dres)) && (keep ? aligned16(keep) : elem_base % 8 == 0);
     if (pipe_ok) {

@@ -440,6 +440,21 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
 
 __device__ __forceinline__ float2 f2(float v) { return make_float2(v, v); }
 
+// 32-byte streaming accesses (sm_100 and later): eight fp32 in one instruction
+// instead of two halves of every sector from two.  p 32-byte aligned.
+__device__ __forceinline__ void ld32(const void* p, uint4& a, uint4& b)
+{
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p));
+}
+__device__ __forceinline__ void st32(void* p, const uint4& a, const uint4& b)
+{
+    asm volatile(MFX_ST_OP ".v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+
 // Eight consecutive elements ("a group"): one 16-byte vector of bf16 or two
 // of fp32.  `p` must be 16-byte aligned.
 template <typename T> struct Raw8;
@@ -924,6 +939,48 @@ __device__ __forceinline__ uint4 mask_block(uint64_t j, uint64_t seed, uint64_t 
                          (uint32_t)seed, (uint32_t)(seed >> 32));
 }
 
+// The generator of one (seed, offset) as a kernel parameter: its rounds' keys,
+// read from the parameters instead of kept in registers, and what the first
+// round makes of the offset, the same for every block.
+struct MaskGen {
+    uint32_t first_x, first_y, first_z;
+    uint32_t key0[10], key1[10];
+};
+
+inline MaskGen make_mask_gen(uint64_t seed, uint64_t offset)
+{
+    MaskGen m;
+    for (uint32_t i = 0; i < 10; ++i)
+        m.key0[i] = (uint32_t)seed + i * 0x9E3779B9u, m.key1[i] = (uint32_t)(seed >> 32) + i * 0xBB67AE85u;
+    const uint64_t product = (uint64_t)0xCD9E8D57u * (uint32_t)offset;
+    m.first_x = (uint32_t)(product >> 32) ^ m.key0[0], m.first_y = (uint32_t)product;
+    m.first_z = (uint32_t)(offset >> 32) ^ m.key1[0];
+    return m;
+}
+
+// mask_block() of the N blocks j, j + step, ...: they go round by round
+// together, a block alone being one chain of dependent products.
+template <int N>
+__device__ __forceinline__ void mask_blocks(const MaskGen& m, uint64_t j, int step, uint4 (&c)[N])
+{
+    uint32_t lo0, hi0, lo1, hi1;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const uint64_t jn = j + (uint64_t)(n * step);
+        mul_hilo(0xD2511F53u, (uint32_t)jn, lo0, hi0);
+        c[n] = make_uint4((uint32_t)(jn >> 32) ^ m.first_x, m.first_y, hi0 ^ m.first_z, lo0);
+    }
+#pragma unroll
+    for (int i = 1; i < 10; ++i) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            mul_hilo(0xD2511F53u, c[n].x, lo0, hi0);
+            mul_hilo(0xCD9E8D57u, c[n].z, lo1, hi1);
+            c[n] = make_uint4(hi1 ^ c[n].y ^ m.key0[i], lo1, hi0 ^ c[n].w ^ m.key1[i], lo0);
+        }
+    }
+}
+
 // The eight 16-bit words of elements [8j + o, 8j + o + 8) (o in 0..7, the
 // same for every call of a launch): words o..7 of block j and 0..o-1 of
 // block j + 1, as one 128-bit block (word k = element 8j + o + k), from the
@@ -950,6 +1007,19 @@ __device__ __forceinline__ uint4 mask_block_at(uint64_t j, int o, uint64_t seed,
     if (o == 0)
         return a;
     return mask_words_at(a, mask_block(j + 1, seed, offset), o);
+}
+
+// The keep flags of a block's words 2i, 2i + 1 as bit masks of a bf16 pair (t2:
+// the threshold in both halves).  With H the top bit of each half, (w | H) -
+// (t & ~H) has it set where the low 15 bits of w reach those of t; one
+// three-input operation adds the top bits' say and a byte permutation spreads it.
+__device__ __forceinline__ uint32_t keep_bits2(uint32_t w, uint32_t t2)
+{
+    const uint32_t z = (w | 0x80008000u) - (t2 & 0x7FFF7FFFu);
+    const uint32_t ge = (w & ~t2) | (~(w ^ t2) & z);
+    uint32_t m;
+    asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(m) : "r"(ge));
+    return m;
 }
 
 // 16-bit word `lane` (0..7, little-endian) of a block.

@@ -29,7 +29,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxExperts = 4096;      // per-warp counters of every expert fit in shared memory
 constexpr int64_t kChunk = 2048;       // least slots of a sorting block
 constexpr int64_t kMaxChunks = 128;    // most sorting blocks (each reads every block's counts)
-constexpr int kGroup = 8;              // choices whose dot products a thread keeps at once
+constexpr int kMostGroup = 8;          // most choices whose rows a thread has in flight at once
+constexpr int kPadRows = 32;           // rows whose padding a block clears
 
 // ---------------------------------------------------------------------------
 // Sorting.
@@ -264,22 +265,39 @@ __device__ __forceinline__ int phase_of(const T* base, int64_t row, int64_t cols
 struct Moe {
     int64_t tokens, cols, rows, slots;
     int topk;
-    int col_blocks;       // blocks over a token's columns
+    int team;             // threads on a token's columns (warps of one block)
+    int col_blocks;       // teams over a token's columns
     int64_t token_blocks; // blocks before the padding's
 };
 
-__device__ __forceinline__ int64_t row_or_none(int r, int64_t rows) { return r >= 0 && r < rows ? r : -1; }
+// The token and the columns' part of a thread's team; false where there is none.
+struct Place {
+    int64_t token, first, step;  // first column (a multiple of 8) and the distance between a thread's chunks
+    int part;                    // which of the token's teams
+};
+__device__ __forceinline__ bool place(const Moe& m, Place& p)
+{
+    const int64_t team = (int64_t)blockIdx.x * (kThreads / m.team) + threadIdx.x / m.team;
+    p.token = team / m.col_blocks;
+    p.part = (int)(team % m.col_blocks);
+    p.first = ((int64_t)p.part * m.team + threadIdx.x % m.team) * 8;
+    p.step = (int64_t)m.col_blocks * m.team * 8;
+    return p.token < m.tokens;
+}
 
-// Zeroes the padding rows among [256 b, 256 b + 256): a warp looks at 32 rows
+__device__ __forceinline__ int row_or_none(int r, int64_t rows) { return r >= 0 && r < rows ? r : -1; }
+
+// Zeroes the padding rows among [32 b, 32 b + 32): a warp looks at four rows
 // and clears those without a slot.
 template <typename T, bool FAST>
 __device__ __forceinline__ void clear_padding(T* out, float* out_weight, const int32_t* __restrict__ slot_of,
                                               const Moe& m, int64_t b)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t r0 = b * kThreads + warp * 32, r = r0 + lane;
+    constexpr int kEach = kPadRows / kWarps;
+    const int64_t r0 = b * kPadRows + warp * kEach, r = r0 + lane;
     bool pad = false;
-    if (r < m.rows) {
+    if (lane < kEach && r < m.rows) {
         const int s = slot_of[r];
         pad = s < 0 || s >= m.slots;
         if (pad && out_weight)
@@ -306,36 +324,35 @@ moe_permute(const T* __restrict__ x, const int32_t* __restrict__ row_of, const i
         clear_padding<T, FAST>(out, out_weight, slot_of, m, (int64_t)blockIdx.x - m.token_blocks);
         return;
     }
-    const int64_t t = blockIdx.x / m.col_blocks;
-    const int cb = (int)(blockIdx.x % m.col_blocks);
-    const int32_t* rows = row_of + t * m.topk;
-    if (weight && cb == 0)
-        for (int j = threadIdx.x; j < m.topk; j += kThreads) {
-            const int64_t r = row_or_none(rows[j], m.rows);
+    Place p;
+    if (!place(m, p))
+        return;
+    const int32_t* rows = row_of + p.token * m.topk;
+    if (weight && p.part == 0)
+        for (int j = threadIdx.x % m.team; j < m.topk; j += m.team) {
+            const int r = row_or_none(rows[j], m.rows);
             if (r >= 0)
-                out_weight[r] = weight[t * m.topk + j];
+                out_weight[r] = weight[p.token * m.topk + j];
         }
     const Span<T> src = span_of(x, m.tokens * m.cols);
     if (FAST) {
-        for (int64_t k = ((int64_t)cb * kThreads + threadIdx.x) * 8; k < m.cols; k += (int64_t)m.col_blocks * kThreads * 8) {
+        for (int64_t k = p.first; k < m.cols; k += p.step) {
             Raw8<T> raw;
-            ld8(x + t * m.cols + k, raw);
+            ld8(x + p.token * m.cols + k, raw);
             for (int j = 0; j < m.topk; ++j) {
-                const int64_t r = row_or_none(rows[j], m.rows);
+                const int r = row_or_none(rows[j], m.rows);
                 if (r >= 0)
                     st8(out + r * m.cols + k, raw);
             }
         }
     } else {
         for (int j = 0; j < m.topk; ++j) {
-            const int64_t r = row_or_none(rows[j], m.rows);
+            const int r = row_or_none(rows[j], m.rows);
             if (r < 0)
                 continue;
-            const int a = phase_of<T, FAST>(out, r, m.cols);
-            for (int64_t k = ((int64_t)cb * kThreads + threadIdx.x) * 8 - a; k < m.cols;
-                 k += (int64_t)m.col_blocks * kThreads * 8) {
+            for (int64_t k = p.first - phase_of<T, FAST>(out, r, m.cols); k < m.cols; k += p.step) {
                 float f[8];
-                load_cols<T, FAST>(src, t, k, m.cols, f);
+                load_cols<T, FAST>(src, p.token, k, m.cols, f);
                 store_cols<T, FAST>(out, r, k, m.cols, f);
             }
         }
@@ -344,48 +361,104 @@ moe_permute(const T* __restrict__ x, const int32_t* __restrict__ row_of, const i
 
 // ---------------------------------------------------------------------------
 // Unpermute (and permute's backward, without weights): a token's rows added
-// in choice order.
+// in choice order, G of them in flight at a time.  A choice without a row
+// reads row 0 instead, which is not added.
 // ---------------------------------------------------------------------------
-template <typename T, bool FAST>
+template <typename T, bool FAST, int G>
 __global__ void __launch_bounds__(kThreads)
 moe_unpermute(const T* __restrict__ y, const int32_t* __restrict__ row_of, const float* __restrict__ weight,
               const float* __restrict__ row_weight, T* __restrict__ out, float* __restrict__ dweight, const Moe m)
 {
-    const int64_t t = blockIdx.x / m.col_blocks;
-    const int cb = (int)(blockIdx.x % m.col_blocks);
-    const int32_t* rows = row_of + t * m.topk;
-    if (dweight && cb == 0)
-        for (int j = threadIdx.x; j < m.topk; j += kThreads) {
-            const int64_t r = row_or_none(rows[j], m.rows);
-            dweight[t * m.topk + j] = r >= 0 ? row_weight[r] : 0.0f;
+    Place p;
+    if (!place(m, p))
+        return;
+    const int32_t* rows = row_of + p.token * m.topk;
+    if (dweight && p.part == 0)
+        for (int j = threadIdx.x % m.team; j < m.topk; j += m.team) {
+            const int r = row_or_none(rows[j], m.rows);
+            dweight[p.token * m.topk + j] = r >= 0 ? row_weight[r] : 0.0f;
         }
     const Span<T> src = span_of(y, m.rows * m.cols);
-    const int a = phase_of<T, FAST>(out, t, m.cols);
-    for (int64_t k = ((int64_t)cb * kThreads + threadIdx.x) * 8 - a; k < m.cols;
-         k += (int64_t)m.col_blocks * kThreads * 8) {
+    for (int64_t k = p.first - phase_of<T, FAST>(out, p.token, m.cols); k < m.cols; k += p.step) {
         float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-        for (int j = 0; j < m.topk; ++j) {
-            const int64_t r = row_or_none(rows[j], m.rows);
-            if (r < 0)
-                continue;
-            const float w = weight ? weight[t * m.topk + j] : 1.0f;
-            float f[8];
-            load_cols<T, FAST>(src, r, k, m.cols, f);
+        for (int j0 = 0; j0 < m.topk; j0 += G) {
+            int r[G];
+            float w[G];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                acc[i] = fmaf(w, f[i], acc[i]);
+            for (int i = 0; i < G; ++i) {
+                r[i] = j0 + i < m.topk ? row_or_none(rows[j0 + i], m.rows) : -1;
+                w[i] = weight && r[i] >= 0 ? weight[p.token * m.topk + j0 + i] : 1.0f;
+            }
+            if constexpr (FAST) {
+                Raw8<T> raw[G];
+                if (m.rows > 0) {
+#pragma unroll
+                    for (int i = 0; i < G; ++i)
+                        ld8(y + (r[i] < 0 ? 0 : r[i]) * m.cols + k, raw[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    if (r[i] < 0)
+                        continue;
+                    float f[8];
+                    widen8(raw[i], f);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        acc[c] = fmaf(w[i], f[c], acc[c]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    if (r[i] < 0)
+                        continue;
+                    float f[8];
+                    load_cols<T, FAST>(src, r[i], k, m.cols, f);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        acc[c] = fmaf(w[i], f[c], acc[c]);
+                }
+            }
         }
-        store_cols<T, FAST>(out, t, k, m.cols, acc);
+        store_cols<T, FAST>(out, p.token, k, m.cols, acc);
     }
 }
 
 // ---------------------------------------------------------------------------
-// Unpermute's backward: one block per token reads g and the token's rows of y
-// once, writes w * g to the rows of dy and keeps the dot products, kGroup
-// choices at a time.
+// Unpermute's backward: a team reads a token's g and its rows of y once,
+// writes w * g to the rows of dy and keeps the dot products, G choices at a
+// time.
 // ---------------------------------------------------------------------------
-template <typename T, bool FAST>
+// Sums G values a lane over the warp, halving what a lane keeps with each
+// exchange: afterwards lane l has the sum of value index_of(l).
+template <int G>
+__device__ __forceinline__ float warp_sums(float (&v)[G])
+{
+    const int lane = threadIdx.x & 31;
+    int n = G;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < G / 2; ++i)
+                if (i < n) {
+                    const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+                }
+        } else {
+            v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+        }
+    }
+    return v[0];
+}
+template <int G>
+__device__ __forceinline__ int index_of(int lane)
+{
+    return G == 8 ? lane >> 2 : G == 4 ? lane >> 3 : G == 2 ? lane >> 4 : 0;
+}
+
+template <typename T, bool FAST, int G>
 __global__ void __launch_bounds__(kThreads)
 moe_unpermute_bwd(const T* __restrict__ g, const T* __restrict__ y, const int32_t* __restrict__ row_of,
                   const int32_t* __restrict__ slot_of, const float* __restrict__ weight, T* __restrict__ dy,
@@ -395,31 +468,39 @@ moe_unpermute_bwd(const T* __restrict__ g, const T* __restrict__ y, const int32_
         clear_padding<T, FAST>(dy, nullptr, slot_of, m, (int64_t)blockIdx.x - m.token_blocks);
         return;
     }
-    __shared__ float part[kGroup][kWarps];
-    const int64_t t = blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float part[kWarps][G];
+    Place p;
+    const bool live = place(m, p);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = m.team >> 5;
     const Span<T> gs = span_of(g, m.tokens * m.cols), ys = span_of(y, m.rows * m.cols);
-    for (int j0 = 0; j0 < m.topk; j0 += kGroup) {
-        int64_t row[kGroup];
-        float w[kGroup], dot[kGroup];
+    for (int j0 = 0; j0 < m.topk; j0 += G) {
+        int r[G];
+        float w[G], dot[G];
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i) {
-            const int64_t s = t * m.topk + j0 + i;
-            row[i] = j0 + i < m.topk ? row_or_none(row_of[s], m.rows) : -1;
-            w[i] = weight && row[i] >= 0 ? weight[s] : 1.0f;
+        for (int i = 0; i < G; ++i) {
+            const int64_t s = p.token * m.topk + j0 + i;
+            r[i] = live && j0 + i < m.topk ? row_or_none(row_of[s], m.rows) : -1;
+            w[i] = weight && r[i] >= 0 ? weight[s] : 1.0f;
             dot[i] = 0.0f;
         }
-        if (FAST) {
-            for (int64_t k = (int64_t)threadIdx.x * 8; k < m.cols; k += kThreads * 8) {
-                float gf[8];
-                load_cols<T, FAST>(gs, t, k, m.cols, gf);
+        if constexpr (FAST) {
+            for (int64_t k = p.first; live && k < m.cols; k += p.step) {
+                Raw8<T> raw[G], graw;
+                ld8(g + p.token * m.cols + k, graw);
+                if (dweight && m.rows > 0) {
 #pragma unroll
-                for (int i = 0; i < kGroup; ++i) {
-                    if (row[i] < 0)
+                    for (int i = 0; i < G; ++i)
+                        ld8(y + (r[i] < 0 ? 0 : r[i]) * m.cols + k, raw[i]);
+                }
+                float gf[8];
+                widen8(graw, gf);
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    if (r[i] < 0)
                         continue;
                     float f[8];
                     if (dweight) {
-                        load_cols<T, FAST>(ys, row[i], k, m.cols, f);
+                        widen8(raw[i], f);
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
                             dot[i] = fmaf(gf[c], f[c], dot[i]);
@@ -427,20 +508,19 @@ moe_unpermute_bwd(const T* __restrict__ g, const T* __restrict__ y, const int32_
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         f[c] = gf[c] * w[i];
-                    store_cols<T, FAST>(dy, row[i], k, m.cols, f);
+                    store_cols<T, FAST>(dy, r[i], k, m.cols, f);
                 }
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) {
-                if (row[i] < 0)
+            for (int i = 0; i < G; ++i) {
+                if (r[i] < 0)
                     continue;
-                const int a = phase_of<T, FAST>(dy, row[i], m.cols);
-                for (int64_t k = (int64_t)threadIdx.x * 8 - a; k < m.cols; k += kThreads * 8) {
+                for (int64_t k = p.first - phase_of<T, FAST>(dy, r[i], m.cols); k < m.cols; k += p.step) {
                     float gf[8], f[8];
-                    load_cols<T, FAST>(gs, t, k, m.cols, gf);
+                    load_cols<T, FAST>(gs, p.token, k, m.cols, gf);
                     if (dweight) {
-                        load_cols<T, FAST>(ys, row[i], k, m.cols, f);
+                        load_cols<T, FAST>(ys, r[i], k, m.cols, f);
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
                             dot[i] = fmaf(gf[c], f[c], dot[i]);
@@ -448,27 +528,29 @@ moe_unpermute_bwd(const T* __restrict__ g, const T* __restrict__ y, const int32_
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         f[c] = gf[c] * w[i];
-                    store_cols<T, FAST>(dy, row[i], k, m.cols, f);
+                    store_cols<T, FAST>(dy, r[i], k, m.cols, f);
                 }
             }
         }
         if (!dweight)
             continue;
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i) {
-            float v = dot[i];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            if (lane == 0)
-                part[i][warp] = v;
+        const float sum = warp_sums<G>(dot);
+        const int i = index_of<G>(lane);
+        const bool first = (lane & (32 / G - 1)) == 0;  // one lane of each value
+        if (warps == 1) {
+            if (first && live && j0 + i < m.topk)
+                dweight[p.token * m.topk + j0 + i] = sum;
+            continue;
         }
+        if (first)
+            part[warp][i] = sum;
         __syncthreads();
-        if (threadIdx.x < kGroup && j0 + (int)threadIdx.x < m.topk) {
+        const int t = threadIdx.x % m.team;
+        if (live && t < G && j0 + t < m.topk) {
             float v = 0.0f;
-            for (int i = 0; i < kWarps; ++i)
-                v += part[threadIdx.x][i];
-            dweight[t * m.topk + j0 + threadIdx.x] = v;
+            for (int q = 0; q < warps; ++q)
+                v += part[warp + q][t];  // t < G <= 32: the team's first warp
+            dweight[p.token * m.topk + j0 + t] = v;
         }
         __syncthreads();
     }
@@ -490,19 +572,38 @@ int check(int dt, int64_t tokens, int64_t topk, int64_t cols, int64_t rows)
     return MFX_OK;
 }
 
-// `blocks` column blocks a token, so that few tokens still fill the device.
+// A team of up to a block's threads on each token, two chunks a thread, and
+// (`split`) several teams where few tokens would leave SMs idle.
 Moe plan(int64_t tokens, int64_t topk, int64_t cols, int64_t rows, bool split)
 {
     Moe m = {};
     m.tokens = tokens, m.cols = cols, m.rows = rows, m.slots = tokens * topk, m.topk = (int)topk;
-    const int64_t most = (cols + 7 + kThreads * 8 - 1) / (kThreads * 8), fill = (int64_t)sm_count() * 8;
+    const int64_t chunks = (cols + 7) / 8, fill = (int64_t)sm_count() * 8 * kThreads;
+    m.team = kThreads;
+    while (m.team > 32 && (int64_t)m.team >= chunks)
+        m.team /= 2;
+    while (m.team < kThreads && tokens * m.team * 2 <= fill && (int64_t)m.team < chunks)
+        m.team *= 2;
     m.col_blocks = 1;
-    if (split && tokens > 0 && tokens < fill) {
-        const int64_t want = fill / tokens;
-        m.col_blocks = (int)(want < most ? want : most);
-    }
-    m.token_blocks = tokens * m.col_blocks;
+    while (split && (int64_t)m.team * m.col_blocks < chunks && tokens * m.team * m.col_blocks < fill)
+        ++m.col_blocks;
+    const int64_t teams = kThreads / m.team;
+    m.token_blocks = (tokens * m.col_blocks + teams - 1) / teams;
     return m;
+}
+
+// Calls f(G) with the choices taken at once, as a type: the least power of two
+// that has them all, up to kMostGroup.
+template <typename F>
+int by_group(int64_t topk, F f)
+{
+    if (topk <= 1)
+        return f(std::integral_constant<int, 1>{});
+    if (topk <= 2)
+        return f(std::integral_constant<int, 2>{});
+    if (topk <= 4)
+        return f(std::integral_constant<int, 4>{});
+    return f(std::integral_constant<int, kMostGroup>{});
 }
 
 bool fast_rows(int64_t cols, const void* a, const void* b, const void* c = nullptr)
@@ -608,7 +709,7 @@ extern "C" int mfx_moe_permute_fwd(int dt, int64_t tokens, int64_t topk, int64_t
         overlaps(out_weight, 4 * rows, row_of, 4 * slots) || overlaps(out_weight, 4 * rows, slot_of, 4 * rows))
         return MFX_ERR_ALIAS;
     Moe m = plan(topk > 0 ? tokens : 0, topk, cols, rows, true);
-    const int64_t blocks = m.token_blocks + (rows + kThreads - 1) / kThreads;
+    const int64_t blocks = m.token_blocks + (rows + kPadRows - 1) / kPadRows;
     if (blocks > INT32_MAX)
         return MFX_ERR_SHAPE;
     const auto go = [&](auto t, auto fast) {
@@ -644,11 +745,13 @@ int unpermute(int dt, int64_t tokens, int64_t topk, int64_t cols, int64_t rows, 
     if (m.token_blocks > INT32_MAX)
         return MFX_ERR_SHAPE;
     const auto go = [&](auto t, auto fast) {
-        using T = decltype(t);
-        moe_unpermute<T, decltype(fast)::value>
-            <<<(unsigned)m.token_blocks, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-                static_cast<const T*>(y), row_of, weight, row_weight, static_cast<T*>(out), dweight, m);
-        return launch_status();
+        return by_group(topk, [&](auto group) {
+            using T = decltype(t);
+            moe_unpermute<T, decltype(fast)::value, decltype(group)::value>
+                <<<(unsigned)m.token_blocks, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+                    static_cast<const T*>(y), row_of, weight, row_weight, static_cast<T*>(out), dweight, m);
+            return launch_status();
+        });
     };
     if (fast_rows(cols, y, out))
         return dt == MFX_BF16 ? go(bf16{}, std::true_type{}) : go(float{}, std::true_type{});
@@ -691,16 +794,18 @@ extern "C" int mfx_moe_unpermute_bwd(int dt, int64_t tokens, int64_t topk, int64
     if (overlaps(dy, yb, dweight, 4 * slots))
         return MFX_ERR_ALIAS;
     const Moe m = plan(topk > 0 ? tokens : 0, topk, cols, rows, false);
-    const int64_t blocks = m.token_blocks + (rows + kThreads - 1) / kThreads;
+    const int64_t blocks = m.token_blocks + (rows + kPadRows - 1) / kPadRows;
     if (blocks > INT32_MAX)
         return MFX_ERR_SHAPE;
     const auto go = [&](auto t, auto fast) {
-        using T = decltype(t);
-        moe_unpermute_bwd<T, decltype(fast)::value>
-            <<<(unsigned)blocks, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-                static_cast<const T*>(g), static_cast<const T*>(y), row_of, slot_of, weight, static_cast<T*>(dy),
-                dweight, m);
-        return launch_status();
+        return by_group(topk, [&](auto group) {
+            using T = decltype(t);
+            moe_unpermute_bwd<T, decltype(fast)::value, decltype(group)::value>
+                <<<(unsigned)blocks, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+                    static_cast<const T*>(g), static_cast<const T*>(y), row_of, slot_of, weight, static_cast<T*>(dy),
+                    dweight, m);
+            return launch_status();
+        });
     };
     if (fast_rows(cols, g, dy, dweight ? y : nullptr))
         return dt == MFX_BF16 ? go(bf16{}, std::true_type{}) : go(float{}, std::true_type{});

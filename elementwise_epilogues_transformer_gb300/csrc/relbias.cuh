@@ -52,41 +52,8 @@ struct Geom {
     float grad_log2, dot, unfold, post;
     uint32_t thresh_hi;        // keep threshold in the upper half-word
     uint64_t elem_base;
-    uint32_t first_x, first_y, first_z;  // what the generator's first round adds to each block
-    uint32_t key0[10], key1[10];         // its key of each round
+    MaskGen gen;
 };
-
-// mask_block() with the rounds' keys read from the parameters instead of kept
-// in registers, and the first round's product of the offset, the same for
-// every block, formed on the host.
-// N blocks, j, j + step, ..., go round by round together: a block alone is one
-// chain of dependent products.
-template <int N>
-__device__ __forceinline__ void keep_blocks(const Geom& g, uint64_t j, int step, uint4 (&c)[N])
-{
-    uint32_t lo0, hi0, lo1, hi1;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const uint64_t jn = j + (uint64_t)(n * step);
-        mul_hilo(0xD2511F53u, (uint32_t)jn, lo0, hi0);
-        c[n] = make_uint4((uint32_t)(jn >> 32) ^ g.first_x, g.first_y, hi0 ^ g.first_z, lo0);
-    }
-#pragma unroll
-    for (int i = 1; i < 10; ++i) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            mul_hilo(0xD2511F53u, c[n].x, lo0, hi0);
-            mul_hilo(0xCD9E8D57u, c[n].z, lo1, hi1);
-            c[n] = make_uint4(hi1 ^ c[n].y ^ g.key0[i], lo1, hi0 ^ c[n].w ^ g.key1[i], lo0);
-        }
-    }
-}
-__device__ __forceinline__ uint4 keep_block(const Geom& g, uint64_t j)
-{
-    uint4 c[1];
-    keep_blocks<1>(g, j, 0, c);
-    return c[0];
-}
 
 // The window holds the bias (times log2 e) of the positions around the query:
 // entry i is the one at k - pos = i - reach, -8 <= i <= reach + hi + 8, the
@@ -428,11 +395,15 @@ __device__ __forceinline__ bool some_part(int k0, int end)
     return !CHECK || __any_sync(0xFFFFFFFFu, k0 < end);
 }
 
+__device__ __forceinline__ uint4 one_block(const MaskGen& m, uint64_t j)
+{
+    uint4 c[1];
+    mask_blocks<1>(m, j, 0, c);
+    return c[0];
+}
+
 // Keep flags of a chunk applied to its values: 16-bit word j of the block
-// belongs to element j.  On packed bf16 pairs the flags become bit masks: with
-// H the top bit of each half, (w | H) - (t & ~H) has it set where the low 15
-// bits of w reach those of t, one three-input operation adds the top bits'
-// say, and a byte permutation spreads it.
+// belongs to element j.
 __device__ __forceinline__ void drop_pairs(float2 (&v)[4], const uint4& blk, uint32_t thresh_hi)
 {
     const uint32_t w[4] = {blk.x, blk.y, blk.z, blk.w};
@@ -441,14 +412,6 @@ __device__ __forceinline__ void drop_pairs(float2 (&v)[4], const uint4& blk, uin
         v[i].x = (w[i] << 16) >= thresh_hi ? v[i].x : 0.0f;
         v[i].y = w[i] >= thresh_hi ? v[i].y : 0.0f;
     }
-}
-__device__ __forceinline__ uint32_t keep_bits2(uint32_t w, uint32_t t2)
-{
-    const uint32_t z = (w | 0x80008000u) - (t2 & 0x7FFF7FFFu);
-    const uint32_t ge = (w & ~t2) | (~(w ^ t2) & z);
-    uint32_t m;
-    asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(m) : "r"(ge));
-    return m;
 }
 __device__ __forceinline__ void drop_raw(Raw8<bf16>& r, const uint4& blk, uint32_t thresh_hi)
 {
@@ -650,11 +613,7 @@ inline Geom make_geom(const Args& a, const Buckets& w, const void* x)
     const double t = std::ceil((double)a.p * 65536.0);
     g.thresh_hi = (uint32_t)(t > 65535.0 ? 65535.0 : t) << 16;
     g.elem_base = a.elem_base;
-    for (uint32_t i = 0; i < 10; ++i)
-        g.key0[i] = (uint32_t)a.seed + i * 0x9E3779B9u, g.key1[i] = (uint32_t)(a.seed >> 32) + i * 0xBB67AE85u;
-    const uint64_t product = (uint64_t)0xCD9E8D57u * (uint32_t)a.offset;
-    g.first_x = (uint32_t)(product >> 32) ^ g.key0[0], g.first_y = (uint32_t)product;
-    g.first_z = (uint32_t)(a.offset >> 32) ^ g.key1[0];
+    g.gen = make_mask_gen(a.seed, a.offset);
     return g;
 }
 

@@ -105,7 +105,7 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
                     if constexpr (DROP && !CHECK) {
                         // the keep flags of all chunks together, while the copies arrive
                         uint4 kb[C];
-                        keep_blocks<C>(g, o.block0 + tid, g.team, kb);
+                        mask_blocks<C>(g.gen, o.block0 + tid, g.team, kb);
                         copies_wait<0>();
                         Raw8<T> r[C];
 #pragma unroll
@@ -146,7 +146,7 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
                     for (int i = 0; i < 4; ++i)
                         Q[c][i] = make_float2(exp2_of(Q[c][i].x), exp2_of(Q[c][i].y));
                     if (DROP && (!STAGED || CHECK) && g.drop)
-                        drop_raw(zc, keep_block(g, o.block0 + ch), g.thresh_hi);
+                        drop_raw(zc, one_block(g.gen, o.block0 + ch), g.thresh_hi);
                     float2 f[4];
                     pairs_of(zc, f);
                     // what the upstream gradient holds at keys left out does not count

@@ -106,7 +106,7 @@ __device__ __noinline__ void shifted_row(const T* x, T* y, float* stats, const R
     for (int k = first; o.chunks && k < g.sk; k += step) {
         float v = k < o.end ? exp2_of(score(k) - ref) * inv : 0.0f;
         if (DROP && g.drop && k < o.end)
-            v = word16(keep_block(g, o.block0 + ((k + o.a) >> 3)), (k + o.a) & 7) >= g.thresh_hi >> 16 ? v * g.keep_scale
+            v = word16(one_block(g.gen, o.block0 + ((k + o.a) >> 3)), (k + o.a) & 7) >= g.thresh_hi >> 16 ? v * g.keep_scale
                                                                                                        : 0.0f;
         store1(y + e + k, v);
     }
@@ -217,7 +217,7 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
                 for (int c = 0; c < C; ++c) {
                     const int ch = c0 + c * g.team, k0 = ch * 8 - o.a;
                     if (DROP && !CHECK && c % PAIR == 0)
-                        keep_blocks<PAIR>(g, o.block0 + ch, g.team, kb);
+                        mask_blocks<PAIR>(g.gen, o.block0 + ch, g.team, kb);
                     float2 p[4];
                     if (some_part<CHECK>(k0, o.end)) {
                         float f = f1;
@@ -235,7 +235,7 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
                         for (int i = 0; i < 4; ++i)
                             p[i] = pmul(s[c][i], f2(f));
                         if (DROP && g.drop)
-                            drop_pairs(p, CHECK ? keep_block(g, o.block0 + ch) : kb[c % PAIR], g.thresh_hi);
+                            drop_pairs(p, CHECK ? one_block(g.gen, o.block0 + ch) : kb[c % PAIR], g.thresh_hi);
                         if (CHECK)
                             MFX_RARELY((!FAST && k0 < 0) || k0 + 8 > o.end)
                                 fill_outside(p, k0, o.end, 0.0f);
