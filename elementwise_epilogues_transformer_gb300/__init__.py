@@ -149,9 +149,14 @@ def _cuda(t, name, dtype=None):
 def _like(t, name, shape, dtype):
     """A CUDA tensor of the given shape and dtype (an output or gradient buffer)."""
     _cuda(t, name, dtype)
-    if t is None or tuple(t.shape) != tuple(shape):
+    if t is None or t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}")
     return t
+
+
+def _same_device(t, dev, name):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on device {dev}, the data's")
 
 
 # the current stream's raw handle without building a Stream object per call
@@ -184,7 +189,7 @@ def mfx_device_error():
 
 
 def _call(name, *args):
-    st = getattr(lib(), name)(*args)
+    st = getattr(_lib or lib(), name)(*args)
     if st != 0:
         raise MfxError(st, name)
 
@@ -384,32 +389,33 @@ def mfx_scaled_upper_triang_masked_softmax_bwd(dy, y, scale, dx=None, stream=Non
 # scale-mask-softmax with a learned relative position bias and dropout
 # ---------------------------------------------------------------------------
 def _relbias_args(x, table, mask, max_distance, bidirectional, causal, q_start, seq_start, p, seed, offset, elem_base):
-    """The arguments that forward and backward share, from table_dt on."""
+    """x's shape and the arguments that forward and backward share, from
+    table_dt on."""
     _cuda(x, "x")
-    _cuda(table, "table")
-    _cuda(mask, "mask", x.dtype)
-    _cuda(seq_start, "seq_start", torch.int32)
     if x.dim() != 4:
         raise ValueError("x must have 4 dims [b, np, sq, sk]")
-    b, np_, sq, sk = x.shape
-    buckets = 0
+    shape = b, np_, _, sk = tuple(x.shape)
+    dev, tdt, tptr, buckets = x.get_device(), MFX_F32, None, 0
     if table is not None:
+        _cuda(table, "table")
         if table.dim() != 2 or table.shape[1] != np_:
             raise ValueError("table must have the shape [num_buckets, np]")
-        buckets = table.shape[0]
-    mb = mnp = msq = 1
+        _same_device(table, dev, "table")
+        tdt, tptr, buckets = dtype_code(table.dtype), table.data_ptr(), table.shape[0]
+    mptr, mb, mnp, msq = None, 1, 1, 1
     if mask is not None:
+        _cuda(mask, "mask", x.dtype)
         if mask.dim() != 4 or mask.shape[3] != sk:
             raise ValueError("mask must have the shape [1 or b, 1 or np, 1 or sq, sk]")
-        mb, mnp, msq, _ = mask.shape
-    if seq_start is not None and tuple(seq_start.shape) != (b,):
-        raise ValueError("seq_start must have one entry per batch")
-    for name, t in (("table", table), ("mask", mask), ("seq_start", seq_start)):
-        if t is not None and t.device != x.device:
-            raise ValueError(f"{name} must be on x's device")
-    return (dtype_code(table.dtype if table is not None else x.dtype), _ptr(table), buckets, int(max_distance),
-            int(bool(bidirectional)), _ptr(mask), mb, mnp, msq, int(bool(causal)), int(q_start), _ptr(seq_start),
-            float(p), int(seed) % 2**64, int(offset) % 2**64, int(elem_base))
+        _same_device(mask, dev, "mask")
+        mptr, (mb, mnp, msq, _) = mask.data_ptr(), mask.shape
+    sptr = None
+    if seq_start is not None:
+        _like(seq_start, "seq_start", (b,), torch.int32)
+        _same_device(seq_start, dev, "seq_start")
+        sptr = seq_start.data_ptr()
+    return shape, (tdt, tptr, buckets, max_distance, 1 if bidirectional else 0, mptr, mb, mnp, msq, 1 if causal else 0,
+                   q_start, sptr, p, seed % 2**64, offset % 2**64, elem_base)
 
 
 def mfx_relbias_softmax_dropout_fwd(x, scale, table=None, mask=None, max_distance=128, bidirectional=True,
@@ -419,14 +425,14 @@ def mfx_relbias_softmax_dropout_fwd(x, scale, table=None, mask=None, max_distanc
     the last dim of x [b, np, sq, sk]; table: [num_buckets, np] (x's dtype or
     float32); pos = q_start + seq_start[b] + q.  Returns (y, stats); stats
     [b, np, sq, 2] is what the backward needs (None with need_stats=False)."""
-    shared = _relbias_args(x, table, mask, max_distance, bidirectional, causal, q_start, seq_start, p, seed, offset,
-                           elem_base)
-    y = torch.empty_like(x) if y is None else _like(y, "y", x.shape, x.dtype)
+    shape, shared = _relbias_args(x, table, mask, max_distance, bidirectional, causal, q_start, seq_start, p, seed,
+                                  offset, elem_base)
+    y = torch.empty_like(x) if y is None else _like(y, "y", shape, x.dtype)
     if stats is not None:
-        _like(stats, "stats", (*x.shape[:3], 2), torch.float32)
+        _like(stats, "stats", (*shape[:3], 2), torch.float32)
     elif need_stats:
-        stats = torch.empty((*x.shape[:3], 2), dtype=torch.float32, device=x.device)
-    _call("mfx_relbias_softmax_dropout_fwd", dtype_code(x.dtype), *x.shape, _ptr(x), float(scale), *shared, _ptr(y),
+        stats = torch.empty((*shape[:3], 2), dtype=torch.float32, device=x.device)
+    _call("mfx_relbias_softmax_dropout_fwd", dtype_code(x.dtype), *shape, x.data_ptr(), scale, *shared, y.data_ptr(),
           _ptr(stats), _stream(stream, x))
     return y, stats
 
@@ -436,23 +442,25 @@ def mfx_relbias_softmax_dropout_bwd(dy, x, stats, scale, table=None, mask=None, 
                                     dx=None, dtable=None, need_dtable=True, workspace=None, stream=None):
     """(dx, dtable) from the forward's inputs and stats; dtable has table's
     shape and dtype (None without a table or with need_dtable=False)."""
-    shared = _relbias_args(x, table, mask, max_distance, bidirectional, causal, q_start, seq_start, p, seed, offset,
-                           elem_base)
-    _like(dy, "dy", x.shape, x.dtype)
-    _like(stats, "stats", (*x.shape[:3], 2), torch.float32)
-    dx = torch.empty_like(x) if dx is None else _like(dx, "dx", x.shape, x.dtype)
+    shape, shared = _relbias_args(x, table, mask, max_distance, bidirectional, causal, q_start, seq_start, p, seed,
+                                  offset, elem_base)
+    _like(dy, "dy", shape, x.dtype)
+    _like(stats, "stats", (*shape[:3], 2), torch.float32)
+    dx = torch.empty_like(x) if dx is None else _like(dx, "dx", shape, x.dtype)
     if dtable is not None:
         if table is None:
             raise ValueError("dtable needs a table")
         _like(dtable, "dtable", table.shape, table.dtype)
     elif table is not None and need_dtable:
         dtable = torch.empty_like(table)
-    head = (dtype_code(x.dtype), *x.shape, _ptr(dy), _ptr(x), _ptr(stats), float(scale), *shared, _ptr(dx), _ptr(dtable))
+    head = (dtype_code(x.dtype), *shape, dy.data_ptr(), x.data_ptr(), stats.data_ptr(), scale, *shared, dx.data_ptr(),
+            _ptr(dtable))
     st = _stream(stream, x)
     if dtable is None:
         _call("mfx_relbias_softmax_dropout_bwd", *head, None, None, st)
     else:
-        _with_workspace("mfx_relbias_softmax_dropout_bwd", head, (st,), x.device, workspace)
+        _with_workspace("mfx_relbias_softmax_dropout_bwd", head, (st,), x.device, workspace,
+                        (x.get_device(), *shape, table.shape[0]))
     return dx, dtable
 
 
@@ -478,31 +486,40 @@ def mfx_moe_sort(expert_of, experts, align=1, capacity=0, rows=None, row_of=None
     tokens, topk = expert_of.shape
     if rows is None:
         rows = slot_of.numel() if slot_of is not None else mfx_moe_rows(tokens, topk, experts, align)
-    new = lambda t, name, shape: (torch.empty(shape, dtype=torch.int32, device=expert_of.device) if t is None  # noqa: E731
-                                  else _like(t, name, shape, torch.int32))
-    row_of, slot_of = new(row_of, "row_of", (tokens, topk)), new(slot_of, "slot_of", (rows,))
-    offsets, counts = new(offsets, "offsets", (experts + 1,)), new(counts, "counts", (experts,))
-    _with_workspace("mfx_moe_sort", (tokens, topk, experts, align, capacity, rows, _ptr(expert_of), _ptr(row_of),
-                                     _ptr(slot_of), _ptr(offsets), _ptr(counts)),
-                    (_stream(stream, expert_of),), expert_of.device, workspace)
+    slots = tokens * topk
+    if row_of is None and slot_of is None and offsets is None and counts is None and experts > 0:
+        # one allocation for the four maps
+        row_of, slot_of, offsets, counts = torch.empty(
+            slots + rows + 2 * experts + 1, dtype=torch.int32, device=expert_of.device).split_with_sizes(
+                [slots, rows, experts + 1, experts])
+        row_of = row_of.view(tokens, topk)
+    else:
+        new = lambda t, name, shape: (torch.empty(shape, dtype=torch.int32, device=expert_of.device)  # noqa: E731
+                                      if t is None else _like(t, name, shape, torch.int32))
+        row_of, slot_of = new(row_of, "row_of", (tokens, topk)), new(slot_of, "slot_of", (rows,))
+        offsets, counts = new(offsets, "offsets", (experts + 1,)), new(counts, "counts", (experts,))
+    _with_workspace("mfx_moe_sort", (tokens, topk, experts, align, capacity, rows, expert_of.data_ptr(),
+                                     row_of.data_ptr(), slot_of.data_ptr(), offsets.data_ptr(), counts.data_ptr()),
+                    (_stream(stream, expert_of),), expert_of.device, workspace, (slots, experts))
     return row_of, slot_of, offsets, counts
 
 
-def _moe_maps(x, row_of, slot_of):
+def _moe_maps(x, row_of, slot_of=None):
+    """(tokens, topk) of the maps, which must be int32 and on x's device."""
     _cuda(row_of, "row_of", torch.int32)
     if row_of.dim() != 2:
         raise ValueError("row_of must have the shape [tokens, topk]")
-    for name, t in (("row_of", row_of), ("slot_of", slot_of)):
-        if t is not None and t.device != x.device:
-            raise ValueError(f"{name} must be on the data's device")
+    dev = x.get_device()
+    _same_device(row_of, dev, "row_of")
     if slot_of is not None:
         _cuda(slot_of, "slot_of", torch.int32)
         if slot_of.dim() != 1:
             raise ValueError("slot_of must have the shape [rows]")
+        _same_device(slot_of, dev, "slot_of")
     return row_of.shape
 
 
-def _moe_data(t, name, rows):
+def _moe_data(t, name, rows=None):
     _cuda(t, name)
     if t.dim() != 2 or (rows is not None and t.shape[0] != rows):
         raise ValueError(f"{name} must have the shape [{'rows' if rows is None else rows}, cols]")
@@ -516,7 +533,7 @@ def mfx_moe_permute_fwd(x, row_of, slot_of, weight=None, out=None, out_weight=No
     tokens, topk = _moe_maps(x, row_of, slot_of)
     _, cols = _moe_data(x, "x", tokens)
     rows = slot_of.shape[0]
-    out = x.new_empty((rows, cols)) if out is None else _like(out, "out", (rows, cols), x.dtype)
+    out = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if out is None else _like(out, "out", (rows, cols), x.dtype)
     if weight is not None:
         _like(weight, "weight", (tokens, topk), torch.float32)
         out_weight = (torch.empty(rows, dtype=torch.float32, device=x.device) if out_weight is None
@@ -532,9 +549,9 @@ def mfx_moe_permute_bwd(g, row_of, g_weight=None, dx=None, dweight=None, stream=
     """(dx [tokens, cols], dweight [tokens, topk]) from the gradients g [rows,
     cols] and g_weight [rows] of mfx_moe_permute_fwd's outputs; dweight is
     None without g_weight."""
-    tokens, topk = _moe_maps(g, row_of, None)
-    rows, cols = _moe_data(g, "g", None)
-    dx = g.new_empty((tokens, cols)) if dx is None else _like(dx, "dx", (tokens, cols), g.dtype)
+    tokens, topk = _moe_maps(g, row_of)
+    rows, cols = _moe_data(g, "g")
+    dx = torch.empty((tokens, cols), dtype=g.dtype, device=g.device) if dx is None else _like(dx, "dx", (tokens, cols), g.dtype)
     if g_weight is not None:
         _like(g_weight, "g_weight", (rows,), torch.float32)
         dweight = (torch.empty((tokens, topk), dtype=torch.float32, device=g.device) if dweight is None
@@ -549,11 +566,11 @@ def mfx_moe_permute_bwd(g, row_of, g_weight=None, dx=None, dweight=None, stream=
 def mfx_moe_unpermute_fwd(y, row_of, weight=None, out=None, stream=None):
     """out [tokens, cols] = sum over a token's rows of y [rows, cols], times
     weight [tokens, topk] (fp32) where given."""
-    tokens, topk = _moe_maps(y, row_of, None)
-    rows, cols = _moe_data(y, "y", None)
+    tokens, topk = _moe_maps(y, row_of)
+    rows, cols = _moe_data(y, "y")
     if weight is not None:
         _like(weight, "weight", (tokens, topk), torch.float32)
-    out = y.new_empty((tokens, cols)) if out is None else _like(out, "out", (tokens, cols), y.dtype)
+    out = torch.empty((tokens, cols), dtype=y.dtype, device=y.device) if out is None else _like(out, "out", (tokens, cols), y.dtype)
     _call("mfx_moe_unpermute_fwd", dtype_code(y.dtype), tokens, topk, cols, rows, _ptr(y), _ptr(row_of), _ptr(weight),
           _ptr(out), _stream(stream, y))
     return out
@@ -579,7 +596,7 @@ def mfx_moe_unpermute_bwd(g, y, row_of, slot_of, weight=None, dy=None, dweight=N
                    else _like(dweight, "dweight", (tokens, topk), torch.float32))
     else:
         dweight = None
-    dy = g.new_empty((rows, cols)) if dy is None else _like(dy, "dy", (rows, cols), g.dtype)
+    dy = torch.empty((rows, cols), dtype=g.dtype, device=g.device) if dy is None else _like(dy, "dy", (rows, cols), g.dtype)
     _call("mfx_moe_unpermute_bwd", dtype_code(g.dtype), tokens, topk, cols, rows, _ptr(g), _ptr(y), _ptr(row_of),
           _ptr(slot_of), _ptr(weight), _ptr(dy), _ptr(dweight), _stream(stream, g))
     return dy, dweight
@@ -722,20 +739,30 @@ def mfx_dropout_bwd(g, p, seed, offset=0, elem_base=0, dx=None, stream=None):
 # ---------------------------------------------------------------------------
 # fused bias gradients (workspace protocol: query the size, then run)
 # ---------------------------------------------------------------------------
-def _with_workspace(name, args_before_ws, tail, device, workspace=None):
+_workspace_bytes = {}  # (entry point, sizes) -> bytes, for calls that say which sizes theirs goes by
+
+
+def _with_workspace(name, args_before_ws, tail, device, workspace=None, sizes=None):
     """Query the workspace size, allocate it and run `name`.  `workspace` is
     None (a fresh uint8 tensor), a uint8 CUDA tensor, or a callable that
-    takes the byte count and returns one (a caller's own allocator)."""
-    size = C.c_size_t(0)
-    _call(name, *args_before_ws, None, C.byref(size), *tail)
+    takes the byte count and returns one (a caller's own allocator).
+    `sizes`: what the workspace's size depends on, so that it is asked for
+    once."""
+    need = _workspace_bytes.get((name, sizes)) if sizes is not None else None
+    if need is None:
+        size = C.c_size_t(0)
+        _call(name, *args_before_ws, None, C.byref(size), *tail)
+        need = int(size.value)
+        if sizes is not None:
+            _workspace_bytes[(name, sizes)] = need
     if workspace is None:
-        workspace = torch.empty(max(int(size.value), 16), dtype=torch.uint8, device=device)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
     else:
         if callable(workspace):
-            workspace = workspace(max(int(size.value), 16))
+            workspace = workspace(max(need, 16))
         _cuda(workspace, "workspace", torch.uint8)
     size = C.c_size_t(workspace.numel())
-    _call(name, *args_before_ws, _ptr(workspace), C.byref(size), *tail)
+    _call(name, *args_before_ws, workspace.data_ptr(), C.byref(size), *tail)
     return workspace
 
 

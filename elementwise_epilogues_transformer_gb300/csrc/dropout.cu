@@ -22,9 +22,6 @@
 #include "mfx_host.h"
 #include "mfx_pipe.cuh"
 
-#ifndef MFX_FLAT_DROP
-#define MFX_FLAT_DROP 1
-#endif
 namespace mfx {
 namespace {
 
@@ -731,38 +728,22 @@ bda_bwd_pipe(const TX* g, const uint8_t* __restrict__ keep, TX* dx, TR* dres, in
     }
 }
 
-// Generic backward: any alignment, length and elem_base (units of up to 8
-// elements; a unit may straddle two generator blocks, as in bda_generic).
+// Generic backward with a read mask: any alignment and length (units of up to
+// 8 elements).
 template <typename TX, typename TR, bool PACKED = false>
 __global__ void __launch_bounds__(kThreads)
-bda_bwd_generic(const TX* g, const uint8_t* keep, TX* dx, TR* dres, int64_t n, float scale, uint32_t thresh,
-                uint64_t seed, uint64_t offset, uint64_t elem_base)
+bda_bwd_generic(const TX* g, const uint8_t* keep, TX* dx, TR* dres, int64_t n, float scale)
 {
     const int64_t S = (int64_t)gridDim.x * kThreads;
     const int64_t units = (n + 7) / 8;
-    const int o = (int)(elem_base & 7u);
     for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units; u += S) {
         const int64_t i0 = u * 8;
         const int cnt = n - i0 < 8 ? (int)(n - i0) : 8;
         float gv[8], d[8];
         load8f(g + i0, false, cnt, gv);
-        uint4 blk0 = make_uint4(0, 0, 0, 0), blk1 = blk0;
-        if (!keep) {
-            const uint64_t j0 = (elem_base + (uint64_t)i0) >> 3;
-            blk0 = mask_block(j0, seed, offset);
-            blk1 = o ? mask_block(j0 + 1, seed, offset) : blk0;
-        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            bool k = false;
-            if (j < cnt) {
-                if (keep) {
-                    k = PACKED ? (keep[u] >> j) & 1u : keep[i0 + j] != 0;
-                } else {
-                    const int lane = o + j;
-                    k = (lane < 8 ? word16(blk0, lane) : word16(blk1, lane - 8)) >= thresh;
-                }
-            }
+            const bool k = j < cnt && (PACKED ? ((keep[u] >> j) & 1u) != 0 : keep[i0 + j] != 0);
             d[j] = k ? __fmul_rn(gv[j], scale) : 0.0f;
         }
         store8f(dx + i0, false, cnt, d);
@@ -779,7 +760,10 @@ bda_bwd_generic(const TX* g, const uint8_t* keep, TX* dx, TR* dres, int64_t n, f
 // elements that do not begin on a generator block (PHASED) a unit needs its
 // block and the next one, which is the block of the lane above: lane 0 hands
 // its next unit's to lane 31, and only the warp's last block is drawn twice.
-// Measured against the ring (bda_bwd_pipe), 32768 x 4099 bf16: see the call.
+// The next round's loads go out before this round's work.  Measured against
+// the ring that the stored-mask backward uses, bf16 32768 x 4099: 90 against
+// 96 us (113 against 253 us at an odd offset, where the ring did not apply);
+// without the early loads 96 us, with two or eight units a lane 98 and 94 us.
 // ---------------------------------------------------------------------------
 struct FlatDrop {
     int64_t n;
@@ -813,19 +797,29 @@ __device__ __forceinline__ void flat_store(T* p, bool wide, const Raw8<T>& r)
 }
 
 template <typename TX, typename TR, int U, bool PHASED>
-__global__ void __launch_bounds__(kThreads, U > 1 ? 4 : 6)
+__global__ void __launch_bounds__(kThreads, U > 1 ? 3 : 6)
 drop_flat(const TX* g, TX* dx, TR* dres, const __grid_constant__ FlatDrop d)
 {
     const int lane = threadIdx.x & 31;
     const int64_t units = (d.n + 7) / 8, whole = d.n / 8;
     const int64_t step = (int64_t)gridDim.x * (kThreads * U);
-    for (int64_t first = ((int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31)) * U; first < units; first += step) {
+    Raw8<TX> ahead[U];
+    const auto load = [&](int64_t first) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if ((d.vec & 1) && first + lane + 32 * k < whole)
+                flat_load(g + (first + lane + 32 * k) * 8, d.vec, ahead[k]);
+    };
+    int64_t first = ((int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31)) * U;
+    if (first < units)
+        load(first);
+    for (; first < units; first += step) {
         const int64_t u0 = first + lane;
         Raw8<TX> r[U];
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            if ((d.vec & 1) && u0 + 32 * k < whole)
-                flat_load(g + (u0 + 32 * k) * 8, d.vec, r[k]);
+            r[k] = ahead[k];
+        load(first + step);
         uint4 kb[U + (PHASED ? 1 : 0)];
         mask_blocks<U + (PHASED ? 1 : 0)>(d.gen, d.block0 + (uint64_t)u0, 32, kb);
 #pragma unroll
@@ -892,9 +886,10 @@ int launch_flat(const TX* g, TX* dx, TR* dres, int64_t n, float scale, uint32_t 
         kern<<<(unsigned)(need < most ? need : most), kThreads, 0, s>>>(g, dx, dres, d);
         return launch_status();
     };
-    // four units a lane where that still gives every SM two blocks
-    if (units >= (int64_t)sm_count() * 2 * kThreads * 4)
-        return d.phase ? go(drop_flat<TX, TR, 4, true>, 4) : go(drop_flat<TX, TR, 4, false>, 4);
+    // several units a lane where that still gives every SM two blocks
+    constexpr int U = sizeof(TX) == 2 ? 4 : 2;
+    if (units >= (int64_t)sm_count() * 2 * kThreads * U)
+        return d.phase ? go(drop_flat<TX, TR, U, true>, U) : go(drop_flat<TX, TR, U, false>, U);
     return d.phase ? go(drop_flat<TX, TR, 1, true>, 1) : go(drop_flat<TX, TR, 1, false>, 1);
 }
 
@@ -908,31 +903,21 @@ int launch_bwd(const void* g, const uint8_t* keep, void* dx, void* dres, int64_t
     double t = std::ceil((double)p * 65536.0);
     const uint32_t thresh = (uint32_t)(t > 65535.0 ? 65535.0 : t);
     const float scale = 1.0f / (1.0f - p);
-    if (!PACKED && !keep && MFX_FLAT_DROP)
+    if (!PACKED && !keep)
         return launch_flat<TX, TR>(gp, dxp, drp, n, scale, thresh, seed, offset, elem_base, s);
-    const bool pipe_ok = MFX_PIPE_BDA && n % 8 == 0 && aligned16(g) && aligned16(dx) &&
-                         (!dres || aligned16(dres)) && (keep ? aligned16(keep) : elem_base % 8 == 0);
-    if (pipe_ok) {
+    if (MFX_PIPE_BDA && n % 8 == 0 && aligned16(g) && aligned16(dx) && (!dres || aligned16(dres)) && aligned16(keep)) {
         const int64_t units = n / 8;
-        if (keep) {
-            constexpr size_t kOut = bwd_bulk_stores(false, false, PACKED) ? BwdOut<TX, TR>::kBytes : 0;
-            constexpr size_t smem = BwdPipe<TX, true, PACKED>::kSmem + kOut;
-            static_assert(smem <= kMaxBlockSmem, "ring and output slots do not fit in a block's shared memory");
-            const Grid grid = plan_grid_ex((const void*)bda_bwd_pipe<TX, TR, false, false, PACKED>, kPipeThreads,
-                                           smem, units, 0, false);
-            bda_bwd_pipe<TX, TR, false, false, PACKED><<<(unsigned)grid.blocks, kPipeThreads, smem, s>>>(
-                gp, keep, dxp, drp, units, scale, thresh, seed, offset, 0);
-        } else {
-            constexpr size_t smem = BwdPipe<TX, false>::kSmem;
-            const Grid grid = plan_grid_ex((const void*)bda_bwd_pipe<TX, TR, true>, kPipeThreads, smem, units, 0, false);
-            bda_bwd_pipe<TX, TR, true><<<(unsigned)grid.blocks, kPipeThreads, smem, s>>>(
-                gp, nullptr, dxp, drp, units, scale, thresh, seed, offset, elem_base / 8);
-        }
+        constexpr size_t kOut = bwd_bulk_stores(false, false, PACKED) ? BwdOut<TX, TR>::kBytes : 0;
+        constexpr size_t smem = BwdPipe<TX, true, PACKED>::kSmem + kOut;
+        static_assert(smem <= kMaxBlockSmem, "ring and output slots do not fit in a block's shared memory");
+        const Grid grid =
+            plan_grid_ex((const void*)bda_bwd_pipe<TX, TR, false, false, PACKED>, kPipeThreads, smem, units, 0, false);
+        bda_bwd_pipe<TX, TR, false, false, PACKED><<<(unsigned)grid.blocks, kPipeThreads, smem, s>>>(
+            gp, keep, dxp, drp, units, scale, thresh, seed, offset, 0);
         return launch_status();
     }
     const Grid grid = plan_grid((const void*)bda_bwd_generic<TX, TR, PACKED>, (n + 7) / 8, 0, false);
-    bda_bwd_generic<TX, TR, PACKED><<<(unsigned)grid.blocks, kThreads, 0, s>>>(gp, keep, dxp, drp, n, scale, thresh,
-                                                                               seed, offset, elem_base);
+    bda_bwd_generic<TX, TR, PACKED><<<(unsigned)grid.blocks, kThreads, 0, s>>>(gp, keep, dxp, drp, n, scale);
     return launch_status();
 }
 

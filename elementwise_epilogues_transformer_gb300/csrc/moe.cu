@@ -204,7 +204,8 @@ moe_place(const int32_t* __restrict__ expert_of, const int* __restrict__ hist, i
 // 16-byte aligned buffers, so every chunk is one (fp32: two) 16-byte access.
 // Otherwise the chunk grid follows the destination row's alignment; sources
 // are read through the aligned vectors that cover them, and the ragged ends
-// element by element.
+// element by element (4096 x 4099, 4 of 60 experts: 45, 64 and 117 us for
+// permute, unpermute and its backward; by 4-byte words instead 74, 145, 193).
 // ---------------------------------------------------------------------------
 template <typename T>
 struct Span {
@@ -272,16 +273,17 @@ struct Moe {
 
 // The token and the columns' part of a thread's team; false where there is none.
 struct Place {
-    int64_t token, first, step;  // first column (a multiple of 8) and the distance between a thread's chunks
-    int part;                    // which of the token's teams
+    int64_t token;
+    int index, count;  // the thread among the token's threads
+    int part;          // which of the token's teams
 };
 __device__ __forceinline__ bool place(const Moe& m, Place& p)
 {
     const int64_t team = (int64_t)blockIdx.x * (kThreads / m.team) + threadIdx.x / m.team;
-    p.token = team / m.col_blocks;
-    p.part = (int)(team % m.col_blocks);
-    p.first = ((int64_t)p.part * m.team + threadIdx.x % m.team) * 8;
-    p.step = (int64_t)m.col_blocks * m.team * 8;
+    p.token = m.col_blocks == 1 ? team : team / m.col_blocks;
+    p.part = (int)(team - p.token * m.col_blocks);
+    p.index = p.part * m.team + threadIdx.x % m.team;
+    p.count = m.col_blocks * m.team;
     return p.token < m.tokens;
 }
 
@@ -306,8 +308,7 @@ __device__ __forceinline__ void clear_padding(T* out, float* out_weight, const i
     const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (unsigned left = __ballot_sync(0xFFFFFFFFu, pad); left; left &= left - 1) {
         const int64_t row = r0 + __ffs(left) - 1;
-        const int a = phase_of<T, FAST>(out, row, m.cols);
-        for (int64_t k = (int64_t)lane * 8 - a; k < m.cols; k += 256)
+        for (int64_t k = (int64_t)lane * 8 - phase_of<T, FAST>(out, row, m.cols); k < m.cols; k += 256)
             store_cols<T, FAST>(out, row, k, m.cols, zero);
     }
 }
@@ -334,25 +335,34 @@ moe_permute(const T* __restrict__ x, const int32_t* __restrict__ row_of, const i
             if (r >= 0)
                 out_weight[r] = weight[p.token * m.topk + j];
         }
-    const Span<T> src = span_of(x, m.tokens * m.cols);
-    if (FAST) {
-        for (int64_t k = p.first; k < m.cols; k += p.step) {
-            Raw8<T> raw;
-            ld8(x + p.token * m.cols + k, raw);
+    const T* src = x + p.token * m.cols;
+    if constexpr (FAST) {
+        const int64_t step = (int64_t)p.count * 8;
+        for (int64_t k = (int64_t)p.index * 8; k < m.cols; k += 2 * step) {
+            const bool two = k + step < m.cols;
+            Raw8<T> raw[2];
+            ld8(src + k, raw[0]);
+            if (two)
+                ld8(src + k + step, raw[1]);
             for (int j = 0; j < m.topk; ++j) {
                 const int r = row_or_none(rows[j], m.rows);
-                if (r >= 0)
-                    st8(out + r * m.cols + k, raw);
+                if (r < 0)
+                    continue;
+                st8(out + r * m.cols + k, raw[0]);
+                if (two)
+                    st8(out + r * m.cols + k + step, raw[1]);
             }
         }
     } else {
+        const Span<T> all = span_of(x, m.tokens * m.cols);
+        const int64_t step = (int64_t)p.count * 8;
         for (int j = 0; j < m.topk; ++j) {
             const int r = row_or_none(rows[j], m.rows);
             if (r < 0)
                 continue;
-            for (int64_t k = p.first - phase_of<T, FAST>(out, r, m.cols); k < m.cols; k += p.step) {
+            for (int64_t k = (int64_t)p.index * 8 - phase_of<T, FAST>(out, r, m.cols); k < m.cols; k += step) {
                 float f[8];
-                load_cols<T, FAST>(src, p.token, k, m.cols, f);
+                load_cols<T, FAST>(all, p.token, k, m.cols, f);
                 store_cols<T, FAST>(out, r, k, m.cols, f);
             }
         }
@@ -378,48 +388,67 @@ moe_unpermute(const T* __restrict__ y, const int32_t* __restrict__ row_of, const
             const int r = row_or_none(rows[j], m.rows);
             dweight[p.token * m.topk + j] = r >= 0 ? row_weight[r] : 0.0f;
         }
-    const Span<T> src = span_of(y, m.rows * m.cols);
-    for (int64_t k = p.first - phase_of<T, FAST>(out, p.token, m.cols); k < m.cols; k += p.step) {
-        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int j0 = 0; j0 < m.topk; j0 += G) {
-            int r[G];
-            float w[G];
+    const auto choice = [&](int j, int& r, float& w) {
+        r = j < m.topk ? row_or_none(rows[j], m.rows) : -1;
+        w = weight && r >= 0 ? weight[p.token * m.topk + j] : 1.0f;
+    };
+    if constexpr (FAST) {
+        constexpr int V = G <= 2 ? 2 : 1;  // chunks at once
+        const int64_t step = (int64_t)p.count * 8;
+        for (int64_t k = (int64_t)p.index * 8; k < m.cols; k += V * step) {
+            float acc[V][8] = {};
+            for (int j0 = 0; j0 < m.topk; j0 += G) {
+                int r[G];
+                float w[G];
 #pragma unroll
-            for (int i = 0; i < G; ++i) {
-                r[i] = j0 + i < m.topk ? row_or_none(rows[j0 + i], m.rows) : -1;
-                w[i] = weight && r[i] >= 0 ? weight[p.token * m.topk + j0 + i] : 1.0f;
-            }
-            if constexpr (FAST) {
-                Raw8<T> raw[G];
+                for (int i = 0; i < G; ++i)
+                    choice(j0 + i, r[i], w[i]);
+                Raw8<T> raw[G][V];
                 if (m.rows > 0) {
 #pragma unroll
                     for (int i = 0; i < G; ++i)
-                        ld8(y + (r[i] < 0 ? 0 : r[i]) * m.cols + k, raw[i]);
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+                            ld8(y + (r[i] < 0 ? 0 : r[i]) * m.cols + (k + v * step < m.cols ? k + v * step : k), raw[i][v]);
                 }
 #pragma unroll
                 for (int i = 0; i < G; ++i) {
                     if (r[i] < 0)
                         continue;
-                    float f[8];
-                    widen8(raw[i], f);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        acc[c] = fmaf(w[i], f[c], acc[c]);
-                }
-            } else {
+                    for (int v = 0; v < V; ++v) {
+                        float f[8];
+                        widen8(raw[i][v], f);
 #pragma unroll
-                for (int i = 0; i < G; ++i) {
-                    if (r[i] < 0)
-                        continue;
-                    float f[8];
-                    load_cols<T, FAST>(src, r[i], k, m.cols, f);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        acc[c] = fmaf(w[i], f[c], acc[c]);
+                        for (int c = 0; c < 8; ++c)
+                            acc[v][c] = fmaf(w[i], f[c], acc[v][c]);
+                    }
                 }
             }
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v == 0 || k + v * step < m.cols)
+                    store_cols<T, FAST>(out, p.token, k + v * step, m.cols, acc[v]);
         }
-        store_cols<T, FAST>(out, p.token, k, m.cols, acc);
+    } else {
+        const Span<T> all = span_of(y, m.rows * m.cols);
+        const int64_t step = (int64_t)p.count * 8;
+        for (int64_t k = (int64_t)p.index * 8 - phase_of<T, FAST>(out, p.token, m.cols); k < m.cols; k += step) {
+            float acc[8] = {};
+#pragma unroll 4
+            for (int j = 0; j < m.topk; ++j) {
+                int r;
+                float w, f[8];
+                choice(j, r, w);
+                if (r < 0)
+                    continue;
+                load_cols<T, FAST>(all, r, k, m.cols, f);
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    acc[c] = fmaf(w, f[c], acc[c]);
+            }
+            store_cols<T, FAST>(out, p.token, k, m.cols, acc);
+        }
     }
 }
 
@@ -472,7 +501,7 @@ moe_unpermute_bwd(const T* __restrict__ g, const T* __restrict__ y, const int32_
     Place p;
     const bool live = place(m, p);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = m.team >> 5;
-    const Span<T> gs = span_of(g, m.tokens * m.cols), ys = span_of(y, m.rows * m.cols);
+    const T* gs = g + p.token * m.cols;
     for (int j0 = 0; j0 < m.topk; j0 += G) {
         int r[G];
         float w[G], dot[G];
@@ -484,43 +513,57 @@ moe_unpermute_bwd(const T* __restrict__ g, const T* __restrict__ y, const int32_
             dot[i] = 0.0f;
         }
         if constexpr (FAST) {
-            for (int64_t k = p.first; live && k < m.cols; k += p.step) {
-                Raw8<T> raw[G], graw;
-                ld8(g + p.token * m.cols + k, graw);
-                if (dweight && m.rows > 0) {
+            constexpr int V = G <= 2 ? 2 : 1;  // chunks at once
+            const int64_t step = (int64_t)p.count * 8;
+            for (int64_t k0 = (int64_t)p.index * 8; live && k0 < m.cols; k0 += V * step) {
+                Raw8<T> raw[V][G], graw[V];
 #pragma unroll
-                    for (int i = 0; i < G; ++i)
-                        ld8(y + (r[i] < 0 ? 0 : r[i]) * m.cols + k, raw[i]);
+                for (int v = 0; v < V; ++v) {
+                    const int64_t k = k0 + v * step < m.cols ? k0 + v * step : k0;
+                    ld8(gs + k, graw[v]);
+                    if (dweight && m.rows > 0) {
+#pragma unroll
+                        for (int i = 0; i < G; ++i)
+                            ld8(y + (r[i] < 0 ? 0 : r[i]) * m.cols + k, raw[v][i]);
+                    }
                 }
-                float gf[8];
-                widen8(graw, gf);
 #pragma unroll
-                for (int i = 0; i < G; ++i) {
-                    if (r[i] < 0)
+                for (int v = 0; v < V; ++v) {
+                    const int64_t k = k0 + v * step;
+                    if (v > 0 && k >= m.cols)
                         continue;
-                    float f[8];
-                    if (dweight) {
-                        widen8(raw[i], f);
+                    float gf[8];
+                    widen8(graw[v], gf);
+#pragma unroll
+                    for (int i = 0; i < G; ++i) {
+                        if (r[i] < 0)
+                            continue;
+                        float f[8];
+                        if (dweight) {
+                            widen8(raw[v][i], f);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                dot[i] = fmaf(gf[c], f[c], dot[i]);
+                        }
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
-                            dot[i] = fmaf(gf[c], f[c], dot[i]);
+                            f[c] = gf[c] * w[i];
+                        store_cols<T, FAST>(dy, r[i], k, m.cols, f);
                     }
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        f[c] = gf[c] * w[i];
-                    store_cols<T, FAST>(dy, r[i], k, m.cols, f);
                 }
             }
         } else {
+            const Span<T> tokens = span_of(g, m.tokens * m.cols), all = span_of(y, m.rows * m.cols);
+            const int64_t step = (int64_t)p.count * 8;
 #pragma unroll
             for (int i = 0; i < G; ++i) {
                 if (r[i] < 0)
                     continue;
-                for (int64_t k = p.first - phase_of<T, FAST>(dy, r[i], m.cols); k < m.cols; k += p.step) {
+                for (int64_t k = (int64_t)p.index * 8 - phase_of<T, FAST>(dy, r[i], m.cols); k < m.cols; k += step) {
                     float gf[8], f[8];
-                    load_cols<T, FAST>(gs, p.token, k, m.cols, gf);
+                    load_cols<T, FAST>(tokens, p.token, k, m.cols, gf);
                     if (dweight) {
-                        load_cols<T, FAST>(ys, r[i], k, m.cols, f);
+                        load_cols<T, FAST>(all, r[i], k, m.cols, f);
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
                             dot[i] = fmaf(gf[c], f[c], dot[i]);
@@ -692,6 +735,28 @@ extern "C" int mfx_moe_sort(int64_t tokens, int64_t topk, int64_t experts, int64
     return e == cudaSuccess ? launch_status() : cuda_failure(e);
 }
 
+namespace mfx {
+namespace {
+int permute(int dt, int64_t tokens, int64_t topk, int64_t cols, int64_t rows, const void* x, const int32_t* row_of,
+            const int32_t* slot_of, const float* weight, void* out, float* out_weight, void* stream)
+{
+    const Moe m = plan(topk > 0 ? tokens : 0, topk, cols, rows, true);
+    const int64_t blocks = m.token_blocks + (rows + kPadRows - 1) / kPadRows;
+    if (blocks > INT32_MAX)
+        return MFX_ERR_SHAPE;
+    const auto go = [&](auto t, auto fast) {
+        using T = decltype(t);
+        moe_permute<T, decltype(fast)::value><<<(unsigned)blocks, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+            static_cast<const T*>(x), row_of, slot_of, weight, static_cast<T*>(out), out_weight, m);
+        return launch_status();
+    };
+    if (fast_rows(cols, x, out))
+        return dt == MFX_BF16 ? go(bf16{}, std::true_type{}) : go(float{}, std::true_type{});
+    return dt == MFX_BF16 ? go(bf16{}, std::false_type{}) : go(float{}, std::false_type{});
+}
+}  // namespace
+}  // namespace mfx
+
 extern "C" int mfx_moe_permute_fwd(int dt, int64_t tokens, int64_t topk, int64_t cols, int64_t rows, const void* x,
                                    const int32_t* row_of, const int32_t* slot_of, const float* weight, void* out,
                                    float* out_weight, void* stream)
@@ -708,19 +773,7 @@ extern "C" int mfx_moe_permute_fwd(int dt, int64_t tokens, int64_t topk, int64_t
         overlaps(out_weight, 4 * rows, x, xb) || overlaps(out_weight, 4 * rows, weight, 4 * slots) ||
         overlaps(out_weight, 4 * rows, row_of, 4 * slots) || overlaps(out_weight, 4 * rows, slot_of, 4 * rows))
         return MFX_ERR_ALIAS;
-    Moe m = plan(topk > 0 ? tokens : 0, topk, cols, rows, true);
-    const int64_t blocks = m.token_blocks + (rows + kPadRows - 1) / kPadRows;
-    if (blocks > INT32_MAX)
-        return MFX_ERR_SHAPE;
-    const auto go = [&](auto t, auto fast) {
-        using T = decltype(t);
-        moe_permute<T, decltype(fast)::value><<<(unsigned)blocks, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-            static_cast<const T*>(x), row_of, slot_of, weight, static_cast<T*>(out), out_weight, m);
-        return launch_status();
-    };
-    if (fast_rows(cols, x, out))
-        return dt == MFX_BF16 ? go(bf16{}, std::true_type{}) : go(float{}, std::true_type{});
-    return dt == MFX_BF16 ? go(bf16{}, std::false_type{}) : go(float{}, std::false_type{});
+    return permute(dt, tokens, topk, cols, rows, x, row_of, slot_of, weight, out, out_weight, stream);
 }
 
 namespace mfx {
@@ -793,6 +846,8 @@ extern "C" int mfx_moe_unpermute_bwd(int dt, int64_t tokens, int64_t topk, int64
             return MFX_ERR_ALIAS;
     if (overlaps(dy, yb, dweight, 4 * slots))
         return MFX_ERR_ALIAS;
+    if (!weight && !dweight)  // the rows of g as they are
+        return permute(dt, tokens, topk, cols, rows, g, row_of, slot_of, nullptr, dy, nullptr, stream);
     const Moe m = plan(topk > 0 ? tokens : 0, topk, cols, rows, false);
     const int64_t blocks = m.token_blocks + (rows + kPadRows - 1) / kPadRows;
     if (blocks > INT32_MAX)
