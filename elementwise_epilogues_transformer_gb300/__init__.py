@@ -424,14 +424,14 @@ def mfx_relbias_softmax_dropout_fwd(x, scale, table=None, mask=None, max_distanc
     """y = dropout(softmax(x * scale + table[bucket(k - pos)] + mask), p) over
     the last dim of x [b, np, sq, sk]; table: [num_buckets, np] (x's dtype or
     float32); pos = q_start + seq_start[b] + q.  Returns (y, stats); stats
-    [b, np, sq, 2] is what the backward needs (None with need_stats=False)."""
+    [b, np, sq, 3] is what the backward needs (None with need_stats=False)."""
     shape, shared = _relbias_args(x, table, mask, max_distance, bidirectional, causal, q_start, seq_start, p, seed,
                                   offset, elem_base)
     y = torch.empty_like(x) if y is None else _like(y, "y", shape, x.dtype)
     if stats is not None:
-        _like(stats, "stats", (*shape[:3], 2), torch.float32)
+        _like(stats, "stats", (*shape[:3], 3), torch.float32)
     elif need_stats:
-        stats = torch.empty((*shape[:3], 2), dtype=torch.float32, device=x.device)
+        stats = torch.empty((*shape[:3], 3), dtype=torch.float32, device=x.device)
     _call("mfx_relbias_softmax_dropout_fwd", dtype_code(x.dtype), *shape, x.data_ptr(), scale, *shared, y.data_ptr(),
           _ptr(stats), _stream(stream, x))
     return y, stats
@@ -445,7 +445,7 @@ def mfx_relbias_softmax_dropout_bwd(dy, x, stats, scale, table=None, mask=None, 
     shape, shared = _relbias_args(x, table, mask, max_distance, bidirectional, causal, q_start, seq_start, p, seed,
                                   offset, elem_base)
     _like(dy, "dy", shape, x.dtype)
-    _like(stats, "stats", (*shape[:3], 2), torch.float32)
+    _like(stats, "stats", (*shape[:3], 3), torch.float32)
     dx = torch.empty_like(x) if dx is None else _like(dx, "dx", shape, x.dtype)
     if dtable is not None:
         if table is None:

@@ -46,10 +46,10 @@ struct Geom {
     int phase0;                // (phase0 + element index) mod 8 = 0 at a chunk's start
     float scale, scale2;       // the score scale; the same times log2 e
     float keep_scale;          // 1 / (1 - p)
-    // backward: exponents get log2(keep_scale * fold), fold being the score
-    // scale where that is a positive normal number (1 else); dot = the factor
-    // that makes D of the sum, unfold = 1 / fold, post = scale / fold
-    float grad_log2, dot, unfold, post;
+    // backward: a row's gradient is formed times fold, the score scale where
+    // that is a normal number (1 else); grad = keep_scale * fold, unfold =
+    // 1 / fold, post = scale / fold
+    float grad, unfold, post;
     uint32_t thresh_hi;        // keep threshold in the upper half-word
     uint64_t elem_base;
     MaskGen gen;
@@ -350,14 +350,14 @@ __device__ __forceinline__ void stage_row(uint4* stage, const bf16* src, const R
 __device__ __forceinline__ void unstage(const uint4* stage, int c, Raw8<bf16>& raw) { raw.v = stage[c * blockDim.x]; }
 __device__ __forceinline__ void restage(uint4* stage, int c, const Raw8<bf16>& raw) { stage[c * blockDim.x] = raw.v; }
 
-// Scores of the chunk at k0 from its raw x, times log2 e, plus `add`: x * scale
-// + (bias + add) (+ mask - shift).  A key whose mask is -inf is left out whatever x holds there.
+// Scores of the chunk at k0 from its raw x, times log2 e: x * scale + bias
+// (+ mask - shift).  A key whose mask is -inf is left out whatever x holds there.
 // Call with whole warps: one with a near chunk reads the window in all lanes,
-// far ones at its ends.  far_lo and far_hi have `add` in them already.
+// far ones at its ends.
 template <typename T, bool FAST, bool MASK>
 __device__ __forceinline__ void score_chunk(const Raw8<T>& raw, const Row<T>& row, const Geom& g, const Buckets& w,
                                             const float4* win, float far_lo, float far_hi, int k0, float shift,
-                                            float add, float2 (&s)[4])
+                                            float2 (&s)[4])
 {
     pairs_of(raw, s);
     const int rel = k0 - row.pos;
@@ -369,10 +369,10 @@ __device__ __forceinline__ void score_chunk(const Raw8<T>& raw, const Row<T>& ro
     } else {
         const int stride = window_stride(w), i0 = min(max(rel + w.reach, -8), w.reach + w.hi + 1);
         const float4 lo = win[window_slot(stride, i0)], hi = win[window_slot(stride, i0 + 4)];
-        s[0] = pfma(s[0], f2(g.scale2), make_float2(lo.x + add, lo.y + add));
-        s[1] = pfma(s[1], f2(g.scale2), make_float2(lo.z + add, lo.w + add));
-        s[2] = pfma(s[2], f2(g.scale2), make_float2(hi.x + add, hi.y + add));
-        s[3] = pfma(s[3], f2(g.scale2), make_float2(hi.z + add, hi.w + add));
+        s[0] = pfma(s[0], f2(g.scale2), make_float2(lo.x, lo.y));
+        s[1] = pfma(s[1], f2(g.scale2), make_float2(lo.z, lo.w));
+        s[2] = pfma(s[2], f2(g.scale2), make_float2(hi.x, hi.y));
+        s[3] = pfma(s[3], f2(g.scale2), make_float2(hi.z, hi.w));
     }
     if (MASK && row.mask) {
         Raw8<T> mraw;
@@ -606,10 +606,8 @@ inline Geom make_geom(const Args& a, const Buckets& w, const void* x)
                           : (int)((reinterpret_cast<uintptr_t>(x) / (size_t)dtype_bytes(a.dt)) & 7);
     g.scale = a.scale, g.scale2 = (float)((double)a.scale * 1.4426950408889634);
     g.keep_scale = 1.0f / (1.0f - a.p);
-    const double fold = a.scale >= 1e-30f && a.scale <= 1e30f ? a.scale : 1.0;
-    g.grad_log2 = (float)std::log2((double)g.keep_scale * fold);
-    g.dot = (float)(1.0 / ((double)g.keep_scale * fold)), g.unfold = (float)(1.0 / fold);
-    g.post = fold == 1.0 ? a.scale : 1.0f;
+    const float size = std::fabs(a.scale), fold = size >= 1e-30f && size <= 1e30f ? a.scale : 1.0f;
+    g.grad = g.keep_scale * fold, g.unfold = 1.0f / fold, g.post = fold == a.scale ? 1.0f : a.scale;
     const double t = std::ceil((double)a.p * 65536.0);
     g.thresh_hi = (uint32_t)(t > 65535.0 ? 65535.0 : t) << 16;
     g.elem_base = a.elem_base;

@@ -2,12 +2,11 @@
 // dropout (relbias_fwd.cu has the operation).
 //
 // P and the keep flags are formed again from x, the row statistics and the
-// generator.  With Q = scale * P / (1 - p), formed by adding the logarithm of
-// the factor to the exponent, and z = keep * dy,
-//   D = (1 - p) / scale * sum Q z,   dx = Q (z - D),
-// so neither factor costs anything per element; the table's sums are divided
-// by scale at a block's end.  (A scale that is not a positive normal number
-// stays out of Q and is multiplied in.)
+// generator.  With Q = 2^(score - maximum), so that P = Q / sum Q, and z =
+// keep * dy,
+//   D = sum Q z / sum Q,   dx = Q (z - D) * scale / ((1 - p) sum Q),
+// one factor a row; the table's sums are divided by scale at a block's end.
+// (A scale that is not a normal number stays out of them and is multiplied in.)
 //
 // The table's gradient takes the form of the bias: far positions add into two
 // registers a thread, near ones into a window in shared memory.  A row's
@@ -88,12 +87,9 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
     }
     for (int64_t first = slice * g.teams; first < g.rows; first += step, row += step, o = ahead, slot ^= 1) {
         uint4* sz = stage_dy + slot * C * blockDim.x;
-        float shift = 0.0f, lse = 0.0f;
-        if (row < g.rows) {
-            shift = stats[2 * o.r], lse = stats[2 * o.r + 1];
-            lse = lse == -INFINITY ? 0.0f : lse;  // an empty row: every score is -inf
-        }
-        const float ref = g.grad_log2 - lse, lo = far_lo + ref, hi = far_hi + ref;
+        float shift = 0.0f, top = 0.0f, inv = 0.0f;
+        if (row < g.rows)
+            shift = stats[3 * o.r], top = stats[3 * o.r + 1], inv = stats[3 * o.r + 2];
         const auto run = [&](auto check) {
             constexpr bool CHECK = decltype(check)::value;
             float2 Q[C][4], D2 = f2(0.0f);
@@ -138,13 +134,13 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
                         unstage(stage, c, rx[c]);
                         unstage(sz, c, zc);
                     }
-                    score_chunk<T, FAST, MASK>(rx[c], o, g, w, win, lo, hi, k0, shift, ref, Q[c]);
+                    score_chunk<T, FAST, MASK>(rx[c], o, g, w, win, far_lo, far_hi, k0, shift, Q[c]);
                     if (CHECK)
                         MFX_RARELY((!FAST && k0 < 0) || k0 + 8 > o.end)
                             fill_outside(Q[c], k0, o.end, -INFINITY);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        Q[c][i] = make_float2(exp2_of(Q[c][i].x), exp2_of(Q[c][i].y));
+                        Q[c][i] = make_float2(exp2_of(Q[c][i].x - top), exp2_of(Q[c][i].y - top));
                     if (DROP && (!STAGED || CHECK) && g.drop)
                         drop_raw(zc, one_block(g.gen, o.block0 + ch), g.thresh_hi);
                     float2 f[4];
@@ -188,7 +184,8 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
             } else {
                 __syncwarp();  // the previous row's window sums before this row's
             }
-            D *= g.dot;
+            D *= inv;
+            const float factor = g.grad * inv;
             for (int blk = 0; blk < blocks; ++blk) {
                 if (LONG && blocks > 1)
                     first_half(blk);
@@ -202,7 +199,7 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
                         pairs_of(z[STAGED ? 0 : c], v);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            v[i] = pmul(Q[c][i], padd(v[i], f2(-D)));
+                            v[i] = pmul(pmul(Q[c][i], padd(v[i], f2(-D))), f2(factor));
                         if (CHECK)
                             MFX_RARELY((!FAST && k0 < 0) || k0 + 8 > o.end)
                                 fill_outside(v, k0, o.end, 0.0f);
@@ -413,7 +410,7 @@ extern "C" int mfx_relbias_softmax_dropout_bwd(int dt, int64_t b, int64_t np, in
     if (!query) {
         if (!dy || !x || !stats || !dx || (dtable && (!table || !workspace || !workspace_bytes)))
             return MFX_ERR_NULL;
-        const int64_t bytes = a.n * dtype_bytes(dt), sb = b * np * sq * 8, tb = a.table_bytes;
+        const int64_t bytes = a.n * dtype_bytes(dt), sb = b * np * sq * 12, tb = a.table_bytes;
         if (partial_overlap(dy, bytes, dx, bytes) || partial_overlap(x, bytes, dx, bytes) ||
             overlaps(mask, a.mask_bytes, dx, bytes) || overlaps(table, tb, dx, bytes) ||
             overlaps(stats, sb, dx, bytes) || overlaps(seq_start, 4 * b, dx, bytes))

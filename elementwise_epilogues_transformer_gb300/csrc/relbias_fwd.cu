@@ -67,6 +67,15 @@ __device__ __forceinline__ float2 join_team(const Team& tm, float2 v, int slot)
     return v;
 }
 
+// What the backward needs of a row: the mask's shift, the maximum that its
+// exponents are taken from (base-2 units) and one over the sum of their
+// powers.  (Kept apart, and not as one logarithm, they form P as exactly as
+// the forward does: one where a row has a single key.)
+__device__ __forceinline__ void put_stats(float* stats, int64_t row, float shift, float top, float inv)
+{
+    stats[3 * row] = shift, stats[3 * row + 1] = top, stats[3 * row + 2] = inv;
+}
+
 // One row whose scores all lie far from zero (a mask of lowest values, say),
 // or that has no key left: the mask is shifted by its own maximum, which
 // leaves the softmax as it is and the scores their digits.  Element by
@@ -98,11 +107,9 @@ __device__ __noinline__ void shifted_row(const T* x, T* y, float* stats, const R
     for (int k = first; k < o.end; k += step)
         l += exp2_of(score(k) - ref);
     l = join_team<LONG>(tm, make_float2(ref, lanes_sum<true>(l, tm.lanes)), slot ^ 1).y;
-    if (stats && first == 0 && o.chunks) {
-        stats[2 * o.r] = shift;
-        stats[2 * o.r + 1] = m == -INFINITY ? m : m + log2f(l);
-    }
     const float inv = m == -INFINITY && l == 0.0f ? 0.0f : 1.0f / l;
+    if (stats && first == 0 && o.chunks)
+        put_stats(stats, o.r, shift, ref, inv);
     for (int k = first; o.chunks && k < g.sk; k += step) {
         float v = k < o.end ? exp2_of(score(k) - ref) * inv : 0.0f;
         if (DROP && g.drop && k < o.end)
@@ -165,7 +172,7 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
                 for (int c = 0; c < C; ++c) {
                     const int k0 = (c0 + c * g.team) * 8 - o.a;
                     if (some_part<CHECK>(k0, o.end)) {
-                        score_chunk<T, FAST, MASK>(raw[c], o, g, w, win, far_lo, far_hi, k0, 0.0f, 0.0f, s[c]);
+                        score_chunk<T, FAST, MASK>(raw[c], o, g, w, win, far_lo, far_hi, k0, 0.0f, s[c]);
                         if (CHECK)
                             MFX_RARELY((!FAST && k0 < 0) || k0 + 8 > o.end)
                                 fill_outside(s[c], k0, o.end, -INFINITY);
@@ -202,12 +209,11 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
                     return;
                 }
             }
-            if (stats && tid == 0 && rank == 0 && row < g.rows) {
-                stats[2 * o.r] = 0.0f;
-                stats[2 * o.r + 1] = m == -INFINITY ? m : m + log2f(l);
-            }
-            const float inv =
-                m == -INFINITY && l == 0.0f ? 0.0f : __fdividef(DROP && g.drop ? g.keep_scale : 1.0f, l);
+            float inv = m == -INFINITY && l == 0.0f ? 0.0f : 1.0f / l;
+            if (stats && tid == 0 && rank == 0 && row < g.rows)
+                put_stats(stats, o.r, 0.0f, m == -INFINITY ? 0.0f : m, inv);
+            if (DROP)
+                inv *= g.keep_scale;
             const float f1 = mw == -INFINITY && l == l ? 0.0f : exp2_of(mw - m) * inv;
             for (int blk = 0; blk < blocks; ++blk) {
                 const int c0 = (blk * cluster + rank) * (C * g.team) + tid;
@@ -224,7 +230,7 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
                         if (LONG && blocks > 1) {
                             Raw8<T> raw;
                             load_chunk<T, FAST>(xr + 8 * (FAST && k0 >= o.end ? 0 : ch), k0, o.end, raw);
-                            score_chunk<T, FAST, MASK>(raw, o, g, w, win, far_lo, far_hi, k0, 0.0f, 0.0f, s[c]);
+                            score_chunk<T, FAST, MASK>(raw, o, g, w, win, far_lo, far_hi, k0, 0.0f, s[c]);
                             const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
@@ -356,7 +362,7 @@ extern "C" int mfx_relbias_softmax_dropout_fwd(int dt, int64_t b, int64_t np, in
         return st;
     if (!x || !y)
         return MFX_ERR_NULL;
-    const int64_t bytes = a.n * dtype_bytes(dt), sb = b * np * sq * 8;
+    const int64_t bytes = a.n * dtype_bytes(dt), sb = b * np * sq * 12;
     if (partial_overlap(x, bytes, y, bytes) || overlaps(mask, a.mask_bytes, y, bytes) ||
         overlaps(table, a.table_bytes, y, bytes) || overlaps(seq_start, 4 * b, y, bytes) ||
         overlaps(stats, sb, y, bytes) || overlaps(stats, sb, x, bytes) || overlaps(stats, sb, mask, a.mask_bytes) ||

@@ -229,8 +229,9 @@ int mfx_scaled_upper_triang_masked_softmax_bwd(int dt, int64_t attn_batches, int
  * Dropout: element (r, k), r = (i * np + h) * sq + q, has the index e =
  * elem_base + r * sk + k, and keep as in mfx_bias_dropout_add_train (same
  * generator, words and threshold); p = 0 keeps everything.
- * stats: [b, np, sq, 2] fp32, what the backward needs of each row (the shift
- * of its mask and the base-2 log of its sum of exponentials), or NULL (inference).
+ * stats: [b, np, sq, 3] fp32, what the backward needs of each row (the shift
+ * of its mask, the maximum of its scores in base-2 units and one over the sum
+ * of its exponentials), or NULL (inference).
  * y: x's shape and dtype; y may equal x (in place, when no backward follows).
  * b, np, sq, sk and |q_start| at most 2^29.  One query per sequence over a long key axis
  * (decoding) splits a row over several thread blocks. */

@@ -306,3 +306,30 @@ def test_graph_capture():
     g.replay()
     for a, b in zip((y, stats, dx, dt), want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("p", [0.0, 0.1])
+@pytest.mark.parametrize("scale", [0.125, 0.0884, -0.3, 0.0])
+def test_one_key_has_no_gradient(scale, p, dtype):
+    """Where one key takes part (by length, position or mask) P is exactly one
+    and the gradient exactly zero, as the difference says."""
+    for sk, mask, causal in ((1, None, False), (9, "one", False), (300, "one", False), (40, None, True)):
+        x, dy, table, _ = inputs(2, 3, 1 if causal else 6, sk, dtype, seed=sk)
+        m = None
+        if mask:
+            m = torch.full((2, 1, 6, sk), -math.inf, device=DEV, dtype=dtype)
+            m[..., sk // 2] = 0
+            m[:, :, 3] = torch.finfo(dtype).min  # next to the lowest value, -inf
+            m[:, :, 3, :sk // 2] = m[:, :, 3, sk // 2 + 1:] = -math.inf
+        y, _, dx, dt = run_both(x, dy, scale, table=table, mask=m, causal=causal, bidirectional=not causal, p=p, seed=7)
+        if p == 0:
+            assert ((y == 0) | (y == 1)).all()
+        assert not dx.any() and not dt.any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-35, 1.0])
+def test_scales(scale, dtype):
+    x, dy, table, m = inputs(2, 2, 7, 130, dtype, seed=21, mask="pad")
+    check(x, dy, scale, table=table, mask=m, p=0.1, seed=8)
