@@ -250,7 +250,7 @@ struct Row {
     int64_t r;        // row index of the tensor
     int64_t e0;       // element index of chunk 0 in the tensor
     uint64_t block0;  // generator block of chunk 0
-    const T* mask;    // its mask row, or null
+    const T* mask;    // its mask row, where there is a mask
     int a, pos, end;  // chunk phase, clamped query position, keys that take part: [0, end)
     int chunks;       // chunks of the row
 };
@@ -285,12 +285,12 @@ __device__ __forceinline__ Row<T> row_at(const Geom& g, const Buckets& w, const 
                                          bool live)
 {
     Row<T> o;
-    o.r = at.r;
+    o.r = live ? at.r : 0;  // chunks past a row's end are read at its start: of a row that exists
     const int64_t e = o.r * (int64_t)g.sk;
     o.a = FAST ? 0 : (int)((uint64_t)(g.phase0 + e) & 7u);
     o.e0 = e - o.a;
     o.block0 = (g.elem_base + (uint64_t)e) >> 3;
-    o.mask = nullptr;
+    o.mask = mask;  // no row, no keys: nothing of it is looked at
     o.pos = o.end = o.chunks = 0;
     if (!live)
         return o;
@@ -350,15 +350,55 @@ __device__ __forceinline__ void stage_row(uint4* stage, const bf16* src, const R
 __device__ __forceinline__ void unstage(const uint4* stage, int c, Raw8<bf16>& raw) { raw.v = stage[c * blockDim.x]; }
 __device__ __forceinline__ void restage(uint4* stage, int c, const Raw8<bf16>& raw) { stage[c * blockDim.x] = raw.v; }
 
+// A mask's chunk, kept in L1: rows share it where the mask is broadcast.
+__device__ __forceinline__ void ld8_cached(const bf16* p, Raw8<bf16>& r) { r.v = ld16_ca(p); }
+__device__ __forceinline__ void ld8_cached(const float* p, Raw8<float>& r) { r.v[0] = ld16_ca(p), r.v[1] = ld16_ca(p + 4); }
+template <typename T, bool FAST>
+__device__ __forceinline__ void load_mask(const T* p, int k0, int end, Raw8<T>& raw)
+{
+    if (FAST)
+        ld8_cached(p, raw);
+    else
+        load_chunk<T, FAST>(p, k0, end, raw);
+}
+
+// Whether a chunk of the mask is all zero (adds nothing) or all -inf (leaves
+// nothing).
+__device__ __forceinline__ bool all_zero(const Raw8<bf16>& r) { return (r.v.x | r.v.y | r.v.z | r.v.w) == 0u; }
+__device__ __forceinline__ bool all_out(const Raw8<bf16>& r)
+{
+    constexpr uint32_t k = 0xFF80FF80u;
+    return ((r.v.x ^ k) | (r.v.y ^ k) | (r.v.z ^ k) | (r.v.w ^ k)) == 0u;
+}
+__device__ __forceinline__ bool all_zero(const Raw8<float>& r)
+{
+    return (r.v[0].x | r.v[0].y | r.v[0].z | r.v[0].w | r.v[1].x | r.v[1].y | r.v[1].z | r.v[1].w) == 0u;
+}
+__device__ __forceinline__ bool all_out(const Raw8<float>& r)
+{
+    constexpr uint32_t k = 0xFF800000u;
+    return ((r.v[0].x ^ k) | (r.v[0].y ^ k) | (r.v[0].z ^ k) | (r.v[0].w ^ k) | (r.v[1].x ^ k) | (r.v[1].y ^ k) |
+            (r.v[1].z ^ k) | (r.v[1].w ^ k)) == 0u;
+}
+
 // Scores of the chunk at k0 from its raw x, times log2 e: x * scale + bias
 // (+ mask - shift).  A key whose mask is -inf is left out whatever x holds there.
 // Call with whole warps: one with a near chunk reads the window in all lanes,
-// far ones at its ends.
+// far ones at its ends, and a mask that is zero in all of them is not added.
+// False, with nothing computed, where the mask leaves the warp no key at all.
 template <typename T, bool FAST, bool MASK>
-__device__ __forceinline__ void score_chunk(const Raw8<T>& raw, const Row<T>& row, const Geom& g, const Buckets& w,
-                                            const float4* win, float far_lo, float far_hi, int k0, float shift,
-                                            float2 (&s)[4])
+__device__ __forceinline__ bool score_chunk(const Raw8<T>& raw, const Row<T>& row, const Geom& g, const Buckets& w,
+                                            const float4* win, float far_lo, float far_hi, int k0, bool masked,
+                                            float shift, float2 (&s)[4])
 {
+    Raw8<T> mraw;
+    bool add = false;
+    if (MASK && masked) {  // the same for every lane, as the votes have to be
+        load_mask<T, FAST>(row.mask + (FAST && k0 >= row.end ? 0 : k0), k0, row.end, mraw);
+        add = __any_sync(0xFFFFFFFFu, !all_zero(mraw) || shift != 0.0f);
+        if (add && __all_sync(0xFFFFFFFFu, all_out(mraw)))
+            return false;
+    }
     pairs_of(raw, s);
     const int rel = k0 - row.pos;
     if (!__any_sync(0xFFFFFFFFu, near_chunk(w, rel))) {
@@ -374,9 +414,7 @@ __device__ __forceinline__ void score_chunk(const Raw8<T>& raw, const Row<T>& ro
         s[2] = pfma(s[2], f2(g.scale2), make_float2(hi.x, hi.y));
         s[3] = pfma(s[3], f2(g.scale2), make_float2(hi.z, hi.w));
     }
-    if (MASK && row.mask) {
-        Raw8<T> mraw;
-        load_chunk<T, FAST>(row.mask + (FAST && k0 >= row.end ? 0 : k0), k0, row.end, mraw);
+    if (MASK && add) {
         float2 m[4];
         pairs_of(mraw, m);
 #pragma unroll
@@ -385,6 +423,7 @@ __device__ __forceinline__ void score_chunk(const Raw8<T>& raw, const Row<T>& ro
             s[i].y = m[i].y == -INFINITY ? -INFINITY : fmaf(m[i].y - shift, kLog2eF, s[i].y);
         }
     }
+    return true;
 }
 
 // Which of a thread's chunks, in a row that may end inside them, the warp

@@ -91,8 +91,9 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
         if (row < g.rows)
             shift = stats[3 * o.r], top = stats[3 * o.r + 1], inv = stats[3 * o.r + 2];
         const auto run = [&](auto check) {
-            constexpr bool CHECK = decltype(check)::value;
+            constexpr bool CHECK = decltype(check)::value, PART = CHECK || MASK;
             float2 Q[C][4], D2 = f2(0.0f);
+            unsigned has_keys = ~0u;  // chunks of which the warp has a key that takes part
             Raw8<T> z[STAGED ? 1 : C];
             // P and z of the row's (or block's) chunks, and their part of D
             const auto first_half = [&](int blk) {
@@ -124,6 +125,8 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
                         load_chunk<T, FAST>(dy + o.e0 + k, k0, o.end, z[c]);
                     }
                 }
+                if (PART)
+                    has_keys = 0;
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     const int ch = (blk * C + c) * g.team + tid, k0 = ch * 8 - o.a;
@@ -134,7 +137,10 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
                         unstage(stage, c, rx[c]);
                         unstage(sz, c, zc);
                     }
-                    score_chunk<T, FAST, MASK>(rx[c], o, g, w, win, far_lo, far_hi, k0, shift, Q[c]);
+                    if (!score_chunk<T, FAST, MASK>(rx[c], o, g, w, win, far_lo, far_hi, k0, mask != nullptr, shift, Q[c]))
+                        continue;
+                    if (PART)
+                        has_keys |= 1u << c;
                     if (CHECK)
                         MFX_RARELY((!FAST && k0 < 0) || k0 + 8 > o.end)
                             fill_outside(Q[c], k0, o.end, -INFINITY);
@@ -193,7 +199,7 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
                 for (int c = 0; c < C; ++c) {
                     const int ch = (blk * C + c) * g.team + tid, k0 = ch * 8 - o.a;
                     float2 v[4];
-                    if (some_part<CHECK>(k0, o.end)) {
+                    if (!PART || (has_keys >> c & 1u)) {
                         if constexpr (STAGED)
                             unstage(sz, c, z[0]);
                         pairs_of(z[STAGED ? 0 : c], v);

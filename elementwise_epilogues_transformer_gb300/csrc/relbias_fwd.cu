@@ -125,7 +125,7 @@ __device__ __noinline__ void shifted_row(const T* x, T* y, float* stats, const R
 }
 
 template <typename T, int C, bool DROP, bool MASK, bool FAST, int MT>
-__global__ void __launch_bounds__(MT, MT > kTeam ? 1 : sizeof(T) == 2 && C < 8 ? 3 : 2)
+__global__ void __launch_bounds__(MT, MT > kTeam ? 1 : sizeof(T) == 2 && C < (MASK ? 4 : 8) ? 3 : 2)
 relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ mask, const void* __restrict__ table,
             const __grid_constant__ Geom g, const __grid_constant__ Buckets w)
 {
@@ -156,8 +156,9 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
         T* yr = y + o.e0;
         // CHECK: some chunk of the row is not there, or not all of it takes part
         const auto run = [&](auto check) {
-            constexpr bool CHECK = decltype(check)::value;
+            constexpr bool CHECK = decltype(check)::value, PART = CHECK || MASK;
             float2 s[C][4];
+            unsigned has_keys = ~0u;  // chunks of which the warp has a key that takes part
             float m = -INFINITY, l = 0.0f;
             for (int blk = 0; blk < blocks; ++blk) {
                 const int c0 = (blk * cluster + rank) * (C * g.team) + tid;
@@ -168,11 +169,16 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
                     load_chunk<T, FAST>(xr + 8 * (CHECK && FAST && k0 >= o.end ? 0 : ch), k0, o.end, raw[c]);
                 }
                 float t = -INFINITY;
+                if (PART)
+                    has_keys = 0;
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     const int k0 = (c0 + c * g.team) * 8 - o.a;
-                    if (some_part<CHECK>(k0, o.end)) {
-                        score_chunk<T, FAST, MASK>(raw[c], o, g, w, win, far_lo, far_hi, k0, 0.0f, s[c]);
+                    const bool has = some_part<CHECK>(k0, o.end) &&
+                                     score_chunk<T, FAST, MASK>(raw[c], o, g, w, win, far_lo, far_hi, k0, mask != nullptr, 0.0f, s[c]);
+                    if (has) {
+                        if (PART)
+                            has_keys |= 1u << c;
                         if (CHECK)
                             MFX_RARELY((!FAST && k0 < 0) || k0 + 8 > o.end)
                                 fill_outside(s[c], k0, o.end, -INFINITY);
@@ -225,12 +231,18 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
                     if (DROP && !CHECK && c % PAIR == 0)
                         mask_blocks<PAIR>(g.gen, o.block0 + ch, g.team, kb);
                     float2 p[4];
-                    if (some_part<CHECK>(k0, o.end)) {
-                        float f = f1;
-                        if (LONG && blocks > 1) {
+                    bool has = !PART || (has_keys >> c & 1u);
+                    if (LONG && blocks > 1) {
+                        has = some_part<true>(k0, o.end);
+                        if (has) {
                             Raw8<T> raw;
                             load_chunk<T, FAST>(xr + 8 * (FAST && k0 >= o.end ? 0 : ch), k0, o.end, raw);
-                            score_chunk<T, FAST, MASK>(raw, o, g, w, win, far_lo, far_hi, k0, 0.0f, s[c]);
+                            has = score_chunk<T, FAST, MASK>(raw, o, g, w, win, far_lo, far_hi, k0, mask != nullptr, 0.0f, s[c]);
+                        }
+                    }
+                    if (has) {
+                        float f = f1;
+                        if (LONG && blocks > 1) {
                             const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
