@@ -33,11 +33,13 @@ struct Buckets {
 
 struct Geom {
     int sq, sk, np;
-    int64_t rows;              // b * sq: rows of one head
+    int rows;                  // b * sq: rows of one head
     int64_t mask_b, mask_np, mask_sq;  // strides of the mask in elements (0 = broadcast)
     int q_start;
     const int32_t* seq_start;  // per batch, or null
-    int64_t slices;            // blocks (clusters) per head
+    int slices;                // blocks (clusters) per head
+    int step, step_i, step_q;  // rows, batches and queries from one row of a team to its next
+    int64_t step_r, wrap_r;    // rows of the tensor with that, and more where a batch ends
     int team, teams, cluster;  // threads per row, rows per block, blocks per row
     int blocks;                // register blocks that a row takes
     int causal, table_bf16;
@@ -244,65 +246,75 @@ __device__ __forceinline__ void store_chunk(T* p, int k0, int end, const float2 
     }
 }
 
-// What a row's chunks share.
+// A row, as little of it as says which it is (the backward keeps one ahead),
+// and what its chunks share.
 template <typename T>
-struct Row {
-    int64_t r;        // row index of the tensor
+struct Seat {
+    int64_t r;      // row index of the tensor
+    const T* mask;  // its mask row, where there is a mask
+    int pos, end;   // clamped query position; keys that take part: [0, end)
+};
+template <typename T>
+struct Row : Seat<T> {
     int64_t e0;       // element index of chunk 0 in the tensor
     uint64_t block0;  // generator block of chunk 0
-    const T* mask;    // its mask row, where there is a mask
-    int a, pos, end;  // chunk phase, clamped query position, keys that take part: [0, end)
-    int chunks;       // chunks of the row
+    int a, chunks;    // chunk phase; chunks of the row
 };
 
-// The rows that a team walks: first + n * step of the b * sq rows of head h,
-// as batch, query and row of the tensor, advanced without divisions.
+// The rows that a team walks, `row` of the b * sq of head h and every step-th
+// from it, as batch, query and row of the tensor, advanced without divisions.
 struct Walk {
-    int64_t r, step_r, wrap_r;
-    int i, q, step_i, step_q;
-    __device__ __forceinline__ Walk(const Geom& g, int h, int64_t first, int64_t step)
-        : i((int)(first / g.sq)), q((int)(first % g.sq)), step_i((int)(step / g.sq)), step_q((int)(step % g.sq))
+    int64_t r;
+    int row, i, q;
+    __device__ __forceinline__ Walk(const Geom& g, int h, int first) : row(first), i(first / g.sq), q(first % g.sq)
     {
-        wrap_r = (int64_t)(g.np - 1) * g.sq;
-        step_r = step + step_i * wrap_r;
-        r = first + i * wrap_r + (int64_t)h * g.sq;
+        r = first + i * g.wrap_r + (int64_t)h * g.sq;
     }
-    __device__ __forceinline__ void next(int sq)
+    __device__ __forceinline__ void next(const Geom& g)
     {
-        i += step_i;
-        q += step_q;
-        r += step_r;
-        if (q >= sq) {
-            q -= sq;
+        row += g.step;
+        i += g.step_i;
+        q += g.step_q;
+        r += g.step_r;
+        if (q >= g.sq) {
+            q -= g.sq;
             ++i;
-            r += wrap_r;
+            r += g.wrap_r;
         }
     }
+    __device__ __forceinline__ bool live(const Geom& g) const { return row < g.rows; }
 };
 
-template <typename T, bool FAST>
-__device__ __forceinline__ Row<T> row_at(const Geom& g, const Buckets& w, const T* mask, int h, const Walk& at,
-                                         bool live)
+// A team without a row has one without keys, whose tensor row is 0 (chunks
+// past a row's end are read at its start: of a row that exists).
+template <typename T>
+__device__ __forceinline__ Seat<T> seat_at(const Geom& g, const Buckets& w, const T* mask, int h, const Walk& at)
 {
-    Row<T> o;
-    o.r = live ? at.r : 0;  // chunks past a row's end are read at its start: of a row that exists
-    const int64_t e = o.r * (int64_t)g.sk;
-    o.a = FAST ? 0 : (int)((uint64_t)(g.phase0 + e) & 7u);
-    o.e0 = e - o.a;
-    o.block0 = (g.elem_base + (uint64_t)e) >> 3;
-    o.mask = mask;  // no row, no keys: nothing of it is looked at
-    o.pos = o.end = o.chunks = 0;
-    if (!live)
+    Seat<T> o{0, mask, 0, 0};
+    if (!at.live(g))
         return o;
+    o.r = at.r;
     o.pos = g.q_start + at.q;
     if (g.seq_start) {
         const int64_t pos = (int64_t)o.pos + g.seq_start[at.i], lo = -w.reach - 1, hi = g.sk + w.reach;
         o.pos = (int)(pos < lo ? lo : pos > hi ? hi : pos);
     }
     o.end = g.causal ? (o.pos < 0 ? 0 : o.pos + 1 < g.sk ? o.pos + 1 : g.sk) : g.sk;
-    o.chunks = (int)((g.sk + o.a + 7) >> 3);
     if (mask)
         o.mask = mask + (at.i * g.mask_b + h * g.mask_np + at.q * g.mask_sq);
+    return o;
+}
+
+template <typename T, bool FAST>
+__device__ __forceinline__ Row<T> row_of(const Geom& g, const Seat<T>& seat, bool live)
+{
+    Row<T> o;
+    static_cast<Seat<T>&>(o) = seat;
+    const int64_t e = seat.r * (int64_t)g.sk;
+    o.a = FAST ? 0 : (int)((uint64_t)(g.phase0 + e) & 7u);
+    o.e0 = e - o.a;
+    o.block0 = (g.elem_base + (uint64_t)e) >> 3;
+    o.chunks = live ? (g.sk + o.a + 7) >> 3 : 0;
     return o;
 }
 
@@ -336,13 +348,14 @@ __device__ __forceinline__ void copies_wait()
 
 // Starts the copies of a row's chunks (those that take part; the others read as zero).
 template <int C>
-__device__ __forceinline__ void stage_row(uint4* stage, const bf16* src, const Row<bf16>& o, int tid, int team)
+__device__ __forceinline__ void stage_row(uint4* stage, const bf16* src, const Seat<bf16>& o, int sk, int tid, int team)
 {
+    const bf16* row = src + o.r * (int64_t)sk;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int ch = tid + c * team;
         const bool there = ch * 8 < o.end;
-        copy16_async(stage + c * blockDim.x, src + o.e0 + (there ? 8 * ch : 0), there);
+        copy16_async(stage + c * blockDim.x, row + (there ? 8 * ch : 0), there);
     }
     copies_commit();
 }
@@ -608,6 +621,8 @@ inline int check(Args& a, Buckets* w)
     if (a.b < 0 || a.np < 0 || a.sq < 0 || a.sk < 0 || a.b > kMost || a.np > kMost || a.sq > kMost || a.sk > kMost ||
         a.q_start > kMost || a.q_start < -kMost)
         return MFX_ERR_SHAPE;
+    if (a.b * a.sq > ((int64_t)1 << 30))
+        return MFX_ERR_SHAPE;
     int64_t n = 1, bytes = 0;
     if (!mul_ok(a.b, a.np, &n) || !mul_ok(n, a.sq, &n) || !mul_ok(n, a.sk, &n) || !mul_ok(n, 16, &bytes))
         return MFX_ERR_SHAPE;
@@ -630,7 +645,7 @@ inline int check(Args& a, Buckets* w)
 inline Geom make_geom(const Args& a, const Buckets& w, const void* x)
 {
     Geom g = {};
-    g.sq = (int)a.sq, g.sk = (int)a.sk, g.np = (int)a.np, g.rows = a.b * a.sq;
+    g.sq = (int)a.sq, g.sk = (int)a.sk, g.np = (int)a.np, g.rows = (int)(a.b * a.sq);
     g.mask_sq = a.mask_sq == 1 ? 0 : a.sk;
     g.mask_np = a.mask_np == 1 ? 0 : a.mask_sq * a.sk;
     g.mask_b = a.mask_b == 1 ? 0 : a.mask_np * a.mask_sq * a.sk;
@@ -684,9 +699,9 @@ inline int plan(Geom& g, bool fast, int most)
 // Blocks per head, of which `slots` run at a time over all heads: the number
 // of waves, up to 8, whose longest block times waves is least, a block's start
 // (its window, say) counted as `extra` rows.
-inline int64_t slices_for(const Geom& g, int64_t slots, int64_t extra)
+inline int slices_for(const Geom& g, int64_t slots, int64_t extra)
 {
-    const int64_t need = (g.rows + g.teams - 1) / g.teams;  // most that have a row each
+    const int64_t need = ((int64_t)g.rows + g.teams - 1) / g.teams;  // most that have a row each
     int64_t best = 1, cost = INT64_MAX;
     for (int64_t waves = 1; waves <= 8; ++waves) {
         int64_t n = slots * waves / g.np;
@@ -696,7 +711,16 @@ inline int64_t slices_for(const Geom& g, int64_t slots, int64_t extra)
         if (c < cost)
             cost = c, best = n;
     }
-    return best;
+    return (int)best;
+}
+
+// The steps of a team's walk, once slices and teams are known.
+inline void set_walk(Geom& g)
+{
+    g.step = g.slices * g.teams;
+    g.step_i = g.step / g.sq, g.step_q = g.step % g.sq;
+    g.wrap_r = (int64_t)(g.np - 1) * g.sq;
+    g.step_r = g.step + g.step_i * g.wrap_r;
 }
 
 // Whether every row is whole chunks of 16-byte vectors.

@@ -58,8 +58,7 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
     __shared__ float2 far_part[MT / 32];
     constexpr bool LONG = MT > kTeam, ANY = C == 1, STAGED = staged<T, FAST, MT>();
     const int blocks = LONG ? g.blocks : 1;
-    const int h = (int)(blockIdx.x / g.slices);
-    const int64_t slice = blockIdx.x % g.slices;
+    const int h = (int)(blockIdx.x / g.slices), slice = (int)(blockIdx.x % g.slices);
     const int tid = threadIdx.x % g.team, tm = threadIdx.x / g.team;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lanes = g.team < 32 ? g.team : 32, warps = g.team >> 5;
     const int last = w.reach + w.hi, stride = window_stride(w), vectors = sum_vectors(w);
@@ -76,19 +75,19 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
     const float far_lo = win[window_slot(stride, 0)].x, far_hi = win[window_slot(stride, last)].x;
     float sum_lo = 0.0f, sum_hi = 0.0f;
 
-    const int64_t step = g.slices * g.teams;
-    int64_t row = slice * g.teams + tm;
-    Walk at(g, h, row, step);
+    Walk at(g, h, slice * g.teams + tm);
     int slot = 0;
-    Row<T> o = row_at<T, FAST>(g, w, MASK ? mask : nullptr, h, at, row < g.rows), ahead = o;
+    Seat<T> seat = seat_at<T>(g, w, MASK ? mask : nullptr, h, at);
     if constexpr (STAGED) {
-        stage_row<C>(stage, x, o, tid, g.team);
-        stage_row<C>(stage_dy, dy, o, tid, g.team);
+        stage_row<C>(stage, x, seat, g.sk, tid, g.team);
+        stage_row<C>(stage_dy, dy, seat, g.sk, tid, g.team);
     }
-    for (int64_t first = slice * g.teams; first < g.rows; first += step, row += step, o = ahead, slot ^= 1) {
+    for (int first = slice * g.teams; first < g.rows; first += g.step, slot ^= 1) {
+        const bool live = at.live(g);
+        const Row<T> o = row_of<T, FAST>(g, seat, live);
         uint4* sz = stage_dy + slot * C * blockDim.x;
         float shift = 0.0f, top = 0.0f, inv = 0.0f;
-        if (row < g.rows)
+        if (live)
             shift = stats[3 * o.r], top = stats[3 * o.r + 1], inv = stats[3 * o.r + 2];
         const auto run = [&](auto check) {
             constexpr bool CHECK = decltype(check)::value, PART = CHECK || MASK;
@@ -174,11 +173,11 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
                 first_half(blk);
             float D = lanes_sum<ANY>(D2.x + D2.y, lanes);
             // every chunk of this row has been read: on to the team's next row
-            at.next(g.sq);
-            ahead = row_at<T, FAST>(g, w, MASK ? mask : nullptr, h, at, row + step < g.rows);
+            at.next(g);
+            seat = seat_at<T>(g, w, MASK ? mask : nullptr, h, at);
             if constexpr (STAGED) {
-                stage_row<C>(stage, x, ahead, tid, g.team);
-                stage_row<C>(stage_dy + (slot ^ 1) * C * blockDim.x, dy, ahead, tid, g.team);
+                stage_row<C>(stage, x, seat, g.sk, tid, g.team);
+                stage_row<C>(stage_dy + (slot ^ 1) * C * blockDim.x, dy, seat, g.sk, tid, g.team);
             }
             if (warps > 1) {
                 if (lane == 0)
@@ -317,7 +316,7 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
         if (lane == 0) {
             for (int k = 0; k < nw; ++k)
                 t += (lo ? far_part[k].x : 0.0f) + (hi ? far_part[k].y : 0.0f);
-            ws[(slice * w.num + u) * g.np + h] = t * g.unfold;
+            ws[((int64_t)slice * w.num + u) * g.np + h] = t * g.unfold;
         }
     }
     pdl_launch_dependents();
@@ -345,8 +344,9 @@ int launch_bwd(Geom g, const Buckets& w, const Args& a, const void* dy, const vo
     const int64_t slots = (int64_t)sm_count() * occupancy((const void*)kern, threads, smem);
     g.slices = slices_for(g, slots, 4);
     if (g.slices > bwd_slices(a))
-        g.slices = bwd_slices(a);
-    if (g.slices * g.np > INT32_MAX)
+        g.slices = (int)bwd_slices(a);
+    set_walk(g);
+    if ((int64_t)g.slices * g.np > INT32_MAX)
         return MFX_ERR_SHAPE;
     kern<<<(unsigned)(g.slices * g.np), threads, smem, s>>>(
         static_cast<const T*>(dy), static_cast<const T*>(x), stats, static_cast<T*>(dx), static_cast<const T*>(a.mask),

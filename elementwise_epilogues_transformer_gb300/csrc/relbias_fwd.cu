@@ -137,8 +137,7 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
     const int blocks = LONG ? g.blocks : 1, cluster = LONG ? g.cluster : 1;
     const int rank = LONG ? (int)(blockIdx.x % cluster) : 0;
     const int64_t unit = LONG ? blockIdx.x / cluster : blockIdx.x;
-    const int h = (int)(unit / g.slices);
-    const int64_t slice = unit % g.slices;
+    const int h = (int)(unit / g.slices), slice = (int)(unit % g.slices);
     const int tid = threadIdx.x % g.team, tm = threadIdx.x / g.team;
     const Team team{part, mine, g.team < 32 ? g.team : 32, g.team >> 5, 0, cluster};
     fill_window(w, g, table, h, win);
@@ -146,12 +145,10 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
     const float far_lo = win[window_slot(window_stride(w), 0)].x;
     const float far_hi = win[window_slot(window_stride(w), w.reach + w.hi)].x;
 
-    const int64_t step = g.slices * g.teams;
-    int64_t row = slice * g.teams + tm;
-    Walk at(g, h, row, step);
+    Walk at(g, h, slice * g.teams + tm);
     int slot = 0;
-    for (int64_t first = slice * g.teams; first < g.rows; first += step, row += step, at.next(g.sq), slot ^= 1) {
-        const Row<T> o = row_at<T, FAST>(g, w, MASK ? mask : nullptr, h, at, row < g.rows);
+    for (int first = slice * g.teams; first < g.rows; first += g.step, at.next(g), slot ^= 1) {
+        const Row<T> o = row_of<T, FAST>(g, seat_at<T>(g, w, MASK ? mask : nullptr, h, at), at.live(g));
         const T* xr = x + o.e0;
         T* yr = y + o.e0;
         // CHECK: some chunk of the row is not there, or not all of it takes part
@@ -216,7 +213,7 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
                 }
             }
             float inv = m == -INFINITY && l == 0.0f ? 0.0f : 1.0f / l;
-            if (stats && tid == 0 && rank == 0 && row < g.rows)
+            if (stats && tid == 0 && rank == 0 && at.live(g))
                 put_stats(stats, o.r, 0.0f, m == -INFINITY ? 0.0f : m, inv);
             if (DROP)
                 inv *= g.keep_scale;
@@ -292,7 +289,8 @@ int launch_fwd(Geom g, const Buckets& w, const Args& a, const void* x, void* y, 
     const size_t smem = window_bytes(w);
     const int64_t slots = (int64_t)sm_count() * occupancy((const void*)kern, threads, smem) / g.cluster;
     g.slices = slices_for(g, slots > 0 ? slots : 1, 1);
-    const int64_t blocks = g.slices * g.np * g.cluster;
+    set_walk(g);
+    const int64_t blocks = (int64_t)g.slices * g.np * g.cluster;
     if (blocks > INT32_MAX)
         return MFX_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};

@@ -233,7 +233,7 @@ int mfx_scaled_upper_triang_masked_softmax_bwd(int dt, int64_t attn_batches, int
  * of its mask, the maximum of its scores in base-2 units and one over the sum
  * of its exponentials), or NULL (inference).
  * y: x's shape and dtype; y may equal x (in place, when no backward follows).
- * b, np, sq, sk and |q_start| at most 2^29.  One query per sequence over a long key axis
+ * b, np, sq, sk and |q_start| at most 2^29, b * sq at most 2^30.  One query per sequence over a long key axis
  * (decoding) splits a row over several thread blocks. */
 int mfx_relbias_softmax_dropout_fwd(int dt, int64_t b, int64_t np, int64_t sq, int64_t sk,
                                     const void* x, float scale,
