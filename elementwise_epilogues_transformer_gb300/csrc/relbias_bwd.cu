@@ -22,6 +22,7 @@ namespace mfx {
 namespace relbias {
 namespace {
 
+constexpr int kWalkTeam = 2 * kLongTeam;  // kernels whose rows take several register blocks (kLongTeam threads too)
 constexpr int kBwdBlocksPerSm = 16;  // most blocks of a backward grid per SM (what its workspace goes by)
 
 // Window sums: vector pair u of residue r holds the sums of entries
@@ -43,20 +44,20 @@ __device__ __forceinline__ void add4(float4* p, float2 a, float2 b)
 template <typename T, bool FAST, int MT>
 constexpr bool staged()
 {
-    return FAST && MT <= kTeam && sizeof(T) == 2;
+    return FAST && MT < kWalkTeam && sizeof(T) == 2;
 }
 
 template <typename T, int C, bool DROP, bool MASK, bool FAST, int MT>
-__global__ void __launch_bounds__(MT, MT > kTeam ? 1 : 2)
+__global__ void __launch_bounds__(MT < kWalkTeam ? MT : kLongTeam, MT > kTeam ? 1 : 2)
 relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, const T* __restrict__ mask,
             const void* __restrict__ table, float* __restrict__ ws, const __grid_constant__ Geom g,
             const __grid_constant__ Buckets w)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     float4* win = reinterpret_cast<float4*>(smem);
-    __shared__ float part[2][MT / 32];
-    __shared__ float2 far_part[MT / 32];
-    constexpr bool LONG = MT > kTeam, ANY = C == 1, STAGED = staged<T, FAST, MT>();
+    __shared__ float part[2][kLongTeam / 32];
+    __shared__ float2 far_part[kLongTeam / 32];
+    constexpr bool LONG = MT == kWalkTeam, ANY = C == 1, STAGED = staged<T, FAST, MT>();
     const int blocks = LONG ? g.blocks : 1;
     const int h = (int)(blockIdx.x / g.slices), slice = (int)(blockIdx.x % g.slices);
     const int tid = threadIdx.x % g.team, tm = threadIdx.x / g.team;
@@ -366,12 +367,14 @@ int dispatch_bwd(const Args& a, const Buckets& w, const void* dy, const void* x,
     constexpr int kMost = sizeof(T) == 2 && FAST ? 4 : 2;
     Geom g = make_geom(a, w, x);
     const int c = plan(g, FAST, kMost);
-    const bool big = g.team * g.teams > kTeam || g.blocks > 1;
+    if (g.blocks > 1)
+        return launch_bwd<T, kMost, DROP, MASK, FAST, kWalkTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s);
     if (c == 1)
         return launch_bwd<T, 1, DROP, MASK, FAST, kTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s);
     if (c == 2 && kMost > 2)
         return launch_bwd<T, 2, DROP, MASK, FAST, kTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s);
-    return big ? launch_bwd<T, kMost, DROP, MASK, FAST, kLongTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s)
+    return g.team * g.teams > kTeam
+               ? launch_bwd<T, kMost, DROP, MASK, FAST, kLongTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s)
                : launch_bwd<T, kMost, DROP, MASK, FAST, kTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s);
 }
 

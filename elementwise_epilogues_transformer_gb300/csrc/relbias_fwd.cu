@@ -44,25 +44,44 @@ struct Team {
     int lanes, warps, warp0, cluster;
 };
 
-// (maximum, sum relative to it) over the team from each warp's.
+// Joins the pairs of the first n lanes (n a power of two here, the others
+// neutral), the same bits in every lane.
+__device__ __forceinline__ float2 join_lanes(float2 v, int n)
+{
+    for (int o = n >> 1; o > 0; o >>= 1)
+        v = join(v, make_float2(__shfl_xor_sync(0xFFFFFFFFu, v.x, o), __shfl_xor_sync(0xFFFFFFFFu, v.y, o)));
+    return v;
+}
+
+// (maximum, sum relative to it) over the team from each warp's.  Few warps'
+// pairs are joined one after another by every thread, more by a warp's lanes,
+// as are those of a cluster's blocks (one trip through distributed shared
+// memory instead of eight).
 template <bool LONG>
 __device__ __forceinline__ float2 join_team(const Team& tm, float2 v, int slot)
 {
     if (tm.warps <= 1)
         return v;
-    if ((threadIdx.x & 31) == 0)
+    const int lane = threadIdx.x & 31;
+    if (lane == 0)
         tm.part[slot][threadIdx.x >> 5] = v;
     __syncthreads();
-    v = tm.part[slot][0];
-    for (int i = 1; i < tm.warps; ++i)
-        v = join(v, tm.part[slot][i]);
+    if (!LONG || tm.warps <= 4) {
+        v = tm.part[slot][0];
+        for (int i = 1; i < tm.warps; ++i)
+            v = join(v, tm.part[slot][i]);
+    } else {
+        v = lane < tm.warps ? tm.part[slot][lane] : make_float2(-INFINITY, 0.0f);
+        v = join_lanes(v, kLongTeam / 32);
+        v = make_float2(__shfl_sync(0xFFFFFFFFu, v.x, 0), __shfl_sync(0xFFFFFFFFu, v.y, 0));
+    }
     if (LONG && tm.cluster > 1) {
         if (threadIdx.x == 0)
             tm.mine[slot] = v;
         cluster_sync();
-        v = peer_pair(&tm.mine[slot], 0);
-        for (int i = 1; i < tm.cluster; ++i)
-            v = join(v, peer_pair(&tm.mine[slot], i));
+        v = lane < tm.cluster ? peer_pair(&tm.mine[slot], lane) : make_float2(-INFINITY, 0.0f);
+        v = join_lanes(v, tm.cluster);
+        v = make_float2(__shfl_sync(0xFFFFFFFFu, v.x, 0), __shfl_sync(0xFFFFFFFFu, v.y, 0));
     }
     return v;
 }
