@@ -144,7 +144,7 @@ __device__ __noinline__ void shifted_row(const T* x, T* y, float* stats, const R
 }
 
 template <typename T, int C, bool DROP, bool MASK, bool FAST, int MT>
-__global__ void __launch_bounds__(MT, MT > kTeam ? 1 : sizeof(T) == 2 && C < (MASK ? 4 : 8) ? 3 : 2)
+__global__ void __launch_bounds__(MT, MT > kTeam ? 1 : C < 8 ? 3 : 2)
 relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ mask, const void* __restrict__ table,
             const __grid_constant__ Geom g, const __grid_constant__ Buckets w)
 {
@@ -166,8 +166,10 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
 
     Walk at(g, h, slice * g.teams + tm);
     int slot = 0;
-    for (int first = slice * g.teams; first < g.rows; first += g.step, at.next(g), slot ^= 1) {
-        const Row<T> o = row_of<T, FAST>(g, seat_at<T>(g, w, MASK ? mask : nullptr, h, at), at.live(g));
+    Seat<T> seat = seat_at<T>(g, w, MASK ? mask : nullptr, h, at);
+    for (int first = slice * g.teams; first < g.rows; first += g.step, slot ^= 1) {
+        const bool live = at.live(g);
+        const Row<T> o = row_of<T, FAST>(g, seat, live);
         const T* xr = x + o.e0;
         T* yr = y + o.e0;
         // CHECK: some chunk of the row is not there, or not all of it takes part
@@ -219,7 +221,10 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
                 m = t;
             }
             const float mw = m;  // what s is relative to
-            const float2 v = join_team<LONG>(team, make_float2(m, lanes_sum<ANY>(l, team.lanes)), slot);
+            l = lanes_sum<ANY>(l, team.lanes);
+            at.next(g);  // the team's next row, while the parts of this one meet
+            seat = seat_at<T>(g, w, MASK ? mask : nullptr, h, at);
+            const float2 v = join_team<LONG>(team, make_float2(m, l), slot);
             m = v.x, l = v.y;
             if (MASK && mask) {
                 // far from zero, or every sum below the type's range (teams that share a warp go together)
@@ -232,7 +237,7 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
                 }
             }
             float inv = m == -INFINITY && l == 0.0f ? 0.0f : 1.0f / l;
-            if (stats && tid == 0 && rank == 0 && at.live(g))
+            if (stats && tid == 0 && rank == 0 && live)
                 put_stats(stats, o.r, 0.0f, m == -INFINITY ? 0.0f : m, inv);
             if (DROP)
                 inv *= g.keep_scale;
