@@ -268,7 +268,8 @@ struct Moe {
     int topk;
     int team;             // threads on a token's columns (warps of one block)
     int col_blocks;       // teams over a token's columns
-    int64_t token_blocks; // blocks before the padding's
+    int64_t pad_blocks;   // blocks that clear padding: the first ones, so that theirs is not a tail
+    int64_t token_blocks; // blocks that work on tokens
 };
 
 // The token and the columns' part of a thread's team; false where there is none.
@@ -279,7 +280,7 @@ struct Place {
 };
 __device__ __forceinline__ bool place(const Moe& m, Place& p)
 {
-    const int64_t team = (int64_t)blockIdx.x * (kThreads / m.team) + threadIdx.x / m.team;
+    const int64_t team = ((int64_t)blockIdx.x - m.pad_blocks) * (kThreads / m.team) + threadIdx.x / m.team;
     p.token = m.col_blocks == 1 ? team : team / m.col_blocks;
     p.part = (int)(team - p.token * m.col_blocks);
     p.index = p.part * m.team + threadIdx.x % m.team;
@@ -321,8 +322,8 @@ __global__ void __launch_bounds__(kThreads)
 moe_permute(const T* __restrict__ x, const int32_t* __restrict__ row_of, const int32_t* __restrict__ slot_of,
             const float* __restrict__ weight, T* __restrict__ out, float* __restrict__ out_weight, const Moe m)
 {
-    if ((int64_t)blockIdx.x >= m.token_blocks) {
-        clear_padding<T, FAST>(out, out_weight, slot_of, m, (int64_t)blockIdx.x - m.token_blocks);
+    if ((int64_t)blockIdx.x < m.pad_blocks) {
+        clear_padding<T, FAST>(out, out_weight, slot_of, m, blockIdx.x);
         return;
     }
     Place p;
@@ -375,7 +376,7 @@ moe_permute(const T* __restrict__ x, const int32_t* __restrict__ row_of, const i
 // reads row 0 instead, which is not added.
 // ---------------------------------------------------------------------------
 template <typename T, bool FAST, int G>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : G <= 4 ? 5 : 4)
 moe_unpermute(const T* __restrict__ y, const int32_t* __restrict__ row_of, const float* __restrict__ weight,
               const float* __restrict__ row_weight, T* __restrict__ out, float* __restrict__ dweight, const Moe m)
 {
@@ -488,13 +489,13 @@ __device__ __forceinline__ int index_of(int lane)
 }
 
 template <typename T, bool FAST, int G>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && G <= 4 ? 4 : 3)
 moe_unpermute_bwd(const T* __restrict__ g, const T* __restrict__ y, const int32_t* __restrict__ row_of,
                   const int32_t* __restrict__ slot_of, const float* __restrict__ weight, T* __restrict__ dy,
                   float* __restrict__ dweight, const Moe m)
 {
-    if ((int64_t)blockIdx.x >= m.token_blocks) {
-        clear_padding<T, FAST>(dy, nullptr, slot_of, m, (int64_t)blockIdx.x - m.token_blocks);
+    if ((int64_t)blockIdx.x < m.pad_blocks) {
+        clear_padding<T, FAST>(dy, nullptr, slot_of, m, blockIdx.x);
         return;
     }
     __shared__ float part[kWarps][G];
@@ -617,7 +618,7 @@ int check(int dt, int64_t tokens, int64_t topk, int64_t cols, int64_t rows)
 
 // A team of up to a block's threads on each token, two chunks a thread, and
 // (`split`) several teams where few tokens would leave SMs idle.
-Moe plan(int64_t tokens, int64_t topk, int64_t cols, int64_t rows, bool split)
+Moe plan(int64_t tokens, int64_t topk, int64_t cols, int64_t rows, bool split, bool clear)
 {
     Moe m = {};
     m.tokens = tokens, m.cols = cols, m.rows = rows, m.slots = tokens * topk, m.topk = (int)topk;
@@ -632,6 +633,7 @@ Moe plan(int64_t tokens, int64_t topk, int64_t cols, int64_t rows, bool split)
         ++m.col_blocks;
     const int64_t teams = kThreads / m.team;
     m.token_blocks = (tokens * m.col_blocks + teams - 1) / teams;
+    m.pad_blocks = clear ? (rows + kPadRows - 1) / kPadRows : 0;
     return m;
 }
 
@@ -740,8 +742,8 @@ namespace {
 int permute(int dt, int64_t tokens, int64_t topk, int64_t cols, int64_t rows, const void* x, const int32_t* row_of,
             const int32_t* slot_of, const float* weight, void* out, float* out_weight, void* stream)
 {
-    const Moe m = plan(topk > 0 ? tokens : 0, topk, cols, rows, true);
-    const int64_t blocks = m.token_blocks + (rows + kPadRows - 1) / kPadRows;
+    const Moe m = plan(topk > 0 ? tokens : 0, topk, cols, rows, true, true);
+    const int64_t blocks = m.pad_blocks + m.token_blocks;
     if (blocks > INT32_MAX)
         return MFX_ERR_SHAPE;
     const auto go = [&](auto t, auto fast) {
@@ -794,7 +796,7 @@ int unpermute(int dt, int64_t tokens, int64_t topk, int64_t cols, int64_t rows, 
         overlaps(dweight, 4 * slots, y, yb) || overlaps(dweight, 4 * slots, row_of, 4 * slots) ||
         overlaps(dweight, 4 * slots, row_weight, 4 * rows))
         return MFX_ERR_ALIAS;
-    const Moe m = plan(tokens, topk, cols, rows, true);
+    const Moe m = plan(tokens, topk, cols, rows, true, false);
     if (m.token_blocks > INT32_MAX)
         return MFX_ERR_SHAPE;
     const auto go = [&](auto t, auto fast) {
@@ -848,8 +850,8 @@ extern "C" int mfx_moe_unpermute_bwd(int dt, int64_t tokens, int64_t topk, int64
         return MFX_ERR_ALIAS;
     if (!weight && !dweight)  // the rows of g as they are
         return permute(dt, tokens, topk, cols, rows, g, row_of, slot_of, nullptr, dy, nullptr, stream);
-    const Moe m = plan(topk > 0 ? tokens : 0, topk, cols, rows, false);
-    const int64_t blocks = m.token_blocks + (rows + kPadRows - 1) / kPadRows;
+    const Moe m = plan(topk > 0 ? tokens : 0, topk, cols, rows, false, true);
+    const int64_t blocks = m.pad_blocks + m.token_blocks;
     if (blocks > INT32_MAX)
         return MFX_ERR_SHAPE;
     const auto go = [&](auto t, auto fast) {
