@@ -197,6 +197,6 @@ int mfx_device_error(unsigned* code)
     return c ? MFX_ERR_DEVICE : MFX_OK;
 }
 
-int mfx_version(void) { return (1 << 16) | 3; }
+int mfx_version(void) { return (1 << 16) | 4; }
 
 }  // extern "C"

@@ -17,6 +17,16 @@
 // so that x and g are read once however many rows they go to, and sums over a
 // token's rows run in choice order in fp32 registers: no atomics on data, the
 // same bits on every run.
+//
+// What bounds them: HBM, each with its bytes moved once.  At 16384 x 4096 bf16,
+// 2 of 8 experts: permute 64 us (403 MB, 6290 GB/s), unpermute 70 us
+// (5750 GB/s), its backward with weight gradients 109 us (671 MB,
+// 6160 GB/s).  At 8192 x 2048, 8 of 128, padding to 16: 53, 47 and 86 us.
+// The sort is two launches and 7 us at 32768 slots, 20 us at 524288 (its
+// counters, not its 8 bytes a slot); with few slots one launch and 4.5 us.
+// The copies launch a block per few tokens: blocks that went on from token to
+// token, looking the next one's rows up meanwhile, spilled the choices and
+// took 86 us in place of 70 for that unpermute.
 #include <type_traits>
 
 #include "mfx_device.cuh"
@@ -316,6 +326,7 @@ __device__ __forceinline__ void clear_padding(T* out, float* out_weight, const i
 
 // ---------------------------------------------------------------------------
 // Permute: a token's chunk is read once and written to each of its rows.
+// Two thirds of its bytes or more are writes.
 // ---------------------------------------------------------------------------
 template <typename T, bool FAST>
 __global__ void __launch_bounds__(kThreads)
@@ -373,7 +384,9 @@ moe_permute(const T* __restrict__ x, const int32_t* __restrict__ row_of, const i
 // ---------------------------------------------------------------------------
 // Unpermute (and permute's backward, without weights): a token's rows added
 // in choice order, G of them in flight at a time.  A choice without a row
-// reads row 0 instead, which is not added.
+// reads row 0 instead, which is not added.  Five blocks an SM for small G: the
+// loads of a thread wait for the row numbers, so it is warps that keep HBM busy
+// (six spill: 102 us in place of 70 at 16384 x 4096, 2 choices).
 // ---------------------------------------------------------------------------
 template <typename T, bool FAST, int G>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : G <= 4 ? 5 : 4)

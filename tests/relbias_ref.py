@@ -10,7 +10,8 @@ With u = 2^-24 (half a step of fp32, relative) and, per row, A the largest
   with one more exponential of an argument <= 2A, u (2A + 4), and summed with
   at most 128 additions in a row; numerator and denominator have all of these:
   P is off by at most rP = u (18A + 160) relative.  The backward forms P from
-  the stored log-sum (rounded: u (A + 20)) instead: rP = u (20A + 200).
+  the stored maximum and reciprocal sum, within the same; it is given
+  rP = u (20A + 200).
 """
 import math
 
