@@ -174,6 +174,28 @@ def _stream(stream, t):
     return int(stream)
 
 
+def _on(stream, device):
+    """Context in which allocations belong to `stream` (as _stream() takes it)."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory of a call's own.  It belongs to the stream that the call runs
+    on, so that it is given to nobody else while the call may use it, and to
+    the call while nobody else may."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty_like(t, stream):
+    return torch.empty_like(t) if stream is None else _empty(t.shape, t.dtype, t.device, stream)
+
+
 def _rows_cols(t):
     cols = t.shape[-1] if t.dim() else 1
     rows = t.numel() // cols if cols else 0
@@ -427,11 +449,11 @@ def mfx_relbias_softmax_dropout_fwd(x, scale, table=None, mask=None, max_distanc
     [b, np, sq, 3] is what the backward needs (None with need_stats=False)."""
     shape, shared = _relbias_args(x, table, mask, max_distance, bidirectional, causal, q_start, seq_start, p, seed,
                                   offset, elem_base)
-    y = torch.empty_like(x) if y is None else _like(y, "y", shape, x.dtype)
+    y = _empty_like(x, stream) if y is None else _like(y, "y", shape, x.dtype)
     if stats is not None:
         _like(stats, "stats", (*shape[:3], 3), torch.float32)
     elif need_stats:
-        stats = torch.empty((*shape[:3], 3), dtype=torch.float32, device=x.device)
+        stats = _empty((*shape[:3], 3), torch.float32, x.device, stream)
     _call("mfx_relbias_softmax_dropout_fwd", dtype_code(x.dtype), *shape, x.data_ptr(), scale, *shared, y.data_ptr(),
           _ptr(stats), _stream(stream, x))
     return y, stats
@@ -446,13 +468,13 @@ def mfx_relbias_softmax_dropout_bwd(dy, x, stats, scale, table=None, mask=None, 
                                   offset, elem_base)
     _like(dy, "dy", shape, x.dtype)
     _like(stats, "stats", (*shape[:3], 3), torch.float32)
-    dx = torch.empty_like(x) if dx is None else _like(dx, "dx", shape, x.dtype)
+    dx = _empty_like(x, stream) if dx is None else _like(dx, "dx", shape, x.dtype)
     if dtable is not None:
         if table is None:
             raise ValueError("dtable needs a table")
         _like(dtable, "dtable", table.shape, table.dtype)
     elif table is not None and need_dtable:
-        dtable = torch.empty_like(table)
+        dtable = _empty_like(table, stream)
     head = (dtype_code(x.dtype), *shape, dy.data_ptr(), x.data_ptr(), stats.data_ptr(), scale, *shared, dx.data_ptr(),
             _ptr(dtable))
     st = _stream(stream, x)
@@ -489,12 +511,12 @@ def mfx_moe_sort(expert_of, experts, align=1, capacity=0, rows=None, row_of=None
     slots = tokens * topk
     if row_of is None and slot_of is None and offsets is None and counts is None and experts > 0:
         # one allocation for the four maps
-        row_of, slot_of, offsets, counts = torch.empty(
-            slots + rows + 2 * experts + 1, dtype=torch.int32, device=expert_of.device).split_with_sizes(
+        row_of, slot_of, offsets, counts = _empty(
+            slots + rows + 2 * experts + 1, torch.int32, expert_of.device, stream).split_with_sizes(
                 [slots, rows, experts + 1, experts])
         row_of = row_of.view(tokens, topk)
     else:
-        new = lambda t, name, shape: (torch.empty(shape, dtype=torch.int32, device=expert_of.device)  # noqa: E731
+        new = lambda t, name, shape: (_empty(shape, torch.int32, expert_of.device, stream)  # noqa: E731
                                       if t is None else _like(t, name, shape, torch.int32))
         row_of, slot_of = new(row_of, "row_of", (tokens, topk)), new(slot_of, "slot_of", (rows,))
         offsets, counts = new(offsets, "offsets", (experts + 1,)), new(counts, "counts", (experts,))
@@ -533,10 +555,10 @@ def mfx_moe_permute_fwd(x, row_of, slot_of, weight=None, out=None, out_weight=No
     tokens, topk = _moe_maps(x, row_of, slot_of)
     _, cols = _moe_data(x, "x", tokens)
     rows = slot_of.shape[0]
-    out = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if out is None else _like(out, "out", (rows, cols), x.dtype)
+    out = _empty((rows, cols), x.dtype, x.device, stream) if out is None else _like(out, "out", (rows, cols), x.dtype)
     if weight is not None:
         _like(weight, "weight", (tokens, topk), torch.float32)
-        out_weight = (torch.empty(rows, dtype=torch.float32, device=x.device) if out_weight is None
+        out_weight = (_empty(rows, torch.float32, x.device, stream) if out_weight is None
                       else _like(out_weight, "out_weight", (rows,), torch.float32))
     elif out_weight is not None:
         raise ValueError("out_weight needs a weight")
@@ -551,10 +573,10 @@ def mfx_moe_permute_bwd(g, row_of, g_weight=None, dx=None, dweight=None, stream=
     None without g_weight."""
     tokens, topk = _moe_maps(g, row_of)
     rows, cols = _moe_data(g, "g")
-    dx = torch.empty((tokens, cols), dtype=g.dtype, device=g.device) if dx is None else _like(dx, "dx", (tokens, cols), g.dtype)
+    dx = _empty((tokens, cols), g.dtype, g.device, stream) if dx is None else _like(dx, "dx", (tokens, cols), g.dtype)
     if g_weight is not None:
         _like(g_weight, "g_weight", (rows,), torch.float32)
-        dweight = (torch.empty((tokens, topk), dtype=torch.float32, device=g.device) if dweight is None
+        dweight = (_empty((tokens, topk), torch.float32, g.device, stream) if dweight is None
                    else _like(dweight, "dweight", (tokens, topk), torch.float32))
     elif dweight is not None:
         raise ValueError("dweight needs g_weight")
@@ -570,7 +592,7 @@ def mfx_moe_unpermute_fwd(y, row_of, weight=None, out=None, stream=None):
     rows, cols = _moe_data(y, "y")
     if weight is not None:
         _like(weight, "weight", (tokens, topk), torch.float32)
-    out = torch.empty((tokens, cols), dtype=y.dtype, device=y.device) if out is None else _like(out, "out", (tokens, cols), y.dtype)
+    out = _empty((tokens, cols), y.dtype, y.device, stream) if out is None else _like(out, "out", (tokens, cols), y.dtype)
     _call("mfx_moe_unpermute_fwd", dtype_code(y.dtype), tokens, topk, cols, rows, _ptr(y), _ptr(row_of), _ptr(weight),
           _ptr(out), _stream(stream, y))
     return out
@@ -592,11 +614,11 @@ def mfx_moe_unpermute_bwd(g, y, row_of, slot_of, weight=None, dy=None, dweight=N
     if need_dweight:
         if y is None:
             raise ValueError("dweight needs y")
-        dweight = (torch.empty((tokens, topk), dtype=torch.float32, device=g.device) if dweight is None
+        dweight = (_empty((tokens, topk), torch.float32, g.device, stream) if dweight is None
                    else _like(dweight, "dweight", (tokens, topk), torch.float32))
     else:
         dweight = None
-    dy = torch.empty((rows, cols), dtype=g.dtype, device=g.device) if dy is None else _like(dy, "dy", (rows, cols), g.dtype)
+    dy = _empty((rows, cols), g.dtype, g.device, stream) if dy is None else _like(dy, "dy", (rows, cols), g.dtype)
     _call("mfx_moe_unpermute_bwd", dtype_code(g.dtype), tokens, topk, cols, rows, _ptr(g), _ptr(y), _ptr(row_of),
           _ptr(slot_of), _ptr(weight), _ptr(dy), _ptr(dweight), _stream(stream, g))
     return dy, dweight
@@ -706,7 +728,7 @@ def mfx_bias_dropout_add_train_nomask(x, bias, residual, p, seed, offset=0, elem
     _cuda(residual, "residual")
     if residual.shape != x.shape:
         raise ValueError("residual must have x's shape")
-    out = torch.empty_like(x) if out is None else _like(out, "out", x.shape, x.dtype)
+    out = _empty_like(x, stream) if out is None else _like(out, "out", x.shape, x.dtype)
     rows, cols = _rows_cols(x)
     if bias is not None and bias.numel() != cols:
         raise ValueError("bias must have one element per column of x")
@@ -718,7 +740,7 @@ def mfx_bias_dropout_add_train_nomask(x, bias, residual, p, seed, offset=0, elem
 
 def _dropout(name, x, p, seed, offset, elem_base, out, what, stream):
     _cuda(x, what[0])
-    out = torch.empty_like(x) if out is None else _like(out, what[1], x.shape, x.dtype)
+    out = _empty_like(x, stream) if out is None else _like(out, what[1], x.shape, x.dtype)
     _call(name, dtype_code(x.dtype), x.numel(), _ptr(x), float(p), int(seed) % 2**64, int(offset) % 2**64,
           int(elem_base), _ptr(out), _stream(stream, x))
     return out
@@ -744,8 +766,9 @@ _workspace_bytes = {}  # (entry point, sizes) -> bytes, for calls that say which
 
 def _with_workspace(name, args_before_ws, tail, device, workspace=None, sizes=None):
     """Query the workspace size, allocate it and run `name`.  `workspace` is
-    None (a fresh uint8 tensor), a uint8 CUDA tensor, or a callable that
-    takes the byte count and returns one (a caller's own allocator).
+    None (a fresh uint8 tensor of the call's stream, the last of tail), a
+    uint8 CUDA tensor, or a callable that takes the byte count and returns
+    one (a caller's own allocator).
     `sizes`: what the workspace's size depends on, so that it is asked for
     once."""
     need = _workspace_bytes.get((name, sizes)) if sizes is not None else None
@@ -756,7 +779,8 @@ def _with_workspace(name, args_before_ws, tail, device, workspace=None, sizes=No
         if sizes is not None:
             _workspace_bytes[(name, sizes)] = need
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        other = tail[-1] != (_raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream)
+        workspace = _empty(max(need, 16), torch.uint8, device, tail[-1] if other else None)
     else:
         if callable(workspace):
             workspace = workspace(max(need, 16))

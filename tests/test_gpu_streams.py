@@ -1,0 +1,60 @@
+"""Calls on another stream than the current one: what they allocate for
+themselves must not be given to the current stream while they have yet to run."""
+import pytest
+import torch
+
+import elementwise_epilogues_transformer_gb300 as mfx
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def calls(stream):
+    """Outputs of the operators that allocate, with workspaces of their own among them."""
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(2, 4, 64, 512, generator=g).bfloat16().to(DEV)
+    table = torch.randn(32, 4, generator=g).to(DEV)
+    chosen = torch.randint(0, 16, (3000, 4), generator=g, dtype=torch.int32).to(DEV)
+    tokens = torch.randn(3000, 256, generator=g).bfloat16().to(DEV)
+    weight = torch.rand(3000, 4, generator=g).to(DEV)
+    bias = torch.randn(256, generator=g).bfloat16().to(DEV)
+    torch.cuda.synchronize()
+
+    def run():
+        kw = dict(table=table, p=0.1, seed=3, stream=stream)
+        y, stats = mfx.mfx_relbias_softmax_dropout_fwd(x, 0.125, **kw)
+        dx, dtable = mfx.mfx_relbias_softmax_dropout_bwd(y, x, stats, 0.125, **kw)
+        row_of, slot_of, ends, counts = mfx.mfx_moe_sort(chosen, 16, align=8, stream=stream)
+        rows, _ = mfx.mfx_moe_permute_fwd(tokens, row_of, slot_of, stream=stream)
+        out = mfx.mfx_moe_unpermute_fwd(rows, row_of, weight, stream=stream)
+        dy, dweight = mfx.mfx_moe_unpermute_bwd(out, rows, row_of, slot_of, weight, stream=stream)
+        dtokens, _ = mfx.mfx_moe_permute_bwd(dy, row_of, stream=stream)
+        add = mfx.mfx_bias_dropout_add_train_nomask(tokens, bias, out, 0.1, 3, stream=stream)
+        drop = mfx.mfx_dropout_bwd(mfx.mfx_dropout_fwd(tokens, 0.1, 3, stream=stream), 0.1, 3, stream=stream)
+        _, dbias = mfx.mfx_bias_gelu_bwd_dbias(tokens, bias, tokens, stream=stream)
+        return [y, stats, dx, dtable, row_of, slot_of, ends, counts, rows, out, dy, dweight, dtokens, add, drop, dbias]
+
+    return run
+
+
+@pytest.mark.parametrize("kind", ["stream", "handle", "default"])
+def test_other_stream(kind):
+    want = calls(None)()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    stream = {"stream": side, "handle": side.cuda_stream, "default": 0}[kind]
+    run = calls(stream)
+    here = torch.cuda.current_stream() if kind != "default" else side
+    other = side if kind != "default" else torch.cuda.default_stream()
+    with torch.cuda.stream(here):
+        with torch.cuda.stream(other):
+            torch.cuda._sleep(20_000_000)  # about 10 ms: the calls wait in line
+        got = run()
+        # whatever memory is free to this stream is written at once
+        for shift in range(9, 24):
+            for _ in range(4):
+                torch.empty(1 << shift, dtype=torch.uint8, device=DEV).fill_(0xFF)
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
