@@ -509,20 +509,13 @@ def mfx_moe_sort(expert_of, experts, align=1, capacity=0, rows=None, row_of=None
     if rows is None:
         rows = slot_of.numel() if slot_of is not None else mfx_moe_rows(tokens, topk, experts, align)
     slots = tokens * topk
-    if row_of is None and slot_of is None and offsets is None and counts is None and experts > 0:
-        # one allocation for the four maps
-        row_of, slot_of, offsets, counts = _empty(
-            slots + rows + 2 * experts + 1, torch.int32, expert_of.device, stream).split_with_sizes(
-                [slots, rows, experts + 1, experts])
-        row_of = row_of.view(tokens, topk)
-    else:
-        new = lambda t, name, shape: (_empty(shape, torch.int32, expert_of.device, stream)  # noqa: E731
-                                      if t is None else _like(t, name, shape, torch.int32))
-        row_of, slot_of = new(row_of, "row_of", (tokens, topk)), new(slot_of, "slot_of", (rows,))
-        offsets, counts = new(offsets, "offsets", (experts + 1,)), new(counts, "counts", (experts,))
+    new = lambda t, name, shape: (_empty(shape, torch.int32, expert_of.device, stream) if t is None  # noqa: E731
+                                  else _like(t, name, shape, torch.int32))
+    row_of, slot_of = new(row_of, "row_of", (tokens, topk)), new(slot_of, "slot_of", (rows,))
+    offsets, counts = new(offsets, "offsets", (max(experts, 0) + 1,)), new(counts, "counts", (max(experts, 0),))
     _with_workspace("mfx_moe_sort", (tokens, topk, experts, align, capacity, rows, expert_of.data_ptr(),
                                      row_of.data_ptr(), slot_of.data_ptr(), offsets.data_ptr(), counts.data_ptr()),
-                    (_stream(stream, expert_of),), expert_of.device, workspace, (slots, experts))
+                    (_stream(stream, expert_of),), expert_of.device, workspace, (slots, experts), none=True)
     return row_of, slot_of, offsets, counts
 
 
@@ -764,13 +757,13 @@ def mfx_dropout_bwd(g, p, seed, offset=0, elem_base=0, dx=None, stream=None):
 _workspace_bytes = {}  # (entry point, sizes) -> bytes, for calls that say which sizes theirs goes by
 
 
-def _with_workspace(name, args_before_ws, tail, device, workspace=None, sizes=None):
+def _with_workspace(name, args_before_ws, tail, device, workspace=None, sizes=None, none=False):
     """Query the workspace size, allocate it and run `name`.  `workspace` is
     None (a fresh uint8 tensor of the call's stream, the last of tail), a
     uint8 CUDA tensor, or a callable that takes the byte count and returns
     one (a caller's own allocator).
     `sizes`: what the workspace's size depends on, so that it is asked for
-    once."""
+    once; `none`: a call whose workspace is empty takes none."""
     need = _workspace_bytes.get((name, sizes)) if sizes is not None else None
     if need is None:
         size = C.c_size_t(0)
@@ -779,6 +772,9 @@ def _with_workspace(name, args_before_ws, tail, device, workspace=None, sizes=No
         if sizes is not None:
             _workspace_bytes[(name, sizes)] = need
     if workspace is None:
+        if none and need == 0:
+            _call(name, *args_before_ws, None, None, *tail)
+            return None
         other = tail[-1] != (_raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream)
         workspace = _empty(max(need, 16), torch.uint8, device, tail[-1] if other else None)
     else:

@@ -706,13 +706,13 @@ extern "C" int mfx_moe_sort(int64_t tokens, int64_t topk, int64_t experts, int64
         p.chunk *= 2;
     p.chunks = slots > p.chunk ? (slots + p.chunk - 1) / p.chunk : 1;
     const size_t bytes = p.chunks > 1 ? (size_t)(p.chunks * experts) * sizeof(int) : 0;
-    if (!workspace_bytes)
+    if (!workspace_bytes && (workspace || bytes > 0))
         return MFX_ERR_NULL;
-    if (!workspace) {
+    if (!workspace && workspace_bytes) {
         *workspace_bytes = bytes;
         return MFX_OK;
     }
-    if (*workspace_bytes < bytes || !aligned16(workspace))
+    if (workspace && (*workspace_bytes < bytes || !aligned16(workspace)))
         return MFX_ERR_WORKSPACE;
     if ((slots > 0 && (!expert_of || !row_of)) || (rows > 0 && !slot_of) || !offsets || !counts)
         return MFX_ERR_NULL;

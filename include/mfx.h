@@ -293,8 +293,9 @@ int64_t mfx_moe_rows(int64_t tokens, int64_t topk, int64_t experts, int64_t alig
  * slot_of: [rows] slot of each row, -1 for padding.
  * offsets: [experts + 1] first row of each expert, and the end of the last.
  * counts:  [experts] slots of each expert that have a row.
- * All int32.  Workspace protocol as for the fused bias gradients (the size
- * may be 0: up to 2048 slots need none, and one kernel does it all). */
+ * All int32.  Workspace protocol as for the fused bias gradients.  The size
+ * may be 0 (up to 2048 slots need none, and one kernel does it all); then
+ * workspace and workspace_bytes may both be NULL. */
 int mfx_moe_sort(int64_t tokens, int64_t topk, int64_t experts, int64_t align, int64_t capacity, int64_t rows,
                  const int32_t* expert_of, int32_t* row_of, int32_t* slot_of, int32_t* offsets, int32_t* counts,
                  void* workspace, size_t* workspace_bytes, void* stream);

@@ -153,6 +153,13 @@ def test_sort_validation(L):
     assert L.mfx_moe_sort(8, 2, 4, 1, 0, 16, X, Y, Z, T, M, W_, None, None) == NULL
 
 
+def test_sort_without_workspace(L):
+    """Both null where the size is 0 (checked on a GPU), an error where it is not."""
+    assert L.mfx_moe_sort(5000, 2, 4, 1, 0, 10000, X, Y, Z, T, M, None, None, None) == NULL
+    assert L.mfx_moe_sort(8, 2, 4, 1, 0, 16, X, None, Z, T, M, None, None, None) == NULL
+    assert L.mfx_moe_sort(8, 2, 4, 1, 0, 16, X, X, Z, T, M, None, None, None) == ALIAS
+
+
 def test_rows():
     assert mfx.mfx_moe_rows(10, 2, 4, 1) == 20
     assert mfx.mfx_moe_rows(10, 2, 4, 16) == 20 + 4 * 15
