@@ -34,6 +34,7 @@ struct Buckets {
 struct Geom {
     int sq, sk, np;
     int rows;                  // b * sq: rows of one head
+    int64_t total, mask_total; // elements of the tensor and of the mask
     int64_t mask_b, mask_np, mask_sq;  // strides of the mask in elements (0 = broadcast)
     int q_start;
     const int32_t* seq_start;  // per batch, or null
@@ -206,9 +207,12 @@ __device__ __forceinline__ void fill_outside(float2 (&f)[4], int k0, int end, fl
     }
 }
 
-// Elements [k0, k0 + 8) of a row, of which [0, end) exist.  FAST: the row is
-// whole chunks of 16-byte vectors.  Otherwise a chunk that is not whole, or
-// not aligned, is read element by element, zero where there is none.
+// Elements [k0, k0 + 8) of a row, of which [0, end) are wanted.  FAST: the row
+// is whole chunks of 16-byte vectors.  Otherwise a chunk is read as vectors
+// where they are aligned and either the row has all of it or (`inner`) the
+// tensor does: what stands outside the row is the neighbours' then, and the
+// caller does not use it.  Chunks at a tensor's ends, and ones that are not
+// aligned, are read element by element, zero where there is none.
 template <typename T>
 __device__ __noinline__ void load_ragged(const T* p, int k0, int end, Raw8<T>* raw)
 {
@@ -220,14 +224,21 @@ __device__ __noinline__ void load_ragged(const T* p, int k0, int end, Raw8<T>* r
 }
 
 template <typename T, bool FAST>
-__device__ __forceinline__ void load_chunk(const T* p, int k0, int end, Raw8<T>& raw)
+__device__ __forceinline__ void load_chunk(const T* p, int k0, int end, bool inner, Raw8<T>& raw)
 {
-    if (FAST || (k0 >= 0 && k0 + 8 <= end && (reinterpret_cast<uintptr_t>(p) & 15u) == 0)) {
+    if constexpr (FAST) {
         ld8(p, raw);
     } else {
-        Raw8<T> r;
-        load_ragged(p, k0, end, &r);
-        raw = r;
+        raw = Raw8<T>{};
+        if (k0 < end) {
+            if ((inner || (k0 >= 0 && k0 + 8 <= end)) && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+                ld8(p, raw);
+            } else {
+                Raw8<T> r;
+                load_ragged(p, k0, end, &r);
+                raw = r;
+            }
+        }
     }
 }
 
@@ -259,6 +270,7 @@ struct Row : Seat<T> {
     int64_t e0;       // element index of chunk 0 in the tensor
     uint64_t block0;  // generator block of chunk 0
     int a, chunks;    // chunk phase; chunks of the row
+    bool inner, mask_inner;  // all of its chunks lie in the tensor, in the mask (not set where chunks are whole)
 };
 
 // The rows that a team walks, `row` of the b * sq of head h and every step-th
@@ -306,7 +318,7 @@ __device__ __forceinline__ Seat<T> seat_at(const Geom& g, const Buckets& w, cons
 }
 
 template <typename T, bool FAST>
-__device__ __forceinline__ Row<T> row_of(const Geom& g, const Seat<T>& seat, bool live)
+__device__ __forceinline__ Row<T> row_of(const Geom& g, const Seat<T>& seat, bool live, const T* mask)
 {
     Row<T> o;
     static_cast<Seat<T>&>(o) = seat;
@@ -315,6 +327,11 @@ __device__ __forceinline__ Row<T> row_of(const Geom& g, const Seat<T>& seat, boo
     o.e0 = e - o.a;
     o.block0 = (g.elem_base + (uint64_t)e) >> 3;
     o.chunks = live ? (g.sk + o.a + 7) >> 3 : 0;
+    if (!FAST) {
+        const int64_t m0 = seat.mask - mask - o.a;
+        o.inner = o.e0 >= 0 && o.e0 + 8 * o.chunks <= g.total;
+        o.mask_inner = m0 >= 0 && m0 + 8 * o.chunks <= g.mask_total;
+    }
     return o;
 }
 
@@ -367,12 +384,12 @@ __device__ __forceinline__ void restage(uint4* stage, int c, const Raw8<bf16>& r
 __device__ __forceinline__ void ld8_cached(const bf16* p, Raw8<bf16>& r) { r.v = ld16_ca(p); }
 __device__ __forceinline__ void ld8_cached(const float* p, Raw8<float>& r) { r.v[0] = ld16_ca(p), r.v[1] = ld16_ca(p + 4); }
 template <typename T, bool FAST>
-__device__ __forceinline__ void load_mask(const T* p, int k0, int end, Raw8<T>& raw)
+__device__ __forceinline__ void load_mask(const T* p, int k0, int end, bool inner, Raw8<T>& raw)
 {
     if (FAST)
         ld8_cached(p, raw);
     else
-        load_chunk<T, FAST>(p, k0, end, raw);
+        load_chunk<T, FAST>(p, k0, end, inner, raw);
 }
 
 // Whether a chunk of the mask is all zero (adds nothing) or all -inf (leaves
@@ -407,7 +424,7 @@ __device__ __forceinline__ bool score_chunk(const Raw8<T>& raw, const Row<T>& ro
     Raw8<T> mraw;
     bool add = false;
     if (MASK && masked) {  // the same for every lane, as the votes have to be
-        load_mask<T, FAST>(row.mask + (FAST && k0 >= row.end ? 0 : k0), k0, row.end, mraw);
+        load_mask<T, FAST>(row.mask + (FAST && k0 >= row.end ? 0 : k0), k0, row.end, row.mask_inner, mraw);
         add = __any_sync(0xFFFFFFFFu, !all_zero(mraw) || shift != 0.0f);
         if (add && __all_sync(0xFFFFFFFFu, all_out(mraw)))
             return false;
@@ -646,6 +663,7 @@ inline Geom make_geom(const Args& a, const Buckets& w, const void* x)
 {
     Geom g = {};
     g.sq = (int)a.sq, g.sk = (int)a.sk, g.np = (int)a.np, g.rows = (int)(a.b * a.sq);
+    g.total = a.n, g.mask_total = a.mask_bytes / dtype_bytes(a.dt);
     g.mask_sq = a.mask_sq == 1 ? 0 : a.sk;
     g.mask_np = a.mask_np == 1 ? 0 : a.mask_sq * a.sk;
     g.mask_b = a.mask_b == 1 ? 0 : a.mask_np * a.mask_sq * a.sk;

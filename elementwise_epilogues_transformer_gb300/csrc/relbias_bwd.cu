@@ -94,7 +94,7 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
     }
     for (int first = slice * g.teams; first < g.rows; first += g.step, slot ^= 1) {
         const bool live = at.live(g);
-        const Row<T> o = row_of<T, FAST>(g, seat, live);
+        const Row<T> o = row_of<T, FAST>(g, seat, live, mask);
         uint4* sz = stage_dy + slot * C * blockDim.x;
         float shift = 0.0f, top = 0.0f, inv = 0.0f;
         if (live)
@@ -130,8 +130,8 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
                     for (int c = 0; c < C; ++c) {
                         const int ch = (blk * C + c) * g.team + tid, k0 = ch * 8 - o.a;
                         const int k = 8 * (CHECK && FAST && k0 >= o.end ? 0 : ch);
-                        load_chunk<T, FAST>(x + o.e0 + k, k0, o.end, rx[c]);
-                        load_chunk<T, FAST>(dy + o.e0 + k, k0, o.end, z[c]);
+                        load_chunk<T, FAST>(x + o.e0 + k, k0, o.end, o.inner, rx[c]);
+                        load_chunk<T, FAST>(dy + o.e0 + k, k0, o.end, o.inner, z[c]);
                     }
                 }
                 if (PART)

@@ -174,7 +174,7 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
     Seat<T> seat = seat_at<T>(g, w, MASK ? mask : nullptr, h, at);
     for (int first = slice * g.teams; first < g.rows; first += g.step, slot ^= 1) {
         const bool live = at.live(g);
-        const Row<T> o = row_of<T, FAST>(g, seat, live);
+        const Row<T> o = row_of<T, FAST>(g, seat, live, mask);
         const T* xr = x + o.e0;
         T* yr = y + o.e0;
         // CHECK: some chunk of the row is not there, or not all of it takes part
@@ -189,7 +189,7 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     const int ch = c0 + c * g.team, k0 = ch * 8 - o.a;
-                    load_chunk<T, FAST>(xr + 8 * (CHECK && FAST && k0 >= o.end ? 0 : ch), k0, o.end, raw[c]);
+                    load_chunk<T, FAST>(xr + 8 * (CHECK && FAST && k0 >= o.end ? 0 : ch), k0, o.end, o.inner, raw[c]);
                 }
                 float t = -INFINITY;
                 if (PART)
@@ -262,7 +262,7 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
                         has = some_part<true>(k0, o.end);
                         if (has) {
                             Raw8<T> raw;
-                            load_chunk<T, FAST>(xr + 8 * (FAST && k0 >= o.end ? 0 : ch), k0, o.end, raw);
+                            load_chunk<T, FAST>(xr + 8 * (FAST && k0 >= o.end ? 0 : ch), k0, o.end, o.inner, raw);
                             has = score_chunk<T, FAST, MASK>(raw, o, g, w, win, far_lo, far_hi, k0, mask != nullptr, 0.0f, s[c]);
                         }
                     }
