@@ -18,14 +18,16 @@
 // workspace, and a second kernel adds those in block order.
 //
 // What bounds it: instruction issue again, 38 warp instructions per 32
-// elements at 64 % of the slots (2x8x2048x2048 bf16 with dropout; two conversions and a
-// multiply-add more than the forward, the sums of the table's gradient, and
-// two trips through shared memory for dy), with x and dy read once from DRAM.
+// elements at 64 % of the slots (2x8x2048x2048 bf16 with dropout), with x and
+// dy read once from DRAM.  Beside the forward's work it has dy's conversion,
+// the products and differences, the sums of the table's gradient, and dy's two
+// trips through shared memory.
 // A thread holds 4 chunks, not the forward's 8, since Q and z live together;
 // the next row arrives in shared memory meanwhile, which hides what the second
 // barrier and the half as many warps leave uncovered.  At 2x32x4096x4096 bf16
 // (6.44 GB): 1008 us (6390 GB/s) without dropout, 1359 us (4740 GB/s) with;
-// 4x12x1024x1024 causal with padding masks and dropout 92 us.
+// 4x12x1024x1024 causal with padding masks and dropout 89 us; fp32 rows of 1001
+// keys, 3x7x333 of them, with full masks and dropout 38 us.
 #include "relbias.cuh"
 
 namespace mfx {
@@ -306,26 +308,30 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
         entry[i] = t;
     }
     __syncthreads();
-    const int nw = blockDim.x >> 5;
-    for (int u = warp; u < w.num; u += nw) {
-        const bool right = u >= w.side;
+    // eight lanes to a bucket (a warp to each took 3 us longer at any size: 15.2
+    // in place of 12.2 us at 8x16x77x77)
+    const int nw = blockDim.x >> 5, sub = threadIdx.x & 7;
+    for (int u0 = 0; u0 < w.num; u0 += blockDim.x >> 3) {
+        const int u = u0 + (threadIdx.x >> 3);
+        const bool right = u >= w.side, lo = u == w.side - 1, hi = u == (w.hi ? w.num - 1 : 0);
         const int v = right ? u - w.side : u;
-        const bool lo = u == w.side - 1, hi = u == (w.hi ? w.num - 1 : 0);
-        int n0 = side_start(w, v);
-        const int n1 = side_start(w, v + 1);
+        int n0 = 0, n1 = 0;
+        if (u < w.num)
+            n0 = side_start(w, v), n1 = side_start(w, v + 1);
         if (right && n0 < 1)
             n0 = 1;
         float t = 0.0f;
-        for (int n = n0 + lane; n < n1; n += 32)
+        for (int n = n0 + sub; n < n1; n += 8)
             t += entry[right ? w.reach + n : w.reach - n];
-        if (lo && lane < 8)
-            t += entry[lane - 8];
-        if (hi && lane < 8)
-            t += entry[last + 1 + lane];
-        t = lanes_sum<false>(t, 32);
-        if (lane == 0) {
-            for (int k = 0; k < nw; ++k)
-                t += (lo ? far_part[k].x : 0.0f) + (hi ? far_part[k].y : 0.0f);
+        if (lo)
+            t += entry[sub - 8];
+        if (hi)
+            t += entry[last + 1 + sub];
+        t = lanes_sum<true>(t, 8);
+        if (u < w.num && sub == 0) {
+            if (lo || hi)
+                for (int k = 0; k < nw; ++k)
+                    t += (lo ? far_part[k].x : 0.0f) + (hi ? far_part[k].y : 0.0f);
             ws[((int64_t)slice * w.num + u) * g.np + h] = t * g.unfold;
         }
     }
