@@ -15,7 +15,7 @@ namespace relbias {
 
 constexpr int kTeam = 256;            // threads per row where rows are not long
 constexpr int kLongTeam = 512;        // ... where they are
-constexpr int kSmallBlock = 128;      // threads of a block whose teams are a warp or less
+constexpr int kSmallBlock = 128;      // threads of a block whose teams are a warp or less (and the largest of kernels for teams of part of a warp)
 constexpr int kMaxBuckets = 256;      // buckets of a table
 constexpr int kMaxSide = 128;         // buckets of one direction
 constexpr int kMaxDistance = 2048;    // keeps the window and its sums within a block's shared memory
@@ -691,17 +691,24 @@ inline Geom make_geom(const Args& a, const Buckets& w, const void* x)
 inline int64_t chunks_of(const Geom& g, bool fast) { return (g.sk + (fast ? 0 : 7) + 7) / 8; }
 
 // Threads, rows and register blocks of a launch; returns the chunks that a
-// thread holds.  A thread holds up to `most` chunks, so that a row's
-// reduction and bookkeeping are small beside its work; rows of at most 32
-// chunks share a warp, 8, 16 or 32 lanes to a row.
-inline int plan(Geom& g, bool fast, int most)
+// thread holds, up to `most`.  A row of at most 32 * `most` chunks has 8, 16 or
+// 32 lanes of a warp: the fewer, the more rows share a warp's reduction and
+// bookkeeping, so as few as still give every SM 512 threads, but not fewer
+// than `least` nor more than `shared` chunks to each.  (bf16 forwards,
+// 16x16x512x512: 16 lanes 62 us, 8 lanes 48; 32x12x256x256: 32 lanes 33 us, 16
+// lanes 25, 8 lanes 20.)
+inline int plan(Geom& g, bool fast, int most, int shared, int least)
 {
-    const int64_t chunks = chunks_of(g, fast);
+    const int64_t chunks = chunks_of(g, fast), rows = (int64_t)g.rows * g.np;
     g.cluster = 1, g.teams = 1, g.blocks = 1;
-    if (chunks <= 32 * (most < 4 ? most : 4)) {
+    if (chunks <= 32 * most) {
+        int c = 1;
+        while (32 * c < chunks)
+            c *= 2;
         g.team = chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
+        while (2 * c <= shared && g.team > least && rows * g.team / 2 >= (int64_t)sm_count() * 512)
+            c *= 2, g.team /= 2;
         g.teams = kSmallBlock / g.team;
-        const int c = chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4;
         g.exact = fast && chunks == (int64_t)g.team * c;
         return c;
     }

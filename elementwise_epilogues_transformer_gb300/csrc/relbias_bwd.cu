@@ -25,9 +25,9 @@
 // A thread holds 4 chunks, not the forward's 8, since Q and z live together;
 // the next row arrives in shared memory meanwhile, which hides what the second
 // barrier and the half as many warps leave uncovered.  At 2x32x4096x4096 bf16
-// (6.44 GB): 1008 us (6390 GB/s) without dropout, 1359 us (4740 GB/s) with;
+// (6.44 GB): 1004 us (6420 GB/s) without dropout, 1353 us (4760 GB/s) with;
 // 4x12x1024x1024 causal with padding masks and dropout 89 us; fp32 rows of 1001
-// keys, 3x7x333 of them, with full masks and dropout 38 us.
+// keys, 3x7x333 of them, with full masks and dropout 36 us.
 #include "relbias.cuh"
 
 namespace mfx {
@@ -58,8 +58,17 @@ constexpr bool staged()
     return FAST && MT < kWalkTeam && sizeof(T) == 2;
 }
 
+// Whether a team may be part of a warp: in the kernels of small blocks, and in
+// those of masked fp32 rows, which this form of the sums suits better for any
+// team (16x12x1024x1024 447 us in place of 497; elsewhere up to 7 % slower).
+template <typename T, bool MASK, bool FAST, int MT>
+constexpr bool any_team()
+{
+    return MT == kSmallBlock || (MT == kTeam && sizeof(T) == 4 && MASK && FAST);
+}
+
 template <typename T, int C, bool DROP, bool MASK, bool FAST, int MT>
-__global__ void __launch_bounds__(MT < kWalkTeam ? MT : kLongTeam, MT > kTeam ? 1 : 2)
+__global__ void __launch_bounds__(MT < kWalkTeam ? MT : kLongTeam, MT > kTeam ? 1 : MT == kSmallBlock ? 4 : 2)
 relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, const T* __restrict__ mask,
             const void* __restrict__ table, float* __restrict__ ws, const __grid_constant__ Geom g,
             const __grid_constant__ Buckets w)
@@ -68,7 +77,7 @@ relbias_bwd(const T* dy, const T* x, const float* __restrict__ stats, T* dx, con
     float4* win = reinterpret_cast<float4*>(smem);
     __shared__ float part[2][kLongTeam / 32];
     __shared__ float2 far_part[kLongTeam / 32];
-    constexpr bool LONG = MT == kWalkTeam, ANY = C == 1, STAGED = staged<T, FAST, MT>();
+    constexpr bool LONG = MT == kWalkTeam, ANY = any_team<T, MASK, FAST, MT>(), STAGED = staged<T, FAST, MT>();
     const int blocks = LONG ? g.blocks : 1;
     const int h = (int)(blockIdx.x / g.slices), slice = (int)(blockIdx.x % g.slices);
     const int tid = threadIdx.x % g.team, tm = threadIdx.x / g.team;
@@ -380,14 +389,21 @@ int dispatch_bwd(const Args& a, const Buckets& w, const void* dy, const void* x,
 {
     // fp32 holds half the chunks: a chunk's gradient takes twice the registers
     // (with four, 2x8x1027x2051 with dropout took 142 us in place of 122; bf16
-    // with two, 4099 keys a row, 90 us in place of 68)
+    // with two, 2x4x515x4099 with padding masks, 90 us in place of 68)
     constexpr int kMost = sizeof(T) == 2 ? 4 : 2;
     Geom g = make_geom(a, w, x);
-    const int c = plan(g, FAST, kMost);
+    // fewer lanes to a row make its near chunks take more turns, which pays
+    // where a causal row leaves chunks out (64x16x128x128: 57 -> 47 us; else 35 -> 36)
+    const int c = plan(g, FAST, kMost, kMost, a.causal ? 8 : 16);
     if (g.blocks > 1)
         return launch_bwd<T, kMost, DROP, MASK, FAST, kWalkTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s);
-    if (c == 1)
-        return launch_bwd<T, 1, DROP, MASK, FAST, kTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s);
+    if (g.team < 32 || c == 1) {
+        if (c == 1)
+            return launch_bwd<T, 1, DROP, MASK, FAST, kSmallBlock>(g, w, a, dy, x, stats, dx, dtable, workspace, s);
+        if (c == 2 && kMost > 2)
+            return launch_bwd<T, 2, DROP, MASK, FAST, kSmallBlock>(g, w, a, dy, x, stats, dx, dtable, workspace, s);
+        return launch_bwd<T, kMost, DROP, MASK, FAST, kSmallBlock>(g, w, a, dy, x, stats, dx, dtable, workspace, s);
+    }
     if (c == 2 && kMost > 2)
         return launch_bwd<T, 2, DROP, MASK, FAST, kTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s);
     return g.team * g.teams > kTeam

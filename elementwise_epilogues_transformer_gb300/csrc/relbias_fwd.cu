@@ -31,8 +31,8 @@
 // 21.7 warp instructions per 32 elements, at 57 % of the issue slots and 45 % of
 // the ALU pipe, about 7 of them the generator's 10 rounds and the 8 keep words;
 // DRAM reads are x once.  At 2x32x4096x4096 bf16 (4.29 GB): 688 us (6240 GB/s) without dropout,
-// 969 us (4430 GB/s) with; 4x12x1024x1024 causal with padding masks and
-// dropout 66 us; decode rows 32x32x8192 9.5 us and 1x16x131072 10.8 us of GPU
+// 970 us (4430 GB/s) with; 4x12x1024x1024 causal with padding masks and
+// dropout 66 us; 16x16x512x512 with dropout 67 us; decode rows 32x32x8192 9.5 us and 1x16x131072 10.8 us of GPU
 // time; 2x8x2048x4096 fp32 with dropout 188 us.
 #include "relbias.cuh"
 
@@ -149,7 +149,7 @@ __device__ __noinline__ void shifted_row(const T* x, T* y, float* stats, const R
 }
 
 template <typename T, int C, bool DROP, bool MASK, bool FAST, int MT>
-__global__ void __launch_bounds__(MT, MT > kTeam ? 1 : C < 8 ? 3 : 2)
+__global__ void __launch_bounds__(MT, MT > kTeam ? 1 : (C < 8 ? 3 : 2) * (kTeam / MT))
 relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ mask, const void* __restrict__ table,
             const __grid_constant__ Geom g, const __grid_constant__ Buckets w)
 {
@@ -157,7 +157,7 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
     float4* win = reinterpret_cast<float4*>(smem);
     __shared__ float2 part[2][kLongTeam / 32];
     __shared__ float2 mine[2];
-    constexpr bool LONG = MT > kTeam, ANY = C == 1;
+    constexpr bool LONG = MT > kTeam, ANY = MT == kSmallBlock;
     const int blocks = LONG ? g.blocks : 1, cluster = LONG ? g.cluster : 1;
     const int rank = LONG ? (int)(blockIdx.x % cluster) : 0;
     const int64_t unit = LONG ? blockIdx.x / cluster : blockIdx.x;
@@ -342,7 +342,10 @@ template <typename T, bool DROP, bool MASK, bool FAST>
 int dispatch_fwd(const Args& a, const Buckets& w, const void* x, void* y, float* stats, cudaStream_t s)
 {
     Geom g = make_geom(a, w, x);
-    int c = plan(g, FAST, FAST && sizeof(T) == 2 ? 8 : 4);
+    constexpr int kMost = FAST && sizeof(T) == 2 ? 8 : 4;
+    // (fp32 rows of which all takes part: four chunks to a thread spill;
+    // 16x16x512x512 95 us in place of 85)
+    int c = plan(g, FAST, kMost, sizeof(T) == 4 && FAST && !MASK && !a.causal ? 2 : kMost, 8);
     const int64_t rows = a.b * a.np * a.sq, sms = sm_count(), chunks = chunks_of(g, FAST);
     if (chunks > 32 && rows < 4 * sms) {
         // few rows: as many threads on each as give every SM work, and rows
@@ -362,17 +365,27 @@ int dispatch_fwd(const Args& a, const Buckets& w, const void* x, void* y, float*
         g.exact = FAST && chunks == held;
     }
     const bool big = g.team * g.teams > kTeam || g.cluster > 1 || g.blocks > 1;
+    // kernels of small blocks take teams that are part of a warp; for others
+    // they are slower (2x32x4096x4096 without dropout 717 us in place of 689)
+    if (c == 2)
+        return launch_fwd<T, 2, DROP, MASK, FAST, kSmallBlock>(g, w, a, x, y, stats, s);
+    if (g.team * g.teams <= kSmallBlock && g.cluster == 1) {
+        if (c == 1)
+            return launch_fwd<T, 1, DROP, MASK, FAST, kSmallBlock>(g, w, a, x, y, stats, s);
+        if (g.team < 32) {
+            if constexpr (FAST && sizeof(T) == 2)
+                if (c == 8)
+                    return launch_fwd<T, 8, DROP, MASK, FAST, kSmallBlock>(g, w, a, x, y, stats, s);
+            return launch_fwd<T, 4, DROP, MASK, FAST, kSmallBlock>(g, w, a, x, y, stats, s);
+        }
+    }
     if constexpr (FAST) {
         if (c == 1)
             return big ? launch_fwd<T, 1, DROP, MASK, FAST, kLongTeam>(g, w, a, x, y, stats, s)
                        : launch_fwd<T, 1, DROP, MASK, FAST, kTeam>(g, w, a, x, y, stats, s);
-        if (c == 2)
-            return launch_fwd<T, 2, DROP, MASK, FAST, kTeam>(g, w, a, x, y, stats, s);
         if constexpr (sizeof(T) == 2)
             if (c == 8)
                 return launch_fwd<T, 8, DROP, MASK, FAST, kTeam>(g, w, a, x, y, stats, s);
-    } else if (c == 1) {
-        return launch_fwd<T, 1, DROP, MASK, FAST, kTeam>(g, w, a, x, y, stats, s);
     }
     return big ? launch_fwd<T, 4, DROP, MASK, FAST, kLongTeam>(g, w, a, x, y, stats, s)
                : launch_fwd<T, 4, DROP, MASK, FAST, kTeam>(g, w, a, x, y, stats, s);
