@@ -17,14 +17,13 @@
 // atomics, a fixed order.  Each block leaves its per-bucket sums in the
 // workspace, and a second kernel adds those in block order.
 //
-// What bounds it: instruction issue again, 38 warp instructions per 32
-// elements at 64 % of the slots (2x8x2048x2048 bf16 with dropout), with x and
+// What bounds it: instruction issue again, 36 warp instructions per 32
+// elements at 65 % of the slots (2x8x2048x2048 bf16 with dropout), with x and
 // dy read once from DRAM.  Beside the forward's work it has dy's conversion,
 // the products and differences, the sums of the table's gradient, and dy's two
 // trips through shared memory.
 // A thread holds 4 chunks, not the forward's 8, since Q and z live together;
-// the next row arrives in shared memory meanwhile, which hides what the second
-// barrier and the half as many warps leave uncovered.  At 2x32x4096x4096 bf16
+// the next row arrives in shared memory meanwhile.  At 2x32x4096x4096 bf16
 // (6.44 GB): 1004 us (6420 GB/s) without dropout, 1353 us (4760 GB/s) with;
 // 4x12x1024x1024 causal with padding masks and dropout 89 us; fp32 rows of 1001
 // keys, 3x7x333 of them, with full masks and dropout 36 us.

@@ -28,12 +28,12 @@
 // registers; which is asked a warp at a time.
 //
 // What bounds it: instruction issue.  2x8x2048x2048 bf16 with dropout spends
-// 21.7 warp instructions per 32 elements, at 57 % of the issue slots and 45 % of
+// 21 warp instructions per 32 elements, at 58 % of the issue slots and 47 % of
 // the ALU pipe, about 7 of them the generator's 10 rounds and the 8 keep words;
-// DRAM reads are x once.  At 2x32x4096x4096 bf16 (4.29 GB): 688 us (6240 GB/s) without dropout,
-// 970 us (4430 GB/s) with; 4x12x1024x1024 causal with padding masks and
-// dropout 66 us; 16x16x512x512 with dropout 67 us; decode rows 32x32x8192 9.5 us and 1x16x131072 10.8 us of GPU
-// time; 2x8x2048x4096 fp32 with dropout 188 us.
+// DRAM reads are x once.  At 2x32x4096x4096 bf16 (4.29 GB): 688 us (6240 GB/s)
+// without dropout, 970 us (4430 GB/s) with; with dropout too, 16x16x512x512
+// 67 us, 4x12x1024x1024 causal with padding masks 66 us, 2x8x2048x4096 fp32
+// 188 us; decode rows 32x32x8192 9.5 us and 1x16x131072 10.8 us of GPU time.
 #include "relbias.cuh"
 
 namespace mfx {
