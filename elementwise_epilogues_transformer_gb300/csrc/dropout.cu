@@ -760,7 +760,7 @@ bda_bwd_generic(const TX* g, const uint8_t* keep, TX* dx, TR* dres, int64_t n, f
 // elements that do not begin on a generator block (PHASED) a unit needs its
 // block and the next one, which is the block of the lane above: lane 0 hands
 // its next unit's to lane 31, and only the warp's last block is drawn twice.
-// The next round's loads go out before this round's work.  Measured against
+// The next turn's loads go out before this turn's work.  Measured against
 // the ring that the stored-mask backward uses, bf16 32768 x 4099: 90 against
 // 96 us (113 against 253 us at an odd offset, where the ring did not apply);
 // without the early loads 96 us, with two or eight units a lane 98 and 94 us.
