@@ -778,10 +778,12 @@ extern "C" int mfx_moe_permute_fwd(int dt, int64_t tokens, int64_t topk, int64_t
 {
     using namespace mfx;
     const int st = check(dt, tokens, topk, cols, rows);
-    if (st != MFX_OK || rows == 0 || cols == 0)
+    if (st != MFX_OK || rows == 0 || (cols == 0 && !weight && !out_weight))
         return st;
     const int64_t slots = tokens * topk, e = dtype_bytes(dt), ob = rows * cols * e, xb = tokens * cols * e;
-    if (!out || !slot_of || (slots > 0 && (!x || !row_of)) || (weight && !out_weight) || (out_weight && !weight && slots > 0))
+    // rows without columns still carry their weights
+    if ((cols > 0 && !out) || !slot_of || (slots > 0 && ((cols > 0 && !x) || !row_of)) || (weight && !out_weight) ||
+        (out_weight && !weight && slots > 0))
         return MFX_ERR_NULL;
     if (overlaps(out, ob, x, xb) || overlaps(out, ob, row_of, 4 * slots) || overlaps(out, ob, slot_of, 4 * rows) ||
         overlaps(out, ob, weight, 4 * slots) || overlaps(out_weight, 4 * rows, out, ob) ||
@@ -798,10 +800,10 @@ int unpermute(int dt, int64_t tokens, int64_t topk, int64_t cols, int64_t rows, 
               const float* weight, const float* row_weight, void* out, float* dweight, void* stream)
 {
     const int st = check(dt, tokens, topk, cols, rows);
-    if (st != MFX_OK || tokens == 0 || cols == 0)
+    if (st != MFX_OK || tokens == 0 || (cols == 0 && !row_weight && !dweight))
         return st;
     const int64_t slots = tokens * topk, e = dtype_bytes(dt), ob = tokens * cols * e, yb = rows * cols * e;
-    if (!out || (slots > 0 && !row_of) || (slots > 0 && rows > 0 && !y) || (row_weight && !dweight) ||
+    if ((cols > 0 && !out) || (slots > 0 && !row_of) || (slots > 0 && yb > 0 && !y) || (row_weight && !dweight) ||
         (dweight && !row_weight && slots > 0 && rows > 0))
         return MFX_ERR_NULL;
     if (overlaps(out, ob, y, yb) || overlaps(out, ob, row_of, 4 * slots) || overlaps(out, ob, weight, 4 * slots) ||
@@ -847,11 +849,15 @@ extern "C" int mfx_moe_unpermute_bwd(int dt, int64_t tokens, int64_t topk, int64
 {
     using namespace mfx;
     const int st = check(dt, tokens, topk, cols, rows);
-    if (st != MFX_OK || cols == 0)
+    if (st != MFX_OK)
         return st;
     const int64_t slots = tokens * topk, e = dtype_bytes(dt), gb = tokens * cols * e, yb = rows * cols * e;
-    if (rows == 0 && (slots == 0 || !dweight))
+    if ((rows == 0 || cols == 0) && (slots == 0 || !dweight))
         return MFX_OK;
+    if (cols == 0)  // sums of no products
+        return cudaMemsetAsync(dweight, 0, 4 * (size_t)slots, static_cast<cudaStream_t>(stream)) == cudaSuccess
+                   ? MFX_OK
+                   : cuda_failure(cudaGetLastError());
     if ((rows > 0 && (!dy || !slot_of)) || (slots > 0 && (!g || !row_of)) || (dweight && rows > 0 && slots > 0 && !y))
         return MFX_ERR_NULL;
     const void* const in[] = {g, y, row_of, slot_of, weight};

@@ -306,7 +306,8 @@ int mfx_moe_sort(int64_t tokens, int64_t topk, int64_t experts, int64_t align, i
  * x: [tokens, cols], out: [rows, cols] of dtype dt; weight: [tokens, topk]
  * fp32 or NULL; out_weight: [rows] fp32, required iff weight.  Outputs must
  * not overlap anything else -> MFX_ERR_ALIAS.  Entries of the maps outside
- * their range count as -1 (here and below). */
+ * their range count as -1 (here and below).  With cols 0 the outputs of fp32
+ * weights are written all the same (here and below; sums over no columns are 0). */
 int mfx_moe_permute_fwd(int dt, int64_t tokens, int64_t topk, int64_t cols, int64_t rows,
                         const void* x, const int32_t* row_of, const int32_t* slot_of, const float* weight,
                         void* out, float* out_weight, void* stream);

@@ -201,6 +201,19 @@ def test_copy_validation(L):
         assert ub(*empty, None, None, None, None, None, None, None, None) == OK
 
 
+def test_copies_without_columns_need_their_maps(L):
+    """Width 0 with weights is work still to be done, so what it reads and writes has to be there."""
+    p, pb, ub = L.mfx_moe_permute_fwd, L.mfx_moe_permute_bwd, L.mfx_moe_unpermute_bwd
+    z = (1, 8, 2, 0, 16)
+    assert p(*z, None, T, None, S, None, D, None) == NULL and p(*z, None, None, M, S, None, D, None) == NULL
+    assert p(*z, None, T, M, S, None, None, None) == NULL and p(*z, None, T, M, None, None, D, None) == NULL
+    assert p(*z, None, T, M, S, None, S, None) == ALIAS and p(*z, None, T, M, S, None, M + 4, None) == ALIAS
+    assert pb(*z, None, None, S, None, D, None) == NULL and pb(*z, None, T, S, None, None, None) == NULL
+    assert pb(*z, None, T, None, None, D, None) == NULL
+    assert pb(*z, None, T, S, None, S + 4, None) == ALIAS
+    assert ub(*z, None, None, None, None, S, None, None, None) == OK
+
+
 def test_binding_refuses_what_is_not_on_the_gpu():
     x = torch.zeros(2, 4, 8, 16)
     for call in (lambda: mfx.mfx_relbias_softmax_dropout_fwd(x, 1.0),

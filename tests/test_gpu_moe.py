@@ -257,3 +257,25 @@ def test_empty():
     dy, dw = mfx.mfx_moe_unpermute_bwd(torch.randn(3, 16, device=DEV), x, row_of, slot_of,
                                        weight=torch.rand(3, 2, device=DEV))
     assert dy.shape == (0, 16) and not dw.any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_zero_width(dtype):
+    """Rows without columns still carry their weights, and a product of no
+    columns is zero: every fp32 output is written (they hold NaN before)."""
+    e = choices(37, 3, 5, seed=13)
+    row_of, slot_of, _, _ = sort(e, 5, align=8)
+    rows = slot_of.numel()
+    x, y = torch.empty(37, 0, device=DEV, dtype=dtype), torch.empty(rows, 0, device=DEV, dtype=dtype)
+    w, gw = torch.rand(37, 3, device=DEV), torch.rand(rows, device=DEV)
+    nan = lambda *s: torch.full(s, float("nan"), device=DEV)
+    has, pad = row_of >= 0, slot_of < 0
+    out, ow = mfx.mfx_moe_permute_fwd(x, row_of, slot_of, weight=w, out_weight=nan(rows))
+    assert out.shape == (rows, 0)
+    assert torch.equal(ow, w.view(-1)[slot_of.clamp(min=0).long()].masked_fill(pad, 0))
+    dx, dw = mfx.mfx_moe_permute_bwd(y, row_of, g_weight=gw, dweight=nan(37, 3))
+    assert dx.shape == (37, 0) and torch.equal(dw, gw[row_of.clamp(min=0).long()].masked_fill(~has, 0))
+    for weight in (w, None):
+        dy, dw = mfx.mfx_moe_unpermute_bwd(x, y, row_of, slot_of, weight=weight, dweight=nan(37, 3))
+        assert dy.shape == (rows, 0) and torch.equal(dw, torch.zeros_like(w))
+    assert mfx.mfx_moe_unpermute_fwd(y, row_of, weight=w).shape == (37, 0)
