@@ -301,6 +301,7 @@
 namespace mfx {
 
 constexpr int kThreadsPerBlock = 256;  // every kernel's block size
+constexpr size_t kMaxBlockSmem = 227 * 1024;  // dynamic shared memory a block may opt into
 
 // Raw bf16 storage (the library never needs bf16 arithmetic: every value is
 // widened to fp32 on load and rounded once on store).

@@ -18,7 +18,7 @@ constexpr int kLongTeam = 512;        // ... where they are
 constexpr int kSmallBlock = 128;      // threads of a block whose teams are a warp or less (and the largest of kernels for teams of part of a warp)
 constexpr int kMaxBuckets = 256;      // buckets of a table
 constexpr int kMaxSide = 128;         // buckets of one direction
-constexpr int kMaxDistance = 2048;    // keeps the window and its sums within a block's shared memory
+constexpr int kMaxDistance = 2048;    // keeps the window and one set of its sums (at most 183 KB) within a block's shared memory
 constexpr int kMaxCluster = 8;        // blocks that may share a row
 constexpr int kBwdBlocksPerSm = 16;   // most blocks of a backward grid per SM (what its workspace goes by)
 constexpr float kLog2eF = 1.4426950408889634f;

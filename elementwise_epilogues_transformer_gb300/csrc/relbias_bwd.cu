@@ -34,6 +34,7 @@ namespace relbias {
 namespace {
 
 constexpr int kWalkTeam = 2 * kLongTeam;  // kernels whose rows take several register blocks (kLongTeam threads too)
+constexpr size_t kMostDynamic = kMaxBlockSmem - 512;  // the kernel's own arrays take less than 512 bytes
 
 // Window sums: vector pair u of residue r holds the sums of entries
 // 8 u + r - 8 .. + 7; first the low halves of all pairs, then the high ones.
@@ -354,17 +355,25 @@ int64_t bwd_slices(const Args& a)
     return a.b * a.sq < most ? a.b * a.sq : most;
 }
 
+// Shared memory of a block: the window, `sets` sets of sums where the table's
+// gradient is formed, and C chunks a thread of x and, twice, of dy where rows
+// are staged.
+template <typename T, int C, bool FAST, int MT>
+size_t block_bytes(const Buckets& w, bool sums, int sets, int threads)
+{
+    return window_bytes(w) + (sums ? sum_bytes(w) * sets : 0) + (staged<T, FAST, MT>() ? (size_t)3 * C * 16 * threads : 0);
+}
+
 template <typename T, int C, bool DROP, bool MASK, bool FAST, int MT>
 int launch_bwd(Geom g, const Buckets& w, const Args& a, const void* dy, const void* x, const float* stats, void* dx,
                void* dtable, void* workspace, cudaStream_t s)
 {
     const auto kern = relbias_bwd<T, C, DROP, MASK, FAST, MT>;
-    const size_t sums = dtable ? sum_bytes(w) : 0;
-    while (g.team <= 32 && g.team * g.teams > 32 && window_bytes(w) + sums * (g.team * g.teams / 32) > 64 * 1024)
+    while (g.team <= 32 && g.team * g.teams > 32 &&
+           window_bytes(w) + (dtable ? sum_bytes(w) * (g.team * g.teams / 32) : 0) > 64 * 1024)
         g.teams /= 2;  // wide windows: fewer rows at a time
     const int threads = g.team * g.teams;
-    const size_t smem = window_bytes(w) + sums * (g.team > 32 ? 1 : threads / 32) +
-                        (staged<T, FAST, MT>() ? (size_t)3 * C * 16 * threads : 0);
+    const size_t smem = block_bytes<T, C, FAST, MT>(w, dtable != nullptr, g.team > 32 ? 1 : threads / 32, threads);
     const int64_t slots = (int64_t)sm_count() * occupancy((const void*)kern, threads, smem);
     g.slices = slices_for(g, slots, 4);
     if (g.slices > bwd_slices(a))
@@ -394,7 +403,12 @@ int dispatch_bwd(const Args& a, const Buckets& w, const void* dy, const void* x,
     // fewer lanes to a row make its near chunks take more turns, which pays
     // where a causal row leaves chunks out (64x16x128x128: 57 -> 47 us; else 35 -> 36)
     const int c = plan(g, FAST, kMost, kMost, a.causal ? 8 : 16);
-    if (g.blocks > 1)
+    // Wide windows leave staged rows of many chunks no room in a block (two
+    // directions and a distance of 2048: bf16 rows of 7176 keys and more with
+    // 256 buckets, 9224 with 128, 13320 with 64): those rows go straight into
+    // registers, as ones of several register blocks do.
+    const bool room = g.team <= 32 || block_bytes<T, kMost, FAST, kTeam>(w, dtable != nullptr, 1, g.team) <= kMostDynamic;
+    if (g.blocks > 1 || !room)
         return launch_bwd<T, kMost, DROP, MASK, FAST, kWalkTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s);
     if (g.team < 32 || c == 1) {
         if (c == 1)

@@ -333,3 +333,15 @@ def test_one_key_has_no_gradient(scale, p, dtype):
 def test_scales(scale, dtype):
     x, dy, table, m = inputs(2, 2, 7, 130, dtype, seed=21, mask="pad")
     check(x, dy, scale, table=table, mask=m, p=0.1, seed=8)
+
+
+# bf16 rows of whole chunks that come through shared memory, with windows up to
+# the widest: some leave the rows room there, some do not
+@pytest.mark.parametrize("sk", [7168, 7176, 8192, 9224, 14344, 16384])
+@pytest.mark.parametrize("buckets,far,two", [(256, 2048, True), (128, 2048, True), (64, 2048, True), (256, 1536, True),
+                                             (128, 2048, False)])
+def test_wide_windows_of_staged_rows(buckets, far, two, sk):
+    x, dy, table, m = inputs(1, 2, 3, sk, BF, seed=22, buckets=buckets, mask="heads")
+    kw = dict(table=table, max_distance=far, bidirectional=two, q_start=sk // 2)
+    check(x, dy, **kw)
+    check(x, dy, mask=m, causal=True, p=0.1, seed=9, **kw)
