@@ -100,10 +100,11 @@ __device__ __forceinline__ void put_stats(float* stats, int64_t row, float shift
     stats[3 * row] = shift, stats[3 * row + 1] = top, stats[3 * row + 2] = inv;
 }
 
-// One row whose scores all lie far from zero (a mask of lowest values, say),
-// or that has no key left: the mask is shifted by its own maximum, which
-// leaves the softmax as it is and the scores their digits.  Element by
-// element, three passes; out of line, so that it costs other rows nothing.
+// One row whose largest score lies far from zero (a mask of lowest values, say,
+// or large scores under any mask), or that has no key left: the mask is shifted
+// by its own maximum, which leaves the softmax as it is and the scores their
+// digits.  Element by element, three or four passes; out of line, so that it
+// costs other rows nothing.
 template <typename T, bool DROP, bool LONG>
 __device__ __noinline__ void shifted_row(const T* x, T* y, float* stats, const Row<T> o, const Geom& g,
                                          const Buckets& w, const float4* win, const Team& tm, int rank, int tid,
@@ -232,8 +233,10 @@ relbias_fwd(const T* x, T* y, float* __restrict__ stats, const T* __restrict__ m
             const float2 v = join_team<LONG>(team, make_float2(m, l), slot);
             m = v.x, l = v.y;
             if (MASK && mask) {
-                // far from zero, or every sum below the type's range (teams that share a warp go together)
-                bool again = fabsf(m) > 96.0f && m < INFINITY;
+                // a largest score far from zero, whether the mask or x took it there, beyond
+                // the type's range in either direction, or no key at all (teams that
+                // share a warp go together)
+                bool again = fabsf(m) > 96.0f;
                 if (ANY)
                     again = __any_sync(0xFFFFFFFFu, again);
                 if (again) {

@@ -345,3 +345,22 @@ def test_wide_windows_of_staged_rows(buckets, far, two, sk):
     kw = dict(table=table, max_distance=far, bidirectional=two, q_start=sk // 2)
     check(x, dy, **kw)
     check(x, dy, mask=m, causal=True, p=0.1, seed=9, **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("sk", [40, 300, 5000, 40000])
+def test_masks_of_any_finite_value(sk, dtype):
+    """Masks whose product with log2 e is beyond the type, up to its largest
+    and down to its lowest, are added as exactly as others; so are scores well
+    above 66 under an ordinary mask."""
+    x, dy, table, _ = inputs(1, 2, 7, sk, dtype, seed=23)
+    m = torch.zeros(1, 1, 7, sk, device=DEV, dtype=dtype)
+    m[:, :, 0] = 3e38
+    m[:, :, 1] = torch.finfo(dtype).max
+    m[:, :, 2, sk // 2:] = 3e38
+    m[:, :, 3, sk // 3] = 3e38  # next to zeros: this key alone
+    m[:, :, 4, : sk // 2], m[:, :, 4, sk // 2:] = 2.5e38, torch.finfo(dtype).min
+    m[:, :, 5, sk // 2:] = -math.inf
+    x[:, :, 5] *= 100
+    check(x, dy, table=table, mask=m)
+    check(x, dy, table=table, mask=m, causal=True, bidirectional=False, q_start=sk - 7, p=0.1, seed=2)
