@@ -771,16 +771,20 @@ def _with_workspace(name, args_before_ws, tail, device, workspace=None, sizes=No
         need = int(size.value)
         if sizes is not None:
             _workspace_bytes[(name, sizes)] = need
+    if workspace is not None:
+        if callable(workspace):
+            workspace = workspace(max(need, 16))
+        _cuda(workspace, "workspace", torch.uint8)
+        if workspace.numel() == 0:  # a null pointer would ask for the size again, and nothing would run
+            if not none or need:
+                raise MfxError(8, name)
+            workspace = None
     if workspace is None:
         if none and need == 0:
             _call(name, *args_before_ws, None, None, *tail)
             return None
         other = tail[-1] != (_raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream)
         workspace = _empty(max(need, 16), torch.uint8, device, tail[-1] if other else None)
-    else:
-        if callable(workspace):
-            workspace = workspace(max(need, 16))
-        _cuda(workspace, "workspace", torch.uint8)
     size = C.c_size_t(workspace.numel())
     _call(name, *args_before_ws, workspace.data_ptr(), C.byref(size), *tail)
     return workspace

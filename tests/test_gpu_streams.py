@@ -58,3 +58,27 @@ def test_other_stream(kind):
     torch.cuda.synchronize()
     for i, (a, b) in enumerate(zip(got, want)):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
+
+
+def test_empty_workspace():
+    """An empty workspace, whose pointer is null, is not taken for a question
+    about the size: it is refused, or does where none is needed."""
+    none = torch.empty(0, dtype=torch.uint8, device=DEV)
+    x = torch.randn(2, 3, 4, 64, device=DEV)
+    table = torch.randn(32, 3, device=DEV)
+    y, stats = mfx.mfx_relbias_softmax_dropout_fwd(x, 0.125, table=table)
+    chosen = torch.arange(8000, dtype=torch.int32, device=DEV).view(2000, 4) % 16
+    g, b = x.view(24, 64), torch.zeros(64, device=DEV)
+    for call in (lambda ws: mfx.mfx_relbias_softmax_dropout_bwd(y, x, stats, 0.125, table=table, workspace=ws),
+                 lambda ws: mfx.mfx_moe_sort(chosen, 16, workspace=ws),
+                 lambda ws: mfx.mfx_bias_gelu_bwd_dbias(g, b, g, workspace=ws),
+                 lambda ws: mfx.mfx_bias_dropout_add_bwd_dbias(g, None, 0.1, 1, workspace=ws)):
+        for ws in (none, lambda n: none):
+            with pytest.raises(mfx.MfxError) as e:
+                call(ws)
+            assert e.value.status == 8
+    few = chosen[:100].contiguous()
+    maps = [torch.full(s, -7, dtype=torch.int32, device=DEV) for s in ((100, 4), (400,), (17,), (16,))]
+    got = mfx.mfx_moe_sort(few, 16, workspace=none, **dict(zip(("row_of", "slot_of", "offsets", "counts"), maps)))
+    for a, c in zip(got, mfx.mfx_moe_sort(few, 16)):
+        assert torch.equal(a, c)
