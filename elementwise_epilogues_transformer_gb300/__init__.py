@@ -755,6 +755,7 @@ def mfx_dropout_bwd(g, p, seed, offset=0, elem_base=0, dx=None, stream=None):
 # fused bias gradients (workspace protocol: query the size, then run)
 # ---------------------------------------------------------------------------
 _workspace_bytes = {}  # (entry point, sizes) -> bytes, for calls that say which sizes theirs goes by
+_WORKSPACE_SIZES = 1024  # most of them (lengths may differ from call to call): then they are asked for anew
 
 
 def _with_workspace(name, args_before_ws, tail, device, workspace=None, sizes=None, none=False):
@@ -770,6 +771,8 @@ def _with_workspace(name, args_before_ws, tail, device, workspace=None, sizes=No
         _call(name, *args_before_ws, None, C.byref(size), *tail)
         need = int(size.value)
         if sizes is not None:
+            if len(_workspace_bytes) >= _WORKSPACE_SIZES:
+                _workspace_bytes.clear()
             _workspace_bytes[(name, sizes)] = need
     if workspace is not None:
         if callable(workspace):

@@ -223,3 +223,16 @@ def test_binding_refuses_what_is_not_on_the_gpu():
                  lambda: mfx.mfx_moe_unpermute_fwd(x[0, 0], torch.zeros(8, 2, dtype=torch.int32))):
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
+
+
+def test_workspace_sizes_kept_are_bounded(monkeypatch):
+    """Calls of ever new sizes do not make the binding grow; sizes seen lately are not asked for again."""
+    asked = []
+    monkeypatch.setattr(mfx, "_workspace_bytes", {})
+    monkeypatch.setattr(mfx, "_call", lambda name, *args: asked.append(args[0]) if args[-2] is not None else None)
+    sort = lambda n: mfx._with_workspace("mfx_moe_sort", (n,), (0,), None, sizes=(n, 8), none=True)
+    for n in range(5000):
+        sort(n)
+        sort(n)
+    assert asked == list(range(5000))
+    assert 0 < len(mfx._workspace_bytes) <= 1024
