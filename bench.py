@@ -72,6 +72,8 @@ def parse_args():
     ap.add_argument("--no-sweep", action="store_true",
                     help="skip the shape sweep (tokens x hidden, both dtypes, every op; medians of 20)")
     ap.add_argument("--sweep-reps", type=int, default=20, help="timed launches per sweep entry (median)")
+    ap.add_argument("--tables", metavar="FILE",
+                    help="write the tables whole (the result line has them in a short form)")
     return ap.parse_args()
 
 
@@ -743,6 +745,50 @@ def measured_peak():
         return 6800.0, "fallback"
 
 
+# ---------------------------------------------------------------------------
+# the result line: what reads it keeps only so much of a program's output, so
+# the line stays below this many bytes, its tables in a short form (--tables
+# writes them whole)
+# ---------------------------------------------------------------------------
+LINE_BYTES = 8192
+
+
+def short_ops(ops, keys=("gbs", "frac_measured")):
+    """{op: its figures under `keys`}."""
+    return {op: {k: v[k] for k in keys} for op, v in ops.items()}
+
+
+def short_sweep(sweep):
+    """The sweep as the result line holds it: the largest bf16 shape's ops as
+    fractions of the nominal peak, and of every cell of the grid torch's copy
+    and the slowest and fastest op (GB/s).  (--tables writes the whole of it.)"""
+    def cell(ent):
+        own = [v[0] for op, v in ent.items() if op != "torch_copy_reference"]
+        return {"torch_copy_reference": round(ent["torch_copy_reference"][0]), "ops": [round(min(own)), round(max(own))]}
+
+    return {"largest_bf16_min_frac_nominal_8tbs": sweep["largest_bf16_min_frac_nominal_8tbs"],
+            "largest": {"bf16": short_ops(sweep["largest"]["bf16"], ("frac_nominal_8tbs",))},
+            "grid": {k: cell(v) for k, v in sweep["grid"].items()}}
+
+
+def result_text(line, per_op, isolated=None, next_ops=None, sweep=None, host_cost=None, largest=None):
+    """The result line: `line` with the tables in their short forms."""
+    line = {**line, "per_op": short_ops(per_op, ("ms", "gbs", "frac_measured"))}
+    if isolated:
+        line["per_op_isolated"] = short_ops(isolated, ("frac_measured",))
+    if next_ops:
+        line["next_per_op"] = short_ops(next_ops)
+    if sweep:
+        line["sweep"] = short_sweep(sweep)
+    if host_cost:
+        line["host_call_cost"] = host_cost
+    if largest:
+        line["largest_per_op"] = {"config": f"{LARGEST['rows']} x {LARGEST['width']} (GLU: F = {LARGEST['width']}, "
+                                            "input 2F wide)",
+                                  **short_ops(largest, ("gbs", "frac_measured", "frac_nominal_8tbs"))}
+    return json.dumps(line, separators=(",", ":"))
+
+
 def run_reference(args, world, rank):
     """The oracle as the reference arm: rank 0 only."""
     if rank != 0:
@@ -896,21 +942,14 @@ def main():
                            **({"rows_scale": ROWS_SCALE} if ROWS_SCALE != 1.0 else {})},
                 "frac_of_measured_peak": round(value / world / peak, 4),
                 "frac_of_nominal_8tbs": round(value / world / NOMINAL_HBM_GBS, 4),
-                "elements_per_s": world * elems * args.steps / (total_ms * 1e-3),
+                "elements_per_s": round(world * elems * args.steps / (total_ms * 1e-3)),
                 "roofline": roofline, "cpu_baseline": cpu, "e2e": e2e,
-                "gpu_launches": len(ops) * args.steps, "clocks": clocks, "per_op": per_op}
-        if isolated:
-            line["per_op_isolated"] = isolated
-        if next_ops:
-            line["next_per_op"] = next_ops
-        if sweep:
-            line["sweep"] = sweep
-        if host_cost:
-            line["host_call_cost"] = host_cost
-        if largest:
-            line["largest_per_op"] = {"config": f"{LARGEST['rows']} x {LARGEST['width']} (GLU: F = "
-                                                f"{LARGEST['width']}, input 2F wide)", **largest}
-        print(json.dumps(line), flush=True)
+                "gpu_launches": len(ops) * args.steps, "clocks": clocks}
+        if args.tables:
+            with open(args.tables, "w") as f:
+                json.dump({"per_op": per_op, "per_op_isolated": isolated, "next_per_op": next_ops, "sweep": sweep,
+                           "largest_per_op": largest}, f, indent=1)
+        print(result_text(line, per_op, isolated, next_ops, sweep, host_cost, largest), flush=True)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()

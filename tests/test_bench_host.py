@@ -55,3 +55,28 @@ def test_misalign_offsets_by_one_element(dtype):
     m = bench.misalign(t)
     assert torch.equal(m, t) and m.shape == t.shape
     assert (m.data_ptr() - m.untyped_storage().data_ptr()) == m.element_size()
+
+
+def test_result_line_is_short_enough_to_be_read_back():
+    """A line with every table of a default run, the figures as wide as they
+    get, stays below its limit and keeps its keys."""
+    ops = lambda names: {n: {"ms": 123.4567, "ms_median": 123.4567, "gbs": 12345.6, "frac_measured": 1.2345,
+                             "frac_nominal_8tbs": 1.2345, "elems_per_s": 1234567890123.4567, "bytes": 12345678901,
+                             "l2": "flushed"} for n in names}
+    beyond = [f"scaled_upper_triang_softmax_{i:02d}" for i in range(14)]
+    family = STEP_OPS[:8] + [f"bias_dropout_add_train(p=0.{i},res=fp32)" for i in range(6)] + ["torch_copy_reference"]
+    entry = ops(family)
+    cells = [f"{d} T={t} H={h}" for d in ("bf16", "fp32") for t in (512, 4096, 32768, 65536)
+             for h in (1024, 4096, 4099, 8192, 16384)]
+    sweep = {"config": "c" * 600, "largest_bf16_min_frac_nominal_8tbs": 0.8192, "largest_bf16_min_frac_measured": 0.9786,
+             "largest": {"bf16": entry, "fp32": entry}, "special": {"s" * 60 + str(i): entry for i in range(7)},
+             "grid": {c: {o: [v["gbs"], v["frac_measured"]] for o, v in entry.items()} for c in cells},
+             "grid_columns": ["GB/s", "fraction of the measured copy peak"]}
+    head = {"metric": bench.METRIC, "value": 6644.4, "unit": "GB/s", "config": {"workload": bench.WORKLOAD},
+            "cpu_baseline": {"sample": ", ".join(f"{o}:12345rows" for o in STEP_OPS)}, "rest": "r" * 1100}
+    text = bench.result_text(head, ops(STEP_OPS), ops(STEP_OPS), ops(beyond), sweep, {"workload": "w" * 220})
+    assert len(text) <= bench.LINE_BYTES and "\n" not in text
+    d = json.loads(text)
+    assert d["value"] == 6644.4 and list(d["per_op"]) == STEP_OPS and len(d["next_per_op"]) == 14
+    assert set(d["sweep"]["grid"]) == set(cells)
+    assert d["sweep"]["grid"][cells[0]] == {"torch_copy_reference": 12346, "ops": [12346, 12346]}

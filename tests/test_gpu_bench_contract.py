@@ -49,3 +49,19 @@ def test_bench_json_line():
         host_us, dev_us = hc[k]
         assert 0 < dev_us <= host_us * 1.05 + 0.5
     assert 0 < hc["cuda_graph_replay_device_us"] < hc["c_abi_us"][1] * 2
+
+
+def test_result_line_length_and_tables(tmp_path):
+    """The line is short enough to be read back; --tables writes what it leaves out."""
+    sys.path.insert(0, ROOT)
+    import bench
+    path = tmp_path / "tables.json"
+    r = subprocess.run([sys.executable, "bench.py", "--steps", "3", "--warmup", "3", "--e2e-steps", "1",
+                        "--cpu-seconds", "1", "--sweep-reps", "3", "--tables", str(path)], cwd=ROOT,
+                       capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stderr[-2000:]
+    line, = [l for l in r.stdout.splitlines() if l.startswith("{")]
+    assert len(line) <= bench.LINE_BYTES
+    d, t = json.loads(line), json.loads(path.read_text())
+    assert set(t["per_op"]) == set(d["per_op"]) and all(v["bytes"] > 0 for v in t["per_op"].values())
+    assert set(t["sweep"]["grid"]) == set(d["sweep"]["grid"]) and len(t["sweep"]["special"]) == 7
