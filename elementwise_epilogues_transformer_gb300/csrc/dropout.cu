@@ -452,8 +452,9 @@ bda_generic(const TX* x, const TX* __restrict__ bias, const TR* __restrict__ res
 // Backward (NEXT row f1): dx = keep ? g * scale : 0 in x's dtype, and
 // optionally dres = g in the residual's dtype.  No column dependence, so the
 // grid is a plain persistent one.  The mask is read from the forward's
-// output (8 bytes per unit, streamed through the ring with g) or
-// regenerated from Philox exactly as the forward drew it (no mask traffic).
+// output (8 bytes per unit, streamed through the ring with g) or, with the
+// bias gradient, regenerated from Philox exactly as the forward drew it (no
+// mask traffic; without that gradient drop_flat below does so).
 // ---------------------------------------------------------------------------
 template <typename TX, bool MASK, bool PACKED = false>
 struct BwdPipe {
@@ -505,14 +506,10 @@ __device__ __forceinline__ void store_dres_warp(float* dres, int64_t ubw, int64_
 // Output slots of the bulk-store form: per consumer warp MFX_BDA_BWD_SLOTS
 // slots, each the warp's 32 units of dx then of dres; a warp fills one while
 // the copy engine still reads the others.  The form serves the byte-mask
-// backward alone: at the D2 layer shape it lifts that kernel from 0.86 to
-// 0.90 of the copy peak, where the regenerated-mask form (more ALU work per
-// unit, two blocks per SM needed) fell from 0.84 to 0.81 and the bit-mask
-// form gained nothing.
-constexpr bool bwd_bulk_stores(bool regen, bool db, bool packed)
-{
-    return MFX_BDA_BWD_BULK_ST && !regen && !db && !packed;
-}
+// backward without a bias gradient alone: at the D2 layer shape it lifts that
+// kernel from 0.86 to 0.90 of the copy peak, where the bit-mask form gained
+// nothing.
+constexpr bool bwd_bulk_stores(bool db, bool packed) { return MFX_BDA_BWD_BULK_ST && !db && !packed; }
 template <typename TX, typename TR>
 struct BwdOut {
     static constexpr uint32_t kDx = 32 * 8 * sizeof(TX), kDr = 32 * 8 * sizeof(TR);
@@ -553,12 +550,13 @@ bda_bwd_pipe(const TX* g, const uint8_t* __restrict__ keep, TX* dx, TR* dres, in
              uint32_t thresh, uint64_t seed, uint64_t offset, uint64_t block_base, int64_t cols = 0,
              float* __restrict__ ws = nullptr)
 {
+    static_assert(DB || !REGEN, "a regenerated mask without a bias gradient is drop_flat's");
     using P = BwdPipe<TX, !REGEN, PACKED>;
     using BO = BwdOut<TX, TR>;
     constexpr int U = P::kU, NS = P::kStages;
     // byte mask read: outputs by bulk stores out of per-warp slots (after
     // the ring); the other forms measured faster with register stores
-    constexpr bool kBulk = bwd_bulk_stores(REGEN, DB, PACKED);
+    constexpr bool kBulk = bwd_bulk_stores(DB, PACKED);
     extern __shared__ __align__(128) unsigned char smem[];
     const Ring ring = ring_setup<NS>(smem);
     unsigned char* data = smem + kRingHeader;
@@ -907,7 +905,7 @@ int launch_bwd(const void* g, const uint8_t* keep, void* dx, void* dres, int64_t
         return launch_flat<TX, TR>(gp, dxp, drp, n, scale, thresh, seed, offset, elem_base, s);
     if (MFX_PIPE_BDA && n % 8 == 0 && aligned16(g) && aligned16(dx) && (!dres || aligned16(dres)) && aligned16(keep)) {
         const int64_t units = n / 8;
-        constexpr size_t kOut = bwd_bulk_stores(false, false, PACKED) ? BwdOut<TX, TR>::kBytes : 0;
+        constexpr size_t kOut = bwd_bulk_stores(false, PACKED) ? BwdOut<TX, TR>::kBytes : 0;
         constexpr size_t smem = BwdPipe<TX, true, PACKED>::kSmem + kOut;
         static_assert(smem <= kMaxBlockSmem, "ring and output slots do not fit in a block's shared memory");
         const Grid grid =
