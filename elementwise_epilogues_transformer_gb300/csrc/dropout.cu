@@ -758,16 +758,24 @@ bda_bwd_generic(const TX* g, const uint8_t* keep, TX* dx, TR* dres, int64_t n, f
 // elements that do not begin on a generator block (PHASED) a unit needs its
 // block and the next one, which is the block of the lane above: lane 0 hands
 // its next unit's to lane 31, and only the warp's last block is drawn twice.
-// The next turn's loads go out before this turn's work.  Measured against
-// the ring that the stored-mask backward uses, bf16 32768 x 4099: 90 against
-// 96 us (113 against 253 us at an odd offset, where the ring did not apply);
-// without the early loads 96 us, with two or eight units a lane 98 and 94 us.
+// The next turn's loads go out before this turn's work.
+// Unit 0 begins where dx is 16-byte aligned; the elements before it (`head`)
+// are one thread's each.  Where g or dres is not aligned there (ANY), a unit
+// of g is read as the vectors that cover it, and dres is written from units of
+// its own, `shift` elements further on: 16384 x 4096, an element off a vector
+// and at an odd offset, bf16 127 -> 56 us and fp32 164 -> 85 us (element by
+// element a unit's accesses are 32 bytes apart in a warp).
+// Measured against the ring that the stored-mask backward uses, bf16 32768 x
+// 4099: 90 against 96 us (113 against 253 us at an odd offset, where the ring
+// did not apply); without the early loads 96 us, with two or eight units a lane
+// 98 and 94 us.
 // ---------------------------------------------------------------------------
 struct FlatDrop {
     int64_t n;
     uint64_t block0;  // generator block of unit 0
-    int phase;        // element 0's word in it
-    int vec;          // 16-byte aligned: g and dx (1), dres (2); 32-byte aligned fp32: g and dx (4), dres (8)
+    int phase;        // its first element's word in it
+    int head, shift;  // elements before unit 0; before dres's first vector from there (ANY)
+    int vec;          // 32-byte aligned fp32: g and dx (4), dres (8)
     float scale;
     uint32_t thresh_hi;
     MaskGen gen;
@@ -794,20 +802,48 @@ __device__ __forceinline__ void flat_store(T* p, bool wide, const Raw8<T>& r)
     st8(p, r);
 }
 
-template <typename TX, typename TR, int U, bool PHASED>
-__global__ void __launch_bounds__(kThreads, U > 1 ? 3 : 6)
+template <typename TX, typename TR, int U, bool PHASED, bool ANY>
+__global__ void __launch_bounds__(kThreads, U > 1 ? 3 : PHASED ? 4 : 6)
 drop_flat(const TX* g, TX* dx, TR* dres, const __grid_constant__ FlatDrop d)
 {
     const int lane = threadIdx.x & 31;
     const int64_t units = (d.n + 7) / 8, whole = d.n / 8;
     const int64_t step = (int64_t)gridDim.x * (kThreads * U);
     Raw8<TX> ahead[U];
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(g - d.head), hi = reinterpret_cast<uintptr_t>(g + d.n);
+    const auto load_any = [&](const TX* p, Raw8<TX>& r) {
+        if (in_vectors(p, lo, hi)) {
+            ld8_any(p, r);
+        } else {
+            float f[8];
+            load8f(p, false, 8, f);
+            narrow8(f, r);
+        }
+    };
     const auto load = [&](int64_t first) {
 #pragma unroll
-        for (int k = 0; k < U; ++k)
-            if ((d.vec & 1) && first + lane + 32 * k < whole)
-                flat_load(g + (first + lane + 32 * k) * 8, d.vec, ahead[k]);
+        for (int k = 0; k < U; ++k) {
+            const int64_t u = first + lane + 32 * k;
+            if (u < whole) {
+                if constexpr (ANY)
+                    load_any(g + u * 8, ahead[k]);
+                else
+                    flat_load(g + u * 8, d.vec, ahead[k]);
+            }
+        }
     };
+    if (ANY && dres && blockIdx.x == 0 && (int)threadIdx.x < d.shift && threadIdx.x < d.n)
+        store1(dres + threadIdx.x, load1(g + threadIdx.x));
+    if (blockIdx.x == 0 && (int)threadIdx.x < d.head) {
+        const int64_t i = (int64_t)threadIdx.x - d.head;
+        const uint64_t e = d.block0 * 8 + (uint64_t)(d.phase + i);
+        uint4 b[1];
+        mask_blocks<1>(d.gen, e >> 3, 0, b);
+        const float f = load1(g + i);
+        store1(dx + i, word16(b[0], (int)(e & 7u)) >= d.thresh_hi >> 16 ? __fmul_rn(f, d.scale) : 0.0f);
+        if (dres)
+            store1(dres + i, f);
+    }
     int64_t first = ((int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31)) * U;
     if (first < units)
         load(first);
@@ -835,7 +871,7 @@ drop_flat(const TX* g, TX* dx, TR* dres, const __grid_constant__ FlatDrop d)
             if (u >= units)
                 continue;
             const int cnt = u < whole ? 8 : (int)(d.n - i0);
-            const bool vec = (d.vec & 1) && cnt == 8;
+            const bool vec = cnt == 8;
             float f[8], v[8];
             if (vec)
                 widen8(r[k], f);
@@ -854,12 +890,22 @@ drop_flat(const TX* g, TX* dx, TR* dres, const __grid_constant__ FlatDrop d)
                 store8f(dx + i0, false, cnt, v);
             }
             if (dres) {
-                if ((d.vec & 2) && cnt == 8) {
+                const int64_t j0 = ANY ? i0 + d.shift : i0;
+                const int left = ANY ? (d.n - j0 < 8 ? (int)(d.n - j0) : 8) : cnt;
+                if (ANY && d.shift && left > 0) {
+                    if (left == 8) {
+                        load_any(g + j0, r[k]);
+                        widen8(r[k], f);
+                    } else {
+                        load8f(g + j0, false, left, f);
+                    }
+                }
+                if (left == 8) {
                     Raw8<TR> o;
                     narrow8(f, o);
-                    flat_store(dres + i0, d.vec & 8, o);
+                    flat_store(dres + j0, d.vec & 8, o);
                 } else {
-                    store8f(dres + i0, false, cnt, f);
+                    store8f(dres + j0, false, left, f);
                 }
             }
         }
@@ -872,12 +918,16 @@ template <typename TX, typename TR>
 int launch_flat(const TX* g, TX* dx, TR* dres, int64_t n, float scale, uint32_t thresh, uint64_t seed,
                 uint64_t offset, uint64_t elem_base, cudaStream_t s)
 {
+    const int to_vector = (int)((0 - reinterpret_cast<uintptr_t>(dx) & 15u) / sizeof(TX));
     FlatDrop d = {};
-    d.n = n, d.block0 = elem_base / 8, d.phase = (int)(elem_base % 8), d.scale = scale, d.thresh_hi = thresh << 16;
-    d.vec = (aligned16(g) && aligned16(dx) ? 1 : 0) | (aligned16(dres) ? 2 : 0) |
-            (sizeof(TX) == 4 && aligned32(g) && aligned32(dx) ? 4 : 0) | (sizeof(TR) == 4 && aligned32(dres) ? 8 : 0);
+    d.head = to_vector < n ? to_vector : (int)n;
+    g += d.head, dx += d.head, dres = dres ? dres + d.head : dres;
+    d.n = n - d.head, d.scale = scale, d.thresh_hi = thresh << 16;
+    d.block0 = (elem_base + d.head) / 8, d.phase = (int)((elem_base + d.head) % 8);
+    d.shift = (int)((0 - reinterpret_cast<uintptr_t>(dres) & 15u) / sizeof(TR));
+    d.vec = (sizeof(TX) == 4 && aligned32(g) && aligned32(dx) ? 4 : 0) | (sizeof(TR) == 4 && aligned32(dres) ? 8 : 0);
     d.gen = make_mask_gen(seed, offset);
-    const int64_t units = (n + 7) / 8;
+    const int64_t units = d.n > 0 ? (d.n + 7) / 8 : 1;
     const auto go = [&](auto kern, int u) {
         const int64_t need = (units + kThreads * u - 1) / (kThreads * u);
         const int64_t most = (int64_t)sm_count() * blocks_per_sm((const void*)kern);
@@ -886,9 +936,12 @@ int launch_flat(const TX* g, TX* dx, TR* dres, int64_t n, float scale, uint32_t 
     };
     // several units a lane where that still gives every SM two blocks
     constexpr int U = sizeof(TX) == 2 ? 4 : 2;
-    if (units >= (int64_t)sm_count() * 2 * kThreads * U)
-        return d.phase ? go(drop_flat<TX, TR, U, true>, U) : go(drop_flat<TX, TR, U, false>, U);
-    return d.phase ? go(drop_flat<TX, TR, 1, true>, 1) : go(drop_flat<TX, TR, 1, false>, 1);
+    const bool many = units >= (int64_t)sm_count() * 2 * kThreads * U;
+    if (!aligned16(g) || !aligned16(dres))
+        return many ? go(drop_flat<TX, TR, U, true, true>, U) : go(drop_flat<TX, TR, 1, true, true>, 1);
+    if (many)
+        return d.phase ? go(drop_flat<TX, TR, U, true, false>, U) : go(drop_flat<TX, TR, U, false, false>, U);
+    return d.phase ? go(drop_flat<TX, TR, 1, true, false>, 1) : go(drop_flat<TX, TR, 1, false, false>, 1);
 }
 
 template <typename TX, typename TR, bool PACKED = false>

@@ -102,3 +102,40 @@ def test_graph_and_stream():
         mfx.mfx_dropout_fwd(x, 0.1, 4, out=out)
     g.replay()
     assert torch.equal(out, want)
+
+
+# several units a lane (from 1.2 million fp32 or 2.5 million bf16 elements on), and one beside it
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [5, 4099, 1_000_003, 3_100_005])
+@pytest.mark.parametrize("base", [0, 5, 12345678901])
+def test_every_alignment(n, base, dtype):
+    """Input and output any number of elements off a vector, alike or not, at
+    element offsets on and off a generator block."""
+    x = torch.randn(n, generator=torch.Generator().manual_seed(n)).to(dtype).to(DEV)
+    p = 0.25
+    scale = torch.tensor(1.0) / (torch.tensor(1.0) - torch.tensor(p))
+    want = torch.where(flags(n, p, 77, 5, base).to(DEV), (x.float() * scale.to(DEV)).to(dtype), torch.zeros_like(x))
+    for a in (0, 1, 3, 4, 7):
+        v = shifted(x, a)
+        for b in (0, 1, 4, 6):
+            out = shifted(torch.full_like(x, float("nan")), b)
+            assert torch.equal(mfx.mfx_dropout_fwd(v, p, 77, 5, base, out=out), want), (a, b)
+        assert torch.equal(mfx.mfx_dropout_bwd(v, p, 77, 5, base, dx=v), want), a
+
+
+@pytest.mark.parametrize("dtype,res", [(BF, F32), (BF, BF), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("rows,cols", [(7, 333), (1033, 3001), (1024, 4096)])
+@pytest.mark.parametrize("base", [0, 5])
+def test_regenerated_backward_at_every_alignment(rows, cols, base, dtype, res):
+    """dx and dresidual are the bits of the backward that reads the mask."""
+    g = torch.Generator().manual_seed(rows)
+    x, up = (torch.randn(rows, cols, generator=g).to(dtype).to(DEV) for _ in range(2))
+    key = (0.25, 99, 3, base)
+    _, mask = mfx.mfx_bias_dropout_add_train(x, None, x, *key)
+    want = mfx.mfx_bias_dropout_add_bwd(up, mask, *key, residual_dtype=res)
+    for a, b, c in ((0, 0, 0), (1, 1, 1), (1, 0, 0), (0, 3, 1), (4, 4, 4), (5, 2, 0), (0, 0, 2)):
+        dx = shifted(torch.full_like(up, float("nan")), b)
+        dres = shifted(torch.full((rows, cols), float("nan"), dtype=res, device=DEV), c)
+        got = mfx.mfx_bias_dropout_add_bwd(shifted(up, a), None, *key, dx=dx, dresidual=dres)
+        for i in range(2):
+            assert torch.equal(got[i], want[i]), (a, b, c, i)
