@@ -482,7 +482,7 @@ def mfx_relbias_softmax_dropout_bwd(dy, x, stats, scale, table=None, mask=None, 
         _call("mfx_relbias_softmax_dropout_bwd", *head, None, None, st)
     else:
         _with_workspace("mfx_relbias_softmax_dropout_bwd", head, (st,), x.device, workspace,
-                        (x.get_device(), *shape, table.shape[0]))
+                        (x.get_device(), *shape, table.shape[0]), stream=stream)
     return dx, dtable
 
 
@@ -515,7 +515,7 @@ def mfx_moe_sort(expert_of, experts, align=1, capacity=0, rows=None, row_of=None
     offsets, counts = new(offsets, "offsets", (max(experts, 0) + 1,)), new(counts, "counts", (max(experts, 0),))
     _with_workspace("mfx_moe_sort", (tokens, topk, experts, align, capacity, rows, expert_of.data_ptr(),
                                      row_of.data_ptr(), slot_of.data_ptr(), offsets.data_ptr(), counts.data_ptr()),
-                    (_stream(stream, expert_of),), expert_of.device, workspace, (slots, experts), none=True)
+                    (_stream(stream, expert_of),), expert_of.device, workspace, (slots, experts), none=True, stream=stream)
     return row_of, slot_of, offsets, counts
 
 
@@ -758,11 +758,11 @@ _workspace_bytes = {}  # (entry point, sizes) -> bytes, for calls that say which
 _WORKSPACE_SIZES = 1024  # most of them (lengths may differ from call to call): then they are asked for anew
 
 
-def _with_workspace(name, args_before_ws, tail, device, workspace=None, sizes=None, none=False):
+def _with_workspace(name, args_before_ws, tail, device, workspace=None, sizes=None, none=False, stream=None):
     """Query the workspace size, allocate it and run `name`.  `workspace` is
-    None (a fresh uint8 tensor of the call's stream, the last of tail), a
-    uint8 CUDA tensor, or a callable that takes the byte count and returns
-    one (a caller's own allocator).
+    None (a fresh uint8 tensor of the call's stream, `stream` as its caller
+    gave it), a uint8 CUDA tensor, or a callable that takes the byte count and
+    returns one (a caller's own allocator).
     `sizes`: what the workspace's size depends on, so that it is asked for
     once; `none`: a call whose workspace is empty takes none."""
     need = _workspace_bytes.get((name, sizes)) if sizes is not None else None
@@ -786,8 +786,7 @@ def _with_workspace(name, args_before_ws, tail, device, workspace=None, sizes=No
         if none and need == 0:
             _call(name, *args_before_ws, None, None, *tail)
             return None
-        other = tail[-1] != (_raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream)
-        workspace = _empty(max(need, 16), torch.uint8, device, tail[-1] if other else None)
+        workspace = _empty(max(need, 16), torch.uint8, device, stream)
     size = C.c_size_t(workspace.numel())
     _call(name, *args_before_ws, workspace.data_ptr(), C.byref(size), *tail)
     return workspace
@@ -804,7 +803,7 @@ def mfx_bias_gelu_bwd_dbias(g, bias, y, dy=None, dbias=None, workspace=None, str
     st = _stream(stream, y)
     _with_workspace("mfx_bias_gelu_bwd_dbias",
                     (dtype_code(y.dtype), rows, cols, _ptr(g), _ptr(bias), _ptr(y), _ptr(dy), _ptr(dbias)),
-                    (st,), y.device, workspace)
+                    (st,), y.device, workspace, stream=stream)
     return dy, dbias
 
 
@@ -833,7 +832,7 @@ def mfx_bias_geglu_bwd_dbias(g, x, bias, dx=None, dbias=None, workspace=None, st
     dbias = x.new_empty((2 * F,)) if dbias is None else _cuda(dbias, "dbias", x.dtype)
     _with_workspace("mfx_bias_geglu_bwd_dbias",
                     (dtype_code(x.dtype), rows, F, _ptr(g), _ptr(x), _ptr(bias), _ptr(dx), _ptr(dbias)),
-                    (_stream(stream, x),), x.device, workspace)
+                    (_stream(stream, x),), x.device, workspace, stream=stream)
     return dx, dbias
 
 
@@ -852,7 +851,7 @@ def mfx_bias_swiglu_bwd_dbias(g, x, bias, weight=None, dx=None, dweight=None, db
     dbias = x.new_empty((2 * F,)) if dbias is None else _cuda(dbias, "dbias", x.dtype)
     _with_workspace("mfx_bias_swiglu_bwd_dbias",
                     (dtype_code(x.dtype), rows, F, _ptr(g), _ptr(x), _ptr(bias), _ptr(weight), _ptr(dx),
-                     _ptr(dweight), _ptr(dbias)), (_stream(stream, x),), x.device, workspace)
+                     _ptr(dweight), _ptr(dbias)), (_stream(stream, x),), x.device, workspace, stream=stream)
     return dx, dweight, dbias
 
 
@@ -873,5 +872,5 @@ def mfx_bias_dropout_add_bwd_dbias(g, keep_mask, p, seed=0, offset=0, elem_base=
     _with_workspace("mfx_bias_dropout_add_bwd_dbias",
                     (dtype_code(g.dtype), rdt, rows, cols, _ptr(g), _ptr(keep_mask), float(p),
                      int(seed) % 2**64, int(offset) % 2**64, int(elem_base), _ptr(dx), _ptr(dresidual),
-                     _ptr(dbias)), (_stream(stream, g),), g.device, workspace)
+                     _ptr(dbias)), (_stream(stream, g),), g.device, workspace, stream=stream)
     return dx, dresidual, dbias
