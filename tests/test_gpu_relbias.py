@@ -364,3 +364,30 @@ def test_masks_of_any_finite_value(sk, dtype):
     x[:, :, 5] *= 100
     check(x, dy, table=table, mask=m)
     check(x, dy, table=table, mask=m, causal=True, bidirectional=False, q_start=sk - 7, p=0.1, seed=2)
+
+
+# Sizes at which a team works on several rows one after another (more rows than
+# the GPU holds teams): 8 or 16 lanes, a warp, several warps, long rows and rows
+# of several register blocks; whole and ragged ones; sq no multiple of a step.
+# (Per window sum that is at most 64 rows of up to 4 chunks.)
+WALKS = [(2, 8, 2101, 40), (3, 8, 1333, 37), (2, 8, 1103, 264), (2, 6, 701, 515), (2, 4, 515, 1032), (3, 2, 333, 2051),
+         (2, 4, 101, 9000), (2, 2, 151, 20008)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("size", WALKS)
+def test_several_rows_a_team(size, dtype):
+    b, np_, sq, sk = size
+    x, dy, table, m = inputs(*size, dtype, seed=sk, mask="pad")
+    check(x, dy, table=table, q_start=sk // 3)
+    check(x, dy, table=table, mask=m, causal=True, bidirectional=False, q_start=sk - sq // 2, p=0.1, seed=3)
+    starts = torch.tensor([7 * i - 3 for i in range(b)], dtype=torch.int32, device=DEV)
+    y, _, dx, dt = run_both(x, dy, table=table, seq_start=starts, q_start=sk // 2, p=0.25, seed=4)
+    for i in range(b):  # each batch alone, at its own position and elements
+        kw = dict(table=table, q_start=sk // 2 + 7 * i - 3, p=0.25, seed=4, elem_base=i * np_ * sq * sk)
+        yi, _, dxi, _ = run_both(x[i:i + 1].clone(), dy[i:i + 1].clone(), **kw)
+        ry, ty, rdx, tdx, _, _ = reference(x[i:i + 1], 0.125, dy=dy[i:i + 1], **kw)
+        for got in (y[i:i + 1], yi):
+            close(got, ry, ty, "y")
+        for got in (dx[i:i + 1], dxi):
+            close(got, rdx, tdx, "dx")
