@@ -436,8 +436,9 @@ def _relbias_args(x, table, mask, max_distance, bidirectional, causal, q_start, 
         _like(seq_start, "seq_start", (b,), torch.int32)
         _same_device(seq_start, dev, "seq_start")
         sptr = seq_start.data_ptr()
-    return shape, (tdt, tptr, buckets, max_distance, 1 if bidirectional else 0, mptr, mb, mnp, msq, 1 if causal else 0,
-                   q_start, sptr, p, seed % 2**64, offset % 2**64, elem_base)
+    return shape, (tdt, tptr, buckets, int(max_distance), 1 if bidirectional else 0, mptr, mb, mnp, msq,
+                   1 if causal else 0, int(q_start), sptr, float(p), int(seed) % 2**64, int(offset) % 2**64,
+                   int(elem_base))
 
 
 def mfx_relbias_softmax_dropout_fwd(x, scale, table=None, mask=None, max_distance=128, bidirectional=True,
@@ -454,8 +455,8 @@ def mfx_relbias_softmax_dropout_fwd(x, scale, table=None, mask=None, max_distanc
         _like(stats, "stats", (*shape[:3], 3), torch.float32)
     elif need_stats:
         stats = _empty((*shape[:3], 3), torch.float32, x.device, stream)
-    _call("mfx_relbias_softmax_dropout_fwd", dtype_code(x.dtype), *shape, x.data_ptr(), scale, *shared, y.data_ptr(),
-          _ptr(stats), _stream(stream, x))
+    _call("mfx_relbias_softmax_dropout_fwd", dtype_code(x.dtype), *shape, x.data_ptr(), float(scale), *shared,
+          y.data_ptr(), _ptr(stats), _stream(stream, x))
     return y, stats
 
 
@@ -475,8 +476,8 @@ def mfx_relbias_softmax_dropout_bwd(dy, x, stats, scale, table=None, mask=None, 
         _like(dtable, "dtable", table.shape, table.dtype)
     elif table is not None and need_dtable:
         dtable = _empty_like(table, stream)
-    head = (dtype_code(x.dtype), *shape, dy.data_ptr(), x.data_ptr(), stats.data_ptr(), scale, *shared, dx.data_ptr(),
-            _ptr(dtable))
+    head = (dtype_code(x.dtype), *shape, dy.data_ptr(), x.data_ptr(), stats.data_ptr(), float(scale), *shared,
+            dx.data_ptr(), _ptr(dtable))
     st = _stream(stream, x)
     if dtable is None:
         _call("mfx_relbias_softmax_dropout_bwd", *head, None, None, st)
@@ -491,7 +492,7 @@ def mfx_relbias_softmax_dropout_bwd(dy, x, stats, scale, table=None, mask=None, 
 # ---------------------------------------------------------------------------
 def mfx_moe_rows(tokens, topk, experts, align=1):
     """Rows that the sorted layout of tokens x topk slots needs at most."""
-    n = lib().mfx_moe_rows(tokens, topk, experts, align)
+    n = lib().mfx_moe_rows(int(tokens), int(topk), int(experts), int(align))
     if n < 0:
         raise MfxError(2, "mfx_moe_rows")
     return n
@@ -506,7 +507,10 @@ def mfx_moe_sort(expert_of, experts, align=1, capacity=0, rows=None, row_of=None
     if expert_of.dim() != 2:
         raise ValueError("expert_of must have the shape [tokens, topk]")
     tokens, topk = expert_of.shape
-    if rows is None:
+    experts, align, capacity = int(experts), int(align), int(capacity)
+    if rows is not None:
+        rows = int(rows)
+    else:
         rows = slot_of.numel() if slot_of is not None else mfx_moe_rows(tokens, topk, experts, align)
     slots = tokens * topk
     new = lambda t, name, shape: (_empty(shape, torch.int32, expert_of.device, stream) if t is None  # noqa: E731

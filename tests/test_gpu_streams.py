@@ -1,5 +1,6 @@
 """Calls on another stream than the current one: what they allocate for
 themselves must not be given to the current stream while they have yet to run."""
+import numpy as np
 import pytest
 import torch
 
@@ -82,3 +83,24 @@ def test_empty_workspace():
     got = mfx.mfx_moe_sort(few, 16, workspace=none, **dict(zip(("row_of", "slot_of", "offsets", "counts"), maps)))
     for a, c in zip(got, mfx.mfx_moe_sort(few, 16)):
         assert torch.equal(a, c)
+
+
+def test_numbers_of_other_kinds():
+    """Scalars from numpy and 0-dim tensors count as the numbers that they are, as in the other calls."""
+    x = torch.randn(2, 3, 4, 64, device=DEV)
+    table = torch.randn(32, 3, device=DEV)
+    kw = dict(table=table, max_distance=100, q_start=20, p=0.25, seed=2**63 + 5, offset=3, elem_base=8)
+    i, f = np.int64, np.float64
+    other = dict(table=table, max_distance=i(100), q_start=i(20), p=f(0.25), seed=np.uint64(2**63 + 5), offset=i(3),
+                 elem_base=torch.tensor(8))
+    y, stats = mfx.mfx_relbias_softmax_dropout_fwd(x, 0.125, **kw)
+    y2, stats2 = mfx.mfx_relbias_softmax_dropout_fwd(x, torch.tensor(0.125), **other)
+    assert torch.equal(y, y2) and torch.equal(stats, stats2)
+    for a, b in zip(mfx.mfx_relbias_softmax_dropout_bwd(y, x, stats, 0.125, **kw),
+                    mfx.mfx_relbias_softmax_dropout_bwd(y, x, stats, np.float32(0.125), **other)):
+        assert torch.equal(a, b)
+    chosen = torch.arange(400, dtype=torch.int32, device=DEV).view(100, 4) % 16
+    for a, b in zip(mfx.mfx_moe_sort(chosen, 16, align=8, capacity=20, rows=600),
+                    mfx.mfx_moe_sort(chosen, torch.tensor(16), align=i(8), capacity=i(20), rows=i(600))):
+        assert torch.equal(a, b)
+    assert mfx.mfx_moe_rows(i(10), i(2), i(4), i(16)) == 80
