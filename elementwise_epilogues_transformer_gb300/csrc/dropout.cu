@@ -766,7 +766,7 @@ bda_bwd_generic(const TX* g, const uint8_t* keep, TX* dx, TR* dres, int64_t n, f
 // and at an odd offset, bf16 127 -> 56 us and fp32 164 -> 85 us (element by
 // element a unit's accesses are 32 bytes apart in a warp).
 // Measured against the ring that the stored-mask backward uses, bf16 32768 x
-// 4099: 90 against 96 us (113 against 253 us at an odd offset, where the ring
+// 4099: 88 against 96 us (107 against 253 us at an odd offset, where the ring
 // did not apply); without the early loads 96 us, with two or eight units a lane
 // 98 and 94 us.
 // ---------------------------------------------------------------------------

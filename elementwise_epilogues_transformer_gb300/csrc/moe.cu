@@ -19,11 +19,17 @@
 // same bits on every run.
 //
 // What bounds them: HBM, each with its bytes moved once.  At 16384 x 4096 bf16,
-// 2 of 8 experts: permute 64 us (403 MB, 6290 GB/s), unpermute 70 us
-// (5750 GB/s), its backward with weight gradients 109 us (671 MB,
-// 6160 GB/s).  At 8192 x 2048, 8 of 128, padding to 16: 53, 47 and 86 us.
-// The sort is two launches and 7 us at 32768 slots, 20 us at 524288 (its
-// counters, not its 8 bytes a slot); with few slots one launch and 4.5 us.
+// 2 of 8 experts: permute 62 us (403 MB, 6490 GB/s), unpermute 67 us
+// (6020 GB/s), its backward with weight gradients 107 us (671 MB,
+// 6300 GB/s); fp32 136, 117 and 194 us (5940 to 6930 GB/s).  At 8192 x 2048, 8
+// of 128, padding to 16: 51, 50 and 93 us; fp32 143, 108 and 211 us (4340 to
+// 5730 GB/s: eight choices at once spill 164 bytes a thread in fp32's unpermute
+// and 280 in its backward, 88 and 16 in bf16's).  Widths that are not a multiple
+// of 8 take their choices one at a time, a token's row read again for each
+// (figures below).
+// The sort is two launches and 7 us at 32768 slots, 20 us at 524288 for 4 MB of
+// maps: at most 128 blocks, each of which reads all blocks' counts, and then up
+// to 16 dependent turns to a warp; with few slots one launch and 4.5 us.
 // The copies launch a block per few tokens: blocks that went on from token to
 // token, looking the next one's rows up meanwhile, spilled the choices and
 // took 86 us in place of 70 for that unpermute.
@@ -214,8 +220,9 @@ moe_place(const int32_t* __restrict__ expert_of, const int* __restrict__ hist, i
 // 16-byte aligned buffers, so every chunk is one (fp32: two) 16-byte access.
 // Otherwise the chunk grid follows the destination row's alignment; sources
 // are read through the aligned vectors that cover them, and the ragged ends
-// element by element (4096 x 4099, 4 of 60 experts: 45, 64 and 117 us for
-// permute, unpermute and its backward; by 4-byte words instead 74, 145, 193).
+// element by element (4096 x 4099, 4 of 60 experts: 42, 62 and 116 us for
+// permute, unpermute and its backward, of which 25, 25 and 45 are bytes; by
+// 4-byte words instead 74, 145, 193).
 // ---------------------------------------------------------------------------
 template <typename T>
 struct Span {
@@ -386,7 +393,8 @@ moe_permute(const T* __restrict__ x, const int32_t* __restrict__ row_of, const i
 // in choice order, G of them in flight at a time.  A choice without a row
 // reads row 0 instead, which is not added.  Five blocks an SM for small G: the
 // loads of a thread wait for the row numbers, so it is warps that keep HBM busy
-// (six spill: 102 us in place of 70 at 16384 x 4096, 2 choices).
+// (two choices spill 40 bytes a thread at five and more at six: 102 us in place
+// of 70 at 16384 x 4096).
 // ---------------------------------------------------------------------------
 template <typename T, bool FAST, int G>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : G <= 4 ? 5 : 4)

@@ -17,16 +17,19 @@
 // atomics, a fixed order.  Each block leaves its per-bucket sums in the
 // workspace, and a second kernel adds those in block order.
 //
-// What bounds it: instruction issue again, 36 warp instructions per 32
-// elements at 65 % of the slots (2x8x2048x2048 bf16 with dropout), with x and
-// dy read once from DRAM.  Beside the forward's work it has dy's conversion,
-// the products and differences, the sums of the table's gradient, and dy's two
-// trips through shared memory.
+// What bounds it: HBM without dropout; with it nothing alone, 36 warp
+// instructions per 32 elements at 65 % of the issue slots, no pipe above 50 %,
+// 14 warps an SM (2x8x2048x2048 bf16), x and dy read once from DRAM.  Beside the
+// forward's work it has dy's conversion, the products and differences, the sums
+// of the table's gradient, and dy's two trips through shared memory.
 // A thread holds 4 chunks, not the forward's 8, since Q and z live together;
 // the next row arrives in shared memory meanwhile.  At 2x32x4096x4096 bf16
-// (6.44 GB): 1004 us (6420 GB/s) without dropout, 1353 us (4760 GB/s) with;
-// 4x12x1024x1024 causal with padding masks and dropout 89 us; fp32 rows of 1001
-// keys, 3x7x333 of them, with full masks and dropout 36 us.
+// (6.44 GB): 1010 us (6380 GB/s) without dropout, 1356 us (4750 GB/s) with;
+// 4x12x1024x1024 causal with padding masks and dropout 90 us; fp32 rows of 1001
+// keys, 3x7x333 of them, with full masks 38 us; 2x8x1027x2051 bf16 with padding
+// masks and dropout 116 us (30 us of bytes; the forward says why).
+// Rows of several register blocks form the first half twice and spill (352 to
+// 552 bytes a thread): 1x8x256x32768 bf16 with dropout 222 us (60 us of bytes).
 #include "relbias.cuh"
 
 namespace mfx {
@@ -406,7 +409,8 @@ int dispatch_bwd(const Args& a, const Buckets& w, const void* dy, const void* x,
     // Wide windows leave staged rows of many chunks no room in a block (two
     // directions and a distance of 2048: bf16 rows of 7176 keys and more with
     // 256 buckets, 9224 with 128, 13320 with 64): those rows go straight into
-    // registers, as ones of several register blocks do.
+    // registers, as ones of several register blocks do (1x8x1024x8192 with 256
+    // buckets and dropout 245 us, with 32 buckets to a distance of 128 94 us).
     const bool room = g.team <= 32 || block_bytes<T, kMost, FAST, kTeam>(w, dtable != nullptr, 1, g.team) <= kMostDynamic;
     if (g.blocks > 1 || !room)
         return launch_bwd<T, kMost, DROP, MASK, FAST, kWalkTeam>(g, w, a, dy, x, stats, dx, dtable, workspace, s);

@@ -27,13 +27,21 @@
 // thread block, which works on one head.  Chunks outside take one of two
 // registers; which is asked a warp at a time.
 //
-// What bounds it: instruction issue.  2x8x2048x2048 bf16 with dropout spends
-// 21 warp instructions per 32 elements, at 58 % of the issue slots and 47 % of
-// the ALU pipe, about 7 of them the generator's 10 rounds and the 8 keep words;
-// DRAM reads are x once.  At 2x32x4096x4096 bf16 (4.29 GB): 688 us (6240 GB/s)
-// without dropout, 970 us (4430 GB/s) with; with dropout too, 16x16x512x512
-// 67 us, 4x12x1024x1024 causal with padding masks 66 us, 2x8x2048x4096 fp32
-// 188 us; decode rows 32x32x8192 9.5 us and 1x16x131072 10.8 us of GPU time.
+// What bounds it: HBM without dropout; with it latency, at the 14 warps an SM
+// that the registers leave.  2x8x2048x2048 bf16 with dropout spends 21 warp
+// instructions per 32 elements, at 58 % of the issue slots and 47 % of the ALU
+// pipe, with loads the second reason to wait; about 7 of the 21 are the
+// generator's 10 rounds and the 8 keep words, which run after the reduction,
+// when the row's loads are long done.  DRAM reads are x once.
+// At 2x32x4096x4096 bf16 (4.29 GB): 691 us (6220 GB/s) without dropout, 968 us
+// (4440 GB/s) with; with dropout too, 16x16x512x512 70 us, 4x12x1024x1024 causal
+// with padding masks 65 us (chunks that a row leaves out still take their
+// exponentials), 2x8x2048x4096 fp32 188 us; decode rows 32x32x8192 9.5 us and
+// 1x16x131072 10.8 us of GPU time.  Rows that are not whole chunks are far from
+// their bytes (2x8x1027x2051 bf16 with padding masks and dropout 94 us, 20 us of
+// bytes): a mask row that is not aligned like its row of x is read element by
+// element, as is all data where elem_base % 8 != 0 with dropout.  Masked variants
+// spill (bf16 40 to 188 bytes a thread, fp32 up to 496).
 #include "relbias.cuh"
 
 namespace mfx {
@@ -346,8 +354,8 @@ int dispatch_fwd(const Args& a, const Buckets& w, const void* x, void* y, float*
 {
     Geom g = make_geom(a, w, x);
     constexpr int kMost = FAST && sizeof(T) == 2 ? 8 : 4;
-    // (fp32 rows of which all takes part: four chunks to a thread spill;
-    // 16x16x512x512 95 us in place of 85)
+    // (fp32 rows of which all takes part: two chunks to a thread; four took 95 us
+    // in place of 85 at 16x16x512x512.  Masked and causal ones take four)
     int c = plan(g, FAST, kMost, sizeof(T) == 4 && FAST && !MASK && !a.causal ? 2 : kMost, 8);
     const int64_t rows = a.b * a.np * a.sq, sms = sm_count(), chunks = chunks_of(g, FAST);
     if (chunks > 32 && rows < 4 * sms) {

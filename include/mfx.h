@@ -222,7 +222,10 @@ int mfx_scaled_upper_triang_masked_softmax_bwd(int dt, int64_t attn_batches, int
  * mask: NULL or an ADDITIVE mask of dtype dt, [mask_b, mask_np, mask_sq, sk]
  * with each size 1 or x's; a key whose mask is -inf takes no part whatever x
  * holds there.  Finite masks are added exactly in effect: a row whose every
- * mask is the type's lowest value is the softmax of its scores.  causal != 0
+ * mask is the type's lowest value is the softmax of its scores.  (Scores
+ * x_k * scale + table[...] beyond fp32's range over log2 e, 2.36e38, count as
+ * infinite; a score of -inf leaves its key out, one of +inf or NaN makes its row
+ * NaN.)  causal != 0
  * leaves out the keys k > pos, whose x is not read (with seq_start: each
  * sequence's unwritten part of a longer key axis).  A row in which no key
  * takes part is zeros.
