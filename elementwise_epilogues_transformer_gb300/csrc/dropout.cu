@@ -918,13 +918,13 @@ template <typename TX, typename TR>
 int launch_flat(const TX* g, TX* dx, TR* dres, int64_t n, float scale, uint32_t thresh, uint64_t seed,
                 uint64_t offset, uint64_t elem_base, cudaStream_t s)
 {
-    const int to_vector = (int)((0 - reinterpret_cast<uintptr_t>(dx) & 15u) / sizeof(TX));
+    const int to_vector = (int)(((0 - reinterpret_cast<uintptr_t>(dx)) & 15u) / sizeof(TX));
     FlatDrop d = {};
     d.head = to_vector < n ? to_vector : (int)n;
     g += d.head, dx += d.head, dres = dres ? dres + d.head : dres;
     d.n = n - d.head, d.scale = scale, d.thresh_hi = thresh << 16;
     d.block0 = (elem_base + d.head) / 8, d.phase = (int)((elem_base + d.head) % 8);
-    d.shift = (int)((0 - reinterpret_cast<uintptr_t>(dres) & 15u) / sizeof(TR));
+    d.shift = (int)(((0 - reinterpret_cast<uintptr_t>(dres)) & 15u) / sizeof(TR));
     d.vec = (sizeof(TX) == 4 && aligned32(g) && aligned32(dx) ? 4 : 0) | (sizeof(TR) == 4 && aligned32(dres) ? 8 : 0);
     d.gen = make_mask_gen(seed, offset);
     const int64_t units = d.n > 0 ? (d.n + 7) / 8 : 1;
@@ -937,7 +937,7 @@ int launch_flat(const TX* g, TX* dx, TR* dres, int64_t n, float scale, uint32_t 
     // several units a lane where that still gives every SM two blocks
     constexpr int U = sizeof(TX) == 2 ? 4 : 2;
     const bool many = units >= (int64_t)sm_count() * 2 * kThreads * U;
-    if (!aligned16(g) || !aligned16(dres))
+    if (!aligned16(g) || !aligned16(dres))  // at any phase, 0 among them
         return many ? go(drop_flat<TX, TR, U, true, true>, U) : go(drop_flat<TX, TR, 1, true, true>, 1);
     if (many)
         return d.phase ? go(drop_flat<TX, TR, U, true, false>, U) : go(drop_flat<TX, TR, U, false, false>, U);

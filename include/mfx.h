@@ -224,11 +224,10 @@ int mfx_scaled_upper_triang_masked_softmax_bwd(int dt, int64_t attn_batches, int
  * holds there.  Finite masks are added exactly in effect: a row whose every
  * mask is the type's lowest value is the softmax of its scores.  (Scores
  * x_k * scale + table[...] beyond fp32's range over log2 e, 2.36e38, count as
- * infinite; a score of -inf leaves its key out, one of +inf or NaN makes its row
- * NaN.)  causal != 0
- * leaves out the keys k > pos, whose x is not read (with seq_start: each
- * sequence's unwritten part of a longer key axis).  A row in which no key
- * takes part is zeros.
+ * infinite; a score of -inf leaves its key out, one of +inf or NaN makes its
+ * row NaN.)  causal != 0 leaves out the keys k > pos, whose x is not read (with
+ * seq_start: each sequence's unwritten part of a longer key axis).  A row in
+ * which no key takes part is zeros.
  * Dropout: element (r, k), r = (i * np + h) * sq + q, has the index e =
  * elem_base + r * sk + k, and keep as in mfx_bias_dropout_add_train (same
  * generator, words and threshold); p = 0 keeps everything.
@@ -236,8 +235,9 @@ int mfx_scaled_upper_triang_masked_softmax_bwd(int dt, int64_t attn_batches, int
  * of its mask, the maximum of its scores in base-2 units and one over the sum
  * of its exponentials), or NULL (inference).
  * y: x's shape and dtype; y may equal x (in place, when no backward follows).
- * b, np, sq, sk and |q_start| at most 2^29, b * sq at most 2^30.  One query per sequence over a long key axis
- * (decoding) splits a row over several thread blocks. */
+ * b, np, sq, sk and |q_start| at most 2^29, b * sq at most 2^30.  One query
+ * per sequence over a long key axis (decoding) splits a row over several
+ * thread blocks. */
 int mfx_relbias_softmax_dropout_fwd(int dt, int64_t b, int64_t np, int64_t sq, int64_t sk,
                                     const void* x, float scale,
                                     int table_dt, const void* table, int64_t num_buckets, int64_t max_distance,
