@@ -759,12 +759,13 @@ bda_bwd_generic(const TX* g, const uint8_t* keep, TX* dx, TR* dres, int64_t n, f
 // block and the next one, which is the block of the lane above: lane 0 hands
 // its next unit's to lane 31, and only the warp's last block is drawn twice.
 // The next turn's loads go out before this turn's work.
-// Unit 0 begins where dx is 16-byte aligned; the elements before it (`head`)
-// are one thread's each.  Where g or dres is not aligned there (ANY), a unit
+// Unit 0 begins where dx (and dres, if it can be) is 16-byte aligned; the
+// elements before it (`head`) are one thread's each.  Where g or dres is not aligned there (ANY), a unit
 // of g is read as the vectors that cover it, and dres is written from units of
 // its own, `shift` elements further on: 16384 x 4096, an element off a vector
 // and at an odd offset, bf16 127 -> 56 us and fp32 164 -> 85 us (element by
-// element a unit's accesses are 32 bytes apart in a warp).
+// element a unit's accesses are 32 bytes apart in a warp).  Two blocks an SM
+// for phased fp32 (three spill: 99 against 89 us there, aligned).
 // Measured against the ring that the stored-mask backward uses, bf16 32768 x
 // 4099: 88 against 96 us (107 against 253 us at an odd offset, where the ring
 // did not apply); without the early loads 96 us, with two or eight units a lane
@@ -803,7 +804,7 @@ __device__ __forceinline__ void flat_store(T* p, bool wide, const Raw8<T>& r)
 }
 
 template <typename TX, typename TR, int U, bool PHASED, bool ANY>
-__global__ void __launch_bounds__(kThreads, U > 1 ? 3 : PHASED ? 4 : 6)
+__global__ void __launch_bounds__(kThreads, U > 1 ? (PHASED && !ANY && sizeof(TX) == 4 ? 2 : 3) : PHASED ? 4 : 6)
 drop_flat(const TX* g, TX* dx, TR* dres, const __grid_constant__ FlatDrop d)
 {
     const int lane = threadIdx.x & 31;
@@ -918,7 +919,11 @@ template <typename TX, typename TR>
 int launch_flat(const TX* g, TX* dx, TR* dres, int64_t n, float scale, uint32_t thresh, uint64_t seed,
                 uint64_t offset, uint64_t elem_base, cudaStream_t s)
 {
-    const int to_vector = (int)(((0 - reinterpret_cast<uintptr_t>(dx)) & 15u) / sizeof(TX));
+    // elements to dx's and dres's first vectors: units begin at dx's, or at dres's
+    // where that is one of dx's too
+    const int to_dx = (int)(((0 - reinterpret_cast<uintptr_t>(dx)) & 15u) / sizeof(TX));
+    const int to_dres = (int)(((0 - reinterpret_cast<uintptr_t>(dres)) & 15u) / sizeof(TR));
+    const int to_vector = dres && !aligned16(dres + to_dx) && aligned16(dx + to_dres) ? to_dres : to_dx;
     FlatDrop d = {};
     d.head = to_vector < n ? to_vector : (int)n;
     g += d.head, dx += d.head, dres = dres ? dres + d.head : dres;
