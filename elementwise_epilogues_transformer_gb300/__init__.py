@@ -11,7 +11,9 @@ Megatron [seq, batch, hidden] layout is accepted as is.
 
 There is no fallback: if ``libmfx.so`` has not been built, every call raises.
 """
+import contextlib
 import ctypes as C
+import math
 import os
 
 import torch
@@ -27,6 +29,9 @@ __all__ = [
     "mfx_relbias_softmax_dropout_fwd", "mfx_relbias_softmax_dropout_bwd",
     "mfx_moe_rows", "mfx_moe_sort", "mfx_moe_permute_fwd", "mfx_moe_permute_bwd",
     "mfx_moe_unpermute_fwd", "mfx_moe_unpermute_bwd",
+    "mfx_add_rmsnorm_fwd", "mfx_add_rmsnorm_quant_fwd", "mfx_add_rmsnorm_bwd",
+    "mfx_token_logprobs_fwd", "mfx_token_logprobs_bwd",
+    "mfx_topk_distill_fwd", "mfx_topk_distill_bwd", "mfx_topk_distill_fwd_bwd",
     "mfx_bias_dropout_add_train", "mfx_bias_dropout_add_inference", "mfx_bias_dropout_add_bwd",
     "mfx_bias_dropout_add_train_packed", "mfx_bias_dropout_add_bwd_packed",
     "mfx_bias_dropout_add_train_nomask", "mfx_dropout_fwd", "mfx_dropout_bwd",
@@ -39,10 +44,10 @@ __all__ = [
 LIB_PATH = os.environ.get("MFX_LIBRARY") or os.path.join(
     os.path.dirname(os.path.abspath(__file__)), "libmfx.so")
 
-MFX_F32, MFX_BF16 = 0, 1
+MFX_F32, MFX_BF16, MFX_E4M3, MFX_E5M2, MFX_E8M0 = 0, 1, 2, 3, 4
 STATUS = {0: "MFX_OK", 1: "MFX_ERR_NULL", 2: "MFX_ERR_SHAPE", 3: "MFX_ERR_DTYPE",
           4: "MFX_ERR_PROB", 5: "MFX_ERR_ALIAS", 6: "MFX_ERR_CUDA", 7: "MFX_ERR_DEVICE",
-          8: "MFX_ERR_WORKSPACE"}
+          8: "MFX_ERR_WORKSPACE", 9: "MFX_ERR_VALUE"}
 
 
 class MfxError(RuntimeError):
@@ -78,6 +83,14 @@ _SIGS = {
     "mfx_moe_permute_bwd": [_I, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P],
     "mfx_moe_unpermute_fwd": [_I, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P],
     "mfx_moe_unpermute_bwd": [_I, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P],
+    "mfx_add_rmsnorm_fwd": [_I, _I, _I, _I64, _I64, _P, _P, _P, _F, _F, _P, _P, _P, _P],
+    "mfx_add_rmsnorm_quant_fwd": [_I, _I, _I, _I64, _I64, _P, _P, _P, _F, _F, _I, _I64, _I, _P, _P, _P, _P, _P],
+    "mfx_add_rmsnorm_bwd": [_I, _I, _I, _I64, _I64, _P, _P, _P, _P, _F, _P, _P, _P, _P, _P, C.POINTER(C.c_size_t), _P],
+    "mfx_token_logprobs_fwd": [_I, _I64, _I64, _I64, _P, _I, _P, _F, _I64, _P, _P, _P, _P, _P, _P],
+    "mfx_token_logprobs_bwd": [_I, _I64, _I64, _I64, _P, _P, _P, _I, _P, _P, _F, _P, _I64, _P],
+    "mfx_topk_distill_fwd": [_I, _I, _I64, _I64, _I64, _I64, _P, _I, _P, _P, _P, _F, _P, _P, _P],
+    "mfx_topk_distill_bwd": [_I, _I, _I64, _I64, _I64, _I64, _P, _P, _I, _P, _P, _P, _F, _P, _I64, _P],
+    "mfx_topk_distill_fwd_bwd": [_I, _I, _I64, _I64, _I64, _I64, _P, _I, _P, _P, _P, _P, _F, _P, _P, _I64, _P],
     "mfx_bias_dropout_add_train": [_I, _I, _I64, _I64, _P, _P, _P, _F, _U64, _U64, _U64, _P, _P, _P],
     "mfx_bias_dropout_add_inference": [_I, _I, _I64, _I64, _P, _P, _P, _F, _U64, _U64, _P],
     "mfx_bias_dropout_add_bwd": [_I, _I, _I64, _I64, _P, _P, _F, _U64, _U64, _U64, _P, _P, _P],
@@ -619,6 +632,319 @@ def mfx_moe_unpermute_bwd(g, y, row_of, slot_of, weight=None, dy=None, dweight=N
     _call("mfx_moe_unpermute_bwd", dtype_code(g.dtype), tokens, topk, cols, rows, _ptr(g), _ptr(y), _ptr(row_of),
           _ptr(slot_of), _ptr(weight), _ptr(dy), _ptr(dweight), _stream(stream, g))
     return dy, dweight
+
+
+# ---------------------------------------------------------------------------
+# root-mean-square norm with the residual's addition
+# ---------------------------------------------------------------------------
+_NOTHING = contextlib.nullcontext()
+
+
+def _here(t):
+    """Context in which t's device is the current one (launches go there)."""
+    dev = t.get_device()
+    return _NOTHING if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _rows_of(t, name, rows, dtype, dev):
+    """t is a vector of one element per row, on the data's device."""
+    _like(t, name, (rows,), dtype)
+    _same_device(t, dev, name)
+    return t.data_ptr()
+
+
+def _norm_args(x, weight, residual):
+    """What the two forwards check: (rows, cols, device, types, pointers)."""
+    _cuda(x, "x")
+    if x.dim() == 0:
+        raise ValueError("x must have at least one dim")
+    rows, cols = math.prod(x.shape[:-1]), x.shape[-1]
+    dev = x.get_device()
+    xdt = rdt = wdt = dtype_code(x.dtype)
+    rptr = None
+    if residual is not None:
+        _like(_cuda(residual, "residual"), "residual", x.shape, residual.dtype)
+        _same_device(residual, dev, "residual")
+        rdt, rptr = dtype_code(residual.dtype), residual.data_ptr()
+    if weight is not None:
+        _like(_cuda(weight, "weight"), "weight", (cols,), weight.dtype)
+        _same_device(weight, dev, "weight")
+        wdt = dtype_code(weight.dtype)
+    return rows, cols, dev, (xdt, rdt, wdt), (x.data_ptr(), rptr, _ptr(weight))
+
+
+def _norm_outputs(x, residual, rows, dev, h, rstd, need_rstd, stream):
+    if residual is None:
+        if h is not None:
+            raise ValueError("h needs a residual")
+    else:
+        h = _empty_like(residual, stream) if h is None else _like(h, "h", x.shape, residual.dtype)
+        _same_device(h, dev, "h")
+    if rstd is not None:
+        _rows_of(rstd, "rstd", rows, torch.float32, dev)
+    elif need_rstd:
+        rstd = _empty((rows,), torch.float32, x.device, stream)
+    return h, rstd
+
+
+def mfx_add_rmsnorm_fwd(x, weight, residual=None, eps=1e-6, weight_offset=0.0, y=None, h=None, rstd=None,
+                        need_rstd=True, stream=None):
+    """(y, h, rstd): h = x + residual in the residual's dtype (None without a
+    residual), y = h * rstd * (weight + weight_offset) over the last dim with
+    rstd = 1 / sqrt(mean(h^2) + eps) ([rows], None with need_rstd=False).
+    weight [cols] may be None."""
+    rows, cols, dev, types, data = _norm_args(x, weight, residual)
+    y = _empty_like(x, stream) if y is None else _like(y, "y", x.shape, x.dtype)
+    _same_device(y, dev, "y")
+    h, rstd = _norm_outputs(x, residual, rows, dev, h, rstd, need_rstd, stream)
+    with _here(x):
+        _call("mfx_add_rmsnorm_fwd", *types, rows, cols, *data, float(eps), float(weight_offset), y.data_ptr(), _ptr(h),
+              _ptr(rstd), _stream(stream, x))
+    return y, h, rstd
+
+
+_Q_DTYPES = {torch.float8_e4m3fn: MFX_E4M3, torch.float8_e5m2: MFX_E5M2}
+_SCALE_DTYPES = {torch.float32: MFX_F32, torch.float8_e8m0fnu: MFX_E8M0}
+
+
+def mfx_add_rmsnorm_quant_fwd(x, weight, residual=None, eps=1e-6, weight_offset=0.0, group=0,
+                              q_dtype=torch.float8_e4m3fn, scale_dtype=torch.float32, q=None, scale=None, h=None,
+                              rstd=None, need_rstd=False, stream=None):
+    """(q, scale, h, rstd): mfx_add_rmsnorm_fwd with y in 8 bits, y ~ q *
+    scale.  One scale per row (group=0) or per 32 or 128 columns of it, scale
+    [..., groups]; float8_e8m0fnu scales are powers of two."""
+    rows, cols, dev, types, data = _norm_args(x, weight, residual)
+    if q_dtype not in _Q_DTYPES or scale_dtype not in _SCALE_DTYPES:
+        raise TypeError("q is float8_e4m3fn or float8_e5m2, scale float32 or float8_e8m0fnu")
+    group = int(group)
+    if group not in (0, 32, 128):
+        raise MfxError(9, "mfx_add_rmsnorm_quant_fwd")
+    groups = -(-cols // group) if group else min(cols, 1)
+    q = _empty(x.shape, q_dtype, x.device, stream) if q is None else _like(q, "q", x.shape, q_dtype)
+    _same_device(q, dev, "q")
+    shape = (*x.shape[:-1], groups)
+    scale = _empty(shape, scale_dtype, x.device, stream) if scale is None else _like(scale, "scale", shape, scale_dtype)
+    _same_device(scale, dev, "scale")
+    h, rstd = _norm_outputs(x, residual, rows, dev, h, rstd, need_rstd, stream)
+    with _here(x):
+        _call("mfx_add_rmsnorm_quant_fwd", *types, rows, cols, *data, float(eps), float(weight_offset), _Q_DTYPES[q_dtype],
+              group, _SCALE_DTYPES[scale_dtype], q.data_ptr(), scale.data_ptr(), _ptr(h), _ptr(rstd), _stream(stream, x))
+    return q, scale, h, rstd
+
+
+def mfx_add_rmsnorm_bwd(dy, h, rstd, weight, dh=None, weight_offset=0.0, dx=None, dresidual=None, residual_dtype=None,
+                        dweight=None, need_dweight=True, workspace=None, stream=None):
+    """(dx, dresidual, dweight) from the forward's h (x where there was no
+    residual) and rstd, the gradient dy of y and, where given, dh of h.
+    dresidual is produced when a buffer is given or residual_dtype (h's dtype)
+    is set; with dy's dtype and no buffer it is dx itself.  dweight is None
+    without a weight or with need_dweight=False."""
+    _cuda(dy, "dy")
+    _cuda(h, "h")
+    if dy.dim() == 0:
+        raise ValueError("dy must have at least one dim")
+    rows, cols = math.prod(dy.shape[:-1]), dy.shape[-1]
+    dev = dy.get_device()
+    _like(h, "h", dy.shape, h.dtype)
+    _same_device(h, dev, "h")
+    _rows_of(rstd, "rstd", rows, torch.float32, dev)
+    xdt, rdt = dtype_code(dy.dtype), dtype_code(h.dtype)
+    wdt = xdt
+    if weight is not None:
+        _like(_cuda(weight, "weight"), "weight", (cols,), weight.dtype)
+        _same_device(weight, dev, "weight")
+        wdt = dtype_code(weight.dtype)
+    if dh is not None:
+        _like(dh, "dh", dy.shape, h.dtype)
+        _same_device(dh, dev, "dh")
+    dx = _empty_like(dy, stream) if dx is None else _like(dx, "dx", dy.shape, dy.dtype)
+    _same_device(dx, dev, "dx")
+    same = False
+    if dresidual is not None:
+        _like(dresidual, "dresidual", dy.shape, h.dtype)
+        _same_device(dresidual, dev, "dresidual")
+    elif residual_dtype is not None:
+        if residual_dtype != h.dtype:
+            raise TypeError(f"residual_dtype must be h's, {h.dtype}")
+        same = h.dtype == dy.dtype
+        dresidual = None if same else _empty_like(h, stream)
+    if dweight is not None:
+        if weight is None:
+            raise ValueError("dweight needs a weight")
+        _like(dweight, "dweight", (cols,), weight.dtype)
+        _same_device(dweight, dev, "dweight")
+    elif weight is not None and need_dweight:
+        dweight = _empty_like(weight, stream)
+    with _here(dy):
+        head = (xdt, rdt, wdt, rows, cols, dy.data_ptr(), h.data_ptr(), rstd.data_ptr(), _ptr(weight), float(weight_offset),
+                _ptr(dh), dx.data_ptr(), _ptr(dresidual), _ptr(dweight))
+        _with_workspace("mfx_add_rmsnorm_bwd", head, (_stream(stream, dy),), dy.device, workspace,
+                        (dev, xdt, rdt, rows, cols, dweight is None), none=True, stream=stream)
+    return dx, dx if same else dresidual, dweight
+
+
+# ---------------------------------------------------------------------------
+# operators on logits
+# ---------------------------------------------------------------------------
+_INDEX_BITS = {torch.int32: 32, torch.int64: 64}
+
+
+def _logit_rows(t, name):
+    """(rows, vocab, ld) of [rows, vocab] data whose rows lie ld elements apart."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have the shape [rows, vocab]")
+    rows, vocab = t.shape
+    if vocab > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s columns must be contiguous")
+    if rows > 1 and t.stride(0) < vocab:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return rows, vocab, t.stride(0) if rows > 1 else vocab
+
+
+def _columns(t, name, shape, dev):
+    """Bits of an index array of the given shape."""
+    bits = _INDEX_BITS.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if bits is None:
+        raise TypeError(f"{name} must be an int32 or int64 tensor")
+    _like(t, name, shape, t.dtype)
+    _same_device(t, dev, name)
+    return bits
+
+
+def _dlogits(dlogits, logits, dev, stream):
+    """(buffer, its ld): contiguous if it is allocated here."""
+    rows, vocab = logits.shape
+    if dlogits is None:
+        return _empty((rows, vocab), logits.dtype, logits.device, stream), vocab
+    if not isinstance(dlogits, torch.Tensor) or dlogits.dtype != logits.dtype:
+        raise TypeError(f"dlogits must be a {logits.dtype} tensor")
+    if _logit_rows(dlogits, "dlogits")[:2] != (rows, vocab):
+        raise ValueError("dlogits must have the logits' shape")
+    _same_device(dlogits, dev, "dlogits")
+    return dlogits, dlogits.stride(0) if rows > 1 else vocab
+
+
+def mfx_token_logprobs_fwd(logits, tokens, scale=1.0, top=0, logprob=None, entropy=None, top_logprob=None,
+                           top_index=None, stats=None, need_stats=True, stream=None):
+    """(logprob [rows], entropy [rows], top_logprob [rows, top], top_index
+    [rows, top], stats [rows, 3]) of softmax(scale * logits [rows, vocab]) at
+    tokens [rows] (int32 or int64; one outside the vocabulary leaves its row
+    out).  The alternatives are None with top=0, stats with need_stats=False.
+    logits' rows may lie further apart than the vocabulary is wide."""
+    rows, vocab, ld = _logit_rows(logits, "logits")
+    dev, top = logits.get_device(), int(top)
+    bits = _columns(tokens, "tokens", (rows,), dev)
+    f32 = torch.float32
+
+    def new(t, name, shape, dtype):
+        if t is None:
+            return _empty(shape, dtype, logits.device, stream)
+        _like(t, name, shape, dtype)
+        _same_device(t, dev, name)
+        return t
+
+    logprob, entropy = new(logprob, "logprob", (rows,), f32), new(entropy, "entropy", (rows,), f32)
+    if top > 0:
+        top_logprob = new(top_logprob, "top_logprob", (rows, top), f32)
+        top_index = new(top_index, "top_index", (rows, top), torch.int32)
+    elif top_logprob is not None or top_index is not None:
+        raise ValueError("top_logprob and top_index need top")
+    if stats is not None or need_stats:
+        stats = new(stats, "stats", (rows, 3), f32)
+    with _here(logits):
+        _call("mfx_token_logprobs_fwd", dtype_code(logits.dtype), rows, vocab, ld, logits.data_ptr(), bits,
+              tokens.data_ptr(), float(scale), top, logprob.data_ptr(), entropy.data_ptr(), _ptr(top_logprob),
+              _ptr(top_index), _ptr(stats), _stream(stream, logits))
+    return logprob, entropy, top_logprob, top_index, stats
+
+
+def mfx_token_logprobs_bwd(g_logprob, g_entropy, logits, tokens, stats, scale=1.0, dlogits=None, stream=None):
+    """dlogits [rows, vocab] from the gradients of logprob and entropy (either
+    may be None) and the forward's inputs and stats; dlogits may be logits."""
+    rows, vocab, ld = _logit_rows(logits, "logits")
+    dev = logits.get_device()
+    bits = _columns(tokens, "tokens", (rows,), dev)
+    g = None if g_logprob is None else _rows_of(g_logprob, "g_logprob", rows, torch.float32, dev)
+    ge = None if g_entropy is None else _rows_of(g_entropy, "g_entropy", rows, torch.float32, dev)
+    _like(stats, "stats", (rows, 3), torch.float32)
+    _same_device(stats, dev, "stats")
+    dlogits, ldo = _dlogits(dlogits, logits, dev, stream)
+    with _here(logits):
+        _call("mfx_token_logprobs_bwd", dtype_code(logits.dtype), rows, vocab, ld, g, ge, logits.data_ptr(), bits,
+              tokens.data_ptr(), stats.data_ptr(), float(scale), dlogits.data_ptr(), ldo, _stream(stream, logits))
+    return dlogits
+
+
+def _distill_args(logits, index, teacher, teacher_lse):
+    """(rows, device, arguments up to teacher, teacher_lse's pointer)."""
+    rows, vocab, ld = _logit_rows(logits, "logits")
+    dev = logits.get_device()
+    if not isinstance(teacher, torch.Tensor) or teacher.dim() != 2:
+        raise ValueError("teacher must have the shape [rows, k]")
+    k = teacher.shape[1]
+    _like(teacher, "teacher", (rows, k), teacher.dtype)
+    _same_device(teacher, dev, "teacher")
+    bits = _columns(index, "index", (rows, k), dev)
+    lse = None if teacher_lse is None else _rows_of(teacher_lse, "teacher_lse", rows, torch.float32, dev)
+    head = (dtype_code(logits.dtype), dtype_code(teacher.dtype), rows, vocab, ld, k)
+    return rows, dev, head, (logits.data_ptr(), bits, index.data_ptr(), teacher.data_ptr()), lse
+
+
+def mfx_topk_distill_fwd(logits, index, teacher, scale=1.0, teacher_lse=None, loss=None, stats=None, need_stats=True,
+                         stream=None):
+    """(loss [rows], stats [rows, 4]): sum of q (log q - log p) over the
+    teacher's entries, p = softmax(scale * logits [rows, vocab]) and q the same
+    of teacher [rows, k] at the columns index [rows, k] (int32 or int64,
+    negative for no entry), or exp(scale * teacher - teacher_lse [rows])."""
+    rows, dev, head, data, lse = _distill_args(logits, index, teacher, teacher_lse)
+    if loss is None:
+        loss = _empty((rows,), torch.float32, logits.device, stream)
+    else:
+        _rows_of(loss, "loss", rows, torch.float32, dev)
+    if stats is not None:
+        _like(stats, "stats", (rows, 4), torch.float32)
+        _same_device(stats, dev, "stats")
+    elif need_stats:
+        stats = _empty((rows, 4), torch.float32, logits.device, stream)
+    with _here(logits):
+        _call("mfx_topk_distill_fwd", *head, *data, lse, float(scale), loss.data_ptr(), _ptr(stats),
+              _stream(stream, logits))
+    return loss, stats
+
+
+def mfx_topk_distill_bwd(g, logits, index, teacher, stats, scale=1.0, teacher_lse=None, dlogits=None, stream=None):
+    """dlogits [rows, vocab] from the gradient g [rows] of the loss and the
+    forward's inputs and stats (which hold what teacher_lse says); dlogits may
+    be logits."""
+    rows, dev, head, data, _ = _distill_args(logits, index, teacher, teacher_lse)
+    gptr = _rows_of(g, "g", rows, torch.float32, dev)
+    _like(stats, "stats", (rows, 4), torch.float32)
+    _same_device(stats, dev, "stats")
+    dlogits, ldo = _dlogits(dlogits, logits, dev, stream)
+    with _here(logits):
+        _call("mfx_topk_distill_bwd", *head, gptr, *data, stats.data_ptr(), float(scale), dlogits.data_ptr(), ldo,
+              _stream(stream, logits))
+    return dlogits
+
+
+def mfx_topk_distill_fwd_bwd(logits, index, teacher, weight, scale=1.0, teacher_lse=None, loss=None, dlogits=None,
+                             stream=None):
+    """(loss [rows], dlogits [rows, vocab]) in one call, where the gradient
+    weight [rows] of each row's loss is known before it; dlogits may be
+    logits."""
+    rows, dev, head, data, lse = _distill_args(logits, index, teacher, teacher_lse)
+    wptr = _rows_of(weight, "weight", rows, torch.float32, dev)
+    if loss is None:
+        loss = _empty((rows,), torch.float32, logits.device, stream)
+    else:
+        _rows_of(loss, "loss", rows, torch.float32, dev)
+    dlogits, ldo = _dlogits(dlogits, logits, dev, stream)
+    with _here(logits):
+        _call("mfx_topk_distill_fwd_bwd", *head, *data, lse, wptr, float(scale), loss.data_ptr(), dlogits.data_ptr(), ldo,
+              _stream(stream, logits))
+    return loss, dlogits
 
 
 # ---------------------------------------------------------------------------

@@ -19,8 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmfx.so")
 
 SOURCES = ["mfx_abi.cu", "gelu.cu", "glu.cu", "dropout.cu", "dbias.cu", "sqrelu.cu", "softmax.cu", "relbias_fwd.cu",
-           "relbias_bwd.cu", "moe.cu"]
-HEADERS = ["mfx_device.cuh", "mfx_host.h", "mfx_pipe.cuh", "relbias.cuh"]
+           "relbias_bwd.cu", "moe.cu", "rmsnorm_fwd.cu", "rmsnorm_bwd.cu", "logprobs.cu", "distill.cu"]
+HEADERS = ["mfx_device.cuh", "mfx_host.h", "mfx_pipe.cuh", "relbias.cuh", "rmsnorm.cuh", "vocab.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-O2",
               "-I", INCLUDE, "-I", CSRC, "--expt-relaxed-constexpr", "-Xptxas", "-v"]

@@ -49,6 +49,10 @@ std::mutex g_occ_mutex;
 std::unordered_map<OccKey, int, OccHash> g_occ;
 std::unordered_map<std::pair<int, const void*>, size_t, FnKeyHash> g_smem_limit;
 
+// Above this much dynamic shared memory the limit is raised: a block has 48 KB
+// without asking, of which a kernel's static arrays take their part.
+constexpr size_t kSmemAsked = 32 * 1024;
+
 constexpr int kMaxDevices = 64;
 thread_local int g_sms[kMaxDevices] = {0};
 
@@ -93,7 +97,7 @@ int occupancy(const void* kernel, int block_threads, size_t smem)
     auto it = g_occ.find(key);
     if (it != g_occ.end())
         return it->second;
-    if (smem > 48 * 1024) {
+    if (smem > kSmemAsked) {
         size_t& lim = g_smem_limit[{dev, kernel}];
         if (smem > lim && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) ==
                               cudaSuccess)
@@ -179,6 +183,7 @@ const char* mfx_status_string(int status)
     case MFX_ERR_CUDA: return "CUDA launch failed (see mfx_last_cuda_error)";
     case MFX_ERR_DEVICE: return "a kernel gave up a bounded wait (see mfx_device_error)";
     case MFX_ERR_WORKSPACE: return "workspace too small or not 16-byte aligned";
+    case MFX_ERR_VALUE: return "a scalar argument outside its range";
     default: return "unknown status";
     }
 }
@@ -197,6 +202,6 @@ int mfx_device_error(unsigned* code)
     return c ? MFX_ERR_DEVICE : MFX_OK;
 }
 
-int mfx_version(void) { return (1 << 16) | 4; }
+int mfx_version(void) { return (1 << 16) | 5; }
 
 }  // extern "C"

@@ -60,7 +60,8 @@ int blocks_per_sm(const void* kernel);
 // Resident blocks per multiprocessor at `block_threads` threads and `smem`
 // bytes of dynamic shared memory (at least 1), cached per device, kernel and
 // size; also raises the kernel's dynamic shared-memory limit to `smem` when
-// it is above 48 KB and above every size set before.
+// it is above 32 KB (with static arrays it may pass 48 KB in all) and above
+// every size set before.
 int occupancy(const void* kernel, int block_threads, size_t smem);
 
 // Launch geometry for a grid-stride loop over `units` work items of 8

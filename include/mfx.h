@@ -45,7 +45,8 @@
 extern "C" {
 #endif
 
-typedef enum { MFX_F32 = 0, MFX_BF16 = 1 } mfx_dtype;
+/* The 8-bit codes are for the quantised norm's outputs alone. */
+typedef enum { MFX_F32 = 0, MFX_BF16 = 1, MFX_E4M3 = 2, MFX_E5M2 = 3, MFX_E8M0 = 4 } mfx_dtype;
 
 typedef enum {
     MFX_OK = 0,
@@ -56,7 +57,8 @@ typedef enum {
     MFX_ERR_ALIAS = 5, /* buffers overlap in a way the op does not allow       */
     MFX_ERR_CUDA = 6,  /* the kernel launch failed (see mfx_last_cuda_error)   */
     MFX_ERR_DEVICE = 7, /* a kernel gave up a bounded wait (mfx_device_error)  */
-    MFX_ERR_WORKSPACE = 8 /* workspace too small or not 16-byte aligned        */
+    MFX_ERR_WORKSPACE = 8, /* workspace too small or not 16-byte aligned       */
+    MFX_ERR_VALUE = 9  /* a scalar argument outside its range                  */
 } mfx_status;
 
 /* ------------------------------------------------------------------------ */
@@ -337,6 +339,128 @@ int mfx_moe_unpermute_fwd(int dt, int64_t tokens, int64_t topk, int64_t cols, in
 int mfx_moe_unpermute_bwd(int dt, int64_t tokens, int64_t topk, int64_t cols, int64_t rows,
                           const void* g, const void* y, const int32_t* row_of, const int32_t* slot_of,
                           const float* weight, void* dy, float* dweight, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Root-mean-square norm with the residual's addition: what stands between    */
+/* the residual path (bias-dropout-add) and the next block's first product.   */
+/* The fusions page names the fused norm beside these ops without describing  */
+/* it; the formulas are those of the literature (Zhang and Sennrich, 2019).   */
+/*   h = x + residual,   rstd = 1 / sqrt(mean(h^2) + eps),                    */
+/*   y = h * rstd * (weight + weight_offset)                                  */
+/* ------------------------------------------------------------------------ */
+
+/* x, y: [rows, cols] dtype x_dt; residual, h: [rows, cols] dtype res_dt;
+ * weight: [cols] dtype w_dt, or NULL (a factor of 1); weight_offset is 1 for
+ * weights that are kept around zero, else 0.  residual NULL: h = x (and h must
+ * be NULL).  h (NULL: not written) is the new residual stream; y is formed
+ * from it before it is rounded.  rstd: [rows] fp32, what the backward needs,
+ * or NULL.  Norms are fp32: squares of values beyond 1.8e19 overflow.
+ * eps >= 0 and finite, else MFX_ERR_VALUE; cols up to 2^30.  y and h may each
+ * be x's or the residual's very buffer; other overlaps -> MFX_ERR_ALIAS. */
+int mfx_add_rmsnorm_fwd(int x_dt, int res_dt, int w_dt, int64_t rows, int64_t cols,
+                        const void* x, const void* residual, const void* weight,
+                        float eps, float weight_offset,
+                        void* y, void* h, float* rstd, void* stream);
+
+/* The same with y in 8 bits.  q: [rows, cols] of q_dt (MFX_E4M3 or MFX_E5M2),
+ * q = y / s rounded to nearest even and saturated, where s is the scale of the
+ * element's group: group = 0 the whole row, 32 or 128 that many columns of it
+ * (a row's last group may be shorter), else MFX_ERR_VALUE.
+ * s = max |y| / 448 (e4m3) or / 57344 (e5m2), at least 2^-126 and 1 for a
+ * group of zeros; scale: [rows, groups of a row], MFX_F32, or MFX_E8M0: s
+ * rounded up to a power of two, stored as its exponent + 127 in a byte.
+ * NaN stays NaN (and counts for nothing in max |y|), infinities saturate.
+ * y is not rounded to x_dt on the way.  q and scale overlap nothing else. */
+int mfx_add_rmsnorm_quant_fwd(int x_dt, int res_dt, int w_dt, int64_t rows, int64_t cols,
+                              const void* x, const void* residual, const void* weight,
+                              float eps, float weight_offset,
+                              int q_dt, int64_t group, int scale_dt,
+                              void* q, void* scale, void* h, float* rstd, void* stream);
+
+/* Gradients from the stored h (x where there was no residual; dtype res_dt)
+ * and rstd.  dy: [rows, cols] x_dt; dh: [rows, cols] res_dt, the gradient that
+ * reaches h from further on, or NULL.  With n = h * rstd, u = dy * (weight +
+ * weight_offset):
+ *   d = rstd * (u - n * mean(u * n)) + dh,   dweight[c] = sum_r dy * n.
+ * d is the gradient of x and of the residual alike: dx gets it as x_dt,
+ * dresidual as res_dt; either may be NULL.  dweight: [cols] w_dt, or NULL.
+ * The output in 8 bits is passed straight through (dy is y's gradient).
+ * dweight is the same bits from run to run on a given GPU model; the workspace
+ * protocol is that of the fused bias gradients below (the size may be 0: then
+ * NULL sizes and workspaces run).  dx and dresidual may each be the very
+ * buffer of dy, h or dh; other overlaps -> MFX_ERR_ALIAS. */
+int mfx_add_rmsnorm_bwd(int x_dt, int res_dt, int w_dt, int64_t rows, int64_t cols,
+                        const void* dy, const void* h, const float* rstd,
+                        const void* weight, float weight_offset, const void* dh,
+                        void* dx, void* dresidual, void* dweight,
+                        void* workspace, size_t* workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Operators on logits [rows, vocab] of dtype dt, whose rows begin ld >= vocab */
+/* elements apart (a vocabulary padded in memory; what lies between is neither */
+/* read nor written).  p = softmax(scale * z) over a row, scale > 0 and finite */
+/* (one over the temperature), else MFX_ERR_VALUE.  Columns at -inf have p = 0.*/
+/* A row with a NaN or +inf gives NaN.  index_bits: 32 or 64, the width of the */
+/* integers that name columns, else MFX_ERR_DTYPE.  vocab up to 2^30.          */
+/* ------------------------------------------------------------------------ */
+
+/* Log probabilities of given tokens, the distribution's entropy, and the `top`
+ * (0 to 64, else MFX_ERR_VALUE) largest logits' log probabilities and columns.
+ * tokens: [rows]; a token outside [0, vocab) leaves its row out: its results
+ * are 0, its alternatives (-inf, -1), and its logits are not read.
+ * logprob[r] = log p[token], entropy[r] = -sum p log p (fp32).
+ * top_logprob, top_index: [rows, top] in falling order, equal logits by the
+ * lower column; (-inf, -1) where fewer than `top` are above -inf; columns with
+ * NaN are never among them.  stats: [rows, 3] fp32, what the backward needs,
+ * or NULL.  A row that is all -inf: logprob -inf, entropy 0.
+ * Outputs must not overlap anything -> MFX_ERR_ALIAS. */
+int mfx_token_logprobs_fwd(int dt, int64_t rows, int64_t vocab, int64_t ld,
+                           const void* logits, int index_bits, const void* tokens,
+                           float scale, int64_t top,
+                           float* logprob, float* entropy,
+                           float* top_logprob, int32_t* top_index, float* stats, void* stream);
+
+/* dlogits[r, k] = scale * (g (1[token = k] - p) - ge p (log p + entropy)) in
+ * dtype dt, rows ld_out apart, from the gradients g of logprob and ge of
+ * entropy ([rows] fp32; either may be NULL) and the forward's inputs and stats.
+ * Rows that are left out or all -inf get zeros.  dlogits may be the very
+ * buffer of logits (with ld_out == ld); other overlaps -> MFX_ERR_ALIAS. */
+int mfx_token_logprobs_bwd(int dt, int64_t rows, int64_t vocab, int64_t ld,
+                           const float* g_logprob, const float* g_entropy,
+                           const void* logits, int index_bits, const void* tokens,
+                           const float* stats, float scale,
+                           void* dlogits, int64_t ld_out, void* stream);
+
+/* Distillation from a teacher's top logits.  index, teacher: [rows, k] columns
+ * and the teacher's logits t there (dtype t_dt), 0 <= k <= 1024; a column
+ * outside [0, vocab) is no entry, and a column may come twice (its entries'
+ * q add up).  q = softmax(scale * t) over a row's entries, or, with
+ * teacher_lse [rows] fp32, exp(scale * t - teacher_lse): the teacher's own
+ * normalisation over its whole vocabulary.
+ *   loss[r] = sum_j q_j (log q_j - log p[column j])           (fp32)
+ * (0 without entries; +inf where a column with q > 0 has p = 0).
+ * stats: [rows, 4] fp32, what the backward needs, or NULL. */
+int mfx_topk_distill_fwd(int dt, int t_dt, int64_t rows, int64_t vocab, int64_t ld, int64_t k,
+                         const void* logits, int index_bits, const void* index,
+                         const void* teacher, const float* teacher_lse, float scale,
+                         float* loss, float* stats, void* stream);
+
+/* dlogits = g * scale * (sum(q) p - q at its columns), from the gradient g
+ * [rows] (fp32) of the loss; rows without entries, and rows that are all -inf,
+ * get zeros.  dlogits as for the log probabilities. */
+int mfx_topk_distill_bwd(int dt, int t_dt, int64_t rows, int64_t vocab, int64_t ld, int64_t k,
+                         const float* g, const void* logits, int index_bits, const void* index,
+                         const void* teacher, const float* stats, float scale,
+                         void* dlogits, int64_t ld_out, void* stream);
+
+/* Both in one call, for a loss whose gradient is known before it (a weight for
+ * each row, [rows] fp32, in the place of g): the logits are read from memory
+ * once instead of twice. */
+int mfx_topk_distill_fwd_bwd(int dt, int t_dt, int64_t rows, int64_t vocab, int64_t ld, int64_t k,
+                             const void* logits, int index_bits, const void* index,
+                             const void* teacher, const float* teacher_lse,
+                             const float* weight, float scale,
+                             float* loss, void* dlogits, int64_t ld_out, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Bias + dropout + residual add, fusions page §3.2-§3.3                     */
