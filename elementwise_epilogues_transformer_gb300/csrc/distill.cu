@@ -26,7 +26,7 @@ constexpr int kMostEntries = 1024;
 
 struct Args {
     int64_t rows, ld, ldo;
-    int n, K, cluster, chunks, per;
+    int n, K, cluster, runs, chunks, per;
     const void *logits, *index, *teacher;
     bool wide, t_bf16;
     float scale, k2;
@@ -36,8 +36,8 @@ struct Args {
     void* out;
 };
 
-// A row's list in shared memory: columns (-1: no entry), q, and the student's
-// logits there.
+// A row's list in shared memory: columns (-1: no entry), q, and the teacher's
+// logits, then log q, then the student's logits.
 struct List {
     int* col;
     float *q, *z;
@@ -49,183 +49,252 @@ __device__ __forceinline__ float teacher_at(const Args& a, int64_t i)
     return a.t_bf16 ? load1(static_cast<const bf16*>(a.teacher) + i) : load1(static_cast<const float*>(a.teacher) + i);
 }
 
-// A sum (or maximum) over the block, the same bits in every thread.
-template <bool MAX>
-__device__ __forceinline__ float over_block(float v, float* part)
+__device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        v = MAX ? fmaxf(v, w) : v + w;
-    }
-    if (blockDim.x > 32) {
-        __syncthreads();  // what the last call left is read
-        if ((threadIdx.x & 31) == 0)
-            part[threadIdx.x >> 5] = v;
-        __syncthreads();
-        const int lane = threadIdx.x & 31;
-        v = lane < (int)(blockDim.x >> 5) ? part[lane] : (MAX ? -INFINITY : 0.0f);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            v = MAX ? fmaxf(v, w) : v + w;
-        }
-    }
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
 
-// What q is formed from: q_j = exp((t_j - ref) * scale) * coef = exp((t_j - ref) * scale + log_coef).
+// What q is formed from: q_j = exp((t_j - ref) * scale) * coef = exp((t_j - ref) * scale + log_coef),
+// their sum Q, and how many of the row's entries the list holds.
 struct Teacher {
     float ref, coef, log_coef, Q;
-    bool any;
+    int n;
 };
 
-__device__ __forceinline__ float q_of(const Args& a, float t, const Teacher& w)
+__device__ __forceinline__ float power_of(const Args& a, float t, float ref)
 {
-    return exp2_approx(at_least_zero_power((t - w.ref) * a.k2)) * w.coef;
+    return exp2_approx(at_least_zero_power((t - ref) * a.k2));
 }
 
-// Reads the row's list (columns, the student's logits there if Z, q) and forms
-// the teacher's statistics.
-template <typename T, bool Z>
-__device__ __forceinline__ Teacher read_list(const Args& a, int64_t row, const T* z, const List& l, float* part)
+// One warp reads the row's entries and leaves those of columns [lo, hi) at the
+// list's front, in order.  Q is over all entries; `given` has ref and coef
+// from the forward (no Q then).
+template <bool GIVEN>
+__device__ __forceinline__ Teacher read_list(const Args& a, int64_t row, const List& l, int lo, int hi, Teacher w)
 {
-    float top = -INFINITY;
-    bool any = false;
-    for (int j = threadIdx.x; j < a.K; j += blockDim.x) {
+    const int lane = threadIdx.x & 31;
+    float top = -INFINITY, sum = 0.0f;
+    for (int j = lane; j < a.K; j += 32) {
         const int c = column_of(a.index, a.wide, row * a.K + j, a.n);
         const float t = c >= 0 ? teacher_at(a, row * a.K + j) : -INFINITY;
-        l.col[j] = c, l.q[j] = t;
-        any |= c >= 0;
-        if (Z)
-            l.z[j] = c >= 0 ? load1(z + c) : -INFINITY;
+        l.col[j] = c, l.z[j] = t;
         top = fmaxf(top, t);
     }
-    top = over_block<true>(top, part);
-    Teacher w = {top == -INFINITY ? 0.0f : top, 0.0f, 0.0f, 0.0f, false};
-    w.any = __syncthreads_or(any);
-    float sum = 0.0f;
-    for (int j = threadIdx.x; j < a.K; j += blockDim.x) {
-        const float e = exp2_approx(at_least_zero_power((l.q[j] - w.ref) * a.k2));
-        l.q[j] = e;
-        sum += e;
+    if (!GIVEN) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        w.ref = top == -INFINITY ? 0.0f : top;
+        for (int j = lane; j < a.K; j += 32)
+            sum += power_of(a, l.z[j], w.ref);
+        sum = warp_sum(sum);
+        if (a.lse) {
+            w.log_coef = fmaf(w.ref, a.scale, -a.lse[row]);
+            w.coef = expf(w.log_coef);
+        } else {
+            w.log_coef = sum == 0.0f ? 0.0f : -logf(sum);
+            w.coef = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+        }
+        w.Q = sum * w.coef;
     }
-    sum = over_block<false>(sum, part);
-    if (a.lse) {
-        w.log_coef = fmaf(w.ref, a.scale, -a.lse[row]);
-        w.coef = expf(w.log_coef);
-    } else {
-        w.log_coef = sum == 0.0f ? 0.0f : -logf(sum);
-        w.coef = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+    w.n = 0;
+    for (int j0 = 0; j0 < a.K; j0 += 32) {  // places at or before the ones just read
+        const int j = j0 + lane, c = j < a.K ? l.col[j] : -1;
+        const float t = j < a.K ? l.z[j] : -INFINITY;
+        const bool here = c >= lo && c < hi;
+        const uint32_t who = __ballot_sync(0xFFFFFFFFu, here);  // (and all lanes have read)
+        if (here) {
+            const int to = w.n + __popc(who & ((1u << lane) - 1u));
+            l.col[to] = c;
+            l.q[to] = power_of(a, t, w.ref) * w.coef;
+            l.z[to] = fmaf(t - w.ref, a.scale, w.log_coef);  // log q from t, not from q
+        }
+        w.n += __popc(who);
+        __syncwarp();
     }
-    w.Q = sum * w.coef;
-    for (int j = threadIdx.x; j < a.K; j += blockDim.x)
-        l.q[j] *= w.coef;
     return w;
 }
 
-// The loss from the list and the row's statistics (thread 0 writes it).
-__device__ __forceinline__ void put_loss(const Args& a, int64_t row, const List& l, const Teacher& w, const Stats& v,
-                                         float* part)
+// One warp: the loss of the list's entries, whose logits (z_of) stay in it.
+template <typename F>
+__device__ __forceinline__ float loss_of(const Args& a, const List& l, int n, const Stats& v, F z_of)
 {
     const float log_l = logf(v.l);
     float sum = 0.0f;
-    for (int j = threadIdx.x; j < a.K; j += blockDim.x) {
-        const float q = l.q[j];
-        if (l.col[j] >= 0 && q != 0.0f) {
-            // log q from t itself, and not as a logarithm of q
-            const float logq = fmaf(teacher_at(a, row * a.K + j) - w.ref, a.scale, w.log_coef);
-            const float logp = v.l == 0.0f ? -INFINITY : fmaf(l.z[j] - v.ref, a.scale, -log_l);
-            sum = fmaf(q, logq - logp, sum);
-        }
+    for (int j = threadIdx.x & 31; j < n; j += 32) {
+        const float z = z_of(l.col[j]), q = l.q[j], logq = l.z[j];
+        l.z[j] = z;
+        if (q != 0.0f)
+            sum = fmaf(q, logq - (v.l == 0.0f ? -INFINITY : fmaf(z - v.ref, a.scale, -log_l)), sum);
     }
-    sum = over_block<false>(sum, part);
-    if (threadIdx.x == 0)
-        a.loss[row] = sum;
+    return warp_sum(sum);
 }
 
-// The gradient of runs [u0, u1) of an output row; `ratio` is Q / l (0: zeros).
+// The gradient exp(t) * A of a run.
 template <typename T>
-__device__ __forceinline__ void put_grads(const Args& a, const T* z, T* o, int u0, int u1, const List& l, float ref,
-                                          float ratio, float g)
+__device__ __forceinline__ uint4 grad_run(const uint4& w, float ref, float k2, float A)
 {
-    const Runs<T> ro(o, a.n);
-    const float A = g * a.scale * ratio;
-    for (int u = u0 + threadIdx.x; u < u1; u += blockDim.x) {
-        const int c = ro.column(u);
-        float f[8];
-        if (ratio == 0.0f) {
+    constexpr int P = Run<T>::V / 2;
+    float2 f[P];
+    Run<T>::widen(w, f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                f[j] = 0.0f;
-        } else {
-            load8_at(z, a.n, c, f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                f[j] = A * exp2_approx(at_least_zero_power((f[j] - ref) * a.k2));
-        }
-        store_run(ro, o, u, f);
+    for (int j = 0; j < P; ++j)
+        f[j] = mul2(exp2_pair(mul2(add2(f[j], f2(-ref)), f2(k2))), f2(A));
+    return Run<T>::narrow(f);
+}
+
+// The gradient of columns [lo, hi) of an output row from the piece that holds
+// them: runs aligned like the piece's (whole ones of it four at a time), or not.
+template <typename T>
+__device__ __forceinline__ void put_piece(const Piece<T>& p, T* o, const Runs<T>& ro, int lo, int hi, float ref, float k2,
+                                          float A, bool zero)
+{
+    constexpr int U = 4, V = Run<T>::V;
+    const int step = p.step, tid = threadIdx.x;
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    // whole runs of the output that lie in [lo, hi): [v0, v1)
+    const int v0 = (lo + ro.phase + V - 1) / V, v1 = max((hi + ro.phase) / V, v0);
+    if (tid < 2) {  // what is before and behind them
+        const int u = tid ? v1 : v0 - 1, c = ro.column(u);
+        if (c + V > lo && c < hi && (tid == 0 || v1 != v0 - 1))
+            store_run(ro, o, u, lo, hi, zero ? none : grad_run<T>(p.run_at(c), ref, k2, A));
     }
-    if (ratio == 0.0f)
-        return;
-    __syncthreads();
-    const int c0 = ro.column(u0), c1 = ro.column(u1);
-    for (int j = threadIdx.x; j < a.K; j += blockDim.x) {
+    T* to = o + ro.column(v0 + tid);
+    int u = v0 + tid;
+    if (zero) {
+        for (; u < v1; u += step, to += step * V)
+            st16(to, none);
+    } else if (ro.phase == p.r.phase) {
+        uint32_t from = p.at(u);
+        for (; u + (U - 1) * step < v1; u += U * step, to += U * step * V, from += 16u * (uint32_t)(U * step)) {
+            uint4 w[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                w[i] = lds16(from + 16u * (uint32_t)(i * step));
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                st16(to + i * step * V, grad_run<T>(w[i], ref, k2, A));
+        }
+        for (; u < v1; u += step, to += step * V, from += 16u * (uint32_t)step)
+            st16(to, grad_run<T>(lds16(from), ref, k2, A));
+    } else {
+        for (; u < v1; u += step, to += step * V)
+            st16(to, grad_run<T>(p.run_at(ro.column(u)), ref, k2, A));
+    }
+}
+
+// Puts the list's columns right: g * scale * (Q p - their q), each by the first
+// entry that names it.
+template <typename T>
+__device__ __forceinline__ void put_listed(const Args& a, T* o, const List& l, int n, float ref, float ratio, float g)
+{
+    for (int j = threadIdx.x; j < n; j += blockDim.x) {
         const int c = l.col[j];
-        if (c < 0 || c < c0 || c >= c1)
-            continue;
         float q = 0.0f;
         bool mine = true;
-        for (int i = 0; i < a.K; ++i)
+        for (int i = 0; i < n; ++i)
             if (l.col[i] == c) {
                 mine &= i >= j;
                 q += l.q[i];
             }
-        if (mine) {
-            const float e = exp2_approx(at_least_zero_power((l.z[j] - ref) * a.k2));
-            store1(o + c, g * a.scale * fmaf(e, ratio, -q));
-        }
+        if (mine)
+            store1(o + c, g * a.scale * fmaf(power_of(a, l.z[j], ref), ratio, -q));
     }
 }
 
 template <typename T, bool GRAD>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(kThreadsMost + 32, MFX_VOCAB_BLOCKS)
 distill_fwd(const Args a)
 {
     extern __shared__ __align__(16) char dynamic[];
-    __shared__ Stats part[32], mine;
-    __shared__ float fpart[32];
-    const List l(dynamic, a.K);
-    const int rank = a.cluster > 1 ? (int)cluster_rank() : 0, tid = threadIdx.x;
+    __shared__ Stats part[8], mine;
+    __shared__ float my_loss, Q;
+    __shared__ int listed;
+    const List l(dynamic + (size_t)(a.runs + 2) * 16, a.K);
+    // one warp more than share the slice: it sees to the list
+    const int rank = a.cluster > 1 ? (int)cluster_rank() : 0, tid = threadIdx.x, threads = blockDim.x - 32;
     for (int64_t row = blockIdx.x / a.cluster; row < a.rows; row += gridDim.x / a.cluster) {
         const T* z = static_cast<const T*>(a.logits) + row * a.ld;
-        T* o = GRAD ? static_cast<T*>(a.out) + row * a.ldo : nullptr;
-        const Teacher w = read_list<T, true>(a, row, z, l, fpart);
+        const Runs<T> r(z, a.n);
+        const int share = (r.count + a.cluster - 1) / a.cluster;
+        const int first = min(rank * share, r.count), last = min(first + share, r.count);
+        const int lo = max(r.column(first), 0), hi = min(r.column(last), a.n);
+        Piece<T> p(r, smem_addr(dynamic), threads);
+        p.set(first, min(first + a.runs, last));
+        Teacher w = {};
         Stats v = no_stats();
-        if (w.any) {  // the same for every block of the cluster
-            Pick best;
-            v = scan<T, false, 4>(Share<T>(Runs<T>(z, a.n), rank, a.cluster), a.k2, best);
-            v = join_block(v, a.k2, part);
+        if (tid >= threads) {
+            w = read_list<false>(a, row, l, lo, hi, w);
+            if (tid == threads)
+                Q = w.Q, listed = w.n;
+            while (p.last < last)
+                p.set(p.last, min(p.last + a.runs, last));
+        } else {
+            BestRun none = {-INFINITY, 0};
+            p.fill();
+            scan<T, false, false>(p, a.k2, v, none);
+            while (p.last < last) {  // (threads read only what they copied)
+                p.set(p.last, min(p.last + a.runs, last));
+                p.fill();
+                scan<T, false, false>(p, a.k2, v, none);
+            }
         }
+        join_block<false>(v, a.k2, part, threads >> 5);  // and the slice and Q are there for all threads
         if (a.cluster > 1)
-            v = join_cluster(v, a.k2, &mine, a.cluster);
-        else
-            __syncthreads();
-        const float ratio = v.l == 0.0f ? 0.0f : __fdiv_rn(w.Q, v.l);
-        if (rank == 0) {
-            put_loss(a, row, l, w, v, fpart);
-            if (!GRAD && a.stats && tid == 0)
-                a.stats[4 * row] = v.ref, a.stats[4 * row + 1] = ratio, a.stats[4 * row + 2] = w.ref, a.stats[4 * row + 3] = w.coef;
+            join_cluster<false>(v, a.k2, &mine, a.cluster);
+        const float ratio = v.l == 0.0f ? 0.0f : __fdiv_rn(Q, v.l);
+        if (tid >= threads) {
+            const float loss = p.first == first ? loss_of(a, l, w.n, v, [&](int c) { return p.value(c); })
+                                                : loss_of(a, l, w.n, v, [&](int c) { return load1(z + c); });
+            if (tid == threads) {
+                my_loss = loss;
+                if (rank == 0 && a.stats)
+                    a.stats[4 * row] = v.ref, a.stats[4 * row + 1] = ratio, a.stats[4 * row + 2] = w.ref, a.stats[4 * row + 3] = w.coef;
+            }
         }
+        __syncwarp();
+        if (a.cluster > 1)
+            cluster_arrive();  // my_loss is there; before the gradient's stores, for which it would wait
         if (GRAD) {
+            T* o = static_cast<T*>(a.out) + row * a.ldo;
             const Runs<T> ro(o, a.n);
-            const int per = (ro.count + a.cluster - 1) / a.cluster, u0 = min(rank * per, ro.count);
-            put_grads<T>(a, z, o, u0, min(u0 + per, ro.count), l, v.ref, ratio, a.g[row]);
+            const float g = a.g[row], A = g * a.scale * ratio;
+            if (p.first != first)
+                __syncthreads();  // listed logits of other pieces are read before they may be written
+            for (;;) {            // the last piece is the one at hand
+                if (tid < threads)
+                    put_piece<T>(p, o, ro, p.lo(), p.hi(), v.ref, a.k2, A, ratio == 0.0f);
+                __syncthreads();
+                if (p.first == first)
+                    break;
+                p.set(max(p.first - a.runs, first), p.first);
+                if (tid < threads) {
+                    p.fill();
+                    copies_wait<0>();
+                }
+                __syncthreads();
+            }
+            if (ratio != 0.0f)
+                put_listed<T>(a, o, l, listed, v.ref, ratio, g);
         }
         if (a.cluster > 1)
-            cluster_sync();
+            cluster_wait();
         else
             __syncthreads();
+        if (rank == 0 && tid == 0) {
+            float s = my_loss;
+            for (int i = 1; i < a.cluster; ++i)
+                s += peer_float(&my_loss, i);
+            a.loss[row] = s;
+        }
+        __syncwarp();
+        if (a.cluster > 1) {  // nobody leaves, or goes on, while its loss is read
+            cluster_arrive_relaxed();
+            cluster_wait();
+        }
     }
 }
 
@@ -234,25 +303,39 @@ __global__ void __launch_bounds__(256)
 distill_bwd(const Args a)
 {
     extern __shared__ __align__(16) char dynamic[];
+    __shared__ int listed;
+    constexpr int U = 4, V = Run<T>::V;
     const List l(dynamic, a.K);
     for (int64_t item = blockIdx.x; item < a.rows * a.chunks; item += gridDim.x) {
         const int64_t row = item / a.chunks;
         const T* z = static_cast<const T*>(a.logits) + row * a.ld;
         T* o = static_cast<T*>(a.out) + row * a.ldo;
         const float ref = a.stats_in[4 * row], ratio = a.stats_in[4 * row + 1];
-        const Teacher w = {a.stats_in[4 * row + 2], a.stats_in[4 * row + 3], 0.0f, 0.0f, true};
         const Runs<T> ro(o, a.n);
-        const int u0 = (int)(item % a.chunks) * a.per, u1 = min(u0 + a.per, ro.count);
-        const int c0 = ro.column(u0), c1 = ro.column(u1);
-        for (int j = threadIdx.x; j < a.K; j += blockDim.x) {
-            const int c = column_of(a.index, a.wide, row * a.K + j, a.n);
-            const bool here = c >= 0 && c >= c0 && c < c1;
-            l.col[j] = here ? c : -1;
-            l.q[j] = here ? q_of(a, teacher_at(a, row * a.K + j), w) : 0.0f;
-            l.z[j] = here ? load1(z + c) : 0.0f;
+        const int u0 = min((int)(item % a.chunks) * a.per, ro.count), u1 = min(u0 + a.per, ro.count), step = blockDim.x;
+        const int lo = max(ro.column(u0), 0), hi = min(ro.column(u1), a.n);
+        const float g = a.g[row], A = g * a.scale * ratio;
+        if (threadIdx.x < 32) {
+            const Teacher w = read_list<true>(a, row, l, lo, hi, {a.stats_in[4 * row + 2], a.stats_in[4 * row + 3], 0.0f, 0.0f, 0});
+            for (int j = threadIdx.x; j < w.n; j += 32)
+                l.z[j] = load1(z + l.col[j]);
+            if (threadIdx.x == 0)
+                listed = w.n;
+        }
+        __syncthreads();  // listed logits are read before they may be written
+        for (int u = u0 + threadIdx.x; u < u1; u += U * step) {
+            uint4 x[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                x[i] = ratio != 0.0f && u + i * step < u1 ? load_run(z, a.n, ro.column(u + i * step)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (u + i * step < u1)
+                    store_run(ro, o, u + i * step, 0, a.n, ratio != 0.0f ? grad_run<T>(x[i], ref, a.k2, A) : x[i]);
         }
         __syncthreads();
-        put_grads<T>(a, z, o, u0, u1, l, ref, ratio, a.g[row]);
+        if (ratio != 0.0f)
+            put_listed<T>(a, o, l, listed, ref, ratio, g);
         __syncthreads();
     }
 }
@@ -260,16 +343,16 @@ distill_bwd(const Args a)
 template <typename T, bool GRAD>
 int launch_fwd(Args a, cudaStream_t s)
 {
-    const Split sp = split(a.rows, a.n);
-    a.cluster = sp.cluster;
-    const cudaError_t e = launch_rows(distill_fwd<T, GRAD>, a, sp, (size_t)a.K * 12, s);
+    const Split sp = split(a.rows, a.n, sizeof(T));
+    a.cluster = sp.cluster, a.runs = sp.runs;
+    const cudaError_t e = launch_rows(distill_fwd<T, GRAD>, a, sp, sp.threads + 32, sp.smem() + (size_t)a.K * 12, s);
     return e == cudaSuccess ? launch_status() : cuda_failure(e);
 }
 
 template <typename T>
 int launch_bwd(Args a, cudaStream_t s)
 {
-    const int64_t runs = (a.n + 14) / 8;
+    const int64_t runs = (a.n * (int64_t)sizeof(T) + 15) / 16 + 1;  // with a head and a tail
     const int threads = threads_for(runs, 256);
     a.per = threads * 8;
     a.chunks = (int)((runs + a.per - 1) / a.per);

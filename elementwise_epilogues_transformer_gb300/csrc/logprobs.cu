@@ -17,12 +17,15 @@ namespace mfx {
 namespace vocab {
 namespace {
 
-constexpr int kMostTop = 64;    // alternatives
-constexpr int kSpare = 1024;    // candidates beside those of one round
+constexpr int kMostTop = 64;  // alternatives
+constexpr int kKeys = 64;      // keys that bound the search for them
+constexpr int kRound = 64;     // runs of a round that cannot overflow the candidates
+constexpr int kKept = 256;     // candidates that a round may find there
+constexpr int kCandidates = kRound * 8 + kKept;
 
 struct Args {
     int64_t rows, ld;
-    int n, top, cluster;
+    int n, top, cluster, runs;
     const void *logits, *tokens;
     bool wide;
     float scale, k2;
@@ -30,148 +33,164 @@ struct Args {
     int32_t* top_index;
 };
 
-// Shared memory of the search for alternatives, for T threads.
+// A column and its logit as one number: larger for larger logits (-0 and 0
+// are equal), and among equal ones for the lower column.  0 is nothing.
+using Key = unsigned long long;
+__device__ __forceinline__ Key key_of(float v, int c)
+{
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return (Key)(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) << 32 | (0xFFFFFFFFu - (uint32_t)c);
+}
+__device__ __forceinline__ float value_of(Key k)
+{
+    const uint32_t b = (uint32_t)(k >> 32);
+    return __uint_as_float(b & 0x80000000u ? b ^ 0x80000000u : ~b);
+}
+__device__ __forceinline__ int column_of(Key k) { return (int)(0xFFFFFFFFu - (uint32_t)k); }
+
+// Shared memory of the search for alternatives.
 struct TopSmem {
-    Pick* best;   // [T] of every thread
-    Pick* four;   // [T / 4] of every four
-    int* list;    // [T] threads
-    Pick* cand;   // [8 T + kSpare]
-    Pick* sel;    // [kMostTop], the block's alternatives in order
-    int* count;   // [4]: threads listed, threads that count, candidates
-    Pick* limit;  // [2]
-    __device__ explicit TopSmem(char* p, int T)
-    {
-        best = reinterpret_cast<Pick*>(p), four = best + T, cand = four + T / 4, sel = cand + 8 * T + kSpare;
-        limit = sel + kMostTop, list = reinterpret_cast<int*>(limit + 2), count = list + T;
-    }
-    static size_t bytes(int T) { return (size_t)(T + T / 4 + 8 * T + kSpare + kMostTop + 2) * sizeof(Pick) + (T + 4) * 4; }
+    Key cand[kCandidates];
+    Key keys[kKeys];
+    Key sel[kMostTop];  // the block's alternatives in order, 0 behind them
+    Key limit;
+    int list[kThreadsMost];  // threads that may hold some
+    int listed, count;
 };
 
-__device__ __forceinline__ Pick shfl_xor(Pick p, int o)
+// The `top` largest of cand[0, n) in order to sel, 0 behind them.  Barriers
+// around it.  Four threads count for each candidate where they are few.
+__device__ __forceinline__ void sort_out(const Key* cand, int n, int top, Key* sel)
 {
-    return {__shfl_xor_sync(0xFFFFFFFFu, p.v, o), __shfl_xor_sync(0xFFFFFFFFu, p.i, o)};
-}
-
-// How many of list[0, n) are better than p.
-__device__ __forceinline__ int rank_in(const Pick* list, int n, const Pick& p)
-{
-    int r = 0;
-    for (int i = 0; i < n; ++i)
-        r += better(list[i], p);
-    return r;
-}
-
-// The `top` best of cand[0, n) in order to sel, (-inf, -1) behind them; a
-// barrier before the call and after it.
-__device__ __forceinline__ void sort_out(const Pick* cand, int n, int top, Pick* sel)
-{
-    for (int j = threadIdx.x; j < top; j += blockDim.x)
+    const int tid = threadIdx.x, T = blockDim.x;
+    for (int j = tid; j < top; j += T)
         if (j >= n)
-            sel[j] = {-INFINITY, -1};
-    for (int c = threadIdx.x; c < n; c += blockDim.x) {
-        const Pick p = cand[c];
-        if (const int r = rank_in(cand, n, p); r < top)
-            sel[r] = p;
+            sel[j] = 0;
+    if (4 * n <= T) {
+        const int c = tid >> 2, part = tid & 3;
+        const Key k = c < n ? cand[c] : 0;
+        int r = 0;
+        for (int j = part; j < n; j += 4)
+            r += cand[j] > k;
+        r += __shfl_xor_sync(0xFFFFFFFFu, r, 1);
+        r += __shfl_xor_sync(0xFFFFFFFFu, r, 2);
+        if (part == 0 && c < n && r < top)
+            sel[r] = k;
+        return;
+    }
+    for (int c = tid; c < n; c += T) {
+        const Key k = cand[c];
+        int r = 0;
+        for (int j = 0; j < n; ++j)
+            r += cand[j] > k;
+        if (r < top)
+            sel[r] = k;
     }
 }
 
-// The block's `top` best columns above -inf, to sm.sel in order.
+// The `top` largest columns above -inf of the slice that `p` holds (`whole`) or
+// ends, to sm.sel in order.
 //
-// The top-th best of the threads' own best columns bounds the top-th best of
-// all from below, and only the `top` threads whose best reaches it can hold a
-// column that does.  Their runs alone are read again (from L2, all at once)
-// for the few columns that reach the bound.  The order is strict (equal
-// logits go by column), so the number of such threads does not depend on the
-// data.  A round adds at most 8 candidates a thread; if they pile up (rows
-// built so that a few threads hold most large logits), they are cut to the
-// `top` best between rounds.
+// Threads know their largest logit and its run.  The top-th largest of 64
+// groups of threads (each one's key with the last column of its run, so not
+// above the true one) bounds the top-th largest of all from below, and only
+// threads whose own key (with the first column) reaches it can hold a column
+// that does: of 4096 runs' elements about as many as are asked for.  Their runs
+// are read again, from shared memory, for the columns that reach the bound.
+// Should those be more than there is room for (rows built so that few threads
+// hold most large logits), the runs are taken in small rounds and cut to the
+// best after each.
 template <typename T>
-__device__ __forceinline__ void find_top(const Share<T>& sh, const Pick best, int top, const TopSmem& sm)
+__device__ __forceinline__ void find_top(const Piece<T>& p, bool whole, int slice_first, int slice_last,
+                                         const BestRun best, int top, TopSmem& sm)
 {
-    const int tid = threadIdx.x, T_ = blockDim.x;
-    // a first bound from every four threads' best: fewer to compare
-    const Pick none = {-INFINITY, 0x7FFFFFFF};
-    Pick four = best;
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        const Pick q = shfl_xor(four, o);
-        if (better(q, four))
-            four = q;
+    constexpr int V = Run<T>::V;
+    const int tid = threadIdx.x, T_ = blockDim.x, nkeys = T_ < kKeys ? T_ : kKeys, per = T_ / nkeys;
+    const bool any = best.m > -INFINITY;
+    const int c0 = p.r.column(best.u);
+    Key k = any ? key_of(best.m, c0 + V - 1) : (Key)tid;  // those without any: below all others, none alike
+    for (int o = 1; o < per; o <<= 1) {
+        const Key q = __shfl_xor_sync(0xFFFFFFFFu, k, o);
+        k = q > k ? q : k;
     }
-    if ((tid & 3) == 0)
-        sm.four[tid >> 2] = four;
-    if (tid < 4)
-        sm.count[tid] = 0;
-    if (tid < 2)
-        sm.limit[tid] = none;
+    if (tid % per == 0)
+        sm.keys[tid / per] = k;
+    if (tid == 0)
+        sm.listed = 0, sm.count = 0, sm.limit = 0;
     __syncthreads();
-    if (T_ / 4 >= top) {
-        if (tid < T_ / 4) {
-            const Pick mine = sm.four[tid];
-            if (rank_in(sm.four, T_ / 4, mine) == top - 1)
-                sm.limit[0] = mine;
-        }
-        __syncthreads();
-        if (!better(sm.limit[0], best))
-            sm.best[atomicAdd(&sm.count[0], 1)] = best;
-        __syncthreads();
-        const int n = sm.count[0];  // at most four for each of `top`
-        for (int j = tid; j < n; j += T_) {
-            const Pick mine = sm.best[j];
-            if (rank_in(sm.best, n, mine) == top - 1)
-                sm.limit[1] = mine;
-        }
+    if (top <= nkeys) {
+        int r = 0;
+        for (int j = tid % per; j < nkeys; j += per)
+            r += sm.keys[j] > k;
+        for (int o = 1; o < per; o <<= 1)
+            r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
+        if (tid % per == 0 && r == top - 1)
+            sm.limit = k;
         __syncthreads();
     }
-    const Pick limit = sm.limit[1];
-    if (best.v > -INFINITY && !better(limit, best))
-        sm.list[atomicAdd(&sm.count[1], 1)] = tid;
+    const Key limit = sm.limit;
+    if (any && key_of(best.m, max(c0, 0)) >= limit)
+        sm.list[atomicAdd(&sm.listed, 1)] = tid;
     __syncthreads();
-    const int each = (sh.last - sh.first + T_ - 1) / T_ + 2, items = sm.count[1] * each;
-    for (int base = 0; base < items; base += T_) {
-        if (base + tid < items) {
-            const int t = sm.list[(base + tid) / each], i = (base + tid) % each;
-            int u = -1;
-            if (i < each - 2)
-                u = sh.first + t + i * T_ < sh.last ? sh.first + t + i * T_ : -1;
-            else if (t == 0)
-                u = i == each - 2 ? (sh.head ? 0 : -1) : (sh.tail ? sh.r.count - 1 : -1);
-            if (u >= 0) {
-                float z[8];
-                sh.r.load(u, z);
+    const int first = whole ? p.first : slice_first, last = whole ? p.last : slice_last;
+    const int each = (last - first + T_ - 1) / T_, items = sm.listed * each;
+    Key bound = limit;
+    for (int base = 0, size = T_; base < items;) {
+        const int before = sm.count;
+        __syncthreads();
+        const int item = base + tid;
+        if (tid < size && item < items) {
+            const int u = first + sm.list[item / each] + item % each * T_;
+            if (u < last) {
+                const uint4 w = whole ? lds16(p.at(u)) : load_run(p.r.p, p.r.n, p.r.column(u));
+                float2 f[V / 2];
+                Run<T>::widen(w, f);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const Pick p = {z[j], sh.r.column(u) + j};
-                    if (z[j] > -INFINITY && !better(limit, p))
-                        sm.cand[atomicAdd(&sm.count[2], 1)] = p;
+                for (int j = 0; j < V; ++j) {
+                    const float z = j & 1 ? f[j >> 1].y : f[j >> 1].x;
+                    const Key q = key_of(z, p.r.column(u) + j);
+                    if (z > -INFINITY && q >= bound)
+                        if (const int at = atomicAdd(&sm.count, 1); at < kCandidates)
+                            sm.cand[at] = q;
                 }
             }
         }
         __syncthreads();
-        if (const int n = sm.count[2]; base + T_ < items && n > kSpare) {
+        const int n = sm.count;
+        if (n > kCandidates) {  // not all of them had room: again, in small rounds
+            __syncthreads();
+            if (tid == 0)
+                sm.count = before;
+            size = kRound;
+            __syncthreads();
+            continue;
+        }
+        base += size;
+        if (base < items && n > kKept) {
             sort_out(sm.cand, n, top, sm.sel);
             __syncthreads();
             for (int j = tid; j < top; j += T_)
                 sm.cand[j] = sm.sel[j];
+            bound = sm.sel[top - 1];
             if (tid == 0)
-                sm.count[2] = top;
+                sm.count = top;
             __syncthreads();
         }
     }
-    sort_out(sm.cand, sm.count[2], top, sm.sel);
+    sort_out(sm.cand, sm.count, top, sm.sel);
     __syncthreads();
 }
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(kThreadsMost, MFX_VOCAB_BLOCKS)
 logprobs_fwd(const Args a)
 {
     extern __shared__ __align__(16) char dynamic[];
-    __shared__ Stats part[32], mine;
-    const TopSmem sm(dynamic, blockDim.x);
+    __shared__ Stats part[8], mine;
+    TopSmem& sm = *reinterpret_cast<TopSmem*>(dynamic + (size_t)(a.runs + 2) * 16);
     const int rank = a.cluster > 1 ? (int)cluster_rank() : 0, tid = threadIdx.x;
     for (int64_t row = blockIdx.x / a.cluster; row < a.rows; row += gridDim.x / a.cluster) {
-        const int token = column_of(a.tokens, a.wide, row, a.n);
+        const int token = vocab::column_of(a.tokens, a.wide, row, a.n);
         if (token < 0) {  // left out; the same for every block of the cluster
             if (rank == 0) {
                 if (tid == 0) {
@@ -187,14 +206,25 @@ logprobs_fwd(const Args a)
         }
         const T* z = static_cast<const T*>(a.logits) + row * a.ld;
         const float zt = load1(z + token);
-        const Share<T> sh(Runs<T>(z, a.n), rank, a.cluster);
-        Pick best;
-        Stats v = scan<T, TOP, 4>(sh, a.k2, best);
+        const Runs<T> r(z, a.n);
+        const int share = (r.count + a.cluster - 1) / a.cluster;
+        const int first = min(rank * share, r.count), last = min(first + share, r.count);
+        Stats v = no_stats();
+        BestRun best = {-INFINITY, 0};
+        Piece<T> p(r, smem_addr(dynamic), blockDim.x);
+        p.set(first, min(first + a.runs, last));
+        p.fill();
+        scan<T, true, TOP>(p, a.k2, v, best);
+        while (p.last < last) {  // (threads read only what they copied)
+            p.set(p.last, min(p.last + a.runs, last));
+            p.fill();
+            scan<T, true, TOP>(p, a.k2, v, best);
+        }
         if (TOP)
-            find_top(sh, best, a.top, sm);
-        v = join_block(v, a.k2, part);
+            find_top(p, p.first == first, first, last, best, a.top, sm);
+        join_block<true>(v, a.k2, part, blockDim.x >> 5);
         if (a.cluster > 1)
-            v = join_cluster(v, a.k2, &mine, a.cluster);
+            join_cluster<true>(v, a.k2, &mine, a.cluster);
         if (rank == 0) {
             const bool empty = v.l == 0.0f;
             const float log_l = logf(v.l), inv = empty ? 0.0f : __fdiv_rn(1.0f, v.l), U = empty ? 0.0f : -kLn2 * v.s * inv;
@@ -205,30 +235,31 @@ logprobs_fwd(const Args a)
                     a.stats[3 * row] = empty ? 0.0f : v.ref, a.stats[3 * row + 1] = inv, a.stats[3 * row + 2] = U;
             }
             if (TOP) {
-                if (a.cluster > 1) {
-                    for (int j = tid; j < a.top * a.cluster; j += blockDim.x) {
-                        const Pick* p = &sm.sel[j % a.top];
-                        sm.cand[j] = {__uint_as_float(peer_word(&p->v, j / a.top)), (int)peer_word(&p->i, j / a.top)};
-                        if (sm.cand[j].i < 0)
-                            sm.cand[j].i = (int)kMostColumns + j;  // nothing: behind all, each in its own place
+                const Key* list = sm.sel;
+                if (a.cluster > 1) {  // the blocks' lists
+                    const int n = a.top * a.cluster;
+                    for (int j = tid; j < n; j += blockDim.x) {
+                        const uint32_t* q = reinterpret_cast<const uint32_t*>(&sm.sel[j % a.top]);
+                        sm.cand[j] = (Key)peer_word(q + 1, j / a.top) << 32 | peer_word(q, j / a.top);
+                    }
+                    for (int j = tid; j < a.top; j += blockDim.x)
+                        sm.keys[j] = 0;
+                    __syncthreads();
+                    for (int c = tid; c < n; c += blockDim.x) {
+                        const Key k = sm.cand[c];
+                        int s = 0;
+                        for (int j = 0; j < n; ++j)
+                            s += sm.cand[j] > k;
+                        if (s < a.top && k)
+                            sm.keys[s] = k;
                     }
                     __syncthreads();
-                }
-                const Pick* list = sm.sel;
-                if (a.cluster > 1) {
-                    list = sm.best;  // free by now; at least as long as `top`
-                    for (int c = tid; c < a.top * a.cluster; c += blockDim.x) {
-                        const Pick p = sm.cand[c];
-                        if (const int r = rank_in(sm.cand, a.top * a.cluster, p); r < a.top)
-                            sm.best[r] = p;
-                    }
-                    __syncthreads();
+                    list = sm.keys;
                 }
                 for (int j = tid; j < a.top; j += blockDim.x) {
-                    const Pick p = list[j];
-                    const bool none = !(p.v > -INFINITY);
-                    a.top_logprob[row * a.top + j] = none ? -INFINITY : (p.v - v.ref) * a.scale - log_l;
-                    a.top_index[row * a.top + j] = none ? -1 : p.i;
+                    const Key k = list[j];
+                    a.top_logprob[row * a.top + j] = k ? (value_of(k) - v.ref) * a.scale - log_l : -INFINITY;
+                    a.top_index[row * a.top + j] = k ? column_of(k) : -1;
                 }
             }
         }
@@ -249,39 +280,52 @@ struct BwdArgs {
     void* out;
 };
 
+// U runs of a thread in flight; a run is four pairs of bf16 or two of fp32.
 template <typename T>
 __global__ void __launch_bounds__(256)
 logprobs_bwd(const BwdArgs a)
 {
+    constexpr int U = 4, V = Run<T>::V;
     for (int64_t item = blockIdx.x; item < a.rows * a.chunks; item += gridDim.x) {
         const int64_t row = item / a.chunks;
         const T* z = static_cast<const T*>(a.logits) + row * a.ld;
         T* o = static_cast<T*>(a.out) + row * a.ldo;
         const Runs<T> ro(o, a.n);
-        const int token = column_of(a.tokens, a.wide, row, a.n);
-        const float ref = a.stats[3 * row], inv = a.stats[3 * row + 1], U = a.stats[3 * row + 2];
+        const int token = vocab::column_of(a.tokens, a.wide, row, a.n);
+        const float ref = a.stats[3 * row], inv = a.stats[3 * row + 1], H = a.stats[3 * row + 2];
         const float g = a.g ? a.g[row] : 0.0f, ge = a.ge ? a.ge[row] : 0.0f;
-        const float A = -a.scale * inv * fmaf(ge, U, g), B = -a.scale * inv * ge * kLn2;
+        const float2 A = f2(-a.scale * inv * fmaf(ge, H, g)), B = f2(-a.scale * inv * ge * kLn2), R = f2(-ref), K = f2(a.k2);
         const bool none = token < 0 || inv == 0.0f;
-        const int u0 = (int)(item % a.chunks) * a.per, u1 = min(u0 + a.per, ro.count);
-        for (int u = u0 + threadIdx.x; u < u1; u += blockDim.x) {
-            const int c = ro.column(u);
-            float f[8];
-            if (none) {
+        const int u0 = (int)(item % a.chunks) * a.per, u1 = min(u0 + a.per, ro.count), step = blockDim.x;
+        for (int u = u0 + threadIdx.x; u < u1; u += U * step) {
+            uint4 w[U];
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    f[j] = 0.0f;
-            } else {
-                load8_at(z, a.n, c, f);
+            for (int i = 0; i < U; ++i)
+                w[i] = !none && u + i * step < u1 ? load_run(z, a.n, ro.column(u + i * step)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float t = at_least_zero_power((f[j] - ref) * a.k2);
-                    f[j] = exp2_approx(t) * fmaf(B, t, A);
-                    if (c + j == token)
-                        f[j] = fmaf(a.scale, g, f[j]);
+            for (int i = 0; i < U; ++i) {
+                if (u + i * step >= u1)
+                    break;
+                const int c = ro.column(u + i * step);
+                if (!none) {
+                    float2 f[V / 2];
+                    Run<T>::widen(w[i], f);
+#pragma unroll
+                    for (int j = 0; j < V / 2; ++j) {
+                        float2 t = mul2(add2(f[j], R), K);
+                        t = make_float2(at_least_zero_power(t.x), at_least_zero_power(t.y));
+                        f[j] = mul2(exp2_pair(t), fma2(B, t, A));
+                    }
+                    if (token >= c && token < c + V) {
+#pragma unroll
+                        for (int j = 0; j < V; ++j)
+                            if (c + j == token)
+                                (j & 1 ? f[j >> 1].y : f[j >> 1].x) += a.scale * g;
+                    }
+                    w[i] = Run<T>::narrow(f);
                 }
+                store_run(ro, o, u + i * step, 0, a.n, w[i]);
             }
-            store_run(ro, o, u, f);
         }
     }
 }
@@ -289,16 +333,16 @@ logprobs_bwd(const BwdArgs a)
 template <typename T, bool TOP>
 int launch_fwd(Args a, cudaStream_t s)
 {
-    const Split sp = split(a.rows, a.n);
-    a.cluster = sp.cluster;
-    const cudaError_t e = launch_rows(logprobs_fwd<T, TOP>, a, sp, TOP ? TopSmem::bytes(sp.threads) : 0, s);
+    const Split sp = split(a.rows, a.n, sizeof(T));
+    a.cluster = sp.cluster, a.runs = sp.runs;
+    const cudaError_t e = launch_rows(logprobs_fwd<T, TOP>, a, sp, sp.threads, sp.smem() + (TOP ? sizeof(TopSmem) : 0), s);
     return e == cudaSuccess ? launch_status() : cuda_failure(e);
 }
 
 template <typename T>
 int launch_bwd(BwdArgs a, cudaStream_t s)
 {
-    const int64_t runs = (a.n + 14) / 8;  // with a head and a tail
+    const int64_t runs = (a.n * (int64_t)sizeof(T) + 15) / 16 + 1;  // with a head and a tail
     const int threads = threads_for(runs, 256);
     a.per = threads * 8;
     a.chunks = (int)((runs + a.per - 1) / a.per);

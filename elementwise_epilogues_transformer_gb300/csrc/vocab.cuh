@@ -1,11 +1,19 @@
 // vocab.cuh -- what the operators on rows of logits share: a row's elements
-// as runs of 8, the running softmax statistics, and joining them over a block
-// and the blocks of a cluster.
+// as 16-byte runs kept in shared memory, the running softmax statistics, and
+// joining them over a block and the blocks of a cluster.
 //
 // With p = softmax(scale * z), the exponents are t = (z - max) * scale * log2 e
-// <= 0, formed by one subtraction (exact next to the maximum) and one product.
-// They are held at -200 from below, where 2^t is zero: columns at -inf then
-// add nothing, also to sums of e * t, and NaN stays NaN.
+// <= 0, formed by one subtraction (exact next to the maximum) and one product,
+// two elements an instruction.  Where t is a factor it is held at -200 from
+// below, where 2^t is zero: columns at -inf then add nothing to sums of e * t,
+// and NaN stays NaN.
+//
+// A row is cut into as many slices as leave a block 64 KB or less, one block
+// of a cluster each.  A block copies its slice to shared memory (16 bytes an
+// asynchronous copy, every thread its own runs, so that it waits for nobody)
+// and reads it there as often as it has to: HBM sees the row once.  Three
+// blocks share a multiprocessor: while one of them waits or sorts, the others'
+// copies are under way.
 #pragma once
 
 #include "mfx_device.cuh"
@@ -15,6 +23,17 @@ namespace mfx {
 namespace vocab {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+#ifndef MFX_VOCAB_THREADS
+#define MFX_VOCAB_THREADS 256
+#endif
+#ifndef MFX_VOCAB_RUNS
+#define MFX_VOCAB_RUNS 4096
+#endif
+#ifndef MFX_VOCAB_BLOCKS
+#define MFX_VOCAB_BLOCKS 3
+#endif
+constexpr int kThreadsMost = MFX_VOCAB_THREADS;  // threads of a block that share a slice
+constexpr int kSliceRuns = MFX_VOCAB_RUNS;       // runs of 16 bytes that a block keeps
 
 __device__ __forceinline__ float exp2_approx(float t)
 {
@@ -31,32 +50,130 @@ __device__ __forceinline__ float at_least_zero_power(float t)
     return r;
 }
 
-// n elements from p on as runs of 8 columns that begin at multiples of 16 bytes:
-// run u holds columns [8u - phase, 8u - phase + 8) of [0, n).
+__device__ __forceinline__ float2 exp2_pair(float2 t) { return make_float2(exp2_approx(t.x), exp2_approx(t.y)); }
+
+// The elements of a 16-byte run as fp32 pairs, their maximum (NaN counts for
+// nothing), and a run of -inf.
+template <typename T> struct Run;
+template <> struct Run<bf16> {
+    static constexpr int V = 8;
+    static __device__ __forceinline__ uint4 none() { return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
+    static __device__ __forceinline__ void widen(const uint4& w, float2 (&f)[4])
+    {
+        f[0] = widen2(w.x), f[1] = widen2(w.y), f[2] = widen2(w.z), f[3] = widen2(w.w);
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+    {
+        uint32_t r;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ float top(const uint4& w)
+    {
+        const float2 m = widen2(max2(max2(w.x, w.y), max2(w.z, w.w)));
+        return fmaxf(m.x, m.y);
+    }
+    static __device__ __forceinline__ uint4 narrow(const float2 (&f)[4])
+    {
+        return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                          pack_bf16x2(f[3].x, f[3].y));
+    }
+};
+template <> struct Run<float> {
+    static constexpr int V = 4;
+    static __device__ __forceinline__ uint4 none() { return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u); }
+    static __device__ __forceinline__ void widen(const uint4& w, float2 (&f)[2])
+    {
+        f[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+        f[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+    }
+    static __device__ __forceinline__ float top(const uint4& w)
+    {
+        return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+    }
+    static __device__ __forceinline__ uint4 narrow(const float2 (&f)[2])
+    {
+        return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+    }
+};
+
+// n elements from p on as runs of 16 bytes that begin at multiples of 16
+// bytes: run u holds columns [V u - phase, V u - phase + V) of [0, n).
 template <typename T> struct Runs {
+    static constexpr int V = Run<T>::V;
     const T* p;
     int n, phase, count;
     __device__ __forceinline__ Runs(const T* p_, int n_)
-        : p(p_), n(n_), phase((int)((reinterpret_cast<uintptr_t>(p_) & 15u) / sizeof(T))), count((n_ + phase + 7) / 8)
+        : p(p_), n(n_), phase((int)((reinterpret_cast<uintptr_t>(p_) & 15u) / sizeof(T))),
+          count((int)(((int64_t)n_ + phase + V - 1) / V))
     {
     }
-    __device__ __forceinline__ int column(int u) const { return 8 * u - phase; }
-    __device__ __forceinline__ bool whole(int u) const { return 8 * u >= phase && 8 * u - phase + 8 <= n; }
-    // Run u (raw), `fill` where it has no element.
-    __device__ __forceinline__ void load(int u, float f[8]) const
-    {
-        const int c = column(u);
-        if (whole(u)) {
-            Raw8<T> r;
-            ld8(p + c, r);
-            widen8(r, f);
-        } else {
+    __device__ __forceinline__ int column(int u) const { return V * u - phase; }
+    __device__ __forceinline__ bool whole(int u) const { return V * u >= phase && V * u - phase + V <= n; }
+};
+
+// V elements of a row of n from column c on, -inf where there is none, element
+// by element.
+template <typename T>
+__device__ __noinline__ uint4 edge_run(const T* row, int n, int c)
+{
+    constexpr int V = Run<T>::V;
+    uint4 w = Run<T>::none();
+    if constexpr (V == 8) {
+        uint32_t h[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                f[j] = c + j >= 0 && c + j < n ? load1(p + c + j) : -INFINITY;
+        for (int j = 0; j < 8; ++j)
+            h[j] = c + j >= 0 && c + j < n ? (uint32_t)row[c + j].bits : 0xFF80u;
+        w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    } else {
+        const auto at = [&](int i) { return i >= 0 && i < n ? __float_as_uint(row[i]) : 0xFF800000u; };
+        w = make_uint4(at(c), at(c + 1), at(c + 2), at(c + 3));
+    }
+    return w;
+}
+
+// The same at any alignment, through the two aligned vectors that hold it
+// where those lie in the row.
+template <typename T>
+__device__ __forceinline__ uint4 load_run(const T* row, int n, int c)
+{
+    constexpr int V = Run<T>::V;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(row + c), v = a & ~(uintptr_t)15;
+    const uint32_t off = (uint32_t)(a & 15u);
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(row), hi = reinterpret_cast<uintptr_t>(row + n);
+    if (c >= 0 && c + V <= n) {
+        if (off == 0)
+            return ld16(reinterpret_cast<const void*>(a));
+        if (v >= lo && v + 32 <= hi) {
+            const uint4 p = ld16_ca(reinterpret_cast<const void*>(v)), q = ld16_ca(reinterpret_cast<const void*>(v + 16));
+            const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+            return extract16(w, off);
         }
     }
-};
+    return edge_run(row, n, c);
+}
+
+// Stores a run's elements that lie in columns [lo, hi) at run v of an output
+// row.
+template <typename T>
+__device__ __forceinline__ void store_run(const Runs<T>& o, T* row, int v, int lo, int hi, const uint4& w)
+{
+    constexpr int V = Run<T>::V;
+    const int c = o.column(v);
+    if (c >= lo && c + V <= hi) {
+        st16(row + c, w);
+    } else {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (c + j >= lo && c + j < hi) {
+                if constexpr (V == 8)
+                    row[c + j].bits = (uint16_t)(j & 1 ? x[j >> 1] >> 16 : x[j >> 1]);
+                else
+                    row[c + j] = __uint_as_float(x[j]);
+            }
+    }
+}
 
 // Running statistics of some of a row's elements: their maximum (-inf for
 // none), the reference that the exponents are taken from (the maximum, or the
@@ -75,58 +192,39 @@ __device__ __forceinline__ void rebase(Stats& v, float ref, float k2)
     v.ref = ref;
 }
 
-__device__ __forceinline__ Stats join(Stats a, Stats b, float k2)
+// Joins the statistics of 2^LEVELS neighbouring lanes, the same bits in each:
+// their references' maximum first, so that each is rebased once.
+template <int LEVELS, bool ENTROPY>
+__device__ __forceinline__ void join_lanes(Stats& v, float k2)
 {
-    const float ref = fmaxf(a.ref, b.ref);
-    rebase(a, ref, k2);
-    rebase(b, ref, k2);
-    return {fmaxf(a.m, b.m), ref, a.l + b.l, a.s + b.s};
-}
-
-__device__ __forceinline__ Stats shfl_xor(Stats v, int o)
-{
-    return {__shfl_xor_sync(0xFFFFFFFFu, v.m, o), __shfl_xor_sync(0xFFFFFFFFu, v.ref, o),
-            __shfl_xor_sync(0xFFFFFFFFu, v.l, o), __shfl_xor_sync(0xFFFFFFFFu, v.s, o)};
-}
-
-// The block's statistics in every thread, joined in a fixed order.
-// `part`: 32 of them in shared memory, free again after the next barrier.
-__device__ __forceinline__ Stats join_block(Stats v, float k2, Stats* part)
-{
+    float ref = v.ref;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v = join(v, shfl_xor(v, o), k2);
-    const int warps = blockDim.x >> 5;
-    if (warps > 1) {
-        if ((threadIdx.x & 31) == 0)
-            part[threadIdx.x >> 5] = v;
-        __syncthreads();
-        const int lane = threadIdx.x & 31;
-        v = lane < warps ? part[lane] : no_stats();
+    for (int o = 1 << (LEVELS - 1); o > 0; o >>= 1)
+        ref = fmaxf(ref, __shfl_xor_sync(0xFFFFFFFFu, ref, o));
+    rebase(v, ref, k2);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            v = join(v, shfl_xor(v, o), k2);
+    for (int o = 1 << (LEVELS - 1); o > 0; o >>= 1) {
+        v.l += __shfl_xor_sync(0xFFFFFFFFu, v.l, o);
+        if (ENTROPY)
+            v.s += __shfl_xor_sync(0xFFFFFFFFu, v.s, o);
     }
-    return v;
 }
 
-// Adds up e and e * t of eight elements.
-__device__ __forceinline__ void add8(Stats& v, const float z[8], float k2)
+// The statistics of the block's first `warps` warps (at most 8) in every
+// thread, joined in a fixed order.  `part`: 8 of them in shared memory, free
+// again after the next barrier.  A barrier in any case.
+template <bool ENTROPY>
+__device__ __forceinline__ void join_block(Stats& v, float k2, Stats* part, int warps)
 {
-    float l = 0.0f, s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float t = at_least_zero_power((z[j] - v.ref) * k2), e = exp2_approx(t);
-        l += e;
-        s = fmaf(e, t, s);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (warp < warps) {
+        join_lanes<5, ENTROPY>(v, k2);
+        if (lane == 0)
+            part[warp] = v;
     }
-    v.l += l;
-    v.s += s;
-}
-
-__device__ __forceinline__ float max8(const float z[8])
-{
-    return fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
+    __syncthreads();
+    v = (lane & 7) < warps ? part[lane & 7] : no_stats();
+    join_lanes<3, ENTROPY>(v, k2);
 }
 
 // Element i of an index array of 32 or 64 bits; a value that is no column of
@@ -137,8 +235,203 @@ __device__ __forceinline__ int column_of(const void* index, bool wide, int64_t i
     return c >= 0 && c < n ? (int)c : -1;
 }
 
-// --- clusters -------------------------------------------------------------
+// --- a block's slice of a row ----------------------------------------------
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from)
+{
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t a, const uint4& v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+constexpr int kGroups = 4;  // copies are waited for in four steps
+
+// Runs [first, last) of a row in shared memory at `buf` (16-byte aligned, one
+// run to spare before and behind).  Those of [whole0, whole1) are whole; one at
+// the row's head and one at its tail may not be.
+template <typename T> struct Piece {
+    Runs<T> r;
+    int first, last, whole0, whole1, step;
+    uint32_t buf;
+
+    // step: the threads that share it (the block's first ones)
+    __device__ __forceinline__ Piece(const Runs<T>& r_, uint32_t buf_, int step_) : r(r_), step(step_), buf(buf_) {}
+    __device__ __forceinline__ void set(int f, int l)
+    {
+        first = f, last = l;
+        whole0 = f < l && !r.whole(f) ? f + 1 : f;
+        whole1 = whole0 < l && !r.whole(l - 1) ? l - 1 : l;
+    }
+    __device__ __forceinline__ uint32_t at(int u) const { return buf + 16u * (uint32_t)(u - first + 1); }
+    // runs of a thread that a step copies
+    __device__ __forceinline__ int each() const
+    {
+        const int mine = (last - first + step - 1) / step;
+        return max((mine + kGroups - 1) / kGroups, min(mine, 4));
+    }
+    // Starts the copies of this thread's runs: every step-th.
+    __device__ __forceinline__ void fill() const
+    {
+        const int n = each();
+        int u = first + threadIdx.x;
+        if (u < whole0)
+            sts16(at(u), edge_run(r.p, r.n, r.column(u)));
+        if (whole1 < last && (last - 1 - u) % step == 0 && last - 1 >= u)
+            sts16(at(last - 1), edge_run(r.p, r.n, r.column(last - 1)));
+        const T* from = r.p + r.column(u);
+        uint32_t to = at(u);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+#pragma unroll 4
+            for (int i = 0; i < n; ++i, u += step, from += step * Run<T>::V, to += 16u * step)
+                if (u >= whole0 && u < whole1)
+                    copy16(to, from);
+            copies_commit();
+        }
+    }
+    // Columns [lo, hi) that it holds.
+    __device__ __forceinline__ int lo() const { return max(r.column(first), 0); }
+    __device__ __forceinline__ int hi() const { return min(r.column(last), r.n); }
+    // One of those columns' elements.
+    __device__ __forceinline__ float value(int c) const
+    {
+        const uint32_t a = buf + 16u + (uint32_t)(c - r.column(first)) * (uint32_t)sizeof(T);
+        if constexpr (sizeof(T) == 2) {
+            uint16_t h;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(a) : "memory");
+            return __uint_as_float((uint32_t)h << 16);
+        } else {
+            float f;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a) : "memory");
+            return f;
+        }
+    }
+    // V elements from column c on, at any alignment (some may lie outside).
+    __device__ __forceinline__ uint4 run_at(int c) const
+    {
+        const uint32_t a = buf + 16u + (uint32_t)((c - r.column(first)) * (int)sizeof(T)), off = a & 15u;
+        const uint4 p = lds16(a - off);
+        if (off == 0)
+            return p;
+        const uint4 q = lds16(a - off + 16);
+        const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+        return extract16(w, off);
+    }
+};
+
+// A thread's best run: its maximum, and which.
+struct BestRun {
+    float m;
+    int u;
+};
+
+// Takes U runs of a thread (from u on, every `step`) into its statistics.
+template <typename T, bool ENTROPY, bool BEST, int U>
+__device__ __forceinline__ void take(Stats& v, BestRun& best, const uint4 (&w)[U], int u, int step, float k2)
+{
+    float m[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+        m[i] = Run<T>::top(w[i]);
+    float top = m[0];
+#pragma unroll
+    for (int i = 1; i < U; ++i)
+        top = fmaxf(top, m[i]);
+    if (BEST) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (m[i] > best.m)
+                best = {m[i], u + i * step};
+    }
+    if (top > v.m) {
+        v.m = top;
+        rebase(v, fmaxf(top, v.ref), k2);
+    }
+    const float2 ref = f2(-v.ref), k = f2(k2);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        constexpr int P = Run<T>::V / 2;
+        float2 f[P], e[P], s = f2(0.0f);
+        Run<T>::widen(w[i], f);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            float2 t = mul2(add2(f[j], ref), k);
+            if (ENTROPY)
+                t = make_float2(at_least_zero_power(t.x), at_least_zero_power(t.y));
+            e[j] = exp2_pair(t);
+            if (ENTROPY)
+                s = fma2(e[j], t, s);
+        }
+#pragma unroll
+        for (int o = 1; o < P; o *= 2)
+#pragma unroll
+            for (int j = 0; j + o < P; j += 2 * o)
+                e[j] = add2(e[j], e[j + o]);
+        v.l += e[0].x + e[0].y;
+        if (ENTROPY)
+            v.s += s.x + s.y;
+    }
+}
+
+// This thread's runs of a piece whose copies are under way.
+template <typename T, bool ENTROPY, bool BEST>
+__device__ __forceinline__ void scan(const Piece<T>& p, float k2, Stats& v, BestRun& best)
+{
+    constexpr int U = 4;
+    const int n = p.each(), step = p.step;
+    int u = p.first + threadIdx.x;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        if (g == 0)
+            copies_wait<3>();
+        else if (g == 1)
+            copies_wait<2>();
+        else if (g == 2)
+            copies_wait<1>();
+        else
+            copies_wait<0>();
+        const int end = u + n * step;
+#pragma unroll 1
+        for (; u + (U - 1) * step < p.last && u + (U - 1) * step < end; u += U * step) {
+            uint4 w[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                w[j] = lds16(p.at(u) + 16u * (uint32_t)(j * step));
+            take<T, ENTROPY, BEST, U>(v, best, w, u, step, k2);
+        }
+#pragma unroll 1
+        for (; u < end; u += step)
+            if (u < p.last) {
+                uint4 w[1];
+                w[0] = lds16(p.at(u));
+                take<T, ENTROPY, BEST, 1>(v, best, w, u, step, k2);
+            }
+    }
+}
+
+// --- clusters -------------------------------------------------------------
+// The same in two steps; the second one alone orders nothing.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
@@ -157,19 +450,32 @@ __device__ __forceinline__ uint32_t peer_word(const void* p, uint32_t rank)
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
+__device__ __forceinline__ float peer_float(const float* p, uint32_t rank) { return __uint_as_float(peer_word(p, rank)); }
 
-__device__ __forceinline__ Stats peer_stats(const Stats* p, uint32_t rank)
+// Statistics over the blocks of a cluster (at most 8) from each block's.
+template <bool ENTROPY>
+__device__ __forceinline__ void join_cluster(Stats& v, float k2, Stats* mine, int blocks)
 {
-    return {__uint_as_float(peer_word(&p->m, rank)), __uint_as_float(peer_word(&p->ref, rank)),
-            __uint_as_float(peer_word(&p->l, rank)), __uint_as_float(peer_word(&p->s, rank))};
+    if (threadIdx.x == 0)
+        *mine = v;
+    cluster_sync();
+    const int peer = threadIdx.x & 7;
+    v = no_stats();
+    if (peer < blocks) {
+        v.ref = peer_float(&mine->ref, peer), v.l = peer_float(&mine->l, peer);
+        if (ENTROPY)
+            v.s = peer_float(&mine->s, peer);
+    }
+    join_lanes<3, ENTROPY>(v, k2);
 }
 
 // --- host -----------------------------------------------------------------
-constexpr int64_t kMostColumns = 1 << 30;
+constexpr int64_t kMostColumns = 1 << 30, kMostClusters = 1 << 26;
 
-// Blocks of a row and threads of a block.
+// Blocks of a row, threads of a block, and runs that it keeps.
 struct Split {
-    int cluster, threads;
+    int cluster, threads, runs;
+    size_t smem() const { return (size_t)(runs + 2) * 16; }
 };
 
 // A thread has four runs or more of its row, up to `most` threads.
@@ -181,26 +487,36 @@ inline int threads_for(int64_t runs, int most)
     return t;
 }
 
-// A block works on a row; where rows are too few for all multiprocessors, the
-// blocks of a cluster do.
-inline Split split(int64_t rows, int64_t n)
+// A block works on a row of 64 KB or less, the blocks of a cluster on longer
+// ones; where rows are too few for all multiprocessors, on shorter ones too.
+// `runs`: what a block keeps in shared memory at a time (rows longer than a
+// cluster of 8 holds are taken in pieces).
+inline Split split(int64_t rows, int64_t n, int64_t bytes)
 {
-    const int64_t runs = (n + 7) / 8;
-    Split sp = {1, 0};
-    while (sp.cluster < 8 && rows * sp.cluster * 2 <= sm_count() && runs >= sp.cluster * 2 * 512)
+    const int64_t all = (n * bytes + 15) / 16 + 1;  // with a head and a tail
+    Split sp = {1, 0, 0};
+    sp.cluster = (int)((all + kSliceRuns) / (kSliceRuns + 1));
+    if (sp.cluster > 8)
+        sp.cluster = 8;
+    while (sp.cluster * 2 <= 8 && rows * sp.cluster * 2 <= sm_count() && all >= sp.cluster * 2 * 2 * kThreadsMost)
         sp.cluster *= 2;
-    sp.threads = threads_for(runs / sp.cluster, 512);
+    const int64_t slice = (all + sp.cluster - 1) / sp.cluster;
+    sp.threads = threads_for(slice, kThreadsMost);
+    sp.runs = (int)(slice <= kSliceRuns + 1 ? slice : kSliceRuns);
     return sp;
 }
 
 // Launches a kernel over rows (grid.x / cluster at a time).
 template <typename A>
-cudaError_t launch_rows(void (*kernel)(const A), const A& a, const Split& sp, size_t smem, cudaStream_t s)
+cudaError_t launch_rows(void (*kernel)(const A), const A& a, const Split& sp, int threads, size_t smem, cudaStream_t s)
 {
-    const int64_t room = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(kernel), sp.threads, smem);
+    const int64_t room = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(kernel), threads, smem);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(sp.cluster > 1 || a.rows < room ? a.rows * sp.cluster : room));
-    cfg.blockDim = dim3((unsigned)sp.threads);
+    // the blocks of a cluster find places together, which leaves some of them
+    // free: clusters come row by row, single blocks stay
+    cfg.gridDim = dim3((unsigned)(sp.cluster > 1 ? (a.rows < kMostClusters ? a.rows : kMostClusters) * sp.cluster
+                                                 : a.rows < room ? a.rows : room));
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -232,165 +548,6 @@ inline bool rows_alias_ok(const void* out, int64_t ldo, const void* in, int64_t 
                           int64_t size)
 {
     return !overlaps(out, span(rows, cols, ldo, size), in, span(rows, cols, ldi, size)) || (out == in && ldo == ldi);
-}
-
-}  // namespace vocab
-}  // namespace mfx
-
-namespace mfx {
-namespace vocab {
-
-// A block's share of a row: whole runs [first, last), and for its thread 0
-// the run at the row's head (run 0, which ends before the first whole one)
-// and the one at its tail, where they are not whole.
-template <typename T> struct Share {
-    Runs<T> r;
-    int first, last;
-    bool head, tail;
-    __device__ __forceinline__ Share(const Runs<T>& r_, int rank, int blocks) : r(r_)
-    {
-        const int w0 = r.count > 0 && !r.whole(0) ? 1 : 0;
-        int w1 = r.count > w0 && !r.whole(r.count - 1) ? r.count - 1 : r.count;
-        const int per = (w1 - w0 + blocks - 1) / blocks;
-        first = min(w0 + rank * per, w1);
-        last = min(first + per, w1);
-        head = w0 == 1 && rank == 0;
-        tail = w1 < r.count && rank == blocks - 1;
-    }
-};
-
-// A column and its logit.  Better: a larger logit, or an equal one further
-// left.  Threads that saw none have a place of their own behind all columns.
-struct Pick {
-    float v;
-    int i;
-};
-__device__ __forceinline__ bool better(const Pick& a, const Pick& b) { return a.v > b.v || (a.v == b.v && a.i < b.i); }
-
-// Takes U runs of a thread into its statistics; `best` is its best column.
-template <bool BEST, int U>
-__device__ __forceinline__ void take(Stats& v, Pick& best, const float (&z)[U][8], const int (&c)[U], float k2)
-{
-    float m = max8(z[0]);
-#pragma unroll
-    for (int i = 1; i < U; ++i)
-        m = fmaxf(m, max8(z[i]));
-    if (m > v.m) {
-        if (BEST) {
-            best.v = m;
-#pragma unroll
-            for (int i = U - 1; i >= 0; --i)
-#pragma unroll
-                for (int j = 7; j >= 0; --j)
-                    if (z[i][j] == m)
-                        best.i = c[i] + j;
-        }
-        v.m = m;
-        rebase(v, fmaxf(m, v.ref), k2);
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-        add8(v, z[i], k2);
-}
-
-// A thread's statistics over its part of a block's share: every blockDim-th
-// whole run, U of them in flight.
-template <typename T, bool BEST, int U>
-__device__ __forceinline__ Stats scan(const Share<T>& sh, float k2, Pick& best)
-{
-    Stats v = no_stats();
-    best = {-INFINITY, (int)kMostColumns + (int)threadIdx.x};
-    if (threadIdx.x == 0 && sh.head) {
-        float z[1][8];
-        const int c[1] = {sh.r.column(0)};
-        sh.r.load(0, z[0]);
-        take<BEST, 1>(v, best, z, c, k2);
-    }
-    const int step = blockDim.x;
-    for (int u = sh.first + threadIdx.x; u < sh.last; u += U * step) {
-        Raw8<T> r[U];
-        float z[U][8];
-        int c[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            c[i] = sh.r.column(u + i * step);
-            if (u + i * step < sh.last)
-                ld8(sh.r.p + c[i], r[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (u + i * step < sh.last) {
-                widen8(r[i], z[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    z[i][j] = -INFINITY;
-            }
-        }
-        take<BEST, U>(v, best, z, c, k2);
-    }
-    if (threadIdx.x == 0 && sh.tail) {
-        float z[1][8];
-        const int c[1] = {sh.r.column(sh.r.count - 1)};
-        sh.r.load(sh.r.count - 1, z[0]);
-        take<BEST, 1>(v, best, z, c, k2);
-    }
-    return v;
-}
-
-// Statistics over the blocks of a cluster from each block's.
-__device__ __forceinline__ Stats join_cluster(Stats v, float k2, Stats* mine, int blocks)
-{
-    if (threadIdx.x == 0)
-        *mine = v;
-    cluster_sync();
-    const int lane = threadIdx.x & 31;
-    v = lane < blocks ? peer_stats(mine, lane) : no_stats();
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1)
-        v = join(v, shfl_xor(v, o), k2);
-    const Stats w = {__shfl_sync(0xFFFFFFFFu, v.m, 0), __shfl_sync(0xFFFFFFFFu, v.ref, 0),
-                     __shfl_sync(0xFFFFFFFFu, v.l, 0), __shfl_sync(0xFFFFFFFFu, v.s, 0)};
-    return w;
-}
-
-// Eight elements of a row of n from column c on (some of them may lie outside:
-// `fill`), at any alignment.
-template <typename T>
-__device__ __forceinline__ void load8_at(const T* row, int n, int c, float f[8])
-{
-    const T* p = row + c;
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(row), hi = reinterpret_cast<uintptr_t>(row + n);
-    if (c >= 0 && c + 8 <= n && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-        Raw8<T> r;
-        ld8(p, r);
-        widen8(r, f);
-    } else if (c >= 0 && c + 8 <= n && in_vectors(p, lo, hi)) {
-        Raw8<T> r;
-        ld8_any(p, r);
-        widen8(r, f);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            f[j] = c + j >= 0 && c + j < n ? load1(p + j) : -INFINITY;
-    }
-}
-
-// Stores run u of an output row.
-template <typename T>
-__device__ __forceinline__ void store_run(const Runs<T>& o, T* row, int u, const float f[8])
-{
-    const int c = o.column(u);
-    if (o.whole(u)) {
-        Raw8<T> r;
-        narrow8(f, r);
-        st8(row + c, r);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c + j >= 0 && c + j < o.n)
-                store1(row + c + j, f[j]);
-    }
 }
 
 }  // namespace vocab
