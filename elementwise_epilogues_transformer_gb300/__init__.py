@@ -11,7 +11,6 @@ Megatron [seq, batch, hidden] layout is accepted as is.
 
 There is no fallback: if ``libmfx.so`` has not been built, every call raises.
 """
-import contextlib
 import ctypes as C
 import math
 import os
@@ -637,54 +636,62 @@ def mfx_moe_unpermute_bwd(g, y, row_of, slot_of, weight=None, dy=None, dweight=N
 # ---------------------------------------------------------------------------
 # root-mean-square norm with the residual's addition
 # ---------------------------------------------------------------------------
-_NOTHING = contextlib.nullcontext()
+_DTYPES = {torch.bfloat16: MFX_BF16, torch.float32: MFX_F32}
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _here(t):
-    """Context in which t's device is the current one (launches go there)."""
-    dev = t.get_device()
-    return _NOTHING if dev == torch.cuda.current_device() else torch.cuda.device(dev)
-
-
-def _rows_of(t, name, rows, dtype, dev):
-    """t is a vector of one element per row, on the data's device."""
-    _like(t, name, (rows,), dtype)
+def _buf(t, name, shape, dtype, dev):
+    """The address of t, a contiguous tensor of this shape and dtype on device
+    dev; says what is wrong otherwise."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _like(t, name, shape, dtype)
     _same_device(t, dev, name)
     return t.data_ptr()
 
 
-def _norm_args(x, weight, residual):
-    """What the two forwards check: (rows, cols, device, types, pointers)."""
-    _cuda(x, "x")
-    if x.dim() == 0:
-        raise ValueError("x must have at least one dim")
-    rows, cols = math.prod(x.shape[:-1]), x.shape[-1]
-    dev = x.get_device()
-    xdt = rdt = wdt = dtype_code(x.dtype)
-    rptr = None
-    if residual is not None:
-        _like(_cuda(residual, "residual"), "residual", x.shape, residual.dtype)
-        _same_device(residual, dev, "residual")
-        rdt, rptr = dtype_code(residual.dtype), residual.data_ptr()
-    if weight is not None:
-        _like(_cuda(weight, "weight"), "weight", (cols,), weight.dtype)
-        _same_device(weight, dev, "weight")
-        wdt = dtype_code(weight.dtype)
-    return rows, cols, dev, (xdt, rdt, wdt), (x.data_ptr(), rptr, _ptr(weight))
+def _new(t, name, shape, dtype, dev, like, stream):
+    """(t or memory of the call's own, its address)."""
+    if t is not None:
+        return t, _buf(t, name, shape, dtype, dev)
+    t = (torch.empty(shape, dtype=dtype, device=like.device) if stream is None
+         else _empty(shape, dtype, like.device, stream))
+    return t, t.data_ptr()
 
 
-def _norm_outputs(x, residual, rows, dev, h, rstd, need_rstd, stream):
-    if residual is None:
-        if h is not None:
-            raise ValueError("h needs a residual")
+def _run(name, dev, *args):
+    """A call whose kernels go to device dev, whichever is the current one."""
+    fn = getattr(_lib or lib(), name)
+    if dev == _current_device():
+        st = fn(*args)
     else:
-        h = _empty_like(residual, stream) if h is None else _like(h, "h", x.shape, residual.dtype)
-        _same_device(h, dev, "h")
-    if rstd is not None:
-        _rows_of(rstd, "rstd", rows, torch.float32, dev)
-    elif need_rstd:
-        rstd = _empty((rows,), torch.float32, x.device, stream)
-    return h, rstd
+        with torch.cuda.device(dev):
+            st = fn(*args)
+    if st != 0:
+        raise MfxError(st, name)
+
+
+def _stream_of(stream, t, dev):
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream, t)
+
+
+def _float_code(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    code = _DTYPES.get(t.dtype)
+    return dtype_code(t.dtype) if code is None else code
+
+
+def _norm_data(x, name):
+    """(type code, device, shape, rows, cols) of the norm's data."""
+    code = _float_code(x, name)
+    dev, shape = x.get_device(), x.shape
+    if dev < 0 or not x.is_contiguous() or not shape:
+        _cuda(x, name)
+        raise ValueError(f"{name} must have at least one dim")
+    cols = shape[-1]
+    return code, dev, shape, x.numel() // cols if cols else math.prod(shape[:-1]), cols
 
 
 def mfx_add_rmsnorm_fwd(x, weight, residual=None, eps=1e-6, weight_offset=0.0, y=None, h=None, rstd=None,
@@ -693,13 +700,23 @@ def mfx_add_rmsnorm_fwd(x, weight, residual=None, eps=1e-6, weight_offset=0.0, y
     residual), y = h * rstd * (weight + weight_offset) over the last dim with
     rstd = 1 / sqrt(mean(h^2) + eps) ([rows], None with need_rstd=False).
     weight [cols] may be None."""
-    rows, cols, dev, types, data = _norm_args(x, weight, residual)
-    y = _empty_like(x, stream) if y is None else _like(y, "y", x.shape, x.dtype)
-    _same_device(y, dev, "y")
-    h, rstd = _norm_outputs(x, residual, rows, dev, h, rstd, need_rstd, stream)
-    with _here(x):
-        _call("mfx_add_rmsnorm_fwd", *types, rows, cols, *data, float(eps), float(weight_offset), y.data_ptr(), _ptr(h),
-              _ptr(rstd), _stream(stream, x))
+    xdt, dev, shape, rows, cols = _norm_data(x, "x")
+    rdt = wdt = xdt
+    rptr = wptr = hptr = sptr = None
+    if weight is not None:
+        wdt = _float_code(weight, "weight")
+        wptr = _buf(weight, "weight", (cols,), weight.dtype, dev)
+    if residual is not None:
+        rdt = _float_code(residual, "residual")
+        rptr = _buf(residual, "residual", shape, residual.dtype, dev)
+        h, hptr = _new(h, "h", shape, residual.dtype, dev, x, stream)
+    elif h is not None:
+        raise ValueError("h needs a residual")
+    y, yptr = _new(y, "y", shape, x.dtype, dev, x, stream)
+    if need_rstd or rstd is not None:
+        rstd, sptr = _new(rstd, "rstd", (rows,), torch.float32, dev, x, stream)
+    _run("mfx_add_rmsnorm_fwd", dev, xdt, rdt, wdt, rows, cols, x.data_ptr(), rptr, wptr, float(eps),
+         float(weight_offset), yptr, hptr, sptr, _stream_of(stream, x, dev))
     return y, h, rstd
 
 
@@ -713,22 +730,31 @@ def mfx_add_rmsnorm_quant_fwd(x, weight, residual=None, eps=1e-6, weight_offset=
     """(q, scale, h, rstd): mfx_add_rmsnorm_fwd with y in 8 bits, y ~ q *
     scale.  One scale per row (group=0) or per 32 or 128 columns of it, scale
     [..., groups]; float8_e8m0fnu scales are powers of two."""
-    rows, cols, dev, types, data = _norm_args(x, weight, residual)
-    if q_dtype not in _Q_DTYPES or scale_dtype not in _SCALE_DTYPES:
+    xdt, dev, shape, rows, cols = _norm_data(x, "x")
+    qdt, sdt = _Q_DTYPES.get(q_dtype), _SCALE_DTYPES.get(scale_dtype)
+    if qdt is None or sdt is None:
         raise TypeError("q is float8_e4m3fn or float8_e5m2, scale float32 or float8_e8m0fnu")
     group = int(group)
     if group not in (0, 32, 128):
         raise MfxError(9, "mfx_add_rmsnorm_quant_fwd")
+    rdt = wdt = xdt
+    rptr = wptr = hptr = sptr = None
+    if weight is not None:
+        wdt = _float_code(weight, "weight")
+        wptr = _buf(weight, "weight", (cols,), weight.dtype, dev)
+    if residual is not None:
+        rdt = _float_code(residual, "residual")
+        rptr = _buf(residual, "residual", shape, residual.dtype, dev)
+        h, hptr = _new(h, "h", shape, residual.dtype, dev, x, stream)
+    elif h is not None:
+        raise ValueError("h needs a residual")
     groups = -(-cols // group) if group else min(cols, 1)
-    q = _empty(x.shape, q_dtype, x.device, stream) if q is None else _like(q, "q", x.shape, q_dtype)
-    _same_device(q, dev, "q")
-    shape = (*x.shape[:-1], groups)
-    scale = _empty(shape, scale_dtype, x.device, stream) if scale is None else _like(scale, "scale", shape, scale_dtype)
-    _same_device(scale, dev, "scale")
-    h, rstd = _norm_outputs(x, residual, rows, dev, h, rstd, need_rstd, stream)
-    with _here(x):
-        _call("mfx_add_rmsnorm_quant_fwd", *types, rows, cols, *data, float(eps), float(weight_offset), _Q_DTYPES[q_dtype],
-              group, _SCALE_DTYPES[scale_dtype], q.data_ptr(), scale.data_ptr(), _ptr(h), _ptr(rstd), _stream(stream, x))
+    q, qptr = _new(q, "q", shape, q_dtype, dev, x, stream)
+    scale, scptr = _new(scale, "scale", (*shape[:-1], groups), scale_dtype, dev, x, stream)
+    if need_rstd or rstd is not None:
+        rstd, sptr = _new(rstd, "rstd", (rows,), torch.float32, dev, x, stream)
+    _run("mfx_add_rmsnorm_quant_fwd", dev, xdt, rdt, wdt, rows, cols, x.data_ptr(), rptr, wptr, float(eps),
+         float(weight_offset), qdt, group, sdt, qptr, scptr, hptr, sptr, _stream_of(stream, x, dev))
     return q, scale, h, rstd
 
 
@@ -739,48 +765,37 @@ def mfx_add_rmsnorm_bwd(dy, h, rstd, weight, dh=None, weight_offset=0.0, dx=None
     dresidual is produced when a buffer is given or residual_dtype (h's dtype)
     is set; with dy's dtype and no buffer it is dx itself.  dweight is None
     without a weight or with need_dweight=False."""
-    _cuda(dy, "dy")
-    _cuda(h, "h")
-    if dy.dim() == 0:
-        raise ValueError("dy must have at least one dim")
-    rows, cols = math.prod(dy.shape[:-1]), dy.shape[-1]
-    dev = dy.get_device()
-    _like(h, "h", dy.shape, h.dtype)
-    _same_device(h, dev, "h")
-    _rows_of(rstd, "rstd", rows, torch.float32, dev)
-    xdt, rdt = dtype_code(dy.dtype), dtype_code(h.dtype)
-    wdt = xdt
+    xdt, dev, shape, rows, cols = _norm_data(dy, "dy")
+    rdt, wdt = _float_code(h, "h"), xdt
+    hptr = _buf(h, "h", shape, h.dtype, dev)
+    sptr = _buf(rstd, "rstd", (rows,), torch.float32, dev)
+    wptr = eptr = rptr = dwptr = None
     if weight is not None:
-        _like(_cuda(weight, "weight"), "weight", (cols,), weight.dtype)
-        _same_device(weight, dev, "weight")
-        wdt = dtype_code(weight.dtype)
+        wdt = _float_code(weight, "weight")
+        wptr = _buf(weight, "weight", (cols,), weight.dtype, dev)
     if dh is not None:
-        _like(dh, "dh", dy.shape, h.dtype)
-        _same_device(dh, dev, "dh")
-    dx = _empty_like(dy, stream) if dx is None else _like(dx, "dx", dy.shape, dy.dtype)
-    _same_device(dx, dev, "dx")
-    same = False
-    if dresidual is not None:
-        _like(dresidual, "dresidual", dy.shape, h.dtype)
-        _same_device(dresidual, dev, "dresidual")
-    elif residual_dtype is not None:
-        if residual_dtype != h.dtype:
+        eptr = _buf(dh, "dh", shape, h.dtype, dev)
+    dx, xptr = _new(dx, "dx", shape, dy.dtype, dev, dy, stream)
+    if dresidual is not None or residual_dtype is not None:
+        if residual_dtype is not None and residual_dtype != h.dtype:
             raise TypeError(f"residual_dtype must be h's, {h.dtype}")
-        same = h.dtype == dy.dtype
-        dresidual = None if same else _empty_like(h, stream)
-    if dweight is not None:
-        if weight is None:
-            raise ValueError("dweight needs a weight")
-        _like(dweight, "dweight", (cols,), weight.dtype)
-        _same_device(dweight, dev, "dweight")
-    elif weight is not None and need_dweight:
-        dweight = _empty_like(weight, stream)
-    with _here(dy):
-        head = (xdt, rdt, wdt, rows, cols, dy.data_ptr(), h.data_ptr(), rstd.data_ptr(), _ptr(weight), float(weight_offset),
-                _ptr(dh), dx.data_ptr(), _ptr(dresidual), _ptr(dweight))
-        _with_workspace("mfx_add_rmsnorm_bwd", head, (_stream(stream, dy),), dy.device, workspace,
-                        (dev, xdt, rdt, rows, cols, dweight is None), none=True, stream=stream)
-    return dx, dx if same else dresidual, dweight
+        if dresidual is None and rdt == xdt:
+            dresidual = dx
+        else:
+            dresidual, rptr = _new(dresidual, "dresidual", shape, h.dtype, dev, dy, stream)
+    if dweight is not None and weight is None:
+        raise ValueError("dweight needs a weight")
+    if dweight is not None or (weight is not None and need_dweight):
+        dweight, dwptr = _new(dweight, "dweight", (cols,), weight.dtype, dev, dy, stream)
+    head = (xdt, rdt, wdt, rows, cols, dy.data_ptr(), hptr, sptr, wptr, float(weight_offset), eptr, xptr, rptr, dwptr)
+    tail = (_stream_of(stream, dy, dev),)
+    sizes = (dev, xdt, rdt, rows, cols, dwptr is None)
+    if dev == _current_device():
+        _with_workspace("mfx_add_rmsnorm_bwd", head, tail, dy.device, workspace, sizes, none=True, stream=stream)
+    else:
+        with torch.cuda.device(dev):
+            _with_workspace("mfx_add_rmsnorm_bwd", head, tail, dy.device, workspace, sizes, none=True, stream=stream)
+    return dx, dresidual, dweight
 
 
 # ---------------------------------------------------------------------------
@@ -790,40 +805,44 @@ _INDEX_BITS = {torch.int32: 32, torch.int64: 64}
 
 
 def _logit_rows(t, name):
-    """(rows, vocab, ld) of [rows, vocab] data whose rows lie ld elements apart."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    """(type code, device, rows, vocab, ld) of [rows, vocab] data whose rows lie
+    ld elements apart."""
+    code = _float_code(t, name)
+    dev, shape = t.get_device(), t.shape
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2:
+    if len(shape) != 2:
         raise ValueError(f"{name} must have the shape [rows, vocab]")
-    rows, vocab = t.shape
-    if vocab > 1 and t.stride(1) != 1:
+    rows, vocab = shape
+    if t.is_contiguous():
+        return code, dev, rows, vocab, vocab
+    ld, step = t.stride()
+    if vocab > 1 and step != 1:
         raise ValueError(f"{name}'s columns must be contiguous")
-    if rows > 1 and t.stride(0) < vocab:
+    if rows > 1 and ld < vocab:
         raise ValueError(f"{name}'s rows must not overlap")
-    return rows, vocab, t.stride(0) if rows > 1 else vocab
+    return code, dev, rows, vocab, ld if rows > 1 else vocab
 
 
 def _columns(t, name, shape, dev):
-    """Bits of an index array of the given shape."""
+    """(bits, address) of an index array of the given shape."""
     bits = _INDEX_BITS.get(t.dtype) if isinstance(t, torch.Tensor) else None
     if bits is None:
         raise TypeError(f"{name} must be an int32 or int64 tensor")
-    _like(t, name, shape, t.dtype)
-    _same_device(t, dev, name)
-    return bits
+    return bits, _buf(t, name, shape, t.dtype, dev)
 
 
-def _dlogits(dlogits, logits, dev, stream):
-    """(buffer, its ld): contiguous if it is allocated here."""
-    rows, vocab = logits.shape
+def _dlogits(dlogits, logits, dev, rows, vocab, stream):
+    """(buffer, its address, its ld): contiguous if it is allocated here."""
     if dlogits is None:
-        return _empty((rows, vocab), logits.dtype, logits.device, stream), vocab
+        return *_new(None, "dlogits", (rows, vocab), logits.dtype, dev, logits, stream), vocab
     if not isinstance(dlogits, torch.Tensor) or dlogits.dtype != logits.dtype:
         raise TypeError(f"dlogits must be a {logits.dtype} tensor")
-    if _logit_rows(dlogits, "dlogits")[:2] != (rows, vocab):
+    _, _, r, v, ld = _logit_rows(dlogits, "dlogits")
+    if (r, v) != (rows, vocab):
         raise ValueError("dlogits must have the logits' shape")
     _same_device(dlogits, dev, "dlogits")
-    return dlogits, dlogits.stride(0) if rows > 1 else vocab
+    return dlogits, dlogits.data_ptr(), ld
 
 
 def mfx_token_logprobs_fwd(logits, tokens, scale=1.0, top=0, logprob=None, entropy=None, top_logprob=None,
@@ -833,63 +852,49 @@ def mfx_token_logprobs_fwd(logits, tokens, scale=1.0, top=0, logprob=None, entro
     tokens [rows] (int32 or int64; one outside the vocabulary leaves its row
     out).  The alternatives are None with top=0, stats with need_stats=False.
     logits' rows may lie further apart than the vocabulary is wide."""
-    rows, vocab, ld = _logit_rows(logits, "logits")
-    dev, top = logits.get_device(), int(top)
-    bits = _columns(tokens, "tokens", (rows,), dev)
-    f32 = torch.float32
-
-    def new(t, name, shape, dtype):
-        if t is None:
-            return _empty(shape, dtype, logits.device, stream)
-        _like(t, name, shape, dtype)
-        _same_device(t, dev, name)
-        return t
-
-    logprob, entropy = new(logprob, "logprob", (rows,), f32), new(entropy, "entropy", (rows,), f32)
+    code, dev, rows, vocab, ld = _logit_rows(logits, "logits")
+    bits, kptr = _columns(tokens, "tokens", (rows,), dev)
+    top, f32 = int(top), torch.float32
+    vptr = iptr = sptr = None
+    logprob, lptr = _new(logprob, "logprob", (rows,), f32, dev, logits, stream)
+    entropy, eptr = _new(entropy, "entropy", (rows,), f32, dev, logits, stream)
     if top > 0:
-        top_logprob = new(top_logprob, "top_logprob", (rows, top), f32)
-        top_index = new(top_index, "top_index", (rows, top), torch.int32)
+        top_logprob, vptr = _new(top_logprob, "top_logprob", (rows, top), f32, dev, logits, stream)
+        top_index, iptr = _new(top_index, "top_index", (rows, top), torch.int32, dev, logits, stream)
     elif top_logprob is not None or top_index is not None:
         raise ValueError("top_logprob and top_index need top")
     if stats is not None or need_stats:
-        stats = new(stats, "stats", (rows, 3), f32)
-    with _here(logits):
-        _call("mfx_token_logprobs_fwd", dtype_code(logits.dtype), rows, vocab, ld, logits.data_ptr(), bits,
-              tokens.data_ptr(), float(scale), top, logprob.data_ptr(), entropy.data_ptr(), _ptr(top_logprob),
-              _ptr(top_index), _ptr(stats), _stream(stream, logits))
+        stats, sptr = _new(stats, "stats", (rows, 3), f32, dev, logits, stream)
+    _run("mfx_token_logprobs_fwd", dev, code, rows, vocab, ld, logits.data_ptr(), bits, kptr, float(scale), top, lptr, eptr,
+         vptr, iptr, sptr, _stream_of(stream, logits, dev))
     return logprob, entropy, top_logprob, top_index, stats
 
 
 def mfx_token_logprobs_bwd(g_logprob, g_entropy, logits, tokens, stats, scale=1.0, dlogits=None, stream=None):
     """dlogits [rows, vocab] from the gradients of logprob and entropy (either
     may be None) and the forward's inputs and stats; dlogits may be logits."""
-    rows, vocab, ld = _logit_rows(logits, "logits")
-    dev = logits.get_device()
-    bits = _columns(tokens, "tokens", (rows,), dev)
-    g = None if g_logprob is None else _rows_of(g_logprob, "g_logprob", rows, torch.float32, dev)
-    ge = None if g_entropy is None else _rows_of(g_entropy, "g_entropy", rows, torch.float32, dev)
-    _like(stats, "stats", (rows, 3), torch.float32)
-    _same_device(stats, dev, "stats")
-    dlogits, ldo = _dlogits(dlogits, logits, dev, stream)
-    with _here(logits):
-        _call("mfx_token_logprobs_bwd", dtype_code(logits.dtype), rows, vocab, ld, g, ge, logits.data_ptr(), bits,
-              tokens.data_ptr(), stats.data_ptr(), float(scale), dlogits.data_ptr(), ldo, _stream(stream, logits))
+    code, dev, rows, vocab, ld = _logit_rows(logits, "logits")
+    bits, kptr = _columns(tokens, "tokens", (rows,), dev)
+    g = None if g_logprob is None else _buf(g_logprob, "g_logprob", (rows,), torch.float32, dev)
+    ge = None if g_entropy is None else _buf(g_entropy, "g_entropy", (rows,), torch.float32, dev)
+    sptr = _buf(stats, "stats", (rows, 3), torch.float32, dev)
+    dlogits, dptr, ldo = _dlogits(dlogits, logits, dev, rows, vocab, stream)
+    _run("mfx_token_logprobs_bwd", dev, code, rows, vocab, ld, g, ge, logits.data_ptr(), bits, kptr, sptr, float(scale), dptr,
+         ldo, _stream_of(stream, logits, dev))
     return dlogits
 
 
 def _distill_args(logits, index, teacher, teacher_lse):
-    """(rows, device, arguments up to teacher, teacher_lse's pointer)."""
-    rows, vocab, ld = _logit_rows(logits, "logits")
-    dev = logits.get_device()
-    if not isinstance(teacher, torch.Tensor) or teacher.dim() != 2:
+    """(device, rows, arguments up to k, logits' to teacher's, teacher_lse's address)."""
+    code, dev, rows, vocab, ld = _logit_rows(logits, "logits")
+    tdt = _float_code(teacher, "teacher")
+    if teacher.dim() != 2:
         raise ValueError("teacher must have the shape [rows, k]")
     k = teacher.shape[1]
-    _like(teacher, "teacher", (rows, k), teacher.dtype)
-    _same_device(teacher, dev, "teacher")
-    bits = _columns(index, "index", (rows, k), dev)
-    lse = None if teacher_lse is None else _rows_of(teacher_lse, "teacher_lse", rows, torch.float32, dev)
-    head = (dtype_code(logits.dtype), dtype_code(teacher.dtype), rows, vocab, ld, k)
-    return rows, dev, head, (logits.data_ptr(), bits, index.data_ptr(), teacher.data_ptr()), lse
+    tptr = _buf(teacher, "teacher", (rows, k), teacher.dtype, dev)
+    bits, iptr = _columns(index, "index", (rows, k), dev)
+    lse = None if teacher_lse is None else _buf(teacher_lse, "teacher_lse", (rows,), torch.float32, dev)
+    return dev, rows, (code, tdt, rows, vocab, ld, k), (logits.data_ptr(), bits, iptr, tptr), lse
 
 
 def mfx_topk_distill_fwd(logits, index, teacher, scale=1.0, teacher_lse=None, loss=None, stats=None, need_stats=True,
@@ -898,19 +903,12 @@ def mfx_topk_distill_fwd(logits, index, teacher, scale=1.0, teacher_lse=None, lo
     teacher's entries, p = softmax(scale * logits [rows, vocab]) and q the same
     of teacher [rows, k] at the columns index [rows, k] (int32 or int64,
     negative for no entry), or exp(scale * teacher - teacher_lse [rows])."""
-    rows, dev, head, data, lse = _distill_args(logits, index, teacher, teacher_lse)
-    if loss is None:
-        loss = _empty((rows,), torch.float32, logits.device, stream)
-    else:
-        _rows_of(loss, "loss", rows, torch.float32, dev)
-    if stats is not None:
-        _like(stats, "stats", (rows, 4), torch.float32)
-        _same_device(stats, dev, "stats")
-    elif need_stats:
-        stats = _empty((rows, 4), torch.float32, logits.device, stream)
-    with _here(logits):
-        _call("mfx_topk_distill_fwd", *head, *data, lse, float(scale), loss.data_ptr(), _ptr(stats),
-              _stream(stream, logits))
+    dev, rows, head, data, lse = _distill_args(logits, index, teacher, teacher_lse)
+    loss, lptr = _new(loss, "loss", (rows,), torch.float32, dev, logits, stream)
+    sptr = None
+    if stats is not None or need_stats:
+        stats, sptr = _new(stats, "stats", (rows, 4), torch.float32, dev, logits, stream)
+    _run("mfx_topk_distill_fwd", dev, *head, *data, lse, float(scale), lptr, sptr, _stream_of(stream, logits, dev))
     return loss, stats
 
 
@@ -918,14 +916,11 @@ def mfx_topk_distill_bwd(g, logits, index, teacher, stats, scale=1.0, teacher_ls
     """dlogits [rows, vocab] from the gradient g [rows] of the loss and the
     forward's inputs and stats (which hold what teacher_lse says); dlogits may
     be logits."""
-    rows, dev, head, data, _ = _distill_args(logits, index, teacher, teacher_lse)
-    gptr = _rows_of(g, "g", rows, torch.float32, dev)
-    _like(stats, "stats", (rows, 4), torch.float32)
-    _same_device(stats, dev, "stats")
-    dlogits, ldo = _dlogits(dlogits, logits, dev, stream)
-    with _here(logits):
-        _call("mfx_topk_distill_bwd", *head, gptr, *data, stats.data_ptr(), float(scale), dlogits.data_ptr(), ldo,
-              _stream(stream, logits))
+    dev, rows, head, data, _ = _distill_args(logits, index, teacher, teacher_lse)
+    gptr = _buf(g, "g", (rows,), torch.float32, dev)
+    sptr = _buf(stats, "stats", (rows, 4), torch.float32, dev)
+    dlogits, dptr, ldo = _dlogits(dlogits, logits, dev, rows, head[3], stream)
+    _run("mfx_topk_distill_bwd", dev, *head, gptr, *data, sptr, float(scale), dptr, ldo, _stream_of(stream, logits, dev))
     return dlogits
 
 
@@ -934,16 +929,12 @@ def mfx_topk_distill_fwd_bwd(logits, index, teacher, weight, scale=1.0, teacher_
     """(loss [rows], dlogits [rows, vocab]) in one call, where the gradient
     weight [rows] of each row's loss is known before it; dlogits may be
     logits."""
-    rows, dev, head, data, lse = _distill_args(logits, index, teacher, teacher_lse)
-    wptr = _rows_of(weight, "weight", rows, torch.float32, dev)
-    if loss is None:
-        loss = _empty((rows,), torch.float32, logits.device, stream)
-    else:
-        _rows_of(loss, "loss", rows, torch.float32, dev)
-    dlogits, ldo = _dlogits(dlogits, logits, dev, stream)
-    with _here(logits):
-        _call("mfx_topk_distill_fwd_bwd", *head, *data, lse, wptr, float(scale), loss.data_ptr(), dlogits.data_ptr(), ldo,
-              _stream(stream, logits))
+    dev, rows, head, data, lse = _distill_args(logits, index, teacher, teacher_lse)
+    gptr = _buf(weight, "weight", (rows,), torch.float32, dev)
+    loss, lptr = _new(loss, "loss", (rows,), torch.float32, dev, logits, stream)
+    dlogits, dptr, ldo = _dlogits(dlogits, logits, dev, rows, head[3], stream)
+    _run("mfx_topk_distill_fwd_bwd", dev, *head, *data, lse, gptr, float(scale), lptr, dptr, ldo,
+         _stream_of(stream, logits, dev))
     return loss, dlogits
 
 

@@ -1,5 +1,23 @@
 // rmsnorm.cuh -- what the root-mean-square norm's forward and backward share:
-// the layout of a row over a team of threads, and sums over a team.
+// rows that come to shared memory while others are worked on, their layout
+// over a team of threads, and sums over a team.
+//
+// A team of `lanes` threads (8, 16 or 32 lanes of a warp, or a whole block)
+// owns a row, E elements a thread; blocks stay on the GPU and take every
+// gridDim-th row.  The rows to come (`depth` of them) are on their way to
+// shared memory by asynchronous copies, so that HBM works while a team waits
+// for its own sum.  A thread has the same columns of every row: their factors,
+// places and bounds are formed once, and per element and row there are some
+// ten instructions left (loops over columns with all that inside had 60 to 180
+// and were bound by them).
+//
+// With vectors a thread's k-th unit is columns V (k lanes + lane) on (V = 8
+// where all data is bf16, 4 where some of it is fp32, so that a warp's
+// accesses cover whole lines of each), and it copies what it reads itself: no
+// barrier.  Without (a width that is not a multiple of 8, or a buffer off a
+// vector) units are single columns, 32 next to each other a warp and four such
+// steps on end, and rows are copied as the 16-byte vectors that cover them, by
+// all threads for all: a barrier more, or two.
 #pragma once
 
 #include "mfx_device.cuh"
@@ -8,91 +26,186 @@
 namespace mfx {
 namespace rmsnorm {
 
-// A team of `lanes` threads (8, 16 or 32 lanes of a warp, or a whole block)
-// owns a row and keeps it in registers, 8 C elements a thread.  With vectors,
-// a thread's k-th run of 8 columns begins at 8 (k lanes + lane); without
-// (a width that is not a multiple of 8, or a buffer off a vector) its e-th
-// element is column e lanes + lane, so that a warp's accesses still cover
-// whole lines.
-template <typename T, int C, bool VEC>
-__device__ __forceinline__ void load_row(const T* p, int cols, int lanes, int tl, float (&f)[8 * C])
+constexpr int kMostDepth = 4;
+constexpr int kPad = 32;  // bytes that a row's covering vectors may be longer by
+
+// --- units ------------------------------------------------------------------
+template <typename T, int V>
+__device__ __forceinline__ void widen_unit(const uint4& w, float (&f)[V])
 {
-    if constexpr (VEC) {
-        Raw8<T> r[C];
-#pragma unroll
-        for (int k = 0; k < C; ++k)
-            if (const int c = (k * lanes + tl) * 8; c < cols)
-                ld8(p + c, r[k]);
-#pragma unroll
-        for (int k = 0; k < C; ++k) {
-            if ((k * lanes + tl) * 8 < cols) {
-                widen8(r[k], f + 8 * k);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    f[8 * k + j] = 0.0f;
-            }
-        }
+    if constexpr (sizeof(T) == 4) {
+        static_assert(V == 4, "fp32 units");
+        f[0] = __uint_as_float(w.x), f[1] = __uint_as_float(w.y), f[2] = __uint_as_float(w.z), f[3] = __uint_as_float(w.w);
     } else {
-#pragma unroll
-        for (int e = 0; e < 8 * C; ++e) {
-            const int c = e * lanes + tl;
-            f[e] = c < cols ? load1(p + c) : 0.0f;
-        }
+        f[0] = bf16lo(w.x), f[1] = bf16hi(w.x), f[2] = bf16lo(w.y), f[3] = bf16hi(w.y);
+        if constexpr (V == 8)
+            f[4] = bf16lo(w.z), f[5] = bf16hi(w.z), f[6] = bf16lo(w.w), f[7] = bf16hi(w.w);
     }
 }
 
-template <typename T, int C, bool VEC>
-__device__ __forceinline__ void store_row(T* p, int cols, int lanes, int tl, const float (&f)[8 * C])
+// A unit at shared address a.
+template <typename T, int V>
+__device__ __forceinline__ void lds_unit(uint32_t a, float (&f)[V])
 {
-    if constexpr (VEC) {
-#pragma unroll
-        for (int k = 0; k < C; ++k)
-            if (const int c = (k * lanes + tl) * 8; c < cols) {
-                Raw8<T> r;
-                narrow8(f + 8 * k, r);
-                st8(p + c, r);
-            }
+    constexpr int bytes = V * (int)sizeof(T);
+    if constexpr (bytes == 16) {
+        uint4 w;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(a) : "memory");
+        widen_unit<T, V>(w, f);
+    } else if constexpr (bytes == 8) {
+        uint4 w;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(a) : "memory");
+        widen_unit<T, V>(w, f);
+    } else if constexpr (bytes == 4) {
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[0]) : "r"(a) : "memory");
     } else {
-#pragma unroll
-        for (int e = 0; e < 8 * C; ++e)
-            if (const int c = e * lanes + tl; c < cols)
-                store1(p + c, f[e]);
+        uint16_t h;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(a) : "memory");
+        f[0] = __uint_as_float((uint32_t)h << 16);
     }
 }
 
-// The factors weight + offset of a thread's k-th eight columns (1 without a
-// weight; 0 past the row's end).  The weight's type is asked at run time: its
-// rows come from L1.
-template <bool VEC>
-__device__ __forceinline__ void factors(const void* weight, bool w_bf16, float offset, int cols, int lanes, int tl,
-                                        int k, float w[8])
+template <typename T, int V>
+__device__ __forceinline__ void store_unit(T* p, const float (&f)[V])
 {
-    if constexpr (VEC) {
-        const int c = (k * lanes + tl) * 8;
-        if (c >= cols || !weight) {
+    if constexpr (V == 1)
+        store1(p, f[0]);
+    else if constexpr (sizeof(T) == 4)
+        st16(p, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+    else if constexpr (V == 4)
+        st8(p, make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])));
+    else
+        st16(p, make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
+}
+
+// The factors weight + offset of the unit at column c (1 without a weight).
+// The weight's type is asked at run time: it comes from L1.
+template <int V>
+__device__ __forceinline__ void factors(const void* weight, bool w_bf16, float offset, int c, float (&w)[V])
+{
+    if (!weight) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                w[j] = c < cols ? 1.0f : 0.0f;
-            return;
-        }
+        for (int j = 0; j < V; ++j)
+            w[j] = 1.0f;
+        return;
+    }
+    if constexpr (V == 1) {
+        w[0] = w_bf16 ? load1(static_cast<const bf16*>(weight) + c) : load1(static_cast<const float*>(weight) + c);
+    } else if constexpr (V == 8) {
         if (w_bf16)
-            bias8(static_cast<const bf16*>(weight), c, w);
+            widen_unit<bf16, 8>(ld16_ro(static_cast<const bf16*>(weight) + c), w);
         else
             bias8(static_cast<const float*>(weight), c, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            w[j] += offset;
     } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = (8 * k + j) * lanes + tl;
-            w[j] = c >= cols  ? 0.0f
-                   : !weight  ? 1.0f
-                   : w_bf16   ? load1(static_cast<const bf16*>(weight) + c) + offset
-                              : load1(static_cast<const float*>(weight) + c) + offset;
+        uint4 r;
+        if (w_bf16) {
+            asm("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(static_cast<const bf16*>(weight) + c));
+            widen_unit<bf16, 4>(r, w);
+        } else {
+            widen_unit<float, 4>(ld16_ro(static_cast<const float*>(weight) + c), w);
         }
     }
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        w[j] += offset;
+}
+
+// First column of a thread's k-th unit.
+template <int V>
+__device__ __forceinline__ int column_of(int k, int lanes, int tl)
+{
+    if constexpr (V > 1)
+        return (k * lanes + tl) * V;
+    else
+        return ((k >> 2) * (lanes >> 5) + (tl >> 5)) * 128 + (k & 3) * 32 + (tl & 31);
+}
+
+// A thread's factors, 0 past the row's end.
+template <int V, int N>
+__device__ __forceinline__ void factors_of(const void* weight, bool w_bf16, float offset, int cols, int lanes, int tl,
+                                           float (&w)[N][V])
+{
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int c = column_of<V>(k, lanes, tl);
+        if (c < cols) {
+            factors<V>(weight, w_bf16, offset, c, w[k]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                w[k][j] = 0.0f;
+        }
+    }
+}
+
+// --- rows on their way --------------------------------------------------------
+template <int BYTES>
+__device__ __forceinline__ void copy_unit(uint32_t to, const void* from)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global.L2::256B [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but the last n of this thread's groups have come.
+__device__ __forceinline__ void copies_wait(int n)
+{
+    switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    }
+}
+
+// Starts a team's copy of one row (cols elements at p) to shared address `to`.
+// Element c is then at to + where(p) + c * size.  Vectors may hold elements of
+// the rows beside it; only those that reach out of all rows ([lo, hi), the
+// first row's first and the last row's last) are copied by element.
+template <typename T>
+__device__ __forceinline__ uint32_t where(const T* p)
+{
+    return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+}
+template <typename T, int V, int N>
+__device__ __forceinline__ void copy_row(uint32_t to, const T* p, int cols, const T* lo, const T* hi, int lanes, int tl)
+{
+    if constexpr (V > 1) {
+        to += tl * (uint32_t)(V * sizeof(T)), p += tl * V;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (column_of<V>(k, lanes, tl) < cols)
+                copy_unit<V * (int)sizeof(T)>(to + (uint32_t)(k * lanes * V) * (uint32_t)sizeof(T), p + k * lanes * V);
+    } else {
+        constexpr int E = 16 / (int)sizeof(T);
+        const int phase = (int)(where(p) / sizeof(T)), vectors = (cols + phase + E - 1) / E;
+        for (int v = tl; v < vectors; v += lanes) {
+            const T* from = p + (v * E - phase);
+            if (from >= lo && from + E <= hi) {
+                copy_unit<16>(to + 16u * v, from);
+            } else {
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    if (from + j >= lo && from + j < hi) {
+                        const uint32_t a = to + 16u * v + (uint32_t)j * (uint32_t)sizeof(T);
+                        if constexpr (sizeof(T) == 2)
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(from[j].bits) : "memory");
+                        else
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(from[j]) : "memory");
+                    }
+            }
+        }
+    }
+}
+
+// What others' threads have copied is there for all of a team.
+__device__ __forceinline__ void team_barrier(int lanes)
+{
+    if (lanes > 32)
+        __syncthreads();
+    else
+        __syncwarp();
 }
 
 // The largest absolute value of two; NaN counts as nothing.
@@ -104,34 +217,75 @@ __device__ __forceinline__ float amax(float a, float b) { return fmaxf(a, fabsf(
 template <bool MAX>
 __device__ __forceinline__ float2 over_team(float2 v, int lanes, float2 (*part)[32], int slot)
 {
-    const int n = lanes < 32 ? lanes : 32;
-    for (int o = n >> 1; o > 0; o >>= 1) {
+    const auto step = [&](int o) {
         v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
         if (MAX)
             v.y = fmaxf(v.y, __shfl_xor_sync(0xFFFFFFFFu, v.y, o));
-    }
+    };
+    if (lanes >= 32)
+        step(16);
+    if (lanes >= 16)
+        step(8);
+    step(4), step(2), step(1);
     if (lanes > 32) {
         const int lane = threadIdx.x & 31, warps = lanes >> 5;
         if (lane == 0)
             part[slot][threadIdx.x >> 5] = v;
         __syncthreads();
         v = lane < warps ? part[slot][lane] : make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
-            if (MAX)
-                v.y = fmaxf(v.y, __shfl_xor_sync(0xFFFFFFFFu, v.y, o));
-        }
+        step(16), step(8), step(4), step(2), step(1);
     }
     return v;
 }
 
-// How a row is laid out: C runs of 8 elements a thread, lanes a row, threads
-// a block (the same for teams of several warps).
+// --- host ---------------------------------------------------------------------
+// Elements of a thread; threads of a row and of a block, rows that a team has
+// on their way, and the shared bytes of one of them.  depth 0: the row does not
+// fit, or is longer than 512 threads of 32 elements.
 struct Layout {
-    int C, lanes, threads;
-    bool longer;  // the row does not fit a block's registers
+    int E, lanes, threads, depth;
+    size_t row, smem;
 };
+
+// Rows of up to 512 columns in a warp, others in a block: 8 elements a thread
+// up to 2048 columns (and for few rows, up to 1024 threads: the shortest way),
+// 16 up to 8192 (single columns: 32, above 8 x 1024), 32 up to 16384.
+// `row`: bytes of a row of all streams (kPad included); `fixed`: bytes that a
+// team needs beside its rows; `resident`: threads of a multiprocessor that the
+// kernel's registers leave with E elements a thread.
+template <typename F>
+Layout layout(int64_t rows, int64_t cols, int V, size_t row, size_t fixed, F resident)
+{
+    const auto lanes_of = [&](int64_t e) { return (int)(((cols + e - 1) / e + 31) / 32 * 32); };
+    Layout l = {8, 32, 256, 0, (row + 15) / 16 * 16, 0};
+    if (cols <= 16 * V && V > 1) {
+        l.lanes = cols <= 8 * V ? 8 : 16;  // one unit each: a group of columns is consecutive lanes' also here
+    } else if (cols <= 512) {
+        l.E = cols <= 256 ? 8 : V > 1 ? 16 : 32;
+    } else {
+        const bool few = rows <= sm_count();
+        l.E = cols <= (few || V == 1 ? 8192 : 2048) ? 8 : V > 1 && cols <= 8192 ? 16 : 32;
+        l.lanes = l.threads = lanes_of(l.E);
+        if (l.E == 32 && l.lanes > 512)
+            return l;
+    }
+    const int64_t teams = l.threads / l.lanes;
+    fixed = (fixed + 15) / 16 * 16;
+    const int most = resident(l.E) / l.threads;
+    for (int blocks = most > 0 ? most : 1; blocks >= 1 && l.depth < 2; --blocks) {
+        // a block's static arrays and what the system keeps of each: 2 KB
+        const size_t each = (kMaxBlockSmem + 1024) / blocks - 2048;
+        if (each / teams <= fixed)
+            continue;
+        const size_t d = (each / teams - fixed) / l.row;
+        l.depth = d > kMostDepth ? kMostDepth : (int)d;
+    }
+    const int64_t share = (rows + teams - 1) / teams;
+    if (l.depth > 1 && share <= sm_count())
+        l.depth = 1;  // no team has a second row
+    l.smem = (size_t)teams * (l.depth * l.row + fixed);
+    return l;
+}
 
 // What the checks of both directions share.
 inline bool sizes_ok(int64_t rows, int64_t cols)

@@ -8,7 +8,7 @@
 // have the same gradient; it is written in each one's type.
 //
 // The weight's gradient is formed on the way: each thread owns the same
-// columns of every row that its block works on and adds them up in registers;
+// columns of every row that its team works on and adds them up in registers;
 // the blocks' partial sums are joined in a fixed order by the kernel that
 // joins those of the bias gradients.
 #include "rmsnorm.cuh"
@@ -21,7 +21,8 @@ namespace {
 
 struct Args {
     int64_t rows;
-    int cols, lanes;
+    int cols, lanes, depth;
+    uint32_t row_bytes, x_bytes, r_bytes;  // of a row on its way: all of it, dy's part, h's
     const void *dy, *h, *dh, *weight;
     const float* rstd;
     bool w_bf16;
@@ -30,247 +31,273 @@ struct Args {
     float *ws, *dots;
 };
 
-constexpr int kMaxLanes = 512;    // threads of a row
-constexpr int kInRegisters = 512 * 8 * 4;
-
-// Gradient of a piece of a row from its dy (g), h and coefficients, into dx and
-// dresidual.
-template <typename XT, typename RT, int C, bool VEC>
-__device__ __forceinline__ void store_grads(const Args& a, int64_t at, int cols, int lanes, int tl, float (&d)[8 * C])
-{
-    if (a.dh) {
-        float e[8 * C];
-        load_row<RT, C, VEC>(static_cast<const RT*>(a.dh) + at, cols, lanes, tl, e);
-#pragma unroll
-        for (int i = 0; i < 8 * C; ++i)
-            d[i] += e[i];
-    }
-    if (a.dx)
-        store_row<XT, C, VEC>(static_cast<XT*>(a.dx) + at, cols, lanes, tl, d);
-    if (a.dres)
-        store_row<RT, C, VEC>(static_cast<RT*>(a.dres) + at, cols, lanes, tl, d);
-}
-
-template <typename XT, typename RT, int C, bool VEC>
-__global__ void __launch_bounds__(kMaxLanes)
+template <typename XT, typename RT, int V, int E>
+__global__ void __launch_bounds__(E == 8 ? 1024 : 512, 1)
 norm_bwd(const Args a)
 {
+    constexpr int N = E / V;
+    constexpr bool VEC = V > 1;
     __shared__ float2 part[2][32];
-    extern __shared__ float sums[];  // teams of a warp or less: their partial sums
+    extern __shared__ __align__(16) char dynamic[];
     const int lanes = a.lanes, teams = blockDim.x / lanes, team = threadIdx.x / lanes, tl = threadIdx.x % lanes;
-    float acc[8 * C];
+    const int cols = a.cols;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(dynamic) + team * (uint32_t)a.depth * a.row_bytes;
+    const uint32_t end = ring + (uint32_t)a.depth * a.row_bytes;
+    const int64_t step = (int64_t)gridDim.x * teams, all = a.rows * cols;
+    const XT* const dy = static_cast<const XT*>(a.dy);
+    const RT *const hs = static_cast<const RT*>(a.h), *const dh = static_cast<const RT*>(a.dh);
+    int64_t row = (int64_t)blockIdx.x * teams + team;
+    const auto start = [&](int64_t r, uint32_t to) {
+        if (r - team < a.rows) {  // a team past the end takes the last row
+            const int64_t at = (r < a.rows ? r : a.rows - 1) * cols;
+            copy_row<XT, V, N>(to, dy + at, cols, dy, dy + all, lanes, tl);
+            copy_row<RT, V, N>(to + a.x_bytes, hs + at, cols, hs, hs + all, lanes, tl);
+            if (dh)
+                copy_row<RT, V, N>(to + a.x_bytes + a.r_bytes, dh + at, cols, dh, dh + all, lanes, tl);
+        }
+        copies_commit();
+    };
+    int64_t next = row;
+    for (uint32_t to = ring; to != end; to += a.row_bytes, next += step)
+        start(next, to);
+    float w[N][V], acc[N][V];
+    factors_of<V, N>(a.weight, a.w_bf16, a.offset, cols, lanes, tl, w);
 #pragma unroll
-    for (int e = 0; e < 8 * C; ++e)
-        acc[e] = 0.0f;
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            acc[k][j] = 0.0f;
     int slot = 0;
-    for (int64_t first = (int64_t)blockIdx.x * teams; first < a.rows; first += (int64_t)gridDim.x * teams, slot ^= 1) {
-        const bool on = first + team < a.rows;
-        const int64_t row = on ? first + team : a.rows - 1, at = row * a.cols;
-        float g[8 * C], h[8 * C];
-        load_row<XT, C, VEC>(static_cast<const XT*>(a.dy) + at, a.cols, lanes, tl, g);
-        load_row<RT, C, VEC>(static_cast<const RT*>(a.h) + at, a.cols, lanes, tl, h);
-        const float rstd = a.rstd[row];
+    uint32_t buf = ring;
+    for (; row - team < a.rows; row += step, next += step, slot ^= 1) {
+        const bool on = row < a.rows;
+        const int64_t r = on ? row : a.rows - 1, at = r * cols;
+        const float rstd = a.rstd[r];
+        copies_wait(a.depth - 1);
+        if (!VEC)
+            team_barrier(lanes);
+        const uint32_t sg = buf + (VEC ? 0u : where(dy + at)), sh = buf + a.x_bytes + (VEC ? 0u : where(hs + at));
+        const uint32_t se = buf + a.x_bytes + a.r_bytes + (VEC || !dh ? 0u : where(dh + at));
+        const float counts = on ? rstd : 0.0f;
         float2 v = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int k = 0; k < C; ++k) {
-            float w[8];
-            factors<VEC>(a.weight, a.w_bf16, a.offset, a.cols, lanes, tl, k, w);
+        for (int k = 0; k < N; ++k) {
+            const int c = column_of<V>(k, lanes, tl);
+            if (c < cols) {
+                float g[V], h[V];
+                lds_unit<XT, V>(sg + c * (uint32_t)sizeof(XT), g);
+                lds_unit<RT, V>(sh + c * (uint32_t)sizeof(RT), h);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int e = 8 * k + j;
-                if (on)
-                    acc[e] = fmaf(g[e], h[e] * rstd, acc[e]);
-                g[e] *= w[j];
-                v.x = fmaf(g[e], h[e], v.x);
+                for (int j = 0; j < V; ++j) {
+                    const float gh = g[j] * h[j];
+                    if (on)
+                        acc[k][j] = fmaf(gh, counts, acc[k][j]);
+                    v.x = fmaf(gh, w[k][j], v.x);
+                }
             }
         }
         v = over_team<false>(v, lanes, part, slot);
-        const float b = rstd * (__fdiv_rn(v.x * rstd, (float)a.cols) * rstd);
+        const float b = rstd * (__fdiv_rn(v.x * rstd, (float)cols) * rstd);
+        XT* dx = a.dx ? static_cast<XT*>(a.dx) + at : nullptr;
+        RT* dres = a.dres ? static_cast<RT*>(a.dres) + at : nullptr;
 #pragma unroll
-        for (int e = 0; e < 8 * C; ++e)
-            g[e] = fmaf(rstd, g[e], -b * h[e]);
-        if (on)
-            store_grads<XT, RT, C, VEC>(a, at, a.cols, lanes, tl, g);
+        for (int k = 0; k < N; ++k) {
+            const int c = column_of<V>(k, lanes, tl);
+            if (on && c < cols) {
+                float g[V], h[V];
+                lds_unit<XT, V>(sg + c * (uint32_t)sizeof(XT), g);
+                lds_unit<RT, V>(sh + c * (uint32_t)sizeof(RT), h);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    g[j] = fmaf(rstd, g[j] * w[k][j], -b * h[j]);
+                if (dh) {
+                    lds_unit<RT, V>(se + c * (uint32_t)sizeof(RT), h);
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        g[j] += h[j];
+                }
+                if (dx)
+                    store_unit<XT, V>(dx + c, g);
+                if (dres)
+                    store_unit<RT, V>(dres + c, g);
+            }
+        }
+        if (!VEC)
+            team_barrier(lanes);
+        start(next, buf);
+        buf = buf + a.row_bytes == end ? ring : buf + a.row_bytes;
     }
     if (!a.ws)
         return;
-    float* ws = a.ws + (int64_t)blockIdx.x * a.cols;
-    if (teams > 1) {  // 8 warps or more teams of a row of at most 1024 columns
-        store_row<float, C, false>(sums + team * a.cols, VEC ? 0 : a.cols, lanes, tl, acc);
-        if (VEC) {
+    float* ws = a.ws + (int64_t)blockIdx.x * cols;
+    if (teams == 1) {
 #pragma unroll
-            for (int e = 0; e < 8 * C; ++e)
-                if (const int c = ((e >> 3) * lanes + tl) * 8 + (e & 7); c < a.cols)
-                    sums[team * a.cols + c] = acc[e];
-        }
-        __syncthreads();
-        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-            float s = 0.0f;
-            for (int t = 0; t < teams; ++t)
-                s += sums[t * a.cols + c];
-            ws[c] = s;
-        }
+        for (int k = 0; k < N; ++k)
+            if (const int c = column_of<V>(k, lanes, tl); c < cols)
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    ws[c + j] = acc[k][j];
         return;
     }
+    // the teams' sums in order (rows are 512 columns at most; nothing is on its way any more)
+    float* sums = reinterpret_cast<float*>(dynamic);
+    __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8 * C; ++e)
-        if (const int c = VEC ? ((e >> 3) * lanes + tl) * 8 + (e & 7) : e * lanes + tl; c < a.cols)
-            ws[c] = acc[e];
+    for (int k = 0; k < N; ++k)
+        if (const int c = column_of<V>(k, lanes, tl); c < cols)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                sums[team * cols + c + j] = acc[k][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+        float s = sums[c];
+        for (int t = 1; t < teams; ++t)
+            s += sums[t * cols + c];
+        ws[c] = s;
+    }
 }
 
-// Rows that do not fit a block's registers: the sums u * h of every row first,
-// then the gradients a slab of columns at a time.
-template <typename XT, typename RT, bool VEC>
-__global__ void __launch_bounds__(kMaxLanes)
+// Rows longer than that: the sums u * h of every row first, then the gradients
+// a slab of columns at a time; column by column.
+constexpr int kLongThreads = 512, kSlab = 4;  // columns of a thread of a slab
+
+template <typename XT, typename RT>
+__global__ void __launch_bounds__(kLongThreads)
 row_dots(const Args a)
 {
     __shared__ float2 part[2][32];
-    const int lanes = a.lanes, tl = threadIdx.x, piece = 8 * lanes;
     int slot = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, slot ^= 1) {
+        const XT* g = static_cast<const XT*>(a.dy) + row * a.cols;
+        const RT* h = static_cast<const RT*>(a.h) + row * a.cols;
         float2 v = make_float2(0.0f, 0.0f);
-        for (int c0 = 0; c0 < a.cols; c0 += piece) {
-            const int cols = a.cols - c0 < piece ? a.cols - c0 : piece;
-            float g[8], h[8], w[8];
-            load_row<XT, 1, VEC>(static_cast<const XT*>(a.dy) + row * a.cols + c0, cols, lanes, tl, g);
-            load_row<RT, 1, VEC>(static_cast<const RT*>(a.h) + row * a.cols + c0, cols, lanes, tl, h);
-            const char* wp = static_cast<const char*>(a.weight);
-            factors<VEC>(wp ? wp + (int64_t)c0 * (a.w_bf16 ? 2 : 4) : wp, a.w_bf16, a.offset, cols, lanes, tl, 0, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v.x = fmaf(g[j] * w[j], h[j], v.x);
+#pragma unroll 4
+        for (int c = threadIdx.x; c < a.cols; c += kLongThreads) {
+            float w[1];
+            factors<1>(a.weight, a.w_bf16, a.offset, c, w);
+            v.x = fmaf(load1(g + c) * w[0], load1(h + c), v.x);
         }
-        v = over_team<false>(v, lanes, part, slot);
-        if (tl == 0)
+        v = over_team<false>(v, kLongThreads, part, slot);
+        if (threadIdx.x == 0)
             a.dots[row] = v.x;
     }
 }
 
-template <typename XT, typename RT, bool VEC>
+template <typename XT, typename RT>
 __global__ void __launch_bounds__(kThreads)
 slab_bwd(const Args a)
 {
-    const int lanes = kThreads, tl = threadIdx.x, c0 = blockIdx.x * 8 * lanes;
-    const int cols = a.cols - c0 < 8 * lanes ? a.cols - c0 : 8 * lanes;
-    float acc[8], w[8];
-    const char* wp = static_cast<const char*>(a.weight);
-    factors<VEC>(wp ? wp + (int64_t)c0 * (a.w_bf16 ? 2 : 4) : wp, a.w_bf16, a.offset, cols, lanes, tl, 0, w);
+    const int64_t c0 = (int64_t)blockIdx.x * kSlab * kThreads + threadIdx.x;
+    float acc[kSlab], w[kSlab][1];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        acc[j] = 0.0f;
+    for (int i = 0; i < kSlab; ++i) {
+        const int64_t c = c0 + i * kThreads;
+        acc[i] = w[i][0] = 0.0f;
+        if (c < a.cols)
+            factors<1>(a.weight, a.w_bf16, a.offset, (int)c, w[i]);
+    }
     for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-        const int64_t at = row * a.cols + c0;
-        float g[8], h[8];
-        load_row<XT, 1, VEC>(static_cast<const XT*>(a.dy) + at, cols, lanes, tl, g);
-        load_row<RT, 1, VEC>(static_cast<const RT*>(a.h) + at, cols, lanes, tl, h);
         const float rstd = a.rstd[row], b = rstd * (__fdiv_rn(a.dots[row] * rstd, (float)a.cols) * rstd);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            acc[j] = fmaf(g[j], h[j] * rstd, acc[j]);
-            g[j] = fmaf(rstd, g[j] * w[j], -b * h[j]);
+        for (int i = 0; i < kSlab; ++i) {
+            const int64_t c = c0 + i * kThreads, at = row * a.cols + c;
+            if (c >= a.cols)
+                continue;
+            const float g = load1(static_cast<const XT*>(a.dy) + at), h = load1(static_cast<const RT*>(a.h) + at);
+            acc[i] = fmaf(g, h * rstd, acc[i]);
+            float d = fmaf(rstd, g * w[i][0], -b * h);
+            if (a.dh)
+                d += load1(static_cast<const RT*>(a.dh) + at);
+            if (a.dx)
+                store1(static_cast<XT*>(a.dx) + at, d);
+            if (a.dres)
+                store1(static_cast<RT*>(a.dres) + at, d);
         }
-        store_grads<XT, RT, 1, VEC>(a, at, cols, lanes, tl, g);
     }
     if (a.ws)
-        store_row<float, 1, false>(a.ws + (int64_t)blockIdx.y * a.cols + c0, VEC ? 0 : cols, lanes, tl, acc);
-    if (a.ws && VEC) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (tl * 8 + j < cols)
-                a.ws[(int64_t)blockIdx.y * a.cols + c0 + tl * 8 + j] = acc[j];
-    }
+        for (int i = 0; i < kSlab; ++i)
+            if (const int64_t c = c0 + i * kThreads; c < a.cols)
+                a.ws[(int64_t)blockIdx.y * a.cols + c] = acc[i];
 }
-
-Layout layout(int64_t cols, bool vec)
-{
-    const int64_t units = (cols + 7) / 8;
-    Layout l = {4, 32, 256, false};
-    if (units <= 32 * 4) {
-        l.C = units <= 32 ? 1 : units <= 64 ? 2 : 4;
-        while (vec && l.C == 1 && l.lanes > 8 && units <= l.lanes / 2)
-            l.lanes /= 2;
-        return l;
-    }
-    l.C = units <= 256 ? 1 : units <= 1024 ? 2 : 4;
-    l.longer = cols > kInRegisters;
-    l.lanes = l.threads = l.longer ? kMaxLanes : (int)(((units + l.C - 1) / l.C + 31) / 32 * 32);
-    return l;
-}
-
-size_t team_smem(const Layout& l, int64_t cols) { return l.lanes < l.threads ? (size_t)(l.threads / l.lanes) * cols * 4 : 0; }
 
 struct Plan {
+    Layout l;
+    uint32_t x_bytes, r_bytes;
     int64_t blocks;    // partial sums of a column
     int64_t ws, dots;  // floats of each in the workspace
 };
 
+// The blocks go by sizes and types alone (a row's bytes with dh, whole vectors
+// if the width has them): the workspace's size must not go by addresses.
 template <typename XT, typename RT>
-const void* kernel_of(int C, bool vec)
+constexpr int unit_of() { return sizeof(XT) > sizeof(RT) ? 1 : sizeof(RT) == 2 ? 8 : 4; }
+
+template <typename XT, typename RT, int V>
+auto kernel_of(int E)
 {
-    if (vec)
-        return C == 1   ? reinterpret_cast<const void*>(norm_bwd<XT, RT, 1, true>)
-               : C == 2 ? reinterpret_cast<const void*>(norm_bwd<XT, RT, 2, true>)
-                        : reinterpret_cast<const void*>(norm_bwd<XT, RT, 4, true>);
-    return C == 1   ? reinterpret_cast<const void*>(norm_bwd<XT, RT, 1, false>)
-           : C == 2 ? reinterpret_cast<const void*>(norm_bwd<XT, RT, 2, false>)
-                    : reinterpret_cast<const void*>(norm_bwd<XT, RT, 4, false>);
+    if constexpr (V > 1)
+        if (E == 16)
+            return norm_bwd<XT, RT, V, 16>;
+    return E == 8 ? norm_bwd<XT, RT, V, 8> : norm_bwd<XT, RT, V, 32>;
 }
 
-// The same blocks whether the buffers are aligned or not: the workspace's
-// size goes by sizes and types alone.
 template <typename XT, typename RT>
-Plan plan(int64_t rows, int64_t cols)
+auto kernel_of(int E, bool vec)
 {
-    const Layout l = layout(cols, cols % 8 == 0);
-    Plan p = {0, 0, 0};
-    if (l.longer) {
-        const int64_t slabs = (cols + 8 * kThreads - 1) / (8 * kThreads);
-        int64_t lanes = (4 * sm_count() + slabs - 1) / slabs;
-        lanes = lanes < 65535 ? lanes : 65535;
+    return vec ? kernel_of<XT, RT, unit_of<XT, RT>()>(E) : kernel_of<XT, RT, 1>(E);
+}
+
+template <typename XT, typename RT>
+Plan plan(int64_t rows, int64_t cols, bool vec)
+{
+    const size_t x = ((size_t)cols * sizeof(XT) + kPad + 15) / 16 * 16, r = ((size_t)cols * sizeof(RT) + kPad + 15) / 16 * 16;
+    Plan p = {{}, (uint32_t)x, (uint32_t)r, 0, 0, 0};
+    const auto laid = [&](bool v) {
+        // teams' sums at the end: no more than a row of dy, h and dh each, which is 6 bytes a column or more
+        return layout(rows, cols, v ? unit_of<XT, RT>() : 1, x + 2 * r, 0, [](int e) { return e == 8 ? 1024 : 512; });
+    };
+    p.l = laid(vec);
+    if (p.l.depth == 0) {
+        const int64_t slabs = (cols + kSlab * kThreads - 1) / (kSlab * kThreads);
+        const int64_t lanes = (8 * sm_count() + slabs - 1) / slabs;
         p.blocks = rows < lanes ? rows : lanes;
         p.dots = (rows + 3) / 4 * 4;
     } else {
+        const bool v = cols % 8 == 0;
+        const Layout l = laid(v);
         const int64_t teams = l.threads / l.lanes, need = (rows + teams - 1) / teams;
         const int64_t room =
-            (int64_t)sm_count() * occupancy(kernel_of<XT, RT>(l.C, cols % 8 == 0), l.threads, team_smem(l, cols));
+            (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(kernel_of<XT, RT>(l.E, v)), l.threads, l.smem);
         p.blocks = need < room ? need : room;
     }
     p.ws = p.blocks * cols;
     return p;
 }
 
-template <typename XT, typename RT, int C, bool VEC>
-void launch(const Args& a, const Layout& l, int64_t blocks, cudaStream_t s)
+template <typename XT, typename RT>
+int launch(Args a, const Plan& p, bool vec, cudaStream_t s)
 {
-    norm_bwd<XT, RT, C, VEC><<<(unsigned)blocks, l.threads, team_smem(l, a.cols), s>>>(a);
-}
-
-template <typename XT, typename RT, bool VEC>
-int launch_any(Args a, const Plan& p, cudaStream_t s)
-{
-    const Layout l = layout(a.cols, VEC);
-    a.lanes = l.lanes;
-    if (l.longer) {
+    if (p.l.depth == 0) {
         const int64_t room = (int64_t)sm_count() * 4;
-        row_dots<XT, RT, VEC><<<(unsigned)(a.rows < room ? a.rows : room), l.threads, 0, s>>>(a);
+        row_dots<XT, RT><<<(unsigned)(a.rows < room ? a.rows : room), kLongThreads, 0, s>>>(a);
         if (const int st = launch_status(); st != MFX_OK)
             return st;
-        const dim3 grid((unsigned)((a.cols + 8 * kThreads - 1) / (8 * kThreads)), (unsigned)p.blocks);
-        slab_bwd<XT, RT, VEC><<<grid, kThreads, 0, s>>>(a);
+        const dim3 grid((unsigned)((a.cols + kSlab * kThreads - 1) / (kSlab * kThreads)), (unsigned)p.blocks);
+        slab_bwd<XT, RT><<<grid, kThreads, 0, s>>>(a);
         return launch_status();
     }
-    switch (l.C) {
-    case 1: launch<XT, RT, 1, VEC>(a, l, p.blocks, s); break;
-    case 2: launch<XT, RT, 2, VEC>(a, l, p.blocks, s); break;
-    default: launch<XT, RT, 4, VEC>(a, l, p.blocks, s); break;
-    }
+    a.lanes = p.l.lanes, a.depth = p.l.depth, a.row_bytes = (uint32_t)p.l.row, a.x_bytes = p.x_bytes, a.r_bytes = p.r_bytes;
+    const auto kernel = kernel_of<XT, RT>(p.l.E, vec);
+    occupancy(reinterpret_cast<const void*>(kernel), p.l.threads, p.l.smem);  // its shared memory is allowed
+    kernel<<<(unsigned)p.blocks, p.l.threads, p.l.smem, s>>>(a);
     return launch_status();
 }
 
 template <typename XT, typename RT>
 int run(int w_dt, Args& a, void* dweight, void* workspace, size_t* bytes, bool vec, cudaStream_t s)
 {
-    const Plan p = plan<XT, RT>(a.rows, a.cols);
+    const Plan p = plan<XT, RT>(a.rows, a.cols, vec);
     // partial sums only where dweight is formed, the rows' sums where rows are long
     const size_t need = (size_t)(p.dots + (dweight ? p.ws : 0)) * sizeof(float);
     if (bytes && !workspace) {
@@ -285,7 +312,7 @@ int run(int w_dt, Args& a, void* dweight, void* workspace, size_t* bytes, bool v
         a.dots = p.dots ? static_cast<float*>(workspace) : nullptr;
         a.ws = dweight ? static_cast<float*>(workspace) + p.dots : nullptr;
     }
-    if (const int st = vec ? launch_any<XT, RT, true>(a, p, s) : launch_any<XT, RT, false>(a, p, s); st != MFX_OK)
+    if (const int st = launch<XT, RT>(a, p, vec, s); st != MFX_OK)
         return st;
     return dweight ? launch_dbias_finish(w_dt, a.ws, p.blocks, a.cols, dweight, s) : MFX_OK;
 }

@@ -18,7 +18,8 @@ namespace {
 
 struct Args {
     int64_t rows;
-    int cols, lanes;
+    int cols, lanes, depth;
+    uint32_t row_bytes, x_bytes;  // of a row on its way: all of it, x's part
     const void *x, *residual, *weight;
     bool w_bf16;
     float eps, offset;
@@ -26,7 +27,7 @@ struct Args {
     float* rstd;
     // output in 8 bits
     bool e5m2, e8m0;
-    int group, groups;  // columns of a group (0: the row), groups of a row
+    int group, shift, groups;  // columns of a group (0: the row) and their logarithm, groups of a row
     void* scale;
 };
 
@@ -44,22 +45,31 @@ __device__ __forceinline__ uint32_t pack_fp8x2(float lo, float hi, bool e5m2)
 
 // A group's scale from its largest absolute value, and the factor that takes
 // values to the 8-bit type's range.  The scale of a group of zeros is 1; it
-// is at least 2^-126 so that its reciprocal is finite, and finite, so that
-// infinities saturate.  Powers of two are rounded up: nothing saturates.
+// is at least 2^-126 and at most 2^125, so that its reciprocal is a normal
+// number and infinities saturate.  Both types' largest values are 1.75 times a
+// power of two (448 = 1.75 * 2^8, 57344 = 1.75 * 2^15): rounding up to a power
+// of two is a matter of the exponent, and exact.  Other scales are formed by a
+// product with the rounded reciprocal (2 roundings instead of 1: the divisions
+// cost more than all else in a group).
 struct Scale {
     float s, inv;
 };
 __device__ __forceinline__ Scale scale_of(float top, bool e5m2, bool e8m0)
 {
-    float s = __fdiv_rn(top, e5m2 ? 57344.0f : 448.0f);
-    s = fminf(fmaxf(s, 1.17549435e-38f), 1e38f);
+    constexpr float least = 1.17549435e-38f, most = 4.25352959e37f;
+    Scale r;
     if (e8m0) {
-        const uint32_t b = __float_as_uint(s);
-        s = __uint_as_float((b + 0x7FFFFFu) & 0x7F800000u);
+        const uint32_t up = (__float_as_uint(fminf(top, 1e38f)) + 0x1FFFFFu) & 0x7F800000u, by = (e5m2 ? 15u : 8u) << 23;
+        const uint32_t b = min(max(up, by + (1u << 23)) - by, __float_as_uint(most));
+        r.s = __uint_as_float(b);
+        r.inv = __uint_as_float((254u << 23) - b);
+    } else {
+        r.s = fminf(fmaxf(top * (e5m2 ? 1.0f / 57344.0f : 1.0f / 448.0f), least), most);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.inv) : "f"(r.s));
     }
-    if (top == 0.0f)
-        s = 1.0f;
-    return {s, __fdiv_rn(1.0f, s)};
+    if (!(top > 0.0f))  // zeros, or nothing but NaN
+        r.s = r.inv = 1.0f;
+    return r;
 }
 
 __device__ __forceinline__ void put_scale(const Args& a, int64_t i, float s)
@@ -70,217 +80,286 @@ __device__ __forceinline__ void put_scale(const Args& a, int64_t i, float s)
         static_cast<float*>(a.scale)[i] = s;
 }
 
-// y of a piece of a row (its first column is c0) as 8 bits.  ROW: `row` holds
-// the whole row's scale.
-template <int C, bool VEC>
-__device__ __forceinline__ void store_fp8(const Args& a, int64_t row, int c0, int cols, int tl, const float (&y)[8 * C],
-                                          Scale row_scale, int* tops, bool on)
+template <int V>
+__device__ __forceinline__ void store_fp8(uint8_t* q, const float (&y)[V], float inv, bool e5m2)
 {
-    uint8_t* q = static_cast<uint8_t*>(a.y) + row * a.cols + c0;
-    const int lanes = a.lanes;
-    if constexpr (VEC) {
-        const int n = a.group / 8 < lanes ? a.group / 8 : lanes;  // lanes of a group
-#pragma unroll
-        for (int k = 0; k < C; ++k) {
-            const int c = (k * lanes + tl) * 8;
-            Scale s = row_scale;
-            if (a.group) {
-                float top = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    top = amax(top, y[8 * k + j]);
-                for (int o = n >> 1; o > 0; o >>= 1)
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                s = scale_of(top, a.e5m2, a.e8m0);
-                if (on && c < cols && (tl & (n - 1)) == 0)
-                    put_scale(a, row * a.groups + (c0 + c) / a.group, s.s);
-            }
-            if (on && c < cols) {
-                uint32_t b[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    b[j] = pack_fp8x2(y[8 * k + 2 * j] * s.inv, y[8 * k + 2 * j + 1] * s.inv, a.e5m2);
-                st8(q + c, make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16));
-            }
-        }
+    if constexpr (V == 1) {
+        *q = (uint8_t)pack_fp8x2(y[0] * inv, 0.0f, e5m2);
     } else {
-        // a warp's e-th elements are 32 columns, one group of 32 or a part of one of 128
-        const int g = a.group, first = tl & ~31, lane = tl & 31;
-        if (g > 32) {
-            for (int i = tl; i * g < 8 * C * lanes; i += lanes)
-                tops[i] = 0;
-            lanes > 32 ? __syncthreads() : __syncwarp();
-        }
+        uint32_t b[V / 4];
+        const auto pack = [&](bool as_e5m2) {
 #pragma unroll
-        for (int e = 0; e < 8 * C; ++e) {
-            const int c = e * lanes + tl;
-            Scale s = row_scale;
-            if (g) {
-                const int top = __reduce_max_sync(0xFFFFFFFFu, __float_as_int(amax(0.0f, y[e])));
-                if (g > 32) {
-                    if (lane == 0)
-                        atomicMax(&tops[(e * lanes + first) / g], top);
-                    continue;
-                }
-                s = scale_of(__int_as_float(top), a.e5m2, a.e8m0);
-                if (on && lane == 0 && c < cols)
-                    put_scale(a, row * a.groups + (c0 + c) / g, s.s);
-            }
-            if (on && c < cols)
-                q[c] = (uint8_t)pack_fp8x2(y[e] * s.inv, 0.0f, a.e5m2);
-        }
-        if (g > 32) {
-            lanes > 32 ? __syncthreads() : __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 8 * C; ++e) {
-                const int c = e * lanes + tl;
-                if (on && c < cols) {
-                    const Scale s = scale_of(__int_as_float(tops[c / g]), a.e5m2, a.e8m0);
-                    if (c % g == 0)
-                        put_scale(a, row * a.groups + (c0 + c) / g, s.s);
-                    q[c] = (uint8_t)pack_fp8x2(y[e] * s.inv, 0.0f, a.e5m2);
-                }
-            }
-            lanes > 32 ? __syncthreads() : __syncwarp();
-        }
+            for (int j = 0; j < V / 4; ++j)
+                b[j] = pack_fp8x2(y[4 * j] * inv, y[4 * j + 1] * inv, as_e5m2) |
+                       pack_fp8x2(y[4 * j + 2] * inv, y[4 * j + 3] * inv, as_e5m2) << 16;
+        };
+        if (e5m2)
+            pack(true);
+        else
+            pack(false);
+        if constexpr (V == 8)
+            st8(q, make_uint2(b[0], b[1]));
+        else
+            asm volatile(MFX_ST_OP ".u32 [%0], %1;" ::"l"(q), "r"(b[0]) : "memory");
     }
 }
 
-// h of a piece of a row, in fp32.
-template <typename XT, typename RT, int C, bool VEC>
-__device__ __forceinline__ void load_h(const Args& a, int64_t at, int cols, int tl, float (&f)[8 * C])
+// One scale for the values of a thread's N units from their largest absolute
+// value in the group; `c`: the first unit's column.
+__device__ __forceinline__ Scale group_scale(const Args& a, float top, int64_t scales, int c, bool put)
 {
-    load_row<XT, C, VEC>(static_cast<const XT*>(a.x) + at, cols, a.lanes, tl, f);
-    if (a.residual) {
-        float r[8 * C];
-        load_row<RT, C, VEC>(static_cast<const RT*>(a.residual) + at, cols, a.lanes, tl, r);
-#pragma unroll
-        for (int e = 0; e < 8 * C; ++e)
-            f[e] += r[e];
-    }
+    const Scale s = scale_of(top, a.e5m2, a.e8m0);
+    if (put)
+        put_scale(a, scales + (c >> a.shift), s.s);
+    return s;
 }
 
-template <int C>
-constexpr int max_threads() { return C == 2 ? 512 : 1024; }
-
-// LONG: rows that do not fit a block's registers are walked twice in pieces
-// of 8 C elements a thread, the second time from L2.
-template <typename XT, typename RT, int C, bool VEC, bool Q, bool LONG>
-__global__ void __launch_bounds__(max_threads<C>())
+// Q: y as it is (0), in 8 bits with a scale per row (1) or per group of columns (2).
+template <typename XT, typename RT, int V, int E, int Q>
+__global__ void __launch_bounds__(E == 8 ? 1024 : 512, E == 32 ? 1 : E == 16 ? 2 : 1)
 norm_fwd(const Args a)
 {
+    constexpr int N = E / V;
+    constexpr bool VEC = V > 1;
     __shared__ float2 part[2][32];
-    __shared__ int tops_of[Q && !VEC ? 256 : 1];
+    extern __shared__ __align__(16) char dynamic[];
     const int lanes = a.lanes, teams = blockDim.x / lanes, team = threadIdx.x / lanes, tl = threadIdx.x % lanes;
-    int* tops = tops_of + (teams > 1 ? team * (8 * C * 32 / 128) : 0);
-    const int piece = LONG ? 8 * C * lanes : a.cols;
+    const int cols = a.cols, c0 = column_of<V>(0, lanes, tl);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(dynamic) + team * (uint32_t)a.depth * a.row_bytes;
+    const uint32_t end = ring + (uint32_t)a.depth * a.row_bytes;
+    const int64_t step = (int64_t)gridDim.x * teams, all = a.rows * cols;
+    const XT* const x = static_cast<const XT*>(a.x);
+    const RT* const res = static_cast<const RT*>(a.residual);
+    int64_t row = (int64_t)blockIdx.x * teams + team;
+    const auto start = [&](int64_t r, uint32_t to) {
+        if (r - team < a.rows) {  // a team past the end takes the last row
+            const int64_t at = (r < a.rows ? r : a.rows - 1) * cols;
+            copy_row<XT, V, N>(to, x + at, cols, x, x + all, lanes, tl);
+            if (res)
+                copy_row<RT, V, N>(to + a.x_bytes, res + at, cols, res, res + all, lanes, tl);
+        }
+        copies_commit();
+    };
+    int64_t next = row;
+    for (uint32_t to = ring; to != end; to += a.row_bytes, next += step)
+        start(next, to);
+    float w[N][V];
+    factors_of<V, N>(a.weight, a.w_bf16, a.offset, cols, lanes, tl, w);
     int slot = 0;
-    for (int64_t first = (int64_t)blockIdx.x * teams; first < a.rows; first += (int64_t)gridDim.x * teams, slot ^= 1) {
-        const bool on = first + team < a.rows;
-        const int64_t row = on ? first + team : a.rows - 1, at = row * a.cols;  // a team past the end reads the last
-        float f[8 * C];
+    uint32_t buf = ring;
+    for (; row - team < a.rows; row += step, next += step, slot ^= 1) {
+        const bool on = row < a.rows;
+        const int64_t at = (on ? row : a.rows - 1) * cols;
+        copies_wait(a.depth - 1);
+        if (!VEC)
+            team_barrier(lanes);
+        const uint32_t sx = buf + (VEC ? 0u : where(x + at)), sr = buf + a.x_bytes + (VEC || !res ? 0u : where(res + at));
+        float f[N][V];
         float2 v = make_float2(0.0f, 0.0f);
-        for (int c0 = 0; c0 < a.cols; c0 += piece) {
-            const int cols = a.cols - c0 < piece ? a.cols - c0 : piece;
-            load_h<XT, RT, C, VEC>(a, at + c0, cols, tl, f);
 #pragma unroll
-            for (int e = 0; e < 8 * C; ++e)
-                v.x = fmaf(f[e], f[e], v.x);
-            if (Q && a.group == 0) {
-                const char* w = static_cast<const char*>(a.weight);
-                w = w ? w + (int64_t)c0 * (a.w_bf16 ? 2 : 4) : w;
+        for (int k = 0; k < N; ++k) {
+            const int c = column_of<V>(k, lanes, tl);
 #pragma unroll
-                for (int k = 0; k < C; ++k) {
-                    float wk[8];
-                    factors<VEC>(w, a.w_bf16, a.offset, cols, lanes, tl, k, wk);
+            for (int j = 0; j < V; ++j)
+                f[k][j] = 0.0f;
+            if (c < cols) {
+                lds_unit<XT, V>(sx + c * (uint32_t)sizeof(XT), f[k]);
+                if (res) {
+                    float g[V];
+                    lds_unit<RT, V>(sr + c * (uint32_t)sizeof(RT), g);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v.y = amax(v.y, f[8 * k + j] * wk[j]);
+                    for (int j = 0; j < V; ++j)
+                        f[k][j] += g[j];
                 }
             }
         }
-        v = over_team<Q>(v, lanes, part, slot);
-        const float rstd = __frsqrt_rn(__fdiv_rn(v.x, (float)a.cols) + a.eps);
+        if (a.h && on) {
+            RT* h = static_cast<RT*>(a.h) + at;
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (const int c = column_of<V>(k, lanes, tl); c < cols)
+                    store_unit<RT, V>(h + c, f[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v.x = fmaf(f[k][j], f[k][j], v.x);
+                f[k][j] *= w[k][j];
+                if (Q == 1)
+                    v.y = amax(v.y, f[k][j]);
+            }
+        v = over_team<Q == 1>(v, lanes, part, slot);
+        start(next, buf);  // all have what they read there: it is in the sum
+        buf = buf + a.row_bytes == end ? ring : buf + a.row_bytes;
+        const float rstd = __frsqrt_rn(__fdiv_rn(v.x, (float)cols) + a.eps);
         if (a.rstd && on && tl == 0)
+            a.rstd[row] = rstd;
+        if constexpr (Q == 0) {
+            if (on) {
+                XT* y = static_cast<XT*>(a.y) + at;
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        f[k][j] *= rstd;
+                    if (const int c = column_of<V>(k, lanes, tl); c < cols)
+                        store_unit<XT, V>(y + c, f[k]);
+                }
+            }
+        } else {
+            uint8_t* q = static_cast<uint8_t*>(a.y) + at;
+            const int64_t scales = (on ? row : 0) * a.groups;
+            const int share = min(a.group >> (V == 8 ? 3 : V == 4 ? 2 : 0), min(lanes, 32));  // lanes of a group
+            Scale s = {1.0f, 1.0f};
+            if (Q == 1) {
+                s = scale_of(v.y * rstd, a.e5m2, a.e8m0);
+                if (on && tl == 0)
+                    put_scale(a, row, s.s);
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int c = column_of<V>(k, lanes, tl);
+                if (Q == 2 && V > 1) {
+                    float top = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        top = amax(top, f[k][j]);
+                    for (int o = share >> 1; o > 0; o >>= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                    s = group_scale(a, top * rstd, scales, c, on && c < cols && (c & (a.group - 1)) == 0);
+                } else if (Q == 2 && a.group == 32) {
+                    const int top = __reduce_max_sync(0xFFFFFFFFu, __float_as_int(amax(0.0f, f[k][0])));
+                    s = group_scale(a, __int_as_float(top) * rstd, scales, c, on && c < cols && (tl & 31) == 0);
+                } else if (Q == 2 && k % 4 == 0) {  // a warp's four steps
+                    float mine = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mine = amax(mine, f[(k + i) % N][0]);
+                    const int top = __reduce_max_sync(0xFFFFFFFFu, __float_as_int(mine));
+                    s = group_scale(a, __int_as_float(top) * rstd, scales, c, on && c < cols && (tl & 31) == 0);
+                }
+                // (h * weight) * (rstd / s): one rounding less than y itself has
+                const float by = rstd * s.inv;
+                if (on && c < cols)
+                    store_fp8<V>(q + c, f[k], by, a.e5m2);
+            }
+        }
+    }
+}
+
+// Rows longer than that: read twice, column by column, a warp's four steps of
+// 32 columns a round.
+template <typename XT, typename RT, bool Q>
+__global__ void __launch_bounds__(1024, 1)
+norm_fwd_long(const Args a)
+{
+    __shared__ float2 part[2][32];
+    const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * 128 + lane;
+    int slot = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, slot ^= 1) {
+        const int64_t at = row * a.cols;
+        const XT* x = static_cast<const XT*>(a.x) + at;
+        const RT* r = a.residual ? static_cast<const RT*>(a.residual) + at : nullptr;
+        float2 v = make_float2(0.0f, 0.0f);
+        float f[4], w[4][1];
+        const auto read = [&](int c0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = c0 + 32 * i;
+                f[i] = w[i][0] = 0.0f;
+                if (c < a.cols) {
+                    f[i] = load1(x + c) + (r ? load1(r + c) : 0.0f);
+                    factors<1>(a.weight, a.w_bf16, a.offset, c, w[i]);
+                }
+            }
+        };
+        for (int c0 = first; c0 - lane < a.cols; c0 += 4096) {
+            read(c0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v.x = fmaf(f[i], f[i], v.x);
+                if (Q)
+                    v.y = amax(v.y, f[i] * w[i][0]);
+            }
+        }
+        v = over_team<Q>(v, 1024, part, slot);
+        const float rstd = __frsqrt_rn(__fdiv_rn(v.x, (float)a.cols) + a.eps);
+        if (a.rstd && threadIdx.x == 0)
             a.rstd[row] = rstd;
         Scale s = {1.0f, 1.0f};
         if (Q && a.group == 0) {
             s = scale_of(v.y * rstd, a.e5m2, a.e8m0);
-            if (on && tl == 0)
+            if (threadIdx.x == 0)
                 put_scale(a, row, s.s);
         }
-        for (int c0 = 0; c0 < a.cols; c0 += piece) {
-            const int cols = a.cols - c0 < piece ? a.cols - c0 : piece;
-            if (LONG)
-                load_h<XT, RT, C, VEC>(a, at + c0, cols, tl, f);
-            if (a.h && on)
-                store_row<RT, C, VEC>(static_cast<RT*>(a.h) + at + c0, cols, lanes, tl, f);
-            const char* w = static_cast<const char*>(a.weight);
-            w = w ? w + (int64_t)c0 * (a.w_bf16 ? 2 : 4) : w;
+        for (int c0 = first; c0 - lane < a.cols; c0 += 4096) {
+            read(c0);
+            float tops[4];
+            if (Q && a.group) {
 #pragma unroll
-            for (int k = 0; k < C; ++k) {
-                float wk[8];
-                factors<VEC>(w, a.w_bf16, a.offset, cols, lanes, tl, k, wk);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    f[8 * k + j] = f[8 * k + j] * rstd * wk[j];
+                for (int i = 0; i < 4; ++i)
+                    tops[i] = __int_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_int(amax(0.0f, f[i] * w[i][0]))));
+                if (a.group == 128)
+                    tops[0] = tops[1] = tops[2] = tops[3] = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             }
-            if constexpr (Q)
-                store_fp8<C, VEC>(a, row, c0, cols, tl, f, s, tops, on);
-            else if (on)
-                store_row<XT, C, VEC>(static_cast<XT*>(a.y) + at + c0, cols, lanes, tl, f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = c0 + 32 * i;
+                if (Q && a.group)
+                    s = group_scale(a, tops[i] * rstd, row * a.groups, c, lane == 0 && c < a.cols && (c & (a.group - 1)) == 0);
+                if (c >= a.cols)
+                    continue;
+                if (a.h)
+                    store1(static_cast<RT*>(a.h) + at + c, f[i]);
+                if constexpr (Q) {
+                    const float y[1] = {f[i] * w[i][0]};
+                    store_fp8<1>(static_cast<uint8_t*>(a.y) + at + c, y, rstd * s.inv, a.e5m2);
+                } else {
+                    store1(static_cast<XT*>(a.y) + at + c, f[i] * w[i][0] * rstd);
+                }
+            }
         }
     }
 }
 
-// Rows in a warp's lanes up to 1024 columns, in a block's threads up to 32768.
-Layout layout(int64_t rows, int64_t cols, bool vec, int sms)
+template <typename K>
+int launch(K kernel, const Args& a, const Layout& l, cudaStream_t s)
 {
-    const int64_t units = (cols + 7) / 8;
-    Layout l = {4, 32, 256, false};
-    if (units <= 32 * 4) {
-        l.C = units <= 32 ? 1 : units <= 64 ? 2 : 4;
-        while (vec && l.C == 1 && l.lanes > 8 && units <= l.lanes / 2)
-            l.lanes /= 2;
-        return l;
-    }
-    // few rows: one run a thread, the shortest way through the block
-    l.C = units <= 256 || (rows <= 2 * sms && units <= 1024) ? 1 : units <= 1024 ? 2 : 4;
-    l.longer = units > 1024 * 4;
-    const int64_t want = (units + l.C - 1) / l.C;
-    l.lanes = l.threads = l.longer ? 1024 : (int)((want + 31) / 32 * 32);
-    return l;
-}
-
-template <typename XT, typename RT, int C, bool VEC, bool Q, bool LONG>
-int launch(const Args& a, const Layout& l, cudaStream_t s)
-{
-    const void* kernel = reinterpret_cast<const void*>(norm_fwd<XT, RT, C, VEC, Q, LONG>);
     const int64_t teams = l.threads / l.lanes, need = (a.rows + teams - 1) / teams;
-    const int64_t room = (int64_t)sm_count() * occupancy(kernel, l.threads, 0);
-    norm_fwd<XT, RT, C, VEC, Q, LONG><<<(unsigned)(need < room ? need : room), l.threads, 0, s>>>(a);
+    const int64_t room = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(kernel), l.threads, l.smem);
+    kernel<<<(unsigned)(need < room ? need : room), l.threads, l.smem, s>>>(a);
     return launch_status();
 }
 
-template <typename XT, typename RT, bool VEC, bool Q>
-int with_layout(const Args& a, const Layout& l, cudaStream_t s)
+template <typename XT, typename RT, int V, int Q>
+int with_units(const Args& a, const Layout& l, cudaStream_t s)
 {
-    if (l.longer)
-        return launch<XT, RT, 4, VEC, Q, true>(a, l, s);
-    switch (l.C) {
-    case 1: return launch<XT, RT, 1, VEC, Q, false>(a, l, s);
-    case 2: return launch<XT, RT, 2, VEC, Q, false>(a, l, s);
-    default: return launch<XT, RT, 4, VEC, Q, false>(a, l, s);
-    }
+    if (l.E == 8)
+        return launch(norm_fwd<XT, RT, V, 8, Q>, a, l, s);
+    if constexpr (V > 1)
+        if (l.E == 16)
+            return launch(norm_fwd<XT, RT, V, 16, Q>, a, l, s);
+    return launch(norm_fwd<XT, RT, V, 32, Q>, a, l, s);
 }
 
+// fp32 with a bf16 residual is no mix that training makes: it goes column by
+// column.
 template <typename XT, typename RT, bool Q>
-int with_types(const Args& a, bool vec, cudaStream_t s)
+int with_types(Args a, bool vec, cudaStream_t s)
 {
-    const Layout l = layout(a.rows, a.cols, vec, sm_count());
-    Args b = a;
-    b.lanes = l.lanes;
-    return vec ? with_layout<XT, RT, true, Q>(b, l, s) : with_layout<XT, RT, false, Q>(b, l, s);
+    constexpr int V = sizeof(XT) > sizeof(RT) ? 1 : sizeof(RT) == 2 ? 8 : 4;
+    a.x_bytes = (uint32_t)(((size_t)a.cols * sizeof(XT) + kPad + 15) / 16 * 16);
+    const size_t row = a.x_bytes + (a.residual ? (size_t)a.cols * sizeof(RT) + kPad : 0);
+    const Layout l = layout(a.rows, a.cols, vec ? V : 1, row, 0, [](int e) { return e == 32 ? 512 : 1024; });
+    if (l.depth == 0) {
+        a.lanes = 1024;
+        return launch(norm_fwd_long<XT, RT, Q>, a, Layout{0, 1024, 1024, 0, 0, 0}, s);
+    }
+    a.lanes = l.lanes, a.depth = l.depth, a.row_bytes = (uint32_t)l.row;
+    if (Q && a.group)
+        return vec ? with_units<XT, RT, V, Q ? 2 : 0>(a, l, s) : with_units<XT, RT, 1, Q ? 2 : 0>(a, l, s);
+    return vec ? with_units<XT, RT, V, Q>(a, l, s) : with_units<XT, RT, 1, Q>(a, l, s);
 }
 
 template <bool Q>
@@ -364,7 +443,7 @@ int mfx_add_rmsnorm_quant_fwd(int x_dt, int res_dt, int w_dt, int64_t rows, int6
     a.x = x, a.residual = residual, a.weight = weight, a.eps = eps, a.offset = weight_offset;
     a.y = q, a.h = h, a.rstd = rstd, a.scale = scale;
     a.e5m2 = q_dt == MFX_E5M2, a.e8m0 = scale_dt == MFX_E8M0;
-    a.group = (int)group, a.groups = group ? (int)((cols + group - 1) / group) : 1;
+    a.group = (int)group, a.shift = group == 32 ? 5 : 7, a.groups = group ? (int)((cols + group - 1) / group) : 1;
     return rmsnorm::run<true>(x_dt, res_dt, w_dt, rows, cols, rows * cols,
                               rows * a.groups * (scale_dt == MFX_E8M0 ? 1 : 4), a, stream);
 }
