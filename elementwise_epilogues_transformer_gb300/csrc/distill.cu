@@ -25,11 +25,12 @@ namespace {
 constexpr int kMostEntries = 1024;
 
 struct Args {
-    int64_t rows, ld, ldo;
+    int64_t rows, ld, ldo, ahead;
     int n, K, cluster, runs, chunks, per;
     const void *logits, *index, *teacher;
     bool wide, t_bf16;
     float scale, k2;
+    Scaling k;
     const float *lse, *g;
     float *loss, *stats;
     const float* stats_in;
@@ -148,12 +149,12 @@ __device__ __forceinline__ uint4 grad_run(const uint4& w, float ref, float k2, f
 
 // The gradient of columns [lo, hi) of an output row from the piece that holds
 // them: runs aligned like the piece's (whole ones of it four at a time), or not.
-template <typename T>
-__device__ __forceinline__ void put_piece(const Piece<T>& p, T* o, const Runs<T>& ro, int lo, int hi, float ref, float k2,
+template <typename T, int STEP>
+__device__ __forceinline__ void put_piece(const Piece<T, STEP>& p, T* o, const Runs<T>& ro, int lo, int hi, float ref, float k2,
                                           float A, bool zero)
 {
     constexpr int U = 4, V = Run<T>::V;
-    const int step = p.step, tid = threadIdx.x;
+    const int step = p.step(), tid = threadIdx.x;
     const uint4 none = make_uint4(0, 0, 0, 0);
     // whole runs of the output that lie in [lo, hi): [v0, v1)
     const int v0 = (lo + ro.phase + V - 1) / V, v1 = max((hi + ro.phase) / V, v0);
@@ -205,7 +206,7 @@ __device__ __forceinline__ void put_listed(const Args& a, T* o, const List& l, i
     }
 }
 
-template <typename T, bool GRAD>
+template <typename T, bool GRAD, int STEP>
 __global__ void __launch_bounds__(kThreadsMost + 32, MFX_VOCAB_BLOCKS)
 distill_fwd(const Args a)
 {
@@ -222,7 +223,7 @@ distill_fwd(const Args a)
         const int share = (r.count + a.cluster - 1) / a.cluster;
         const int first = min(rank * share, r.count), last = min(first + share, r.count);
         const int lo = max(r.column(first), 0), hi = min(r.column(last), a.n);
-        Piece<T> p(r, smem_addr(dynamic), threads);
+        Piece<T, STEP> p(r, smem_addr(dynamic), threads);
         p.set(first, min(first + a.runs, last));
         Teacher w = {};
         Stats v = no_stats();
@@ -235,11 +236,13 @@ distill_fwd(const Args a)
         } else {
             BestRun none = {-INFINITY, 0};
             p.fill();
-            scan<T, false, false>(p, a.k2, v, none);
+            if (tid == 0 && row + a.ahead < a.rows)
+                p.prefetch(a.ahead * a.ld);
+            scan<T, STEP, false, false>(p, a.k, v, none);
             while (p.last < last) {  // (threads read only what they copied)
                 p.set(p.last, min(p.last + a.runs, last));
                 p.fill();
-                scan<T, false, false>(p, a.k2, v, none);
+                scan<T, STEP, false, false>(p, a.k, v, none);
             }
         }
         join_block<false>(v, a.k2, part, threads >> 5);  // and the slice and Q are there for all threads
@@ -266,7 +269,7 @@ distill_fwd(const Args a)
                 __syncthreads();  // listed logits of other pieces are read before they may be written
             for (;;) {            // the last piece is the one at hand
                 if (tid < threads)
-                    put_piece<T>(p, o, ro, p.lo(), p.hi(), v.ref, a.k2, A, ratio == 0.0f);
+                    put_piece(p, o, ro, p.lo(), p.hi(), v.ref, a.k2, A, ratio == 0.0f);
                 __syncthreads();
                 if (p.first == first)
                     break;
@@ -345,7 +348,8 @@ int launch_fwd(Args a, cudaStream_t s)
 {
     const Split sp = split(a.rows, a.n, sizeof(T));
     a.cluster = sp.cluster, a.runs = sp.runs;
-    const cudaError_t e = launch_rows(distill_fwd<T, GRAD>, a, sp, sp.threads + 32, sp.smem() + (size_t)a.K * 12, s);
+    const cudaError_t e = launch_rows(known_step(sp) ? distill_fwd<T, GRAD, kThreadsMost> : distill_fwd<T, GRAD, 0>, a, sp,
+                                      sp.threads + 32, sp.smem() + (size_t)a.K * 12, s);
     return e == cudaSuccess ? launch_status() : cuda_failure(e);
 }
 
@@ -370,7 +374,7 @@ int check(int dt, int t_dt, int64_t rows, int64_t vocab, int64_t ld, int64_t k, 
         return MFX_ERR_DTYPE;
     if (!row_sizes_ok(rows, vocab, ld) || k < 0 || k > kMostEntries)
         return MFX_ERR_SHAPE;
-    if (!(scale > 0.0f) || std::isinf(scale))
+    if (!(scale > 0.0f) || !std::isfinite(scale * kLog2e))
         return MFX_ERR_VALUE;
     return MFX_OK;
 }
@@ -403,7 +407,7 @@ int run(int dt, int t_dt, int64_t rows, int64_t vocab, int64_t ld, int64_t k, co
     Args a = {};
     a.rows = rows, a.ld = ld, a.ldo = ldo, a.n = (int)vocab, a.K = (int)k, a.logits = logits, a.index = index;
     a.teacher = teacher, a.wide = index_bits == 64, a.t_bf16 = t_dt == MFX_BF16, a.scale = scale;
-    a.k2 = scale * kLog2e, a.lse = lse, a.g = g, a.loss = loss, a.stats = stats, a.stats_in = stats_in, a.out = out;
+    a.k2 = scale * kLog2e, a.k = scaling_of(scale), a.lse = lse, a.g = g, a.loss = loss, a.stats = stats, a.stats_in = stats_in, a.out = out;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!loss)
         return dt == MFX_BF16 ? launch_bwd<bf16>(a, s) : launch_bwd<float>(a, s);

@@ -24,11 +24,12 @@ constexpr int kKept = 256;     // candidates that a round may find there
 constexpr int kCandidates = kRound * 8 + kKept;
 
 struct Args {
-    int64_t rows, ld;
+    int64_t rows, ld, ahead;
     int n, top, cluster, runs;
     const void *logits, *tokens;
     bool wide;
-    float scale, k2;
+    float scale;
+    Scaling k;
     float *logprob, *entropy, *top_logprob, *stats;
     int32_t* top_index;
 };
@@ -100,8 +101,8 @@ __device__ __forceinline__ void sort_out(const Key* cand, int n, int top, Key* s
 // Should those be more than there is room for (rows built so that few threads
 // hold most large logits), the runs are taken in small rounds and cut to the
 // best after each.
-template <typename T>
-__device__ __forceinline__ void find_top(const Piece<T>& p, bool whole, int slice_first, int slice_last,
+template <typename T, int STEP>
+__device__ __forceinline__ void find_top(const Piece<T, STEP>& p, bool whole, int slice_first, int slice_last,
                                          const BestRun best, int top, TopSmem& sm)
 {
     constexpr int V = Run<T>::V;
@@ -133,45 +134,48 @@ __device__ __forceinline__ void find_top(const Piece<T>& p, bool whole, int slic
         sm.list[atomicAdd(&sm.listed, 1)] = tid;
     __syncthreads();
     const int first = whole ? p.first : slice_first, last = whole ? p.last : slice_last;
-    const int each = (last - first + T_ - 1) / T_, items = sm.listed * each;
+    // a warp goes over a listed thread's runs, a lane each
+    const int each = (last - first + T_ - 1) / T_, lane = tid & 31, warp = tid >> 5, listed = sm.listed;
     Key bound = limit;
-    for (int base = 0, size = T_; base < items;) {
+    float least = limit >> 32 ? value_of(limit) : -INFINITY;
+    for (int warps = T_ >> 5, l0 = 0, i0 = 0; l0 < listed;) {
         const int before = sm.count;
         __syncthreads();
-        const int item = base + tid;
-        if (tid < size && item < items) {
-            const int u = first + sm.list[item / each] + item % each * T_;
-            if (u < last) {
-                const uint4 w = whole ? lds16(p.at(u)) : load_run(p.r.p, p.r.n, p.r.column(u));
+        const int u = first + (warp < warps && l0 + warp < listed ? sm.list[l0 + warp] + (i0 + lane) * T_ : last);
+        if (i0 + lane < each && u < last) {
+            const uint4 w = whole ? lds16(p.at(u)) : load_run(p.r.p, p.r.n, p.r.column(u));
+            if (Run<T>::top(w) >= least) {
                 float2 f[V / 2];
                 Run<T>::widen(w, f);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const float z = j & 1 ? f[j >> 1].y : f[j >> 1].x;
-                    const Key q = key_of(z, p.r.column(u) + j);
-                    if (z > -INFINITY && q >= bound)
-                        if (const int at = atomicAdd(&sm.count, 1); at < kCandidates)
-                            sm.cand[at] = q;
+                    if (z >= least && z > -INFINITY)
+                        if (const Key q = key_of(z, p.r.column(u) + j); q >= bound)
+                            if (const int at = atomicAdd(&sm.count, 1); at < kCandidates)
+                                sm.cand[at] = q;
                 }
             }
         }
         __syncthreads();
         const int n = sm.count;
-        if (n > kCandidates) {  // not all of them had room: again, in small rounds
+        if (n > kCandidates) {  // not all of them had room: again, in rounds that cannot overflow
             __syncthreads();
             if (tid == 0)
                 sm.count = before;
-            size = kRound;
+            warps = kRound / 32;
             __syncthreads();
             continue;
         }
-        base += size;
-        if (base < items && n > kKept) {
+        i0 += 32;
+        if (i0 >= each)
+            i0 = 0, l0 += warps;
+        if (l0 < listed && n > kKept) {
             sort_out(sm.cand, n, top, sm.sel);
             __syncthreads();
             for (int j = tid; j < top; j += T_)
                 sm.cand[j] = sm.sel[j];
-            bound = sm.sel[top - 1];
+            bound = sm.sel[top - 1], least = value_of(bound);
             if (tid == 0)
                 sm.count = top;
             __syncthreads();
@@ -181,7 +185,7 @@ __device__ __forceinline__ void find_top(const Piece<T>& p, bool whole, int slic
     __syncthreads();
 }
 
-template <typename T, bool TOP>
+template <typename T, bool TOP, int STEP>
 __global__ void __launch_bounds__(kThreadsMost, MFX_VOCAB_BLOCKS)
 logprobs_fwd(const Args a)
 {
@@ -211,21 +215,23 @@ logprobs_fwd(const Args a)
         const int first = min(rank * share, r.count), last = min(first + share, r.count);
         Stats v = no_stats();
         BestRun best = {-INFINITY, 0};
-        Piece<T> p(r, smem_addr(dynamic), blockDim.x);
+        Piece<T, STEP> p(r, smem_addr(dynamic), blockDim.x);
         p.set(first, min(first + a.runs, last));
         p.fill();
-        scan<T, true, TOP>(p, a.k2, v, best);
+        if (tid == 0 && row + a.ahead < a.rows)
+            p.prefetch(a.ahead * a.ld);
+        scan<T, STEP, true, TOP>(p, a.k, v, best);
         while (p.last < last) {  // (threads read only what they copied)
             p.set(p.last, min(p.last + a.runs, last));
             p.fill();
-            scan<T, true, TOP>(p, a.k2, v, best);
+            scan<T, STEP, true, TOP>(p, a.k, v, best);
         }
         if (TOP)
             find_top(p, p.first == first, first, last, best, a.top, sm);
-        join_block<true>(v, a.k2, part, blockDim.x >> 5);
+        join_block<true>(v, a.k.k2, part, blockDim.x >> 5);
         if (a.cluster > 1)
-            join_cluster<true>(v, a.k2, &mine, a.cluster);
-        if (rank == 0) {
+            join_cluster<true>(v, a.k.k2, &mine, a.cluster);
+        if (rank == 0 && (TOP || tid < 32)) {
             const bool empty = v.l == 0.0f;
             const float log_l = logf(v.l), inv = empty ? 0.0f : __fdiv_rn(1.0f, v.l), U = empty ? 0.0f : -kLn2 * v.s * inv;
             if (tid == 0) {
@@ -335,7 +341,9 @@ int launch_fwd(Args a, cudaStream_t s)
 {
     const Split sp = split(a.rows, a.n, sizeof(T));
     a.cluster = sp.cluster, a.runs = sp.runs;
-    const cudaError_t e = launch_rows(logprobs_fwd<T, TOP>, a, sp, sp.threads, sp.smem() + (TOP ? sizeof(TopSmem) : 0), s);
+    const size_t smem = sp.smem() + (TOP ? sizeof(TopSmem) : 0);
+    const cudaError_t e = launch_rows(known_step(sp) ? logprobs_fwd<T, TOP, kThreadsMost> : logprobs_fwd<T, TOP, 0>, a, sp,
+                                      sp.threads, smem, s);
     return e == cudaSuccess ? launch_status() : cuda_failure(e);
 }
 
@@ -358,7 +366,7 @@ int check(int dt, int64_t rows, int64_t vocab, int64_t ld, int index_bits, float
         return MFX_ERR_DTYPE;
     if (!row_sizes_ok(rows, vocab, ld))
         return MFX_ERR_SHAPE;
-    if (!(scale > 0.0f) || std::isinf(scale))
+    if (!(scale > 0.0f) || !std::isfinite(scale * kLog2e))
         return MFX_ERR_VALUE;
     return MFX_OK;
 }
@@ -396,7 +404,7 @@ int mfx_token_logprobs_fwd(int dt, int64_t rows, int64_t vocab, int64_t ld, cons
     }
     V::Args a = {};
     a.rows = rows, a.ld = ld, a.n = (int)vocab, a.top = (int)top, a.logits = logits, a.tokens = tokens;
-    a.wide = index_bits == 64, a.scale = scale, a.k2 = scale * V::kLog2e;
+    a.wide = index_bits == 64, a.scale = scale, a.k = V::scaling_of(scale);
     a.logprob = logprob, a.entropy = entropy, a.top_logprob = top_logprob, a.top_index = top_index, a.stats = stats;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dt == MFX_BF16)

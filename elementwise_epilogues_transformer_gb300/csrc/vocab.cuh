@@ -68,6 +68,17 @@ template <> struct Run<bf16> {
         asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
         return r;
     }
+    // Elements below a floor raised to it; NaN stays.
+    static __device__ __forceinline__ uint32_t raise2(uint32_t a, uint32_t floor)
+    {
+        uint32_t r;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(floor));
+        return r;
+    }
+    static __device__ __forceinline__ uint4 raise(const uint4& w, uint32_t f)
+    {
+        return make_uint4(raise2(w.x, f), raise2(w.y, f), raise2(w.z, f), raise2(w.w, f));
+    }
     static __device__ __forceinline__ float top(const uint4& w)
     {
         const float2 m = widen2(max2(max2(w.x, w.y), max2(w.z, w.w)));
@@ -175,13 +186,13 @@ __device__ __forceinline__ void store_run(const Runs<T>& o, T* row, int v, int l
     }
 }
 
-// Running statistics of some of a row's elements: their maximum (-inf for
-// none), the reference that the exponents are taken from (the maximum, or the
-// lowest finite value while there is none), l = sum of e, s = sum of e * t.
+// Running statistics of some of a row's elements: the reference that the
+// exponents are taken from (their maximum; the lowest finite value while there
+// is none above), l = sum of e, s = sum of e * t.
 struct Stats {
-    float m, ref, l, s;
+    float ref, l, s;
 };
-__device__ __forceinline__ Stats no_stats() { return {-INFINITY, -3.402823466e38f, 0.0f, 0.0f}; }
+__device__ __forceinline__ Stats no_stats() { return {-3.402823466e38f, 0.0f, 0.0f}; }
 
 // Takes the sums of `v` to the reference `ref`, which is at least its own.
 __device__ __forceinline__ void rebase(Stats& v, float ref, float k2)
@@ -263,14 +274,16 @@ constexpr int kGroups = 4;  // copies are waited for in four steps
 
 // Runs [first, last) of a row in shared memory at `buf` (16-byte aligned, one
 // run to spare before and behind).  Those of [whole0, whole1) are whole; one at
-// the row's head and one at its tail may not be.
-template <typename T> struct Piece {
+// the row's head and one at its tail may not be.  STEP: the threads that share
+// it (the block's first ones) where that is known when this is compiled, which
+// turns a thread's addresses into constants, else 0.
+template <typename T, int STEP> struct Piece {
     Runs<T> r;
-    int first, last, whole0, whole1, step;
+    int first, last, whole0, whole1, step_;
     uint32_t buf;
 
-    // step: the threads that share it (the block's first ones)
-    __device__ __forceinline__ Piece(const Runs<T>& r_, uint32_t buf_, int step_) : r(r_), step(step_), buf(buf_) {}
+    __device__ __forceinline__ Piece(const Runs<T>& r_, uint32_t buf_, int step) : r(r_), step_(step), buf(buf_) {}
+    __device__ __forceinline__ int step() const { return STEP ? STEP : step_; }
     __device__ __forceinline__ void set(int f, int l)
     {
         first = f, last = l;
@@ -281,28 +294,49 @@ template <typename T> struct Piece {
     // runs of a thread that a step copies
     __device__ __forceinline__ int each() const
     {
-        const int mine = (last - first + step - 1) / step;
+        const int mine = (last - first + step() - 1) / step();
         return max((mine + kGroups - 1) / kGroups, min(mine, 4));
     }
     // Starts the copies of this thread's runs: every step-th.
     __device__ __forceinline__ void fill() const
     {
-        const int n = each();
-        int u = first + threadIdx.x;
-        if (u < whole0)
-            sts16(at(u), edge_run(r.p, r.n, r.column(u)));
-        if (whole1 < last && (last - 1 - u) % step == 0 && last - 1 >= u)
+        const int n = each(), tid = threadIdx.x;
+        const uint32_t tail = (uint32_t)(last - 1 - first - tid);
+        if (tid == 0 && whole0 > first)
+            sts16(at(first), edge_run(r.p, r.n, r.column(first)));
+        if (whole1 < last && tail % (uint32_t)step() == 0 && last - 1 >= first + tid)
             sts16(at(last - 1), edge_run(r.p, r.n, r.column(last - 1)));
-        const T* from = r.p + r.column(u);
-        uint32_t to = at(u);
+        // this thread's runs up to whole1, the first of them left out if it is not whole
+        int left = whole1 - first - tid;
+        const T* from = r.p + r.column(first + tid);
+        uint32_t to = at(first + tid);
+        bool skip = tid == 0 && whole0 > first;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-#pragma unroll 4
-            for (int i = 0; i < n; ++i, u += step, from += step * Run<T>::V, to += 16u * step)
-                if (u >= whole0 && u < whole1)
+            int i = 0;
+            for (; i + 4 <= n && left > 3 * step() && !skip; i += 4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    copy16(to + 16u * (uint32_t)(j * step()), from + j * step() * Run<T>::V);
+                left -= 4 * step(), from += 4 * step() * Run<T>::V, to += 64u * (uint32_t)step();
+            }
+#pragma unroll 1
+            for (; i < n; ++i) {
+                if (left > 0 && !skip)
                     copy16(to, from);
+                skip = false;
+                left -= step(), from += step() * Run<T>::V, to += 16u * (uint32_t)step();
+            }
             copies_commit();
         }
+    }
+    // Asks L2 for the same runs of the row that begins `ahead` elements further
+    // on (one thread; its vectors there are the ones around these elements).
+    __device__ __forceinline__ void prefetch(int64_t ahead) const
+    {
+        const uintptr_t a = (reinterpret_cast<uintptr_t>(r.p + ahead + r.column(whole0)) + 15u) & ~(uintptr_t)15;
+        const uint32_t n = whole1 - whole0 > 1 ? (uint32_t)(whole1 - whole0 - 1) * 16u : 0u;
+        prefetch_l2_if(reinterpret_cast<const void*>(a), n, n);
     }
     // Columns [lo, hi) that it holds.
     __device__ __forceinline__ int lo() const { return max(r.column(first), 0); }
@@ -340,9 +374,59 @@ struct BestRun {
     int u;
 };
 
+// What a launch's scale says of exponents: scale * log2 e, and up to where a
+// row's maximum leaves room for a floor (bf16 pairs of it) that is far enough
+// below it to have no power and near enough for a finite exponent.
+struct Scaling {
+    float k2, tame;
+    uint32_t floor;
+};
+inline Scaling scaling_of(float scale)
+{
+    Scaling s = {scale * kLog2e, 0.0f, 0u};
+    if (s.k2 >= 1e-30f) {
+        // 2^122 (about 5e36), or less where the scale is large: a power of two, so exact in bf16
+        int e = 122;
+        float k = s.k2;
+        for (; k > 1.0f && e > -100; k *= 0.5f)
+            --e;
+        const uint32_t f = 0x8000u | (uint32_t)(e + 127) << 7;
+        s.floor = f << 16 | f;
+        s.tame = ldexpf(0.5f, e);
+    }
+    return s;
+}
+
+// Adds up e (and e * t) of U runs.  CLAMP: exponents are held at -200.
+template <typename T, bool ENTROPY, bool CLAMP, int U>
+__device__ __forceinline__ void add_runs(Stats& v, const uint4 (&w)[U], float k2)
+{
+    constexpr int P = Run<T>::V / 2;
+    const float2 ref = f2(-v.ref), k = f2(k2);
+    float2 l = f2(0.0f), s = f2(0.0f);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        float2 f[P];
+        Run<T>::widen(w[i], f);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            float2 t = mul2(add2(f[j], ref), k);
+            if (CLAMP)
+                t = make_float2(at_least_zero_power(t.x), at_least_zero_power(t.y));
+            const float2 e = exp2_pair(t);
+            l = add2(l, e);
+            if (ENTROPY)
+                s = fma2(e, t, s);
+        }
+    }
+    v.l += l.x + l.y;
+    if (ENTROPY)
+        v.s += s.x + s.y;
+}
+
 // Takes U runs of a thread (from u on, every `step`) into its statistics.
 template <typename T, bool ENTROPY, bool BEST, int U>
-__device__ __forceinline__ void take(Stats& v, BestRun& best, const uint4 (&w)[U], int u, int step, float k2)
+__device__ __forceinline__ void take(Stats& v, BestRun& best, uint4 (&w)[U], int u, int step, const Scaling& k)
 {
     float m[U];
 #pragma unroll
@@ -356,45 +440,32 @@ __device__ __forceinline__ void take(Stats& v, BestRun& best, const uint4 (&w)[U
 #pragma unroll
         for (int i = 0; i < U; ++i)
             if (m[i] > best.m)
-                best = {m[i], u + i * step};
+                best.m = m[i], best.u = u + i * step;
     }
-    if (top > v.m) {
-        v.m = top;
-        rebase(v, fmaxf(top, v.ref), k2);
-    }
-    const float2 ref = f2(-v.ref), k = f2(k2);
+    if (top > v.ref)
+        rebase(v, top, k.k2);
+    if constexpr (!ENTROPY) {
+        add_runs<T, false, false, U>(v, w, k.k2);
+    } else if constexpr (sizeof(T) == 4) {
+        add_runs<T, true, true, U>(v, w, k.k2);
+    } else if (fabsf(v.ref) < k.tame) {  // columns at -inf are raised in pairs, for half the instructions
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        constexpr int P = Run<T>::V / 2;
-        float2 f[P], e[P], s = f2(0.0f);
-        Run<T>::widen(w[i], f);
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-            float2 t = mul2(add2(f[j], ref), k);
-            if (ENTROPY)
-                t = make_float2(at_least_zero_power(t.x), at_least_zero_power(t.y));
-            e[j] = exp2_pair(t);
-            if (ENTROPY)
-                s = fma2(e[j], t, s);
-        }
-#pragma unroll
-        for (int o = 1; o < P; o *= 2)
-#pragma unroll
-            for (int j = 0; j + o < P; j += 2 * o)
-                e[j] = add2(e[j], e[j + o]);
-        v.l += e[0].x + e[0].y;
-        if (ENTROPY)
-            v.s += s.x + s.y;
+        for (int i = 0; i < U; ++i)
+            w[i] = Run<T>::raise(w[i], k.floor);
+        add_runs<T, true, false, U>(v, w, k.k2);
+    } else {
+        add_runs<T, true, true, U>(v, w, k.k2);
     }
 }
 
 // This thread's runs of a piece whose copies are under way.
-template <typename T, bool ENTROPY, bool BEST>
-__device__ __forceinline__ void scan(const Piece<T>& p, float k2, Stats& v, BestRun& best)
+template <typename T, int STEP, bool ENTROPY, bool BEST>
+__device__ __forceinline__ void scan(const Piece<T, STEP>& p, const Scaling& k, Stats& v, BestRun& best)
 {
     constexpr int U = 4;
-    const int n = p.each(), step = p.step;
+    const int n = p.each(), step = p.step();
     int u = p.first + threadIdx.x;
+    uint32_t from = p.at(u);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
         if (g == 0)
@@ -405,21 +476,21 @@ __device__ __forceinline__ void scan(const Piece<T>& p, float k2, Stats& v, Best
             copies_wait<1>();
         else
             copies_wait<0>();
-        const int end = u + n * step;
+        int i = 0;
 #pragma unroll 1
-        for (; u + (U - 1) * step < p.last && u + (U - 1) * step < end; u += U * step) {
+        for (; i + U <= n && u + (U - 1) * step < p.last; i += U, u += U * step, from += 16u * (uint32_t)(U * step)) {
             uint4 w[U];
 #pragma unroll
             for (int j = 0; j < U; ++j)
-                w[j] = lds16(p.at(u) + 16u * (uint32_t)(j * step));
-            take<T, ENTROPY, BEST, U>(v, best, w, u, step, k2);
+                w[j] = lds16(from + 16u * (uint32_t)(j * step));
+            take<T, ENTROPY, BEST, U>(v, best, w, u, step, k);
         }
 #pragma unroll 1
-        for (; u < end; u += step)
+        for (; i < n; ++i, u += step, from += 16u * (uint32_t)step)
             if (u < p.last) {
                 uint4 w[1];
-                w[0] = lds16(p.at(u));
-                take<T, ENTROPY, BEST, 1>(v, best, w, u, step, k2);
+                w[0] = lds16(from);
+                take<T, ENTROPY, BEST, 1>(v, best, w, u, step, k);
             }
     }
 }
@@ -506,11 +577,17 @@ inline Split split(int64_t rows, int64_t n, int64_t bytes)
     return sp;
 }
 
-// Launches a kernel over rows (grid.x / cluster at a time).
+// A kernel's STEP for a launch.
+inline bool known_step(const Split& sp) { return sp.threads == kThreadsMost; }
+
+// Launches a kernel over rows (grid.x / cluster at a time).  a.ahead: rows
+// that are worked on at a time, so that a block knows which one comes when it
+// is done.
 template <typename A>
-cudaError_t launch_rows(void (*kernel)(const A), const A& a, const Split& sp, int threads, size_t smem, cudaStream_t s)
+cudaError_t launch_rows(void (*kernel)(const A), A a, const Split& sp, int threads, size_t smem, cudaStream_t s)
 {
     const int64_t room = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(kernel), threads, smem);
+    a.ahead = room / sp.cluster;
     cudaLaunchConfig_t cfg = {};
     // the blocks of a cluster find places together, which leaves some of them
     // free: clusters come row by row, single blocks stay
