@@ -301,44 +301,42 @@ distill_fwd(const Args a)
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256)
+template <typename T, int STEP>
+__global__ void __launch_bounds__(kThreadsMost + 32)
 distill_bwd(const Args a)
 {
     extern __shared__ __align__(16) char dynamic[];
     __shared__ int listed;
-    constexpr int U = 4, V = Run<T>::V;
     const List l(dynamic, a.K);
+    // one warp more than write the row: it sees to the list
+    const int threads = blockDim.x - 32, tid = threadIdx.x;
     for (int64_t item = blockIdx.x; item < a.rows * a.chunks; item += gridDim.x) {
         const int64_t row = item / a.chunks;
         const T* z = static_cast<const T*>(a.logits) + row * a.ld;
         T* o = static_cast<T*>(a.out) + row * a.ldo;
         const float ref = a.stats_in[4 * row], ratio = a.stats_in[4 * row + 1];
         const Runs<T> ro(o, a.n);
-        const int u0 = min((int)(item % a.chunks) * a.per, ro.count), u1 = min(u0 + a.per, ro.count), step = blockDim.x;
+        const int u0 = min((int)(item % a.chunks) * a.per, ro.count), u1 = min(u0 + a.per, ro.count);
+        if (ratio == 0.0f) {  // the same for all threads
+            if (tid < threads)
+                zero_runs(o, ro, u0, u1, threads);
+            continue;
+        }
         const int lo = max(ro.column(u0), 0), hi = min(ro.column(u1), a.n);
         const float g = a.g[row], A = g * a.scale * ratio;
-        if (threadIdx.x < 32) {
+        if (tid >= threads) {
             const Teacher w = read_list<true>(a, row, l, lo, hi, {a.stats_in[4 * row + 2], a.stats_in[4 * row + 3], 0.0f, 0.0f, 0});
-            for (int j = threadIdx.x; j < w.n; j += 32)
+            for (int j = tid & 31; j < w.n; j += 32)
                 l.z[j] = load1(z + l.col[j]);
-            if (threadIdx.x == 0)
+            if (tid == threads)
                 listed = w.n;
         }
-        __syncthreads();  // listed logits are read before they may be written
-        for (int u = u0 + threadIdx.x; u < u1; u += U * step) {
-            uint4 x[U];
-#pragma unroll
-            for (int i = 0; i < U; ++i)
-                x[i] = ratio != 0.0f && u + i * step < u1 ? load_run(z, a.n, ro.column(u + i * step)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < U; ++i)
-                if (u + i * step < u1)
-                    store_run(ro, o, u + i * step, 0, a.n, ratio != 0.0f ? grad_run<T>(x[i], ref, a.k2, A) : x[i]);
-        }
+        if (a.out == a.logits)
+            __syncthreads();  // listed logits are read before they are written
+        if (tid < threads)
+            map_runs<T, STEP>(z, o, ro, u0, u1, threads, [&](const uint4& w, int) { return grad_run<T>(w, ref, a.k2, A); });
         __syncthreads();
-        if (ratio != 0.0f)
-            put_listed<T>(a, o, l, listed, ref, ratio, g);
+        put_listed<T>(a, o, l, listed, ref, ratio, g);
         __syncthreads();
     }
 }
@@ -356,14 +354,14 @@ int launch_fwd(Args a, cudaStream_t s)
 template <typename T>
 int launch_bwd(Args a, cudaStream_t s)
 {
-    const int64_t runs = (a.n * (int64_t)sizeof(T) + 15) / 16 + 1;  // with a head and a tail
-    const int threads = threads_for(runs, 256);
-    a.per = threads * 8;
-    a.chunks = (int)((runs + a.per - 1) / a.per);
+    const Chunks c = chunks_of(a.rows, a.n, sizeof(T));
+    a.per = c.per, a.chunks = c.count;
     const size_t smem = (size_t)a.K * 12;
     const int64_t need = a.rows * a.chunks;
-    const int64_t room = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(distill_bwd<T>), threads, smem);
-    distill_bwd<T><<<(unsigned)(need < room ? need : room), threads, smem, s>>>(a);
+    const int threads = c.threads + 32;
+    const auto kernel = c.threads == kThreadsMost ? distill_bwd<T, kThreadsMost> : distill_bwd<T, 0>;
+    const int64_t room = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(kernel), threads, smem);
+    kernel<<<(unsigned)(need < room ? need : room), threads, smem, s>>>(a);
     return launch_status();
 }
 

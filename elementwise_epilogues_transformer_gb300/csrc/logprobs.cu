@@ -27,7 +27,7 @@ struct Args {
     int64_t rows, ld, ahead;
     int n, top, cluster, runs;
     const void *logits, *tokens;
-    bool wide;
+    bool wide, eager;  // eager: rows are read before it is known whether they count
     float scale;
     Scaling k;
     float *logprob, *entropy, *top_logprob, *stats;
@@ -194,8 +194,17 @@ logprobs_fwd(const Args a)
     TopSmem& sm = *reinterpret_cast<TopSmem*>(dynamic + (size_t)(a.runs + 2) * 16);
     const int rank = a.cluster > 1 ? (int)cluster_rank() : 0, tid = threadIdx.x;
     for (int64_t row = blockIdx.x / a.cluster; row < a.rows; row += gridDim.x / a.cluster) {
+        const T* z = static_cast<const T*>(a.logits) + row * a.ld;
+        const Runs<T> r(z, a.n);
+        const int share = (r.count + a.cluster - 1) / a.cluster;
+        const int first = min(rank * share, r.count), last = min(first + share, r.count);
+        Piece<T, STEP> p(r, smem_addr(dynamic), blockDim.x);
+        p.set(first, min(first + a.runs, last));
+        if (a.eager)
+            p.fill();
         const int token = vocab::column_of(a.tokens, a.wide, row, a.n);
         if (token < 0) {  // left out; the same for every block of the cluster
+            copies_wait<0>();
             if (rank == 0) {
                 if (tid == 0) {
                     a.logprob[row] = 0.0f, a.entropy[row] = 0.0f;
@@ -208,16 +217,11 @@ logprobs_fwd(const Args a)
             }
             continue;
         }
-        const T* z = static_cast<const T*>(a.logits) + row * a.ld;
+        if (!a.eager)
+            p.fill();
         const float zt = load1(z + token);
-        const Runs<T> r(z, a.n);
-        const int share = (r.count + a.cluster - 1) / a.cluster;
-        const int first = min(rank * share, r.count), last = min(first + share, r.count);
         Stats v = no_stats();
         BestRun best = {-INFINITY, 0};
-        Piece<T, STEP> p(r, smem_addr(dynamic), blockDim.x);
-        p.set(first, min(first + a.runs, last));
-        p.fill();
         if (tid == 0 && row + a.ahead < a.rows)
             p.prefetch(a.ahead * a.ld);
         scan<T, STEP, true, TOP>(p, a.k, v, best);
@@ -286,53 +290,43 @@ struct BwdArgs {
     void* out;
 };
 
-// U runs of a thread in flight; a run is four pairs of bf16 or two of fp32.
-template <typename T>
-__global__ void __launch_bounds__(256)
+template <typename T, int STEP>
+__global__ void __launch_bounds__(kThreadsMost)
 logprobs_bwd(const BwdArgs a)
 {
-    constexpr int U = 4, V = Run<T>::V;
+    constexpr int V = Run<T>::V;
     for (int64_t item = blockIdx.x; item < a.rows * a.chunks; item += gridDim.x) {
         const int64_t row = item / a.chunks;
         const T* z = static_cast<const T*>(a.logits) + row * a.ld;
         T* o = static_cast<T*>(a.out) + row * a.ldo;
         const Runs<T> ro(o, a.n);
+        const int u0 = min((int)(item % a.chunks) * a.per, ro.count), u1 = min(u0 + a.per, ro.count);
         const int token = vocab::column_of(a.tokens, a.wide, row, a.n);
         const float ref = a.stats[3 * row], inv = a.stats[3 * row + 1], H = a.stats[3 * row + 2];
         const float g = a.g ? a.g[row] : 0.0f, ge = a.ge ? a.ge[row] : 0.0f;
-        const float2 A = f2(-a.scale * inv * fmaf(ge, H, g)), B = f2(-a.scale * inv * ge * kLn2), R = f2(-ref), K = f2(a.k2);
-        const bool none = token < 0 || inv == 0.0f;
-        const int u0 = (int)(item % a.chunks) * a.per, u1 = min(u0 + a.per, ro.count), step = blockDim.x;
-        for (int u = u0 + threadIdx.x; u < u1; u += U * step) {
-            uint4 w[U];
-#pragma unroll
-            for (int i = 0; i < U; ++i)
-                w[i] = !none && u + i * step < u1 ? load_run(z, a.n, ro.column(u + i * step)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                if (u + i * step >= u1)
-                    break;
-                const int c = ro.column(u + i * step);
-                if (!none) {
-                    float2 f[V / 2];
-                    Run<T>::widen(w[i], f);
-#pragma unroll
-                    for (int j = 0; j < V / 2; ++j) {
-                        float2 t = mul2(add2(f[j], R), K);
-                        t = make_float2(at_least_zero_power(t.x), at_least_zero_power(t.y));
-                        f[j] = mul2(exp2_pair(t), fma2(B, t, A));
-                    }
-                    if (token >= c && token < c + V) {
-#pragma unroll
-                        for (int j = 0; j < V; ++j)
-                            if (c + j == token)
-                                (j & 1 ? f[j >> 1].y : f[j >> 1].x) += a.scale * g;
-                    }
-                    w[i] = Run<T>::narrow(f);
-                }
-                store_run(ro, o, u + i * step, 0, a.n, w[i]);
-            }
+        if (token < 0 || inv == 0.0f) {
+            zero_runs(o, ro, u0, u1, blockDim.x);
+            continue;
         }
+        const float2 A = f2(-a.scale * inv * fmaf(ge, H, g)), B = f2(-a.scale * inv * ge * kLn2), R = f2(-ref), K = f2(a.k2);
+        const float sg = a.scale * g;
+        map_runs<T, STEP>(z, o, ro, u0, u1, blockDim.x, [&](const uint4& w, int c) {
+            float2 f[V / 2];
+            Run<T>::widen(w, f);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                float2 t = mul2(add2(f[j], R), K);
+                t = make_float2(at_least_zero_power(t.x), at_least_zero_power(t.y));
+                f[j] = mul2(exp2_pair(t), fma2(B, t, A));
+            }
+            if ((uint32_t)(token - c) < (uint32_t)V) {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (c + j == token)
+                        (j & 1 ? f[j >> 1].y : f[j >> 1].x) += sg;
+            }
+            return Run<T>::narrow(f);
+        });
     }
 }
 
@@ -341,6 +335,7 @@ int launch_fwd(Args a, cudaStream_t s)
 {
     const Split sp = split(a.rows, a.n, sizeof(T));
     a.cluster = sp.cluster, a.runs = sp.runs;
+    a.eager = a.rows * a.cluster <= sm_count();  // few rows: time counts, not bytes
     const size_t smem = sp.smem() + (TOP ? sizeof(TopSmem) : 0);
     const cudaError_t e = launch_rows(known_step(sp) ? logprobs_fwd<T, TOP, kThreadsMost> : logprobs_fwd<T, TOP, 0>, a, sp,
                                       sp.threads, smem, s);
@@ -350,13 +345,12 @@ int launch_fwd(Args a, cudaStream_t s)
 template <typename T>
 int launch_bwd(BwdArgs a, cudaStream_t s)
 {
-    const int64_t runs = (a.n * (int64_t)sizeof(T) + 15) / 16 + 1;  // with a head and a tail
-    const int threads = threads_for(runs, 256);
-    a.per = threads * 8;
-    a.chunks = (int)((runs + a.per - 1) / a.per);
+    const Chunks c = chunks_of(a.rows, a.n, sizeof(T));
+    a.per = c.per, a.chunks = c.count;
     const int64_t need = a.rows * a.chunks;
-    const int64_t room = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(logprobs_bwd<T>), threads, 0);
-    logprobs_bwd<T><<<(unsigned)(need < room ? need : room), threads, 0, s>>>(a);
+    const auto kernel = c.threads == kThreadsMost ? logprobs_bwd<T, kThreadsMost> : logprobs_bwd<T, 0>;
+    const int64_t room = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(kernel), c.threads, 0);
+    kernel<<<(unsigned)(need < room ? need : room), c.threads, 0, s>>>(a);
     return launch_status();
 }
 

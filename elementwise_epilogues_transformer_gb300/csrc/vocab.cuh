@@ -495,6 +495,60 @@ __device__ __forceinline__ void scan(const Piece<T, STEP>& p, const Scaling& k, 
     }
 }
 
+// A block's runs [u0, u1) of an output row from a row of logits: `f` makes a
+// run of results of a run of logits and its first column.  Four runs of a
+// thread are in flight.  Rows that lie alike take whole vectors, others the
+// vectors around each run.
+template <typename T, int STEP, typename F>
+__device__ __forceinline__ void map_runs(const T* z, T* o, const Runs<T>& ro, int u0, int u1, int threads, F f)
+{
+    constexpr int U = 4, V = Run<T>::V;
+    const int step = STEP ? STEP : threads;
+    const bool alike = (reinterpret_cast<uintptr_t>(z) & 15u) == (reinterpret_cast<uintptr_t>(o) & 15u);
+    int u = u0 + threadIdx.x;
+    if (alike) {
+        // whole runs: all but one at the row's head and one at its tail
+        if (u < u1 && !ro.whole(u)) {
+            store_run(ro, o, u, 0, ro.n, f(edge_run(z, ro.n, ro.column(u)), ro.column(u)));
+            u += step;
+        }
+        const int whole = u1 > u0 && !ro.whole(u1 - 1) ? u1 - 1 : u1;
+        int c = ro.column(u);
+        for (; u + (U - 1) * step < whole; u += U * step, c += U * step * V) {
+            uint4 w[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                w[i] = ld16(z + c + i * step * V);
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                st16(o + c + i * step * V, f(w[i], c + i * step * V));
+        }
+        for (; u < whole; u += step, c += step * V)
+            st16(o + c, f(ld16(z + c), c));
+        if (u < u1)
+            store_run(ro, o, u, 0, ro.n, f(edge_run(z, ro.n, c), c));
+        return;
+    }
+    for (; u < u1; u += U * step) {
+        uint4 w[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            w[i] = u + i * step < u1 ? load_run(z, ro.n, ro.column(u + i * step)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (u + i * step < u1)
+                store_run(ro, o, u + i * step, 0, ro.n, f(w[i], ro.column(u + i * step)));
+    }
+}
+
+// Zeros in a block's runs [u0, u1) of an output row.
+template <typename T>
+__device__ __forceinline__ void zero_runs(T* o, const Runs<T>& ro, int u0, int u1, int step)
+{
+    for (int u = u0 + threadIdx.x; u < u1; u += step)
+        store_run(ro, o, u, 0, ro.n, make_uint4(0, 0, 0, 0));
+}
+
 // --- clusters -------------------------------------------------------------
 // The same in two steps; the second one alone orders nothing.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
@@ -605,6 +659,24 @@ cudaError_t launch_rows(void (*kernel)(const A), A a, const Split& sp, int threa
     if (e != cudaSuccess)
         cudaGetLastError();  // it is this call's, not the next one's
     return e;
+}
+
+// How the backwards cut rows: threads of a block, runs of a chunk, chunks of a
+// row.  A chunk is eight runs a thread or, where those leave multiprocessors
+// without one, four.
+struct Chunks {
+    int threads, per, count;
+};
+inline Chunks chunks_of(int64_t rows, int64_t n, int64_t bytes)
+{
+    const int64_t runs = (n * bytes + 15) / 16 + 1;  // with a head and a tail
+    Chunks c;
+    c.threads = threads_for(runs, kThreadsMost);
+    c.per = c.threads * 8;
+    if (rows * ((runs + c.per - 1) / c.per) < 8 * sm_count())
+        c.per = c.threads * 4;
+    c.count = (int)((runs + c.per - 1) / c.per);
+    return c;
 }
 
 inline bool row_sizes_ok(int64_t rows, int64_t vocab, int64_t ld)
