@@ -85,7 +85,8 @@ _SIGS = {
     "mfx_add_rmsnorm_fwd": [_I, _I, _I, _I64, _I64, _P, _P, _P, _F, _F, _P, _P, _P, _P],
     "mfx_add_rmsnorm_quant_fwd": [_I, _I, _I, _I64, _I64, _P, _P, _P, _F, _F, _I, _I64, _I, _P, _P, _P, _P, _P],
     "mfx_add_rmsnorm_bwd": [_I, _I, _I, _I64, _I64, _P, _P, _P, _P, _F, _P, _P, _P, _P, _P, C.POINTER(C.c_size_t), _P],
-    "mfx_token_logprobs_fwd": [_I, _I64, _I64, _I64, _P, _I, _P, _F, _I64, _P, _P, _P, _P, _P, _P],
+    "mfx_token_logprobs_fwd": [_I, _I64, _I64, _I64, _P, _I, _P, _F, _I64, _P, _P, _P, _P, _P, _P, C.POINTER(C.c_size_t),
+                               _P],
     "mfx_token_logprobs_bwd": [_I, _I64, _I64, _I64, _P, _P, _P, _I, _P, _P, _F, _P, _I64, _P],
     "mfx_topk_distill_fwd": [_I, _I, _I64, _I64, _I64, _I64, _P, _I, _P, _P, _P, _F, _P, _P, _P],
     "mfx_topk_distill_bwd": [_I, _I, _I64, _I64, _I64, _I64, _P, _P, _I, _P, _P, _P, _F, _P, _I64, _P],
@@ -672,6 +673,15 @@ def _run(name, dev, *args):
         raise MfxError(st, name)
 
 
+def _run_with_workspace(name, dev, head, tail, device, workspace, sizes, stream):
+    """The same for a call with a workspace, which may need none."""
+    if dev == _current_device():
+        _with_workspace(name, head, tail, device, workspace, sizes, none=True, stream=stream)
+    else:
+        with torch.cuda.device(dev):
+            _with_workspace(name, head, tail, device, workspace, sizes, none=True, stream=stream)
+
+
 def _stream_of(stream, t, dev):
     return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream, t)
 
@@ -788,13 +798,8 @@ def mfx_add_rmsnorm_bwd(dy, h, rstd, weight, dh=None, weight_offset=0.0, dx=None
     if dweight is not None or (weight is not None and need_dweight):
         dweight, dwptr = _new(dweight, "dweight", (cols,), weight.dtype, dev, dy, stream)
     head = (xdt, rdt, wdt, rows, cols, dy.data_ptr(), hptr, sptr, wptr, float(weight_offset), eptr, xptr, rptr, dwptr)
-    tail = (_stream_of(stream, dy, dev),)
-    sizes = (dev, xdt, rdt, rows, cols, dwptr is None)
-    if dev == _current_device():
-        _with_workspace("mfx_add_rmsnorm_bwd", head, tail, dy.device, workspace, sizes, none=True, stream=stream)
-    else:
-        with torch.cuda.device(dev):
-            _with_workspace("mfx_add_rmsnorm_bwd", head, tail, dy.device, workspace, sizes, none=True, stream=stream)
+    _run_with_workspace("mfx_add_rmsnorm_bwd", dev, head, (_stream_of(stream, dy, dev),), dy.device, workspace,
+                        (dev, xdt, rdt, rows, cols, dwptr is None), stream)
     return dx, dresidual, dweight
 
 
@@ -846,7 +851,7 @@ def _dlogits(dlogits, logits, dev, rows, vocab, stream):
 
 
 def mfx_token_logprobs_fwd(logits, tokens, scale=1.0, top=0, logprob=None, entropy=None, top_logprob=None,
-                           top_index=None, stats=None, need_stats=True, stream=None):
+                           top_index=None, stats=None, need_stats=True, workspace=None, stream=None):
     """(logprob [rows], entropy [rows], top_logprob [rows, top], top_index
     [rows, top], stats [rows, 3]) of softmax(scale * logits [rows, vocab]) at
     tokens [rows] (int32 or int64; one outside the vocabulary leaves its row
@@ -865,8 +870,12 @@ def mfx_token_logprobs_fwd(logits, tokens, scale=1.0, top=0, logprob=None, entro
         raise ValueError("top_logprob and top_index need top")
     if stats is not None or need_stats:
         stats, sptr = _new(stats, "stats", (rows, 3), f32, dev, logits, stream)
-    _run("mfx_token_logprobs_fwd", dev, code, rows, vocab, ld, logits.data_ptr(), bits, kptr, float(scale), top, lptr, eptr,
-         vptr, iptr, sptr, _stream_of(stream, logits, dev))
+    head = (code, rows, vocab, ld, logits.data_ptr(), bits, kptr, float(scale), top, lptr, eptr, vptr, iptr, sptr)
+    st = _stream_of(stream, logits, dev)
+    if top > 0:
+        _run_with_workspace("mfx_token_logprobs_fwd", dev, head, (st,), logits.device, workspace, (dev, code, rows, vocab), stream)
+    else:
+        _run("mfx_token_logprobs_fwd", dev, *head, None, None, st)
     return logprob, entropy, top_logprob, top_index, stats
 
 

@@ -234,7 +234,7 @@ distill_fwd(const Args a)
             while (p.last < last)
                 p.set(p.last, min(p.last + a.runs, last));
         } else {
-            BestRun none = {-INFINITY, 0};
+            float none;
             p.fill();
             if (tid == 0 && row + a.ahead < a.rows)
                 p.prefetch(a.ahead * a.ld);

@@ -17,10 +17,11 @@ namespace mfx {
 namespace vocab {
 namespace {
 
-constexpr int kMostTop = 64;  // alternatives
-constexpr int kKeys = 64;      // keys that bound the search for them
-constexpr int kRound = 64;     // runs of a round that cannot overflow the candidates
-constexpr int kKept = 256;     // candidates that a round may find there
+constexpr int kMostTop = 64;   // alternatives
+constexpr int kMostKeys = 128;  // groups of threads that bound the search for them
+constexpr int kMostListed = 8 * kThreadsMost;  // threads of all slices
+constexpr int kRound = 64;      // runs of a round that cannot overflow the candidates
+constexpr int kKept = 256;      // candidates that a round may find there
 constexpr int kCandidates = kRound * 8 + kKept;
 
 struct Args {
@@ -32,6 +33,7 @@ struct Args {
     Scaling k;
     float *logprob, *entropy, *top_logprob, *stats;
     int32_t* top_index;
+    float* ws;  // of each row: its reference, log l, every thread's largest logit
 };
 
 // A column and its logit as one number: larger for larger logits (-0 and 0
@@ -52,11 +54,11 @@ __device__ __forceinline__ int column_of(Key k) { return (int)(0xFFFFFFFFu - (ui
 // Shared memory of the search for alternatives.
 struct TopSmem {
     Key cand[kCandidates];
-    Key keys[kKeys];
-    Key sel[kMostTop];  // the block's alternatives in order, 0 behind them
+    Key keys[kMostKeys];
+    Key sel[kMostTop];  // the alternatives in order, 0 behind them
     Key limit;
-    int list[kThreadsMost];  // threads that may hold some
     int listed, count;
+    uint16_t list[kMostListed];  // threads (of slices) that may hold some
 };
 
 // The `top` largest of cand[0, n) in order to sel, 0 behind them.  Barriers
@@ -89,27 +91,30 @@ __device__ __forceinline__ void sort_out(const Key* cand, int n, int top, Key* s
     }
 }
 
-// The `top` largest columns above -inf of the slice that `p` holds (`whole`) or
-// ends, to sm.sel in order.
+// The `top` largest columns above -inf of runs [begin, end) of a row, in
+// `slices` slices of `share` runs, to sm.sel in order.  m: the largest logit of this thread's runs of each
+// slice; run_at(u): run u of the row.
 //
-// Threads know their largest logit and its run.  The top-th largest of 64
-// groups of threads (each one's key with the last column of its run, so not
-// above the true one) bounds the top-th largest of all from below, and only
-// threads whose own key (with the first column) reaches it can hold a column
-// that does: of 4096 runs' elements about as many as are asked for.  Their runs
-// are read again, from shared memory, for the columns that reach the bound.
-// Should those be more than there is room for (rows built so that few threads
-// hold most large logits), the runs are taken in small rounds and cut to the
-// best after each.
-template <typename T, int STEP>
-__device__ __forceinline__ void find_top(const Piece<T, STEP>& p, bool whole, int slice_first, int slice_last,
-                                         const BestRun best, int top, TopSmem& sm)
+// The top-th largest of 64 groups of threads (128 for more than 24) bounds the
+// top-th largest logit from below, and only threads whose largest logit
+// reaches it can hold a column that does: of all elements about as many as are
+// asked for.  Their runs are read again for the columns that reach the bound.
+// Should those be more than there is room for (many equal logits, or few
+// threads with most of the large ones), the runs are taken in small rounds and
+// the candidates cut to the best, which raises the bound.
+template <typename T, int S, typename F>
+__device__ __forceinline__ void find_top(const Runs<T>& r, int begin, int end, int slices, int share, const float (&m)[S],
+                                         int top, TopSmem& sm, F run_at)
 {
     constexpr int V = Run<T>::V;
-    const int tid = threadIdx.x, T_ = blockDim.x, nkeys = T_ < kKeys ? T_ : kKeys, per = T_ / nkeys;
-    const bool any = best.m > -INFINITY;
-    const int c0 = p.r.column(best.u);
-    Key k = any ? key_of(best.m, c0 + V - 1) : (Key)tid;  // those without any: below all others, none alike
+    const int tid = threadIdx.x, T_ = blockDim.x, lane = tid & 31, warp = tid >> 5;
+    const int want = top <= 24 ? 64 : kMostKeys, nkeys = T_ < want ? T_ : want, per = T_ / nkeys;
+    float best = m[0];
+#pragma unroll
+    for (int s = 1; s < S; ++s)
+        best = fmaxf(best, m[s]);
+    // equal ones in some order: a thread's place, below all columns
+    Key k = (best > -INFINITY ? key_of(best, 0) >> 32 << 32 : 0) | (Key)tid;
     for (int o = 1; o < per; o <<= 1) {
         const Key q = __shfl_xor_sync(0xFFFFFFFFu, k, o);
         k = q > k ? q : k;
@@ -120,46 +125,50 @@ __device__ __forceinline__ void find_top(const Piece<T, STEP>& p, bool whole, in
         sm.listed = 0, sm.count = 0, sm.limit = 0;
     __syncthreads();
     if (top <= nkeys) {
-        int r = 0;
+        int rank = 0;
         for (int j = tid % per; j < nkeys; j += per)
-            r += sm.keys[j] > k;
+            rank += sm.keys[j] > k;
         for (int o = 1; o < per; o <<= 1)
-            r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
-        if (tid % per == 0 && r == top - 1)
-            sm.limit = k;
+            rank += __shfl_xor_sync(0xFFFFFFFFu, rank, o);
+        if (tid % per == 0 && rank == top - 1)
+            sm.limit = k >> 32 << 32;
         __syncthreads();
     }
-    const Key limit = sm.limit;
-    if (any && key_of(best.m, max(c0, 0)) >= limit)
-        sm.list[atomicAdd(&sm.listed, 1)] = tid;
+    Key bound = sm.limit;
+    float least = bound ? value_of(bound) : -INFINITY;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+        if (s < slices && m[s] > -INFINITY && m[s] >= least)
+            sm.list[atomicAdd(&sm.listed, 1)] = (uint16_t)(s * kThreadsMost + tid);
     __syncthreads();
-    const int first = whole ? p.first : slice_first, last = whole ? p.last : slice_last;
     // a warp goes over a listed thread's runs, a lane each
-    const int each = (last - first + T_ - 1) / T_, lane = tid & 31, warp = tid >> 5, listed = sm.listed;
-    Key bound = limit;
-    float least = limit >> 32 ? value_of(limit) : -INFINITY;
-    for (int warps = T_ >> 5, l0 = 0, i0 = 0; l0 < listed;) {
+    const int each = (share + T_ - 1) / T_, listed = sm.listed, all = T_ >> 5;
+    for (int warps = all, l0 = 0, i0 = 0; l0 < listed;) {
         const int before = sm.count;
         __syncthreads();
-        const int u = first + (warp < warps && l0 + warp < listed ? sm.list[l0 + warp] + (i0 + lane) * T_ : last);
-        if (i0 + lane < each && u < last) {
-            const uint4 w = whole ? lds16(p.at(u)) : load_run(p.r.p, p.r.n, p.r.column(u));
-            if (Run<T>::top(w) >= least) {
-                float2 f[V / 2];
-                Run<T>::widen(w, f);
+        if (warp < warps && l0 + warp < listed && i0 + lane < each) {
+            const int who = sm.list[l0 + warp], first = begin + who / kThreadsMost * share;
+            const int u = first + who % kThreadsMost + (i0 + lane) * T_;
+            if (u < min(first + share, end)) {
+                const uint4 w[1] = {run_at(u)};
+                const int c = r.column(u);
+                if (key_of(Run<T>::template top_of<1>(w), max(c, 0)) >= bound) {
+                    float2 f[V / 2];
+                    Run<T>::widen(w[0], f);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float z = j & 1 ? f[j >> 1].y : f[j >> 1].x;
-                    if (z >= least && z > -INFINITY)
-                        if (const Key q = key_of(z, p.r.column(u) + j); q >= bound)
-                            if (const int at = atomicAdd(&sm.count, 1); at < kCandidates)
-                                sm.cand[at] = q;
+                    for (int j = 0; j < V; ++j) {
+                        const float z = j & 1 ? f[j >> 1].y : f[j >> 1].x;
+                        if (z >= least && z > -INFINITY)
+                            if (const Key q = key_of(z, c + j); q >= bound)
+                                if (const int at = atomicAdd(&sm.count, 1); at < kCandidates)
+                                    sm.cand[at] = q;
+                    }
                 }
             }
         }
         __syncthreads();
         const int n = sm.count;
-        if (n > kCandidates) {  // not all of them had room: again, in rounds that cannot overflow
+        if (n > kCandidates) {  // not all of them had room: again, in a round that cannot overflow
             __syncthreads();
             if (tid == 0)
                 sm.count = before;
@@ -178,6 +187,8 @@ __device__ __forceinline__ void find_top(const Piece<T, STEP>& p, bool whole, in
             bound = sm.sel[top - 1], least = value_of(bound);
             if (tid == 0)
                 sm.count = top;
+            if (i0 == 0)
+                warps = all;
             __syncthreads();
         }
     }
@@ -185,7 +196,21 @@ __device__ __forceinline__ void find_top(const Piece<T, STEP>& p, bool whole, in
     __syncthreads();
 }
 
-template <typename T, bool TOP, int STEP>
+// The alternatives of a row from its list, by a block.
+__device__ __forceinline__ void put_top(const Args& a, int64_t row, const Key* list, float ref, float log_l)
+{
+    for (int j = threadIdx.x; j < a.top; j += blockDim.x) {
+        const Key k = list[j];
+        a.top_logprob[row * a.top + j] = k ? (value_of(k) - ref) * a.scale - log_l : -INFINITY;
+        a.top_index[row * a.top + j] = k ? column_of(k) : -1;
+    }
+}
+
+// TOP: without alternatives (0); their search within the kernel (1: few rows,
+// where a second launch would cost more), or by pick_top, for which every
+// thread leaves its largest logit in the workspace (2: the search's barriers
+// would stand in the way of the next rows' copies).
+template <typename T, int TOP, int STEP>
 __global__ void __launch_bounds__(kThreadsMost, MFX_VOCAB_BLOCKS)
 logprobs_fwd(const Args a)
 {
@@ -211,7 +236,7 @@ logprobs_fwd(const Args a)
                     if (a.stats)
                         a.stats[3 * row] = 0.0f, a.stats[3 * row + 1] = 0.0f, a.stats[3 * row + 2] = 0.0f;
                 }
-                if (TOP)
+                if (TOP == 1)
                     for (int j = tid; j < a.top; j += blockDim.x)
                         a.top_logprob[row * a.top + j] = -INFINITY, a.top_index[row * a.top + j] = -1;
             }
@@ -221,21 +246,27 @@ logprobs_fwd(const Args a)
             p.fill();
         const float zt = load1(z + token);
         Stats v = no_stats();
-        BestRun best = {-INFINITY, 0};
+        float best[1] = {-INFINITY};
         if (tid == 0 && row + a.ahead < a.rows)
             p.prefetch(a.ahead * a.ld);
-        scan<T, STEP, true, TOP>(p, a.k, v, best);
+        scan<T, STEP, true, TOP != 0>(p, a.k, v, best[0]);
         while (p.last < last) {  // (threads read only what they copied)
             p.set(p.last, min(p.last + a.runs, last));
             p.fill();
-            scan<T, STEP, true, TOP>(p, a.k, v, best);
+            scan<T, STEP, true, TOP != 0>(p, a.k, v, best[0]);
         }
-        if (TOP)
-            find_top(p, p.first == first, first, last, best, a.top, sm);
+        if (TOP == 2)
+            a.ws[row * (2 + a.cluster * blockDim.x) + 2 + rank * blockDim.x + tid] = best[0];
+        if constexpr (TOP == 1) {
+            if (p.first == first)
+                find_top(r, first, last, 1, share, best, a.top, sm, [&](int u) { return lds16(p.at(u)); });
+            else
+                find_top(r, first, last, 1, share, best, a.top, sm, [&](int u) { return load_run(z, a.n, r.column(u)); });
+        }
         join_block<true>(v, a.k.k2, part, blockDim.x >> 5);
         if (a.cluster > 1)
             join_cluster<true>(v, a.k.k2, &mine, a.cluster);
-        if (rank == 0 && (TOP || tid < 32)) {
+        if (rank == 0 && (TOP == 1 || tid < 32)) {
             const bool empty = v.l == 0.0f;
             const float log_l = logf(v.l), inv = empty ? 0.0f : __fdiv_rn(1.0f, v.l), U = empty ? 0.0f : -kLn2 * v.s * inv;
             if (tid == 0) {
@@ -243,8 +274,12 @@ logprobs_fwd(const Args a)
                 a.entropy[row] = empty ? 0.0f : log_l + U;
                 if (a.stats)
                     a.stats[3 * row] = empty ? 0.0f : v.ref, a.stats[3 * row + 1] = inv, a.stats[3 * row + 2] = U;
+                if (TOP == 2) {
+                    float* ws = a.ws + row * (2 + a.cluster * blockDim.x);
+                    ws[0] = v.ref, ws[1] = log_l;
+                }
             }
-            if (TOP) {
+            if (TOP == 1) {
                 const Key* list = sm.sel;
                 if (a.cluster > 1) {  // the blocks' lists
                     const int n = a.top * a.cluster;
@@ -266,17 +301,42 @@ logprobs_fwd(const Args a)
                     __syncthreads();
                     list = sm.keys;
                 }
-                for (int j = tid; j < a.top; j += blockDim.x) {
-                    const Key k = list[j];
-                    a.top_logprob[row * a.top + j] = k ? (value_of(k) - v.ref) * a.scale - log_l : -INFINITY;
-                    a.top_index[row * a.top + j] = k ? column_of(k) : -1;
-                }
+                put_top(a, row, list, v.ref, log_l);
             }
         }
         if (a.cluster > 1)
             cluster_sync();
         else
             __syncthreads();
+    }
+}
+
+// The alternatives of many rows, a block each, with the threads and slices of
+// logprobs_fwd.
+template <typename T>
+__global__ void __launch_bounds__(kThreadsMost)
+pick_top(const Args a)
+{
+    __shared__ TopSmem sm;
+    pdl_wait();
+    const int tid = threadIdx.x, T_ = blockDim.x;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        if (vocab::column_of(a.tokens, a.wide, row, a.n) < 0) {
+            for (int j = tid; j < a.top; j += T_)
+                a.top_logprob[row * a.top + j] = -INFINITY, a.top_index[row * a.top + j] = -1;
+            continue;
+        }
+        const T* z = static_cast<const T*>(a.logits) + row * a.ld;
+        const float* ws = a.ws + row * (2 + a.cluster * T_);
+        const Runs<T> r(z, a.n);
+        float m[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            m[s] = s < a.cluster ? ws[2 + s * T_ + tid] : -INFINITY;
+        find_top(r, 0, r.count, a.cluster, (r.count + a.cluster - 1) / a.cluster, m, a.top, sm,
+                 [&](int u) { return load_run(z, a.n, r.column(u)); });
+        put_top(a, row, sm.sel, ws[0], ws[1]);
+        __syncthreads();
     }
 }
 
@@ -330,16 +390,56 @@ logprobs_bwd(const BwdArgs a)
     }
 }
 
-template <typename T, bool TOP>
-int launch_fwd(Args a, cudaStream_t s)
+template <typename T, int TOP>
+int launch_scan(const Args& a, const Split& sp, cudaStream_t s)
+{
+    const cudaError_t e = launch_rows(known_step(sp) ? logprobs_fwd<T, TOP, kThreadsMost> : logprobs_fwd<T, TOP, 0>, a, sp,
+                                      sp.threads, sp.smem() + (TOP == 1 ? sizeof(TopSmem) : 0), s);
+    return e == cudaSuccess ? launch_status() : cuda_failure(e);
+}
+
+template <typename T>
+int launch_pick(const Args& a, const Split& sp, cudaStream_t s)
+{
+    const int64_t room = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(pick_top<T>), sp.threads, 0);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.rows < room ? a.rows : room));
+    cfg.blockDim = dim3((unsigned)sp.threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, pick_top<T>, a);
+    if (e != cudaSuccess)
+        cudaGetLastError();
+    return e == cudaSuccess ? launch_status() : cuda_failure(e);
+}
+
+template <typename T>
+int launch_fwd(Args a, void* workspace, size_t* bytes, cudaStream_t s)
 {
     const Split sp = split(a.rows, a.n, sizeof(T));
     a.cluster = sp.cluster, a.runs = sp.runs;
     a.eager = a.rows * a.cluster <= sm_count();  // few rows: time counts, not bytes
-    const size_t smem = sp.smem() + (TOP ? sizeof(TopSmem) : 0);
-    const cudaError_t e = launch_rows(known_step(sp) ? logprobs_fwd<T, TOP, kThreadsMost> : logprobs_fwd<T, TOP, 0>, a, sp,
-                                      sp.threads, smem, s);
-    return e == cudaSuccess ? launch_status() : cuda_failure(e);
+    const size_t need = a.top && !a.eager ? (size_t)a.rows * (2 + sp.cluster * sp.threads) * sizeof(float) : 0;
+    if (bytes && !workspace) {
+        *bytes = need;
+        return MFX_OK;
+    }
+    if (!a.top)
+        return launch_scan<T, 0>(a, sp, s);
+    if (!need)
+        return launch_scan<T, 1>(a, sp, s);
+    if (!workspace || !bytes)
+        return MFX_ERR_NULL;
+    if (*bytes < need || !aligned16(workspace))
+        return MFX_ERR_WORKSPACE;
+    a.ws = static_cast<float*>(workspace);
+    if (const int st = launch_scan<T, 2>(a, sp, s); st != MFX_OK)
+        return st;
+    return launch_pick<T>(a, sp, s);
 }
 
 template <typename T>
@@ -373,7 +473,8 @@ extern "C" {
 
 int mfx_token_logprobs_fwd(int dt, int64_t rows, int64_t vocab, int64_t ld, const void* logits, int index_bits,
                            const void* tokens, float scale, int64_t top, float* logprob, float* entropy,
-                           float* top_logprob, int32_t* top_index, float* stats, void* stream)
+                           float* top_logprob, int32_t* top_index, float* stats, void* workspace, size_t* workspace_bytes,
+                           void* stream)
 {
     using namespace mfx;
     namespace V = vocab;
@@ -381,14 +482,19 @@ int mfx_token_logprobs_fwd(int dt, int64_t rows, int64_t vocab, int64_t ld, cons
         return st;
     if (top < 0 || top > V::kMostTop)
         return MFX_ERR_VALUE;
-    if (rows == 0)
+    const bool query = workspace_bytes && !workspace;
+    if (rows == 0) {
+        if (query)
+            *workspace_bytes = 0;
         return MFX_OK;
-    if ((!logits && vocab) || !tokens || !logprob || !entropy || (top && (!top_logprob || !top_index)))
+    }
+    if (!query && ((!logits && vocab) || !tokens || !logprob || !entropy || (top && (!top_logprob || !top_index))))
         return MFX_ERR_NULL;
     struct Buf { const void* p; int64_t n; };
     const Buf in[2] = {{logits, V::span(rows, vocab, ld, dtype_bytes(dt))}, {tokens, rows * index_bits / 8}};
-    const Buf out[5] = {{logprob, rows * 4}, {entropy, rows * 4}, {stats, rows * 12}, {top_logprob, rows * top * 4}, {top_index, rows * top * 4}};
-    for (int i = 0; i < 5; ++i) {
+    const Buf out[6] = {{logprob, rows * 4}, {entropy, rows * 4}, {stats, rows * 12}, {top_logprob, rows * top * 4},
+                        {top_index, rows * top * 4}, {workspace, workspace_bytes ? (int64_t)*workspace_bytes : 0}};
+    for (int i = 0; i < 6 && !query; ++i) {
         for (const Buf& b : in)
             if (overlaps(out[i].p, out[i].n, b.p, b.n))
                 return MFX_ERR_ALIAS;
@@ -401,9 +507,8 @@ int mfx_token_logprobs_fwd(int dt, int64_t rows, int64_t vocab, int64_t ld, cons
     a.wide = index_bits == 64, a.scale = scale, a.k = V::scaling_of(scale);
     a.logprob = logprob, a.entropy = entropy, a.top_logprob = top_logprob, a.top_index = top_index, a.stats = stats;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dt == MFX_BF16)
-        return top ? V::launch_fwd<bf16, true>(a, s) : V::launch_fwd<bf16, false>(a, s);
-    return top ? V::launch_fwd<float, true>(a, s) : V::launch_fwd<float, false>(a, s);
+    return dt == MFX_BF16 ? V::launch_fwd<bf16>(a, workspace, workspace_bytes, s)
+                          : V::launch_fwd<float>(a, workspace, workspace_bytes, s);
 }
 
 int mfx_token_logprobs_bwd(int dt, int64_t rows, int64_t vocab, int64_t ld, const float* g_logprob,

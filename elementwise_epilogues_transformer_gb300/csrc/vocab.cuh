@@ -79,10 +79,17 @@ template <> struct Run<bf16> {
     {
         return make_uint4(raise2(w.x, f), raise2(w.y, f), raise2(w.z, f), raise2(w.w, f));
     }
-    static __device__ __forceinline__ float top(const uint4& w)
+    template <int U> static __device__ __forceinline__ float top_of(const uint4 (&w)[U])
     {
-        const float2 m = widen2(max2(max2(w.x, w.y), max2(w.z, w.w)));
-        return fmaxf(m.x, m.y);
+        uint32_t m[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            m[i] = max2(max2(w[i].x, w[i].y), max2(w[i].z, w[i].w));
+#pragma unroll
+        for (int i = 1; i < U; ++i)
+            m[0] = max2(m[0], m[i]);
+        const float2 f = widen2(m[0]);
+        return fmaxf(f.x, f.y);
     }
     static __device__ __forceinline__ uint4 narrow(const float2 (&f)[4])
     {
@@ -98,9 +105,14 @@ template <> struct Run<float> {
         f[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
         f[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
     }
-    static __device__ __forceinline__ float top(const uint4& w)
+    template <int U> static __device__ __forceinline__ float top_of(const uint4 (&w)[U])
     {
-        return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(w[i].x), __uint_as_float(w[i].y)),
+                               fmaxf(__uint_as_float(w[i].z), __uint_as_float(w[i].w))));
+        return m;
     }
     static __device__ __forceinline__ uint4 narrow(const float2 (&f)[2])
     {
@@ -368,12 +380,6 @@ template <typename T, int STEP> struct Piece {
     }
 };
 
-// A thread's best run: its maximum, and which.
-struct BestRun {
-    float m;
-    int u;
-};
-
 // What a launch's scale says of exponents: scale * log2 e, and up to where a
 // row's maximum leaves room for a floor (bf16 pairs of it) that is far enough
 // below it to have no power and near enough for a finite exponent.
@@ -424,24 +430,13 @@ __device__ __forceinline__ void add_runs(Stats& v, const uint4 (&w)[U], float k2
         v.s += s.x + s.y;
 }
 
-// Takes U runs of a thread (from u on, every `step`) into its statistics.
+// Takes U runs of a thread into its statistics, and (BEST) into its maximum.
 template <typename T, bool ENTROPY, bool BEST, int U>
-__device__ __forceinline__ void take(Stats& v, BestRun& best, uint4 (&w)[U], int u, int step, const Scaling& k)
+__device__ __forceinline__ void take(Stats& v, float& best, uint4 (&w)[U], const Scaling& k)
 {
-    float m[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-        m[i] = Run<T>::top(w[i]);
-    float top = m[0];
-#pragma unroll
-    for (int i = 1; i < U; ++i)
-        top = fmaxf(top, m[i]);
-    if (BEST) {
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (m[i] > best.m)
-                best.m = m[i], best.u = u + i * step;
-    }
+    const float top = Run<T>::template top_of<U>(w);
+    if (BEST)
+        best = fmaxf(best, top);
     if (top > v.ref)
         rebase(v, top, k.k2);
     if constexpr (!ENTROPY) {
@@ -460,7 +455,7 @@ __device__ __forceinline__ void take(Stats& v, BestRun& best, uint4 (&w)[U], int
 
 // This thread's runs of a piece whose copies are under way.
 template <typename T, int STEP, bool ENTROPY, bool BEST>
-__device__ __forceinline__ void scan(const Piece<T, STEP>& p, const Scaling& k, Stats& v, BestRun& best)
+__device__ __forceinline__ void scan(const Piece<T, STEP>& p, const Scaling& k, Stats& v, float& best)
 {
     constexpr int U = 4;
     const int n = p.each(), step = p.step();
@@ -483,14 +478,14 @@ __device__ __forceinline__ void scan(const Piece<T, STEP>& p, const Scaling& k, 
 #pragma unroll
             for (int j = 0; j < U; ++j)
                 w[j] = lds16(from + 16u * (uint32_t)(j * step));
-            take<T, ENTROPY, BEST, U>(v, best, w, u, step, k);
+            take<T, ENTROPY, BEST, U>(v, best, w, k);
         }
 #pragma unroll 1
         for (; i < n; ++i, u += step, from += 16u * (uint32_t)step)
             if (u < p.last) {
                 uint4 w[1];
                 w[0] = lds16(from);
-                take<T, ENTROPY, BEST, 1>(v, best, w, u, step, k);
+                take<T, ENTROPY, BEST, 1>(v, best, w, k);
             }
     }
 }

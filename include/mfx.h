@@ -413,12 +413,15 @@ int mfx_add_rmsnorm_bwd(int x_dt, int res_dt, int w_dt, int64_t rows, int64_t co
  * lower column; (-inf, -1) where fewer than `top` are above -inf; columns with
  * NaN are never among them.  stats: [rows, 3] fp32, what the backward needs,
  * or NULL.  A row that is all -inf: logprob -inf, entropy 0.
- * Outputs must not overlap anything -> MFX_ERR_ALIAS. */
+ * Workspace protocol as for the fused bias gradients; the size may be 0 (no
+ * alternatives, or few rows): then NULL sizes and workspaces run, and two
+ * kernels otherwise.  Outputs must not overlap anything -> MFX_ERR_ALIAS. */
 int mfx_token_logprobs_fwd(int dt, int64_t rows, int64_t vocab, int64_t ld,
                            const void* logits, int index_bits, const void* tokens,
                            float scale, int64_t top,
                            float* logprob, float* entropy,
-                           float* top_logprob, int32_t* top_index, float* stats, void* stream);
+                           float* top_logprob, int32_t* top_index, float* stats,
+                           void* workspace, size_t* workspace_bytes, void* stream);
 
 /* dlogits[r, k] = scale * (g (1[token = k] - p) - ge p (log p + entropy)) in
  * dtype dt, rows ld_out apart, from the gradients g of logprob and ge of
