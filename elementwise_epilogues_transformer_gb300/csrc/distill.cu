@@ -35,6 +35,7 @@ struct Args {
     float *loss, *stats;
     const float* stats_in;
     void* out;
+    StreamArgs in;
 };
 
 // A row's list in shared memory: columns (-1: no entry), q, and the teacher's
@@ -301,6 +302,43 @@ distill_fwd(const Args a)
     }
 }
 
+// The loss of many rows, one after another.
+template <typename T, int STEP>
+__global__ void __launch_bounds__(kThreadsMost + 32, MFX_VOCAB_BLOCKS)
+distill_rows(const Args a)
+{
+    extern __shared__ __align__(16) char dynamic[];
+    __shared__ Stats part[2][8];
+    const int threads = blockDim.x - 32, tid = threadIdx.x;
+    if (tid >= threads) {  // the warp that sees to the lists
+        const List l(dynamic + Stream<T, STEP>::smem(threads), a.K);
+        int slot = 0;
+        for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, slot ^= 1) {
+            const T* z = static_cast<const T*>(a.logits) + row * a.ld;
+            const Teacher w = read_list<false>(a, row, l, 0, a.n, {});
+            Stats v = no_stats();
+            join_block<false>(v, a.k2, part[slot], threads >> 5);
+            const float loss = loss_of(a, l, w.n, v, [&](int c) { return load1(z + c); });
+            if (tid == threads) {
+                a.loss[row] = loss;
+                if (a.stats) {
+                    const float ratio = v.l == 0.0f ? 0.0f : __fdiv_rn(w.Q, v.l);
+                    a.stats[4 * row] = v.ref, a.stats[4 * row + 1] = ratio, a.stats[4 * row + 2] = w.ref, a.stats[4 * row + 3] = w.coef;
+                }
+            }
+            __syncwarp();
+        }
+        return;
+    }
+    Stream<T, STEP> in(a.in, dynamic);
+    int slot = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, slot ^= 1) {
+        Stats v = no_stats();
+        in.template take_row<false, false>(row, a.k, v, [](int, bool, float&) {});
+        join_block<false>(v, a.k2, part[slot], threads >> 5);
+    }
+}
+
 template <typename T, int STEP>
 __global__ void __launch_bounds__(kThreadsMost + 32)
 distill_bwd(const Args a)
@@ -344,6 +382,16 @@ distill_bwd(const Args a)
 template <typename T, bool GRAD>
 int launch_fwd(Args a, cudaStream_t s)
 {
+    if (!GRAD && streamed(a.rows)) {
+        const int64_t runs = (a.n * (int64_t)sizeof(T) + 15) / 16 + 1;  // with a head and a tail
+        a.in = {a.rows, a.ld, a.n, threads_for(runs, kThreadsMost), a.logits, nullptr, false};
+        const int threads = a.in.step + 32;
+        const auto kernel = a.in.step == kThreadsMost ? distill_rows<T, kThreadsMost> : distill_rows<T, 0>;
+        const size_t smem = Stream<T, 0>::smem(a.in.step) + (size_t)a.K * 12;
+        const int64_t room = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(kernel), threads, smem);
+        kernel<<<(unsigned)(a.rows < room ? a.rows : room), threads, smem, s>>>(a);
+        return launch_status();
+    }
     const Split sp = split(a.rows, a.n, sizeof(T));
     a.cluster = sp.cluster, a.runs = sp.runs;
     const cudaError_t e = launch_rows(known_step(sp) ? distill_fwd<T, GRAD, kThreadsMost> : distill_fwd<T, GRAD, 0>, a, sp,

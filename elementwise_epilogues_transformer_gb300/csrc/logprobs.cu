@@ -19,7 +19,9 @@ namespace {
 
 constexpr int kMostTop = 64;   // alternatives
 constexpr int kMostKeys = 128;  // groups of threads that bound the search for them
-constexpr int kMostListed = 8 * kThreadsMost;  // threads of all slices
+constexpr int kMostChunks = 8;  // parts of a thread's runs
+constexpr int kPickThreads = 128;
+constexpr int kMostListed = kMostChunks * kThreadsMost;
 constexpr int kRound = 64;      // runs of a round that cannot overflow the candidates
 constexpr int kKept = 256;      // candidates that a round may find there
 constexpr int kCandidates = kRound * 8 + kKept;
@@ -33,7 +35,10 @@ struct Args {
     Scaling k;
     float *logprob, *entropy, *top_logprob, *stats;
     int32_t* top_index;
-    float* ws;  // of each row: its reference, log l, every thread's largest logit
+    // rows one after another
+    StreamArgs in;
+    int gran, chunks;  // groups of a thread's runs that share a maximum, maxima of a thread
+    float* ws;  // of each row: its reference, log l, every thread's largest logits
 };
 
 // A column and its logit as one number: larger for larger logits (-0 and 0
@@ -91,20 +96,20 @@ __device__ __forceinline__ void sort_out(const Key* cand, int n, int top, Key* s
     }
 }
 
-// The `top` largest columns above -inf of runs [begin, end) of a row, in
-// `slices` slices of `share` runs, to sm.sel in order.  m: the largest logit of this thread's runs of each
-// slice; run_at(u): run u of the row.
+// The `top` largest columns above -inf of a row's parts, to sm.sel in order.
+// m: the largest logit of part s blockDim + thread for each s below `parts`;
+// run_of(part, i): its i-th run of `each`, -1 for none; run_at(u): run u.
 //
 // The top-th largest of 64 groups of threads (128 for more than 24) bounds the
-// top-th largest logit from below, and only threads whose largest logit
-// reaches it can hold a column that does: of all elements about as many as are
-// asked for.  Their runs are read again for the columns that reach the bound.
+// top-th largest logit from below, and only parts whose largest logit reaches
+// it can hold a column that does: of all elements about as many as are asked
+// for.  Their runs are read again for the columns that reach the bound.
 // Should those be more than there is room for (many equal logits, or few
-// threads with most of the large ones), the runs are taken in small rounds and
+// parts with most of the large ones), the runs are taken in small rounds and
 // the candidates cut to the best, which raises the bound.
-template <typename T, int S, typename F>
-__device__ __forceinline__ void find_top(const Runs<T>& r, int begin, int end, int slices, int share, const float (&m)[S],
-                                         int top, TopSmem& sm, F run_at)
+template <typename T, int S, typename R, typename F>
+__device__ __forceinline__ void find_top(const Runs<T>& r, int parts, int each, const float (&m)[S], int top, TopSmem& sm,
+                                         R run_of, F run_at)
 {
     constexpr int V = Run<T>::V;
     const int tid = threadIdx.x, T_ = blockDim.x, lane = tid & 31, warp = tid >> 5;
@@ -138,18 +143,16 @@ __device__ __forceinline__ void find_top(const Runs<T>& r, int begin, int end, i
     float least = bound ? value_of(bound) : -INFINITY;
 #pragma unroll
     for (int s = 0; s < S; ++s)
-        if (s < slices && m[s] > -INFINITY && m[s] >= least)
-            sm.list[atomicAdd(&sm.listed, 1)] = (uint16_t)(s * kThreadsMost + tid);
+        if (s < parts && m[s] > -INFINITY && m[s] >= least)
+            sm.list[atomicAdd(&sm.listed, 1)] = (uint16_t)(s * T_ + tid);
     __syncthreads();
-    // a warp goes over a listed thread's runs, a lane each
-    const int each = (share + T_ - 1) / T_, listed = sm.listed, all = T_ >> 5;
+    // a warp goes over a listed part's runs, a lane each
+    const int listed = sm.listed, all = T_ >> 5;
     for (int warps = all, l0 = 0, i0 = 0; l0 < listed;) {
         const int before = sm.count;
         __syncthreads();
         if (warp < warps && l0 + warp < listed && i0 + lane < each) {
-            const int who = sm.list[l0 + warp], first = begin + who / kThreadsMost * share;
-            const int u = first + who % kThreadsMost + (i0 + lane) * T_;
-            if (u < min(first + share, end)) {
+            if (const int u = run_of((int)sm.list[l0 + warp], i0 + lane); u >= 0) {
                 const uint4 w[1] = {run_at(u)};
                 const int c = r.column(u);
                 if (key_of(Run<T>::template top_of<1>(w), max(c, 0)) >= bound) {
@@ -206,11 +209,9 @@ __device__ __forceinline__ void put_top(const Args& a, int64_t row, const Key* l
     }
 }
 
-// TOP: without alternatives (0); their search within the kernel (1: few rows,
-// where a second launch would cost more), or by pick_top, for which every
-// thread leaves its largest logit in the workspace (2: the search's barriers
-// would stand in the way of the next rows' copies).
-template <typename T, int TOP, int STEP>
+// Few rows: slices of each in the blocks of a cluster, and the alternatives
+// found within the kernel.
+template <typename T, bool TOP, int STEP>
 __global__ void __launch_bounds__(kThreadsMost, MFX_VOCAB_BLOCKS)
 logprobs_fwd(const Args a)
 {
@@ -236,7 +237,7 @@ logprobs_fwd(const Args a)
                     if (a.stats)
                         a.stats[3 * row] = 0.0f, a.stats[3 * row + 1] = 0.0f, a.stats[3 * row + 2] = 0.0f;
                 }
-                if (TOP == 1)
+                if (TOP)
                     for (int j = tid; j < a.top; j += blockDim.x)
                         a.top_logprob[row * a.top + j] = -INFINITY, a.top_index[row * a.top + j] = -1;
             }
@@ -249,24 +250,24 @@ logprobs_fwd(const Args a)
         float best[1] = {-INFINITY};
         if (tid == 0 && row + a.ahead < a.rows)
             p.prefetch(a.ahead * a.ld);
-        scan<T, STEP, true, TOP != 0>(p, a.k, v, best[0]);
+        scan<T, STEP, true, TOP>(p, a.k, v, best[0]);
         while (p.last < last) {  // (threads read only what they copied)
             p.set(p.last, min(p.last + a.runs, last));
             p.fill();
-            scan<T, STEP, true, TOP != 0>(p, a.k, v, best[0]);
+            scan<T, STEP, true, TOP>(p, a.k, v, best[0]);
         }
-        if (TOP == 2)
-            a.ws[row * (2 + a.cluster * blockDim.x) + 2 + rank * blockDim.x + tid] = best[0];
-        if constexpr (TOP == 1) {
+        if constexpr (TOP) {
+            const int T_ = blockDim.x, each = (last - first + T_ - 1) / T_;
+            const auto run_of = [&](int part, int i) { return first + part + i * T_ < last ? first + part + i * T_ : -1; };
             if (p.first == first)
-                find_top(r, first, last, 1, share, best, a.top, sm, [&](int u) { return lds16(p.at(u)); });
+                find_top(r, 1, each, best, a.top, sm, run_of, [&](int u) { return lds16(p.at(u)); });
             else
-                find_top(r, first, last, 1, share, best, a.top, sm, [&](int u) { return load_run(z, a.n, r.column(u)); });
+                find_top(r, 1, each, best, a.top, sm, run_of, [&](int u) { return load_run(z, a.n, r.column(u)); });
         }
         join_block<true>(v, a.k.k2, part, blockDim.x >> 5);
         if (a.cluster > 1)
             join_cluster<true>(v, a.k.k2, &mine, a.cluster);
-        if (rank == 0 && (TOP == 1 || tid < 32)) {
+        if (rank == 0 && (TOP || tid < 32)) {
             const bool empty = v.l == 0.0f;
             const float log_l = logf(v.l), inv = empty ? 0.0f : __fdiv_rn(1.0f, v.l), U = empty ? 0.0f : -kLn2 * v.s * inv;
             if (tid == 0) {
@@ -274,12 +275,8 @@ logprobs_fwd(const Args a)
                 a.entropy[row] = empty ? 0.0f : log_l + U;
                 if (a.stats)
                     a.stats[3 * row] = empty ? 0.0f : v.ref, a.stats[3 * row + 1] = inv, a.stats[3 * row + 2] = U;
-                if (TOP == 2) {
-                    float* ws = a.ws + row * (2 + a.cluster * blockDim.x);
-                    ws[0] = v.ref, ws[1] = log_l;
-                }
             }
-            if (TOP == 1) {
+            if (TOP) {
                 const Key* list = sm.sel;
                 if (a.cluster > 1) {  // the blocks' lists
                     const int n = a.top * a.cluster;
@@ -311,30 +308,94 @@ logprobs_fwd(const Args a)
     }
 }
 
-// The alternatives of many rows, a block each, with the threads and slices of
-// logprobs_fwd.
+// Many rows.  TOP: every thread leaves the largest logits of its runs, `gran`
+// groups at a time, in the workspace for pick_top (a search within the kernel
+// has barriers that stand in the way of the next rows).
+template <typename T, bool TOP, int STEP>
+__global__ void __launch_bounds__(kThreadsMost, MFX_VOCAB_BLOCKS)
+logprobs_rows(const Args a)
+{
+    extern __shared__ __align__(16) char dynamic[];
+    __shared__ Stats part[2][8];
+    const int tid = threadIdx.x, T_ = blockDim.x;
+    Stream<T, STEP> in(a.in, dynamic);
+    int slot = 0, token = vocab::column_of(a.tokens, a.wide, blockIdx.x, a.n), next = -1;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, token = next) {
+        if (row + gridDim.x < a.rows)
+            next = vocab::column_of(a.tokens, a.wide, row + gridDim.x, a.n);
+        if (token < 0) {  // left out
+            if (tid == 0) {
+                a.logprob[row] = 0.0f, a.entropy[row] = 0.0f;
+                if (a.stats)
+                    a.stats[3 * row] = 0.0f, a.stats[3 * row + 1] = 0.0f, a.stats[3 * row + 2] = 0.0f;
+            }
+            continue;
+        }
+        const float zt = load1(static_cast<const T*>(a.logits) + row * a.ld + token);
+        Stats v = no_stats();
+        float* ws = TOP ? a.ws + row * (2 + a.chunks * T_) : nullptr;
+        int chunk = 0, until = a.gran;
+        in.template take_row<true, TOP>(row, a.k, v, [&](int g, bool last, float& best) {
+            if (TOP && (last || g + 1 == until)) {
+                ws[2 + chunk * T_ + tid] = best;
+                best = -INFINITY, until += a.gran, ++chunk;
+            }
+        });
+        if (TOP)
+            for (; chunk < a.chunks; ++chunk)
+                ws[2 + chunk * T_ + tid] = -INFINITY;
+        join_block<true>(v, a.k.k2, part[slot], T_ >> 5);
+        slot ^= 1;
+        if (tid < 32) {
+            const bool empty = v.l == 0.0f;
+            const float log_l = logf(v.l), inv = empty ? 0.0f : __fdiv_rn(1.0f, v.l), U = empty ? 0.0f : -kLn2 * v.s * inv;
+            if (tid == 0) {
+                a.logprob[row] = empty ? -INFINITY : (zt - v.ref) * a.scale - log_l;
+                a.entropy[row] = empty ? 0.0f : log_l + U;
+                if (a.stats)
+                    a.stats[3 * row] = empty ? 0.0f : v.ref, a.stats[3 * row + 1] = inv, a.stats[3 * row + 2] = U;
+                if (TOP)
+                    ws[0] = v.ref, ws[1] = log_l;
+            }
+        }
+    }
+}
+
+// Their alternatives, a block a row.
 template <typename T>
-__global__ void __launch_bounds__(kThreadsMost)
+__global__ void __launch_bounds__(kPickThreads)
 pick_top(const Args a)
 {
+    constexpr int S = kMostChunks * kThreadsMost / kPickThreads;
     __shared__ TopSmem sm;
     pdl_wait();
-    const int tid = threadIdx.x, T_ = blockDim.x;
+    const int tid = threadIdx.x, P = blockDim.x, T_ = a.in.step;  // parts: chunk T_ + thread
+    const int parts = (a.chunks * T_ + P - 1) / P;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         if (vocab::column_of(a.tokens, a.wide, row, a.n) < 0) {
-            for (int j = tid; j < a.top; j += T_)
+            for (int j = tid; j < a.top; j += P)
                 a.top_logprob[row * a.top + j] = -INFINITY, a.top_index[row * a.top + j] = -1;
             continue;
         }
         const T* z = static_cast<const T*>(a.logits) + row * a.ld;
-        const float* ws = a.ws + row * (2 + a.cluster * T_);
-        const Runs<T> r(z, a.n);
-        float m[8];
+        const float* ws = a.ws + row * (2 + a.chunks * T_);
+        const RowRuns<T> q(z, a.n, T_);
+        float m[S];
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-            m[s] = s < a.cluster ? ws[2 + s * T_ + tid] : -INFINITY;
-        find_top(r, 0, r.count, a.cluster, (r.count + a.cluster - 1) / a.cluster, m, a.top, sm,
-                 [&](int u) { return load_run(z, a.n, r.column(u)); });
+        for (int s = 0; s < S; ++s)
+            m[s] = s * P + tid < a.chunks * T_ ? ws[2 + s * P + tid] : -INFINITY;
+        const int each = 4 * a.gran, ends = (q.groups - 1) / a.gran;  // the chunk that has the row's borders
+        const auto run_of = [&](int id, int i) {
+            const int chunk = id / T_, t = id % T_;
+            if (i >= each) {
+                if (chunk == ends && i == each && t == 0 && q.head())
+                    return 0;
+                return chunk == ends && i == each + 1 && t == T_ - 1 && q.tail() ? q.r.count - 1 : -1;
+            }
+            const int u = q.whole0 + t + (chunk * each + i) * T_;
+            return u < q.whole1 ? u : -1;
+        };
+        find_top(q.r, parts, each + 2, m, a.top, sm, run_of, [&](int u) { return load_run(z, a.n, q.r.column(u)); });
         put_top(a, row, sm.sel, ws[0], ws[1]);
         __syncthreads();
     }
@@ -390,56 +451,70 @@ logprobs_bwd(const BwdArgs a)
     }
 }
 
-template <typename T, int TOP>
-int launch_scan(const Args& a, const Split& sp, cudaStream_t s)
+int status_of(cudaError_t e)
 {
-    const cudaError_t e = launch_rows(known_step(sp) ? logprobs_fwd<T, TOP, kThreadsMost> : logprobs_fwd<T, TOP, 0>, a, sp,
-                                      sp.threads, sp.smem() + (TOP == 1 ? sizeof(TopSmem) : 0), s);
+    if (e != cudaSuccess)
+        cudaGetLastError();  // it is this call's, not the next one's
     return e == cudaSuccess ? launch_status() : cuda_failure(e);
 }
 
-template <typename T>
-int launch_pick(const Args& a, const Split& sp, cudaStream_t s)
+template <typename T, bool TOP>
+int launch_few(Args a, cudaStream_t s)
 {
-    const int64_t room = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(pick_top<T>), sp.threads, 0);
+    const Split sp = split(a.rows, a.n, sizeof(T));
+    a.cluster = sp.cluster, a.runs = sp.runs;
+    a.eager = a.rows * a.cluster <= sm_count();  // time counts, not bytes
+    return status_of(launch_rows(known_step(sp) ? logprobs_fwd<T, TOP, kThreadsMost> : logprobs_fwd<T, TOP, 0>, a, sp,
+                                 sp.threads, sp.smem() + (TOP ? sizeof(TopSmem) : 0), s));
+}
+
+template <typename T, bool TOP>
+int launch_many(const Args& a, cudaStream_t s)
+{
+    const auto kernel = a.in.step == kThreadsMost ? logprobs_rows<T, TOP, kThreadsMost> : logprobs_rows<T, TOP, 0>;
+    const size_t smem = Stream<T, 0>::smem(a.in.step);
+    const int64_t room = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(kernel), a.in.step, smem);
+    kernel<<<(unsigned)(a.rows < room ? a.rows : room), a.in.step, smem, s>>>(a);
+    const int st = launch_status();
+    if (!TOP || st != MFX_OK)
+        return st;
+    const int64_t places = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(pick_top<T>), kPickThreads, 0);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.rows < room ? a.rows : room));
-    cfg.blockDim = dim3((unsigned)sp.threads);
+    cfg.gridDim = dim3((unsigned)(a.rows < places ? a.rows : places));
+    cfg.blockDim = dim3(kPickThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, pick_top<T>, a);
-    if (e != cudaSuccess)
-        cudaGetLastError();
-    return e == cudaSuccess ? launch_status() : cuda_failure(e);
+    return status_of(cudaLaunchKernelEx(&cfg, pick_top<T>, a));
 }
 
 template <typename T>
 int launch_fwd(Args a, void* workspace, size_t* bytes, cudaStream_t s)
 {
-    const Split sp = split(a.rows, a.n, sizeof(T));
-    a.cluster = sp.cluster, a.runs = sp.runs;
-    a.eager = a.rows * a.cluster <= sm_count();  // few rows: time counts, not bytes
-    const size_t need = a.top && !a.eager ? (size_t)a.rows * (2 + sp.cluster * sp.threads) * sizeof(float) : 0;
+    const bool many = streamed(a.rows);
+    const int64_t runs = (a.n * (int64_t)sizeof(T) + 15) / 16 + 1;  // with a head and a tail
+    a.in = {a.rows, a.ld, a.n, threads_for(runs, kThreadsMost), a.logits, a.tokens, a.wide};
+    const int64_t groups = (runs + 4 * a.in.step - 1) / (4 * a.in.step);
+    a.gran = (int)(groups > 4 * kMostChunks ? (groups + kMostChunks - 1) / kMostChunks : 4);
+    a.chunks = (int)((groups + a.gran - 1) / a.gran);
+    const size_t need = a.top && many ? (size_t)a.rows * (2 + a.chunks * a.in.step) * sizeof(float) : 0;
     if (bytes && !workspace) {
         *bytes = need;
         return MFX_OK;
     }
+    if (!many)
+        return a.top ? launch_few<T, true>(a, s) : launch_few<T, false>(a, s);
     if (!a.top)
-        return launch_scan<T, 0>(a, sp, s);
-    if (!need)
-        return launch_scan<T, 1>(a, sp, s);
+        return launch_many<T, false>(a, s);
     if (!workspace || !bytes)
         return MFX_ERR_NULL;
     if (*bytes < need || !aligned16(workspace))
         return MFX_ERR_WORKSPACE;
     a.ws = static_cast<float*>(workspace);
-    if (const int st = launch_scan<T, 2>(a, sp, s); st != MFX_OK)
-        return st;
-    return launch_pick<T>(a, sp, s);
+    return launch_many<T, true>(a, s);
 }
 
 template <typename T>

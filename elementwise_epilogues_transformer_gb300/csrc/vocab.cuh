@@ -490,6 +490,173 @@ __device__ __forceinline__ void scan(const Piece<T, STEP>& p, const Scaling& k, 
     }
 }
 
+// --- rows one after another -------------------------------------------------
+// Many rows that are read once: a block works on one after another, and each
+// thread keeps four groups of four runs on their way to shared memory of its
+// own, over the rows' borders, so that HBM works while a row's sums are joined.
+// A row's whole runs [whole0, whole1) are dealt to the threads in turn; the
+// vector at its head goes to the first thread and the one at its tail to the
+// last, with the row's last group.
+template <typename T> struct RowRuns {
+    Runs<T> r;
+    int whole0, whole1, groups;
+    __device__ __forceinline__ RowRuns(const T* p, int n, int step) : r(p, n)
+    {
+        whole0 = r.count > 0 && !r.whole(0) ? 1 : 0;
+        whole1 = r.count > whole0 && !r.whole(r.count - 1) ? r.count - 1 : max(r.count, whole0);
+        groups = max((whole1 - whole0 + 4 * step - 1) / (4 * step), 1);
+    }
+    __device__ __forceinline__ bool head() const { return whole0 > 0; }
+    __device__ __forceinline__ bool tail() const { return whole1 < r.count; }
+};
+
+// A vector at a row's border with -inf for what is not the row's.
+template <typename T>
+__device__ __forceinline__ uint4 only_row(const uint4& w, int c, int n)
+{
+    uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < Run<T>::V; ++j)
+        if (c + j < 0 || c + j >= n) {
+            if constexpr (sizeof(T) == 2)
+                x[j >> 1] = j & 1 ? (x[j >> 1] & 0xFFFFu) | 0xFF800000u : (x[j >> 1] & 0xFFFF0000u) | 0xFF80u;
+            else
+                x[j] = 0xFF800000u;
+        }
+    return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+struct StreamArgs {
+    int64_t rows, ld;
+    int n, step;
+    const void *logits, *tokens;  // tokens (or NULL): rows whose token is no column are passed over
+    bool wide;
+};
+
+template <typename T, int STEP> struct Stream {
+    static constexpr int V = Run<T>::V, kSlots = 4;
+    const StreamArgs& a;
+    int64_t row;     // whose groups are asked for next
+    int left, group, groups, slot;
+    const T* from;
+    uint32_t buf;    // this thread's place in slot 0; the border vectors' slots lie behind all slots
+    bool head, tail; // of that row, this thread's
+    bool next_counts;
+
+    __device__ __forceinline__ int step() const { return STEP ? STEP : a.step; }
+    __host__ __device__ static size_t smem(int step) { return (size_t)(kSlots * 4 * step + kSlots * 2) * 16; }
+    __device__ __forceinline__ uint32_t border(int s, int which) const
+    {
+        return buf - 16u * threadIdx.x + 16u * (uint32_t)(kSlots * 4 * step() + 2 * s + which);
+    }
+    __device__ __forceinline__ bool counts(int64_t r) const
+    {
+        return !a.tokens || (r < a.rows && column_of(a.tokens, a.wide, r, a.n) >= 0);
+    }
+    // Goes to row `r`, or the next one that counts; `now`: whether it does.
+    __device__ __forceinline__ void begin(int64_t r, bool now)
+    {
+        while (r < a.rows && !now)
+            r += gridDim.x, now = counts(r);
+        row = r, group = 0;
+        if (row >= a.rows)
+            return;
+        next_counts = counts(row + gridDim.x);  // asked long before it is needed
+        const RowRuns<T> q(static_cast<const T*>(a.logits) + row * a.ld, a.n, step());
+        groups = q.groups, left = q.whole1 - q.whole0 - (int)threadIdx.x;
+        from = q.r.p + q.r.column(q.whole0 + threadIdx.x);
+        head = q.head() && threadIdx.x == 0, tail = q.tail() && (int)threadIdx.x == step() - 1;
+    }
+    __device__ __forceinline__ Stream(const StreamArgs& a_, char* smem) : a(a_), slot(0)
+    {
+        buf = smem_addr(smem) + 16u * threadIdx.x;
+        begin(blockIdx.x, counts(blockIdx.x));
+        for (int s = 0; s < kSlots; ++s)
+            ask();
+    }
+    // A vector at a border, or its elements where it reaches out of the logits.
+    __device__ __forceinline__ void ask_border(int which, int u) const
+    {
+        const Runs<T> r(static_cast<const T*>(a.logits) + row * a.ld, a.n);
+        const T* v = r.p + r.column(u);
+        const T *lo = static_cast<const T*>(a.logits), *hi = lo + (a.rows - 1) * a.ld + a.n;
+        if (v >= lo && v + V <= hi)
+            copy16(border(slot, which), v);
+        else
+            sts16(border(slot, which), edge_run(r.p, r.n, r.column(u)));
+    }
+    // Asks for the next group, into the slot that was read last.
+    __device__ __forceinline__ void ask()
+    {
+        if (row < a.rows) {
+            const uint32_t to = buf + 64u * (uint32_t)(slot * step());
+            if (left > 3 * step()) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    copy16(to + 16u * (uint32_t)(j * step()), from + j * step() * V);
+            } else {
+                for (int j = 0; j < 4; ++j)
+                    if (left > j * step())
+                        copy16(to + 16u * (uint32_t)(j * step()), from + j * step() * V);
+            }
+            left -= 4 * step(), from += 4 * step() * V;
+            if (++group == groups) {
+                if (head)
+                    ask_border(0, 0);
+                if (tail)
+                    ask_border(1, Runs<T>(static_cast<const T*>(a.logits) + row * a.ld, a.n).count - 1);
+                begin(row + gridDim.x, next_counts);
+            }
+        }
+        copies_commit();
+        slot = (slot + 1) & (kSlots - 1);
+    }
+    // Takes a row (the one that counts next) into `v`; `after(g, last,
+    // best)` is called after its g-th group with the maximum of this thread's
+    // elements since `best` was last set.
+    template <bool ENTROPY, bool BEST, typename F>
+    __device__ __forceinline__ void take_row(int64_t which, const Scaling& k, Stats& v, F after)
+    {
+        const RowRuns<T> q(static_cast<const T*>(a.logits) + which * a.ld, a.n, step());
+        int rest = q.whole1 - q.whole0 - (int)threadIdx.x;
+        float best = -INFINITY;
+#pragma unroll 1
+        for (int g = 0; g < q.groups; ++g, rest -= 4 * step()) {
+            copies_wait<kSlots - 1>();
+            const uint32_t at = buf + 64u * (uint32_t)(slot * step());
+            if (rest > 3 * step()) {
+                uint4 w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = lds16(at + 16u * (uint32_t)(j * step()));
+                take<T, ENTROPY, BEST, 4>(v, best, w, k);
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j)
+                    if (rest > j * step()) {
+                        uint4 w[1] = {lds16(at + 16u * (uint32_t)(j * step()))};
+                        take<T, ENTROPY, BEST, 1>(v, best, w, k);
+                    }
+            }
+            if (g == q.groups - 1) {
+                if (q.head() && threadIdx.x == 0) {
+                    uint4 w[1] = {only_row<T>(lds16(border(slot, 0)), q.r.column(0), a.n)};
+                    take<T, ENTROPY, BEST, 1>(v, best, w, k);
+                }
+                if (q.tail() && (int)threadIdx.x == step() - 1) {
+                    uint4 w[1] = {only_row<T>(lds16(border(slot, 1)), q.r.column(q.r.count - 1), a.n)};
+                    take<T, ENTROPY, BEST, 1>(v, best, w, k);
+                }
+            }
+            after(g, g == q.groups - 1, best);
+            ask();
+        }
+    }
+};
+
+// Rows that are read once, and enough of them, go one after another.
+inline bool streamed(int64_t rows) { return rows >= 2 * (int64_t)sm_count(); }
+
 // A block's runs [u0, u1) of an output row from a row of logits: `f` makes a
 // run of results of a run of logits and its first column.  Four runs of a
 // thread are in flight.  Rows that lie alike take whole vectors, others the
