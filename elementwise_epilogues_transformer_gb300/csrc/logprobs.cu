@@ -19,9 +19,9 @@ namespace {
 
 constexpr int kMostTop = 64;   // alternatives
 constexpr int kMostKeys = 128;  // groups of threads that bound the search for them
-constexpr int kMostChunks = 8;  // parts of a thread's runs
-constexpr int kPickThreads = 128;
+constexpr int kMostChunks = 8;  // maxima of a thread of logprobs_rows
 constexpr int kMostListed = kMostChunks * kThreadsMost;
+constexpr int kPickThreads = 128;
 constexpr int kRound = 64;      // runs of a round that cannot overflow the candidates
 constexpr int kKept = 256;      // candidates that a round may find there
 constexpr int kCandidates = kRound * 8 + kKept;
@@ -63,7 +63,7 @@ struct TopSmem {
     Key sel[kMostTop];  // the alternatives in order, 0 behind them
     Key limit;
     int listed, count;
-    uint16_t list[kMostListed];  // threads (of slices) that may hold some
+    int list[kThreadsMost];  // threads that may hold some
 };
 
 // The `top` largest of cand[0, n) in order to sel, 0 behind them.  Barriers
@@ -96,28 +96,23 @@ __device__ __forceinline__ void sort_out(const Key* cand, int n, int top, Key* s
     }
 }
 
-// The `top` largest columns above -inf of a row's parts, to sm.sel in order.
-// m: the largest logit of part s blockDim + thread for each s below `parts`;
-// run_of(part, i): its i-th run of `each`, -1 for none; run_at(u): run u.
+// The `top` largest columns above -inf of a block's runs [first, last), every
+// blockDim-th of them a thread's, to sm.sel in order.  best: the largest logit
+// of this thread's runs; run_at(u): run u.
 //
 // The top-th largest of 64 groups of threads (128 for more than 24) bounds the
-// top-th largest logit from below, and only parts whose largest logit reaches
-// it can hold a column that does: of all elements about as many as are asked
-// for.  Their runs are read again for the columns that reach the bound.
+// top-th largest logit from below, and only threads whose largest logit
+// reaches it can hold a column that does: of all elements about as many as are
+// asked for.  Their runs are read again for the columns that reach the bound.
 // Should those be more than there is room for (many equal logits, or few
-// parts with most of the large ones), the runs are taken in small rounds and
+// threads with most of the large ones), the runs are taken in small rounds and
 // the candidates cut to the best, which raises the bound.
-template <typename T, int S, typename R, typename F>
-__device__ __forceinline__ void find_top(const Runs<T>& r, int parts, int each, const float (&m)[S], int top, TopSmem& sm,
-                                         R run_of, F run_at)
+template <typename T, typename F>
+__device__ __forceinline__ void find_top(const Runs<T>& r, int first, int last, float best, int top, TopSmem& sm, F run_at)
 {
     constexpr int V = Run<T>::V;
     const int tid = threadIdx.x, T_ = blockDim.x, lane = tid & 31, warp = tid >> 5;
     const int want = top <= 24 ? 64 : kMostKeys, nkeys = T_ < want ? T_ : want, per = T_ / nkeys;
-    float best = m[0];
-#pragma unroll
-    for (int s = 1; s < S; ++s)
-        best = fmaxf(best, m[s]);
     // equal ones in some order: a thread's place, below all columns
     Key k = (best > -INFINITY ? key_of(best, 0) >> 32 << 32 : 0) | (Key)tid;
     for (int o = 1; o < per; o <<= 1) {
@@ -141,18 +136,16 @@ __device__ __forceinline__ void find_top(const Runs<T>& r, int parts, int each, 
     }
     Key bound = sm.limit;
     float least = bound ? value_of(bound) : -INFINITY;
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-        if (s < parts && m[s] > -INFINITY && m[s] >= least)
-            sm.list[atomicAdd(&sm.listed, 1)] = (uint16_t)(s * T_ + tid);
+    if (best > -INFINITY && best >= least)
+        sm.list[atomicAdd(&sm.listed, 1)] = tid;
     __syncthreads();
-    // a warp goes over a listed part's runs, a lane each
-    const int listed = sm.listed, all = T_ >> 5;
+    // a warp goes over a listed thread's runs, a lane each
+    const int each = (last - first + T_ - 1) / T_, listed = sm.listed, all = T_ >> 5;
     for (int warps = all, l0 = 0, i0 = 0; l0 < listed;) {
         const int before = sm.count;
         __syncthreads();
         if (warp < warps && l0 + warp < listed && i0 + lane < each) {
-            if (const int u = run_of((int)sm.list[l0 + warp], i0 + lane); u >= 0) {
+            if (const int u = first + sm.list[l0 + warp] + (i0 + lane) * T_; u < last) {
                 const uint4 w[1] = {run_at(u)};
                 const int c = r.column(u);
                 if (key_of(Run<T>::template top_of<1>(w), max(c, 0)) >= bound) {
@@ -247,22 +240,20 @@ logprobs_fwd(const Args a)
             p.fill();
         const float zt = load1(z + token);
         Stats v = no_stats();
-        float best[1] = {-INFINITY};
+        float best = -INFINITY;
         if (tid == 0 && row + a.ahead < a.rows)
             p.prefetch(a.ahead * a.ld);
-        scan<T, STEP, true, TOP>(p, a.k, v, best[0]);
+        scan<T, STEP, true, TOP>(p, a.k, v, best);
         while (p.last < last) {  // (threads read only what they copied)
             p.set(p.last, min(p.last + a.runs, last));
             p.fill();
-            scan<T, STEP, true, TOP>(p, a.k, v, best[0]);
+            scan<T, STEP, true, TOP>(p, a.k, v, best);
         }
         if constexpr (TOP) {
-            const int T_ = blockDim.x, each = (last - first + T_ - 1) / T_;
-            const auto run_of = [&](int part, int i) { return first + part + i * T_ < last ? first + part + i * T_ : -1; };
             if (p.first == first)
-                find_top(r, 1, each, best, a.top, sm, run_of, [&](int u) { return lds16(p.at(u)); });
+                find_top(r, first, last, best, a.top, sm, [&](int u) { return lds16(p.at(u)); });
             else
-                find_top(r, 1, each, best, a.top, sm, run_of, [&](int u) { return load_run(z, a.n, r.column(u)); });
+                find_top(r, first, last, best, a.top, sm, [&](int u) { return load_run(z, a.n, r.column(u)); });
         }
         join_block<true>(v, a.k.k2, part, blockDim.x >> 5);
         if (a.cluster > 1)
@@ -361,43 +352,200 @@ logprobs_rows(const Args a)
     }
 }
 
-// Their alternatives, a block a row.
+// Their alternatives, a warp a row: the search of find_top over the maxima in
+// the workspace (part p: chunk p / step of thread p % step), without barriers.
+struct WarpTop {
+    Key cand[kCandidates];  // the keys of groups first
+    Key sel[kMostTop];
+    Key limit;
+    uint16_t list[kMostListed];
+};
+
+__device__ __forceinline__ void warp_sort(const Key* cand, int n, int top, Key* sel)
+{
+    const int lane = threadIdx.x & 31;
+    for (int j = lane; j < top; j += 32)
+        if (j >= n)
+            sel[j] = 0;
+    for (int c = lane; c < n; c += 32) {
+        const Key k = cand[c];
+        int r = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j)
+            r += cand[j] > k;
+        if (r < top)
+            sel[r] = k;
+    }
+    __syncwarp();
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads)
 pick_top(const Args a)
 {
-    constexpr int S = kMostChunks * kThreadsMost / kPickThreads;
-    __shared__ TopSmem sm;
+    constexpr int U = 4, B = 16, V = Run<T>::V;
+    extern __shared__ __align__(16) char dynamic[];
+    WarpTop& sm = reinterpret_cast<WarpTop*>(dynamic)[threadIdx.x >> 5];
+    const int lane = threadIdx.x & 31, T_ = a.in.step, parts = a.chunks * T_;
+    const int each = 4 * a.gran, shift = 31 - __clz(T_);  // runs of a part; T_ is a power of two
+    const int64_t step = (int64_t)gridDim.x * (kPickThreads / 32);
     pdl_wait();
-    const int tid = threadIdx.x, P = blockDim.x, T_ = a.in.step;  // parts: chunk T_ + thread
-    const int parts = (a.chunks * T_ + P - 1) / P;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    for (int64_t row = (int64_t)blockIdx.x * (kPickThreads / 32) + (threadIdx.x >> 5); row < a.rows; row += step) {
         if (vocab::column_of(a.tokens, a.wide, row, a.n) < 0) {
-            for (int j = tid; j < a.top; j += P)
+            for (int j = lane; j < a.top; j += 32)
                 a.top_logprob[row * a.top + j] = -INFINITY, a.top_index[row * a.top + j] = -1;
             continue;
         }
         const T* z = static_cast<const T*>(a.logits) + row * a.ld;
-        const float* ws = a.ws + row * (2 + a.chunks * T_);
+        const float *ws = a.ws + row * (2 + parts), *maxima = ws + 2 + lane;
         const RowRuns<T> q(z, a.n, T_);
-        float m[S];
+        // the bound: 64 or 128 groups' maxima, 2 or 4 of them a lane
+        float sub[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        for (int s = 0; s < parts; s += 32 * B) {  // B loads in flight
+            float m[B];
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-            m[s] = s * P + tid < a.chunks * T_ ? ws[2 + s * P + tid] : -INFINITY;
-        const int each = 4 * a.gran, ends = (q.groups - 1) / a.gran;  // the chunk that has the row's borders
-        const auto run_of = [&](int id, int i) {
-            const int chunk = id / T_, t = id % T_;
-            if (i >= each) {
-                if (chunk == ends && i == each && t == 0 && q.head())
-                    return 0;
-                return chunk == ends && i == each + 1 && t == T_ - 1 && q.tail() ? q.r.count - 1 : -1;
+            for (int i = 0; i < B; ++i)
+                m[i] = s + 32 * i < parts ? maxima[s + 32 * i] : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+                sub[i & 3] = fmaxf(sub[i & 3], m[i]);
+        }
+        const int mine = a.top <= 24 ? 2 : 4;
+        if (mine == 2)
+            sub[0] = fmaxf(sub[0], sub[2]), sub[1] = fmaxf(sub[1], sub[3]);
+        Key k[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            k[i] = (sub[i] > -INFINITY ? key_of(sub[i], 0) >> 32 << 32 : 0) | (Key)(32 * i + lane);
+            if (i < mine)
+                sm.cand[32 * i + lane] = k[i];
+        }
+        __syncwarp();
+        int rank[4] = {0, 0, 0, 0};
+        if (mine == 2) {
+#pragma unroll 8
+            for (int j = 0; j < 64; ++j) {
+                const Key o = sm.cand[j];
+                rank[0] += o > k[0], rank[1] += o > k[1];
             }
-            const int u = q.whole0 + t + (chunk * each + i) * T_;
-            return u < q.whole1 ? u : -1;
+        } else {
+#pragma unroll 8
+            for (int j = 0; j < 128; ++j) {
+                const Key o = sm.cand[j];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    rank[i] += o > k[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < mine && rank[i] == a.top - 1)
+                sm.limit = k[i] >> 32 << 32;
+        __syncwarp();
+        Key bound = sm.limit;
+        const float least = bound ? value_of(bound) : -INFINITY;
+        int listed = 0;
+        for (int s = 0; s < parts; s += 32 * B) {
+            float m[B];
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+                m[i] = s + 32 * i < parts ? maxima[s + 32 * i] : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                const bool on = m[i] > -INFINITY && m[i] >= least;
+                const uint32_t who = __ballot_sync(0xFFFFFFFFu, on);
+                if (on)
+                    sm.list[listed + __popc(who & ((1u << lane) - 1u))] = (uint16_t)(s + 32 * i + lane);
+                listed += __popc(who);
+            }
+        }
+        __syncwarp();
+        int count = 0;
+        // Elements of the lanes' runs (at columns c, if `on`) that reach the
+        // bound: few runs have any, and a run's V elements go to V lanes.
+        const auto collect = [&](const uint4& w, int c, bool on) {
+            const uint4 x[1] = {w};
+            const float m = Run<T>::template top_of<1>(x);
+            uint32_t left = __ballot_sync(0xFFFFFFFFu, on && m > -INFINITY && key_of(m, max(c, 0)) >= bound);
+            while (left) {
+                uint32_t mine = left;
+#pragma unroll
+                for (int n = 0; n < 32 / V; ++n) {
+                    if (n < lane / V)
+                        mine &= mine - 1;
+                    left &= left - 1;
+                }
+                const int from = mine ? __ffs(mine) - 1 : 0, j = lane % V;
+                const uint4 y = make_uint4(__shfl_sync(0xFFFFFFFFu, w.x, from), __shfl_sync(0xFFFFFFFFu, w.y, from),
+                                           __shfl_sync(0xFFFFFFFFu, w.z, from), __shfl_sync(0xFFFFFFFFu, w.w, from));
+                const int at = __shfl_sync(0xFFFFFFFFu, c, from) + j;
+                float2 f[V / 2];
+                Run<T>::widen(y, f);
+                float e = f[0].x;
+#pragma unroll
+                for (int n = 1; n < V; ++n)
+                    if (n == j)
+                        e = n & 1 ? f[n >> 1].y : f[n >> 1].x;
+                const Key o = key_of(e, at);
+                const bool in = mine && e > -INFINITY && o >= bound;
+                const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
+                const int to = count + __popc(who & ((1u << lane) - 1u));
+                if (in && to < kCandidates)
+                    sm.cand[to] = o;
+                count += __popc(who);
+            }
         };
-        find_top(q.r, parts, each + 2, m, a.top, sm, run_of, [&](int u) { return load_run(z, a.n, q.r.column(u)); });
-        put_top(a, row, sm.sel, ws[0], ws[1]);
-        __syncthreads();
+        // the vectors at the row's borders, then the listed parts' runs, two parts at a time
+        if (q.head() || q.tail()) {
+            const bool on = lane == 0 ? q.head() : lane == 1 && q.tail();
+            const int c = q.r.column(lane == 0 ? 0 : q.r.count - 1);
+            collect(on ? load_run(z, a.n, c) : Run<T>::none(), c, on);
+        }
+        for (int l0 = 0, i0 = 0, rounds = U; l0 < listed;) {
+            const int before = count;
+            uint4 w[U];
+            int c[U];
+            bool on[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int l = l0 + 2 * i + (lane >> 4), n = i0 + (lane & 15);
+                on[i] = i < rounds && l < listed && n < each;
+                const int id = on[i] ? sm.list[l] : 0;
+                const int u = q.whole0 + (id & (T_ - 1)) + ((id >> shift) * each + n) * T_;
+                on[i] = on[i] && u < q.whole1;
+                c[i] = q.r.column(u);
+                w[i] = on[i] ? load_run(z, a.n, c[i]) : Run<T>::none();
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                collect(w[i], c[i], on[i]);
+            if (count > kCandidates) {  // not all of them had room: again, in a round that cannot overflow
+                count = before, rounds = kRound / 32;
+                continue;
+            }
+            i0 += 16;
+            if (i0 >= each)
+                i0 = 0, l0 += 2 * rounds;
+            if (l0 < listed && count > kKept) {
+                __syncwarp();
+                warp_sort(sm.cand, count, a.top, sm.sel);
+                for (int j = lane; j < a.top; j += 32)
+                    sm.cand[j] = sm.sel[j];
+                bound = sm.sel[a.top - 1], count = a.top;
+                if (i0 == 0)
+                    rounds = U;
+                __syncwarp();
+            }
+        }
+        __syncwarp();
+        warp_sort(sm.cand, count, a.top, sm.sel);
+        const float ref = ws[0], log_l = ws[1];
+        for (int j = lane; j < a.top; j += 32) {
+            const Key o = sm.sel[j];
+            a.top_logprob[row * a.top + j] = o ? (value_of(o) - ref) * a.scale - log_l : -INFINITY;
+            a.top_index[row * a.top + j] = o ? column_of(o) : -1;
+        }
+        __syncwarp();
     }
 }
 
@@ -478,10 +626,14 @@ int launch_many(const Args& a, cudaStream_t s)
     const int st = launch_status();
     if (!TOP || st != MFX_OK)
         return st;
-    const int64_t places = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(pick_top<T>), kPickThreads, 0);
+    constexpr int warps = kPickThreads / 32;
+    const size_t tops = warps * sizeof(WarpTop);
+    const int64_t need = (a.rows + warps - 1) / warps;
+    const int64_t places = (int64_t)sm_count() * occupancy(reinterpret_cast<const void*>(pick_top<T>), kPickThreads, tops);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.rows < places ? a.rows : places));
+    cfg.gridDim = dim3((unsigned)(need < places ? need : places));
     cfg.blockDim = dim3(kPickThreads);
+    cfg.dynamicSmemBytes = tops;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
