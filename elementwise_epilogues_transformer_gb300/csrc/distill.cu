@@ -81,7 +81,7 @@ __device__ __forceinline__ Teacher read_list(const Args& a, int64_t row, const L
     float top = -INFINITY, sum = 0.0f;
     for (int j = lane; j < a.K; j += 32) {
         const int c = column_of(a.index, a.wide, row * a.K + j, a.n);
-        const float t = c >= 0 ? teacher_at(a, row * a.K + j) : -INFINITY;
+        const float at = teacher_at(a, row * a.K + j), t = c >= 0 ? at : -INFINITY;  // both loads at once
         l.col[j] = c, l.z[j] = t;
         top = fmaxf(top, t);
     }
@@ -261,7 +261,7 @@ distill_fwd(const Args a)
         }
         __syncwarp();
         if (a.cluster > 1)
-            cluster_arrive();  // my_loss is there; before the gradient's stores, for which it would wait
+            cluster_arrive(tid >= threads);  // my_loss is there; before the gradient's stores, for which it would wait
         if (GRAD) {
             T* o = static_cast<T*>(a.out) + row * a.ldo;
             const Runs<T> ro(o, a.n);
@@ -296,7 +296,7 @@ distill_fwd(const Args a)
         }
         __syncwarp();
         if (a.cluster > 1) {  // nobody leaves, or goes on, while its loss is read
-            cluster_arrive_relaxed();
+            cluster_arrive(false);
             cluster_wait();
         }
     }

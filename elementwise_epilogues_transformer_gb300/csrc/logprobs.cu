@@ -292,10 +292,12 @@ logprobs_fwd(const Args a)
                 put_top(a, row, list, v.ref, log_l);
             }
         }
-        if (a.cluster > 1)
-            cluster_sync();
-        else
+        if (a.cluster > 1) {  // nobody leaves, or goes on, while its list is read
+            cluster_arrive(false);
+            cluster_wait();
+        } else {
             __syncthreads();
+        }
     }
 }
 

@@ -712,17 +712,17 @@ __device__ __forceinline__ void zero_runs(T* o, const Runs<T>& ro, int u0, int u
 }
 
 // --- clusters -------------------------------------------------------------
-// The same in two steps; the second one alone orders nothing.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_arrive_relaxed()
+// The cluster's barrier in two steps.  Only warps that have written what other
+// blocks read arrive with a release (`wrote`, the same for a whole warp): for
+// it a warp waits until all that it has stored is there.
+__device__ __forceinline__ void cluster_arrive(bool wrote)
 {
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    if (wrote)
+        asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+    else
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -745,7 +745,9 @@ __device__ __forceinline__ void join_cluster(Stats& v, float k2, Stats* mine, in
 {
     if (threadIdx.x == 0)
         *mine = v;
-    cluster_sync();
+    __syncwarp();
+    cluster_arrive(threadIdx.x < 32);
+    cluster_wait();
     const int peer = threadIdx.x & 7;
     v = no_stats();
     if (peer < blocks) {
