@@ -17,6 +17,9 @@ namespace mfx {
 namespace vocab {
 namespace {
 
+#ifndef MFX_TOP_FEW
+#define MFX_TOP_FEW 24
+#endif
 constexpr int kMostTop = 64;   // alternatives
 constexpr int kMostKeys = 128;  // groups of threads that bound the search for them
 constexpr int kMostChunks = 8;  // maxima of a thread of logprobs_rows
@@ -112,7 +115,7 @@ __device__ __forceinline__ void find_top(const Runs<T>& r, int first, int last, 
 {
     constexpr int V = Run<T>::V;
     const int tid = threadIdx.x, T_ = blockDim.x, lane = tid & 31, warp = tid >> 5;
-    const int want = top <= 24 ? 64 : kMostKeys, nkeys = T_ < want ? T_ : want, per = T_ / nkeys;
+    const int want = top <= MFX_TOP_FEW ? 64 : kMostKeys, nkeys = T_ < want ? T_ : want, per = T_ / nkeys;
     // equal ones in some order: a thread's place, below all columns
     Key k = (best > -INFINITY ? key_of(best, 0) >> 32 << 32 : 0) | (Key)tid;
     for (int o = 1; o < per; o <<= 1) {
@@ -412,7 +415,7 @@ pick_top(const Args a)
             for (int i = 0; i < B; ++i)
                 sub[i & 3] = fmaxf(sub[i & 3], m[i]);
         }
-        const int mine = a.top <= 24 ? 2 : 4;
+        const int mine = a.top <= MFX_TOP_FEW ? 2 : 4;
         if (mine == 2)
             sub[0] = fmaxf(sub[0], sub[2]), sub[1] = fmaxf(sub[1], sub[3]);
         Key k[4];
@@ -516,7 +519,7 @@ pick_top(const Args a)
                 const int u = q.whole0 + (id & (T_ - 1)) + ((id >> shift) * each + n) * T_;
                 on[i] = on[i] && u < q.whole1;
                 c[i] = q.r.column(u);
-                w[i] = on[i] ? load_run(z, a.n, c[i]) : Run<T>::none();
+                w[i] = on[i] ? load_run<T, true>(z, a.n, c[i]) : Run<T>::none();
             }
 #pragma unroll
             for (int i = 0; i < U; ++i)

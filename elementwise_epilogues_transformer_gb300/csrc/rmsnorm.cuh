@@ -26,7 +26,13 @@
 namespace mfx {
 namespace rmsnorm {
 
-constexpr int kMostDepth = 4;
+#ifndef MFX_NORM_E8
+#define MFX_NORM_E8 2048  // columns up to which a thread has 8 elements of a row, where rows are many
+#endif
+#ifndef MFX_NORM_DEPTH
+#define MFX_NORM_DEPTH 4
+#endif
+constexpr int kMostDepth = MFX_NORM_DEPTH;
 constexpr int kPad = 32;  // bytes that a row's covering vectors may be longer by
 
 // --- units ------------------------------------------------------------------
@@ -249,7 +255,7 @@ struct Layout {
 
 // Rows of up to 512 columns in a warp, others in a block: 8 elements a thread
 // up to 2048 columns (and for few rows, up to 1024 threads: the shortest way),
-// 16 up to 8192 (single columns: 32, above 8 x 1024), 32 up to 16384.
+// 16 up to 8192, 32 up to 16384.
 // `row`: bytes of a row of all streams (kPad included); `fixed`: bytes that a
 // team needs beside its rows; `resident`: threads of a multiprocessor that the
 // kernel's registers leave with E elements a thread.
@@ -261,10 +267,10 @@ Layout layout(int64_t rows, int64_t cols, int V, size_t row, size_t fixed, F res
     if (cols <= 16 * V && V > 1) {
         l.lanes = cols <= 8 * V ? 8 : 16;  // one unit each: a group of columns is consecutive lanes' also here
     } else if (cols <= 512) {
-        l.E = cols <= 256 ? 8 : V > 1 ? 16 : 32;
+        l.E = cols <= 256 ? 8 : 16;
     } else {
         const bool few = rows <= sm_count();
-        l.E = cols <= (few || V == 1 ? 8192 : 2048) ? 8 : V > 1 && cols <= 8192 ? 16 : 32;
+        l.E = cols <= (few ? 8192 : MFX_NORM_E8) ? 8 : cols <= 8192 ? 16 : 32;
         l.lanes = l.threads = lanes_of(l.E);
         if (l.E == 32 && l.lanes > 512)
             return l;

@@ -236,9 +236,8 @@ constexpr int unit_of() { return sizeof(XT) > sizeof(RT) ? 1 : sizeof(RT) == 2 ?
 template <typename XT, typename RT, int V>
 auto kernel_of(int E)
 {
-    if constexpr (V > 1)
-        if (E == 16)
-            return norm_bwd<XT, RT, V, 16>;
+    if (E == 16)
+        return norm_bwd<XT, RT, V, 16>;
     return E == 8 ? norm_bwd<XT, RT, V, 8> : norm_bwd<XT, RT, V, 32>;
 }
 

@@ -337,9 +337,8 @@ int with_units(const Args& a, const Layout& l, cudaStream_t s)
 {
     if (l.E == 8)
         return launch(norm_fwd<XT, RT, V, 8, Q>, a, l, s);
-    if constexpr (V > 1)
-        if (l.E == 16)
-            return launch(norm_fwd<XT, RT, V, 16, Q>, a, l, s);
+    if (l.E == 16)
+        return launch(norm_fwd<XT, RT, V, 16, Q>, a, l, s);
     return launch(norm_fwd<XT, RT, V, 32, Q>, a, l, s);
 }
 

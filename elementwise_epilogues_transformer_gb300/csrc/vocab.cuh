@@ -156,8 +156,8 @@ __device__ __noinline__ uint4 edge_run(const T* row, int n, int c)
 }
 
 // The same at any alignment, through the two aligned vectors that hold it
-// where those lie in the row.
-template <typename T>
+// where those lie in the row.  ALONE: its neighbours are not read.
+template <typename T, bool ALONE = false>
 __device__ __forceinline__ uint4 load_run(const T* row, int n, int c)
 {
     constexpr int V = Run<T>::V;
@@ -166,7 +166,7 @@ __device__ __forceinline__ uint4 load_run(const T* row, int n, int c)
     const uintptr_t lo = reinterpret_cast<uintptr_t>(row), hi = reinterpret_cast<uintptr_t>(row + n);
     if (c >= 0 && c + V <= n) {
         if (off == 0)
-            return ld16(reinterpret_cast<const void*>(a));
+            return ALONE ? ld16_ca(reinterpret_cast<const void*>(a)) : ld16(reinterpret_cast<const void*>(a));
         if (v >= lo && v + 32 <= hi) {
             const uint4 p = ld16_ca(reinterpret_cast<const void*>(v)), q = ld16_ca(reinterpret_cast<const void*>(v + 16));
             const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
@@ -655,7 +655,10 @@ template <typename T, int STEP> struct Stream {
 };
 
 // Rows that are read once, and enough of them, go one after another.
-inline bool streamed(int64_t rows) { return rows >= 2 * (int64_t)sm_count(); }
+#ifndef MFX_VOCAB_STREAM
+#define MFX_VOCAB_STREAM 2
+#endif
+inline bool streamed(int64_t rows) { return rows >= MFX_VOCAB_STREAM * (int64_t)sm_count(); }
 
 // A block's runs [u0, u1) of an output row from a row of logits: `f` makes a
 // run of results of a run of logits and its first column.  Four runs of a
