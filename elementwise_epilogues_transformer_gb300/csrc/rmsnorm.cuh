@@ -11,13 +11,14 @@
 // ten instructions left (loops over columns with all that inside had 60 to 180
 // and were bound by them).
 //
-// With vectors a thread's k-th unit is columns V (k lanes + lane) on (V = 8
-// where all data is bf16, 4 where some of it is fp32, so that a warp's
-// accesses cover whole lines of each), and it copies what it reads itself: no
-// barrier.  Without (a width that is not a multiple of 8, or a buffer off a
-// vector) units are single columns, 32 next to each other a warp and four such
-// steps on end, and rows are copied as the 16-byte vectors that cover them, by
-// all threads for all: a barrier more, or two.
+// A warp has 32 E columns on end.  With vectors a thread's k-th unit is columns
+// 32 V k + V lane on of them (V = 8 where all data is bf16, 4 where some of it
+// is fp32, so that a warp's accesses cover whole lines of each), and it copies
+// what it reads itself: no barrier; places past the row's end are zeros from
+// the start.  Without (a width that is not a multiple of 8, or a buffer off a
+// vector) units are single columns, 32 k + lane, and rows are copied as the
+// 16-byte vectors that cover them, by all threads for all: a barrier more, or
+// two.
 #pragma once
 
 #include "mfx_device.cuh"
@@ -116,32 +117,44 @@ __device__ __forceinline__ void factors(const void* weight, bool w_bf16, float o
         w[j] += offset;
 }
 
-// First column of a thread's k-th unit.
-template <int V>
-__device__ __forceinline__ int column_of(int k, int lanes, int tl)
+// First column of a thread's k-th unit, and how many of its N units begin
+// before the row's end (they do in order).
+template <int V, int E>
+__device__ __forceinline__ int column_of(int k, int tl)
 {
-    if constexpr (V > 1)
-        return (k * lanes + tl) * V;
-    else
-        return ((k >> 2) * (lanes >> 5) + (tl >> 5)) * 128 + (k & 3) * 32 + (tl & 31);
+    return (tl >> 5) * (32 * E) + k * (32 * V) + (tl & 31) * V;
+}
+template <int V, int E>
+__device__ __forceinline__ int units_of(int cols, int lanes, int tl)
+{
+    const int left = cols - column_of<V, E>(0, tl), n = left > 0 ? (left + 32 * V - 1) / (32 * V) : 0;
+    return min(lanes < 32 ? min(n, 1) : n, E / V);
 }
 
 // A thread's factors, 0 past the row's end.
-template <int V, int N>
-__device__ __forceinline__ void factors_of(const void* weight, bool w_bf16, float offset, int cols, int lanes, int tl,
-                                           float (&w)[N][V])
+template <int V, int E>
+__device__ __forceinline__ void factors_of(const void* weight, bool w_bf16, float offset, int mine, int tl, float (&w)[E / V][V])
 {
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const int c = column_of<V>(k, lanes, tl);
-        if (c < cols) {
-            factors<V>(weight, w_bf16, offset, c, w[k]);
+    for (int k = 0; k < E / V; ++k) {
+        if (k < mine) {
+            factors<V>(weight, w_bf16, offset, column_of<V, E>(k, tl), w[k]);
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j)
                 w[k][j] = 0.0f;
         }
     }
+}
+
+// A row's data that a thread reads: its k-th unit at shared address
+// a + k * 32 V size; 0 past the row's end.
+template <typename T, int V>
+__device__ __forceinline__ void read_unit(uint32_t a, int k, int mine, float (&f)[V])
+{
+    lds_unit<T, V>(a + (uint32_t)(k * 32 * V * (int)sizeof(T)), f);
+    if (V == 1 && k >= mine)  // a neighbour's element, or none (vectors: zeros from the start)
+        f[0] = 0.0f;
 }
 
 // --- rows on their way --------------------------------------------------------
@@ -174,15 +187,16 @@ __device__ __forceinline__ uint32_t where(const T* p)
 {
     return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
 }
-template <typename T, int V, int N>
-__device__ __forceinline__ void copy_row(uint32_t to, const T* p, int cols, const T* lo, const T* hi, int lanes, int tl)
+template <typename T, int V, int E>
+__device__ __forceinline__ void copy_row(uint32_t to, const T* p, int cols, const T* lo, const T* hi, int lanes, int tl,
+                                         int mine)
 {
     if constexpr (V > 1) {
-        to += tl * (uint32_t)(V * sizeof(T)), p += tl * V;
+        to += column_of<V, E>(0, tl) * (uint32_t)sizeof(T), p += column_of<V, E>(0, tl);
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-            if (column_of<V>(k, lanes, tl) < cols)
-                copy_unit<V * (int)sizeof(T)>(to + (uint32_t)(k * lanes * V) * (uint32_t)sizeof(T), p + k * lanes * V);
+        for (int k = 0; k < E / V; ++k)
+            if (k < mine)
+                copy_unit<V * (int)sizeof(T)>(to + (uint32_t)(k * 32 * V * (int)sizeof(T)), p + k * 32 * V);
     } else {
         constexpr int E = 16 / (int)sizeof(T);
         const int phase = (int)(where(p) / sizeof(T)), vectors = (cols + phase + E - 1) / E;
@@ -202,6 +216,20 @@ __device__ __forceinline__ void copy_row(uint32_t to, const T* p, int cols, cons
                     }
             }
         }
+    }
+}
+
+// Zeros for a thread's units past the row's end, in one row of a stream.
+template <typename T, int V, int E>
+__device__ __forceinline__ void clear_rest(uint32_t to, int tl, int mine)
+{
+    if constexpr (V > 1) {
+#pragma unroll
+        for (int k = 0; k < E / V; ++k)
+            if (k >= mine)
+                for (int j = 0; j < V * (int)sizeof(T); j += 4)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + (uint32_t)(column_of<V, E>(k, tl) * (int)sizeof(T) + j)),
+                                 "r"(0) : "memory");
     }
 }
 
@@ -246,50 +274,50 @@ __device__ __forceinline__ float2 over_team(float2 v, int lanes, float2 (*part)[
 
 // --- host ---------------------------------------------------------------------
 // Elements of a thread; threads of a row and of a block, rows that a team has
-// on their way, and the shared bytes of one of them.  depth 0: the row does not
+// on their way, the columns that one of them has room for, and its shared
+// bytes.  depth 0: the row does not
 // fit, or is longer than 512 threads of 32 elements.
 struct Layout {
     int E, lanes, threads, depth;
+    int64_t room;
     size_t row, smem;
 };
 
 // Rows of up to 512 columns in a warp, others in a block: 8 elements a thread
 // up to 2048 columns (and for few rows, up to 1024 threads: the shortest way),
-// 16 up to 8192, 32 up to 16384.
-// `row`: bytes of a row of all streams (kPad included); `fixed`: bytes that a
-// team needs beside its rows; `resident`: threads of a multiprocessor that the
-// kernel's registers leave with E elements a thread.
-template <typename F>
-Layout layout(int64_t rows, int64_t cols, int V, size_t row, size_t fixed, F resident)
+// 16 up to 8192, 32 up to 16384.  `most8`: columns up to which the kernel
+// takes 8 in any case.  row_bytes(room): bytes of a row of all streams;
+// resident(E): threads of a multiprocessor that the kernel's registers leave.
+template <typename B, typename F>
+Layout layout(int64_t rows, int64_t cols, int V, int64_t most8, B row_bytes, F resident)
 {
     const auto lanes_of = [&](int64_t e) { return (int)(((cols + e - 1) / e + 31) / 32 * 32); };
-    Layout l = {8, 32, 256, 0, (row + 15) / 16 * 16, 0};
+    Layout l = {8, 32, 256, 0, 0, 0, 0};
     if (cols <= 16 * V && V > 1) {
         l.lanes = cols <= 8 * V ? 8 : 16;  // one unit each: a group of columns is consecutive lanes' also here
     } else if (cols <= 512) {
         l.E = cols <= 256 ? 8 : 16;
     } else {
         const bool few = rows <= sm_count();
-        l.E = cols <= (few ? 8192 : MFX_NORM_E8) ? 8 : cols <= 8192 ? 16 : 32;
+        l.E = cols <= (few ? 8192 : most8) ? 8 : cols <= 8192 ? 16 : 32;
         l.lanes = l.threads = lanes_of(l.E);
         if (l.E == 32 && l.lanes > 512)
             return l;
     }
+    l.room = (int64_t)(l.lanes < 32 ? 32 : l.lanes) * l.E;
+    l.row = (row_bytes(l.room) + 15) / 16 * 16;
     const int64_t teams = l.threads / l.lanes;
-    fixed = (fixed + 15) / 16 * 16;
     const int most = resident(l.E) / l.threads;
     for (int blocks = most > 0 ? most : 1; blocks >= 1 && l.depth < 2; --blocks) {
         // a block's static arrays and what the system keeps of each: 2 KB
         const size_t each = (kMaxBlockSmem + 1024) / blocks - 2048;
-        if (each / teams <= fixed)
-            continue;
-        const size_t d = (each / teams - fixed) / l.row;
+        const size_t d = each / teams / l.row;
         l.depth = d > kMostDepth ? kMostDepth : (int)d;
     }
     const int64_t share = (rows + teams - 1) / teams;
     if (l.depth > 1 && share <= sm_count())
         l.depth = 1;  // no team has a second row
-    l.smem = (size_t)teams * (l.depth * l.row + fixed);
+    l.smem = (size_t)teams * l.depth * l.row;
     return l;
 }
 

@@ -40,7 +40,7 @@ norm_bwd(const Args a)
     __shared__ float2 part[2][32];
     extern __shared__ __align__(16) char dynamic[];
     const int lanes = a.lanes, teams = blockDim.x / lanes, team = threadIdx.x / lanes, tl = threadIdx.x % lanes;
-    const int cols = a.cols;
+    const int cols = a.cols, c0 = column_of<V, E>(0, tl), mine = units_of<V, E>(cols, lanes, tl);
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(dynamic) + team * (uint32_t)a.depth * a.row_bytes;
     const uint32_t end = ring + (uint32_t)a.depth * a.row_bytes;
     const int64_t step = (int64_t)gridDim.x * teams, all = a.rows * cols;
@@ -50,18 +50,23 @@ norm_bwd(const Args a)
     const auto start = [&](int64_t r, uint32_t to) {
         if (r - team < a.rows) {  // a team past the end takes the last row
             const int64_t at = (r < a.rows ? r : a.rows - 1) * cols;
-            copy_row<XT, V, N>(to, dy + at, cols, dy, dy + all, lanes, tl);
-            copy_row<RT, V, N>(to + a.x_bytes, hs + at, cols, hs, hs + all, lanes, tl);
+            copy_row<XT, V, E>(to, dy + at, cols, dy, dy + all, lanes, tl, mine);
+            copy_row<RT, V, E>(to + a.x_bytes, hs + at, cols, hs, hs + all, lanes, tl, mine);
             if (dh)
-                copy_row<RT, V, N>(to + a.x_bytes + a.r_bytes, dh + at, cols, dh, dh + all, lanes, tl);
+                copy_row<RT, V, E>(to + a.x_bytes + a.r_bytes, dh + at, cols, dh, dh + all, lanes, tl, mine);
         }
         copies_commit();
     };
     int64_t next = row;
-    for (uint32_t to = ring; to != end; to += a.row_bytes, next += step)
+    for (uint32_t to = ring; to != end; to += a.row_bytes, next += step) {
+        clear_rest<XT, V, E>(to, tl, mine);
+        clear_rest<RT, V, E>(to + a.x_bytes, tl, mine);
+        if (dh)
+            clear_rest<RT, V, E>(to + a.x_bytes + a.r_bytes, tl, mine);
         start(next, to);
+    }
     float w[N][V], acc[N][V];
-    factors_of<V, N>(a.weight, a.w_bf16, a.offset, cols, lanes, tl, w);
+    factors_of<V, E>(a.weight, a.w_bf16, a.offset, mine, tl, w);
 #pragma unroll
     for (int k = 0; k < N; ++k)
 #pragma unroll
@@ -72,54 +77,51 @@ norm_bwd(const Args a)
     for (; row - team < a.rows; row += step, next += step, slot ^= 1) {
         const bool on = row < a.rows;
         const int64_t r = on ? row : a.rows - 1, at = r * cols;
+        const int put = on ? mine : 0;  // units that count
         const float rstd = a.rstd[r];
         copies_wait(a.depth - 1);
         if (!VEC)
             team_barrier(lanes);
-        const uint32_t sg = buf + (VEC ? 0u : where(dy + at)), sh = buf + a.x_bytes + (VEC ? 0u : where(hs + at));
-        const uint32_t se = buf + a.x_bytes + a.r_bytes + (VEC || !dh ? 0u : where(dh + at));
-        const float counts = on ? rstd : 0.0f;
+        const uint32_t sg = buf + (VEC ? 0u : where(dy + at)) + c0 * (uint32_t)sizeof(XT);
+        const uint32_t sh = buf + a.x_bytes + (VEC ? 0u : where(hs + at)) + c0 * (uint32_t)sizeof(RT);
+        const uint32_t se = buf + a.x_bytes + a.r_bytes + (VEC || !dh ? 0u : where(dh + at)) + c0 * (uint32_t)sizeof(RT);
         float2 v = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const int c = column_of<V>(k, lanes, tl);
-            if (c < cols) {
-                float g[V], h[V];
-                lds_unit<XT, V>(sg + c * (uint32_t)sizeof(XT), g);
-                lds_unit<RT, V>(sh + c * (uint32_t)sizeof(RT), h);
+            float g[V], h[V];
+            read_unit<XT, V>(sg, k, mine, g);
+            read_unit<RT, V>(sh, k, mine, h);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float gh = g[j] * h[j];
-                    if (on)
-                        acc[k][j] = fmaf(gh, counts, acc[k][j]);
-                    v.x = fmaf(gh, w[k][j], v.x);
-                }
+            for (int j = 0; j < V; ++j) {
+                const float gh = g[j] * h[j];
+                if (k < put)
+                    acc[k][j] = fmaf(gh, rstd, acc[k][j]);
+                v.x = fmaf(gh, w[k][j], v.x);
             }
         }
         v = over_team<false>(v, lanes, part, slot);
         const float b = rstd * (__fdiv_rn(v.x * rstd, (float)cols) * rstd);
-        XT* dx = a.dx ? static_cast<XT*>(a.dx) + at : nullptr;
-        RT* dres = a.dres ? static_cast<RT*>(a.dres) + at : nullptr;
+        XT* dx = a.dx ? static_cast<XT*>(a.dx) + at + c0 : nullptr;
+        RT* dres = a.dres ? static_cast<RT*>(a.dres) + at + c0 : nullptr;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const int c = column_of<V>(k, lanes, tl);
-            if (on && c < cols) {
-                float g[V], h[V];
-                lds_unit<XT, V>(sg + c * (uint32_t)sizeof(XT), g);
-                lds_unit<RT, V>(sh + c * (uint32_t)sizeof(RT), h);
+            float g[V], h[V];
+            read_unit<XT, V>(sg, k, mine, g);
+            read_unit<RT, V>(sh, k, mine, h);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                g[j] = fmaf(rstd, g[j] * w[k][j], -b * h[j]);
+            if (dh) {
+                read_unit<RT, V>(se, k, mine, h);
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    g[j] = fmaf(rstd, g[j] * w[k][j], -b * h[j]);
-                if (dh) {
-                    lds_unit<RT, V>(se + c * (uint32_t)sizeof(RT), h);
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        g[j] += h[j];
-                }
+                    g[j] += h[j];
+            }
+            if (k < put) {
                 if (dx)
-                    store_unit<XT, V>(dx + c, g);
+                    store_unit<XT, V>(dx + k * 32 * V, g);
                 if (dres)
-                    store_unit<RT, V>(dres + c, g);
+                    store_unit<RT, V>(dres + k * 32 * V, g);
             }
         }
         if (!VEC)
@@ -133,10 +135,10 @@ norm_bwd(const Args a)
     if (teams == 1) {
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            if (const int c = column_of<V>(k, lanes, tl); c < cols)
+            if (k < mine)
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    ws[c + j] = acc[k][j];
+                    ws[c0 + k * 32 * V + j] = acc[k][j];
         return;
     }
     // the teams' sums in order (rows are 512 columns at most; nothing is on its way any more)
@@ -144,10 +146,10 @@ norm_bwd(const Args a)
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < N; ++k)
-        if (const int c = column_of<V>(k, lanes, tl); c < cols)
+        if (k < mine)
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                sums[team * cols + c + j] = acc[k][j];
+                sums[team * cols + c0 + k * 32 * V + j] = acc[k][j];
     __syncthreads();
     for (int c = threadIdx.x; c < cols; c += blockDim.x) {
         float s = sums[c];
@@ -250,13 +252,17 @@ auto kernel_of(int E, bool vec)
 template <typename XT, typename RT>
 Plan plan(int64_t rows, int64_t cols, bool vec)
 {
-    const size_t x = ((size_t)cols * sizeof(XT) + kPad + 15) / 16 * 16, r = ((size_t)cols * sizeof(RT) + kPad + 15) / 16 * 16;
-    Plan p = {{}, (uint32_t)x, (uint32_t)r, 0, 0, 0};
+    const auto x_bytes = [](int64_t room) { return ((size_t)room * sizeof(XT) + kPad + 15) / 16 * 16; };
+    const auto r_bytes = [](int64_t room) { return ((size_t)room * sizeof(RT) + kPad + 15) / 16 * 16; };
+    Plan p = {};
     const auto laid = [&](bool v) {
-        // teams' sums at the end: no more than a row of dy, h and dh each, which is 6 bytes a column or more
-        return layout(rows, cols, v ? unit_of<XT, RT>() : 1, x + 2 * r, 0, [](int e) { return e == 8 ? 1024 : 512; });
+        // (teams' sums at the end take no more than a row of dy, h and dh: 6 bytes a column or more)
+        return layout(rows, cols, v ? unit_of<XT, RT>() : 1, v ? MFX_NORM_E8 : 8192,
+                      [&](int64_t room) { return x_bytes(room) + 2 * r_bytes(room); },
+                      [](int e) { return e == 8 ? 1024 : 512; });
     };
     p.l = laid(vec);
+    p.x_bytes = (uint32_t)x_bytes(p.l.room), p.r_bytes = (uint32_t)r_bytes(p.l.room);
     if (p.l.depth == 0) {
         const int64_t slabs = (cols + kSlab * kThreads - 1) / (kSlab * kThreads);
         const int64_t lanes = (8 * sm_count() + slabs - 1) / slabs;

@@ -124,7 +124,7 @@ norm_fwd(const Args a)
     __shared__ float2 part[2][32];
     extern __shared__ __align__(16) char dynamic[];
     const int lanes = a.lanes, teams = blockDim.x / lanes, team = threadIdx.x / lanes, tl = threadIdx.x % lanes;
-    const int cols = a.cols, c0 = column_of<V>(0, lanes, tl);
+    const int cols = a.cols, c0 = column_of<V, E>(0, tl), mine = units_of<V, E>(cols, lanes, tl);
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(dynamic) + team * (uint32_t)a.depth * a.row_bytes;
     const uint32_t end = ring + (uint32_t)a.depth * a.row_bytes;
     const int64_t step = (int64_t)gridDim.x * teams, all = a.rows * cols;
@@ -134,51 +134,53 @@ norm_fwd(const Args a)
     const auto start = [&](int64_t r, uint32_t to) {
         if (r - team < a.rows) {  // a team past the end takes the last row
             const int64_t at = (r < a.rows ? r : a.rows - 1) * cols;
-            copy_row<XT, V, N>(to, x + at, cols, x, x + all, lanes, tl);
+            copy_row<XT, V, E>(to, x + at, cols, x, x + all, lanes, tl, mine);
             if (res)
-                copy_row<RT, V, N>(to + a.x_bytes, res + at, cols, res, res + all, lanes, tl);
+                copy_row<RT, V, E>(to + a.x_bytes, res + at, cols, res, res + all, lanes, tl, mine);
         }
         copies_commit();
     };
     int64_t next = row;
-    for (uint32_t to = ring; to != end; to += a.row_bytes, next += step)
+    for (uint32_t to = ring; to != end; to += a.row_bytes, next += step) {
+        clear_rest<XT, V, E>(to, tl, mine);
+        if (res)
+            clear_rest<RT, V, E>(to + a.x_bytes, tl, mine);
         start(next, to);
+    }
     float w[N][V];
-    factors_of<V, N>(a.weight, a.w_bf16, a.offset, cols, lanes, tl, w);
+    factors_of<V, E>(a.weight, a.w_bf16, a.offset, mine, tl, w);
     int slot = 0;
     uint32_t buf = ring;
     for (; row - team < a.rows; row += step, next += step, slot ^= 1) {
         const bool on = row < a.rows;
         const int64_t at = (on ? row : a.rows - 1) * cols;
+        const int put = on ? mine : 0;  // units to store
         copies_wait(a.depth - 1);
         if (!VEC)
             team_barrier(lanes);
-        const uint32_t sx = buf + (VEC ? 0u : where(x + at)), sr = buf + a.x_bytes + (VEC || !res ? 0u : where(res + at));
+        const uint32_t sx = buf + (VEC ? 0u : where(x + at)) + c0 * (uint32_t)sizeof(XT);
+        const uint32_t sr = buf + a.x_bytes + (VEC || !res ? 0u : where(res + at)) + c0 * (uint32_t)sizeof(RT);
         float f[N][V];
         float2 v = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int c = column_of<V>(k, lanes, tl);
+        for (int k = 0; k < N; ++k)
+            read_unit<XT, V>(sx, k, mine, f[k]);
+        if (res) {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                f[k][j] = 0.0f;
-            if (c < cols) {
-                lds_unit<XT, V>(sx + c * (uint32_t)sizeof(XT), f[k]);
-                if (res) {
-                    float g[V];
-                    lds_unit<RT, V>(sr + c * (uint32_t)sizeof(RT), g);
+            for (int k = 0; k < N; ++k) {
+                float g[V];
+                read_unit<RT, V>(sr, k, mine, g);
 #pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        f[k][j] += g[j];
-                }
+                for (int j = 0; j < V; ++j)
+                    f[k][j] += g[j];
             }
         }
-        if (a.h && on) {
-            RT* h = static_cast<RT*>(a.h) + at;
+        if (a.h) {
+            RT* h = static_cast<RT*>(a.h) + at + c0;
 #pragma unroll
             for (int k = 0; k < N; ++k)
-                if (const int c = column_of<V>(k, lanes, tl); c < cols)
-                    store_unit<RT, V>(h + c, f[k]);
+                if (k < put)
+                    store_unit<RT, V>(h + k * 32 * V, f[k]);
         }
 #pragma unroll
         for (int k = 0; k < N; ++k)
@@ -196,19 +198,17 @@ norm_fwd(const Args a)
         if (a.rstd && on && tl == 0)
             a.rstd[row] = rstd;
         if constexpr (Q == 0) {
-            if (on) {
-                XT* y = static_cast<XT*>(a.y) + at;
+            XT* y = static_cast<XT*>(a.y) + at + c0;
 #pragma unroll
-                for (int k = 0; k < N; ++k) {
+            for (int k = 0; k < N; ++k) {
 #pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        f[k][j] *= rstd;
-                    if (const int c = column_of<V>(k, lanes, tl); c < cols)
-                        store_unit<XT, V>(y + c, f[k]);
-                }
+                for (int j = 0; j < V; ++j)
+                    f[k][j] *= rstd;
+                if (k < put)
+                    store_unit<XT, V>(y + k * 32 * V, f[k]);
             }
         } else {
-            uint8_t* q = static_cast<uint8_t*>(a.y) + at;
+            uint8_t* q = static_cast<uint8_t*>(a.y) + at + c0;
             const int64_t scales = (on ? row : 0) * a.groups;
             const int share = min(a.group >> (V == 8 ? 3 : V == 4 ? 2 : 0), min(lanes, 32));  // lanes of a group
             Scale s = {1.0f, 1.0f};
@@ -219,7 +219,7 @@ norm_fwd(const Args a)
             }
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                const int c = column_of<V>(k, lanes, tl);
+                const int c = c0 + k * 32 * V;
                 if (Q == 2 && V > 1) {
                     float top = 0.0f;
 #pragma unroll
@@ -227,22 +227,22 @@ norm_fwd(const Args a)
                         top = amax(top, f[k][j]);
                     for (int o = share >> 1; o > 0; o >>= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                    s = group_scale(a, top * rstd, scales, c, on && c < cols && (c & (a.group - 1)) == 0);
+                    s = group_scale(a, top * rstd, scales, c, k < put && (c & (a.group - 1)) == 0);
                 } else if (Q == 2 && a.group == 32) {
                     const int top = __reduce_max_sync(0xFFFFFFFFu, __float_as_int(amax(0.0f, f[k][0])));
-                    s = group_scale(a, __int_as_float(top) * rstd, scales, c, on && c < cols && (tl & 31) == 0);
+                    s = group_scale(a, __int_as_float(top) * rstd, scales, c, k < put && (tl & 31) == 0);
                 } else if (Q == 2 && k % 4 == 0) {  // a warp's four steps
                     float mine = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         mine = amax(mine, f[(k + i) % N][0]);
                     const int top = __reduce_max_sync(0xFFFFFFFFu, __float_as_int(mine));
-                    s = group_scale(a, __int_as_float(top) * rstd, scales, c, on && c < cols && (tl & 31) == 0);
+                    s = group_scale(a, __int_as_float(top) * rstd, scales, c, k < put && (tl & 31) == 0);
                 }
                 // (h * weight) * (rstd / s): one rounding less than y itself has
                 const float by = rstd * s.inv;
-                if (on && c < cols)
-                    store_fp8<V>(q + c, f[k], by, a.e5m2);
+                if (k < put)
+                    store_fp8<V>(q + k * 32 * V, f[k], by, a.e5m2);
             }
         }
     }
@@ -348,12 +348,15 @@ template <typename XT, typename RT, bool Q>
 int with_types(Args a, bool vec, cudaStream_t s)
 {
     constexpr int V = sizeof(XT) > sizeof(RT) ? 1 : sizeof(RT) == 2 ? 8 : 4;
-    a.x_bytes = (uint32_t)(((size_t)a.cols * sizeof(XT) + kPad + 15) / 16 * 16);
-    const size_t row = a.x_bytes + (a.residual ? (size_t)a.cols * sizeof(RT) + kPad : 0);
-    const Layout l = layout(a.rows, a.cols, vec ? V : 1, row, 0, [](int e) { return e == 32 ? 512 : 1024; });
+    const auto x_bytes = [](int64_t room) { return ((size_t)room * sizeof(XT) + kPad + 15) / 16 * 16; };
+    const bool res = a.residual != nullptr;
+    const Layout l = layout(a.rows, a.cols, vec ? V : 1, MFX_NORM_E8,
+                            [&](int64_t room) { return x_bytes(room) + (res ? (size_t)room * sizeof(RT) + kPad : 0); },
+                            [](int e) { return e == 32 ? 512 : 1024; });
+    a.x_bytes = (uint32_t)x_bytes(l.room);
     if (l.depth == 0) {
         a.lanes = 1024;
-        return launch(norm_fwd_long<XT, RT, Q>, a, Layout{0, 1024, 1024, 0, 0, 0}, s);
+        return launch(norm_fwd_long<XT, RT, Q>, a, Layout{0, 1024, 1024, 0, 0, 0, 0}, s);
     }
     a.lanes = l.lanes, a.depth = l.depth, a.row_bytes = (uint32_t)l.row;
     if (Q && a.group)
