@@ -9,6 +9,16 @@
 // where U >= 0 and log l >= 0: nothing cancels, however far the row lies from
 // zero.  (m, 1 / l, U) are kept for the backward, which is then one pass:
 //   dz = scale * (g 1[token] - exp(t) / l * (g + ge * (t + U))).
+//
+// What bounds them: the backward HBM (8192x32768 bf16 161 us, 6670 GB/s, 0.98
+// of the copy rate).  The forward HBM in long rows (1024x131072 bf16 46 us,
+// 5860 GB/s), in shorter ones the instructions (8192x32768 99 us, 5440 GB/s:
+// nine an element, one of them the power, and a row's sums after every 64 KB);
+// rows below some 4 KB the sums alone (16384x1000 bf16 19 us, 5 of bytes).
+// Alternatives cost a second kernel for many rows (1024x131072 with 20: 65 us
+// in all, with 64: 96; found within the kernel, behind its barriers, they took
+// 122 and 361), whose time is the reach of single sectors, and some 4 us
+// within the kernel for few (8x131072 with 5: 8.3 us in all).
 #include "vocab.cuh"
 
 #include <cmath>
@@ -106,7 +116,8 @@ __device__ __forceinline__ void sort_out(const Key* cand, int n, int top, Key* s
 // The top-th largest of 64 groups of threads (128 for more than 24) bounds the
 // top-th largest logit from below, and only threads whose largest logit
 // reaches it can hold a column that does: of all elements about as many as are
-// asked for.  Their runs are read again for the columns that reach the bound.
+// asked for.  (64 groups for 64 alternatives: five times as many columns, 193
+// us instead of 96 at 1024x131072; 128 for 5: 9.7 us instead of 8.3 at 8x131072.)  Their runs are read again for the columns that reach the bound.
 // Should those be more than there is room for (many equal logits, or few
 // threads with most of the large ones), the runs are taken in small rounds and
 // the candidates cut to the best, which raises the bound.

@@ -31,7 +31,7 @@ namespace rmsnorm {
 #define MFX_NORM_E8 2048  // columns up to which a thread has 8 elements of a row, where rows are many
 #endif
 #ifndef MFX_NORM_DEPTH
-#define MFX_NORM_DEPTH 4
+#define MFX_NORM_DEPTH 2  // rows on their way (65536x1024 bf16 backward 122 us; 133 with four)
 #endif
 constexpr int kMostDepth = MFX_NORM_DEPTH;
 constexpr int kPad = 32;  // bytes that a row's covering vectors may be longer by
@@ -286,7 +286,9 @@ struct Layout {
 // Rows of up to 512 columns in a warp, others in a block: 8 elements a thread
 // up to 2048 columns (and for few rows, up to 1024 threads: the shortest way),
 // 16 up to 8192, 32 up to 16384.  `most8`: columns up to which the kernel
-// takes 8 in any case.  row_bytes(room): bytes of a row of all streams;
+// takes 8 in any case (forward 16384x4096 as e4m3 blocks: 89 us with 8, 83 with
+// 16; 32768x2048: 96 with 16, 98 with 8; the backward of single columns takes
+// 8 to the end: 8192x4099 bf16 157 us, 180 with 16).  row_bytes(room): bytes of a row of all streams;
 // resident(E): threads of a multiprocessor that the kernel's registers leave.
 template <typename B, typename F>
 Layout layout(int64_t rows, int64_t cols, int V, int64_t most8, B row_bytes, F resident)

@@ -7,7 +7,18 @@
 //   s = max |y| / largest,   q = y / s.
 // h stays in fp32 registers between the sum of its squares and y, so x and
 // the residual are read once, h and y (or q) written once; h is rounded only
-// where it is stored for the next layer.
+// where it is stored for the next layer.  rstd is a common factor of a row:
+// the largest |h * weight| is found along with the sum, and h * weight goes to
+// q by one factor rstd / s.
+//
+// What bounds it: HBM, at one read and one write of everything; with 8-bit
+// outputs the issue slots come near (a group's maximum and scale, the
+// conversions: some 30 instructions an element at 70 % of the slots).
+// Measured: 16384x4096 bf16 with an fp32 residual 132 us (6120 GB/s, 0.90 of
+// the copy rate), all bf16 92 us; 8192x8192 bf16 91 us, as e4m3 with a scale a
+// row 84 us (5590 GB/s); 16384x4096 as e4m3 with a power of two per 32 columns
+// 79 us; 3001x2051 fp32 (single columns) 16.8 us (5850 GB/s); 8192x4099 bf16
+// 66 us (4050 GB/s: two bytes an access); one row of 4096 2.6 us.
 #include "rmsnorm.cuh"
 
 #include <cmath>
