@@ -354,7 +354,8 @@ int mfx_moe_unpermute_bwd(int dt, int64_t tokens, int64_t topk, int64_t cols, in
  * weights that are kept around zero, else 0.  residual NULL: h = x (and h must
  * be NULL).  h (NULL: not written) is the new residual stream; y is formed
  * from it before it is rounded.  rstd: [rows] fp32, what the backward needs,
- * or NULL.  Norms are fp32: squares of values beyond 1.8e19 overflow.
+ * or NULL.  Norms are fp32: squares of values beyond 1.8e19 overflow, and a
+ * row of zeros with eps = 0 gives NaN.
  * eps >= 0 and finite, else MFX_ERR_VALUE; cols up to 2^30.  y and h may each
  * be x's or the residual's very buffer; other overlaps -> MFX_ERR_ALIAS. */
 int mfx_add_rmsnorm_fwd(int x_dt, int res_dt, int w_dt, int64_t rows, int64_t cols,
