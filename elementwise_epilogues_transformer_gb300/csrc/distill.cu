@@ -114,7 +114,8 @@ __device__ __forceinline__ Teacher read_list(const Args& a, int64_t row, const L
         const int j = j0 + lane, c = j < a.K ? l.col[j] : -1;
         const float t = j < a.K ? l.z[j] : -INFINITY;
         const bool here = c >= lo && c < hi;
-        const uint32_t who = __ballot_sync(0xFFFFFFFFu, here);  // (and all lanes have read)
+        const uint32_t who = __ballot_sync(0xFFFFFFFFu, here);
+        __syncwarp();  // all lanes have read
         if (here) {
             const int to = w.n + __popc(who & ((1u << lane) - 1u));
             l.col[to] = c;
@@ -458,7 +459,8 @@ int run(int dt, int t_dt, int64_t rows, int64_t vocab, int64_t ld, int64_t k, co
     if (out && !rows_alias_ok(out, ldo, logits, ld, rows, vocab, z))
         return MFX_ERR_ALIAS;
     Args a = {};
-    a.rows = rows, a.ld = ld, a.ldo = ldo, a.n = (int)vocab, a.K = (int)k, a.logits = logits, a.index = index;
+    // rows without columns hold nothing to read, whatever their distance says
+    a.rows = rows, a.ld = vocab ? ld : 0, a.ldo = ldo, a.n = (int)vocab, a.K = (int)k, a.logits = logits, a.index = index;
     a.teacher = teacher, a.wide = index_bits == 64, a.t_bf16 = t_dt == MFX_BF16, a.scale = scale;
     a.k2 = scale * kLog2e, a.k = scaling_of(scale), a.lse = lse, a.g = g, a.loss = loss, a.stats = stats, a.stats_in = stats_in, a.out = out;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -278,3 +278,29 @@ def test_gradients_against_differences():
         by = (loss(z.double() + s * v) - loss(z.double() - s * v)) / (2 * s)
         # 32-bit gradients (a few 2^-22 of each term) and s^2 of third derivatives
         assert abs((d * v).sum() - by) <= 4e-6 * (d * v).abs().sum() + 1e-8
+
+
+@pytest.mark.parametrize("dt", [0, 1])
+@pytest.mark.parametrize("address", ["none", "off a vector"])
+def test_rows_without_columns_lie_apart(dt, address):
+    """Rows of no columns, a distance apart, in every number: nothing is read,
+    and no entry or token counts."""
+    L, k, ld = mfx.lib(), 3, 5
+    some = torch.zeros(64, device=DEV)
+    z = None if address == "none" else some.data_ptr() + 4
+    for rows in (1, 7, 400):
+        index = torch.zeros((rows, k), dtype=torch.int64, device=DEV)
+        teacher, loss = torch.zeros((rows, k), device=DEV), torch.full((rows,), 7.0, device=DEV)
+        lp, ent = torch.full((rows,), 7.0, device=DEV), torch.full((rows,), 7.0, device=DEV)
+        s = torch.cuda.current_stream().cuda_stream
+        assert L.mfx_topk_distill_fwd(dt, 0, rows, 0, ld, k, z, 64, index.data_ptr(), teacher.data_ptr(), None, 1.0,
+                                      loss.data_ptr(), None, s) == 0
+        assert (loss == 0).all()
+        loss.fill_(7.0)
+        assert L.mfx_topk_distill_fwd_bwd(dt, 0, rows, 0, ld, k, z, 64, index.data_ptr(), teacher.data_ptr(), None,
+                                          teacher.data_ptr(), 1.0, loss.data_ptr(), None,
+                                          ld, s) == 0
+        assert (loss == 0).all()
+        assert L.mfx_token_logprobs_fwd(dt, rows, 0, ld, z, 64, index.data_ptr(), 1.0, 0, lp.data_ptr(), ent.data_ptr(),
+                                        None, None, None, None, None, s) == 0
+        assert (lp == 0).all() and (ent == 0).all()
