@@ -15,8 +15,8 @@
 // 5860 GB/s), in shorter ones the instructions (8192x32768 99 us, 5440 GB/s:
 // nine an element, one of them the power, and a row's sums after every 64 KB);
 // rows below some 4 KB the sums alone (16384x1000 bf16 19 us, 5 of bytes).
-// Alternatives cost a second kernel for many rows (1024x131072 with 20: 65 us
-// in all, with 64: 96; found within the kernel, behind its barriers, they took
+// Alternatives cost a second kernel for many rows (1024x131072 with 20: 64 us
+// in all, with 64: 90; found within the kernel, behind its barriers, they took
 // 122 and 361), whose time is the reach of single sectors, and some 4 us
 // within the kernel for few (8x131072 with 5: 8.3 us in all).
 #include "vocab.cuh"
@@ -32,7 +32,9 @@ namespace {
 #endif
 constexpr int kMostTop = 64;   // alternatives
 constexpr int kMostKeys = 128;  // groups of threads that bound the search for them
-constexpr int kMostChunks = 8;  // maxima of a thread of logprobs_rows
+// Maxima of a thread of logprobs_rows, all used where its runs allow it: what pick_top reads again is 4 runs for each
+// that counts, or more in long rows (4096x32768 with 20: 80 us, 102 with 16 runs to a maximum; 1024x131072 with 64: 90 and 97).
+constexpr int kMostChunks = 8;
 constexpr int kMostListed = kMostChunks * kThreadsMost;
 constexpr int kPickThreads = 128;
 constexpr int kRound = 64;      // runs of a round that cannot overflow the candidates
@@ -117,7 +119,7 @@ __device__ __forceinline__ void sort_out(const Key* cand, int n, int top, Key* s
 // top-th largest logit from below, and only threads whose largest logit
 // reaches it can hold a column that does: of all elements about as many as are
 // asked for.  (64 groups for 64 alternatives: five times as many columns, 193
-// us instead of 96 at 1024x131072; 128 for 5: 9.7 us instead of 8.3 at 8x131072.)  Their runs are read again for the columns that reach the bound.
+// us instead of 96 at 1024x131072 at that step; 128 for 5: 9.7 us instead of 8.3 at 8x131072.)  Their runs are read again for the columns that reach the bound.
 // Should those be more than there is room for (many equal logits, or few
 // threads with most of the large ones), the runs are taken in small rounds and
 // the candidates cut to the best, which raises the bound.
@@ -404,6 +406,7 @@ pick_top(const Args a)
     WarpTop& sm = reinterpret_cast<WarpTop*>(dynamic)[threadIdx.x >> 5];
     const int lane = threadIdx.x & 31, T_ = a.in.step, parts = a.chunks * T_;
     const int each = 4 * a.gran, shift = 31 - __clz(T_);  // runs of a part; T_ is a power of two
+    const int log_reach = a.gran == 1 ? 2 : a.gran == 2 ? 3 : 4, reach = 1 << log_reach;  // lanes of a part: 4, 8 or 16
     const int64_t step = (int64_t)gridDim.x * (kPickThreads / 32);
     pdl_wait();
     for (int64_t row = (int64_t)blockIdx.x * (kPickThreads / 32) + (threadIdx.x >> 5); row < a.rows; row += step) {
@@ -511,7 +514,7 @@ pick_top(const Args a)
                 count += __popc(who);
             }
         };
-        // the vectors at the row's borders, then the listed parts' runs, two parts at a time
+        // the vectors at the row's borders, then the listed parts' runs, 2 to 8 parts at a time
         if (q.head() || q.tail()) {
             const bool on = lane == 0 ? q.head() : lane == 1 && q.tail();
             const int c = q.r.column(lane == 0 ? 0 : q.r.count - 1);
@@ -524,7 +527,7 @@ pick_top(const Args a)
             bool on[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const int l = l0 + 2 * i + (lane >> 4), n = i0 + (lane & 15);
+                const int l = l0 + (i << (5 - log_reach)) + (lane >> log_reach), n = i0 + (lane & (reach - 1));
                 on[i] = i < rounds && l < listed && n < each;
                 const int id = on[i] ? sm.list[l] : 0;
                 const int u = q.whole0 + (id & (T_ - 1)) + ((id >> shift) * each + n) * T_;
@@ -539,9 +542,9 @@ pick_top(const Args a)
                 count = before, rounds = kRound / 32;
                 continue;
             }
-            i0 += 16;
+            i0 += reach;
             if (i0 >= each)
-                i0 = 0, l0 += 2 * rounds;
+                i0 = 0, l0 += rounds << (5 - log_reach);
             if (l0 < listed && count > kKept) {
                 __syncwarp();
                 warp_sort(sm.cand, count, a.top, sm.sel);
@@ -666,7 +669,7 @@ int launch_fwd(Args a, void* workspace, size_t* bytes, cudaStream_t s)
     const int64_t runs = (a.n * (int64_t)sizeof(T) + 15) / 16 + 1;  // with a head and a tail
     a.in = {a.rows, a.ld, a.n, threads_for(runs, kThreadsMost), a.logits, a.tokens, a.wide};
     const int64_t groups = (runs + 4 * a.in.step - 1) / (4 * a.in.step);
-    a.gran = (int)(groups > 4 * kMostChunks ? (groups + kMostChunks - 1) / kMostChunks : 4);
+    a.gran = (int)((groups + kMostChunks - 1) / kMostChunks);
     a.chunks = (int)((groups + a.gran - 1) / a.gran);
     const size_t need = a.top && many ? (size_t)a.rows * (2 + a.chunks * a.in.step) * sizeof(float) : 0;
     if (bytes && !workspace) {
