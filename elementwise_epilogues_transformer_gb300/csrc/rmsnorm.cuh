@@ -27,9 +27,6 @@
 namespace mfx {
 namespace rmsnorm {
 
-#ifndef MFX_NORM_E8
-#define MFX_NORM_E8 2048  // columns up to which a thread has 8 elements of a row, where rows are many
-#endif
 #ifndef MFX_NORM_DEPTH
 #define MFX_NORM_DEPTH 2  // rows on their way (65536x1024 bf16 backward 122 us; 133 with four)
 #endif
@@ -284,14 +281,13 @@ struct Layout {
 };
 
 // Rows of up to 512 columns in a warp, others in a block: 8 elements a thread
-// up to 2048 columns (and for few rows, up to 1024 threads: the shortest way),
-// 16 up to 8192, 32 up to 16384.  `most8`: columns up to which the kernel
-// takes 8 in any case (forward 16384x4096 as e4m3 blocks: 89 us with 8, 83 with
-// 16; 32768x2048: 96 with 16, 98 with 8; the backward of single columns takes
-// 8 to the end: 8192x4099 bf16 157 us, 180 with 16).  row_bytes(room): bytes of a row of all streams;
-// resident(E): threads of a multiprocessor that the kernel's registers leave.
+// up to `most8` columns (and for few rows, up to 1024 threads: the shortest
+// way), 16 up to `most16`, 32 up to 16384.  The more a thread has, the less a
+// row's sum and bookkeeping weigh, as long as its registers leave enough
+// threads for what is on its way.  row_bytes(room): bytes of a row of all
+// streams; resident(E): threads of a multiprocessor that the kernel's registers leave.
 template <typename B, typename F>
-Layout layout(int64_t rows, int64_t cols, int V, int64_t most8, B row_bytes, F resident)
+Layout layout(int64_t rows, int64_t cols, int V, int64_t most8, int64_t most16, B row_bytes, F resident)
 {
     const auto lanes_of = [&](int64_t e) { return (int)(((cols + e - 1) / e + 31) / 32 * 32); };
     Layout l = {8, 32, 256, 0, 0, 0, 0};
@@ -301,7 +297,7 @@ Layout layout(int64_t rows, int64_t cols, int V, int64_t most8, B row_bytes, F r
         l.E = cols <= 256 ? 8 : 16;
     } else {
         const bool few = rows <= sm_count();
-        l.E = cols <= (few ? 8192 : most8) ? 8 : cols <= 8192 ? 16 : 32;
+        l.E = cols <= (few ? 8192 : most8) ? 8 : cols <= most16 ? 16 : 32;
         l.lanes = l.threads = lanes_of(l.E);
         if (l.E == 32 && l.lanes > 512)
             return l;

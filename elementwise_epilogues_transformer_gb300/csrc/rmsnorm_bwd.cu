@@ -14,7 +14,7 @@
 //
 // What bounds it: HBM where units are wide and a residual is fp32 (16384x4096
 // 164 us, 6540 GB/s, 0.96 of the copy rate); latency at the warps that the
-// registers of the sums leave in bf16 (8192x8192 128 us, 5250 GB/s); single
+// registers of the sums leave in bf16 (8192x8192 112.5 us, 5960 GB/s); single
 // columns their instructions (3001x2051 fp32 29.5 us with 4.5 of the sums'
 // kernel; 8192x4099 bf16 139 us).  Reading dy and h a second time from shared
 // memory costs less than the registers that would hold them.
@@ -38,14 +38,8 @@ struct Args {
     float *ws, *dots;
 };
 
-// Blocks of 512 threads that a multiprocessor's registers hold with 16 elements
-// a thread: two (64 registers) where all is bf16, one (128) where units are
-// smaller (8192x8192 bf16 129 against 145 us; 16384x4096 with an fp32 residual
-// 176 against 163).
-template <int V> constexpr int blocks16() { return V == 8 ? 2 : 1; }
-
 template <typename XT, typename RT, int V, int E>
-__global__ void __launch_bounds__(E == 8 ? 1024 : 512, E == 16 ? blocks16<V>() : 1)
+__global__ void __launch_bounds__(E == 8 ? 1024 : 512, 1)
 norm_bwd(const Args a)
 {
     constexpr int N = E / V;
@@ -269,10 +263,14 @@ Plan plan(int64_t rows, int64_t cols, bool vec)
     const auto r_bytes = [](int64_t room) { return ((size_t)room * sizeof(RT) + kPad + 15) / 16 * 16; };
     Plan p = {};
     const auto laid = [&](bool v) {
+        // One type: 32 elements a thread beyond 1024 columns (bf16 8192x8192 112.5 us, 128 with 16; 32768x2048 120, 126
+        // with 8; 65536x1024 122, 129 with 32; fp32 16384x4096 203, 210 with 16).  Two types 8 and 16 (16384x4096 164,
+        // 171 with 32), single columns 8 to the end (8192x4099 bf16 138, 180 with 16).
+        const bool wide = sizeof(XT) == sizeof(RT) && v;
         // (teams' sums at the end take no more than a row of dy, h and dh: 6 bytes a column or more)
-        return layout(rows, cols, v ? unit_of<XT, RT>() : 1, v ? MFX_NORM_E8 : 8192,
+        return layout(rows, cols, v ? unit_of<XT, RT>() : 1, wide ? 1024 : v ? 2048 : 8192, wide ? 1024 : 8192,
                       [&](int64_t room) { return x_bytes(room) + 2 * r_bytes(room); },
-                      [&](int e) { return e == 8 ? 1024 : e == 16 && v ? 512 * blocks16<unit_of<XT, RT>()>() : 512; });
+                      [&](int e) { return e == 8 ? 1024 : 512; });
     };
     p.l = laid(vec);
     p.x_bytes = (uint32_t)x_bytes(p.l.room), p.r_bytes = (uint32_t)r_bytes(p.l.room);

@@ -15,10 +15,10 @@
 // outputs the issue slots come near (a group's maximum and scale, the
 // conversions: some 30 instructions an element at 70 % of the slots).
 // Measured: 16384x4096 bf16 with an fp32 residual 132 us (6120 GB/s, 0.90 of
-// the copy rate), all bf16 92 us; 8192x8192 bf16 91 us, as e4m3 with a scale a
-// row 84 us (5590 GB/s); 16384x4096 as e4m3 with a power of two per 32 columns
-// 79 us; 3001x2051 fp32 (single columns) 16.8 us (5850 GB/s); 8192x4099 bf16
-// 66 us (4050 GB/s: two bytes an access); one row of 4096 2.6 us.
+// the copy rate), all bf16 89 us; 8192x8192 bf16 89 us, as e4m3 with a scale a
+// row 80.5 us (5830 GB/s); 16384x4096 as e4m3 with a power of two per 32
+// columns 79.5 us; 3001x2051 fp32 (single columns) 16.8 us (5850 GB/s);
+// 8192x4099 bf16 66 us (4050 GB/s: two bytes an access); one row of 4096 2.6 us.
 #include "rmsnorm.cuh"
 
 #include <cmath>
@@ -361,7 +361,11 @@ int with_types(Args a, bool vec, cudaStream_t s)
     constexpr int V = sizeof(XT) > sizeof(RT) ? 1 : sizeof(RT) == 2 ? 8 : 4;
     const auto x_bytes = [](int64_t room) { return ((size_t)room * sizeof(XT) + kPad + 15) / 16 * 16; };
     const bool res = a.residual != nullptr;
-    const Layout l = layout(a.rows, a.cols, vec ? V : 1, MFX_NORM_E8,
+    // One type and no groups: 32 elements a thread (65536x1024 bf16 91 us, 96 with 8; 16384x4096 89, 91.5 with 16; to
+    // e4m3 by rows 8192x8192 80.5, 84).  A group's maximum and scale, and two types, leave registers for fewer (e4m3 by
+    // 32 columns 16384x4096 79.5, 86 with 32 and 89 with 8; single columns 3001x2051 fp32 16.7, 18.4 with 32).
+    const bool wide = sizeof(XT) == sizeof(RT) && vec && !a.group;
+    const Layout l = layout(a.rows, a.cols, vec ? V : 1, wide ? 512 : 2048, wide ? 512 : 8192,
                             [&](int64_t room) { return x_bytes(room) + (res ? (size_t)room * sizeof(RT) + kPad : 0); },
                             [](int e) { return e == 32 ? 512 : 1024; });
     a.x_bytes = (uint32_t)x_bytes(l.room);

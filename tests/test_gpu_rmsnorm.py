@@ -237,3 +237,26 @@ def test_bwd_against_differences():
     assert abs((dx.double() * vx).sum() - by_x) <= 1e-6 * size
     assert abs((dw.double() * vw).sum() - by_w) <= 1e-6 * (dw.double() * vw).abs().sum()
     assert torch.equal(dx, dres)
+
+
+@pytest.mark.parametrize("cols", [264, 504, 512, 520, 768, 1000, 1024, 1032, 1544, 2048, 2056, 4096, 5000, 8192, 8200, 16384])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_rows_of_one_type(cols, dtype):
+    """Up to 32 elements a thread, with rows on their way: forward, in place,
+    8 bits with a scale a row, backward in place, the same bits again."""
+    rows = 1203
+    x, residual, weight = rand((rows, cols), dtype), rand((rows, cols), dtype, 2.0), rand((cols,), dtype, 0.3) + 1
+    y, h, rstd = check_fwd(x, residual, weight)
+    x2, r2 = x.clone(), residual.clone()
+    mfx.mfx_add_rmsnorm_fwd(x2, weight, residual=r2, y=x2, h=r2)
+    assert torch.equal(y, x2) and torch.equal(h, r2)
+    q, scale, h2, _ = mfx.mfx_add_rmsnorm_quant_fwd(x, weight, residual=residual)
+    assert torch.equal(h, h2)
+    want, _, rel = norm_fwd(x, residual, weight, 1e-6, 0.0)[1:]
+    # half a step of the type, or of its smallest numbers
+    assert excess(dequantised(q, scale, 0), want, want.abs() * (2.0 ** -4 + 2 * rel + 8 * U) + scale.double().view(-1, 1) * 2.0 ** -10 * (1 + 1e-6)) <= 1
+    dy, dh = rand((rows, cols), dtype), rand((rows, cols), dtype)
+    a = check_bwd(dy, h, rstd, weight, dh)
+    g = dy.clone()
+    dx, _, dw = mfx.mfx_add_rmsnorm_bwd(g, h, rstd, weight, dh=dh, dx=g)
+    assert torch.equal(dx, a[0]) and torch.equal(dw, a[2])
