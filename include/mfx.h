@@ -408,7 +408,7 @@ int mfx_add_rmsnorm_bwd(int x_dt, int res_dt, int w_dt, int64_t rows, int64_t co
 /* Log probabilities of given tokens, the distribution's entropy, and the `top`
  * (0 to 64, else MFX_ERR_VALUE) largest logits' log probabilities and columns.
  * tokens: [rows]; a token outside [0, vocab) leaves its row out: its results
- * are 0, its alternatives (-inf, -1), and its logits are not read.
+ * are 0, its alternatives (-inf, -1), and nothing comes of its logits.
  * logprob[r] = log p[token], entropy[r] = -sum p log p (fp32).
  * top_logprob, top_index: [rows, top] in falling order, equal logits by the
  * lower column; (-inf, -1) where fewer than `top` are above -inf; columns with
