@@ -100,12 +100,14 @@ __device__ __forceinline__ Teacher read_list(const Args& a, int64_t row, const L
         for (int j = lane; j < a.K; j += 32)
             sum += power_of(a, l.z[j], w.ref);
         sum = warp_sum(sum);
-        if (a.lse) {
+        if (sum == 0.0f) {  // no entries: q is 0 whatever lse says, whose power may be infinite (a NaN makes the sum one)
+            w.log_coef = w.coef = 0.0f;
+        } else if (a.lse) {
             w.log_coef = fmaf(w.ref, a.scale, -a.lse[row]);
             w.coef = expf(w.log_coef);
         } else {
-            w.log_coef = sum == 0.0f ? 0.0f : -logf(sum);
-            w.coef = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+            w.log_coef = -logf(sum);
+            w.coef = __fdiv_rn(1.0f, sum);
         }
         w.Q = sum * w.coef;
     }

@@ -442,7 +442,9 @@ int mfx_token_logprobs_bwd(int dt, int64_t rows, int64_t vocab, int64_t ld,
  * teacher_lse [rows] fp32, exp(scale * t - teacher_lse): the teacher's own
  * normalisation over its whole vocabulary.
  *   loss[r] = sum_j q_j (log q_j - log p[column j])           (fp32)
- * (0 without entries; +inf where a column with q > 0 has p = 0).
+ * (+inf where a column with q > 0 has p = 0).  A row whose list names no column,
+ * or whose entries are all -inf, has no entries: loss 0, whatever teacher_lse
+ * says of it.
  * stats: [rows, 4] fp32, what the backward needs, or NULL. */
 int mfx_topk_distill_fwd(int dt, int t_dt, int64_t rows, int64_t vocab, int64_t ld, int64_t k,
                          const void* logits, int index_bits, const void* index,
