@@ -145,6 +145,13 @@ __device__ __forceinline__ float loss_of(const Args& a, const List& l, int n, co
     return warp_sum(sum);
 }
 
+// What a row's gradient has of p: Q over the student's sum, 0 where nothing
+// comes of the row (no entries, whatever its logits are, or no column left).
+__device__ __forceinline__ float ratio_of(float Q, const Stats& v)
+{
+    return Q == 0.0f || v.l == 0.0f ? 0.0f : __fdiv_rn(Q, v.l);
+}
+
 // The gradient exp(t) * A of a run.
 template <typename T>
 __device__ __forceinline__ uint4 grad_run(const uint4& w, float ref, float k2, float A)
@@ -259,7 +266,7 @@ distill_fwd(const Args a)
         join_block<false>(v, a.k2, part, threads >> 5);  // and the slice and Q are there for all threads
         if (a.cluster > 1)
             join_cluster<false>(v, a.k2, &mine, a.cluster);
-        const float ratio = v.l == 0.0f ? 0.0f : __fdiv_rn(Q, v.l);
+        const float ratio = ratio_of(Q, v);
         if (tid >= threads) {
             const float loss = p.first == first ? loss_of(a, l, w.n, v, [&](int c) { return p.value(c); })
                                                 : loss_of(a, l, w.n, v, [&](int c) { return load1(z + c); });
@@ -332,7 +339,7 @@ distill_rows(const Args a)
             if (tid == threads) {
                 a.loss[row] = loss;
                 if (a.stats) {
-                    const float ratio = v.l == 0.0f ? 0.0f : __fdiv_rn(w.Q, v.l);
+                    const float ratio = ratio_of(w.Q, v);
                     a.stats[4 * row] = v.ref, a.stats[4 * row + 1] = ratio, a.stats[4 * row + 2] = w.ref, a.stats[4 * row + 3] = w.coef;
                 }
             }

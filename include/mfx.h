@@ -401,8 +401,10 @@ int mfx_add_rmsnorm_bwd(int x_dt, int res_dt, int w_dt, int64_t rows, int64_t co
 /* elements apart (a vocabulary padded in memory; what lies between counts for */
 /* nothing and is not written).  p = softmax(scale * z) over a row, scale > 0 and finite */
 /* (one over the temperature), else MFX_ERR_VALUE.  Columns at -inf have p = 0.*/
-/* A row with a NaN or +inf gives NaN.  index_bits: 32 or 64, the width of the */
-/* integers that name columns, else MFX_ERR_DTYPE.  vocab up to 2^30.          */
+/* A row with a NaN or +inf gives NaN, unless it is left out: nothing comes of */
+/* the logits of a row without a token, or without entries, whatever they are. */
+/* index_bits: 32 or 64, the width of the integers that name columns, else     */
+/* MFX_ERR_DTYPE.  vocab up to 2^30.                                           */
 /* ------------------------------------------------------------------------ */
 
 /* Log probabilities of given tokens, the distribution's entropy, and the `top`

@@ -66,3 +66,24 @@ def test_in_place_and_nan():
                      (z.clone(), lambda z2: mfx.mfx_topk_distill_fwd_bwd(z2, index, t, g, teacher_lse=lse, dlogits=z2)[1])):
         call(z2)
         assert z2[empty].eq(0).all() and z2[1].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,vocab", [(44, 1000), (44, 131), (1200, 700), (44, 70001), (640, 20011), (44, 600007)])
+def test_logits_of_rows_left_out_are_anything(rows, vocab, dtype):
+    """A padded batch: rows without entries hold NaN and infinities."""
+    z, index, t, _, _ = rows_of(rows, vocab, 5, dtype, F32)
+    empty = torch.arange(rows, device=DEV) % 2 == 0
+    g = torch.randn(rows, device=DEV)
+    for lse in (None, torch.where(empty, -INF, torch.logsumexp(t, 1) + 0.5)):
+        y = z.clone()
+        y[0::8], y[2::8, 3], y[4::8, vocab // 2], y[6::8, -1] = math.nan, math.nan, INF, -INF
+        loss, stats = mfx.mfx_topk_distill_fwd(y, index, t, teacher_lse=lse)
+        d = mfx.mfx_topk_distill_bwd(g, y, index, t, stats)
+        loss2, d2 = mfx.mfx_topk_distill_fwd_bwd(y, index, t, g, teacher_lse=lse)
+        clean, d_clean = mfx.mfx_topk_distill_fwd_bwd(z, index, t, g, teacher_lse=lse)
+        assert loss[empty].eq(0).all() and loss2[empty].eq(0).all()
+        assert d[empty].eq(0).all() and d2[empty].eq(0).all()
+        assert torch.equal(loss2[~empty], clean[~empty]) and torch.equal(d2[~empty], d_clean[~empty])
+        mfx.mfx_topk_distill_fwd_bwd(y, index, t, g, teacher_lse=lse, dlogits=y)
+        assert torch.equal(y, d2)
