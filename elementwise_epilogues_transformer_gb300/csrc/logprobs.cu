@@ -121,7 +121,7 @@ __device__ __forceinline__ void sort_out(const Key* cand, int n, int top, Key* s
 // asked for.  (64 groups for 64 alternatives: five times as many columns, 193
 // us instead of 96 at 1024x131072 at that step; 128 for 5: 9.7 us instead of 8.3 at 8x131072.)  Their runs are read again for the columns that reach the bound.
 // Should those be more than there is room for (many equal logits, or few
-// threads with most of the large ones), the runs are taken in small rounds and
+// threads with most of the large ones), the runs are taken in small steps and
 // the candidates cut to the best, which raises the bound.
 template <typename T, typename F>
 __device__ __forceinline__ void find_top(const Runs<T>& r, int first, int last, float best, int top, TopSmem& sm, F run_at)
@@ -155,18 +155,21 @@ __device__ __forceinline__ void find_top(const Runs<T>& r, int first, int last, 
     if (best > -INFINITY && best >= least)
         sm.list[atomicAdd(&sm.listed, 1)] = tid;
     __syncthreads();
-    // a warp goes over a listed thread's runs, a lane each
+    // A warp goes over a listed thread's runs, a lane each: a group of as many
+    // threads as there are warps, 32 runs of each at a time.  A step of `warps`
+    // of the group from `w0` on; the group stays until all its runs are through.
     const int each = (last - first + T_ - 1) / T_, listed = sm.listed, all = T_ >> 5;
-    for (int warps = all, l0 = 0, i0 = 0; l0 < listed;) {
+    for (int warps = all, l0 = 0, w0 = 0, i0 = 0; l0 < listed;) {
         const int before = sm.count;
         __syncthreads();
-        if (warp < warps && l0 + warp < listed && i0 + lane < each) {
-            if (const int u = first + sm.list[l0 + warp] + (i0 + lane) * T_; u < last) {
-                const uint4 w[1] = {run_at(u)};
+        const int w = w0 + warp;
+        if (warp < warps && w < all && l0 + w < listed && i0 + lane < each) {
+            if (const int u = first + sm.list[l0 + w] + (i0 + lane) * T_; u < last) {
+                const uint4 x[1] = {run_at(u)};
                 const int c = r.column(u);
-                if (key_of(Run<T>::template top_of<1>(w), max(c, 0)) >= bound) {
+                if (key_of(Run<T>::template top_of<1>(x), max(c, 0)) >= bound) {
                     float2 f[V / 2];
-                    Run<T>::widen(w[0], f);
+                    Run<T>::widen(x[0], f);
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         const float z = j & 1 ? f[j >> 1].y : f[j >> 1].x;
@@ -180,7 +183,7 @@ __device__ __forceinline__ void find_top(const Runs<T>& r, int first, int last, 
         }
         __syncthreads();
         const int n = sm.count;
-        if (n > kCandidates) {  // not all of them had room: again, in a round that cannot overflow
+        if (n > kCandidates) {  // not all of them had room: again, in steps that cannot overflow
             __syncthreads();
             if (tid == 0)
                 sm.count = before;
@@ -188,9 +191,12 @@ __device__ __forceinline__ void find_top(const Runs<T>& r, int first, int last, 
             __syncthreads();
             continue;
         }
-        i0 += 32;
-        if (i0 >= each)
-            i0 = 0, l0 += warps;
+        w0 += warps;
+        if (w0 >= all) {
+            w0 = 0, i0 += 32;
+            if (i0 >= each)
+                i0 = 0, l0 += all;
+        }
         if (l0 < listed && n > kKept) {
             sort_out(sm.cand, n, top, sm.sel);
             __syncthreads();
@@ -199,7 +205,7 @@ __device__ __forceinline__ void find_top(const Runs<T>& r, int first, int last, 
             bound = sm.sel[top - 1], least = value_of(bound);
             if (tid == 0)
                 sm.count = top;
-            if (i0 == 0)
+            if (w0 == 0)
                 warps = all;
             __syncthreads();
         }
