@@ -37,8 +37,8 @@ constexpr int kMostKeys = 128;  // groups of threads that bound the search for t
 constexpr int kMostChunks = 8;
 constexpr int kMostListed = kMostChunks * kThreadsMost;
 constexpr int kPickThreads = 128;
-constexpr int kRound = 64;      // runs of a round that cannot overflow the candidates
-constexpr int kKept = 256;      // candidates that a round may find there
+constexpr int kRound = 64;      // runs of a step that cannot overflow the candidates
+constexpr int kKept = 256;      // candidates that a step may find there
 constexpr int kCandidates = kRound * 8 + kKept;
 
 struct Args {
@@ -520,20 +520,21 @@ pick_top(const Args a)
                 count += __popc(who);
             }
         };
-        // the vectors at the row's borders, then the listed parts' runs, 2 to 8 parts at a time
+        // The vectors at the row's borders, then the listed parts' runs: a group of 8, 16 or 32 parts (U times as many as
+        // the lanes reach) stays until all its runs are through, and a step takes `rounds` of its U quarters from r0 on.
         if (q.head() || q.tail()) {
             const bool on = lane == 0 ? q.head() : lane == 1 && q.tail();
             const int c = q.r.column(lane == 0 ? 0 : q.r.count - 1);
             collect(on ? load_run(z, a.n, c) : Run<T>::none(), c, on);
         }
-        for (int l0 = 0, i0 = 0, rounds = U; l0 < listed;) {
+        for (int l0 = 0, r0 = 0, i0 = 0, rounds = U; l0 < listed;) {
             const int before = count;
             uint4 w[U];
             int c[U];
             bool on[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const int l = l0 + (i << (5 - log_reach)) + (lane >> log_reach), n = i0 + (lane & (reach - 1));
+                const int l = l0 + ((r0 + i) << (5 - log_reach)) + (lane >> log_reach), n = i0 + (lane & (reach - 1));
                 on[i] = i < rounds && l < listed && n < each;
                 const int id = on[i] ? sm.list[l] : 0;
                 const int u = q.whole0 + (id & (T_ - 1)) + ((id >> shift) * each + n) * T_;
@@ -544,20 +545,23 @@ pick_top(const Args a)
 #pragma unroll
             for (int i = 0; i < U; ++i)
                 collect(w[i], c[i], on[i]);
-            if (count > kCandidates) {  // not all of them had room: again, in a round that cannot overflow
+            if (count > kCandidates) {  // not all of them had room: again, in steps that cannot overflow
                 count = before, rounds = kRound / 32;
                 continue;
             }
-            i0 += reach;
-            if (i0 >= each)
-                i0 = 0, l0 += rounds << (5 - log_reach);
+            r0 += rounds;
+            if (r0 >= U) {
+                r0 = 0, i0 += reach;
+                if (i0 >= each)
+                    i0 = 0, l0 += U << (5 - log_reach);
+            }
             if (l0 < listed && count > kKept) {
                 __syncwarp();
                 warp_sort(sm.cand, count, a.top, sm.sel);
                 for (int j = lane; j < a.top; j += 32)
                     sm.cand[j] = sm.sel[j];
                 bound = sm.sel[a.top - 1], count = a.top;
-                if (i0 == 0)
+                if (r0 == 0)
                     rounds = U;
                 __syncwarp();
             }

@@ -48,3 +48,12 @@ def test_few_rows(vocab, dtype, period):
     torch.manual_seed(7)
     z = plateaus(vocab, dtype, period, [period // 4, period // 3, period // 2, period - 3000], (0, 3, 19, 60, 100))
     check(z, 1, (1, 5, 24, 25, 64))
+
+
+# a part's first 16 runs are 32768 columns (bf16) of 65536 or more
+@pytest.mark.parametrize("vocab,dtype,period", [(500_000, BF, 65_536), (500_009, BF, 65_536), (800_000, BF, 106_496),
+                                                (300_000, F32, 40_960)])
+def test_many_rows(vocab, dtype, period):
+    torch.manual_seed(8)
+    z = plateaus(vocab, dtype, period, [period // 2, period // 2 + 5000, period - 9000], (0, 3, 10, 60, 100))
+    check(z, 20, (1, 20, 24, 25, 64))
