@@ -17,7 +17,7 @@
 // Measured: 16384x4096 bf16 with an fp32 residual 132 us (6120 GB/s, 0.90 of
 // the copy rate), all bf16 89 us; 8192x8192 bf16 89 us, as e4m3 with a scale a
 // row 80.5 us (5830 GB/s); 16384x4096 as e4m3 with a power of two per 32
-// columns 79.5 us; 3001x2051 fp32 (single columns) 16.8 us (5850 GB/s);
+// columns 80 us; 3001x2051 fp32 (single columns) 16.8 us (5850 GB/s);
 // 8192x4099 bf16 66 us (4050 GB/s: two bytes an access); one row of 4096 2.6 us.
 #include "rmsnorm.cuh"
 
@@ -119,9 +119,10 @@ __device__ __forceinline__ void store_fp8(uint8_t* q, const float (&y)[V], float
 // of a group is below some 1e-36 (e4m3) or 1e-34 (e5m2) and rstd above 4, rstd
 // times a scale's reciprocal passes fp32's range, though y and s do not: the
 // power goes to the values first, which is exact, and what is left times a
-// reciprocal (2^126 at most) stays within.  (For every row whose rstd is above
-// 2, which costs a product an element: 16384x4096 with rows of 0.05 84.8 us
-// per 128 columns, 81.5 where only values below kTiny have it.)
+// reciprocal (2^126 at most) stays within.  Only where a thread's values are
+// below kTiny, or in single columns: for every row whose rstd is above 2 the
+// products cost more (16384x4096 bf16 with rows of 0.05, per 128 columns: 84.8
+// us, 82.6 with the question asked, 81.8 without either).
 constexpr float kTiny = 1e-33f;
 struct Parts {
     float power, rest;

@@ -354,8 +354,9 @@ int mfx_moe_unpermute_bwd(int dt, int64_t tokens, int64_t topk, int64_t cols, in
  * weights that are kept around zero, else 0.  residual NULL: h = x (and h must
  * be NULL).  h (NULL: not written) is the new residual stream; y is formed
  * from it before it is rounded.  rstd: [rows] fp32, what the backward needs,
- * or NULL.  Norms are fp32: squares of values beyond 1.8e19 overflow, and a
- * row of zeros with eps = 0 gives NaN.
+ * or NULL.  Norms are fp32: squares of values beyond 1.8e19 overflow, h *
+ * (weight + weight_offset) is formed before rstd comes to it and has to be
+ * within fp32's range too, and a row of zeros with eps = 0 gives NaN.
  * eps >= 0 and finite, else MFX_ERR_VALUE; cols up to 2^30.  y and h may each
  * be x's or the residual's very buffer; other overlaps -> MFX_ERR_ALIAS. */
 int mfx_add_rmsnorm_fwd(int x_dt, int res_dt, int w_dt, int64_t rows, int64_t cols,
@@ -370,6 +371,9 @@ int mfx_add_rmsnorm_fwd(int x_dt, int res_dt, int w_dt, int64_t rows, int64_t co
  * s = max |y| / 448 (e4m3) or / 57344 (e5m2), at least 2^-126 and 1 for a
  * group of zeros; scale: [rows, groups of a row], MFX_F32, or MFX_E8M0: s
  * rounded up to a power of two, stored as its exponent + 127 in a byte.
+ * Both are products in fp32: beside rstd's own error, an fp32 scale is off by
+ * up to 2^-21 of it, and what is rounded to q by up to 2^-21 of y / s (with the
+ * stored s), so that a y / s next to the middle of two values may go to either.
  * NaN stays NaN (and counts for nothing in max |y|), infinities saturate.
  * y is not rounded to x_dt on the way.  q and scale overlap nothing else. */
 int mfx_add_rmsnorm_quant_fwd(int x_dt, int res_dt, int w_dt, int64_t rows, int64_t cols,
