@@ -911,7 +911,8 @@ def mfx_topk_distill_fwd(logits, index, teacher, scale=1.0, teacher_lse=None, lo
     """(loss [rows], stats [rows, 4]): sum of q (log q - log p) over the
     teacher's entries, p = softmax(scale * logits [rows, vocab]) and q the same
     of teacher [rows, k] at the columns index [rows, k] (int32 or int64,
-    negative for no entry), or exp(scale * teacher - teacher_lse [rows])."""
+    negative for no entry), or exp(scale * teacher - teacher_lse [rows]).  A row
+    without entries has loss 0 and a gradient of zeros."""
     dev, rows, head, data, lse = _distill_args(logits, index, teacher, teacher_lse)
     loss, lptr = _new(loss, "loss", (rows,), torch.float32, dev, logits, stream)
     sptr = None

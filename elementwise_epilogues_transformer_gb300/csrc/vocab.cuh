@@ -19,8 +19,7 @@
 //    forward and gradient 483 us instead of 425 at that step.)
 //  - Rows one after another (many rows that are read once; see Stream): no
 //    cluster to wait for, and copies under way over the rows' borders.
-//    From two rows a multiprocessor on: 400x131072 bf16 19.4 us and 28.2 by
-//    slices, 1024x131072 46 and 63; 160x131072 13.4 and 12.7.
+//    From two rows a multiprocessor on (see streamed()).
 // Four groups of a thread's four runs are in flight; a group's largest element
 // is found first, so that its sums are rebased at most once.
 #pragma once
@@ -664,7 +663,25 @@ template <typename T, int STEP> struct Stream {
     }
 };
 
-// Rows that are read once, and enough of them, go one after another.
+// Rows that are read once, and enough of them, go one after another: from two
+// rows a multiprocessor on, which lies between what short and long rows want.
+// Measured, us by slices and one after another, inputs not in L2:
+//    log probabilities          alone                 with 20 alternatives
+//    bf16  288 x  32768       8.2    8.2                12.3   17.1
+//    bf16  304 x  32768       8.4    8.3                12.6   16.9
+//    bf16  456 x  32768      10.5   10.5                15.6   19.0
+//    bf16  608 x  32768      13.6   13.1                21.7   21.9
+//    bf16  160 x 131072      16.5   14.4                27.5   27.3
+//    bf16  288 x 131072      23.4   15.7                39.9   29.2
+//    bf16  304 x 131072      24.1   16.0                41.1   29.4
+//    bf16  608 x 131072      41.0   30.7                73.3   47.2
+//    fp32  160 x  50021      12.8   10.4                23.5   21.1
+//    fp32  304 x  50021      19.2   14.5                34.6   25.4
+// The distillation's forward goes like the first pair (304 x 131072 25.2 and
+// 16.1).  What tips it is whether the slices of all rows find places at once
+// (three a multiprocessor): rows of one slice with alternatives lose up to a
+// third from here to 456 rows, rows of four slices as much from one row a
+// multiprocessor to here.  A border by slices would suit both.
 #ifndef MFX_VOCAB_STREAM
 #define MFX_VOCAB_STREAM 2
 #endif

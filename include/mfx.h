@@ -404,7 +404,9 @@ int mfx_add_rmsnorm_bwd(int x_dt, int res_dt, int w_dt, int64_t rows, int64_t co
 /* Operators on logits [rows, vocab] of dtype dt, whose rows begin ld >= vocab */
 /* elements apart (a vocabulary padded in memory; what lies between counts for */
 /* nothing and is not written).  p = softmax(scale * z) over a row, scale > 0 and finite */
-/* (one over the temperature), else MFX_ERR_VALUE.  Columns at -inf have p = 0.*/
+/* (one over the temperature), else MFX_ERR_VALUE.  Columns at -inf have p = 0,*/
+/* and so have those whose scale * (z - max) passes fp32's range (log p = -inf);*/
+/* powers below 2^-126 add nothing to sums and gradients.                      */
 /* A row with a NaN or +inf gives NaN, unless it is left out: nothing comes of */
 /* the logits of a row without a token, or without entries, whatever they are. */
 /* index_bits: 32 or 64, the width of the integers that name columns, else     */
